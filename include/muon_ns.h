@@ -71,7 +71,7 @@ typedef enum {
 typedef enum {
     MUON_BF16 = 0,   /* grad, W (and X/out of muon_ns_batched) are bfloat16; momentum is fp32 */
     MUON_FP32 = 1,   /* all tensors fp32; NS computed with fp32 arithmetic */
-    MUON_FP16 = 2    /* muon_debug_gemm only: fp16 operands and an fp16 output pair */
+    MUON_FP16 = 2    /* muon_debug_gemm (fp16 operands and an fp16 output pair), and the operators from muon_clip_grads on */
 } muon_dtype;
 
 typedef enum {
@@ -414,6 +414,148 @@ MUON_API muon_status muon_cost_estimate(const int64_t* shapes, int count, int st
  */
 MUON_API muon_status muon_partition(const double* cost, int count, int world, int exact_limit,
                                     int32_t* owner, double* load);
+
+/*
+ * ---- operators around the update
+ *
+ * What a training step with 8-bit products runs next to muon_step: the gradients
+ * are clipped by their global norm, the residual stream is normalised and
+ * quantised, and the weights, activations and gradients are multiplied as 8-bit
+ * matrices.  Their matrices have a row stride (`ld`, elements; ignored for a single
+ * row) and consecutive elements within a row.  They take bf16, fp16 or fp32;
+ * sums and statistics are fp32 or wider, and every output is rounded once, to
+ * nearest even.  Outputs have the same bits on every call with the same inputs.
+ * Pointers aligned to 16 bytes with strides of whole 16 bytes use vector
+ * accesses; others are only slower.
+ *
+ * The 8-bit format.  A matrix [rows, cols] that a product sums along its columns is
+ *   data   [rows][ld] e4m3 or e5m2; 16-byte aligned, ld a multiple of 16 that is at
+ *          least cols (rounded up to 16 where a call of this library writes it;
+ *          the bytes from cols up to there are unspecified)
+ *   scale  [ceil(cols / 512)][rows rounded up to 4][4] bytes, 4-byte aligned: the
+ *          scale of columns 128 kb .. 128 kb + 127 of row r is 2^(s - 127), s the byte
+ *          at [kb / 4][r][kb % 4].  255 stands for NaN.  Entries of no row or no block
+ *          are written as 127 (1) and never read.
+ * Element (r, c) stands for data * scale.  A scale shared by 128 x 128 elements is
+ * kept once for each of its rows.
+ */
+
+typedef enum {
+    MUON_E4M3 = 0,   /* largest value 448 */
+    MUON_E5M2 = 1    /* largest value 57344 */
+} muon_fp8;
+
+#define MUON_MAX_ROWS 4194304LL   /* largest accepted size of these operators (the norms' cols: MUON_MAX_DIM) */
+#define MUON_MAX_SMS 152          /* SMs that workspace sizes are counted for */
+#define MUON_CLIP_CTAS 2048       /* partial sums per launch of muon_clip_grads */
+
+/* Bytes of muon_clip_grads' workspace for `count` tensors. */
+MUON_API size_t muon_clip_workspace_bytes(int count);
+
+/*
+ * muon_clip_grads -- the global norm of a list of gradients, and clipping:
+ *
+ *   N = sqrt(sum over all elements of g^2)
+ *   c = min(1, max_norm / (N + eps))        out = round(g * c)
+ *
+ *   grads, numel, dtypes  host arrays of `count`: device pointers, element
+ *         counts (0 allowed) and muon_dtype of each tensor.
+ *   out   host array of device pointers to the clipped gradients (same dtypes);
+ *         out[i] == grads[i] clips in place, and then nothing is written where
+ *         c = 1.  NULL: only the norm.
+ *   norm  device pointer to the fp32 norm, or NULL.
+ *   ws    device workspace of muon_clip_workspace_bytes(count), 8-byte aligned.
+ * Squares that leave fp32's range do not spoil the norm of finite gradients.  An
+ * infinite norm gives c = 0 (infinite elements become NaN), a NaN one gives NaN.
+ * max_norm may be infinite.  Sums run in a fixed order.  Two launches up to 1024
+ * tensors.
+ * Errors (nothing launched): MUON_ERR_ARG for count < 0, NULL arrays or pointers
+ * of non-empty tensors, no output at all, a bad dtype, max_norm or eps negative or
+ * NaN (eps: or infinite), an out that partly overlaps its gradient or the
+ * workspace; MUON_ERR_SHAPE, MUON_ERR_ALIGN, MUON_ERR_WORKSPACE,
+ * MUON_ERR_UNSUPPORTED as elsewhere.
+ */
+MUON_API muon_status muon_clip_grads(const void* const* grads, void* const* out, const int64_t* numel,
+                                     const int32_t* dtypes, int count, float max_norm, float eps, float* norm,
+                                     void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * muon_rms_norm -- root-mean-square norm over the rows of a matrix, with the
+ * residual's addition and an 8-bit copy:
+ *
+ *   s = x + residual (fp32)      h = round(s)      rho = 1 / sqrt(mean_j s_j^2 + eps)
+ *   y = s rho weight             q = 8-bit y with its scales (blocks of 128 columns)
+ *
+ *   x, residual, y, h  [rows, cols] of dtype dt; residual, y, h may be NULL.
+ *   weight  [cols] of weight_dt, or NULL for 1.
+ *   rstd    [rows] fp32 rho (the gradient needs it), or NULL.
+ *   q, q_scale  8-bit copy of the unrounded y (see above), or both NULL.
+ * y or h may be x or residual themselves.  cols in [1, MUON_MAX_DIM], rows in
+ * [0, MUON_MAX_ROWS].  Errors as elsewhere, before anything is launched.
+ */
+MUON_API muon_status muon_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                   const void* weight, muon_dtype weight_dt, int64_t rows, int64_t cols, float eps,
+                                   void* y, int64_t ldy, void* h, int64_t ldh, float* rstd, void* q, int64_t ldq,
+                                   void* q_scale, muon_fp8 fmt, muon_dtype dt, void* stream);
+
+/*
+ * muon_rms_norm_backward -- its gradient, for dy = dL/dy and h as stored:
+ *
+ *   g = dy weight      dx = rho (g - h rho^2 mean_j(g_j h_j)) + dresidual
+ *   dweight_j = sum over rows of dy_j h_j rho   (fp32, overwritten)
+ *
+ * dx is the gradient of x and of residual alike; dresidual (or NULL) is what reaches
+ * h on its way past the norm.  dx may be dy, dresidual or h itself.  dx or
+ * dweight may be NULL.  The workspace (16-byte aligned, size from
+ * muon_rms_norm_backward_workspace_bytes) is needed with dweight.
+ */
+MUON_API size_t muon_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+MUON_API muon_status muon_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh,
+                                            const void* weight, muon_dtype weight_dt, const float* rstd,
+                                            const void* dresidual, int64_t lddr, int64_t rows, int64_t cols,
+                                            void* dx, int64_t lddx, float* dweight, void* ws, size_t ws_bytes,
+                                            muon_dtype dt, void* stream);
+
+/* Bytes of the scales of an 8-bit matrix [rows, cols]. */
+MUON_API size_t muon_fp8_scale_bytes(int64_t rows, int64_t cols);
+
+/*
+ * muon_fp8_quantize -- x [rows, cols] to 8 bits in one pass, along its columns (q),
+ * transposed along its rows (qt, an 8-bit matrix [cols, rows]), or both:
+ *
+ *   e = the smallest exponent (at least -127) with max |x| over the block <= top * 2^e
+ *   q = round8(x * 2^-e)
+ *
+ * square = 0: blocks of 128 along the summed axis.  square = 1: blocks of 128 x 128
+ * (weights; q and qt then stand for the same values).  A block of zeros has scale 1;
+ * a block with an infinity or NaN becomes NaN.  q with q_scale, or qt with qt_scale,
+ * may be NULL.  An empty x writes nothing.
+ */
+MUON_API muon_status muon_fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_t cols, muon_dtype dt,
+                                       muon_fp8 fmt, int square, void* q, int64_t ldq, void* q_scale, void* qt,
+                                       int64_t ldqt, void* qt_scale, void* stream);
+
+/*
+ * muon_fp8_matmul -- out = round(A B^T + add) for 8-bit A [m, k] and B [n, k] as
+ * described above, of either format each; add (or NULL) and out are [m, n] of
+ * out_dt.  add may be out itself.  Products are summed in fp32.  k = 0 gives
+ * add, or zeros.  With few tiles k is split; the workspace (16-byte aligned, size
+ * from muon_fp8_matmul_workspace_bytes; 0: none, NULL allowed) holds the parts.
+ * A kernel that gives up on a bounded wait leaves the output incomplete and is
+ * reported by muon_fp8_status.
+ */
+MUON_API size_t muon_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+MUON_API muon_status muon_fp8_matmul(const void* a, int64_t lda, const void* a_scale, muon_fp8 a_fmt, const void* b,
+                                     int64_t ldb, const void* b_scale, muon_fp8 b_fmt, int64_t m, int64_t n,
+                                     int64_t k, const void* add, int64_t ldadd, void* out, int64_t ldc,
+                                     muon_dtype out_dt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * muon_fp8_status -- synchronise `stream`, then read and clear the 8-bit product's
+ * status word: MUON_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last
+ * check, MUON_ERR_CUDA on a CUDA error, else MUON_OK.
+ */
+MUON_API muon_status muon_fp8_status(void* stream);
 
 /* Thread-local message of the last failed call on this thread ("" if none). */
 MUON_API const char* muon_last_error(void);

@@ -10,3 +10,7 @@ from .binding import (  # noqa: F401
     ns_batched, ns_batched_static, owned, partition, profile_enable, profile_records, resolve_schedule,
     sched_code, schedule_candidates, static_status, tune_schedules, workspace_bytes,
 )
+from .training import (  # noqa: F401
+    Fp8Tensor, RmsNormOutput, clip_grads, fp8_matmul, fp8_matmul_workspace_bytes, fp8_quantize, fp8_status, grad_norm,
+    rms_norm, rms_norm_backward,
+)

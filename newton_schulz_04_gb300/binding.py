@@ -100,6 +100,28 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.muon_partition.argtypes = [ctypes.POINTER(ctypes.c_double), i32, i32, i32, ctypes.POINTER(i32),
                                    ctypes.POINTER(ctypes.c_double)]
     lib.muon_partition.restype = i32
+    lib.muon_clip_workspace_bytes.argtypes = [i32]
+    lib.muon_clip_workspace_bytes.restype = sz
+    lib.muon_clip_grads.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i64),
+                                    ctypes.POINTER(ctypes.c_int32), i32, f32, f32, vp, vp, sz, vp]
+    lib.muon_clip_grads.restype = i32
+    lib.muon_rms_norm.argtypes = [vp, i64, vp, i64, vp, i32, i64, i64, f32, vp, i64, vp, i64, vp, vp, i64, vp, i32, i32,
+                                  vp]
+    lib.muon_rms_norm.restype = i32
+    lib.muon_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.muon_rms_norm_backward_workspace_bytes.restype = sz
+    lib.muon_rms_norm_backward.argtypes = [vp, i64, vp, i64, vp, i32, vp, vp, i64, i64, i64, vp, i64, vp, vp, sz, i32, vp]
+    lib.muon_rms_norm_backward.restype = i32
+    lib.muon_fp8_scale_bytes.argtypes = [i64, i64]
+    lib.muon_fp8_scale_bytes.restype = sz
+    lib.muon_fp8_quantize.argtypes = [vp, i64, i64, i64, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp]
+    lib.muon_fp8_quantize.restype = i32
+    lib.muon_fp8_matmul_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.muon_fp8_matmul_workspace_bytes.restype = sz
+    lib.muon_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i64, vp, i64, i32, vp, sz, vp]
+    lib.muon_fp8_matmul.restype = i32
+    lib.muon_fp8_status.argtypes = [vp]
+    lib.muon_fp8_status.restype = i32
     lib.muon_last_error.argtypes = []
     lib.muon_last_error.restype = ctypes.c_char_p
     lib.muon_version.argtypes = []

@@ -44,6 +44,7 @@
 #include "muon_ns.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "train_ops.h"
 
 namespace muon {
 
@@ -58,6 +59,7 @@ muon_status fail(muon_status s, const char* fmt, ...) {
   g_last_error = buf;
   return s;
 }
+void clear_error() { g_last_error.clear(); }
 
 // ------------------------------------------------------------------ profiling
 // Optional per-launch CUDA-event timing on the caller's stream (off by default).
@@ -431,7 +433,7 @@ static int fit_batch(const Group& g, int want, muon_dtype dt, size_t ws_bytes) {
 }
 
 // ------------------------------------------------------------------ device info
-static int device_sms(int* major, int* minor, muon_status* st) {
+int device_sms(int* major, int* minor, muon_status* st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();

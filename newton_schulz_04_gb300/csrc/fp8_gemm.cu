@@ -1,0 +1,587 @@
+// fp8_gemm.cu -- C = A B^T (+ D) of 8-bit operands with a power-of-two scale for each row and block of 128 of K.
+//
+//   C[m][n] = round( sum_k a[m][k] 2^ea[m][k/128] b[n][k] 2^eb[n][k/128]  + D[m][n] )
+//
+// One form serves a layer's three products: the forward pass (A tokens, B the
+// weight), the data gradient (B the weight's transposed copy) and the weight
+// gradient (both operands laid out along the tokens).
+//
+// tcgen05.mma kind::mxf8f6f4 multiplies every 32 of K by a scale byte (E8M0) of the
+// row of A and the row of B, taken from TMEM, and accumulates in fp32 over all of K.
+// A block of 128 is four such steps that name the same byte, so one 32-bit TMEM
+// column serves 512 of K, which is how the scales are kept in memory: words of four
+// blocks, rows side by side.
+//
+// A persistent grid of CTA pairs (clusters of two) works through output tiles of
+// 256 rows of B by T rows of A (T a multiple of 32, at most 224), one pair MMA of
+// M = 256, N = T per 32 of K: the rows of B (output columns) are the MMA's M, so
+// that the 32 lanes of a TMEM row group are 32 consecutive elements of C's row.
+// Every store of a warp is then one contiguous segment whatever C's alignment or
+// stride, with no staging.  Each CTA loads its 128 rows of B and half of the T rows of A.
+//
+// TMEM (512 columns): two accumulators of 224, so the epilogue of one tile overlaps
+// the next main loop, and two sets of scales (4 + 7 columns each).
+//
+// Warp roles (448 threads):
+//   warp 0       TMA producer: stages of 256 of K (two swizzled 128-byte boxes per operand)
+//   warp 1       TMEM allocation; the leader's lane 0 issues the MMAs
+//   warps 2..5   scales: every warp copies the words of all rows of the tile to its
+//                own quarter of TMEM's lanes (the MMA reads a copy in each quarter),
+//                a 512-deep group ahead of the MMAs
+//   warps 6..13  epilogue: two warps per lane quarter, alternating 32-column chunks
+//
+// When there are too few tiles to fill the GPU, K is split: each part's fp32 sums go to
+// the caller's workspace and a second kernel adds them in order.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "train_ops.h"
+
+namespace muon {
+
+// A kernel that gives up on a wait records it here (muon_fp8_status reads and clears it).
+static __device__ int g_fp8_status;
+
+struct F8Cfg {
+  static constexpr int BN = 128;        // rows of B per CTA (256 per pair)
+  static constexpr int TMAX = 224;      // rows of A per tile
+  static constexpr int KB = 128;        // K per block: one 128-byte swizzled row of 8-bit values
+  static constexpr int KPS = 2;         // blocks per stage
+  static constexpr int B_BOX = BN * KB;
+  static constexpr int A_BOX = TMAX / 2 * KB;
+  static constexpr int STAGE = KPS * (B_BOX + A_BOX);
+  static constexpr int STAGES = 3;
+  static constexpr int SCALE_WARP = 2, EPI_WARP = 6, EPI_WARPS = 8;
+  static constexpr int THREADS = 32 * (EPI_WARP + EPI_WARPS);
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int SMEM = STAGES * STAGE + BAR_BYTES + 1024;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t ACC_COLS = TMAX;
+  static constexpr uint32_t SCALE_COL = 2 * TMAX;  // + 16 per set: rows of B in the first 4 columns, of A from the 8th on
+  static constexpr uint32_t EPI_ARRIVALS = 2 * EPI_WARPS;
+  static constexpr uint32_t SCALE_ARRIVALS = 2 * 4;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(SCALE_COL + 2 * 32 <= TMEM_COLS, "TMEM budget");
+  static_assert(A_BOX % 1024 == 0 && B_BOX % 1024 == 0, "swizzle atoms of 1024 bytes");
+};
+
+struct F8Args {
+  CUtensorMap ta, tb;   // {128, T / 2} boxes of A, {128, 128} boxes of B
+  const uint32_t *sa, *sb;  // scale words [group][rows4]
+  long long m, n;
+  long long sa_rows, sb_rows;
+  int kblocks;          // blocks of 128
+  int tail_steps;       // 32-deep MMA steps of the last block
+  int tile_m;
+  int nI, nJ;           // tiles along n (256) and m
+  int splits, gps;      // parts of K, 512-deep groups per part
+  int items;
+  int rgroup;           // tiles along n walked together
+  uint32_t idesc;
+  const void* add;
+  void* out;
+  float* partial;       // with splits > 1: [splits][m][n]
+  long long ldadd, ldc;
+  int out_dt;
+  int* status;
+};
+
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* m, uint32_t bar_cluster, void* dst, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y)
+      : "memory");
+}
+// D[tmem] (+)= (A scale_a) (B scale_b) over the pair, 32 of K; scales in TMEM, one byte per row and 32 of K.
+__device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                                uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// Each thread stores words to consecutive TMEM columns of its own lane.
+__device__ __forceinline__ void tmem_st_x4(uint32_t t, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t t, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct F8Item {
+  int i, j;        // tile along n, along m
+  int g0, g1;      // 512-deep groups of K
+  int split;
+};
+__device__ __forceinline__ F8Item decode_item(const F8Args& a, int t) {
+  F8Item it;
+  const int tiles = a.nI * a.nJ;
+  it.split = t / tiles;
+  const int u = t - it.split * tiles;
+  // rgroup tile rows of B at a time, so that they stay in L2 while A streams by
+  const int per = a.rgroup * a.nJ;
+  const int g = u / per, first = g * a.rgroup, gs = min(a.nI - first, a.rgroup), w = u - g * per;
+  it.i = first + w % gs;
+  it.j = w / gs;
+  it.g0 = it.split * a.gps;
+  it.g1 = min((a.kblocks + 3) >> 2, it.g0 + a.gps);
+  return it;
+}
+
+// Rows m0 .. m0 + rows - 1 (at most 32, one register each) of column n of the output.
+template <typename T>
+__device__ __forceinline__ void epi_chunk(const F8Args& a, int split, long long m0, int rows, long long n,
+                                          const float (&v)[32]) {
+  if (n >= a.n) return;
+  if (a.splits > 1) {
+    float* p = a.partial + (split * a.m + m0) * a.n + n;
+#pragma unroll
+    for (int u = 0; u < 32; ++u) {
+      if (u < rows) *p = v[u];
+      p += a.n;
+    }
+    return;
+  }
+  T* o = static_cast<T*>(a.out) + m0 * a.ldc + n;
+  if (a.add) {
+    const T* d = static_cast<const T*>(a.add) + m0 * a.ldadd + n;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      T x[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        if (16 * h + u < rows) x[u] = *d;
+        d += a.ldadd;
+      }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        if (16 * h + u < rows) *o = from_f32<T>(v[16 * h + u] + to_f32(x[u]));
+        o += a.ldc;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 32; ++u) {
+      if (u < rows) *o = from_f32<T>(v[u]);
+      o += a.ldc;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ F8Args a) {
+  using C = F8Cfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + C::STAGES * C::STAGE);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;   // [2] accumulator complete
+  uint64_t* tempty = tfull + 2;          // [2] accumulator read
+  uint64_t* sfull = tempty + 2;          // [2] scales of a group in TMEM
+  uint64_t* sempty = sfull + 2;          // [2] scales read by the group's MMAs
+  uint64_t* drain = sempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert(C::BAR_BYTES >= (2 * C::STAGES + 9) * 8 + 8, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], C::EPI_ARRIVALS);
+      mbar_init(&sfull[b], C::SCALE_ARRIVALS);
+      mbar_init(&sempty[b], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&a.ta);
+    tma_prefetch_desc(&a.tb);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  tc_fence_after();
+  pdl_launch_dependents();
+  pdl_wait();
+  const int rank = static_cast<int>(cluster_ctarank());
+  const uint32_t tmem = *tmem_slot;
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  const int half = a.tile_m >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      int st = 0;
+      bool ok = true;
+      for (int t = cid; t < a.items && ok; t += ncl) {
+        const F8Item it = decode_item(a, t);
+        const int nb0 = it.i * 256 + rank * C::BN, ma0 = it.j * a.tile_m + rank * half;
+        const int kb1 = min(a.kblocks, it.g1 * 4);
+        for (int kb = it.g0 * 4; kb < kb1; kb += C::KPS, ++st) {
+          const int s = st % C::STAGES;
+          if (*abort_flag || !mbar_wait(&empty[s], ((st / C::STAGES) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          const int nb = min(C::KPS, kb1 - kb);
+          uint8_t* p = tiles + s * C::STAGE;
+          const uint32_t fbar = mapa_cluster(&full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * nb * (C::B_BOX + half * C::KB));
+          for (int q = 0; q < nb; ++q) {
+            tma_load_2d_pair(&a.tb, fbar, p + q * C::B_BOX, (kb + q) * C::KB, nb0);
+            tma_load_2d_pair(&a.ta, fbar, p + C::KPS * C::B_BOX + q * C::A_BOX, (kb + q) * C::KB, ma0);
+          }
+        }
+      }
+      if (!ok) {
+        atomicOr(a.status, kStatusTimeout);
+        *abort_flag = 1;
+        if (rank == 0)  // copies in flight land before the CTAs exit
+          for (int q = st > C::STAGES ? st - C::STAGES : 0; q < st; ++q)
+            mbar_wait(&full[q % C::STAGES], (q / C::STAGES) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      int st = 0, grp = 0, tile = 0;
+      bool ok = true;
+      for (int t = cid; t < a.items && ok; t += ncl, ++tile) {
+        const F8Item it = decode_item(a, t);
+        const int abuf = tile & 1;
+        if (*abort_flag || !mbar_wait_cluster(&tempty[abuf], ((tile >> 1) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + abuf * C::ACC_COLS;
+        const int kb0 = it.g0 * 4, kb1 = min(a.kblocks, it.g1 * 4);
+        for (int kb = kb0; kb < kb1; kb += C::KPS, ++st) {
+          const int s = st % C::STAGES;
+          if (((kb - kb0) & 3) == 0) {  // a new group of four blocks: its scales
+            if (*abort_flag || !mbar_wait_cluster(&sfull[grp & 1], (grp >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+          }
+          if (*abort_flag || !mbar_wait_cluster(&full[s], (st / C::STAGES) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int nb = min(C::KPS, kb1 - kb);
+          const uint32_t b0 = smem_u32(tiles + s * C::STAGE), a0 = b0 + C::KPS * C::B_BOX;
+          const uint32_t sc = tmem + C::SCALE_COL + (grp & 1) * 32;
+          for (int q = 0; q < nb; ++q) {
+            const uint32_t id = static_cast<uint32_t>((kb + q) & 3);
+            const uint32_t idesc = a.idesc | (id << 29) | (id << 4);
+            const int steps = kb + q == a.kblocks - 1 ? a.tail_steps : 4;
+            for (int kk = 0; kk < steps; ++kk)
+              mma_pair_scaled(d, make_sdesc(b0 + q * C::B_BOX + kk * 32, 16, 1024, 2u),
+                              make_sdesc(a0 + q * C::A_BOX + kk * 32, 16, 1024, 2u), idesc, sc, sc + 8,
+                              (kb + q != kb0 || kk != 0) ? 1u : 0u);
+          }
+          tc_commit_pair(&empty[s], 0x3);
+          if (((kb - kb0) & 3) == 4 - C::KPS || kb + C::KPS >= kb1) {  // the group's last stage
+            tc_commit_pair(&sempty[grp & 1], 0x3);
+            ++grp;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair(&tfull[abuf], 0x3);
+      }
+      if (!ok) {
+        atomicOr(a.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      tc_commit_pair(drain, 0x1);
+      mbar_wait(drain, 0);
+    }
+  } else if (warp < C::EPI_WARP) {
+    // -------------------------------------------------------------- scales
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's quarter of the lanes
+    int grp = 0;
+    bool ok = true;
+    for (int t = cid; t < a.items && ok; t += ncl) {
+      const F8Item it = decode_item(a, t);
+      const long long n0 = it.i * 256LL + rank * C::BN, m0 = static_cast<long long>(it.j) * a.tile_m;
+      for (int g = it.g0; g < it.g1; ++g, ++grp) {
+        uint32_t wb[4], wa[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const long long r = n0 + j * 32 + lane;
+          wb[j] = r < a.n ? __ldg(a.sb + g * a.sb_rows + r) : 0x7f7f7f7fu;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const long long r = m0 + j * 32 + lane;
+          wa[j] = j * 32 < a.tile_m && r < a.m ? __ldg(a.sa + g * a.sa_rows + r) : 0x7f7f7f7fu;
+        }
+        if (lane == 0) ok = !*abort_flag && mbar_wait(&sempty[grp & 1], ((grp >> 1) & 1) ^ 1);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sc = tmem + lanes + C::SCALE_COL + (grp & 1) * 32;
+        tmem_st_x4(sc, wb);
+        tmem_st_x8(sc + 8, wa);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_cluster(&sfull[grp & 1], 0));
+      }
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(a.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3, part = (warp - C::EPI_WARP) >> 2;
+    int tile = 0;
+    bool ok = true;
+    for (int t = cid; t < a.items; t += ncl, ++tile) {
+      const F8Item it = decode_item(a, t);
+      const int abuf = tile & 1;
+      if (lane == 0) ok = !*abort_flag && mbar_wait(&tfull[abuf], (tile >> 1) & 1);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const long long n = it.i * 256LL + rank * C::BN + quarter * 32 + lane;
+      const long long m0 = static_cast<long long>(it.j) * a.tile_m;
+      const int rows = static_cast<int>(min(static_cast<long long>(a.tile_m), a.m - m0));
+      for (int c = part * 32; c < rows; c += 64) {
+        float v[32];
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter) << 21) + abuf * C::ACC_COLS + c, v);
+        const int cols = min(32, rows - c);
+        if (a.out_dt == MUON_FP32) epi_chunk<float>(a, it.split, m0 + c, cols, n, v);
+        else if (a.out_dt == MUON_BF16) epi_chunk<__nv_bfloat16>(a, it.split, m0 + c, cols, n, v);
+        else epi_chunk<__half>(a, it.split, m0 + c, cols, n, v);
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_cluster(&tempty[abuf], 0));
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(a.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while its peer may still signal it
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem, C::TMEM_COLS);
+  }
+}
+
+// C = round(sum over splits + D); splits = 0 where K is 0.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_join_kernel(const float* partial, int splits, long long m, long long n,
+                                                       const T* add, long long ldadd, T* out, long long ldc) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long total = m * n;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    const long long r = i / n, c = i - r * n;
+    float v = 0.f;
+    for (int s = 0; s < splits; ++s) v += partial[s * total + i];
+    if (add) v += to_f32(add[r * ldadd + c]);
+    out[r * ldc + c] = from_f32<T>(v);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  return fn;
+}
+
+// [rows][k] bytes, boxes of 128 bytes by `box_rows`; reads past k or the last row give 0.
+static bool byte_map(CUtensorMap* m, const void* base, long long k, long long rows, long long ld, int box_rows) {
+  const auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters that can be resident at once, and the kernel's shared-memory limit, once per device.
+static cudaError_t fp8_clusters(int sms, int* out) {
+  static std::mutex mu;
+  static int cached[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!cached[dev]) {
+    e = cudaFuncSetAttribute(fp8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F8Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms / 2 * 2);
+    cfg.blockDim = dim3(F8Cfg::THREADS);
+    cfg.dynamicSmemBytes = F8Cfg::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = sms / 2;
+    }
+    cached[dev] = std::min(n, sms / 2);
+  }
+  *out = cached[dev];
+  return cudaSuccess;
+}
+
+// The tile of tokens and the splits of K with the least estimated time, in SM
+// cycles: a pair MMA of 128 of K by T takes 2 T cycles, its loads (128 + T / 2 rows of 128
+// bytes per CTA) at 64 bytes a cycle 256 + T; an item costs some 1500 cycles of pipeline
+// fill and drain, and joining the splits a second launch and the partial sums' traffic.
+Fp8Plan fp8_plan(long long m, long long n, long long k, int sms) {
+  const long long groups = (k + 511) / 512, nI = (n + 255) / 256, pairs = std::max(1, sms / 2);
+  Fp8Plan best = {32, 1, static_cast<int>(groups)};
+  double best_time = 1e300;
+  for (int t = 32; t <= F8Cfg::TMAX; t += 32) {
+    const long long nJ = (m + t - 1) / t;
+    const double block = std::max(2.0 * t, 256.0 + t);
+    for (long long want = 1; want <= std::min<long long>(groups, 16); ++want) {
+      const long long gps = (groups + want - 1) / want, splits = (groups + gps - 1) / gps;
+      if (splits != want) continue;
+      const double waves = static_cast<double>((nI * nJ * splits + pairs - 1) / pairs);
+      double time = waves * (gps * 4 * block + 1500.0);
+      if (splits > 1) time += 4000.0 + 8.0 * splits * static_cast<double>(m) * n / 3500.0;
+      if (time < best_time) {
+        best_time = time;
+        best = {t, static_cast<int>(splits), static_cast<int>(gps)};
+      }
+      if (nI * nJ * splits >= 2 * pairs) break;
+    }
+    if (t >= m) break;
+  }
+  return best;
+}
+
+template <typename T>
+static cudaError_t launch_join(const Fp8GemmDesc& d, int splits, int sms, cudaStream_t st) {
+  const long long want = (d.m * d.n + 255) / 256;
+  const int grid = static_cast<int>(std::min<long long>(want, 8LL * sms));
+  return launch_pdl(fp8_join_kernel<T>, dim3(grid), dim3(256), 0, st, static_cast<const float*>(d.partial), splits, d.m,
+                    d.n, static_cast<const T*>(d.add), d.ldadd, static_cast<T*>(d.out), d.ldc);
+}
+static cudaError_t join(const Fp8GemmDesc& d, int splits, int sms, cudaStream_t st) {
+  if (d.out_dt == MUON_FP32) return launch_join<float>(d, splits, sms, st);
+  if (d.out_dt == MUON_BF16) return launch_join<__nv_bfloat16>(d, splits, sms, st);
+  return launch_join<__half>(d, splits, sms, st);
+}
+
+cudaError_t fp8_status_address(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fp8_status); }
+
+cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, const Fp8Plan& p, int sms, cudaStream_t st, const char** why) {
+  using C = F8Cfg;
+  *why = nullptr;
+  if (d.k == 0) return join(d, 0, sms, st);
+  int clusters = 0;
+  cudaError_t e = fp8_clusters(sms, &clusters);
+  if (e != cudaSuccess) return e;
+  F8Args a;
+  if (!byte_map(&a.ta, d.a, d.k, d.m, d.lda, p.tile_m / 2) || !byte_map(&a.tb, d.b, d.k, d.n, d.ldb, C::BN)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  a.sa = static_cast<const uint32_t*>(d.a_scale);
+  a.sb = static_cast<const uint32_t*>(d.b_scale);
+  a.m = d.m;
+  a.n = d.n;
+  a.sa_rows = (d.m + 3) & ~3LL;
+  a.sb_rows = (d.n + 3) & ~3LL;
+  a.kblocks = static_cast<int>((d.k + 127) / 128);
+  a.tail_steps = static_cast<int>((d.k - (a.kblocks - 1) * 128LL + 31) / 32);
+  a.tile_m = p.tile_m;
+  a.nI = static_cast<int>((d.n + 255) / 256);
+  a.nJ = static_cast<int>((d.m + p.tile_m - 1) / p.tile_m);
+  a.splits = p.splits;
+  a.gps = p.groups_per_split;
+  const long long items = static_cast<long long>(a.nI) * a.nJ * a.splits;
+  if (items > 0x7fffffffLL) {
+    *why = "too many tiles";
+    return cudaErrorInvalidValue;
+  }
+  a.items = static_cast<int>(items);
+  // as many 256-row panels of B as fit 32 MB of the 126 MB L2, at least 4
+  a.rgroup = static_cast<int>(std::min<long long>(a.nI, std::max<long long>(4, (32LL << 20) / (256 * d.k))));
+  // instruction descriptor: A (the kernel's B) and B formats, N >> 3, E8M0 scales, M >> 4 with M = 256
+  a.idesc = (static_cast<uint32_t>(d.b_fmt) << 7) | (static_cast<uint32_t>(d.a_fmt) << 10) |
+            (static_cast<uint32_t>(p.tile_m >> 3) << 17) | (1u << 23) | (16u << 24);
+  a.add = p.splits > 1 ? nullptr : d.add;
+  a.out = d.out;
+  a.partial = d.partial;
+  a.ldadd = d.ldadd;
+  a.ldc = d.ldc;
+  a.out_dt = d.out_dt;
+  e = fp8_status_address(&a.status);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * std::min(a.items, clusters));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, fp8_gemm_kernel, a);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return join(d, p.splits, sms, st);
+}
+
+}  // namespace muon
