@@ -20,7 +20,7 @@
 // stride, with no staging.  Each CTA loads its 128 rows of B and half of the T rows of A.
 //
 // TMEM (512 columns): two accumulators of 224, so the epilogue of one tile overlaps
-// the next main loop, and two sets of scales (4 + 7 columns each).
+// the next main loop, and four sets of scales (4 + 7 columns each).
 //
 // Warp roles (448 threads):
 //   warp 0       TMA producer: stages of 256 of K (two swizzled 128-byte boxes per operand)
@@ -65,11 +65,13 @@ struct F8Cfg {
   static constexpr int SMEM = STAGES * STAGE + BAR_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t ACC_COLS = TMAX;
-  static constexpr uint32_t SCALE_COL = 2 * TMAX;  // + 16 per set: rows of B in the first 4 columns, of A from the 8th on
+  static constexpr uint32_t SCALE_COL = 2 * TMAX;
+  static constexpr int SETS = 4;                   // groups of scales in TMEM
+  static constexpr uint32_t SET_COLS = 16;         // rows of B in the first 4 columns, of A from the 8th on
   static constexpr uint32_t EPI_ARRIVALS = 2 * EPI_WARPS;
   static constexpr uint32_t SCALE_ARRIVALS = 2 * 4;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(SCALE_COL + 2 * 32 <= TMEM_COLS, "TMEM budget");
+  static_assert(SCALE_COL + SETS * SET_COLS <= TMEM_COLS, "TMEM budget");
   static_assert(A_BOX % 1024 == 0 && B_BOX % 1024 == 0, "swizzle atoms of 1024 bytes");
 };
 
@@ -110,6 +112,13 @@ __device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t adesc, uint
       "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p)::"memory");
+  return p != 0;
 }
 // Each thread stores words to consecutive TMEM columns of its own lane.
 __device__ __forceinline__ void tmem_st_x4(uint32_t t, const uint32_t (&v)[4]) {
@@ -192,12 +201,12 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;   // [2] accumulator complete
   uint64_t* tempty = tfull + 2;          // [2] accumulator read
-  uint64_t* sfull = tempty + 2;          // [2] scales of a group in TMEM
-  uint64_t* sempty = sfull + 2;          // [2] scales read by the group's MMAs
-  uint64_t* drain = sempty + 2;
+  uint64_t* sfull = tempty + 2;          // [SETS] scales of a group in TMEM
+  uint64_t* sempty = sfull + C::SETS;    // [SETS] scales read by the group's MMAs
+  uint64_t* drain = sempty + C::SETS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(C::BAR_BYTES >= (2 * C::STAGES + 9) * 8 + 8, "barrier area");
+  static_assert(C::BAR_BYTES >= (2 * C::STAGES + 2 * C::SETS + 5) * 8 + 8, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -208,6 +217,8 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], C::EPI_ARRIVALS);
+    }
+    for (int b = 0; b < C::SETS; ++b) {
       mbar_init(&sfull[b], C::SCALE_ARRIVALS);
       mbar_init(&sempty[b], 1);
     }
@@ -266,14 +277,22 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ------------------------------------------------------------ MMA issuer
+      // The whole warp runs the loop, so that addresses and descriptors stay in
+      // uniform registers; one elected lane issues.  An MMA lasts T / 2 cycles: issued by
+      // a divergent lane that rebuilt its descriptors, each took longer than that
+      // (8192 x 14336 x 4096 in 473 us instead of 326).
       int st = 0, grp = 0, tile = 0;
       bool ok = true;
+      const uint32_t base = smem_u32(tiles);
+      auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, !*abort_flag && mbar_wait_cluster(bar, parity));
+      };
       for (int t = cid; t < a.items && ok; t += ncl, ++tile) {
         const F8Item it = decode_item(a, t);
         const int abuf = tile & 1;
-        if (*abort_flag || !mbar_wait_cluster(&tempty[abuf], ((tile >> 1) & 1) ^ 1)) {
+        if (!warp_wait(&tempty[abuf], ((tile >> 1) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -282,43 +301,56 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         const int kb0 = it.g0 * 4, kb1 = min(a.kblocks, it.g1 * 4);
         for (int kb = kb0; kb < kb1; kb += C::KPS, ++st) {
           const int s = st % C::STAGES;
-          if (((kb - kb0) & 3) == 0) {  // a new group of four blocks: its scales
-            if (*abort_flag || !mbar_wait_cluster(&sfull[grp & 1], (grp >> 1) & 1)) {
+          const uint32_t in_group = static_cast<uint32_t>(kb) & 3u;
+          if (in_group == 0) {  // a new group of four blocks: its scales
+            if (!warp_wait(&sfull[grp % C::SETS], (grp / C::SETS) & 1)) {
               ok = false;
               break;
             }
           }
-          if (*abort_flag || !mbar_wait_cluster(&full[s], (st / C::STAGES) & 1)) {
+          if (!warp_wait(&full[s], (st / C::STAGES) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const int nb = min(C::KPS, kb1 - kb);
-          const uint32_t b0 = smem_u32(tiles + s * C::STAGE), a0 = b0 + C::KPS * C::B_BOX;
-          const uint32_t sc = tmem + C::SCALE_COL + (grp & 1) * 32;
-          for (int q = 0; q < nb; ++q) {
-            const uint32_t id = static_cast<uint32_t>((kb + q) & 3);
-            const uint32_t idesc = a.idesc | (id << 29) | (id << 4);
-            const int steps = kb + q == a.kblocks - 1 ? a.tail_steps : 4;
-            for (int kk = 0; kk < steps; ++kk)
-              mma_pair_scaled(d, make_sdesc(b0 + q * C::B_BOX + kk * 32, 16, 1024, 2u),
-                              make_sdesc(a0 + q * C::A_BOX + kk * 32, 16, 1024, 2u), idesc, sc, sc + 8,
-                              (kb + q != kb0 || kk != 0) ? 1u : 0u);
+          const uint64_t bd = make_sdesc(base + s * C::STAGE, 16, 1024, 2u);
+          const uint64_t ad = make_sdesc(base + s * C::STAGE + C::KPS * C::B_BOX, 16, 1024, 2u);
+          const uint32_t sc = tmem + C::SCALE_COL + (grp % C::SETS) * C::SET_COLS;
+          const uint32_t idesc = a.idesc | (in_group << 29) | (in_group << 4);
+          const bool whole = nb == C::KPS && (kb + C::KPS < a.kblocks || a.tail_steps == 4);
+          const bool group_end = in_group == 4 - C::KPS || kb + C::KPS >= kb1;
+          if (elect_one()) {
+            if (whole) {
+#pragma unroll
+              for (int q = 0; q < C::KPS; ++q)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_pair_scaled(d, bd + (q * C::B_BOX + kk * 32) / 16, ad + (q * C::A_BOX + kk * 32) / 16,
+                                  idesc + q * ((1u << 29) | (1u << 4)), sc, sc + 8, (q | kk) != 0 || kb != kb0 ? 1u : 0u);
+            } else {
+              for (int q = 0; q < nb; ++q) {
+                const int steps = kb + q == a.kblocks - 1 ? a.tail_steps : 4;
+                for (int kk = 0; kk < steps; ++kk)
+                  mma_pair_scaled(d, bd + (q * C::B_BOX + kk * 32) / 16, ad + (q * C::A_BOX + kk * 32) / 16,
+                                  idesc + q * ((1u << 29) | (1u << 4)), sc, sc + 8, (q | kk) != 0 || kb != kb0 ? 1u : 0u);
+              }
+            }
+            tc_commit_pair(&empty[s], 0x3);
+            if (group_end) tc_commit_pair(&sempty[grp % C::SETS], 0x3);
+            if (kb + C::KPS >= kb1) tc_commit_pair(&tfull[abuf], 0x3);
           }
-          tc_commit_pair(&empty[s], 0x3);
-          if (((kb - kb0) & 3) == 4 - C::KPS || kb + C::KPS >= kb1) {  // the group's last stage
-            tc_commit_pair(&sempty[grp & 1], 0x3);
-            ++grp;
-          }
+          __syncwarp();
+          if (group_end) ++grp;
         }
-        if (!ok) break;
-        tc_commit_pair(&tfull[abuf], 0x3);
       }
       if (!ok) {
-        atomicOr(a.status, kStatusTimeout);
+        if (lane == 0) atomicOr(a.status, kStatusTimeout);
         *abort_flag = 1;
       }
-      tc_commit_pair(drain, 0x1);
+      // tcgen05.commit covers the MMAs of the thread that issues it
+      if (elect_one()) tc_commit_pair(drain, 0x1);
+      __syncwarp();
       mbar_wait(drain, 0);
     }
   } else if (warp < C::EPI_WARP) {
@@ -326,32 +358,48 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's quarter of the lanes
     int grp = 0;
     bool ok = true;
-    for (int t = cid; t < a.items && ok; t += ncl) {
-      const F8Item it = decode_item(a, t);
-      const long long n0 = it.i * 256LL + rank * C::BN, m0 = static_cast<long long>(it.j) * a.tile_m;
-      for (int g = it.g0; g < it.g1; ++g, ++grp) {
-        uint32_t wb[4], wa[8];
+    uint32_t wb[4], wa[8];
+    // words of group g of an item: rows of B, rows of A
+    auto load = [&](const F8Item& it, int g) {
+      const long long n0 = it.i * 256LL + rank * C::BN + lane, m0 = static_cast<long long>(it.j) * a.tile_m + lane;
+      const uint32_t* sb = a.sb + g * a.sb_rows + n0;
+      const uint32_t* sa = a.sa + g * a.sa_rows + m0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const long long r = n0 + j * 32 + lane;
-          wb[j] = r < a.n ? __ldg(a.sb + g * a.sb_rows + r) : 0x7f7f7f7fu;
-        }
+      for (int j = 0; j < 4; ++j) wb[j] = n0 + j * 32 < a.n ? __ldg(sb + j * 32) : 0x7f7f7f7fu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const long long r = m0 + j * 32 + lane;
-          wa[j] = j * 32 < a.tile_m && r < a.m ? __ldg(a.sa + g * a.sa_rows + r) : 0x7f7f7f7fu;
-        }
-        if (lane == 0) ok = !*abort_flag && mbar_wait(&sempty[grp & 1], ((grp >> 1) & 1) ^ 1);
+      for (int j = 0; j < 8; ++j)
+        wa[j] = j * 32 < a.tile_m && m0 + j * 32 < a.m ? __ldg(sa + j * 32) : 0x7f7f7f7fu;
+    };
+    int t = cid;
+    if (t < a.items) {
+      F8Item it = decode_item(a, t);
+      int g = it.g0;
+      load(it, g);
+      while (true) {
+        if (lane == 0) ok = !*abort_flag && mbar_wait(&sempty[grp % C::SETS], ((grp / C::SETS) & 1) ^ 1);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sc = tmem + lanes + C::SCALE_COL + (grp & 1) * 32;
+        const uint32_t sc = tmem + lanes + C::SCALE_COL + (grp % C::SETS) * C::SET_COLS;
         tmem_st_x4(sc, wb);
         tmem_st_x8(sc + 8, wa);
+        // the next group's words are on their way while this one is stored
+        bool more = true;
+        if (++g == it.g1) {
+          t += ncl;
+          more = t < a.items;
+          if (more) {
+            it = decode_item(a, t);
+            g = it.g0;
+          }
+        }
         tmem_st_wait();
+        if (more) load(it, g);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_cluster(&sfull[grp & 1], 0));
+        if (lane == 0) mbar_arrive_cluster(mapa_cluster(&sfull[grp % C::SETS], 0));
+        ++grp;
+        if (!more) break;
       }
     }
     if (!ok) {
