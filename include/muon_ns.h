@@ -432,10 +432,10 @@ MUON_API muon_status muon_partition(const double* cost, int count, int world, in
  *   data   [rows][ld] e4m3 or e5m2; 16-byte aligned, ld a multiple of 16 that is at
  *          least cols (rounded up to 16 where a call of this library writes it;
  *          the bytes from cols up to there are unspecified)
- *   scale  [ceil(cols / 512)][rows rounded up to 4][4] bytes, 4-byte aligned: the
+ *   scale  [ceil(cols / 512)][rows rounded up to 4][4] bytes, 16-byte aligned: the
  *          scale of columns 128 kb .. 128 kb + 127 of row r is 2^(s - 127), s the byte
  *          at [kb / 4][r][kb % 4].  255 stands for NaN.  Entries of no row or no block
- *          are written as 127 (1) and never read.
+ *          are written as 127 (1); what they hold does not matter.
  * Element (r, c) stands for data * scale.  A scale shared by 128 x 128 elements is
  * kept once for each of its rows.
  */

@@ -22,13 +22,17 @@
 // TMEM (512 columns): two accumulators of 224, so the epilogue of one tile overlaps
 // the next main loop, and four sets of scales (4 + 7 columns each).
 //
-// Warp roles (448 threads):
+// Warp roles (480 threads):
 //   warp 0       TMA producer: stages of 256 of K (two swizzled 128-byte boxes per operand)
 //   warp 1       TMEM allocation; the leader's lane 0 issues the MMAs
-//   warps 2..5   scales: every warp copies the words of all rows of the tile to its
+//   warps 2..5   scales: every warp stores the words of all rows of the tile to its
 //                own quarter of TMEM's lanes (the MMA reads a copy in each quarter),
-//                a 512-deep group ahead of the MMAs
+//                up to four 512-deep groups ahead of the MMAs
 //   warps 6..13  epilogue: two warps per lane quarter, alternating 32-column chunks
+//   warp 14      fetches the words to shared memory, up to eight groups ahead: behind a
+//                queue of TMA loads a fetch takes 1500 to 2500 cycles, and one that
+//                was issued a group (1792 cycles) ahead held the MMAs up at every
+//                other stage (8192 x 14336 x 4096 in 326 us instead of 308)
 //
 // When there are too few tiles to fill the GPU, K is split: each part's fp32 sums go to
 // the caller's workspace and a second kernel adds them in order.
@@ -59,14 +63,16 @@ struct F8Cfg {
   static constexpr int A_BOX = TMAX / 2 * KB;
   static constexpr int STAGE = KPS * (B_BOX + A_BOX);
   static constexpr int STAGES = 3;
-  static constexpr int SCALE_WARP = 2, EPI_WARP = 6, EPI_WARPS = 8;
-  static constexpr int THREADS = 32 * (EPI_WARP + EPI_WARPS);
-  static constexpr int BAR_BYTES = 256;
-  static constexpr int SMEM = STAGES * STAGE + BAR_BYTES + 1024;
+  static constexpr int EPI_WARP = 6, EPI_WARPS = 8, LOAD_WARP = EPI_WARP + EPI_WARPS;
+  static constexpr int THREADS = 32 * (LOAD_WARP + 1);
+  static constexpr int SETS = 4;                     // groups of scales in TMEM
+  static constexpr int SLOTS = 8;                    // and in shared memory
+  static constexpr int SCALE_SLOT = (BN + 256) * 4;  // read in 32-row pieces, up to 256 rows of A
+  static constexpr int BAR_BYTES = 512;
+  static constexpr int SMEM = STAGES * STAGE + SLOTS * SCALE_SLOT + BAR_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t ACC_COLS = TMAX;
   static constexpr uint32_t SCALE_COL = 2 * TMAX;
-  static constexpr int SETS = 4;                   // groups of scales in TMEM
   static constexpr uint32_t SET_COLS = 16;         // rows of B in the first 4 columns, of A from the 8th on
   static constexpr uint32_t EPI_ARRIVALS = 2 * EPI_WARPS;
   static constexpr uint32_t SCALE_ARRIVALS = 2 * 4;
@@ -103,6 +109,12 @@ __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* m, uint32_t 
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y)
       : "memory");
 }
+// 16-byte aligned global -> shared copy of whole 16 bytes, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 // D[tmem] (+)= (A scale_a) (B scale_b) over the pair, 32 of K; scales in TMEM, one byte per row and 32 of K.
 __device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                                 uint32_t sfb, uint32_t accumulate) {
@@ -112,6 +124,9 @@ __device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t adesc, uint
       "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -197,16 +212,19 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
   using C = F8Cfg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + C::STAGES * C::STAGE);
+  uint8_t* scales = tiles + C::STAGES * C::STAGE;  // [SLOTS] words of the rows of B, then of A
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::SLOTS * C::SCALE_SLOT);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;   // [2] accumulator complete
   uint64_t* tempty = tfull + 2;          // [2] accumulator read
   uint64_t* sfull = tempty + 2;          // [SETS] scales of a group in TMEM
   uint64_t* sempty = sfull + C::SETS;    // [SETS] scales read by the group's MMAs
-  uint64_t* drain = sempty + C::SETS;
+  uint64_t* sload = sempty + C::SETS;    // [SLOTS] scales of a group in shared memory
+  uint64_t* sfree = sload + C::SLOTS;    // [SLOTS] and copied on
+  uint64_t* drain = sfree + C::SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(C::BAR_BYTES >= (2 * C::STAGES + 2 * C::SETS + 5) * 8 + 8, "barrier area");
+  static_assert(C::BAR_BYTES >= (2 * C::STAGES + 2 * C::SETS + 2 * C::SLOTS + 5) * 8 + 8, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -221,6 +239,10 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
     for (int b = 0; b < C::SETS; ++b) {
       mbar_init(&sfull[b], C::SCALE_ARRIVALS);
       mbar_init(&sempty[b], 1);
+    }
+    for (int b = 0; b < C::SLOTS; ++b) {
+      mbar_init(&sload[b], 1);
+      mbar_init(&sfree[b], 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -358,48 +380,30 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's quarter of the lanes
     int grp = 0;
     bool ok = true;
-    uint32_t wb[4], wa[8];
-    // words of group g of an item: rows of B, rows of A
-    auto load = [&](const F8Item& it, int g) {
-      const long long n0 = it.i * 256LL + rank * C::BN + lane, m0 = static_cast<long long>(it.j) * a.tile_m + lane;
-      const uint32_t* sb = a.sb + g * a.sb_rows + n0;
-      const uint32_t* sa = a.sa + g * a.sa_rows + m0;
+    for (int t = cid; t < a.items && ok; t += ncl) {
+      const F8Item it = decode_item(a, t);
+      for (int g = it.g0; g < it.g1; ++g, ++grp) {
+        const int slot = grp % C::SLOTS, set = grp % C::SETS;
+        ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sload[slot], (grp / C::SLOTS) & 1));
+        if (!ok) break;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(scales + slot * C::SCALE_SLOT) + lane;
+        uint32_t wb[4], wa[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wb[j] = n0 + j * 32 < a.n ? __ldg(sb + j * 32) : 0x7f7f7f7fu;
+        for (int j = 0; j < 4; ++j) wb[j] = w[j * 32];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        wa[j] = j * 32 < a.tile_m && m0 + j * 32 < a.m ? __ldg(sa + j * 32) : 0x7f7f7f7fu;
-    };
-    int t = cid;
-    if (t < a.items) {
-      F8Item it = decode_item(a, t);
-      int g = it.g0;
-      load(it, g);
-      while (true) {
-        if (lane == 0) ok = !*abort_flag && mbar_wait(&sempty[grp % C::SETS], ((grp / C::SETS) & 1) ^ 1);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (int j = 0; j < 8; ++j) wa[j] = w[C::BN + j * 32];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfree[slot]);
+        ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sempty[set], ((grp / C::SETS) & 1) ^ 1));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sc = tmem + lanes + C::SCALE_COL + (grp % C::SETS) * C::SET_COLS;
+        const uint32_t sc = tmem + lanes + C::SCALE_COL + set * C::SET_COLS;
         tmem_st_x4(sc, wb);
         tmem_st_x8(sc + 8, wa);
-        // the next group's words are on their way while this one is stored
-        bool more = true;
-        if (++g == it.g1) {
-          t += ncl;
-          more = t < a.items;
-          if (more) {
-            it = decode_item(a, t);
-            g = it.g0;
-          }
-        }
         tmem_st_wait();
-        if (more) load(it, g);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_cluster(&sfull[grp % C::SETS], 0));
-        ++grp;
-        if (!more) break;
+        if (lane == 0) mbar_arrive_cluster(mapa_cluster(&sfull[set], 0));
       }
     }
     if (!ok) {
@@ -407,6 +411,35 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
       *abort_flag = 1;
     }
     __syncwarp();
+  } else if (warp == C::LOAD_WARP) {
+    if (lane == 0) {
+      // ------------------------------------------------------- scale fetch
+      int grp = 0;
+      bool ok = true;
+      for (int t = cid; t < a.items && ok; t += ncl) {
+        const F8Item it = decode_item(a, t);
+        const long long n0 = it.i * 256LL + rank * C::BN, m0 = static_cast<long long>(it.j) * a.tile_m;
+        const uint32_t nb = static_cast<uint32_t>(max(0LL, min(static_cast<long long>(C::BN), a.sb_rows - n0))) * 4;
+        const uint32_t na = static_cast<uint32_t>(min(static_cast<long long>(a.tile_m), a.sa_rows - m0)) * 4;
+        for (int g = it.g0; g < it.g1; ++g, ++grp) {
+          const int slot = grp % C::SLOTS;
+          if (*abort_flag || !mbar_wait(&sfree[slot], ((grp / C::SLOTS) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* p = scales + slot * C::SCALE_SLOT;
+          mbar_arrive_expect_tx(&sload[slot], nb + na);
+          if (nb) bulk_load(p, a.sb + g * a.sb_rows + n0, nb, &sload[slot]);
+          bulk_load(p + C::BN * 4, a.sa + g * a.sa_rows + m0, na, &sload[slot]);
+        }
+      }
+      if (!ok) {
+        atomicOr(a.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      // every copy lands before the CTA exits
+      for (int q = grp > C::SLOTS ? grp - C::SLOTS : 0; q < grp; ++q) mbar_wait(&sload[q % C::SLOTS], (q / C::SLOTS) & 1);
+    }
   } else {
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3, part = (warp - C::EPI_WARP) >> 2;

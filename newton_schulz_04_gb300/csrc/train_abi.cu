@@ -106,8 +106,8 @@ static muon_status check_fp8_out(const char* name, const void* q, const void* sc
                                  long long ld) {
   if (!q && !scale) return MUON_OK;
   if (!q || !scale) return fail(MUON_ERR_ARG, "%s: data and scale go together", name);
-  if (misaligned(q, 16) || misaligned(scale, 4) || ld % 16)
-    return fail(MUON_ERR_ALIGN, "%s: data must be 16-byte aligned with a row stride that is a multiple of 16", name);
+  if (misaligned(q, 16) || misaligned(scale, 16) || ld % 16)
+    return fail(MUON_ERR_ALIGN, "%s: data and scale must be 16-byte aligned, the row stride a multiple of 16", name);
   if (ld < (cols + 15) / 16 * 16 && rows > 0)
     return fail(MUON_ERR_SHAPE, "%s: row stride %lld does not hold %lld columns padded to 16", name, ld, cols);
   return MUON_OK;
@@ -285,8 +285,8 @@ muon_status muon_fp8_matmul(const void* a, int64_t lda, const void* a_scale, muo
     for (int i = 0; i < 2; ++i) {
       const char name = i ? 'b' : 'a';
       if (!p[i] || !s[i]) return fail(MUON_ERR_ARG, "%c or its scale is NULL", name);
-      if (misaligned(p[i], 16) || ld[i] % 16 || misaligned(s[i], 4))
-        return fail(MUON_ERR_ALIGN, "%c must be 16-byte aligned with a row stride that is a multiple of 16", name);
+      if (misaligned(p[i], 16) || ld[i] % 16 || misaligned(s[i], 16))
+        return fail(MUON_ERR_ALIGN, "%c and its scale must be 16-byte aligned, %c's row stride a multiple of 16", name, name);
       if (ld[i] < k) return fail(MUON_ERR_SHAPE, "%c: row stride %lld < k=%lld", name, ld[i], static_cast<long long>(k));
       if (overlap(out, span(m, n, ldc, size), p[i], span(rows[i], k, ld[i], 1)) ||
           overlap(out, span(m, n, ldc, size), s[i], static_cast<long long>(muon_fp8_scale_bytes(rows[i], k))))

@@ -141,6 +141,8 @@ class Fp8Tensor:
             raise ValueError("elements of a row must be consecutive and rows must not overlap")
         if data.numel() and (data.data_ptr() % 16 or (rows > 1 and data.stride(0) % 16)):
             raise ValueError("data must be 16-byte aligned with a row stride that is a multiple of 16")
+        if scale.numel() and scale.data_ptr() % 16:
+            raise ValueError("scale must be 16-byte aligned")
         self.data, self.scale = data, scale
 
     @classmethod
