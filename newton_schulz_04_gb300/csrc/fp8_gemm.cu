@@ -125,6 +125,12 @@ __device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t adesc, uint
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
+// Arrive on a barrier that may be the peer CTA's, where only TMEM is handed over: tcgen05.wait and the
+// tcgen05 fences order that, and a release at cluster scope would wait for every
+// access of this thread in flight, 2000 cycles behind a queue of TMA loads.
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_cluster(&sfull[set], 0));
+        if (lane == 0) mbar_arrive_tmem(mapa_cluster(&sfull[set], 0));
       }
     }
     if (!ok) {
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_cluster(&tempty[abuf], 0));
+      if (lane == 0) mbar_arrive_tmem(mapa_cluster(&tempty[abuf], 0));
     }
     if (!ok) {
       if (lane == 0) atomicOr(a.status, kStatusTimeout);
