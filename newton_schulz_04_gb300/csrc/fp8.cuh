@@ -30,18 +30,26 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax_bits, int top) 
 __device__ __forceinline__ float fp8_inverse_scale(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - byte) << 23);
 }
-// Two values to 8 bits, round to nearest even; `lo` in the low byte.
-__device__ __forceinline__ uint32_t fp8_pack2(float lo, float hi, bool e5m2) {
-  uint16_t r;
-  if (e5m2) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+// Values to 8 bits, round to nearest even; the first in the low byte.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+  uint32_t r;
+  if (E5M2)
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e5m2x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
-__device__ __forceinline__ uint2 fp8_pack8(const float (&v)[8], float inv, bool e5m2) {
-  uint2 r;
-  r.x = fp8_pack2(v[0] * inv, v[1] * inv, e5m2) | fp8_pack2(v[2] * inv, v[3] * inv, e5m2) << 16;
-  r.y = fp8_pack2(v[4] * inv, v[5] * inv, e5m2) | fp8_pack2(v[6] * inv, v[7] * inv, e5m2) << 16;
-  return r;
+template <bool E5M2>
+__device__ __forceinline__ uint2 fp8_pack8(const float (&v)[8], float inv) {
+  return make_uint2(fp8_pack4<E5M2>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    fp8_pack4<E5M2>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
 // Byte offset of the scale of block kb of row r; rows4 = rows rounded up to 4.
 __host__ __device__ __forceinline__ long long fp8_scale_offset(long long kb, long long r, long long rows4) {

@@ -67,7 +67,8 @@ __device__ __forceinline__ void store_q8(const RmsNormArgs& a, long long row, in
   if (!live) return;
   // up to the row's next multiple of 16 bytes: columns past the end hold 0
   if (col < ((a.cols + 15) & ~15))
-    *reinterpret_cast<uint2*>(a.q + row * a.ldq + col) = fp8_pack8(y, fp8_inverse_scale(byte), a.fmt != 0);
+    *reinterpret_cast<uint2*>(a.q + row * a.ldq + col) =
+        a.fmt ? fp8_pack8<true>(y, fp8_inverse_scale(byte)) : fp8_pack8<false>(y, fp8_inverse_scale(byte));
   const int kb = col >> 7, blocks = ((a.cols + 511) >> 9) * 4;
   if ((threadIdx.x & 15) == 0 && kb < blocks) {
     const long long rows4 = (a.rows + 3) & ~3LL;
