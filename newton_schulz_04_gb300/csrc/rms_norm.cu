@@ -66,27 +66,43 @@ __device__ __forceinline__ float row_sum(float v, float* sh) {
   return s;
 }
 
-// y's 8-bit copy of one 8-column piece: all 16 lanes of the 128-column block call.
-__device__ __forceinline__ void store_q8(const RmsNormArgs& a, long long row, int col, const float (&y)[8], bool live) {
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(y[i]));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const uint32_t byte = fp8_scale_byte(m, a.fmt ? 15 : 8);
-  if (!live) return;
-  // up to the row's next multiple of 16 bytes: columns past the end hold 0
-  if (col < ((a.cols + 15) & ~15))
-    *reinterpret_cast<uint2*>(a.q + row * a.ldq + col) =
-        a.fmt ? fp8_pack8<true>(y, fp8_inverse_scale(byte)) : fp8_pack8<false>(y, fp8_inverse_scale(byte));
-  const int kb = col >> 7, blocks = ((a.cols + 511) >> 9) * 4;
-  if ((threadIdx.x & 15) == 0 && kb < blocks) {
-    const long long rows4 = (a.rows + 3) & ~3LL;
-    a.qscale[fp8_scale_offset(kb, row, rows4)] = static_cast<uint8_t>(byte);
-    if (row == a.rows - 1)  // scales of no row are 1
-      for (long long r = a.rows; r < rows4; ++r) a.qscale[fp8_scale_offset(kb, r, rows4)] = 127;
+// y's 8-bit copy.  A thread holds pieces t, t + G, ... of 8 columns (G a multiple of 16),
+// so the 16 lanes of a 128-column block are neighbours.
+struct QOut {
+  uint8_t* data;   // this row, column 8 t
+  uint8_t* scale;  // scale word of this row, first group
+  int t;
+  long long rows4;
+  __device__ __forceinline__ QOut(const RmsNormArgs& a, long long row, int t_) : t(t_), rows4((a.rows + 3) & ~3LL) {
+    data = a.q + (a.q ? row * a.ldq + 8 * t_ : 0);
+    scale = a.qscale + (a.q ? row * 4 : 0);
   }
-}
+  __device__ __forceinline__ void advance(const RmsNormArgs& a, long long rows) {
+    data += rows * a.ldq;
+    scale += rows * 4;
+  }
+  // piece `piece` + t (piece a multiple of G); all lanes call.  Up to the row's
+  // next multiple of 16 bytes: columns past the end hold 0.
+  __device__ __forceinline__ void store(const RmsNormArgs& a, int piece, const float (&y)[8], bool live, bool last) const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(y[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t byte = fp8_scale_byte(m, a.fmt ? 15 : 8);
+    if (!live) return;
+    const float inv = fp8_inverse_scale(byte);
+    if ((piece + t) * 8 < ((a.cols + 15) & ~15))
+      *reinterpret_cast<uint2*>(data + piece * 8) = a.fmt ? fp8_pack8<true>(y, inv) : fp8_pack8<false>(y, inv);
+    const int kb = (piece + t) >> 4;
+    if ((t & 15) == 0 && kb < ((a.cols + 511) >> 9) * 4) {
+      uint8_t* p = scale + (kb >> 2) * rows4 * 4 + (kb & 3);
+      *p = static_cast<uint8_t>(byte);
+      if (last)  // scales of no row are 1
+        for (long long r = a.rows; r < rows4; ++r) p[(r - a.rows + 1) * 4] = 127;
+    }
+  }
+};
 
 // Scale words are four blocks: blocks first, first + step, ... past the last column.
 __device__ __forceinline__ void pad_q_scales(const RmsNormArgs& a, long long row, int first, int step) {
@@ -114,12 +130,12 @@ struct Ring {
   __device__ __forceinline__ int at(int slot, int arr, int c, int p) const {
     return ((((slot * NA + arr) * C + c) * P + p) * TH + static_cast<int>(threadIdx.x)) * 16;
   }
-  // columns col .. col + 7 of a row (n of them exist)
-  __device__ __forceinline__ void fetch(int slot, int arr, int c, const T* row, int col, int n) const {
+  // Piece c of a row: src + 8 elements, `bytes` of which exist (the rest reads as 0).
+  __device__ __forceinline__ void fetch(int slot, int arr, int c, const T* src, int bytes) const {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int live = max(0, min(16 / static_cast<int>(sizeof(T)), n - p * 4)) * static_cast<int>(sizeof(T));
-      copy16(smem_u32(base + at(slot, arr, c, p)), live ? row + col + p * 4 : row, live);
+      const int b = P == 1 ? bytes : max(0, min(16, bytes - 16 * p));
+      copy16(smem_u32(base + at(slot, arr, c, p)), P == 1 || b ? src + p * 4 : src, b);
     }
   }
   __device__ __forceinline__ void read(int slot, int arr, int c, float (&v)[8]) const {
@@ -155,50 +171,63 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ float sh[2][TH / 32];
   const Ring<T, TH, C, S, 2> ring{ring_smem};
-  const int t = threadIdx.x % G;
-  int n[C];
+  constexpr bool KEEP = C <= 2;  // the weight stays in registers
+  const int t = threadIdx.x % G, rr = threadIdx.x / G;
+  int n[C], off[C];  // existing columns of each piece, and its first (0 where none exists)
 #pragma unroll
-  for (int c = 0; c < C; ++c) n[c] = max(0, min(8, a.cols - (c * G + t) * 8));
-  const long long step = static_cast<long long>(gridDim.x) * R, row0 = static_cast<long long>(blockIdx.x) * R + threadIdx.x / G;
-  auto fetch = [&](long long row, int slot) {
-    if (row < a.rows) {
+  for (int c = 0; c < C; ++c) {
+    n[c] = max(0, min(8, a.cols - (c * G + t) * 8));
+    off[c] = n[c] ? (c * G + t) * 8 : 0;
+  }
+  const long long step = static_cast<long long>(gridDim.x) * R, row0 = static_cast<long long>(blockIdx.x) * R + rr;
+  long long frow = row0;  // next row to fetch
+  const T* fx = static_cast<const T*>(a.x) + row0 * a.ldx;
+  const T* fr = a.residual ? static_cast<const T*>(a.residual) + row0 * a.ldr : nullptr;
+  auto fetch = [&](int slot) {
+    if (frow < a.rows) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        ring.fetch(slot, 0, c, static_cast<const T*>(a.x) + row * a.ldx, (c * G + t) * 8, n[c]);
-        if (a.residual) ring.fetch(slot, 1, c, static_cast<const T*>(a.residual) + row * a.ldr, (c * G + t) * 8, n[c]);
+      for (int c = 0; c < C; ++c) ring.fetch(slot, 0, c, fx + off[c], n[c] * static_cast<int>(sizeof(T)));
+      if (fr) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) ring.fetch(slot, 1, c, fr + off[c], n[c] * static_cast<int>(sizeof(T)));
       }
     }
     cp_async_commit();
+    frow += step;
+    fx += step * a.ldx;
+    if (fr) fr += step * a.ldr;
   };
   pdl_launch_dependents();
   pdl_wait();
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) fetch(row0 + s * step, s);
-  float w[C <= 2 ? C : 1][8];
-  if (C <= 2) {
+  for (int s = 0; s < S - 1; ++s) fetch(s);
+  float w[KEEP ? C : 1][8];
+  if (KEEP) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) load_weight8(a.weight, a.weight_dt, (c * G + t) * 8, n[c], n[c] == 8, w[c % (C <= 2 ? C : 1)]);
+    for (int c = 0; c < C; ++c) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[KEEP ? c : 0]);
   }
   const float inv_cols = 1.f / static_cast<float>(a.cols);
+  T* ph = static_cast<T*>(a.h) + (a.h ? row0 * a.ldh : 0);
+  T* py = static_cast<T*>(a.y) + (a.y ? row0 * a.ldy : 0);
+  QOut q(a, row0, t);
   int slot = 0, turn = 0;
   // all threads of a CTA take the same number of turns (the barrier in ring_sum)
-  for (long long base = static_cast<long long>(blockIdx.x) * R; base < a.rows; base += step, ++turn) {
-    const long long row = base + threadIdx.x / G;
-    const bool live = row < a.rows;
-    fetch(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+  for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
+    const bool live = R == 1 || row < a.rows;
+    fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
     float s[C][8];
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       ring.read(slot, 0, c, s[c]);
-      if (a.residual) {
+      if (fr) {
         float r[8];
         ring.read(slot, 1, c, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[c][i] += r[i];
       }
-      if (!live) {
+      if (R > 1 && !live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[c][i] = 0.f;
       }
@@ -206,30 +235,26 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
       for (int i = 0; i < 8; ++i) sum = fmaf(s[c][i], s[c][i], sum);
     }
     sum = ring_sum<G, TH>(sum, sh, turn);
-    const float rstd = 1.f / sqrtf(sum * inv_cols + a.eps);
+    const float rstd = rsqrtf(sum * inv_cols + a.eps);
     if (live && t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * G + t) * 8;
-      if (live && a.h) store8(static_cast<T*>(a.h) + row * a.ldh + col, n[c], n[c] == 8, s[c]);
-      if (C <= 2) {
+      if (live && a.h) store8(ph + off[c], n[c], n[c] == 8, s[c]);
+      if (!KEEP) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[c][i] *= rstd * w[c % (C <= 2 ? C : 1)][i];
-      } else {
-        float u[8];
-        load_weight8(a.weight, a.weight_dt, col, n[c], n[c] == 8, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[c][i] *= rstd * u[i];
-      }
+      for (int i = 0; i < 8; ++i) s[c][i] *= rstd * w[KEEP ? c : 0][i];
       if (n[c] < 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (i >= n[c]) s[c][i] = 0.f;
       }
-      if (live && a.y) store8(static_cast<T*>(a.y) + row * a.ldy + col, n[c], n[c] == 8, s[c]);
-      if (a.q) store_q8(a, row, col, s[c], live);
+      if (live && a.y) store8(py + off[c], n[c], n[c] == 8, s[c]);
+      if (a.q) q.store(a, c * G, s[c], live, row == a.rows - 1);
     }
     if (a.q && live) pad_q_scales(a, row, C * G / 16 + t, G);
+    ph += step * a.ldh;
+    py += step * a.ldy;
+    q.advance(a, step);
     slot = slot + 1 == S ? 0 : slot + 1;
   }
 }
@@ -274,7 +299,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(const RmsNo
       for (int i = 0; i < 8; ++i) sum = fmaf(s[c][i], s[c][i], sum);
   }
   sum = row_sum<G>(sum, sh);
-  const float rstd = 1.f / sqrtf(sum * (1.f / static_cast<float>(a.cols)) + a.eps);
+  const float rstd = rsqrtf(sum * (1.f / static_cast<float>(a.cols)) + a.eps);
+  const QOut q(a, live ? row : 0, t);
   if (live && t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
   for (int c = 0; c < (WIDE ? 1 : C); ++c) {
@@ -294,7 +320,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(const RmsNo
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < n ? v[i] * (rstd * w[i]) : 0.f;
       if (a.y) store8(static_cast<T*>(a.y) + row * a.ldy + col, n, full, v);
-      if (a.q) store_q8(a, row, col, v, live);
+      if (a.q) q.store(a, cc * G, v, live, row == a.rows - 1);
     }
   }
   if (a.q && live) pad_q_scales(a, row, chunks * G / 16 + t, G);
@@ -484,30 +510,42 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
   __shared__ float sh[2][TH / 32];
   const Ring<T, TH, C, S, 3> ring{ring_smem};
   const int t = threadIdx.x % G, rr = threadIdx.x / G;
-  int n[C];
+  int n[C], off[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) n[c] = max(0, min(8, a.cols - (c * G + t) * 8));
-  const long long step = static_cast<long long>(gridDim.x) * R;
-  auto fetch = [&](long long row, int slot) {
-    if (row < a.rows) {
+  for (int c = 0; c < C; ++c) {
+    n[c] = max(0, min(8, a.cols - (c * G + t) * 8));
+    off[c] = n[c] ? (c * G + t) * 8 : 0;
+  }
+  const long long step = static_cast<long long>(gridDim.x) * R, row0 = static_cast<long long>(blockIdx.x) * R + rr;
+  const bool add = a.dres && a.dx;
+  long long frow = row0;  // next row to fetch
+  const T* fd = static_cast<const T*>(a.dy) + row0 * a.lddy;
+  const T* fh = static_cast<const T*>(a.h) + row0 * a.ldh;
+  const T* fr = static_cast<const T*>(a.dres) + (add ? row0 * a.lddr : 0);
+  auto fetch = [&](int slot) {
+    if (frow < a.rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int col = (c * G + t) * 8;
-        ring.fetch(slot, 0, c, static_cast<const T*>(a.dy) + row * a.lddy, col, n[c]);
-        ring.fetch(slot, 1, c, static_cast<const T*>(a.h) + row * a.ldh, col, n[c]);
-        if (a.dres && a.dx) ring.fetch(slot, 2, c, static_cast<const T*>(a.dres) + row * a.lddr, col, n[c]);
+        const int bytes = n[c] * static_cast<int>(sizeof(T));
+        ring.fetch(slot, 0, c, fd + off[c], bytes);
+        ring.fetch(slot, 1, c, fh + off[c], bytes);
+        if (add) ring.fetch(slot, 2, c, fr + off[c], bytes);
       }
     }
     cp_async_commit();
+    frow += step;
+    fd += step * a.lddy;
+    fh += step * a.ldh;
+    fr += step * a.lddr;
   };
   pdl_launch_dependents();
   pdl_wait();
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) fetch(static_cast<long long>(blockIdx.x) * R + rr + s * step, s);
+  for (int s = 0; s < S - 1; ++s) fetch(s);
   float w[KEEP ? C : 1][8], dw[C][8];
   if (KEEP) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) load_weight8(a.weight, a.weight_dt, (c * G + t) * 8, n[c], n[c] == 8, w[KEEP ? c : 0]);
+    for (int c = 0; c < C; ++c) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[KEEP ? c : 0]);
   }
 #pragma unroll
   for (int c = 0; c < C; ++c)
@@ -515,14 +553,13 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
   const float inv_cols = 1.f / static_cast<float>(a.cols);
   int slot = 0, turn = 0;
-  const long long row0 = static_cast<long long>(blockIdx.x) * R + rr;
   float next_rstd = row0 < a.rows ? __ldg(a.rstd + row0) : 0.f;  // a row ahead
-  for (long long base = static_cast<long long>(blockIdx.x) * R; base < a.rows; base += step, ++turn) {
-    const long long row = base + rr;
-    const bool live = row < a.rows;
+  T* px = static_cast<T*>(a.dx) + (a.dx ? row0 * a.lddx : 0);
+  for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
+    const bool live = R == 1 || row < a.rows;
     const float rstd = next_rstd;
     next_rstd = row + step < a.rows ? __ldg(a.rstd + row + step) : 0.f;
-    fetch(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+    fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
     float d[C][8], x[C][8];
     float sum = 0.f;
@@ -530,11 +567,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
     for (int c = 0; c < C; ++c) {
       ring.read(slot, 0, c, d[c]);
       ring.read(slot, 1, c, x[c]);
-      if (!live) {
+      if (R > 1 && !live) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[c][i] = x[c][i] = 0.f;
       }
-      if (!KEEP) load_weight8(a.weight, a.weight_dt, (c * G + t) * 8, n[c], n[c] == 8, w[0]);
+      if (!KEEP) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[0]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sum = fmaf(d[c][i] * w[KEEP ? c : 0][i], x[c][i], sum);
@@ -547,8 +584,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         float v[8];
-        if (!KEEP) load_weight8(a.weight, a.weight_dt, (c * G + t) * 8, n[c], n[c] == 8, w[0]);
-        if (a.dres) {
+        if (!KEEP) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[0]);
+        if (add) {
           ring.read(slot, 2, c, v);
         } else {
 #pragma unroll
@@ -556,9 +593,10 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += rstd * (d[c][i] * w[KEEP ? c : 0][i] - x[c][i] * k);
-        store8(static_cast<T*>(a.dx) + row * a.lddx + (c * G + t) * 8, n[c], n[c] == 8, v);
+        store8(px + off[c], n[c], n[c] == 8, v);
       }
     }
+    px += step * a.lddx;
     slot = slot + 1 == S ? 0 : slot + 1;
   }
   if (!a.partial) return;
