@@ -102,8 +102,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.muon_partition.restype = i32
     lib.muon_clip_workspace_bytes.argtypes = [i32]
     lib.muon_clip_workspace_bytes.restype = sz
-    lib.muon_clip_grads.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i64),
-                                    ctypes.POINTER(ctypes.c_int32), i32, f32, f32, vp, vp, sz, vp]
+    lib.muon_clip_grads.argtypes = [vp, vp, vp, vp, i32, f32, f32, vp, vp, sz, vp]  # host arrays by address
     lib.muon_clip_grads.restype = i32
     lib.muon_rms_norm.argtypes = [vp, i64, vp, i64, vp, i32, i64, i64, f32, vp, i64, vp, i64, vp, vp, i64, vp, i32, i32,
                                   vp]

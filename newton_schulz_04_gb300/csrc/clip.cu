@@ -2,14 +2,15 @@
 //
 //   N = sqrt(sum_i sum_j g_ij^2)      c = min(1, max_norm / (N + eps))      out = round(g c)
 //
-// Two launches.  The first strides a fixed grid over chunks of 8192 elements of
-// the listed tensors (binary search over the chunk offsets) and leaves one partial
-// sum per CTA; which CTA sums which elements in which order is fixed, so the norm
-// has the same bits every time.  The second has every CTA add the partial sums (at
-// most a few thousand) in order and scale its chunks.  Without a pass over memory in
-// between, the floor is one read and one write of every gradient; reading them twice
-// is what the norm's dependence costs, less what the second pass finds in the 126 MB
-// L2: it runs the chunks in the reverse order.
+// Two launches.  The first gives every CTA of a fixed grid a contiguous run of the
+// listed tensors' 32 KB chunks and leaves one partial sum per CTA; which CTA sums
+// which elements in which order is fixed, so the norm has the same bits every
+// time.  The second has every CTA add the partial sums (608, in order) and scale its
+// run.  Bound by memory: the norm's dependence costs a second read of the gradients
+// that the floor (one read, one write) does not have, less what that read finds in the
+// 126 MB L2: each CTA scales its run backwards, from what it read last, and reads and
+// writes with the evict-first policy so as not to push out what is still to be read.
+// Its first chunk is on its way before the sums are complete.
 //
 // Sums: fp32 per thread, 64 bits across threads.  Squares that leave fp32's range
 // (a CTA's sum that is not finite, or below 2^-100) are summed again, scaled by
@@ -25,11 +26,13 @@
 
 namespace muon {
 
+constexpr int kClipParts = 8;  // 16-byte parts of a chunk per thread
+static_assert(kClipChunkBytes == kClipParts * 16 * 256, "one chunk is a CTA's pass");
+
 template <int MAX>
 struct ClipArgs {
   int count;
   int chunks;           // of this launch
-  int first;            // start[] of the first tensor: 0
   int nparts;           // partial sums over all launches
   float max_norm, eps;
   double* partial;
@@ -37,7 +40,7 @@ struct ClipArgs {
   long long numel[MAX];
   const void* g[MAX];
   void* out[MAX];
-  int start[MAX];       // first chunk of each tensor
+  int start[MAX + 1];   // first chunk of each tensor; start[count] = chunks
   unsigned char dt[MAX];  // dtype, | 16: 16-byte aligned
 };
 
@@ -51,22 +54,54 @@ __device__ __forceinline__ int clip_tensor(const ClipArgs<MAX>& a, int chunk) {
   }
   return lo;
 }
+// Chunks [lo, hi) of this CTA.
+template <int MAX>
+__device__ __forceinline__ int2 clip_run(const ClipArgs<MAX>& a) {
+  const long long n = a.chunks;
+  return make_int2(static_cast<int>(n * blockIdx.x / gridDim.x), static_cast<int>(n * (blockIdx.x + 1) / gridDim.x));
+}
 
-// Sum of (x s)^2 over elements e0 .. e0 + kClipChunk of a tensor, this thread's part.
+__device__ __forceinline__ void clip_unpack(const uint4& w, float (&v)[8], __nv_bfloat16 t) { unpack8(w, v, t); }
+__device__ __forceinline__ void clip_unpack(const uint4& w, float (&v)[8], __half t) { unpack8(w, v, t); }
+__device__ __forceinline__ void clip_unpack(const uint4& w, float (&v)[4], float) {
+  v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ uint4 clip_pack(const float (&v)[4], float) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
 template <typename T>
-__device__ __forceinline__ void clip_sum_chunk(const T* g, long long e0, long long n, bool aligned, float s,
-                                               float (&acc)[4]) {
+__device__ __forceinline__ uint4 clip_pack(const float (&v)[8], T) {
+  union {
+    uint4 w;
+    T e[8];
+  } u;
 #pragma unroll
-  for (int u = 0; u < kClipChunk / (8 * 256); ++u) {
-    const long long e = e0 + (u * 256 + threadIdx.x) * 8;
-    if (e < n) {
-      float v[8];
-      load8(g + e, static_cast<int>(min(n - e, 8LL)), aligned && e + 8 <= n, v);
+  for (int i = 0; i < 8; ++i) u.e[i] = from_f32<T>(v[i]);
+  return u.w;
+}
+
+// This thread's part of sum (x s)^2 over the chunk of n elements at g.
+template <typename T>
+__device__ __forceinline__ void clip_sum_chunk(const T* g, int n, bool aligned, float s, float (&acc)[4]) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));  // elements of a part
+  if (aligned && n == kClipChunkBytes / static_cast<int>(sizeof(T))) {
+    uint4 w[kClipParts];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+    for (int u = 0; u < kClipParts; ++u) w[u] = reinterpret_cast<const uint4*>(g)[u * 256 + threadIdx.x];
+#pragma unroll
+    for (int u = 0; u < kClipParts; ++u) {
+      float v[E];
+      clip_unpack(w[u], v, T());
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
         const float x = v[i] * s;
         acc[i & 3] = fmaf(x, x, acc[i & 3]);
       }
+    }
+  } else {
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const float x = to_f32(g[i]) * s;
+      acc[0] = fmaf(x, x, acc[0]);
     }
   }
 }
@@ -74,14 +109,18 @@ __device__ __forceinline__ void clip_sum_chunk(const T* g, long long e0, long lo
 template <int MAX>
 __device__ __forceinline__ float clip_thread_sum(const ClipArgs<MAX>& a, float s) {
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    const int t = clip_tensor(a, c);
-    const long long e0 = static_cast<long long>(c - a.start[t]) * kClipChunk, n = a.numel[t];
-    const bool al = a.dt[t] & 16;
+  const int2 run = clip_run(a);
+  int t = clip_tensor(a, run.x);
+  for (int c = run.x; c < run.y; ++c) {
+    while (a.start[t + 1] <= c) ++t;
+    const bool al = a.dt[t] & 16, wide = (a.dt[t] & 15) == MUON_FP32;
+    const int per = kClipChunkBytes / (wide ? 4 : 2);
+    const long long e0 = static_cast<long long>(c - a.start[t]) * per;
+    const int n = static_cast<int>(min(a.numel[t] - e0, static_cast<long long>(per)));
     switch (a.dt[t] & 15) {
-      case MUON_BF16: clip_sum_chunk(static_cast<const __nv_bfloat16*>(a.g[t]), e0, n, al, s, acc); break;
-      case MUON_FP16: clip_sum_chunk(static_cast<const __half*>(a.g[t]), e0, n, al, s, acc); break;
-      default: clip_sum_chunk(static_cast<const float*>(a.g[t]), e0, n, al, s, acc); break;
+      case MUON_BF16: clip_sum_chunk(static_cast<const __nv_bfloat16*>(a.g[t]) + e0, n, al, s, acc); break;
+      case MUON_FP16: clip_sum_chunk(static_cast<const __half*>(a.g[t]) + e0, n, al, s, acc); break;
+      default: clip_sum_chunk(static_cast<const float*>(a.g[t]) + e0, n, al, s, acc); break;
     }
   }
   return (acc[0] + acc[1]) + (acc[2] + acc[3]);
@@ -101,62 +140,84 @@ __device__ __forceinline__ double clip_block_sum(double v, double* sh) {
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(256) clip_norm_kernel(const __grid_constant__ ClipArgs<MAX> a) {
+__global__ void __launch_bounds__(256, kClipCtasPerSm) clip_norm_kernel(const __grid_constant__ ClipArgs<MAX> a) {
   __shared__ double sh[8];
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // after the wait: the scaling kernel reads the gradients before its own
   double sum = clip_block_sum(static_cast<double>(clip_thread_sum(a, 1.f)), sh);
   if (!(sum < 3e38)) sum = clip_block_sum(static_cast<double>(clip_thread_sum(a, 0x1p-80f)), sh) * 0x1p160;
   else if (sum < 0x1p-100) sum = clip_block_sum(static_cast<double>(clip_thread_sum(a, 0x1p100f)), sh) * 0x1p-200;
   if (threadIdx.x == 0) a.partial[blockIdx.x] = sum;
 }
 
-template <typename T>
-__device__ __forceinline__ void clip_scale_chunk(const T* g, T* out, long long e0, long long n, bool aligned, float c) {
+// out = round(g c) for a chunk of n elements; `factor` gives c, after this thread's loads are on their way.
+template <typename T, typename F>
+__device__ __forceinline__ void clip_scale_chunk(const T* g, T* out, int n, bool aligned, const F& factor) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  if (aligned && n == kClipChunkBytes / static_cast<int>(sizeof(T))) {
+    uint4 w[kClipParts];
 #pragma unroll
-  for (int u = 0; u < kClipChunk / (8 * 256); ++u) {
-    const long long e = e0 + (u * 256 + threadIdx.x) * 8;
-    if (e < n) {
-      const int k = static_cast<int>(min(n - e, 8LL));
-      const bool full = aligned && e + 8 <= n;
-      float v[8];
-      load8(g + e, k, full, v);
+    for (int u = 0; u < kClipParts; ++u) w[u] = __ldcs(reinterpret_cast<const uint4*>(g) + u * 256 + threadIdx.x);
+    const float c = factor();
+    if (c == 1.f && g == out) return;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= c;
-      store8(out + e, k, full, v);
+    for (int u = 0; u < kClipParts; ++u) {
+      float v[E];
+      clip_unpack(w[u], v, T());
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] *= c;
+      __stcs(reinterpret_cast<uint4*>(out) + u * 256 + threadIdx.x, clip_pack(v, T()));
     }
+  } else {
+    const float c = factor();
+    if (c == 1.f && g == out) return;
+    for (int i = threadIdx.x; i < n; i += 256) out[i] = from_f32<T>(to_f32(g[i]) * c);
   }
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(256) clip_scale_kernel(const __grid_constant__ ClipArgs<MAX> a) {
+__global__ void __launch_bounds__(256, kClipCtasPerSm) clip_scale_kernel(const __grid_constant__ ClipArgs<MAX> a) {
   __shared__ double sh[8];
   pdl_launch_dependents();
-  pdl_wait();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < a.nparts; i += 256) s += a.partial[i];
-  const float norm = static_cast<float>(sqrt(clip_block_sum(s, sh)));
-  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-  float c = a.max_norm / (norm + a.eps);
-  if (c > 1.f) c = 1.f;  // NaN stays
-  for (int k = blockIdx.x; k < a.chunks; k += gridDim.x) {
-    const int chunk = a.chunks - 1 - k;
-    const int t = clip_tensor(a, chunk);
-    if (c == 1.f && a.g[t] == a.out[t]) continue;
-    const long long e0 = static_cast<long long>(chunk - a.start[t]) * kClipChunk, n = a.numel[t];
-    const bool al = a.dt[t] & 16;
+  float c = 0.f;
+  bool known = false;
+  // The factor, on first use: every CTA adds the partial sums.
+  const auto factor = [&]() -> float {
+    if (!known) {
+      known = true;
+      pdl_wait();
+      double s = 0.0;
+      for (int i = threadIdx.x; i < a.nparts; i += 256) s += a.partial[i];
+      const float norm = static_cast<float>(sqrt(clip_block_sum(s, sh)));
+      if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
+      c = a.max_norm / (norm + a.eps);
+      if (c > 1.f) c = 1.f;  // NaN stays
+    }
+    return c;
+  };
+  const int2 run = clip_run(a);
+  int t = clip_tensor(a, max(run.y - 1, 0));
+  for (int k = run.y - 1; k >= run.x; --k) {
+    while (a.start[t] > k) --t;
+    if (known && c == 1.f && a.g[t] == a.out[t]) continue;
+    const bool al = a.dt[t] & 16, wide = (a.dt[t] & 15) == MUON_FP32;
+    const int per = kClipChunkBytes / (wide ? 4 : 2);
+    const long long e0 = static_cast<long long>(k - a.start[t]) * per;
+    const int n = static_cast<int>(min(a.numel[t] - e0, static_cast<long long>(per)));
     switch (a.dt[t] & 15) {
       case MUON_BF16:
-        clip_scale_chunk(static_cast<const __nv_bfloat16*>(a.g[t]), static_cast<__nv_bfloat16*>(a.out[t]), e0, n, al, c);
+        clip_scale_chunk(static_cast<const __nv_bfloat16*>(a.g[t]) + e0, static_cast<__nv_bfloat16*>(a.out[t]) + e0, n, al,
+                         factor);
         break;
       case MUON_FP16:
-        clip_scale_chunk(static_cast<const __half*>(a.g[t]), static_cast<__half*>(a.out[t]), e0, n, al, c);
+        clip_scale_chunk(static_cast<const __half*>(a.g[t]) + e0, static_cast<__half*>(a.out[t]) + e0, n, al, factor);
         break;
       default:
-        clip_scale_chunk(static_cast<const float*>(a.g[t]), static_cast<float*>(a.out[t]), e0, n, al, c);
+        clip_scale_chunk(static_cast<const float*>(a.g[t]) + e0, static_cast<float*>(a.out[t]) + e0, n, al, factor);
         break;
     }
   }
+  factor();  // a CTA without chunks (the norm alone) gets here first
 }
 
 // Fills the argument block with tensors [c0, c0 + n).
@@ -173,8 +234,10 @@ static void clip_fill(ClipArgs<MAX>& a, const void* const* grads, void* const* o
     a.start[i] = chunk;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(grads[k]) | (out ? reinterpret_cast<uintptr_t>(out[k]) : 0);
     a.dt[i] = static_cast<unsigned char>(dts[k] | (bits % 16 == 0 ? 16 : 0));
-    chunk += static_cast<int>((numel[k] + kClipChunk - 1) / kClipChunk);
+    const long long per = kClipChunkBytes / dtype_bytes(dts[k]);
+    chunk += static_cast<int>((numel[k] + per - 1) / per);
   }
+  a.start[n] = chunk;
   a.chunks = chunk;
 }
 
@@ -183,7 +246,6 @@ static cudaError_t run_clip(const void* const* grads, void* const* out, const in
                             int count, float max_norm, float eps, double* partial, int grid, float* norm,
                             cudaStream_t st) {
   ClipArgs<MAX> a;
-  a.first = 0;
   a.max_norm = max_norm;
   a.eps = eps;
   int parts = 0;
@@ -200,7 +262,7 @@ static cudaError_t run_clip(const void* const* grads, void* const* out, const in
   const int step = out ? MAX : count;  // without outputs one CTA turns the partial sums into the norm
   for (int c0 = 0; c0 < count || c0 == 0; c0 += std::max(step, 1)) {
     if (out) clip_fill(a, grads, out, numel, dts, c0, std::min(MAX, count - c0));
-    else a.chunks = 0;
+    else a.count = a.chunks = 0;
     a.norm = c0 == 0 ? norm : nullptr;
     const int g = std::max(1, std::min(grid, a.chunks));
     const cudaError_t e = launch_pdl(clip_scale_kernel<MAX>, dim3(g), dim3(256), 0, st, a);

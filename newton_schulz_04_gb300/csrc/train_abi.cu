@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -26,8 +27,17 @@ static bool overlap(const void* a, long long na, const void* b, long long nb) {
   return a && b && na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
 }
 
-// The device is an sm_103 GPU: its SM count, or 0 with *st set.
+// The device is an sm_103 GPU: its SM count (asked for once per device), or 0 with *st set.
 static int gpu(muon_status* st) {
+  static std::atomic<int> known[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
+    const int sms = known[dev].load(std::memory_order_relaxed);
+    if (sms) {
+      *st = MUON_OK;
+      return sms;
+    }
+  }
   int major = 0, minor = 0;
   const int sms = device_sms(&major, &minor, st);
   if (*st != MUON_OK) return 0;
@@ -35,6 +45,7 @@ static int gpu(muon_status* st) {
     *st = fail(MUON_ERR_UNSUPPORTED, "this library is built for sm_103a (GB300); device is sm_%d%d", major, minor);
     return 0;
   }
+  if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 static muon_status launched(cudaError_t e, const char* what, const char* why = nullptr) {
@@ -80,7 +91,7 @@ muon_status muon_clip_grads(const void* const* grads, void* const* out, const in
       return fail(MUON_ERR_ARG, "tensor %d: out overlaps the gradient", i);
     if (out && overlap(out[i], numel[i] * size, ws, static_cast<long long>(ws_bytes)))
       return fail(MUON_ERR_ARG, "tensor %d: out overlaps the workspace", i);
-    chunks += (numel[i] + kClipChunk - 1) / kClipChunk;
+    chunks += (numel[i] * size + kClipChunkBytes - 1) / kClipChunkBytes;
     if (chunks > 0x7fffffffLL) return fail(MUON_ERR_SHAPE, "too many elements");
   }
   muon_status st;

@@ -20,8 +20,8 @@ inline int dtype_bytes(int dt) { return dt == MUON_FP32 ? 4 : 2; }
 // Tensors per launch: two sizes of the argument block, so that a short list
 // does not pay for copying the long one (29 bytes per tensor, 32 KB at most).
 constexpr int kClipSmall = 64, kClipLarge = 1024;
-constexpr int kClipChunk = 8192;     // elements of one tensor that a CTA takes at a time
-constexpr int kClipCtasPerSm = 8;    // 256-thread CTAs
+constexpr int kClipChunkBytes = 32768;  // of one tensor, that a CTA takes at a time
+constexpr int kClipCtasPerSm = 4;       // 256-thread CTAs
 cudaError_t launch_clip(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* dts, int count,
                         float max_norm, float eps, double* partial, int grid, float* norm, cudaStream_t st);
 

@@ -13,6 +13,7 @@ gradient clipping by the global norm, the RMS norm with an 8-bit copy and its gr
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -33,30 +34,31 @@ def _dt(t: torch.Tensor, name: str) -> int:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}: bfloat16, float16 or float32") from None
 
 
-def _rows(t: torch.Tensor, name: str, cols=None):
+def _rows(t: torch.Tensor, name: str):
     """(rows, row stride) of a tensor seen as rows of its last dimension."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() == 2:  # the ordinary case, without a view
-        rows, width = t.shape
-        ld = t.stride(0)
-        unit = t.stride(1)
+    shape, strides = t.shape, t.stride()
+    dims = len(shape)
+    if dims == 2:  # the ordinary case, without a view
+        rows, width = shape
+        ld, unit = strides
     else:
-        if t.dim() < 1:
+        if dims < 1:
             raise ValueError(f"{name} must have at least one dimension")
-        width = t.shape[-1]
+        width, unit = shape[-1], strides[-1]
         try:
             v = t.view(-1, width) if width else t.reshape(0, 0)
         except RuntimeError:
             raise ValueError(f"{name}: the rows must be evenly spaced (one stride for all leading dimensions)") from None
-        rows, ld, unit = v.shape[0], v.stride(0), v.stride(1) if width else 1
-    if width > 1 and unit != 1:
+        rows, ld = v.shape[0], v.stride(0)
+    if unit != 1 and width > 1:
         raise ValueError(f"{name}: elements of a row must be consecutive (last stride 1, not {unit})")
-    if rows > 1 and ld < width:
-        raise ValueError(f"{name}: rows overlap (stride {ld} for {width} columns)")
-    if cols is not None and width != cols:
-        raise ValueError(f"{name} has {width} columns, {cols} expected")
-    return rows, max(ld, width)
+    if ld < width:
+        if rows > 1:
+            raise ValueError(f"{name}: rows overlap (stride {ld} for {width} columns)")
+        ld = width
+    return rows, ld
 
 
 def _like(t, ref, name):
@@ -64,55 +66,19 @@ def _like(t, ref, name):
         raise ValueError(f"{name} must have the shape, dtype and device of the input")
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not {ref.device}")
+def _workspace(workspace, device):
+    if not (workspace.is_cuda and workspace.is_contiguous() and workspace.device == device):
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _workspace(workspace, need, device, name="workspace"):
-    """(pointer, bytes) of the caller's workspace, or of a new one (returned to be kept alive)."""
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not (workspace.is_cuda and workspace.is_contiguous() and workspace.device == device):
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-class _on:
-    """Makes `stream` (None: the current one) current, so that tensors made within belong to it."""
-
-    def __new__(cls, stream, device):
-        if stream is None and device.index == torch.cuda.current_device():
-            return _HERE
-        return _Guard(stream, device)
-
-
-class _Here:
-    def __enter__(self):
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        return False
-
-
-class _Guard:
-    def __init__(self, stream, device):
-        self.stream, self.device = stream, device
-
-    def __enter__(self):
-        self.dev = torch.cuda.device(self.device)
-        self.dev.__enter__()
-        self.ctx = torch.cuda.stream(self.stream)
-        self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        self.ctx.__exit__(*exc)
-        return self.dev.__exit__(*exc)
-
-
-_HERE = _Here()
+def _on(stream, device, call, *args):
+    """call(*args, stream pointer) with `device` and `stream` (None: its current one) current, so that the tensors made
+    within belong to that stream."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(*args, torch.cuda.current_stream().cuda_stream)
 
 
 # ---------------------------------------------------------------- 8-bit matrices
@@ -196,22 +162,25 @@ def fp8_quantize(x: torch.Tensor, fmt: str = "e4m3", square: bool = False, rows:
     The first is x as an operand summed over its columns, the second x transposed, summed over x's rows; each is an
     Fp8Tensor, or None where `rows` / `cols` is false.  Scales belong to 128 elements along the summed axis, or with
     `square` to 128 x 128 (weights: both then stand for the same values)."""
-    lib = _b.load()
-    code = _fmt_code(fmt)
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     if not (rows or cols):
         raise ValueError("neither rows nor cols is asked for")
     n, ld = _rows(x, "x")
-    m = x.shape[1]
-    dt = _dt(x, "x")
-    with _on(stream, x.device) as st:
-        q = Fp8Tensor.empty(n, m, fmt, x.device) if rows else None
-        qt = Fp8Tensor.empty(m, n, fmt, x.device) if cols else None
-        _b._check(lib.muon_fp8_quantize(
-            x.data_ptr(), ld, n, m, dt, code, 1 if square else 0, q.data.data_ptr() if rows else None,
-            q._ld() if rows else 0, q.scale.data_ptr() if rows else None, qt.data.data_ptr() if cols else None,
-            qt._ld() if cols else 0, qt.scale.data_ptr() if cols else None, st))
+    return _on(stream, x.device, _quantize, x, n, ld, _dt(x, "x"), _fmt_code(fmt), fmt, 1 if square else 0, rows, cols)
+
+
+def _quantize(x, n, ld, dt, code, fmt, square, rows, cols, st):
+    m, dev = x.shape[1], x.device
+    q = qt = None
+    args, argst = (None, 0, None), (None, 0, None)
+    if rows:
+        q = Fp8Tensor.empty(n, m, fmt, dev)
+        args = (q.data.data_ptr(), q._ld(), q.scale.data_ptr())
+    if cols:
+        qt = Fp8Tensor.empty(m, n, fmt, dev)
+        argst = (qt.data.data_ptr(), qt._ld(), qt.scale.data_ptr())
+    _b._check(_b.load().muon_fp8_quantize(x.data_ptr(), ld, n, m, dt, code, square, *args, *argst, st))
     return q, qt
 
 
@@ -222,38 +191,44 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, out_dtype=torch.bfloat16, add: Option
     `add` and `out` are [m, n] of `out_dtype` (bf16, fp16 or fp32; `out` decides where it is given); `out` may be `add`,
     which accumulates.  Where few tiles make the library split k, `workspace` (uint8, fp8_matmul_workspace_bytes) holds
     the parts; a new one is made if None."""
-    lib = _b.load()
     if not isinstance(a, Fp8Tensor) or not isinstance(b, Fp8Tensor):
         raise TypeError("a and b must be Fp8Tensor")
-    (m, k), (n, kb) = a.data.shape, b.data.shape
-    if k != kb:
-        raise ValueError(f"a has {k} columns and b {kb}: both are summed over them")
     dev = a.data.device
+    if a.data.shape[1] != b.data.shape[1]:
+        raise ValueError(f"a has {a.data.shape[1]} columns and b {b.data.shape[1]}: both are summed over them")
     if not a.data.is_cuda:
         raise ValueError("a must be on a CUDA device")
     if b.data.device != dev:
         raise ValueError(f"b is on {b.data.device}, not {dev}")
-    with _on(stream, dev) as st:
-        if out is None:
-            out = torch.empty((m, n), dtype=out_dtype, device=dev)
-            ldc = n
-        else:
-            if out.shape != (m, n) or out.device != dev:
-                raise ValueError(f"out must be [{m}, {n}] on {dev}")
-            ldc = _rows(out, "out")[1]
-        dt = _dt(out, "out")
-        ldadd = 0
-        if add is not None:
-            _like(add, out, "add")
-            ldadd = _rows(add, "add")[1]
-        need = lib.muon_fp8_matmul_workspace_bytes(m, n, k)
-        ws = size = None
-        if need:
-            keep, ws, size = _workspace(workspace, need, dev)
-        _b._check(lib.muon_fp8_matmul(
-            a.data.data_ptr(), a._ld(), a.scale.data_ptr(), _TYPE_FMT[a.data.dtype], b.data.data_ptr(), b._ld(),
-            b.scale.data_ptr(), _TYPE_FMT[b.data.dtype], m, n, k, None if add is None else add.data_ptr(), ldadd,
-            out.data_ptr(), ldc, dt, ws, size or 0, st))
+    return _on(stream, dev, _matmul, a, b, out_dtype, add, out, workspace, dev)
+
+
+def _matmul(a, b, out_dtype, add, out, workspace, dev, st):
+    lib = _b.load()
+    ad, bd = a.data, b.data
+    (m, k), n = ad.shape, bd.shape[0]
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+        ldc = n
+    else:
+        if out.shape != (m, n) or out.device != dev:
+            raise ValueError(f"out must be [{m}, {n}] on {dev}")
+        ldc = _rows(out, "out")[1]
+    addp, ldadd = None, 0
+    if add is not None:
+        _like(add, out, "add")
+        addp, ldadd = add.data_ptr(), _rows(add, "add")[1]
+    ws = size = 0
+    if workspace is not None:
+        ws, size = _workspace(workspace, dev)
+    else:
+        size = lib.muon_fp8_matmul_workspace_bytes(m, n, k)
+        if size:
+            keep = torch.empty(size, dtype=torch.uint8, device=dev)
+            ws = keep.data_ptr()
+    _b._check(lib.muon_fp8_matmul(ad.data_ptr(), a._ld(), a.scale.data_ptr(), _TYPE_FMT[ad.dtype], bd.data_ptr(), b._ld(),
+                                  b.scale.data_ptr(), _TYPE_FMT[bd.dtype], m, n, k, addp, ldadd, out.data_ptr(), ldc,
+                                  _dt(out, "out"), ws, size, st))
     return out
 
 
@@ -290,29 +265,39 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Optional
     y = h / sqrt(mean(h^2) + eps) * weight, and with `fp8` ("e4m3" or "e5m2") y in 8 bits as well; `y=False` leaves out
     the 16- or 32-bit y.  x is bf16, fp16 or fp32 with any leading dimensions; weight (or None) may have another of these
     types."""
-    lib = _b.load()
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("x needs a last dimension of at least 1")
-    cols = x.shape[-1]
     rows, ldx = _rows(x, "x")
-    dt = _dt(x, "x")
-    code = _fmt_code(fp8) if fp8 is not None else 0
     if not (y or fp8):
         raise ValueError("neither y nor an 8-bit copy is asked for")
     ldr, res = 0, None
     if residual is not None:
         _like(residual, x, "residual")
         ldr, res = _rows(residual, "residual")[1], residual.data_ptr()
-    wp, wdt = _weight(weight, cols, x.device)
-    with _on(stream, x.device) as st:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y else None
-        h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else None
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-        q = Fp8Tensor.empty(rows, cols, fp8, x.device) if fp8 is not None else None
-        _b._check(lib.muon_rms_norm(
-            x.data_ptr(), ldx, res, ldr, wp, wdt, rows, cols, eps, out.data_ptr() if y else None, cols,
-            h.data_ptr() if h is not None else None, cols, rstd.data_ptr(), q.data.data_ptr() if q is not None else None,
-            q._ld() if q is not None else 0, q.scale.data_ptr() if q is not None else None, code, dt, st))
+    dev = x.device
+    wp, wdt = _weight(weight, shape[-1], dev)
+    return _on(stream, dev, _rms_norm, x, ldx, res, ldr, wp, wdt, rows, shape[-1], float(eps), fp8, y, _dt(x, "x"), dev)
+
+
+def _rms_norm(x, ldx, res, ldr, wp, wdt, rows, cols, eps, fp8, y, dt, dev, st):
+    out = h = q = None
+    yp = hp = None
+    qa, code = (None, 0, None), 0
+    contiguous = x.is_contiguous()
+    if y:
+        out = torch.empty_like(x) if contiguous else torch.empty(x.shape, dtype=x.dtype, device=dev)
+        yp = out.data_ptr()
+    if res is not None:
+        h = torch.empty_like(x) if contiguous else torch.empty(x.shape, dtype=x.dtype, device=dev)
+        hp = h.data_ptr()
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    if fp8 is not None:
+        code = _fmt_code(fp8)
+        q = Fp8Tensor.empty(rows, cols, fp8, dev)
+        qa = (q.data.data_ptr(), q._ld(), q.scale.data_ptr())
+    _b._check(_b.load().muon_rms_norm(x.data_ptr(), ldx, res, ldr, wp, wdt, rows, cols, eps, yp, cols, hp, cols,
+                                      rstd.data_ptr(), *qa, code, dt, st))
     return RmsNormOutput(out, x if h is None else h, rstd, q)
 
 
@@ -322,68 +307,77 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.
 
     dx is the gradient of x and of the residual alike, plus `dresidual`, what reaches h on its way past the norm;
     dweight is fp32 [cols], or None with `dweight=False`."""
-    lib = _b.load()
-    if dy.dim() < 1 or dy.shape[-1] < 1:
+    shape = dy.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("dy needs a last dimension of at least 1")
-    cols = dy.shape[-1]
+    cols = shape[-1]
     rows, lddy = _rows(dy, "dy")
-    dt = _dt(dy, "dy")
     _like(h, dy, "h")
     ldh = _rows(h, "h")[1]
     lddr, res = 0, None
     if dresidual is not None:
         _like(dresidual, dy, "dresidual")
         lddr, res = _rows(dresidual, "dresidual")[1], dresidual.data_ptr()
-    if rstd.dtype != torch.float32 or rstd.numel() != rows or not rstd.is_contiguous() or rstd.device != dy.device:
-        raise ValueError(f"rstd must be {rows} contiguous float32 values on {dy.device}")
-    wp, wdt = _weight(weight, cols, dy.device)
-    with _on(stream, dy.device) as st:
-        dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-        dw = ws = size = None
-        if dweight:
-            dw = torch.empty(cols, dtype=torch.float32, device=dy.device)
-            keep, ws, size = _workspace(None, lib.muon_rms_norm_backward_workspace_bytes(rows, cols), dy.device)
-        _b._check(lib.muon_rms_norm_backward(
-            dy.data_ptr(), lddy, h.data_ptr(), ldh, wp, wdt, rstd.data_ptr(), res, lddr, rows, cols, dx.data_ptr(), cols,
-            dw.data_ptr() if dweight else None, ws, size or 0, dt, st))
+    dev = dy.device
+    if rstd.dtype != torch.float32 or rstd.numel() != rows or not rstd.is_contiguous() or rstd.device != dev:
+        raise ValueError(f"rstd must be {rows} contiguous float32 values on {dev}")
+    wp, wdt = _weight(weight, cols, dev)
+    return _on(stream, dev, _rms_norm_backward, dy, lddy, h.data_ptr(), ldh, wp, wdt, rstd.data_ptr(), res, lddr, rows, cols,
+               dweight, _dt(dy, "dy"), dev)
+
+
+def _rms_norm_backward(dy, lddy, hp, ldh, wp, wdt, rp, res, lddr, rows, cols, dweight, dt, dev, st):
+    lib = _b.load()
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    dw = dwp = ws = None
+    size = 0
+    if dweight:
+        dw = torch.empty(cols, dtype=torch.float32, device=dev)
+        size = lib.muon_rms_norm_backward_workspace_bytes(rows, cols)
+        keep = torch.empty(size, dtype=torch.uint8, device=dev)
+        dwp, ws = dw.data_ptr(), keep.data_ptr()
+    _b._check(lib.muon_rms_norm_backward(dy.data_ptr(), lddy, hp, ldh, wp, wdt, rp, res, lddr, rows, cols, dx.data_ptr(), cols,
+                                         dwp, ws, size, dt, st))
     return dx, dw
 
 
 # ---------------------------------------------------------------- clipping
 
 def _clip(grads, max_norm, out, eps, stream):
-    lib = _b.load()
     count = len(grads)
     if count == 0:
         raise ValueError("no gradients")
     dev = grads[0].device
-    for g in grads:
-        if not g.is_cuda or g.device != dev or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous CUDA tensors on one device")
-    P = ctypes.c_void_p * count
+    if not grads[0].is_cuda or not all([g.device == dev and g.is_contiguous() for g in grads]):
+        raise ValueError("gradients must be contiguous CUDA tensors on one device")
+    kinds = [g.dtype for g in grads]
     try:
-        dts = (ctypes.c_int32 * count)(*[_DT[g.dtype] for g in grads])
+        dts = array("i", [_DT[k] for k in kinds])
     except KeyError as e:
         raise TypeError(f"unsupported dtype {e.args[0]}: bfloat16, float16 or float32") from None
-    ptrs = P(*[g.data_ptr() for g in grads])
-    numel = (ctypes.c_int64 * count)(*[g.numel() for g in grads])
-    if out is None:
-        outs = None
-    elif out is grads:
-        outs = ptrs
-    else:
+    table = [g.data_ptr() for g in grads]
+    if out is not None and out is not grads:
         if len(out) != count:
             raise ValueError("out and the gradients must have the same length")
-        for g, o in zip(grads, out):
-            if o.shape != g.shape or o.dtype != g.dtype or o.device != dev or not o.is_contiguous():
-                raise ValueError("each out must be contiguous with its gradient's shape, dtype and device")
-        outs = P(*[o.data_ptr() for o in out])
-    with _on(stream, dev) as st:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        need = lib.muon_clip_workspace_bytes(count)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _b._check(lib.muon_clip_grads(ptrs, outs, numel, dts, count, max_norm, eps, norm.data_ptr(), ws.data_ptr(), need,
-                                      st))
+        if [o.dtype for o in out] != kinds or [o.shape for o in out] != [g.shape for g in grads] \
+                or not all([o.device == dev and o.is_contiguous() for o in out]):
+            raise ValueError("each out must be contiguous with its gradient's shape, dtype and device")
+        table += [o.data_ptr() for o in out]
+    table += [g.numel() for g in grads]
+    # one host array: gradient pointers, the outputs' where they are others, element counts
+    table = array("q", table)
+    base = table.buffer_info()[0]
+    numel = base + 8 * (len(table) - count)
+    outs = None if out is None else base if out is grads else base + 8 * count
+    return _on(stream, dev, _clip_call, base, outs, numel, dts.buffer_info()[0], count, max_norm, eps, dev, (table, dts))
+
+
+def _clip_call(grads, outs, numel, dts, count, max_norm, eps, dev, keep, st):
+    lib = _b.load()
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    size = lib.muon_clip_workspace_bytes(count)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _b._check(lib.muon_clip_grads(grads, outs, numel, dts, count, max_norm, eps, norm.data_ptr(), ws.data_ptr(), size, st))
     return norm
 
 
