@@ -539,16 +539,14 @@ MUON_API muon_status muon_fp8_quantize(const void* x, int64_t ldx, int64_t rows,
  * muon_fp8_matmul -- out = round(A B^T + add) for 8-bit A [m, k] and B [n, k] as
  * described above, of either format each; add (or NULL) and out are [m, n] of
  * out_dt.  add may be out itself.  Products are summed in fp32.  k = 0 gives
- * add, or zeros.  With few tiles k is split; the workspace (16-byte aligned, size
- * from muon_fp8_matmul_workspace_bytes; 0: none, NULL allowed) holds the parts.
- * A kernel that gives up on a bounded wait leaves the output incomplete and is
+ * add, or zeros.  With few tiles k is split over the CTAs of a cluster, whose sums
+ * are added in a fixed order.  A kernel that gives up on a bounded wait leaves the output incomplete and is
  * reported by muon_fp8_status.
  */
-MUON_API size_t muon_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 MUON_API muon_status muon_fp8_matmul(const void* a, int64_t lda, const void* a_scale, muon_fp8 a_fmt, const void* b,
                                      int64_t ldb, const void* b_scale, muon_fp8 b_fmt, int64_t m, int64_t n,
                                      int64_t k, const void* add, int64_t ldadd, void* out, int64_t ldc,
-                                     muon_dtype out_dt, void* ws, size_t ws_bytes, void* stream);
+                                     muon_dtype out_dt, void* stream);
 
 /*
  * muon_fp8_status -- synchronise `stream`, then read and clear the 8-bit product's

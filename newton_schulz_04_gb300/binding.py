@@ -115,9 +115,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.muon_fp8_scale_bytes.restype = sz
     lib.muon_fp8_quantize.argtypes = [vp, i64, i64, i64, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp]
     lib.muon_fp8_quantize.restype = i32
-    lib.muon_fp8_matmul_workspace_bytes.argtypes = [i64, i64, i64]
-    lib.muon_fp8_matmul_workspace_bytes.restype = sz
-    lib.muon_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i64, vp, i64, i32, vp, sz, vp]
+    lib.muon_fp8_matmul.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i64, i64, i64, vp, i64, vp, i64, i32, vp]
     lib.muon_fp8_matmul.restype = i32
     lib.muon_fp8_status.argtypes = [vp]
     lib.muon_fp8_status.restype = i32

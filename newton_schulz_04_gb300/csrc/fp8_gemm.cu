@@ -34,8 +34,10 @@
 //                was issued a group (1792 cycles) ahead held the MMAs up at every
 //                other stage (8192 x 14336 x 4096 in 326 us instead of 308)
 //
-// When there are too few tiles to fill the GPU, K is split: each part's fp32 sums go to
-// the caller's workspace and a second kernel adds them in order.
+// When there are too few tiles to fill the GPU, 2 or 4 pairs of one cluster share a tile of
+// at most 64 rows of A, each with its part of K.  Every pair sends the others their
+// share of the tile's rows of A through distributed shared memory and adds up its own, in
+// the order of the parts: no workspace, no second launch, the same bits every time.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -69,14 +71,18 @@ struct F8Cfg {
   static constexpr int SLOTS = 8;                    // and in shared memory
   static constexpr int SCALE_SLOT = (BN + 256) * 4;  // read in 32-row pieces, up to 256 rows of A
   static constexpr int BAR_BYTES = 512;
+  // Split K: the parts' sums of this pair's share of the tile, [parts][T / parts][128] fp32
+  static constexpr int SPLIT_T = 64;
+  static constexpr int RECV = SPLIT_T * BN * 4;
   static constexpr int SMEM = STAGES * STAGE + SLOTS * SCALE_SLOT + BAR_BYTES + 1024;
+  static constexpr int SMEM_SPLIT = SMEM + RECV;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t ACC_COLS = TMAX;
   static constexpr uint32_t SCALE_COL = 2 * TMAX;
   static constexpr uint32_t SET_COLS = 16;         // rows of B in the first 4 columns, of A from the 8th on
   static constexpr uint32_t EPI_ARRIVALS = 2 * EPI_WARPS;
   static constexpr uint32_t SCALE_ARRIVALS = 2 * 4;
-  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(SMEM_SPLIT <= 232448, "shared memory budget");
   static_assert(SCALE_COL + SETS * SET_COLS <= TMEM_COLS, "TMEM budget");
   static_assert(A_BOX % 1024 == 0 && B_BOX % 1024 == 0, "swizzle atoms of 1024 bytes");
 };
@@ -90,13 +96,12 @@ struct F8Args {
   int tail_steps;       // 32-deep MMA steps of the last block
   int tile_m;
   int nI, nJ;           // tiles along n (256) and m
-  int splits, gps;      // parts of K, 512-deep groups per part
-  int items;
+  int splits, gps;      // parts of K (pairs of a cluster), 512-deep groups per part
+  int items;            // tiles
   int rgroup;           // tiles along n walked together
   uint32_t idesc;
   const void* add;
   void* out;
-  float* partial;       // with splits > 1: [splits][m][n]
   long long ldadd, ldc;
   int out_dt;
   int* status;
@@ -157,37 +162,23 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 struct F8Item {
   int i, j;        // tile along n, along m
   int g0, g1;      // 512-deep groups of K
-  int split;
 };
-__device__ __forceinline__ F8Item decode_item(const F8Args& a, int t) {
+__device__ __forceinline__ F8Item decode_item(const F8Args& a, int u, int part) {
   F8Item it;
-  const int tiles = a.nI * a.nJ;
-  it.split = t / tiles;
-  const int u = t - it.split * tiles;
   // rgroup tile rows of B at a time, so that they stay in L2 while A streams by
   const int per = a.rgroup * a.nJ;
   const int g = u / per, first = g * a.rgroup, gs = min(a.nI - first, a.rgroup), w = u - g * per;
   it.i = first + w % gs;
   it.j = w / gs;
-  it.g0 = it.split * a.gps;
+  it.g0 = part * a.gps;
   it.g1 = min((a.kblocks + 3) >> 2, it.g0 + a.gps);
   return it;
 }
 
 // Rows m0 .. m0 + rows - 1 (at most 32, one register each) of column n of the output.
 template <typename T>
-__device__ __forceinline__ void epi_chunk(const F8Args& a, int split, long long m0, int rows, long long n,
-                                          const float (&v)[32]) {
+__device__ __forceinline__ void epi_chunk(const F8Args& a, long long m0, int rows, long long n, const float (&v)[32]) {
   if (n >= a.n) return;
-  if (a.splits > 1) {
-    float* p = a.partial + (split * a.m + m0) * a.n + n;
-#pragma unroll
-    for (int u = 0; u < 32; ++u) {
-      if (u < rows) *p = v[u];
-      p += a.n;
-    }
-    return;
-  }
   T* o = static_cast<T*>(a.out) + m0 * a.ldc + n;
   if (a.add) {
     const T* d = static_cast<const T*>(a.add) + m0 * a.ldadd + n;
@@ -213,7 +204,26 @@ __device__ __forceinline__ void epi_chunk(const F8Args& a, int split, long long 
     }
   }
 }
+__device__ __forceinline__ void epi_chunk(const F8Args& a, long long m0, int rows, long long n, const float (&v)[32]) {
+  if (a.out_dt == MUON_FP32) epi_chunk<float>(a, m0, rows, n, v);
+  else if (a.out_dt == MUON_BF16) epi_chunk<__nv_bfloat16>(a, m0, rows, n, v);
+  else epi_chunk<__half>(a, m0, rows, n, v);
+}
+// One element.
+__device__ __forceinline__ void epi_one(const F8Args& a, long long m, long long n, float v) {
+  if (a.add) {
+    const long long i = m * a.ldadd + n;
+    v += a.out_dt == MUON_FP32   ? static_cast<const float*>(a.add)[i]
+         : a.out_dt == MUON_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(a.add)[i])
+                                 : to_f32(static_cast<const __half*>(a.add)[i]);
+  }
+  const long long o = m * a.ldc + n;
+  if (a.out_dt == MUON_FP32) static_cast<float*>(a.out)[o] = v;
+  else if (a.out_dt == MUON_BF16) static_cast<__nv_bfloat16*>(a.out)[o] = from_f32<__nv_bfloat16>(v);
+  else static_cast<__half*>(a.out)[o] = from_f32<__half>(v);
+}
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ F8Args a) {
   using C = F8Cfg;
   extern __shared__ uint8_t smem_raw[];
@@ -227,10 +237,12 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
   uint64_t* sempty = sfull + C::SETS;    // [SETS] scales read by the group's MMAs
   uint64_t* sload = sempty + C::SETS;    // [SLOTS] scales of a group in shared memory
   uint64_t* sfree = sload + C::SLOTS;    // [SLOTS] and copied on
-  uint64_t* drain = sfree + C::SLOTS;
+  uint64_t* joined = sfree + C::SLOTS;   // the other parts' sums have arrived
+  uint64_t* drain = joined + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(C::BAR_BYTES >= (2 * C::STAGES + 2 * C::SETS + 2 * C::SLOTS + 5) * 8 + 8, "barrier area");
+  uint8_t* recv = reinterpret_cast<uint8_t*>(full) + C::BAR_BYTES;
+  static_assert(C::BAR_BYTES >= (2 * C::STAGES + 2 * C::SETS + 2 * C::SLOTS + 6) * 8 + 8, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -250,6 +262,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
       mbar_init(&sload[b], 1);
       mbar_init(&sfree[b], 4);
     }
+    mbar_init(joined, C::EPI_WARPS * a.splits);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -266,9 +279,13 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
   tc_fence_after();
   pdl_launch_dependents();
   pdl_wait();
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int crank = static_cast<int>(cluster_ctarank());
+  const int rank = crank & 1, part = SPLIT ? crank >> 1 : 0;  // in the pair; the pair's part of K
+  const uint32_t leader = static_cast<uint32_t>(crank & ~1);
+  const uint16_t pair_mask = static_cast<uint16_t>(0x3 << (crank & ~1));
   const uint32_t tmem = *tmem_slot;
-  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  const int per_cluster = SPLIT ? 2 * a.splits : 2;
+  const int cid = blockIdx.x / per_cluster, ncl = gridDim.x / per_cluster;
   const int half = a.tile_m >> 1;
 
   if (warp == 0) {
@@ -277,7 +294,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
       int st = 0;
       bool ok = true;
       for (int t = cid; t < a.items && ok; t += ncl) {
-        const F8Item it = decode_item(a, t);
+        const F8Item it = decode_item(a, t, part);
         const int nb0 = it.i * 256 + rank * C::BN, ma0 = it.j * a.tile_m + rank * half;
         const int kb1 = min(a.kblocks, it.g1 * 4);
         for (int kb = it.g0 * 4; kb < kb1; kb += C::KPS, ++st) {
@@ -288,7 +305,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
           }
           const int nb = min(C::KPS, kb1 - kb);
           uint8_t* p = tiles + s * C::STAGE;
-          const uint32_t fbar = mapa_cluster(&full[s], 0);
+          const uint32_t fbar = mapa_cluster(&full[s], leader);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * nb * (C::B_BOX + half * C::KB));
           for (int q = 0; q < nb; ++q) {
             tma_load_2d_pair(&a.tb, fbar, p + q * C::B_BOX, (kb + q) * C::KB, nb0);
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         return __all_sync(0xffffffffu, !*abort_flag && mbar_wait_cluster(bar, parity));
       };
       for (int t = cid; t < a.items && ok; t += ncl, ++tile) {
-        const F8Item it = decode_item(a, t);
+        const F8Item it = decode_item(a, t, part);
         const int abuf = tile & 1;
         if (!warp_wait(&tempty[abuf], ((tile >> 1) & 1) ^ 1)) {
           ok = false;
@@ -364,9 +381,9 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
                                   idesc + q * ((1u << 29) | (1u << 4)), sc, sc + 8, (q | kk) != 0 || kb != kb0 ? 1u : 0u);
               }
             }
-            tc_commit_pair(&empty[s], 0x3);
-            if (group_end) tc_commit_pair(&sempty[grp % C::SETS], 0x3);
-            if (kb + C::KPS >= kb1) tc_commit_pair(&tfull[abuf], 0x3);
+            tc_commit_pair(&empty[s], pair_mask);
+            if (group_end) tc_commit_pair(&sempty[grp % C::SETS], pair_mask);
+            if (kb + C::KPS >= kb1) tc_commit_pair(&tfull[abuf], pair_mask);
           }
           __syncwarp();
           if (group_end) ++grp;
@@ -377,7 +394,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         *abort_flag = 1;
       }
       // tcgen05.commit covers the MMAs of the thread that issues it
-      if (elect_one()) tc_commit_pair(drain, 0x1);
+      if (elect_one()) tc_commit_pair(drain, static_cast<uint16_t>(1u << leader));
       __syncwarp();
       mbar_wait(drain, 0);
     }
@@ -387,7 +404,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
     int grp = 0;
     bool ok = true;
     for (int t = cid; t < a.items && ok; t += ncl) {
-      const F8Item it = decode_item(a, t);
+      const F8Item it = decode_item(a, t, part);
       for (int g = it.g0; g < it.g1; ++g, ++grp) {
         const int slot = grp % C::SLOTS, set = grp % C::SETS;
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sload[slot], (grp / C::SLOTS) & 1));
@@ -409,7 +426,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_tmem(mapa_cluster(&sfull[set], 0));
+        if (lane == 0) mbar_arrive_tmem(mapa_cluster(&sfull[set], leader));
       }
     }
     if (!ok) {
@@ -423,7 +440,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
       int grp = 0;
       bool ok = true;
       for (int t = cid; t < a.items && ok; t += ncl) {
-        const F8Item it = decode_item(a, t);
+        const F8Item it = decode_item(a, t, part);
         const long long n0 = it.i * 256LL + rank * C::BN, m0 = static_cast<long long>(it.j) * a.tile_m;
         const uint32_t nb = static_cast<uint32_t>(max(0LL, min(static_cast<long long>(C::BN), a.sb_rows - n0))) * 4;
         const uint32_t na = static_cast<uint32_t>(min(static_cast<long long>(a.tile_m), a.sa_rows - m0)) * 4;
@@ -448,31 +465,61 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    const int quarter = warp & 3, part = (warp - C::EPI_WARP) >> 2;
+    const int quarter = warp & 3, half_tile = (warp - C::EPI_WARP) >> 2;
     int tile = 0;
     bool ok = true;
     for (int t = cid; t < a.items; t += ncl, ++tile) {
-      const F8Item it = decode_item(a, t);
+      const F8Item it = decode_item(a, t, part);
       const int abuf = tile & 1;
+      const long long n = it.i * 256LL + rank * C::BN + quarter * 32 + lane;
+      const long long m0 = static_cast<long long>(it.j) * a.tile_m;
+      const int rows = static_cast<int>(min(static_cast<long long>(a.tile_m), a.m - m0));
       if (lane == 0) ok = !*abort_flag && mbar_wait(&tfull[abuf], (tile >> 1) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const long long n = it.i * 256LL + rank * C::BN + quarter * 32 + lane;
-      const long long m0 = static_cast<long long>(it.j) * a.tile_m;
-      const int rows = static_cast<int>(min(static_cast<long long>(a.tile_m), a.m - m0));
-      for (int c = part * 32; c < rows; c += 64) {
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + abuf * C::ACC_COLS;
+      if (SPLIT) {
+        // Rows of A p share .. are added up by part p.  One item per cluster: nothing is received twice.
+        const int share = a.tile_m / a.splits, shift = __ffs(share) - 1, c = half_tile * 32;  // 8, 16 or 32 rows
+        const float* sums = reinterpret_cast<const float*>(recv) + quarter * 32 + lane;  // [part][row][128]
         float v[32];
-        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter) << 21) + abuf * C::ACC_COLS + c, v);
-        const int cols = min(32, rows - c);
-        if (a.out_dt == MUON_FP32) epi_chunk<float>(a, it.split, m0 + c, cols, n, v);
-        else if (a.out_dt == MUON_BF16) epi_chunk<__nv_bfloat16>(a, it.split, m0 + c, cols, n, v);
-        else epi_chunk<__half>(a, it.split, m0 + c, cols, n, v);
+        if (c < a.tile_m) tmem_ld_32x32b_x32(acc + c, v);
+#pragma unroll 1
+        for (int p = 0; p < a.splits; ++p) {
+          const uint32_t to = mapa_cluster(sums + part * share * C::BN, static_cast<uint32_t>(2 * p + rank));
+          if (c < a.tile_m) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u)
+              if ((c + u) >> shift == p)
+                st_shared_cluster(to + static_cast<uint32_t>((c + u - p * share) * C::BN * 4), __float_as_int(v[u]));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_cluster(joined, static_cast<uint32_t>(2 * p + rank)));
+        }
+        ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait_cluster(joined, 0));
+        if (!ok) break;
+        // one rolled loop: unrolled over the rows its code took longer to fetch than to run (19000 cycles)
+#pragma unroll 1
+        for (int r = half_tile; r < share; r += 2) {
+          if (part * share + r >= rows || n >= a.n) break;
+          float sum = sums[r * C::BN];
+#pragma unroll 1
+          for (int p = 1; p < a.splits; ++p) sum += sums[(p * share + r) * C::BN];
+          epi_one(a, m0 + part * share + r, n, sum);
+        }
         __syncwarp();
+      } else {
+        for (int c = half_tile * 32; c < rows; c += 64) {
+          float v[32];
+          tmem_ld_32x32b_x32(acc + c, v);
+          epi_chunk(a, m0 + c, min(32, rows - c), n, v);
+          __syncwarp();
+        }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_tmem(mapa_cluster(&tempty[abuf], 0));
+      if (lane == 0) mbar_arrive_tmem(mapa_cluster(&tempty[abuf], leader));
     }
     if (!ok) {
       if (lane == 0) atomicOr(a.status, kStatusTimeout);
@@ -491,19 +538,16 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
   }
 }
 
-// C = round(sum over splits + D); splits = 0 where K is 0.
+// K = 0: C = D, or zeros.
 template <typename T>
-__global__ void __launch_bounds__(256) fp8_join_kernel(const float* partial, int splits, long long m, long long n,
-                                                       const T* add, long long ldadd, T* out, long long ldc) {
+__global__ void __launch_bounds__(256) fp8_empty_kernel(long long m, long long n, const T* add, long long ldadd, T* out,
+                                                        long long ldc) {
   pdl_launch_dependents();
   pdl_wait();
   const long long total = m * n;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
     const long long r = i / n, c = i - r * n;
-    float v = 0.f;
-    for (int s = 0; s < splits; ++s) v += partial[s * total + i];
-    if (add) v += to_f32(add[r * ldadd + c]);
-    out[r * ldc + c] = from_f32<T>(v);
+    out[r * ldc + c] = add ? add[r * ldadd + c] : from_f32<T>(0.f);
   }
 }
 
@@ -533,61 +577,82 @@ static bool byte_map(CUtensorMap* m, const void* base, long long k, long long ro
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters that can be resident at once, and the kernel's shared-memory limit, once per device.
-static cudaError_t fp8_clusters(int sms, int* out) {
+// Launch configuration: clusters of `parts` pairs.
+struct Fp8Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  Fp8Launch(int parts, int clusters, cudaStream_t st, bool pdl) {
+    cfg.gridDim = dim3(2 * parts * clusters);
+    cfg.blockDim = dim3(F8Cfg::THREADS);
+    cfg.dynamicSmemBytes = parts > 1 ? F8Cfg::SMEM_SPLIT : F8Cfg::SMEM;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+  }
+};
+
+// Clusters of 1, 2 and 4 pairs that can be resident at once; with the kernels' shared-memory limits, once per device.
+struct Fp8Clusters {
+  int of[3];
+};
+static cudaError_t fp8_clusters(int sms, Fp8Clusters* out) {
   static std::mutex mu;
-  static int cached[64] = {0};
+  static Fp8Clusters cached[64];
+  static bool done[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
-  if (!cached[dev]) {
-    e = cudaFuncSetAttribute(fp8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F8Cfg::SMEM);
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(fp8_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, F8Cfg::SMEM);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fp8_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, F8Cfg::SMEM_SPLIT);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sms / 2 * 2);
-    cfg.blockDim = dim3(F8Cfg::THREADS);
-    cfg.dynamicSmemBytes = F8Cfg::SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel, &cfg) != cudaSuccess || n <= 0) {
-      cudaGetLastError();
-      n = sms / 2;
+    for (int i = 0; i < 3; ++i) {
+      const int parts = 1 << i, most = sms / (2 * parts);
+      Fp8Launch l(parts, std::max(most, 1), nullptr, false);
+      int n = 0;
+      e = i ? cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<true>, &l.cfg)
+            : cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<false>, &l.cfg);
+      if (e != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = i ? 0 : most;  // no clusters of that size: K is not split so far
+      }
+      cached[dev].of[i] = std::min(n, most);
     }
-    cached[dev] = std::min(n, sms / 2);
+    done[dev] = true;
   }
   *out = cached[dev];
   return cudaSuccess;
 }
 
-// The tile of tokens and the splits of K with the least estimated time, in SM
+// The tile of tokens and the parts of K with the least estimated time, in SM
 // cycles: a pair MMA of 128 of K by T takes 2 T cycles, its loads (128 + T / 2 rows of 128
 // bytes per CTA) at 64 bytes a cycle 256 + T; an item costs some 1500 cycles of pipeline
-// fill and drain, and joining the splits a second launch and the partial sums' traffic.
-Fp8Plan fp8_plan(long long m, long long n, long long k, int sms) {
-  const long long groups = (k + 511) / 512, nI = (n + 255) / 256, pairs = std::max(1, sms / 2);
+// fill and drain, and joining the parts as much again.  K is split only where every
+// tile has a cluster of its own.
+static Fp8Plan fp8_plan(long long m, long long n, long long k, const Fp8Clusters& fit) {
+  const long long groups = (k + 511) / 512, nI = (n + 255) / 256;
   Fp8Plan best = {32, 1, static_cast<int>(groups)};
   double best_time = 1e300;
   for (int t = 32; t <= F8Cfg::TMAX; t += 32) {
-    const long long nJ = (m + t - 1) / t;
+    const long long tiles = nI * ((m + t - 1) / t);
     const double block = std::max(2.0 * t, 256.0 + t);
-    for (long long want = 1; want <= std::min<long long>(groups, 16); ++want) {
-      const long long gps = (groups + want - 1) / want, splits = (groups + gps - 1) / gps;
-      if (splits != want) continue;
-      const double waves = static_cast<double>((nI * nJ * splits + pairs - 1) / pairs);
-      double time = waves * (gps * 4 * block + 1500.0);
-      if (splits > 1) time += 4000.0 + 8.0 * splits * static_cast<double>(m) * n / 3500.0;
+    for (int i = 0; i < 3; ++i) {
+      const long long parts = 1 << i, gps = (groups + parts - 1) / parts;
+      if (i && (t > F8Cfg::SPLIT_T || tiles > fit.of[i] || (groups + gps - 1) / gps != parts)) break;
+      const double waves = static_cast<double>((tiles + fit.of[i] - 1) / std::max(1, fit.of[i]));
+      const double time = waves * (gps * 4 * block + (i ? 3000.0 : 1500.0));
       if (time < best_time) {
         best_time = time;
-        best = {t, static_cast<int>(splits), static_cast<int>(gps)};
+        best = {t, static_cast<int>(parts), static_cast<int>(gps)};
       }
-      if (nI * nJ * splits >= 2 * pairs) break;
     }
     if (t >= m) break;
   }
@@ -595,27 +660,25 @@ Fp8Plan fp8_plan(long long m, long long n, long long k, int sms) {
 }
 
 template <typename T>
-static cudaError_t launch_join(const Fp8GemmDesc& d, int splits, int sms, cudaStream_t st) {
+static cudaError_t launch_empty(const Fp8GemmDesc& d, int sms, cudaStream_t st) {
   const long long want = (d.m * d.n + 255) / 256;
-  const int grid = static_cast<int>(std::min<long long>(want, 8LL * sms));
-  return launch_pdl(fp8_join_kernel<T>, dim3(grid), dim3(256), 0, st, static_cast<const float*>(d.partial), splits, d.m,
-                    d.n, static_cast<const T*>(d.add), d.ldadd, static_cast<T*>(d.out), d.ldc);
-}
-static cudaError_t join(const Fp8GemmDesc& d, int splits, int sms, cudaStream_t st) {
-  if (d.out_dt == MUON_FP32) return launch_join<float>(d, splits, sms, st);
-  if (d.out_dt == MUON_BF16) return launch_join<__nv_bfloat16>(d, splits, sms, st);
-  return launch_join<__half>(d, splits, sms, st);
+  return launch_pdl(fp8_empty_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>(want, 8LL * sms))), dim3(256), 0, st,
+                    d.m, d.n, static_cast<const T*>(d.add), d.ldadd, static_cast<T*>(d.out), d.ldc);
 }
 
 cudaError_t fp8_status_address(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fp8_status); }
 
-cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, const Fp8Plan& p, int sms, cudaStream_t st, const char** why) {
+cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, int sms, cudaStream_t st, const char** why) {
   using C = F8Cfg;
   *why = nullptr;
-  if (d.k == 0) return join(d, 0, sms, st);
-  int clusters = 0;
-  cudaError_t e = fp8_clusters(sms, &clusters);
+  if (d.k == 0)
+    return d.out_dt == MUON_FP32   ? launch_empty<float>(d, sms, st)
+           : d.out_dt == MUON_BF16 ? launch_empty<__nv_bfloat16>(d, sms, st)
+                                   : launch_empty<__half>(d, sms, st);
+  Fp8Clusters fit;
+  cudaError_t e = fp8_clusters(sms, &fit);
   if (e != cudaSuccess) return e;
+  const Fp8Plan p = fp8_plan(d.m, d.n, d.k, fit);
   F8Args a;
   if (!byte_map(&a.ta, d.a, d.k, d.m, d.lda, p.tile_m / 2) || !byte_map(&a.tb, d.b, d.k, d.n, d.ldb, C::BN)) {
     *why = "cuTensorMapEncodeTiled failed";
@@ -634,8 +697,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, const Fp8Plan& p, int sms, cud
   a.nJ = static_cast<int>((d.m + p.tile_m - 1) / p.tile_m);
   a.splits = p.splits;
   a.gps = p.groups_per_split;
-  const long long items = static_cast<long long>(a.nI) * a.nJ * a.splits;
-  if (items > 0x7fffffffLL) {
+  const long long items = static_cast<long long>(a.nI) * a.nJ;
+  if (items > 0x3fffffffLL) {
     *why = "too many tiles";
     return cudaErrorInvalidValue;
   }
@@ -645,30 +708,16 @@ cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, const Fp8Plan& p, int sms, cud
   // instruction descriptor: A (the kernel's B) and B formats, N >> 3, E8M0 scales, M >> 4 with M = 256
   a.idesc = (static_cast<uint32_t>(d.b_fmt) << 7) | (static_cast<uint32_t>(d.a_fmt) << 10) |
             (static_cast<uint32_t>(p.tile_m >> 3) << 17) | (1u << 23) | (16u << 24);
-  a.add = p.splits > 1 ? nullptr : d.add;
+  a.add = d.add;
   a.out = d.out;
-  a.partial = d.partial;
   a.ldadd = d.ldadd;
   a.ldc = d.ldc;
   a.out_dt = d.out_dt;
   e = fp8_status_address(&a.status);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * std::min(a.items, clusters));
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, fp8_gemm_kernel, a);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  return join(d, p.splits, sms, st);
+  Fp8Launch l(p.splits, p.splits > 1 ? a.items : std::min(a.items, fit.of[0]), st, true);
+  return p.splits > 1 ? cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<true>, a)
+                      : cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<false>, a);
 }
 
 }  // namespace muon

@@ -265,19 +265,9 @@ muon_status muon_fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_t 
   return launched(launch_fp8_quantize(a, dt, static_cast<cudaStream_t>(stream)), "launch_fp8_quantize");
 }
 
-static size_t matmul_bytes(const Fp8Plan& p, long long m, long long n) {
-  return p.splits > 1 ? static_cast<size_t>(p.splits) * m * n * sizeof(float) : 0;
-}
-
-size_t muon_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  if (m < 1 || n < 1 || k < 1 || m > MUON_MAX_ROWS || n > MUON_MAX_ROWS || k > MUON_MAX_ROWS) return 0;
-  return matmul_bytes(fp8_plan(m, n, k, MUON_MAX_SMS), m, n);
-}
-
 muon_status muon_fp8_matmul(const void* a, int64_t lda, const void* a_scale, muon_fp8 a_fmt, const void* b, int64_t ldb,
                             const void* b_scale, muon_fp8 b_fmt, int64_t m, int64_t n, int64_t k, const void* add,
-                            int64_t ldadd, void* out, int64_t ldc, muon_dtype out_dt, void* ws, size_t ws_bytes,
-                            void* stream) {
+                            int64_t ldadd, void* out, int64_t ldc, muon_dtype out_dt, void* stream) {
   clear_error();
   if (m < 0 || n < 0 || k < 0 || m > MUON_MAX_ROWS || n > MUON_MAX_ROWS || k > MUON_MAX_ROWS)
     return fail(MUON_ERR_SHAPE, "m=%lld n=%lld k=%lld: sizes in [0, %lld]", static_cast<long long>(m),
@@ -305,24 +295,14 @@ muon_status muon_fp8_matmul(const void* a, int64_t lda, const void* a_scale, muo
     }
   }
   if (add && clash(out, ldc, add, ldadd, m, n, size)) return fail(MUON_ERR_ARG, "out partly overlaps add");
-  const Fp8Plan plan = k > 0 ? fp8_plan(m, n, k, MUON_MAX_SMS) : Fp8Plan{32, 1, 0};
-  const size_t need = matmul_bytes(plan, m, n);
-  if (need) {
-    if (!ws) return fail(MUON_ERR_ARG, "workspace is NULL");
-    if (misaligned(ws, 16)) return fail(MUON_ERR_ALIGN, "workspace is not 16-byte aligned");
-    if (ws_bytes < need) return fail(MUON_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
-    if (overlap(ws, static_cast<long long>(need), out, span(m, n, ldc, size)))
-      return fail(MUON_ERR_ARG, "out overlaps the workspace");
-  }
   muon_status st;
   const int sms = gpu(&st);
   if (st != MUON_OK) return st;
   Fp8GemmDesc d = {};
   d.a = a, d.b = b, d.a_scale = a_scale, d.b_scale = b_scale, d.lda = lda, d.ldb = ldb, d.m = m, d.n = n, d.k = k;
   d.a_fmt = a_fmt, d.b_fmt = b_fmt, d.add = add, d.out = out, d.ldadd = ldadd, d.ldc = ldc, d.out_dt = out_dt;
-  d.partial = static_cast<float*>(ws);
   const char* why = nullptr;
-  return launched(launch_fp8_gemm(d, plan, sms, static_cast<cudaStream_t>(stream), &why), "launch_fp8_gemm", why);
+  return launched(launch_fp8_gemm(d, sms, static_cast<cudaStream_t>(stream), &why), "launch_fp8_gemm", why);
 }
 
 muon_status muon_fp8_status(void* stream) {

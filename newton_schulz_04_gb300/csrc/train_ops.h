@@ -84,16 +84,14 @@ struct Fp8GemmDesc {
   void* out;                       // [m][ldc]
   long long ldadd, ldc;
   int out_dt;
-  float* partial;                  // [splits][m][n] when the k axis is split
 };
-// Tile of tokens and splits of the k axis for a problem (see fp8_gemm.cu).
+// Tile of tokens and parts of the k axis for a problem (see fp8_gemm.cu).
 struct Fp8Plan {
   int tile_m;
   int splits;
   int groups_per_split;  // 512-deep groups of k
 };
-Fp8Plan fp8_plan(long long m, long long n, long long k, int sms);
-cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, const Fp8Plan& p, int sms, cudaStream_t st, const char** why);
+cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, int sms, cudaStream_t st, const char** why);
 // Address of the 8-bit product's status word (device memory of the library).
 cudaError_t fp8_status_address(int** p);
 

@@ -66,12 +66,6 @@ def _like(t, ref, name):
         raise ValueError(f"{name} must have the shape, dtype and device of the input")
 
 
-def _workspace(workspace, device):
-    if not (workspace.is_cuda and workspace.is_contiguous() and workspace.device == device):
-        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
 def _on(stream, device, call, *args):
     """call(*args, stream pointer) with `device` and `stream` (None: its current one) current, so that the tensors made
     within belong to that stream."""
@@ -185,12 +179,11 @@ def _quantize(x, n, ld, dt, code, fmt, square, rows, cols, st):
 
 
 def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, out_dtype=torch.bfloat16, add: Optional[torch.Tensor] = None,
-               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """a @ b.T (+ add) for 8-bit a [m, k] and b [n, k] (C-ABI muon_fp8_matmul), summed in fp32 and rounded once.
 
     `add` and `out` are [m, n] of `out_dtype` (bf16, fp16 or fp32; `out` decides where it is given); `out` may be `add`,
-    which accumulates.  Where few tiles make the library split k, `workspace` (uint8, fp8_matmul_workspace_bytes) holds
-    the parts; a new one is made if None."""
+    which accumulates."""
     if not isinstance(a, Fp8Tensor) or not isinstance(b, Fp8Tensor):
         raise TypeError("a and b must be Fp8Tensor")
     dev = a.data.device
@@ -200,11 +193,10 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, out_dtype=torch.bfloat16, add: Option
         raise ValueError("a must be on a CUDA device")
     if b.data.device != dev:
         raise ValueError(f"b is on {b.data.device}, not {dev}")
-    return _on(stream, dev, _matmul, a, b, out_dtype, add, out, workspace, dev)
+    return _on(stream, dev, _matmul, a, b, out_dtype, add, out, dev)
 
 
-def _matmul(a, b, out_dtype, add, out, workspace, dev, st):
-    lib = _b.load()
+def _matmul(a, b, out_dtype, add, out, dev, st):
     ad, bd = a.data, b.data
     (m, k), n = ad.shape, bd.shape[0]
     if out is None:
@@ -218,23 +210,10 @@ def _matmul(a, b, out_dtype, add, out, workspace, dev, st):
     if add is not None:
         _like(add, out, "add")
         addp, ldadd = add.data_ptr(), _rows(add, "add")[1]
-    ws = size = 0
-    if workspace is not None:
-        ws, size = _workspace(workspace, dev)
-    else:
-        size = lib.muon_fp8_matmul_workspace_bytes(m, n, k)
-        if size:
-            keep = torch.empty(size, dtype=torch.uint8, device=dev)
-            ws = keep.data_ptr()
-    _b._check(lib.muon_fp8_matmul(ad.data_ptr(), a._ld(), a.scale.data_ptr(), _TYPE_FMT[ad.dtype], bd.data_ptr(), b._ld(),
-                                  b.scale.data_ptr(), _TYPE_FMT[bd.dtype], m, n, k, addp, ldadd, out.data_ptr(), ldc,
-                                  _dt(out, "out"), ws, size, st))
+    _b._check(_b.load().muon_fp8_matmul(
+        ad.data_ptr(), a._ld(), a.scale.data_ptr(), _TYPE_FMT[ad.dtype], bd.data_ptr(), b._ld(), b.scale.data_ptr(),
+        _TYPE_FMT[bd.dtype], m, n, k, addp, ldadd, out.data_ptr(), ldc, _dt(out, "out"), st))
     return out
-
-
-def fp8_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
-    """Bytes of workspace that fp8_matmul uses for a product of these sizes (0: none)."""
-    return int(_b.load().muon_fp8_matmul_workspace_bytes(int(m), int(n), int(k)))
 
 
 def fp8_status(stream=None) -> int:

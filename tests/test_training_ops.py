@@ -179,19 +179,17 @@ def _mm_call(mm, **kw):
     g = lambda k, d: kw.get(k, d)  # noqa: E731
     return mm.load().muon_fp8_matmul(g("a", A), g("lda", 128), g("sa", A + (1 << 20)), g("fa", 0), g("b", B_), g("ldb", 128),
                                      g("sb", B_ + (1 << 20)), 0, g("m", 8), g("n", 16), g("k", 128), g("add", None),
-                                     g("ldadd", 16), g("out", C_), g("ldc", 16), g("dt", 0), g("ws", None), g("bytes", 0), None)
+                                     g("ldadd", 16), g("out", C_), g("ldc", 16), g("dt", 0), None)
 
 
 def test_matmul_refuses(mm):
     for kw in (dict(a=None), dict(sb=None), dict(out=None), dict(fa=2), dict(dt=3), dict(out=A + 64), dict(out=B_ + (1 << 20)),
-               dict(add=C_ + 2), dict(add=C_, ldadd=24), dict(k=8192, lda=8192, ldb=8192)):
+               dict(add=C_ + 2), dict(add=C_, ldadd=24)):
         assert _mm_call(mm, **kw) == 1, kw
     for kw in (dict(m=-1), dict(n=4194305), dict(k=-5), dict(lda=112), dict(ldc=15)):
         assert _mm_call(mm, **kw) == 2, kw
     for kw in (dict(a=A + 8), dict(lda=136), dict(out=C_ + 1), dict(sa=A + (1 << 20) + 2)):
         assert _mm_call(mm, **kw) == 3, kw
-    assert mm.fp8_matmul_workspace_bytes(8, 16, 8192) > 0        # a single tile: k is split
-    assert _mm_call(mm, k=8192, lda=8192, ldb=8192, ws=D_, bytes=64) == 4
     assert _mm_call(mm, m=0) == 0 and _mm_call(mm, n=0) == 0
 
 
@@ -542,20 +540,23 @@ def test_matmul_matches_oracle(mm, out, fa, fb, m, n, k):
 
 
 @gpu
-@pytest.mark.parametrize("m,n,k", [(1, 2048, 8192), (7, 512, 20000), (2, 4100, 4096)])
-def test_matmul_split_k(mm, m, n, k):
-    """Few tiles: k is split and joined; same bits every time, and the caller's workspace gives the same."""
-    assert mm.fp8_matmul_workspace_bytes(m, n, k) > 0
+@pytest.mark.parametrize("m,n,k", [(1, 2048, 8192), (7, 512, 20000), (2, 4100, 4096), (33, 700, 1500), (64, 256, 6000),
+                                   (100, 300, 9000), (5, 9000, 1030), (40, 64, 513)])
+@pytest.mark.parametrize("out", DTYPES)
+def test_matmul_few_tiles(mm, m, n, k, out):
+    """k is split over the pairs of a cluster and joined; the same bits every time."""
     a, av = _operand(mm, 1, m, k, "e4m3")
     b, bv = _operand(mm, 3, n, k, "e4m3")
     want = ref.matmul(av, bv)
-    c = mm.fp8_matmul(a, b, torch.float32)
-    close(c, want, _mm_tol(av, bv, want, torch.float32, k))
-    ws = torch.full((mm.fp8_matmul_workspace_bytes(m, n, k),), 255, dtype=torch.uint8, device="cuda")
+    add = gen(5, m, n).to(out)
+    c = mm.fp8_matmul(a, b, out)
+    close(c, want, _mm_tol(av, bv, want, out, k))
     for _ in range(3):
-        assert torch.equal(mm.fp8_matmul(a, b, torch.float32, workspace=ws), c)
-    with pytest.raises(mm.MuonError):
-        mm.fp8_matmul(a, b, workspace=ws[:64])
+        assert torch.equal(mm.fp8_matmul(a, b, out), c)
+    d = mm.fp8_matmul(a, b, out, add=add.cuda())
+    want = want + add.double()
+    close(d, want, _mm_tol(av, bv, want, out, k) + F24 * want.abs())
+    assert mm.fp8_status() == 0
 
 
 @gpu
