@@ -111,7 +111,7 @@ class Fp8Tensor:
         self = object.__new__(cls)
         pitch = (cols + 15) // 16 * 16
         data = torch.empty((rows, pitch), dtype=_FMT_TYPE[fmt], device=device or "cuda")
-        self.data = data if pitch == cols else data[:, :cols]
+        self.data = data if pitch == cols else data.as_strided((rows, cols), (pitch, 1))
         self.scale = torch.empty(((cols + 511) // 512, (rows + 3) // 4 * 4, 4), dtype=torch.float8_e8m0fnu,
                                  device=data.device)
         return self
@@ -327,36 +327,37 @@ def _clip(grads, max_norm, out, eps, stream):
     if count == 0:
         raise ValueError("no gradients")
     dev = grads[0].device
-    if not grads[0].is_cuda or not all([g.device == dev and g.is_contiguous() for g in grads]):
+    tensor = torch.Tensor
+    on = list(map(tensor.get_device, grads))  # -1 on the CPU
+    if on[0] < 0 or on.count(on[0]) != count or not all(map(tensor.is_contiguous, grads)):
         raise ValueError("gradients must be contiguous CUDA tensors on one device")
     kinds = [g.dtype for g in grads]
     try:
         dts = array("i", [_DT[k] for k in kinds])
     except KeyError as e:
         raise TypeError(f"unsupported dtype {e.args[0]}: bfloat16, float16 or float32") from None
-    table = [g.data_ptr() for g in grads]
+    numel = list(map(tensor.numel, grads))
+    # one host array: gradient pointers, element counts, the outputs' pointers where they are others
+    table = list(map(tensor.data_ptr, grads)) + numel
     if out is not None and out is not grads:
-        if len(out) != count:
-            raise ValueError("out and the gradients must have the same length")
-        if [o.dtype for o in out] != kinds or [o.shape for o in out] != [g.shape for g in grads] \
-                or not all([o.device == dev and o.is_contiguous() for o in out]):
-            raise ValueError("each out must be contiguous with its gradient's shape, dtype and device")
-        table += [o.data_ptr() for o in out]
-    table += [g.numel() for g in grads]
-    # one host array: gradient pointers, the outputs' where they are others, element counts
+        if [o.dtype for o in out] != kinds or list(map(tensor.numel, out)) != numel \
+                or list(map(tensor.get_device, out)) != on or not all(map(tensor.is_contiguous, out)):
+            raise ValueError("there must be one out per gradient, contiguous, of its size, dtype and device")
+        table += map(tensor.data_ptr, out)
     table = array("q", table)
     base = table.buffer_info()[0]
-    numel = base + 8 * (len(table) - count)
-    outs = None if out is None else base if out is grads else base + 8 * count
-    return _on(stream, dev, _clip_call, base, outs, numel, dts.buffer_info()[0], count, max_norm, eps, dev, (table, dts))
+    outs = None if out is None else base if out is grads else base + 16 * count
+    return _on(stream, dev, _clip_call, base, outs, base + 8 * count, dts.buffer_info()[0], count, max_norm, eps, dev,
+               (table, dts))
 
 
 def _clip_call(grads, outs, numel, dts, count, max_norm, eps, dev, keep, st):
     lib = _b.load()
-    norm = torch.empty((), dtype=torch.float32, device=dev)
     size = lib.muon_clip_workspace_bytes(count)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    _b._check(lib.muon_clip_grads(grads, outs, numel, dts, count, max_norm, eps, norm.data_ptr(), ws.data_ptr(), size, st))
+    ws = torch.empty(size // 4 + 1, dtype=torch.float32, device=dev)  # partial sums, then the norm
+    norm = ws.as_strided((), (), size // 4)
+    at = ws.data_ptr()
+    _b._check(lib.muon_clip_grads(grads, outs, numel, dts, count, max_norm, eps, at + size, at, size, st))
     return norm
 
 
