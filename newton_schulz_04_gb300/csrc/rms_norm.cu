@@ -9,7 +9,7 @@
 //   g = dy w      dx = rho (g - h rho^2 mean_j(g_j h_j)) + dres      dw_j = sum_rows dy_j h_j rho
 //
 // Both are one pass over memory, and bound by it.  A row belongs to G threads,
-// 8 consecutive columns each, C times.  CTAs are persistent: every thread copies
+// 16 bytes of it each, C times.  CTAs are persistent: every thread copies
 // its own pieces of the next rows to a ring in shared memory (cp.async, S rows
 // deep) that no other thread reads, so the ring needs no barrier, and the only
 // synchronisation of a row is the one of its sum.  One short-lived CTA per row
@@ -19,8 +19,8 @@
 // Rows that allow no 16-byte accesses, or that are too wide for a ring, take kernels
 // that load straight to registers, the widest (WIDE) a second time from L1 / L2.
 //
-// A block of 128 columns lies in 16 neighbouring lanes, so its largest magnitude
-// takes four shuffles.  The weight's gradient is summed over a CTA's rows in
+// A block of 128 columns lies in 16 neighbouring lanes (32 in fp32), so its
+// largest magnitude takes four or five shuffles.  The weight's gradient is summed over a CTA's rows in
 // registers, written per CTA, and the CTAs' rows are added in a fixed order by a
 // second kernel (no atomics: the same bits every time).
 #include <cuda_runtime.h>
@@ -66,15 +66,16 @@ __device__ __forceinline__ float row_sum(float v, float* sh) {
   return s;
 }
 
-// y's 8-bit copy.  A thread holds pieces t, t + G, ... of 8 columns (G a multiple of 16),
-// so the 16 lanes of a 128-column block are neighbours.
+// y's 8-bit copy.  A thread holds pieces t, t + G, ... of E columns (G a multiple of 128 / E),
+// so the 128 / E lanes of a 128-column block are neighbours.
+template <int E>
 struct QOut {
-  uint8_t* data;   // this row, column 8 t
+  uint8_t* data;   // this row, column E t
   uint8_t* scale;  // scale word of this row, first group
   int t;
   long long rows4;
   __device__ __forceinline__ QOut(const RmsNormArgs& a, long long row, int t_) : t(t_), rows4((a.rows + 3) & ~3LL) {
-    data = a.q + (a.q ? row * a.ldq + 8 * t_ : 0);
+    data = a.q + (a.q ? row * a.ldq + E * t_ : 0);
     scale = a.qscale + (a.q ? row * 4 : 0);
   }
   __device__ __forceinline__ void advance(const RmsNormArgs& a, long long rows) {
@@ -83,19 +84,27 @@ struct QOut {
   }
   // piece `piece` + t (piece a multiple of G); all lanes call.  Up to the row's
   // next multiple of 16 bytes: columns past the end hold 0.
-  __device__ __forceinline__ void store(const RmsNormArgs& a, int piece, const float (&y)[8], bool live, bool last) const {
+  __device__ __forceinline__ void store(const RmsNormArgs& a, int piece, const float (&y)[E], bool live, bool last) const {
+    constexpr int LANES = 128 / E;
     uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(y[i]));
+    for (int i = 0; i < E; ++i) m = max(m, abs_bits(y[i]));
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const uint32_t byte = fp8_scale_byte(m, a.fmt ? 15 : 8);
     if (!live) return;
     const float inv = fp8_inverse_scale(byte);
-    if ((piece + t) * 8 < ((a.cols + 15) & ~15))
-      *reinterpret_cast<uint2*>(data + piece * 8) = a.fmt ? fp8_pack8<true>(y, inv) : fp8_pack8<false>(y, inv);
-    const int kb = (piece + t) >> 4;
-    if ((t & 15) == 0 && kb < ((a.cols + 511) >> 9) * 4) {
+    if ((piece + t) * E < ((a.cols + 15) & ~15)) {
+      if constexpr (E == 8) {
+        *reinterpret_cast<uint2*>(data + piece * E) = a.fmt ? fp8_pack8<true>(y, inv) : fp8_pack8<false>(y, inv);
+      } else {
+        *reinterpret_cast<uint32_t*>(data + piece * E) =
+            a.fmt ? fp8_pack4<true>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv)
+                  : fp8_pack4<false>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+      }
+    }
+    const int kb = (piece + t) / LANES;
+    if (t % LANES == 0 && kb < ((a.cols + 511) >> 9) * 4) {
       uint8_t* p = scale + (kb >> 2) * rows4 * 4 + (kb & 3);
       *p = static_cast<uint8_t>(byte);
       if (last)  // scales of no row are 1
@@ -121,31 +130,73 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
                : "memory");
 }
 
-// A thread's slots: S rows of NA arrays of C pieces of 8 elements; thread-private.
+// E elements of 16 bytes: a thread's piece of a row.
+template <typename T>
+__device__ __forceinline__ void unpack_piece(const uint4& w, float (&v)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 2) {
+    unpack8(w, v, T());
+  } else {
+    v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+  }
+}
+// n of the elements exist.
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, int n, const float (&v)[16 / sizeof(T)]) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  union {
+    uint4 w;
+    T e[E];
+  } u;
+#pragma unroll
+  for (int i = 0; i < E; ++i) u.e[i] = from_f32<T>(v[i]);
+  if (n == E) {
+    *reinterpret_cast<uint4*>(p) = u.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i < n) p[i] = u.e[i];
+  }
+}
+template <int E>
+__device__ __forceinline__ void load_weight_piece(const void* w, int dt, int col, int n, float (&v)[E]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = 1.f;
+  } else if (dt == MUON_FP32) {
+    const float* p = static_cast<const float*>(w) + col;
+    if (n == E) {
+#pragma unroll
+      for (int q = 0; q < E / 4; ++q) {
+        const float4 f = reinterpret_cast<const float4*>(p)[q];
+        v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = i < n ? p[i] : 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      v[i] = i >= n               ? 0.f
+             : dt == MUON_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(w)[col + i])
+                               : to_f32(static_cast<const __half*>(w)[col + i]);
+  }
+}
+
+// A thread's slots: S rows of NA arrays of C pieces; thread-private.
 template <typename T, int TH, int C, int S, int NA>
 struct Ring {
-  static constexpr int P = static_cast<int>(sizeof(T)) / 2;  // 16-byte parts of a piece
-  static constexpr int BYTES = S * NA * C * P * TH * 16;
+  static constexpr int BYTES = S * NA * C * TH * 16;
   uint8_t* base;
-  __device__ __forceinline__ int at(int slot, int arr, int c, int p) const {
-    return ((((slot * NA + arr) * C + c) * P + p) * TH + static_cast<int>(threadIdx.x)) * 16;
+  __device__ __forceinline__ uint8_t* at(int slot, int arr, int c) const {
+    return base + (((slot * NA + arr) * C + c) * TH + static_cast<int>(threadIdx.x)) * 16;
   }
-  // Piece c of a row: src + 8 elements, `bytes` of which exist (the rest reads as 0).
+  // Piece c of a row: the 16 bytes at src, `bytes` of which exist (the rest reads as 0).
   __device__ __forceinline__ void fetch(int slot, int arr, int c, const T* src, int bytes) const {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int b = P == 1 ? bytes : max(0, min(16, bytes - 16 * p));
-      copy16(smem_u32(base + at(slot, arr, c, p)), P == 1 || b ? src + p * 4 : src, b);
-    }
+    copy16(smem_u32(at(slot, arr, c)), src, bytes);
   }
-  __device__ __forceinline__ void read(int slot, int arr, int c, float (&v)[8]) const {
-    if constexpr (P == 1) {
-      unpack8(*reinterpret_cast<const uint4*>(base + at(slot, arr, c, 0)), v, T());
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(base + at(slot, arr, c, 0));
-      const float4 b = *reinterpret_cast<const float4*>(base + at(slot, arr, c, 1));
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
+  __device__ __forceinline__ void read(int slot, int arr, int c, float (&v)[16 / sizeof(T)]) const {
+    unpack_piece<T>(*reinterpret_cast<const uint4*>(at(slot, arr, c)), v);
   }
 };
 
@@ -167,7 +218,7 @@ __device__ __forceinline__ float ring_sum(float v, float (*sh)[TH / 32], int tur
 
 template <typename T, int G, int C, int S, int MINB>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(const RmsNormArgs a) {
-  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G, E = 16 / static_cast<int>(sizeof(T));
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ float sh[2][TH / 32];
   const Ring<T, TH, C, S, 2> ring{ring_smem};
@@ -176,8 +227,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
   int n[C], off[C];  // existing columns of each piece, and its first (0 where none exists)
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    n[c] = max(0, min(8, a.cols - (c * G + t) * 8));
-    off[c] = n[c] ? (c * G + t) * 8 : 0;
+    n[c] = max(0, min(E, a.cols - (c * G + t) * E));
+    off[c] = n[c] ? (c * G + t) * E : 0;
   }
   const long long step = static_cast<long long>(gridDim.x) * R, row0 = static_cast<long long>(blockIdx.x) * R + rr;
   long long frow = row0;  // next row to fetch
@@ -201,57 +252,57 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
   pdl_wait();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
-  float w[KEEP ? C : 1][8];
+  float w[KEEP ? C : 1][E];
   if (KEEP) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[KEEP ? c : 0]);
+    for (int c = 0; c < C; ++c) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[KEEP ? c : 0]);
   }
   const float inv_cols = 1.f / static_cast<float>(a.cols);
   T* ph = static_cast<T*>(a.h) + (a.h ? row0 * a.ldh : 0);
   T* py = static_cast<T*>(a.y) + (a.y ? row0 * a.ldy : 0);
-  QOut q(a, row0, t);
+  QOut<E> q(a, row0, t);
   int slot = 0, turn = 0;
   // all threads of a CTA take the same number of turns (the barrier in ring_sum)
   for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
     const bool live = R == 1 || row < a.rows;
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
-    float s[C][8];
+    float s[C][E];
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       ring.read(slot, 0, c, s[c]);
       if (fr) {
-        float r[8];
+        float r[E];
         ring.read(slot, 1, c, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[c][i] += r[i];
+        for (int i = 0; i < E; ++i) s[c][i] += r[i];
       }
       if (R > 1 && !live) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[c][i] = 0.f;
+        for (int i = 0; i < E; ++i) s[c][i] = 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(s[c][i], s[c][i], sum);
+      for (int i = 0; i < E; ++i) sum = fmaf(s[c][i], s[c][i], sum);
     }
     sum = ring_sum<G, TH>(sum, sh, turn);
     const float rstd = rsqrtf(sum * inv_cols + a.eps);
     if (live && t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (live && a.h) store8(ph + off[c], n[c], n[c] == 8, s[c]);
-      if (!KEEP) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[0]);
+      if (live && a.h) store_piece(ph + off[c], n[c], s[c]);
+      if (!KEEP) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[c][i] *= rstd * w[KEEP ? c : 0][i];
-      if (n[c] < 8) {
+      for (int i = 0; i < E; ++i) s[c][i] *= rstd * w[KEEP ? c : 0][i];
+      if (n[c] < E) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < E; ++i)
           if (i >= n[c]) s[c][i] = 0.f;
       }
-      if (live && a.y) store8(py + off[c], n[c], n[c] == 8, s[c]);
+      if (live && a.y) store_piece(py + off[c], n[c], s[c]);
       if (a.q) q.store(a, c * G, s[c], live, row == a.rows - 1);
     }
-    if (a.q && live) pad_q_scales(a, row, C * G / 16 + t, G);
+    if (a.q && live) pad_q_scales(a, row, C * G * E / 128 + t, G);
     ph += step * a.ldh;
     py += step * a.ldy;
     q.advance(a, step);
@@ -300,7 +351,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(const RmsNo
   }
   sum = row_sum<G>(sum, sh);
   const float rstd = rsqrtf(sum * (1.f / static_cast<float>(a.cols)) + a.eps);
-  const QOut q(a, live ? row : 0, t);
+  const QOut<8> q(a, live ? row : 0, t);
   if (live && t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
   for (int c = 0; c < (WIDE ? 1 : C); ++c) {
@@ -350,9 +401,9 @@ static cudaError_t ring_smem_limit(F kernel, int bytes, bool (&done)[64]) {
   return cudaSuccess;
 }
 
-template <typename T, int G, int C, int S2, int MINB>
+template <typename T, int G, int C, int S, int MINB>
 static cudaError_t launch_norm_ring(const RmsNormArgs& a, int sms, cudaStream_t st) {
-  constexpr int TH = G < 128 ? 128 : G, R = TH / G, S = sizeof(T) == 4 ? (S2 + 1) / 2 : S2;
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
   constexpr int smem = Ring<T, TH, C, S, 2>::BYTES;
   static_assert(smem * MINB <= 220 * 1024, "shared memory of an SM");
   static bool done[64] = {false};
@@ -363,21 +414,24 @@ static cudaError_t launch_norm_ring(const RmsNormArgs& a, int sms, cudaStream_t 
                     dim3(TH), smem, st, a);
 }
 
+// Threads per row, pieces of 16 bytes per thread, rows of the ring and CTAs per SM by the row's width, as measured at
+// 33.5M elements; without 16-byte accesses, 8 columns per thread.
 template <typename T>
 static cudaError_t dispatch_norm(const RmsNormArgs& a, int sms, cudaStream_t st) {
-  const int pieces = (a.cols + 7) / 8;
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const int pieces = (a.cols + E - 1) / E;
   if (a.vec) {
     if (pieces <= 32) return launch_norm_ring<T, 32, 1, 4, 8>(a, sms, st);
     if (pieces <= 64) return launch_norm_ring<T, 32, 2, 4, 6>(a, sms, st);
     if (pieces <= 128) return launch_norm_ring<T, 128, 1, 4, 8>(a, sms, st);
-    if (pieces <= 256) return launch_norm_ring<T, 128, 2, 4, 6>(a, sms, st);
-    if (pieces <= 512) return launch_norm_ring<T, 256, 2, 4, 3>(a, sms, st);
+    if (pieces <= 256) return launch_norm_ring<T, 256, 1, 4, 4>(a, sms, st);
+    if (pieces <= 512) return launch_norm_ring<T, 512, 1, 5, 2>(a, sms, st);
     if (pieces <= 1024) return launch_norm_ring<T, 512, 2, 4, 1>(a, sms, st);
-    if (pieces <= 2048) return launch_norm_ring<T, 512, 4, 2, 1>(a, sms, st);
+    if (pieces <= 2048) return launch_norm_ring<T, 512, 4, 3, 1>(a, sms, st);
   } else {
-    if (pieces <= 64) return launch_norm<T, 32, 2, false>(a, st);
-    if (pieces <= 512) return launch_norm<T, 256, 2, false>(a, st);
-    if (pieces <= 2048) return launch_norm<T, 512, 4, false>(a, st);
+    if (a.cols <= 512) return launch_norm<T, 32, 2, false>(a, st);
+    if (a.cols <= 4096) return launch_norm<T, 256, 2, false>(a, st);
+    if (a.cols <= 16384) return launch_norm<T, 512, 4, false>(a, st);
   }
   return launch_norm<T, 512, 1, true>(a, st);
 }
@@ -504,7 +558,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_grad_kernel(const 
 
 template <typename T, int G, int C, int S, int MINB>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_kernel(const RmsNormGradArgs a) {
-  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G, E = 16 / static_cast<int>(sizeof(T));
   constexpr bool KEEP = C <= 2;  // the weight stays in registers
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ float sh[2][TH / 32];
@@ -513,8 +567,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
   int n[C], off[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    n[c] = max(0, min(8, a.cols - (c * G + t) * 8));
-    off[c] = n[c] ? (c * G + t) * 8 : 0;
+    n[c] = max(0, min(E, a.cols - (c * G + t) * E));
+    off[c] = n[c] ? (c * G + t) * E : 0;
   }
   const long long step = static_cast<long long>(gridDim.x) * R, row0 = static_cast<long long>(blockIdx.x) * R + rr;
   const bool add = a.dres && a.dx;
@@ -542,15 +596,15 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
   pdl_wait();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
-  float w[KEEP ? C : 1][8], dw[C][8];
+  float w[KEEP ? C : 1][E], dw[C][E];
   if (KEEP) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[KEEP ? c : 0]);
+    for (int c = 0; c < C; ++c) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[KEEP ? c : 0]);
   }
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
+    for (int i = 0; i < E; ++i) dw[c][i] = 0.f;
   const float inv_cols = 1.f / static_cast<float>(a.cols);
   int slot = 0, turn = 0;
   float next_rstd = row0 < a.rows ? __ldg(a.rstd + row0) : 0.f;  // a row ahead
@@ -561,7 +615,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
     next_rstd = row + step < a.rows ? __ldg(a.rstd + row + step) : 0.f;
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
-    float d[C][8], x[C][8];
+    float d[C][E], x[C][E];
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -569,11 +623,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
       ring.read(slot, 1, c, x[c]);
       if (R > 1 && !live) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[c][i] = x[c][i] = 0.f;
+        for (int i = 0; i < E; ++i) d[c][i] = x[c][i] = 0.f;
       }
-      if (!KEEP) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[0]);
+      if (!KEEP) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < E; ++i) {
         sum = fmaf(d[c][i] * w[KEEP ? c : 0][i], x[c][i], sum);
         dw[c][i] = fmaf(d[c][i] * x[c][i], rstd, dw[c][i]);
       }
@@ -583,17 +637,17 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
     if (a.dx && live) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float v[8];
-        if (!KEEP) load_weight8(a.weight, a.weight_dt, off[c], n[c], n[c] == 8, w[0]);
+        float v[E];
+        if (!KEEP) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[0]);
         if (add) {
           ring.read(slot, 2, c, v);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = 0.f;
+          for (int i = 0; i < E; ++i) v[i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += rstd * (d[c][i] * w[KEEP ? c : 0][i] - x[c][i] * k);
-        store8(px + off[c], n[c], n[c] == 8, v);
+        for (int i = 0; i < E; ++i) v[i] += rstd * (d[c][i] * w[KEEP ? c : 0][i] - x[c][i] * k);
+        store_piece(px + off[c], n[c], v);
       }
     }
     px += step * a.lddx;
@@ -604,26 +658,26 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
   if (R > 1) {  // join the CTA's row groups through the ring's memory
     cp_async_wait<0>();
     __syncthreads();
-    float* dwsh = reinterpret_cast<float*>(ring_smem);  // [R - 1][G * C * 8]
+    float* dwsh = reinterpret_cast<float*>(ring_smem);  // [R - 1][C * E][G]
     if (rr > 0) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dwsh[((rr - 1) * C * 8 + c * 8 + i) * G + t] = dw[c][i];
+        for (int i = 0; i < E; ++i) dwsh[((rr - 1) * C * E + c * E + i) * G + t] = dw[c][i];
     }
     __syncthreads();
     if (rr > 0) return;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        for (int r = 1; r < R; ++r) dw[c][i] += dwsh[((r - 1) * C * 8 + c * 8 + i) * G + t];
+      for (int i = 0; i < E; ++i)
+        for (int r = 1; r < R; ++r) dw[c][i] += dwsh[((r - 1) * C * E + c * E + i) * G + t];
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int col = (c * G + t) * 8;
+    const int col = (c * G + t) * E;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < E; ++i)
       if (i < n[c]) part[col + i] = dw[c][i];
   }
 }
@@ -650,17 +704,17 @@ __global__ void __launch_bounds__(256) rms_norm_dweight_kernel(const float* part
 struct GradPlan {
   int rows_per_cta, ctas_per_sm;
 };
-static GradPlan grad_plan(int cols) {
-  const int pieces = (cols + 7) / 8;
+static GradPlan grad_plan(int cols, int dt) {
+  const int pieces = dt == MUON_FP32 ? (cols + 3) / 4 : (cols + 7) / 8;
   if (pieces <= 32) return {4, 6};
   if (pieces <= 64) return {4, 4};
   if (pieces <= 128) return {1, 6};
-  if (pieces <= 256) return {1, 4};
+  if (pieces <= 256) return {1, 3};
   if (pieces <= 512 || pieces > 2048) return {1, 2};
   return {1, 1};
 }
-int rms_norm_grad_ctas(long long rows, int cols, int sms) {
-  const GradPlan p = grad_plan(cols);
+int rms_norm_grad_ctas(long long rows, int cols, int dt, int sms) {
+  const GradPlan p = grad_plan(cols, dt);
   return static_cast<int>(
       std::max(1LL, std::min<long long>((rows + p.rows_per_cta - 1) / p.rows_per_cta, static_cast<long long>(p.ctas_per_sm) * sms)));
 }
@@ -672,9 +726,9 @@ static cudaError_t launch_grad(const RmsNormGradArgs& a, int ctas, cudaStream_t 
   return launch_pdl(rms_norm_grad_kernel<T, G, C, WIDE>, dim3(ctas), dim3(TH), smem, st, a);
 }
 
-template <typename T, int G, int C, int S2, int MINB>
+template <typename T, int G, int C, int S, int MINB>
 static cudaError_t launch_grad_ring(const RmsNormGradArgs& a, int ctas, cudaStream_t st) {
-  constexpr int TH = G < 128 ? 128 : G, S = sizeof(T) == 4 ? (S2 + 1) / 2 : S2;
+  constexpr int TH = G < 128 ? 128 : G;
   constexpr int smem = Ring<T, TH, C, S, 3>::BYTES;
   static_assert(smem * MINB <= 224 * 1024, "shared memory of an SM");
   static bool done[64] = {false};
@@ -683,29 +737,30 @@ static cudaError_t launch_grad_ring(const RmsNormGradArgs& a, int ctas, cudaStre
   return launch_pdl(rms_norm_grad_ring_kernel<T, G, C, S, MINB>, dim3(ctas), dim3(TH), smem, st, a);
 }
 
-// The ring kernels' rows per CTA and CTAs per SM are grad_plan's.
+// The ring kernels' rows per CTA and CTAs per SM are grad_plan's; the others step over any number of CTAs.
 template <typename T>
 static cudaError_t dispatch_grad(const RmsNormGradArgs& a, int ctas, cudaStream_t st) {
-  const int pieces = (a.cols + 7) / 8;
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const int pieces = (a.cols + E - 1) / E;
   if (a.vec) {
     if (pieces <= 32) return launch_grad_ring<T, 32, 1, 4, 6>(a, ctas, st);
     if (pieces <= 64) return launch_grad_ring<T, 32, 2, 4, 4>(a, ctas, st);
     if (pieces <= 128) return launch_grad_ring<T, 128, 1, 4, 6>(a, ctas, st);
-    if (pieces <= 256) return launch_grad_ring<T, 128, 2, 4, 4>(a, ctas, st);
+    if (pieces <= 256) return launch_grad_ring<T, 256, 1, 5, 3>(a, ctas, st);
     if (pieces <= 512) return launch_grad_ring<T, 256, 2, 4, 2>(a, ctas, st);
     if (pieces <= 1024) return launch_grad_ring<T, 512, 2, 4, 1>(a, ctas, st);
     if (pieces <= 2048) return launch_grad_ring<T, 512, 4, 2, 1>(a, ctas, st);
   } else {
-    if (pieces <= 64) return launch_grad<T, 32, 2, false>(a, ctas, st);
-    if (pieces <= 256) return launch_grad<T, 128, 2, false>(a, ctas, st);
-    if (pieces <= 512) return launch_grad<T, 256, 2, false>(a, ctas, st);
-    if (pieces <= 1024) return launch_grad<T, 512, 2, false>(a, ctas, st);
+    if (a.cols <= 512) return launch_grad<T, 32, 2, false>(a, ctas, st);
+    if (a.cols <= 2048) return launch_grad<T, 128, 2, false>(a, ctas, st);
+    if (a.cols <= 4096) return launch_grad<T, 256, 2, false>(a, ctas, st);
+    if (a.cols <= 8192) return launch_grad<T, 512, 2, false>(a, ctas, st);
   }
   return launch_grad<T, 512, 1, true>(a, ctas, st);
 }
 
 cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, int dt, int sms, cudaStream_t st) {
-  const int ctas = rms_norm_grad_ctas(a.rows, a.cols, sms);
+  const int ctas = rms_norm_grad_ctas(a.rows, a.cols, dt, sms);
   cudaError_t e = dt == MUON_BF16   ? dispatch_grad<__nv_bfloat16>(a, ctas, st)
                   : dt == MUON_FP16 ? dispatch_grad<__half>(a, ctas, st)
                                     : dispatch_grad<float>(a, ctas, st);

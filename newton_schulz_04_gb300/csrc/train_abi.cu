@@ -182,8 +182,10 @@ muon_status muon_rms_norm(const void* x, int64_t ldx, const void* residual, int6
 
 size_t muon_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1 || cols > MUON_MAX_DIM) return 0;
-  // the most CTAs that any sm_103 device gives the kernel
-  return static_cast<size_t>(rms_norm_grad_ctas(rows, static_cast<int>(cols), MUON_MAX_SMS)) * cols * sizeof(float);
+  // the most CTAs that any type and sm_103 device give the kernel
+  const int c = static_cast<int>(cols);
+  const int ctas = std::max(rms_norm_grad_ctas(rows, c, MUON_FP32, MUON_MAX_SMS), rms_norm_grad_ctas(rows, c, MUON_BF16, MUON_MAX_SMS));
+  return static_cast<size_t>(ctas) * cols * sizeof(float);
 }
 
 muon_status muon_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,

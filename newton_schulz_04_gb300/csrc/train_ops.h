@@ -60,7 +60,7 @@ struct RmsNormGradArgs {
   int vec;
 };
 // CTAs of the gradient kernel, i.e. rows of `partial`.
-int rms_norm_grad_ctas(long long rows, int cols, int sms);
+int rms_norm_grad_ctas(long long rows, int cols, int dt, int sms);
 cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, int dt, int sms, cudaStream_t st);
 
 // ---- fp8_quant.cu
