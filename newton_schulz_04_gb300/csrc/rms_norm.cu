@@ -14,7 +14,9 @@
 // deep) that no other thread reads, so the ring needs no barrier, and the only
 // synchronisation of a row is the one of its sum.  One short-lived CTA per row
 // moved 8192 x 4096 bf16 rows in 60 us (forward) and, with its rows in a loop but
-// nothing fetched ahead, 119 us (gradient); the ring takes RING_F and RING_B.
+// nothing fetched ahead, 119 us (gradient); the ring takes 50 (6.1 TB/s) and 49.5 (5.4 TB/s,
+// with the second kernel).  The depths below were measured at 33.5M elements: more CTAs per SM
+// than two or three, or rings that no longer let them fit, cost up to a third.
 //
 // Rows that allow no 16-byte accesses, or that are too wide for a ring, take kernels
 // that load straight to registers, the widest (WIDE) a second time from L1 / L2.
@@ -208,12 +210,21 @@ __device__ __forceinline__ float ring_sum(float v, float (*sh)[TH / 32], int tur
   if (G == 32) return v;
   if ((threadIdx.x & 31) == 0) sh[turn & 1][threadIdx.x >> 5] = v;
   __syncthreads();
-  constexpr int W = G / 32;
-  const int first = (threadIdx.x / G) * W;
-  float s = 0.f;
+  constexpr int W = G / 32;  // added as a tree: each of the last additions rounds the whole
+  float s = sh[turn & 1][(threadIdx.x / G) * W + (threadIdx.x & (W - 1))];
 #pragma unroll
-  for (int w = 0; w < W; ++w) s += sh[turn & 1][first + w];
+  for (int o = W / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
+}
+
+// 1 / sqrt(sum / cols + eps), the quotient and the root corrected by a step of Newton's:
+// y goes on to 8 bits, and an error common to a row moves all its values that lie near the middle of two.
+__device__ __forceinline__ float row_rstd(float sum, float cols, float inv_cols, float eps) {
+  const float q = sum * inv_cols;
+  const float m = (isfinite(q) ? fmaf(fmaf(-q, cols, sum), inv_cols, q) : q) + eps;
+  const float r = rsqrtf(m);
+  const float better = fmaf(0.5f * r, fmaf(-(m * r), r, 1.f), r);
+  return isfinite(better) ? better : r;  // of a sum of 0 (without eps), infinity or NaN
 }
 
 template <typename T, int G, int C, int S, int MINB>
@@ -286,14 +297,14 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
       for (int i = 0; i < E; ++i) sum = fmaf(s[c][i], s[c][i], sum);
     }
     sum = ring_sum<G, TH>(sum, sh, turn);
-    const float rstd = rsqrtf(sum * inv_cols + a.eps);
+    const float rstd = row_rstd(sum, static_cast<float>(a.cols), inv_cols, a.eps);
     if (live && t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (live && a.h) store_piece(ph + off[c], n[c], s[c]);
       if (!KEEP) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[0]);
 #pragma unroll
-      for (int i = 0; i < E; ++i) s[c][i] *= rstd * w[KEEP ? c : 0][i];
+      for (int i = 0; i < E; ++i) s[c][i] = s[c][i] * rstd * w[KEEP ? c : 0][i];
       if (n[c] < E) {
 #pragma unroll
         for (int i = 0; i < E; ++i)
@@ -350,7 +361,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(const RmsNo
       for (int i = 0; i < 8; ++i) sum = fmaf(s[c][i], s[c][i], sum);
   }
   sum = row_sum<G>(sum, sh);
-  const float rstd = rsqrtf(sum * (1.f / static_cast<float>(a.cols)) + a.eps);
+  const float cols = static_cast<float>(a.cols), rstd = row_rstd(sum, cols, 1.f / cols, a.eps);
   const QOut<8> q(a, live ? row : 0, t);
   if (live && t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(const RmsNo
       if (a.h) store8(static_cast<T*>(a.h) + row * a.ldh + col, n, full, v);
       load_weight8(a.weight, a.weight_dt, col, n, full, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < n ? v[i] * (rstd * w[i]) : 0.f;
+      for (int i = 0; i < 8; ++i) v[i] = i < n ? v[i] * rstd * w[i] : 0.f;
       if (a.y) store8(static_cast<T*>(a.y) + row * a.ldy + col, n, full, v);
       if (a.q) q.store(a, cc * G, v, live, row == a.rows - 1);
     }
@@ -422,12 +433,12 @@ static cudaError_t dispatch_norm(const RmsNormArgs& a, int sms, cudaStream_t st)
   const int pieces = (a.cols + E - 1) / E;
   if (a.vec) {
     if (pieces <= 32) return launch_norm_ring<T, 32, 1, 4, 8>(a, sms, st);
-    if (pieces <= 64) return launch_norm_ring<T, 32, 2, 4, 6>(a, sms, st);
-    if (pieces <= 128) return launch_norm_ring<T, 128, 1, 4, 8>(a, sms, st);
-    if (pieces <= 256) return launch_norm_ring<T, 256, 1, 4, 4>(a, sms, st);
+    if (pieces <= 64) return launch_norm_ring<T, 64, 1, 5, 6>(a, sms, st);
+    if (pieces <= 128) return launch_norm_ring<T, 64, 2, 4, 3>(a, sms, st);
+    if (pieces <= 256) return launch_norm_ring<T, 256, 1, 4, 3>(a, sms, st);
     if (pieces <= 512) return launch_norm_ring<T, 512, 1, 5, 2>(a, sms, st);
     if (pieces <= 1024) return launch_norm_ring<T, 512, 2, 4, 1>(a, sms, st);
-    if (pieces <= 2048) return launch_norm_ring<T, 512, 4, 3, 1>(a, sms, st);
+    if (pieces <= 2048) return launch_norm_ring<T, 1024, 2, 3, 1>(a, sms, st);
   } else {
     if (a.cols <= 512) return launch_norm<T, 32, 2, false>(a, st);
     if (a.cols <= 4096) return launch_norm<T, 256, 2, false>(a, st);
@@ -707,8 +718,8 @@ struct GradPlan {
 static GradPlan grad_plan(int cols, int dt) {
   const int pieces = dt == MUON_FP32 ? (cols + 3) / 4 : (cols + 7) / 8;
   if (pieces <= 32) return {4, 6};
-  if (pieces <= 64) return {4, 4};
-  if (pieces <= 128) return {1, 6};
+  if (pieces <= 64) return {4, 3};
+  if (pieces <= 128) return {2, 3};
   if (pieces <= 256) return {1, 3};
   if (pieces <= 512 || pieces > 2048) return {1, 2};
   return {1, 1};
@@ -744,12 +755,12 @@ static cudaError_t dispatch_grad(const RmsNormGradArgs& a, int ctas, cudaStream_
   const int pieces = (a.cols + E - 1) / E;
   if (a.vec) {
     if (pieces <= 32) return launch_grad_ring<T, 32, 1, 4, 6>(a, ctas, st);
-    if (pieces <= 64) return launch_grad_ring<T, 32, 2, 4, 4>(a, ctas, st);
-    if (pieces <= 128) return launch_grad_ring<T, 128, 1, 4, 6>(a, ctas, st);
+    if (pieces <= 64) return launch_grad_ring<T, 32, 2, 4, 3>(a, ctas, st);
+    if (pieces <= 128) return launch_grad_ring<T, 64, 2, 4, 3>(a, ctas, st);
     if (pieces <= 256) return launch_grad_ring<T, 256, 1, 5, 3>(a, ctas, st);
     if (pieces <= 512) return launch_grad_ring<T, 256, 2, 4, 2>(a, ctas, st);
     if (pieces <= 1024) return launch_grad_ring<T, 512, 2, 4, 1>(a, ctas, st);
-    if (pieces <= 2048) return launch_grad_ring<T, 512, 4, 2, 1>(a, ctas, st);
+    if (pieces <= 2048) return launch_grad_ring<T, 1024, 2, 2, 1>(a, ctas, st);
   } else {
     if (a.cols <= 512) return launch_grad<T, 32, 2, false>(a, ctas, st);
     if (a.cols <= 2048) return launch_grad<T, 128, 2, false>(a, ctas, st);
