@@ -438,6 +438,14 @@ MUON_API muon_status muon_partition(const double* cost, int count, int world, in
  *          are written as 127 (1); what they hold does not matter.
  * Element (r, c) stands for data * scale.  A scale shared by 128 x 128 elements is
  * kept once for each of its rows.
+ *
+ * The first call of each operator on a device loads its code and sets it up: make it
+ * before any stream capture.  Errors, before anything is launched, are those of the
+ * update: MUON_ERR_ARG for a NULL pointer that is not optional, a bad type, format or
+ * scalar, no output at all, or matrices that overlap in another way than allowed;
+ * MUON_ERR_SHAPE for sizes out of range and strides below the row length;
+ * MUON_ERR_ALIGN, MUON_ERR_WORKSPACE, MUON_ERR_UNSUPPORTED and MUON_ERR_CUDA as
+ * everywhere.
  */
 
 typedef enum {
@@ -468,12 +476,7 @@ MUON_API size_t muon_clip_workspace_bytes(int count);
  * Squares that leave fp32's range do not spoil the norm of finite gradients.  An
  * infinite norm gives c = 0 (infinite elements become NaN), a NaN one gives NaN.
  * max_norm may be infinite.  Sums run in a fixed order.  Two launches up to 1024
- * tensors.
- * Errors (nothing launched): MUON_ERR_ARG for count < 0, NULL arrays or pointers
- * of non-empty tensors, no output at all, a bad dtype, max_norm or eps negative or
- * NaN (eps: or infinite), an out that partly overlaps its gradient or the
- * workspace; MUON_ERR_SHAPE, MUON_ERR_ALIGN, MUON_ERR_WORKSPACE,
- * MUON_ERR_UNSUPPORTED as elsewhere.
+ * tensors.  A tensor is listed once, and outputs overlap no other tensor.
  */
 MUON_API muon_status muon_clip_grads(const void* const* grads, void* const* out, const int64_t* numel,
                                      const int32_t* dtypes, int count, float max_norm, float eps, float* norm,
@@ -491,7 +494,7 @@ MUON_API muon_status muon_clip_grads(const void* const* grads, void* const* out,
  *   rstd    [rows] fp32 rho (the gradient needs it), or NULL.
  *   q, q_scale  8-bit copy of the unrounded y (see above), or both NULL.
  * y or h may be x or residual themselves.  cols in [1, MUON_MAX_DIM], rows in
- * [0, MUON_MAX_ROWS].  Errors as elsewhere, before anything is launched.
+ * [0, MUON_MAX_ROWS].
  */
 MUON_API muon_status muon_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                    const void* weight, muon_dtype weight_dt, int64_t rows, int64_t cols, float eps,

@@ -434,7 +434,7 @@ static cudaError_t dispatch_norm(const RmsNormArgs& a, int sms, cudaStream_t st)
   if (a.vec) {
     if (pieces <= 32) return launch_norm_ring<T, 32, 1, 4, 8>(a, sms, st);
     if (pieces <= 64) return launch_norm_ring<T, 64, 1, 5, 6>(a, sms, st);
-    if (pieces <= 128) return launch_norm_ring<T, 64, 2, 4, 3>(a, sms, st);
+    if (pieces <= 128) return launch_norm_ring<T, 64, 2, 4, 4>(a, sms, st);
     if (pieces <= 256) return launch_norm_ring<T, 256, 1, 4, 3>(a, sms, st);
     if (pieces <= 512) return launch_norm_ring<T, 512, 1, 5, 2>(a, sms, st);
     if (pieces <= 1024) return launch_norm_ring<T, 512, 2, 4, 1>(a, sms, st);

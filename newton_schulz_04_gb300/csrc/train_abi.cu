@@ -170,6 +170,10 @@ muon_status muon_rms_norm(const void* x, int64_t ldx, const void* residual, int6
       return fail(MUON_ERR_ARG, "an output partly overlaps an input");
   if (y && h && overlap(y, span(rows, cols, ldy, size), h, span(rows, cols, ldh, size)))
     return fail(MUON_ERR_ARG, "y and h overlap");
+  const long long nq = span(rows, cols, ldq, 1);
+  if (overlap(q, nq, x, span(rows, cols, ldx, size)) || overlap(q, nq, residual, span(rows, cols, ldr, size)) ||
+      overlap(q, nq, y, span(rows, cols, ldy, size)) || overlap(q, nq, h, span(rows, cols, ldh, size)))
+    return fail(MUON_ERR_ARG, "q overlaps another matrix");
   muon_status st;
   const int sms = gpu(&st);
   if (st != MUON_OK) return st;

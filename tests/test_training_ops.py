@@ -638,3 +638,48 @@ def test_operators_under_graph_capture(mm):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want) and float(m) == float(n)
+
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "fp8_training_step.py")
+    spec = importlib.util.spec_from_file_location("fp8_training_step", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+@gpu
+def test_example_gradients_match_autograd(mm):
+    """The example's 8-bit forward and backward pass against fp32 autograd of the same model, to 8-bit accuracy."""
+    ex = _example()
+    model = ex.Mlp(2, 256, 384, seed=3)
+    x = gen(1, 300, 256).bfloat16().cuda()
+    y, saved = model.forward(x)
+    dy = gen(2, 300, 256).bfloat16().cuda()
+    matrices, norms = model.backward(dy, saved)
+    ws = [w.master.float().requires_grad_() for w in model.weights]
+    ns = [n.clone().requires_grad_() for n in model.norms]
+    s = x.float()
+    for i in range(2):
+        n = s * torch.rsqrt(s.square().mean(1, keepdim=True) + 1e-6) * ns[i]
+        s = s + torch.nn.functional.silu(n @ ws[2 * i].t()) @ ws[2 * i + 1].t()
+    out = s * torch.rsqrt(s.square().mean(1, keepdim=True) + 1e-6) * ns[2]
+    (out * dy.float()).sum().backward()
+    # an 8-bit operand is off by 2^-4 (e4m3) or 2^-3 (e5m2) of its value at most, a third of that in the mean square;
+    # a gradient passes at most six such operands in a row
+    far = lambda a, b: float((a.float() - b.detach()).norm() / b.detach().norm())  # noqa: E731
+    limit = 6 ** 0.5 * 2.0 ** -3 / 3 ** 0.5
+    assert far(y, out) < limit
+    for got, want in zip(matrices, ws):
+        assert far(got, want.grad) < limit
+    for got, want in zip(norms, ns):
+        assert far(got, want.grad) < limit
+
+
+@gpu
+def test_example_learns(mm):
+    losses, norms = _example().train(steps=12, tokens=1024, log=lambda *_: None)
+    assert all(math.isfinite(v) for v in losses + norms)
+    assert losses[-1] < 0.9 * losses[0]
