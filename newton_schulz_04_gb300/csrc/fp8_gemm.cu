@@ -175,39 +175,66 @@ __device__ __forceinline__ F8Item decode_item(const F8Args& a, int u, int part) 
   return it;
 }
 
-// Rows m0 .. m0 + rows - 1 (at most 32, one register each) of column n of the output.
-template <typename T>
-__device__ __forceinline__ void epi_chunk(const F8Args& a, long long m0, int rows, long long n, const float (&v)[32]) {
-  if (n >= a.n) return;
-  T* o = static_cast<T*>(a.out) + m0 * a.ldc + n;
-  if (a.add) {
-    const T* d = static_cast<const T*>(a.add) + m0 * a.ldadd + n;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      T x[16];
-#pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        if (16 * h + u < rows) x[u] = *d;
-        d += a.ldadd;
-      }
-#pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        if (16 * h + u < rows) *o = from_f32<T>(v[16 * h + u] + to_f32(x[u]));
-        o += a.ldc;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < 32; ++u) {
-      if (u < rows) *o = from_f32<T>(v[u]);
-      o += a.ldc;
-    }
-  }
+// p + ld, kept as a step from the last row: computed at once, the 32 addresses take 64 registers.
+template <typename P>
+__device__ __forceinline__ P* step(P* p, long long ld) {
+  p += ld;
+  asm volatile("" : "+l"(p));
+  return p;
 }
-__device__ __forceinline__ void epi_chunk(const F8Args& a, long long m0, int rows, long long n, const float (&v)[32]) {
-  if (a.out_dt == MUON_FP32) epi_chunk<float>(a, m0, rows, n, v);
-  else if (a.out_dt == MUON_BF16) epi_chunk<__nv_bfloat16>(a, m0, rows, n, v);
-  else epi_chunk<__half>(a, m0, rows, n, v);
+__device__ __forceinline__ void tmem_ld_rows(uint32_t t, float (&v)[32]) { tmem_ld_32x32b_x32(t, v); }
+__device__ __forceinline__ void tmem_ld_rows(uint32_t t, float (&v)[16]) { tmem_ld_32x32b_x16(t, v); }
+
+// A warp's share of a tile: every other chunk of CH rows of C, one row per register, from
+// row m0 on (`rows` of them exist), column n of this lane.  `ready` waits for the accumulator.  The
+// first rows to add are on their way before that, the next ones while a chunk is stored
+// (the weight gradient of 4096 x 4096 over 8192 tokens, repeated under the power cap: 105 -> 103 us).
+template <typename T, bool ADD, typename F>
+__device__ __forceinline__ bool epi_tile(const F8Args& a, uint32_t acc, long long m0, int rows, int half, long long n,
+                                         const F& ready) {
+  constexpr int CH = ADD ? 16 : 32;
+  const bool in = n < a.n;
+  int c = half * CH;
+  T x[ADD ? CH : 1];
+  const T* d = static_cast<const T*>(a.add) + (ADD ? (m0 + c) * a.ldadd + n : 0);
+  const auto fetch = [&](int left) {
+    if (in) {
+#pragma unroll
+      for (int u = 0; u < CH; ++u) {
+        if (u < left) x[ADD ? u : 0] = *d;
+        d = step(d, a.ldadd);
+      }
+      d += CH * a.ldadd;
+    }
+  };
+  if (ADD) fetch(rows - c);
+  if (!ready()) return false;
+  T* o = static_cast<T*>(a.out) + (m0 + c) * a.ldc + n;
+  for (; c < rows; c += 2 * CH) {
+    float v[CH];
+    tmem_ld_rows(acc + c, v);
+    if (in) {
+      if (ADD) {
+#pragma unroll
+        for (int u = 0; u < CH; ++u)
+          if (c + u < rows) v[u] += to_f32(x[ADD ? u : 0]);
+        fetch(rows - c - 2 * CH);
+      }
+#pragma unroll
+      for (int u = 0; u < CH; ++u) {
+        if (c + u < rows) *o = from_f32<T>(v[u]);
+        o = step(o, a.ldc);
+      }
+      o += CH * a.ldc;
+    }
+    __syncwarp();
+  }
+  return true;
+}
+template <typename T, typename F>
+__device__ __forceinline__ bool epi_tile(const F8Args& a, uint32_t acc, long long m0, int rows, int half, long long n,
+                                         const F& ready) {
+  return a.add ? epi_tile<T, true>(a, acc, m0, rows, half, n, ready) : epi_tile<T, false>(a, acc, m0, rows, half, n, ready);
 }
 // One element.
 __device__ __forceinline__ void epi_one(const F8Args& a, long long m, long long n, float v) {
@@ -474,16 +501,19 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
       const long long n = it.i * 256LL + rank * C::BN + quarter * 32 + lane;
       const long long m0 = static_cast<long long>(it.j) * a.tile_m;
       const int rows = static_cast<int>(min(static_cast<long long>(a.tile_m), a.m - m0));
-      if (lane == 0) ok = !*abort_flag && mbar_wait(&tfull[abuf], (tile >> 1) & 1);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + abuf * C::ACC_COLS;
+      const auto ready = [&]() -> bool {
+        const bool full_now = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&tfull[abuf], (tile >> 1) & 1));
+        tc_fence_after();
+        return full_now;
+      };
       if (SPLIT) {
         // Rows of A p share .. are added up by part p.  One item per cluster: nothing is received twice.
         const int share = a.tile_m / a.splits, shift = __ffs(share) - 1, c = half_tile * 32;  // 8, 16 or 32 rows
         const float* sums = reinterpret_cast<const float*>(recv) + quarter * 32 + lane;  // [part][row][128]
         float v[32];
+        ok = ready();
+        if (!ok) break;
         if (c < a.tile_m) tmem_ld_32x32b_x32(acc + c, v);
 #pragma unroll 1
         for (int p = 0; p < a.splits; ++p) {
@@ -510,12 +540,10 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         }
         __syncwarp();
       } else {
-        for (int c = half_tile * 32; c < rows; c += 64) {
-          float v[32];
-          tmem_ld_32x32b_x32(acc + c, v);
-          epi_chunk(a, m0 + c, min(32, rows - c), n, v);
-          __syncwarp();
-        }
+        ok = a.out_dt == MUON_FP32   ? epi_tile<float>(a, acc, m0, rows, half_tile, n, ready)
+             : a.out_dt == MUON_BF16 ? epi_tile<__nv_bfloat16>(a, acc, m0, rows, half_tile, n, ready)
+                                     : epi_tile<__half>(a, acc, m0, rows, half_tile, n, ready);
+        if (!ok) break;
       }
       tc_fence_before();
       __syncwarp();
