@@ -12,7 +12,7 @@
 // writes with the evict-first policy so as not to push out what is still to be read.
 // Its first chunk is on its way before the sums are complete.
 //
-// Sums: fp32 per thread, 64 bits across threads.  Squares that leave fp32's range
+// Sums: fp32 within a warp, 64 bits across.  Squares that leave fp32's range
 // (a CTA's sum that is not finite, or below 2^-100) are summed again, scaled by
 // 2^-80 or 2^100, so the norm of finite gradients is right over the whole range.
 #include <cuda_runtime.h>

@@ -5,11 +5,15 @@
 // Blocks are 1 x 128 along the axis that the product sums over, or 128 x 128.
 // `q` keeps x's orientation (blocks along its columns); `qt` is x transposed
 // (blocks along x's rows), what a weight gradient reads, where the summed axis is
-// the tokens.  One pass over x writes both: bound by memory (2 + 1 + 1 bytes per
-// bf16 element).  A CTA takes a 128 x 128 tile, each thread 8 x 8 of it in
-// registers; row maxima are four shuffles, column maxima and the transposed bytes go
-// through 16 KB of shared memory (8-byte slots swizzled, so both the writes by
-// column and the reads by row are free of bank conflicts).
+// the tokens.  One pass over x writes both: 2 + 1 + 1 bytes per bf16 element.  A CTA
+// takes a 128 x 128 tile, each thread 8 x 8 of it in registers (16-bit types as
+// loaded, two to a register, with maxima of packed halves); row maxima are four
+// shuffles, column maxima and the transposed bytes go through 16 KB of shared memory
+// (8-byte slots swizzled, so both the writes by column and the reads by row are free
+// of bank conflicts).  A square block's bytes are the same both ways and are only
+// transposed, four by four.  Bound by memory and, close behind, by the conversions: 4096 x
+// 14336 bf16 takes 39 us (6.0 TB/s); with values unpacked to fp32, formats chosen at run
+// time and every byte converted twice it took 106.
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"
@@ -71,7 +75,7 @@ struct Piece {
 };
 
 template <typename T, bool E5M2, bool SQUARE>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp8_quantize_kernel(const Fp8QuantArgs a) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : SQUARE ? 3 : 2) fp8_quantize_kernel(const Fp8QuantArgs a) {
   constexpr int W = Piece<T>::W;
   __shared__ uint2 tile[128][16];  // transposed bytes: [column][8-row slot, swizzled]
   __shared__ __align__(16) uint32_t cmax[8][16][W];  // column maxima of each warp's 16 rows
