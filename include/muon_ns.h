@@ -558,6 +558,9 @@ MUON_API muon_status muon_fp8_matmul(const void* a, int64_t lda, const void* a_s
  */
 MUON_API muon_status muon_fp8_status(void* stream);
 
+/* muon_debug_bounded_wait on the 8-bit product's status word (failure-detection self-test of muon_fp8_status). */
+MUON_API muon_status muon_debug_bounded_wait_fp8(long long max_cycles, void* stream);
+
 /* Thread-local message of the last failed call on this thread ("" if none). */
 MUON_API const char* muon_last_error(void);
 

@@ -11,6 +11,6 @@ from .binding import (  # noqa: F401
     sched_code, schedule_candidates, static_status, tune_schedules, workspace_bytes,
 )
 from .training import (  # noqa: F401
-    Fp8Tensor, RmsNormOutput, clip_grads, fp8_matmul, fp8_quantize, fp8_status, grad_norm,
+    Fp8Tensor, RmsNormOutput, clip_grads, debug_bounded_wait_fp8, fp8_matmul, fp8_quantize, fp8_status, grad_norm,
     rms_norm, rms_norm_backward,
 )

@@ -119,6 +119,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.muon_fp8_matmul.restype = i32
     lib.muon_fp8_status.argtypes = [vp]
     lib.muon_fp8_status.restype = i32
+    lib.muon_debug_bounded_wait_fp8.argtypes = [ctypes.c_longlong, vp]
+    lib.muon_debug_bounded_wait_fp8.restype = i32
     lib.muon_last_error.argtypes = []
     lib.muon_last_error.restype = ctypes.c_char_p
     lib.muon_version.argtypes = []

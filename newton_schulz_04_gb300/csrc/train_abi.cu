@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "kernels.h"
 #include "train_ops.h"
 
 namespace muon {
@@ -322,6 +323,15 @@ muon_status muon_fp8_status(void* stream) {
   if (e != cudaSuccess) return fail(MUON_ERR_CUDA, "status: %s", cudaGetErrorString(e));
   if (word & kStatusTimeout) return fail(MUON_ERR_TIMEOUT, "a kernel gave up on a bounded wait");
   return MUON_OK;
+}
+
+muon_status muon_debug_bounded_wait_fp8(long long max_cycles, void* stream) {
+  clear_error();
+  if (max_cycles <= 0 || max_cycles > 10000000000LL) return fail(MUON_ERR_ARG, "max_cycles out of range");
+  int* p = nullptr;
+  cudaError_t e = fp8_status_address(&p);
+  if (e == cudaSuccess) e = launch_debug_wait(p, max_cycles, static_cast<cudaStream_t>(stream));
+  return launched(e, "launch_debug_wait");
 }
 
 }  // extern "C"

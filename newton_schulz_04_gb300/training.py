@@ -221,6 +221,10 @@ def fp8_status(stream=None) -> int:
     return _b.load().muon_fp8_status(ctypes.c_void_p(_b._stream_ptr(stream)))
 
 
+def debug_bounded_wait_fp8(max_cycles: int, stream=None) -> None:
+    _b._check(_b.load().muon_debug_bounded_wait_fp8(int(max_cycles), ctypes.c_void_p(_b._stream_ptr(stream))))
+
+
 # ---------------------------------------------------------------- RMS norm
 
 class RmsNormOutput(NamedTuple):

@@ -683,3 +683,66 @@ def test_example_learns(mm):
     losses, norms = _example().train(steps=12, tokens=1024, log=lambda *_: None)
     assert all(math.isfinite(v) for v in losses + norms)
     assert losses[-1] < 0.9 * losses[0]
+
+
+@gpu
+def test_fp8_status_reports_a_wait_that_ran_out(mm):
+    assert mm.fp8_status() == 0
+    mm.debug_bounded_wait_fp8(100_000)
+    assert mm.fp8_status() == 6   # MUON_ERR_TIMEOUT, once
+    assert mm.fp8_status() == 0
+    with pytest.raises(mm.MuonError):
+        mm.debug_bounded_wait_fp8(0)
+
+
+@gpu
+def test_rms_norm_weight_off_16_bytes(mm):
+    """A weight at an odd address takes the kernels without 16-byte accesses; so do odd strides, with the same values."""
+    x, w = gen(1, 37, 1200).bfloat16(), 1 + gen(2, 1201, std=0.1)
+    a = mm.rms_norm(x.cuda(), w.cuda()[1:], fp8="e4m3")
+    b = mm.rms_norm(x.cuda(), w[1:].clone().cuda(), fp8="e4m3")
+    y, _, rstd = ref.rms_norm(x, w[1:])
+    for r in (a, b):
+        close(r.y, y, (U[torch.bfloat16] + 100 * F24) * y.abs())
+        close(r.rstd, rstd, 80 * F24 * rstd)
+    dy = gen(3, 37, 1200).bfloat16().cuda()
+    want = ref.rms_norm_backward(dy.cpu(), x, w[1:], rstd)
+    for weight in (w.cuda()[1:], w[1:].clone().cuda()):
+        dx, dw = mm.rms_norm_backward(dy, x.cuda(), weight, rstd.float().cuda())
+        assert float((dx.cpu().double() - want[0]).norm() / want[0].norm()) < U[torch.bfloat16]
+        assert float((dw.cpu().double() - want[1]).norm() / want[1].norm()) < 64 * F24
+
+
+@gpu
+def test_offsets_past_32_bits(mm):
+    """Matrices of more than 2^31 elements: their last rows and columns equal those of the same rows and columns alone."""
+    rows, cols = 66_003, 33_000
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    raw = lambda t: t.contiguous().view(torch.uint8)  # noqa: E731
+    q, qt = mm.fp8_quantize(x, rows=True, cols=True)
+    tail, _ = mm.fp8_quantize(x[-7:].contiguous())
+    assert torch.equal(raw(q.data[-7:]), raw(tail.data))
+    assert torch.equal(q.scales()[-7:], tail.scales())
+    _, side = mm.fp8_quantize(x[:, -9:].contiguous(), rows=False, cols=True)
+    assert torch.equal(raw(qt.data[-9:]), raw(side.data)) and torch.equal(qt.scales()[-9:], side.scales())
+    w, _ = mm.fp8_quantize(x[:300].contiguous())
+    c = mm.fp8_matmul(q, w)                       # both operands' rows past 2^31 bytes
+    assert torch.equal(c[-7:], mm.fp8_matmul(q, w)[-7:])
+    few = mm.fp8_matmul(tail, w, torch.float32)
+    assert float((c[-7:].float() - few).norm() / few.norm()) < U[torch.bfloat16]
+    del q, qt, c
+    r = mm.rms_norm(x, None, fp8="e4m3")
+    s = mm.rms_norm(x[-7:].contiguous(), None, fp8="e4m3")
+    assert torch.equal(r.y[-7:], s.y) and torch.equal(r.rstd[-7:], s.rstd) and torch.equal(raw(r.q.data[-7:]), raw(s.q.data))
+    dx, _ = mm.rms_norm_backward(r.y, x, None, r.rstd)
+    assert torch.equal(dx[-7:], mm.rms_norm_backward(s.y, x[-7:].contiguous(), None, s.rstd)[0])
+    del r, s, dx
+    last = x[-1, -300:].clone()
+    norm = mm.clip_grads([x], 1000.0)
+    want = sum(float(last_rows.double().square().sum()) for last_rows in x.split(2048)) ** 0.5
+    assert abs(want - 1000.0) < 1000.0 * 1e-3     # in place; bf16 rounding of 2e9 values averages out
+    assert torch.equal(x[-1, -300:], (last.float() * float(torch.tensor(1000.0) / (norm.cpu() + 1e-6))).bfloat16())
+    small_k = mm.fp8_quantize(torch.ones(66_003, 128, device="cuda", dtype=torch.bfloat16))[0]
+    wide = mm.fp8_quantize(torch.ones(33_000, 128, device="cuda", dtype=torch.bfloat16))[0]
+    big = mm.fp8_matmul(small_k, wide)            # an output past 2^31 elements
+    assert float(big[-1, -1]) == 128.0 and float(big[-5:].float().sum()) == 5 * 33_000 * 128.0
