@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
   __syncwarp();
   cluster_sync();
   tc_fence_after();
-  pdl_launch_dependents();
   pdl_wait();
   const int crank = static_cast<int>(cluster_ctarank());
   const int rank = crank & 1, part = SPLIT ? crank >> 1 : 0;  // in the pair; the pair's part of K
@@ -557,6 +556,7 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
   }
 
   __syncwarp();
+  pdl_launch_dependents();
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while its peer may still signal it
   tc_fence_after();
@@ -624,9 +624,12 @@ struct Fp8Launch {
   }
 };
 
+cudaError_t fp8_status_address(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fp8_status); }
+
 // Clusters of 1, 2 and 4 pairs that can be resident at once; with the kernels' shared-memory limits, once per device.
 struct Fp8Clusters {
   int of[3];
+  int* status;  // g_fp8_status on that device
 };
 static cudaError_t fp8_clusters(int sms, Fp8Clusters* out) {
   static std::mutex mu;
@@ -654,6 +657,8 @@ static cudaError_t fp8_clusters(int sms, Fp8Clusters* out) {
       }
       cached[dev].of[i] = std::min(n, most);
     }
+    e = fp8_status_address(&cached[dev].status);
+    if (e != cudaSuccess) return e;
     done[dev] = true;
   }
   *out = cached[dev];
@@ -693,8 +698,6 @@ static cudaError_t launch_empty(const Fp8GemmDesc& d, int sms, cudaStream_t st) 
   return launch_pdl(fp8_empty_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>(want, 8LL * sms))), dim3(256), 0, st,
                     d.m, d.n, static_cast<const T*>(d.add), d.ldadd, static_cast<T*>(d.out), d.ldc);
 }
-
-cudaError_t fp8_status_address(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fp8_status); }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, int sms, cudaStream_t st, const char** why) {
   using C = F8Cfg;
@@ -741,8 +744,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, int sms, cudaStream_t st, cons
   a.ldadd = d.ldadd;
   a.ldc = d.ldc;
   a.out_dt = d.out_dt;
-  e = fp8_status_address(&a.status);
-  if (e != cudaSuccess) return e;
+  a.status = fit.status;
   Fp8Launch l(p.splits, p.splits > 1 ? a.items : std::min(a.items, fit.of[0]), st, true);
   return p.splits > 1 ? cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<true>, a)
                       : cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<false>, a);

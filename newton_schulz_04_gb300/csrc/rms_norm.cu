@@ -14,9 +14,12 @@
 // deep) that no other thread reads, so the ring needs no barrier, and the only
 // synchronisation of a row is the one of its sum.  One short-lived CTA per row
 // moved 8192 x 4096 bf16 rows in 60 us (forward) and, with its rows in a loop but
-// nothing fetched ahead, 119 us (gradient); the ring takes 50 (6.1 TB/s) and 49.5 (5.4 TB/s,
-// with the second kernel).  The depths below were measured at 33.5M elements: more CTAs per SM
-// than two or three, or rings that no longer let them fit, cost up to a third.
+// nothing fetched ahead, 119 us (gradient); the ring takes 49 (6.2 TB/s) and 47.5 (5.7 TB/s,
+// with the second kernel).  The depths below were measured at 33.5M elements: at 4096 columns, rings of 3
+// to 6 rows on 2 CTAs per SM take 49 to 53 us, on 3 or 4 CTAs 56 to 69.
+//
+// The next kernel on the stream is let in only at a CTA's last row: started earlier, the CTAs of
+// another ring kernel crowd onto the SMs that have room and leave others short of their share.
 //
 // Rows that allow no 16-byte accesses, or that are too wide for a ring, take kernels
 // that load straight to registers, the widest (WIDE) a second time from L1 / L2.
@@ -259,7 +262,6 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
     fx += step * a.ldx;
     if (fr) fr += step * a.ldr;
   };
-  pdl_launch_dependents();
   pdl_wait();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
@@ -276,6 +278,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
   // all threads of a CTA take the same number of turns (the barrier in ring_sum)
   for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
     const bool live = R == 1 || row < a.rows;
+    if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row, see above
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
     float s[C][E];
@@ -432,11 +435,11 @@ static cudaError_t dispatch_norm(const RmsNormArgs& a, int sms, cudaStream_t st)
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const int pieces = (a.cols + E - 1) / E;
   if (a.vec) {
-    if (pieces <= 32) return launch_norm_ring<T, 32, 1, 4, 8>(a, sms, st);
-    if (pieces <= 64) return launch_norm_ring<T, 64, 1, 5, 6>(a, sms, st);
+    if (pieces <= 32) return launch_norm_ring<T, 32, 1, 8, 6>(a, sms, st);
+    if (pieces <= 64) return launch_norm_ring<T, 64, 1, 4, 8>(a, sms, st);
     if (pieces <= 128) return launch_norm_ring<T, 64, 2, 4, 4>(a, sms, st);
     if (pieces <= 256) return launch_norm_ring<T, 256, 1, 4, 3>(a, sms, st);
-    if (pieces <= 512) return launch_norm_ring<T, 512, 1, 5, 2>(a, sms, st);
+    if (pieces <= 512) return launch_norm_ring<T, 256, 2, 5, 2>(a, sms, st);
     if (pieces <= 1024) return launch_norm_ring<T, 512, 2, 4, 1>(a, sms, st);
     if (pieces <= 2048) return launch_norm_ring<T, 1024, 2, 3, 1>(a, sms, st);
   } else {
@@ -603,7 +606,6 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
     fh += step * a.ldh;
     fr += step * a.lddr;
   };
-  pdl_launch_dependents();
   pdl_wait();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
@@ -622,6 +624,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
   T* px = static_cast<T*>(a.dx) + (a.dx ? row0 * a.lddx : 0);
   for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
     const bool live = R == 1 || row < a.rows;
+    if (row - rr + step >= a.rows) pdl_launch_dependents();
     const float rstd = next_rstd;
     next_rstd = row + step < a.rows ? __ldg(a.rstd + row + step) : 0.f;
     fetch(slot == 0 ? S - 1 : slot - 1);
@@ -693,22 +696,24 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
   }
 }
 
-// dweight[j] = sum over the CTAs' rows: 32 columns by 8 row groups per CTA.
-__global__ void __launch_bounds__(256) rms_norm_dweight_kernel(const float* partial, int ctas, int cols, float* dweight) {
-  __shared__ float sh[8][33];
-  pdl_launch_dependents();
+// dweight[j] = sum over the CTAs' rows: 32 columns by 32 row groups per CTA, then a column to a
+// warp (8 row groups, each a chain of 38 loads, took 2 us longer).
+__global__ void __launch_bounds__(1024) rms_norm_dweight_kernel(const float* partial, int ctas, int cols, float* dweight) {
+  __shared__ float sh[32][33];
   pdl_wait();
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (col < cols)
-    for (int r = g; r < ctas; r += 8) s += partial[static_cast<long long>(r) * cols + col];
+  if (col < cols) {
+#pragma unroll 4
+    for (int r = g; r < ctas; r += 32) s += partial[static_cast<long long>(r) * cols + col];
+  }
   sh[g][lane] = s;
   __syncthreads();
-  if (g == 0 && col < cols) {
+  pdl_launch_dependents();  // not before: a persistent grid that starts beside these CTAs finds no room for all of its own
+  s = sh[lane][g];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += sh[k][lane];
-    dweight[col] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + g < cols) dweight[blockIdx.x * 32 + g] = s;
 }
 
 // CTAs of the gradient kernel: what an SM holds of the ring kernels (the others take as many).
@@ -776,7 +781,7 @@ cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, int dt, int sms, cuda
                   : dt == MUON_FP16 ? dispatch_grad<__half>(a, ctas, st)
                                     : dispatch_grad<float>(a, ctas, st);
   if (e != cudaSuccess || !a.partial) return e;
-  return launch_pdl(rms_norm_dweight_kernel, dim3((a.cols + 31) / 32), dim3(256), 0, st,
+  return launch_pdl(rms_norm_dweight_kernel, dim3((a.cols + 31) / 32), dim3(1024), 0, st,
                     static_cast<const float*>(a.partial), ctas, a.cols, a.dweight);
 }
 
