@@ -23,7 +23,7 @@
 // the next main loop, and four sets of scales (4 + 7 columns each).
 //
 // Warp roles (480 threads):
-//   warp 0       TMA producer: stages of 256 of K (two swizzled 128-byte boxes per operand)
+//   warp 0       TMA producer: stages of 128 of K (one swizzled 128-byte box per operand)
 //   warp 1       TMEM allocation; the leader's lane 0 issues the MMAs
 //   warps 2..5   scales: every warp stores the words of all rows of the tile to its
 //                own quarter of TMEM's lanes (the MMA reads a copy in each quarter),
@@ -56,15 +56,23 @@ namespace muon {
 // A kernel that gives up on a wait records it here (muon_fp8_status reads and clears it).
 static __device__ int g_fp8_status;
 
+// Three shapes of the kernel, by the tile's rows of A.
+//   BIG    224: single blocks of K in a ring of 7, taken two at a time by the MMAs (against
+//          3 stages of two blocks: 270 instead of 280 us at 8192 x 14336 x 4096)
+//   MID    96 to 192: a pair of blocks' MMAs are shorter than two waits and two commits, so
+//          stages of two blocks (2048^3: 11 us, in single blocks 12.5)
+//   SMALL  32 and 64: smaller boxes, and room for the split of K
+enum F8Kind : int { F8_BIG, F8_MID, F8_SMALL };
+template <F8Kind KIND>
 struct F8Cfg {
-  static constexpr int BN = 128;        // rows of B per CTA (256 per pair)
-  static constexpr int TMAX = 224;      // rows of A per tile
-  static constexpr int KB = 128;        // K per block: one 128-byte swizzled row of 8-bit values
-  static constexpr int KPS = 2;         // blocks per stage
+  static constexpr int BN = 128;                 // rows of B per CTA (256 per pair)
+  static constexpr int TMAX = KIND == F8_BIG ? 224 : KIND == F8_MID ? 192 : 64;  // rows of A per tile
+  static constexpr int KB = 128;                 // K per block: one 128-byte swizzled row of 8-bit values
+  static constexpr int KPS = KIND == F8_BIG ? 1 : 2;  // blocks per stage
+  static constexpr int STAGES = KIND == F8_BIG ? 7 : KIND == F8_MID ? 3 : 4;
   static constexpr int B_BOX = BN * KB;
   static constexpr int A_BOX = TMAX / 2 * KB;
   static constexpr int STAGE = KPS * (B_BOX + A_BOX);
-  static constexpr int STAGES = 3;
   static constexpr int EPI_WARP = 6, EPI_WARPS = 8, LOAD_WARP = EPI_WARP + EPI_WARPS;
   static constexpr int THREADS = 32 * (LOAD_WARP + 1);
   static constexpr int SETS = 4;                     // groups of scales in TMEM
@@ -72,19 +80,17 @@ struct F8Cfg {
   static constexpr int SCALE_SLOT = (BN + 256) * 4;  // read in 32-row pieces, up to 256 rows of A
   static constexpr int BAR_BYTES = 512;
   // Split K: the parts' sums of this pair's share of the tile, [parts][T / parts][128] fp32
-  static constexpr int SPLIT_T = 64;
-  static constexpr int RECV = SPLIT_T * BN * 4;
-  static constexpr int SMEM = STAGES * STAGE + SLOTS * SCALE_SLOT + BAR_BYTES + 1024;
-  static constexpr int SMEM_SPLIT = SMEM + RECV;
+  static constexpr int RECV = KIND == F8_SMALL ? TMAX * BN * 4 : 0;
+  static constexpr int SMEM = STAGES * STAGE + SLOTS * SCALE_SLOT + BAR_BYTES + 1024 + RECV;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t ACC_COLS = TMAX;
-  static constexpr uint32_t SCALE_COL = 2 * TMAX;
-  static constexpr uint32_t SET_COLS = 16;         // rows of B in the first 4 columns, of A from the 8th on
+  static constexpr uint32_t SCALE_COL = 2 * 224;
+  static constexpr uint32_t SET_COLS = 16;  // rows of B in the first 4 columns, of A from the 8th on
   static constexpr uint32_t EPI_ARRIVALS = 2 * EPI_WARPS;
   static constexpr uint32_t SCALE_ARRIVALS = 2 * 4;
-  static_assert(SMEM_SPLIT <= 232448, "shared memory budget");
-  static_assert(SCALE_COL + SETS * SET_COLS <= TMEM_COLS, "TMEM budget");
-  static_assert(A_BOX % 1024 == 0 && B_BOX % 1024 == 0, "swizzle atoms of 1024 bytes");
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(2 * ACC_COLS <= SCALE_COL && SCALE_COL + SETS * SET_COLS <= TMEM_COLS, "TMEM budget");
+  static_assert(A_BOX % 1024 == 0 && B_BOX % 1024 == 0 && STAGE % 1024 == 0, "swizzle atoms of 1024 bytes");
 };
 
 struct F8Args {
@@ -250,15 +256,17 @@ __device__ __forceinline__ void epi_one(const F8Args& a, long long m, long long 
   else static_cast<__half*>(a.out)[o] = from_f32<__half>(v);
 }
 
-template <bool SPLIT>
-__global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ F8Args a) {
-  using C = F8Cfg;
+template <F8Kind KIND, bool SPLIT>
+__global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ F8Args a) {
+  using C = F8Cfg<KIND>;
+  constexpr int STAGES = C::STAGES;
+  static_assert(KIND == F8_SMALL || !SPLIT, "only small tiles are split");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* scales = tiles + C::STAGES * C::STAGE;  // [SLOTS] words of the rows of B, then of A
+  uint8_t* scales = tiles + STAGES * C::STAGE;  // [SLOTS] words of the rows of B, then of A
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::SLOTS * C::SCALE_SLOT);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;   // [2] accumulator complete
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;   // [2] accumulator complete
   uint64_t* tempty = tfull + 2;          // [2] accumulator read
   uint64_t* sfull = tempty + 2;          // [SETS] scales of a group in TMEM
   uint64_t* sempty = sfull + C::SETS;    // [SETS] scales read by the group's MMAs
@@ -269,11 +277,11 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* recv = reinterpret_cast<uint8_t*>(full) + C::BAR_BYTES;
-  static_assert(C::BAR_BYTES >= (2 * C::STAGES + 2 * C::SETS + 2 * C::SLOTS + 6) * 8 + 8, "barrier area");
+  static_assert(C::BAR_BYTES >= (2 * STAGES + 2 * C::SETS + 2 * C::SLOTS + 6) * 8 + 8, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -324,8 +332,8 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         const int nb0 = it.i * 256 + rank * C::BN, ma0 = it.j * a.tile_m + rank * half;
         const int kb1 = min(a.kblocks, it.g1 * 4);
         for (int kb = it.g0 * 4; kb < kb1; kb += C::KPS, ++st) {
-          const int s = st % C::STAGES;
-          if (*abort_flag || !mbar_wait(&empty[s], ((st / C::STAGES) & 1) ^ 1)) {
+          const int s = st % STAGES;
+          if (*abort_flag || !mbar_wait(&empty[s], ((st / STAGES) & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -343,8 +351,8 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         atomicOr(a.status, kStatusTimeout);
         *abort_flag = 1;
         if (rank == 0)  // copies in flight land before the CTAs exit
-          for (int q = st > C::STAGES ? st - C::STAGES : 0; q < st; ++q)
-            mbar_wait(&full[q % C::STAGES], (q / C::STAGES) & 1);
+          for (int q = st > STAGES ? st - STAGES : 0; q < st; ++q)
+            mbar_wait(&full[q % STAGES], (q / STAGES) & 1);
       }
     }
   } else if (warp == 1) {
@@ -357,8 +365,9 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
       int st = 0, grp = 0, tile = 0;
       bool ok = true;
       const uint32_t base = smem_u32(tiles);
+      // Without a look at the abort flag, which costs as much again: a wait that another role gave up on runs out here too.
       auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, !*abort_flag && mbar_wait_cluster(bar, parity));
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity));
       };
       for (int t = cid; t < a.items && ok; t += ncl, ++tile) {
         const F8Item it = decode_item(a, t, part);
@@ -370,8 +379,12 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
         tc_fence_after();
         const uint32_t d = tmem + abuf * C::ACC_COLS;
         const int kb0 = it.g0 * 4, kb1 = min(a.kblocks, it.g1 * 4);
-        for (int kb = kb0; kb < kb1; kb += C::KPS, ++st) {
-          const int s = st % C::STAGES;
+        for (int kb = kb0; kb < kb1; kb += 2) {
+          // Two blocks at a time, in one stage or two: the waits and commits of one
+          // block took longer than its MMAs.
+          const bool two = kb + 1 < kb1;
+          const int stages = C::KPS == 2 || !two ? 1 : 2;
+          const int s0 = st % STAGES, s1 = (st + 1) % STAGES;
           const uint32_t in_group = static_cast<uint32_t>(kb) & 3u;
           if (in_group == 0) {  // a new group of four blocks: its scales
             if (!warp_wait(&sfull[grp % C::SETS], (grp / C::SETS) & 1)) {
@@ -379,39 +392,45 @@ __global__ void __launch_bounds__(F8Cfg::THREADS, 1) fp8_gemm_kernel(const __gri
               break;
             }
           }
-          if (!warp_wait(&full[s], (st / C::STAGES) & 1)) {
+          if (!warp_wait(&full[s0], (st / STAGES) & 1) ||
+              (stages == 2 && !warp_wait(&full[s1], ((st + 1) / STAGES) & 1))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const int nb = min(C::KPS, kb1 - kb);
-          const uint64_t bd = make_sdesc(base + s * C::STAGE, 16, 1024, 2u);
-          const uint64_t ad = make_sdesc(base + s * C::STAGE + C::KPS * C::B_BOX, 16, 1024, 2u);
+          const uint64_t bd0 = make_sdesc(base + s0 * C::STAGE, 16, 1024, 2u);
+          const uint64_t bd1 = C::KPS == 2 ? bd0 + C::B_BOX / 16 : make_sdesc(base + s1 * C::STAGE, 16, 1024, 2u);
+          const uint64_t ad0 = bd0 + C::KPS * C::B_BOX / 16;
+          const uint64_t ad1 = C::KPS == 2 ? ad0 + C::A_BOX / 16 : bd1 + C::B_BOX / 16;
           const uint32_t sc = tmem + C::SCALE_COL + (grp % C::SETS) * C::SET_COLS;
           const uint32_t idesc = a.idesc | (in_group << 29) | (in_group << 4);
-          const bool whole = nb == C::KPS && (kb + C::KPS < a.kblocks || a.tail_steps == 4);
-          const bool group_end = in_group == 4 - C::KPS || kb + C::KPS >= kb1;
+          constexpr uint32_t NEXT_SF = (1u << 29) | (1u << 4);
+          const bool whole = two && (kb + 2 < a.kblocks || a.tail_steps == 4);
+          const bool group_end = in_group == 2 || kb + 2 >= kb1;
           if (elect_one()) {
             if (whole) {
 #pragma unroll
-              for (int q = 0; q < C::KPS; ++q)
+              for (int kk = 0; kk < 4; ++kk)
+                mma_pair_scaled(d, bd0 + kk * 2, ad0 + kk * 2, idesc, sc, sc + 8, kk != 0 || kb != kb0 ? 1u : 0u);
+              if (C::KPS == 1) tc_commit_pair(&empty[s0], pair_mask);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_pair_scaled(d, bd + (q * C::B_BOX + kk * 32) / 16, ad + (q * C::A_BOX + kk * 32) / 16,
-                                  idesc + q * ((1u << 29) | (1u << 4)), sc, sc + 8, (q | kk) != 0 || kb != kb0 ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk) mma_pair_scaled(d, bd1 + kk * 2, ad1 + kk * 2, idesc + NEXT_SF, sc, sc + 8, 1u);
+              tc_commit_pair(&empty[C::KPS == 1 ? s1 : s0], pair_mask);
             } else {
-              for (int q = 0; q < nb; ++q) {
+              for (int q = 0; q < (two ? 2 : 1); ++q) {
                 const int steps = kb + q == a.kblocks - 1 ? a.tail_steps : 4;
                 for (int kk = 0; kk < steps; ++kk)
-                  mma_pair_scaled(d, bd + (q * C::B_BOX + kk * 32) / 16, ad + (q * C::A_BOX + kk * 32) / 16,
-                                  idesc + q * ((1u << 29) | (1u << 4)), sc, sc + 8, (q | kk) != 0 || kb != kb0 ? 1u : 0u);
+                  mma_pair_scaled(d, (q ? bd1 : bd0) + kk * 2, (q ? ad1 : ad0) + kk * 2, idesc + q * NEXT_SF, sc, sc + 8,
+                                  (q | kk) != 0 || kb != kb0 ? 1u : 0u);
+                if (C::KPS == 1) tc_commit_pair(&empty[q ? s1 : s0], pair_mask);
               }
+              if (C::KPS == 2) tc_commit_pair(&empty[s0], pair_mask);
             }
-            tc_commit_pair(&empty[s], pair_mask);
             if (group_end) tc_commit_pair(&sempty[grp % C::SETS], pair_mask);
-            if (kb + C::KPS >= kb1) tc_commit_pair(&tfull[abuf], pair_mask);
+            if (kb + 2 >= kb1) tc_commit_pair(&tfull[abuf], pair_mask);
           }
           __syncwarp();
+          st += stages;
           if (group_end) ++grp;
         }
       }
@@ -609,10 +628,10 @@ static bool byte_map(CUtensorMap* m, const void* base, long long k, long long ro
 struct Fp8Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  Fp8Launch(int parts, int clusters, cudaStream_t st, bool pdl) {
+  Fp8Launch(F8Kind kind, int parts, int clusters, cudaStream_t st, bool pdl) {
     cfg.gridDim = dim3(2 * parts * clusters);
-    cfg.blockDim = dim3(F8Cfg::THREADS);
-    cfg.dynamicSmemBytes = parts > 1 ? F8Cfg::SMEM_SPLIT : F8Cfg::SMEM;
+    cfg.blockDim = dim3(F8Cfg<F8_BIG>::THREADS);
+    cfg.dynamicSmemBytes = kind == F8_BIG ? F8Cfg<F8_BIG>::SMEM : kind == F8_MID ? F8Cfg<F8_MID>::SMEM : F8Cfg<F8_SMALL>::SMEM;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2 * parts;
@@ -641,16 +660,18 @@ static cudaError_t fp8_clusters(int sms, Fp8Clusters* out) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, F8Cfg::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(fp8_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, F8Cfg::SMEM_SPLIT);
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    e = cudaFuncSetAttribute(fp8_gemm_kernel<F8_BIG, false>, attr, F8Cfg<F8_BIG>::SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_gemm_kernel<F8_MID, false>, attr, F8Cfg<F8_MID>::SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_gemm_kernel<F8_SMALL, false>, attr, F8Cfg<F8_SMALL>::SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_gemm_kernel<F8_SMALL, true>, attr, F8Cfg<F8_SMALL>::SMEM);
     if (e != cudaSuccess) return e;
     for (int i = 0; i < 3; ++i) {
       const int parts = 1 << i, most = sms / (2 * parts);
-      Fp8Launch l(parts, std::max(most, 1), nullptr, false);
+      Fp8Launch l(i ? F8_SMALL : F8_BIG, parts, std::max(most, 1), nullptr, false);
       int n = 0;
-      e = i ? cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<true>, &l.cfg)
-            : cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<false>, &l.cfg);
+      e = i ? cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<F8_SMALL, true>, &l.cfg)
+            : cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<F8_BIG, false>, &l.cfg);
       if (e != cudaSuccess || n <= 0) {
         cudaGetLastError();
         n = i ? 0 : most;  // no clusters of that size: K is not split so far
@@ -674,12 +695,12 @@ static Fp8Plan fp8_plan(long long m, long long n, long long k, const Fp8Clusters
   const long long groups = (k + 511) / 512, nI = (n + 255) / 256;
   Fp8Plan best = {32, 1, static_cast<int>(groups)};
   double best_time = 1e300;
-  for (int t = 32; t <= F8Cfg::TMAX; t += 32) {
+  for (int t = 32; t <= F8Cfg<F8_BIG>::TMAX; t += 32) {
     const long long tiles = nI * ((m + t - 1) / t);
     const double block = std::max(2.0 * t, 256.0 + t);
     for (int i = 0; i < 3; ++i) {
       const long long parts = 1 << i, gps = (groups + parts - 1) / parts;
-      if (i && (t > F8Cfg::SPLIT_T || tiles > fit.of[i] || (groups + gps - 1) / gps != parts)) break;
+      if (i && (t > F8Cfg<F8_SMALL>::TMAX || tiles > fit.of[i] || (groups + gps - 1) / gps != parts)) break;
       const double waves = static_cast<double>((tiles + fit.of[i] - 1) / std::max(1, fit.of[i]));
       const double time = waves * (gps * 4 * block + (i ? 3000.0 : 1500.0));
       if (time < best_time) {
@@ -700,7 +721,7 @@ static cudaError_t launch_empty(const Fp8GemmDesc& d, int sms, cudaStream_t st) 
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, int sms, cudaStream_t st, const char** why) {
-  using C = F8Cfg;
+  using C = F8Cfg<F8_BIG>;
   *why = nullptr;
   if (d.k == 0)
     return d.out_dt == MUON_FP32   ? launch_empty<float>(d, sms, st)
@@ -745,9 +766,12 @@ cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, int sms, cudaStream_t st, cons
   a.ldc = d.ldc;
   a.out_dt = d.out_dt;
   a.status = fit.status;
-  Fp8Launch l(p.splits, p.splits > 1 ? a.items : std::min(a.items, fit.of[0]), st, true);
-  return p.splits > 1 ? cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<true>, a)
-                      : cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<false>, a);
+  const F8Kind kind = p.tile_m <= F8Cfg<F8_SMALL>::TMAX ? F8_SMALL : p.tile_m <= F8Cfg<F8_MID>::TMAX ? F8_MID : F8_BIG;
+  Fp8Launch l(kind, p.splits, p.splits > 1 ? a.items : std::min(a.items, fit.of[0]), st, true);
+  return p.splits > 1       ? cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<F8_SMALL, true>, a)
+         : kind == F8_SMALL ? cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<F8_SMALL, false>, a)
+         : kind == F8_MID   ? cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<F8_MID, false>, a)
+                            : cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<F8_BIG, false>, a);
 }
 
 }  // namespace muon
