@@ -136,12 +136,13 @@ __device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t adesc, uint
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// Arrive on a barrier that may be the peer CTA's, where only TMEM is handed over: tcgen05.wait and the
-// tcgen05 fences order that, and a release at cluster scope would wait for every
+// Arrive on a barrier that may be another CTA's, after a fence at cluster scope or where only TMEM is handed
+// over: tcgen05.wait and the tcgen05 fences order that, and a release at cluster scope would wait for every
 // access of this thread in flight, 2000 cycles behind a queue of TMA loads.
 __device__ __forceinline__ void mbar_arrive_tmem(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -533,28 +534,29 @@ __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const
         ok = ready();
         if (!ok) break;
         if (c < a.tile_m) tmem_ld_32x32b_x32(acc + c, v);
-#pragma unroll 1
-        for (int p = 0; p < a.splits; ++p) {
-          const uint32_t to = mapa_cluster(sums + part * share * C::BN, static_cast<uint32_t>(2 * p + rank));
-          if (c < a.tile_m) {
+        if (c < a.tile_m) {
 #pragma unroll
-            for (int u = 0; u < 32; ++u)
-              if ((c + u) >> shift == p)
-                st_shared_cluster(to + static_cast<uint32_t>((c + u - p * share) * C::BN * 4), __float_as_int(v[u]));
+          for (int u = 0; u < 32; ++u) {
+            const float* to = sums + (part * share + ((c + u) & (share - 1))) * C::BN;
+            st_shared_cluster(mapa_cluster(to, static_cast<uint32_t>(2 * ((c + u) >> shift) + rank)), __float_as_int(v[u]));
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_cluster(joined, static_cast<uint32_t>(2 * p + rank)));
+        }
+        __syncwarp();
+        if (lane == 0) {  // one release for all parts: each waits for the stores in flight
+          fence_cluster();
+          for (int p = 0; p < a.splits; ++p) mbar_arrive_tmem(mapa_cluster(joined, static_cast<uint32_t>(2 * p + rank)));
         }
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait_cluster(joined, 0));
         if (!ok) break;
-        // one rolled loop: unrolled over the rows its code took longer to fetch than to run (19000 cycles)
-#pragma unroll 1
+        // not unrolled over all rows: its code then took longer to fetch than to run (19000 cycles)
+#pragma unroll 2
         for (int r = half_tile; r < share; r += 2) {
-          if (part * share + r >= rows || n >= a.n) break;
-          float sum = sums[r * C::BN];
-#pragma unroll 1
-          for (int p = 1; p < a.splits; ++p) sum += sums[(p * share + r) * C::BN];
-          epi_one(a, m0 + part * share + r, n, sum);
+          const long long m = part * share + r;
+          if (m < rows && n < a.n) {
+            float sum = sums[r * C::BN] + sums[(share + r) * C::BN];
+            if (a.splits == 4) sum = (sum + sums[(2 * share + r) * C::BN]) + sums[(3 * share + r) * C::BN];
+            epi_one(a, m0 + m, n, sum);
+          }
         }
         __syncwarp();
       } else {
@@ -686,23 +688,24 @@ static cudaError_t fp8_clusters(int sms, Fp8Clusters* out) {
   return cudaSuccess;
 }
 
-// The tile of tokens and the parts of K with the least estimated time, in SM
-// cycles: a pair MMA of 128 of K by T takes 2 T cycles, its loads (128 + T / 2 rows of 128
-// bytes per CTA) at 64 bytes a cycle 256 + T; an item costs some 1500 cycles of pipeline
-// fill and drain, and joining the parts as much again.  K is split only where every
-// tile has a cluster of its own.
+// The tile of tokens and the parts of K with the least estimated time, in SM cycles.  As measured over T of 32 to 224
+// and 1, 2 and 4 parts: a block of K takes the longest of its MMAs (2 T), its loads ((128 + T / 2)
+// rows of 128 bytes at 64 bytes a cycle: 256 + T) and the handling of a stage (313); a tile some 2000 cycles to
+// fill and drain the pipeline; joining parts 85 T.  K is split only where every tile has a cluster of
+// its own.  One token of 4096 x 4096 takes 6.7 us on two parts (32 clusters; of four parts 15 fit) and 7.9 unsplit, of
+// 1024 x 4096 5.4 on four and 7.9; 512 x 4096 x 4096 10.3 with T = 128, 14.9 with 64, 12.7 with 224.
 static Fp8Plan fp8_plan(long long m, long long n, long long k, const Fp8Clusters& fit) {
   const long long groups = (k + 511) / 512, nI = (n + 255) / 256;
   Fp8Plan best = {32, 1, static_cast<int>(groups)};
   double best_time = 1e300;
   for (int t = 32; t <= F8Cfg<F8_BIG>::TMAX; t += 32) {
     const long long tiles = nI * ((m + t - 1) / t);
-    const double block = std::max(2.0 * t, 256.0 + t);
+    const double block = std::max({2.0 * t, 256.0 + t, 313.0});
     for (int i = 0; i < 3; ++i) {
       const long long parts = 1 << i, gps = (groups + parts - 1) / parts;
       if (i && (t > F8Cfg<F8_SMALL>::TMAX || tiles > fit.of[i] || (groups + gps - 1) / gps != parts)) break;
       const double waves = static_cast<double>((tiles + fit.of[i] - 1) / std::max(1, fit.of[i]));
-      const double time = waves * (gps * 4 * block + (i ? 3000.0 : 1500.0));
+      const double time = waves * (gps * 4 * block + 2000.0) + (i ? 85.0 * t : 0.0);
       if (time < best_time) {
         best_time = time;
         best = {t, static_cast<int>(parts), static_cast<int>(gps)};
