@@ -461,8 +461,6 @@ __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const
         for (int j = 0; j < 4; ++j) wb[j] = w[j * 32];
 #pragma unroll
         for (int j = 0; j < 8; ++j) wa[j] = w[C::BN + j * 32];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfree[slot]);
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sempty[set], ((grp / C::SETS) & 1) ^ 1));
         if (!ok) break;
         tc_fence_after();
@@ -472,7 +470,12 @@ __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_tmem(mapa_cluster(&sfull[set], leader));
+        if (lane == 0) {
+          // The slot is free once its words are in TMEM.  An arrive right after the loads overtook them when the
+          // epilogue kept the load unit busy, and the next copy into the slot was read by some of the warps.
+          mbar_arrive(&sfree[slot]);
+          mbar_arrive_tmem(mapa_cluster(&sfull[set], leader));
+        }
       }
     }
     if (!ok) {

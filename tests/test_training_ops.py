@@ -571,6 +571,28 @@ def test_matmul_many_tiles(mm, m, n, k):
 
 
 @gpu
+@pytest.mark.parametrize("m,n,k", [(4096, 4096, 4096), (2048, 2500, 2048), (300, 4096, 6000), (64, 8000, 3000)])
+def test_matmul_add_keeps_its_bits(mm, m, n, k):
+    """An epilogue that reads as well as writes holds the MMAs up and the scales wait for them: still the plain
+    product plus the addend, one rounding in fp32, call after call."""
+    a, av = _operand(mm, 1, m, k, "e4m3")
+    b, bv = _operand(mm, 3, n, k, "e4m3")
+    plain = mm.fp8_matmul(a, b, torch.float32)
+    rows = torch.arange(0, m, max(1, m // 32))
+    want = ref.matmul(av[rows], bv)
+    close(plain[rows.cuda()], want, _mm_tol(av[rows], bv, want, torch.float32, k))
+    add = gen(7, m, n).cuda()
+    want = plain + add
+    outs = [mm.fp8_matmul(a, b, torch.float32, add=add) for _ in range(12)]
+    assert [torch.equal(c, want) for c in outs] == [True] * 12
+    low = add.bfloat16()
+    want = (plain + low.float()).bfloat16()
+    outs = [mm.fp8_matmul(a, b, torch.bfloat16, add=low) for _ in range(12)]
+    assert [torch.equal(c, want) for c in outs] == [True] * 12
+    assert mm.fp8_status() == 0
+
+
+@gpu
 def test_matmul_strided_output_and_extreme_scales(mm):
     a, av = _operand(mm, 1, 50, 300, "e4m3")
     b, bv = _operand(mm, 3, 70, 300, "e4m3")
