@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmuon_ns.so")
 SOURCES = ["engine.cu", "tc_gemm.cu", "simt_gemm.cu", "elementwise.cu", "adamw.cu", "planner.cpp",
-           "train_abi.cu", "clip.cu", "rms_norm.cu", "fp8_quant.cu", "fp8_gemm.cu"]
+           "train_abi.cu", "clip.cu", "rms_norm.cu", "fp8_quant.cu", "fp8_gemm.cu",
+           "fp8_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

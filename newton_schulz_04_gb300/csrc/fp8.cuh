@@ -15,6 +15,8 @@
 
 #include <cstdint>
 
+#include "muon_ns.h"
+
 namespace muon {
 
 constexpr int kFp8Block = 128;
@@ -74,6 +76,21 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) {
   return __float2half_rn(v);
+}
+
+// One element of a product: out = round(v + add).
+template <typename Args>
+__device__ __forceinline__ void fp8_product_out(const Args& a, long long m, long long n, float v) {
+  if (a.add) {
+    const long long i = m * a.ldadd + n;
+    v += a.out_dt == MUON_FP32   ? static_cast<const float*>(a.add)[i]
+         : a.out_dt == MUON_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(a.add)[i])
+                                 : to_f32(static_cast<const __half*>(a.add)[i]);
+  }
+  const long long o = m * a.ldc + n;
+  if (a.out_dt == MUON_FP32) static_cast<float*>(a.out)[o] = v;
+  else if (a.out_dt == MUON_BF16) static_cast<__nv_bfloat16*>(a.out)[o] = from_f32<__nv_bfloat16>(v);
+  else static_cast<__half*>(a.out)[o] = from_f32<__half>(v);
 }
 
 // ---- 8 consecutive elements; `full`: all in range and 16-byte aligned

@@ -34,6 +34,7 @@
 //                was issued a group (1792 cycles) ahead held the MMAs up at every
 //                other stage (8192 x 14336 x 4096 in 326 us instead of 308)
 //
+// At most 8 rows of A with a B that small tiles cover at once have a kernel of their own (fp8_few.cu).
 // When there are too few tiles to fill the GPU, 2 or 4 pairs of one cluster share a tile of
 // at most 64 rows of A, each with its part of K.  Every pair sends the others their
 // share of the tile's rows of A through distributed shared memory and adds up its own, in
@@ -243,20 +244,6 @@ __device__ __forceinline__ bool epi_tile(const F8Args& a, uint32_t acc, long lon
                                          const F& ready) {
   return a.add ? epi_tile<T, true>(a, acc, m0, rows, half, n, ready) : epi_tile<T, false>(a, acc, m0, rows, half, n, ready);
 }
-// One element.
-__device__ __forceinline__ void epi_one(const F8Args& a, long long m, long long n, float v) {
-  if (a.add) {
-    const long long i = m * a.ldadd + n;
-    v += a.out_dt == MUON_FP32   ? static_cast<const float*>(a.add)[i]
-         : a.out_dt == MUON_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(a.add)[i])
-                                 : to_f32(static_cast<const __half*>(a.add)[i]);
-  }
-  const long long o = m * a.ldc + n;
-  if (a.out_dt == MUON_FP32) static_cast<float*>(a.out)[o] = v;
-  else if (a.out_dt == MUON_BF16) static_cast<__nv_bfloat16*>(a.out)[o] = from_f32<__nv_bfloat16>(v);
-  else static_cast<__half*>(a.out)[o] = from_f32<__half>(v);
-}
-
 template <F8Kind KIND, bool SPLIT>
 __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const __grid_constant__ F8Args a) {
   using C = F8Cfg<KIND>;
@@ -558,7 +545,7 @@ __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const
           if (m < rows && n < a.n) {
             float sum = sums[r * C::BN] + sums[(share + r) * C::BN];
             if (a.splits == 4) sum = (sum + sums[(2 * share + r) * C::BN]) + sums[(3 * share + r) * C::BN];
-            epi_one(a, m0 + m, n, sum);
+            fp8_product_out(a, m0 + m, n, sum);
           }
         }
         __syncwarp();
@@ -695,8 +682,8 @@ static cudaError_t fp8_clusters(int sms, Fp8Clusters* out) {
 // and 1, 2 and 4 parts: a block of K takes the longest of its MMAs (2 T), its loads ((128 + T / 2)
 // rows of 128 bytes at 64 bytes a cycle: 256 + T) and the handling of a stage (313); a tile some 2000 cycles to
 // fill and drain the pipeline; joining parts 85 T.  K is split only where every tile has a cluster of
-// its own.  One token of 4096 x 4096 takes 6.7 us on two parts (32 clusters; of four parts 15 fit) and 7.9 unsplit, of
-// 1024 x 4096 5.4 on four and 7.9; 512 x 4096 x 4096 10.3 with T = 128, 14.9 with 64, 12.7 with 224.
+// its own.  A tile of 32 rows of A by 4096 x 4096 takes 6.7 us on two parts (32 clusters; of four parts 15
+// fit) and 7.9 unsplit, by 1024 x 4096 5.4 on four and 7.9; 512 x 4096 x 4096 10.3 with T = 128, 14.9 with 64, 12.7 with 224.
 static Fp8Plan fp8_plan(long long m, long long n, long long k, const Fp8Clusters& fit) {
   const long long groups = (k + 511) / 512, nI = (n + 255) / 256;
   Fp8Plan best = {32, 1, static_cast<int>(groups)};
@@ -733,6 +720,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, int sms, cudaStream_t st, cons
     return d.out_dt == MUON_FP32   ? launch_empty<float>(d, sms, st)
            : d.out_dt == MUON_BF16 ? launch_empty<__nv_bfloat16>(d, sms, st)
                                    : launch_empty<__half>(d, sms, st);
+  if (fp8_few_rows(d, sms)) return launch_fp8_few(d, sms, st);
   Fp8Clusters fit;
   cudaError_t e = fp8_clusters(sms, &fit);
   if (e != cudaSuccess) return e;

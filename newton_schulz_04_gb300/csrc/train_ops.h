@@ -92,6 +92,9 @@ struct Fp8Plan {
   int groups_per_split;  // 512-deep groups of k
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmDesc& d, int sms, cudaStream_t st, const char** why);
+// The kernel for a few rows of a (fp8_few.cu), and whether it is the one to take.
+bool fp8_few_rows(const Fp8GemmDesc& d, int sms);
+cudaError_t launch_fp8_few(const Fp8GemmDesc& d, int sms, cudaStream_t st);
 // Address of the 8-bit product's status word (device memory of the library).
 cudaError_t fp8_status_address(int** p);
 

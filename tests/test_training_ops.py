@@ -571,6 +571,67 @@ def test_matmul_many_tiles(mm, m, n, k):
 
 
 @gpu
+@pytest.mark.parametrize("out", DTYPES)
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("m,n,k", [(1, 16, 16), (8, 17, 48), (4, 15, 127), (8, 33, 2500), (9, 33, 2500), (1, 2500, 1000),
+                                   (6, 50, 4144), (3, 4870, 600), (2, 1, 9000), (8, 700, 513)])
+def test_matmul_few_rows(mm, out, fa, fb, m, n, k):
+    """At most 8 rows of a: the kernel for single tokens, on both sides of its limits."""
+    a, av = _operand(mm, 11, m, k, fa)
+    b, bv = _operand(mm, 13, n, k, fb, std=0.1)
+    want = ref.matmul(av, bv)
+    buf = torch.full((m, n + 5), 3.0, device="cuda", dtype=out)
+    c = mm.fp8_matmul(a, b, out=buf[:, 2:n + 2])
+    close(c, want, _mm_tol(av, bv, want, out, k))
+    assert bool((buf[:, :2] == 3).all()) and bool((buf[:, n + 2:] == 3).all())
+    add = gen(9, m, n).to(out)
+    acc = add.cuda()
+    want = want + add.double()
+    close(mm.fp8_matmul(a, b, add=acc, out=acc), want, _mm_tol(av, bv, want, out, k) + F24 * want.abs())
+    for _ in range(3):
+        assert torch.equal(mm.fp8_matmul(a, b, out), c)
+
+
+@gpu
+@pytest.mark.parametrize("m", [1, 8, 9])
+@pytest.mark.parametrize("ea,eb", [(60, 60), (-60, -60), (120, -115), (-115, 125)])
+def test_matmul_few_rows_extreme_scales(mm, m, ea, eb):
+    """The product of two scales may leave fp32's range where the result does not."""
+    n, k = 40, 700
+    a, _ = _operand(mm, 1, m, k, "e4m3", std=0.01)
+    b, _ = _operand(mm, 3, n, k, "e4m3", std=0.01)
+    a = mm.Fp8Tensor(a.data, a.scale.view(torch.uint8) + ea)  # a few bytes wrap round, so that large meets large too
+    b = mm.Fp8Tensor(b.data, b.scale.view(torch.uint8) + eb)
+    av, bv = (ref.values(q.data.cpu(), q.scale.cpu()) for q in (a, b))
+    want, most = ref.matmul(av, bv), av.abs() @ bv.abs().t()
+    got = mm.fp8_matmul(a, b, torch.float32).cpu()
+    assert bool(got[want.isnan() | (want.abs() >= 2.0 ** 128)].isfinite().logical_not().all())
+    fits = most < 2.0 ** 127  # none of the last case's
+    close(got[fits], want[fits], (_mm_tol(av, bv, want, torch.float32, k) + 2.0 ** -140)[fits])
+
+
+@gpu
+@pytest.mark.parametrize("m", [1, 2, 8, 9])
+@pytest.mark.parametrize("fmt,nan", [("e4m3", 0x7f), ("e4m3", 0xff), ("e5m2", 0x7e)])
+def test_matmul_few_rows_nan(mm, m, fmt, nan):
+    """A NaN among the values or the scales reaches its row and column and nothing else."""
+    n, k = 37, 1300
+    a, _ = _operand(mm, 1, m, k, fmt)
+    b, _ = _operand(mm, 3, n, k, fmt)
+    c = mm.fp8_matmul(a, b, torch.float32)
+    a.data.view(torch.uint8)[m - 1, 1298] = nan
+    d = mm.fp8_matmul(a, b, torch.float32)
+    assert bool(d[m - 1].isnan().all()) and torch.equal(d[:m - 1], c[:m - 1])
+    x = (gen(3, n, k) * torch.exp(gen(4, n, 1))).cuda()
+    x[20, 130] = float("inf")
+    b, _ = mm.fp8_quantize(x, fmt)
+    d = mm.fp8_matmul(a, b, torch.float32)
+    assert bool(d[:, 20].isnan().all()) and bool(d[m - 1].isnan().all())
+    rest = [j for j in range(n) if j != 20]
+    assert torch.equal(d[:m - 1][:, rest], c[:m - 1][:, rest])
+
+
+@gpu
 @pytest.mark.parametrize("m,n,k", [(4096, 4096, 4096), (2048, 2500, 2048), (300, 4096, 6000), (64, 8000, 3000)])
 def test_matmul_add_keeps_its_bits(mm, m, n, k):
     """An epilogue that reads as well as writes holds the MMAs up and the scales wait for them: still the plain
