@@ -11,7 +11,8 @@
 //
 // Taken while all CTAs are resident at once, two of 8 warps on an SM with 111 registers a thread.  Device times in us, this
 // kernel and fp8_gemm.cu's, one token: 300 x 4096 2.8 and 5.0; 1024 x 4096 3.0 and 5.0; 2500 x 2500 3.7 and
-// 6.5; 4096 x 4096 5.4 (3.1 TB/s, 4.2 with B partly in L2) and 7.3; 4096 x 14336 13.6 (4.3 TB/s) and 15.0.  Beyond,
+// 6.5; 4096 x 4096 5.4 (3.1 TB/s, 4.2 with B partly in L2) and 7.3; 4096 x 14336 13.6 (4.3 TB/s) and 15.0; 256 x
+// 65536 23.8 and 25.0; 4864 x 512 1.9 and 3.3; 4864 x 14336 15.0 and 15.9, with 8 rows 15.0 and 16.3.  Beyond,
 // stepping over the tiles: 6144 x 4096 8.3 and 8.1; 8192 x 8192 15.5 and 14.1; 28672 x 4096 22.1 and 20.8.
 // Two blocks of a warp in flight are 64 KB on an SM.  Slower were: the conversion's bits moved by integer
 // instructions, 7.9 at 4096 x 4096; four blocks in flight in a ring of cp.async copies, 6.2; the 8-bit
