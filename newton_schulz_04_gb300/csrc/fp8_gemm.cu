@@ -137,11 +137,12 @@ __device__ __forceinline__ void mma_pair_scaled(uint32_t d, uint64_t adesc, uint
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// Arrive on a barrier that may be another CTA's, after a fence at cluster scope or where only TMEM is handed
-// over: tcgen05.wait and the tcgen05 fences order that, and a release at cluster scope would wait for every
-// access of this thread in flight, 2000 cycles behind a queue of TMA loads.
-__device__ __forceinline__ void mbar_arrive_tmem(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+// Arrive on a barrier that may be another CTA's, without a release: after a fence at cluster scope (which needs an
+// arrive of that scope to count for the other CTA), or where only TMEM is handed over, which tcgen05.wait and the
+// tcgen05 fences order.  A release at cluster scope would wait for every access of this thread in flight, 2000
+// cycles behind a queue of TMA loads.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const
           // The slot is free once its words are in TMEM.  An arrive right after the loads overtook them when the
           // epilogue kept the load unit busy, and the next copy into the slot was read by some of the warps.
           mbar_arrive(&sfree[slot]);
-          mbar_arrive_tmem(mapa_cluster(&sfull[set], leader));
+          mbar_arrive_relaxed(mapa_cluster(&sfull[set], leader));
         }
       }
     }
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const
         __syncwarp();
         if (lane == 0) {  // one release for all parts: each waits for the stores in flight
           fence_cluster();
-          for (int p = 0; p < a.splits; ++p) mbar_arrive_tmem(mapa_cluster(joined, static_cast<uint32_t>(2 * p + rank)));
+          for (int p = 0; p < a.splits; ++p) mbar_arrive_relaxed(mapa_cluster(joined, static_cast<uint32_t>(2 * p + rank)));
         }
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait_cluster(joined, 0));
         if (!ok) break;
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_tmem(mapa_cluster(&tempty[abuf], leader));
+      if (lane == 0) mbar_arrive_relaxed(mapa_cluster(&tempty[abuf], leader));
     }
     if (!ok) {
       if (lane == 0) atomicOr(a.status, kStatusTimeout);

@@ -1,0 +1,91 @@
+"""The operators around the update where the other tests do not reach: many turns of the persistent kernels, in-place
+calls, streams, the failure report, extreme ranges.
+
+Comparisons here fail on a NaN that the oracle does not have (`close` asks that every difference is within the
+tolerance, not that none is beyond it)."""
+import ctypes
+import glob
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import oracle.training as ref
+
+U = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+TINY = {torch.float32: 2.0 ** -149, torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -24}
+F24 = 2.0 ** -24
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "newton_schulz_04_gb300", "csrc")
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mm():
+    from newton_schulz_04_gb300 import build as b
+    b.build()
+    import newton_schulz_04_gb300 as m
+    m.load()
+    return m
+
+
+def gen(seed, *shape, std=1.0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float32) * std
+
+
+def close(got, want, tol):
+    got, want = got.cpu().double(), want.cpu().double()
+    assert got.shape == want.shape
+    fine = (got - want).abs() <= tol
+    assert bool(fine.all()), f"{int((~fine).sum())} of {fine.numel()} off, worst {float(((got - want).abs() - tol).max()):.3g}"
+
+
+def test_close_rejects_nan():
+    one = torch.ones(3)
+    close(one, one, 0.0)
+    for bad in (torch.tensor([1.0, math.nan, 1.0]), torch.tensor([1.0, 1.0, math.inf])):
+        with pytest.raises(AssertionError):
+            close(bad, one, 1.0)
+
+
+# ---------------------------------------------------------------- split products
+
+def test_arrivals_on_other_ctas_barriers_have_cluster_scope():
+    """An arrive that names no scope orders nothing for a waiter in another CTA of the cluster, whatever fence stands
+    before it: the sums of a split product are published so."""
+    seen = 0
+    for path in glob.glob(os.path.join(CSRC, "*.cu*")):
+        for ins in re.findall(r"mbarrier\.arrive[\w.:]*shared::cluster[\w.:]*", open(path).read()):
+            seen += 1
+            assert ".cluster." in ins.replace("shared::cluster", ""), (os.path.basename(path), ins)
+    assert seen >= 2
+
+
+def _operand(mm, seed, rows, cols, fmt="e4m3"):
+    x = gen(seed, rows, cols) * torch.exp(gen(seed + 1, rows, 1))
+    q, _ = mm.fp8_quantize(x.cuda(), fmt)
+    return q, ref.values(q.data.cpu(), q.scale.view(torch.uint8).cpu())
+
+
+def _product_tol(a, b, want, dtype, k):
+    # fp32 over k / 32 steps that may truncate (2^-23), 32 products inside a step, and up to 16 parts
+    return U[dtype] * want.abs() + (k / 32 + 48) * 2.0 ** -23 * (a.abs() @ b.abs().t()) + TINY[dtype]
+
+
+@gpu
+@pytest.mark.parametrize("m,n,k", [(9, 256, 8192), (12, 1024, 4096), (33, 700, 1500), (64, 513, 6000), (17, 4096, 2049),
+                                   (225, 257, 513), (500, 40, 2049)])
+def test_products_have_no_nan_and_the_same_bits(mm, m, n, k):
+    """Split and whole products, written over NaN, call after call: a part that comes too late would change a sum."""
+    a, av = _operand(mm, 1, m, k)
+    b, bv = _operand(mm, 3, n, k)
+    want = ref.matmul(av, bv)
+    first = mm.fp8_matmul(a, b, torch.float32)
+    close(first, want, _product_tol(av, bv, want, torch.float32, k))
+    out = torch.empty_like(first)
+    for _ in range(50):
+        out.fill_(math.nan)
+        mm.fp8_matmul(a, b, out=out)
+        assert torch.equal(out, first)
+    assert mm.fp8_status() == 0
