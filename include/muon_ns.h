@@ -552,9 +552,11 @@ MUON_API muon_status muon_fp8_matmul(const void* a, int64_t lda, const void* a_s
                                      muon_dtype out_dt, void* stream);
 
 /*
- * muon_fp8_status -- synchronise `stream`, then read and clear the 8-bit product's
- * status word: MUON_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last
- * check, MUON_ERR_CUDA on a CUDA error, else MUON_OK.
+ * muon_fp8_status -- synchronise `stream` (of the current device), and read and clear
+ * the 8-bit product's status word: MUON_ERR_TIMEOUT if a kernel gave up on a bounded
+ * wait since the last check, MUON_ERR_CUDA on a CUDA error, else MUON_OK.  There is
+ * one word per device, for the products of all streams and callers; each report is
+ * given once.
  */
 MUON_API muon_status muon_fp8_status(void* stream);
 

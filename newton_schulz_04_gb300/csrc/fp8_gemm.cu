@@ -54,8 +54,10 @@
 
 namespace muon {
 
-// A kernel that gives up on a wait records it here (muon_fp8_status reads and clears it).
+// A kernel that gives up on a wait records it here (muon_fp8_status takes it).
 static __device__ int g_fp8_status;
+static __device__ int g_fp8_taken;
+__global__ void fp8_take_status_kernel() { g_fp8_taken = atomicExch(&g_fp8_status, 0); }
 
 // Three shapes of the kernel, by the tile's rows of A.
 //   BIG    224: single blocks of K in a ring of 7, taken two at a time by the MMAs (against
@@ -637,6 +639,19 @@ struct Fp8Launch {
 };
 
 cudaError_t fp8_status_address(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fp8_status); }
+
+// Read and cleared in one atomic step, after the stream's work: what a kernel on another stream records meanwhile is
+// in this answer or in the next.  One caller at a time, for the word that carries the answer.
+cudaError_t fp8_take_status(cudaStream_t st, int* word) {
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  fp8_take_status_kernel<<<1, 1, 0, st>>>();
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(word, g_fp8_taken, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+  const cudaError_t done = cudaStreamSynchronize(st);
+  return e != cudaSuccess ? e : done;
+}
 
 // Clusters of 1, 2 and 4 pairs that can be resident at once; with the kernels' shared-memory limits, once per device.
 struct Fp8Clusters {

@@ -314,12 +314,8 @@ muon_status muon_fp8_matmul(const void* a, int64_t lda, const void* a_scale, muo
 
 muon_status muon_fp8_status(void* stream) {
   clear_error();
-  int* p = nullptr;
-  cudaError_t e = fp8_status_address(&p);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   int word = 0;
-  if (e == cudaSuccess) e = cudaMemcpy(&word, p, sizeof(word), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && word) e = cudaMemset(p, 0, sizeof(word));
+  const cudaError_t e = fp8_take_status(static_cast<cudaStream_t>(stream), &word);
   if (e != cudaSuccess) return fail(MUON_ERR_CUDA, "status: %s", cudaGetErrorString(e));
   if (word & kStatusTimeout) return fail(MUON_ERR_TIMEOUT, "a kernel gave up on a bounded wait");
   return MUON_OK;

@@ -97,5 +97,7 @@ bool fp8_few_rows(const Fp8GemmDesc& d, int sms);
 cudaError_t launch_fp8_few(const Fp8GemmDesc& d, int sms, cudaStream_t st);
 // Address of the 8-bit product's status word (device memory of the library).
 cudaError_t fp8_status_address(int** p);
+// Synchronises the stream; *word is the status word's value, which is 0 from then on.
+cudaError_t fp8_take_status(cudaStream_t st, int* word);
 
 }  // namespace muon

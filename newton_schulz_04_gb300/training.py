@@ -216,13 +216,24 @@ def _matmul(a, b, out_dtype, add, out, dev, st):
     return out
 
 
-def fp8_status(stream=None) -> int:
-    """Synchronise and read/clear the 8-bit product's status (OK, or ERR_TIMEOUT where a kernel gave up on a wait)."""
-    return _b.load().muon_fp8_status(ctypes.c_void_p(_b._stream_ptr(stream)))
+def _status_device(stream, device):
+    if device is None:
+        return torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
+    device = torch.device(device)
+    return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
-def debug_bounded_wait_fp8(max_cycles: int, stream=None) -> None:
-    _b._check(_b.load().muon_debug_bounded_wait_fp8(int(max_cycles), ctypes.c_void_p(_b._stream_ptr(stream))))
+def fp8_status(stream=None, device=None) -> int:
+    """Synchronise and read/clear the 8-bit product's status (OK, or ERR_TIMEOUT where a kernel gave up on a wait).
+
+    The status is that of `device` (default: the stream's, or the current one): one for all its streams, each report given
+    once."""
+    return _on(stream, _status_device(stream, device), _b.load().muon_fp8_status)
+
+
+def debug_bounded_wait_fp8(max_cycles: int, stream=None, device=None) -> None:
+    """Self-test of fp8_status: a wait on `device` that runs out after `max_cycles`."""
+    _b._check(_on(stream, _status_device(stream, device), _b.load().muon_debug_bounded_wait_fp8, int(max_cycles)))
 
 
 # ---------------------------------------------------------------- RMS norm

@@ -89,3 +89,106 @@ def test_products_have_no_nan_and_the_same_bits(mm, m, n, k):
         mm.fp8_matmul(a, b, out=out)
         assert torch.equal(out, first)
     assert mm.fp8_status() == 0
+
+
+# ---------------------------------------------------------------- streams and devices
+
+class FakeStream:
+    def __init__(self, index, pointer):
+        self.device, self.cuda_stream = torch.device("cuda", index), pointer
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """torch.cuda as on a host with two GPUs, cuda:0 current; returns the list of (device, stream pointer) entered."""
+    now = [0, 100]
+
+    class Enter:
+        def __init__(self, at, value):
+            self.at, self.value = at, value
+
+        def __enter__(self):
+            self.old = list(now)
+            if self.value is not None:
+                now[self.at] = self.value
+                if self.at == 0:
+                    now[1] = 100 + self.value  # that device's own current stream
+
+        def __exit__(self, *exc):
+            now[:] = self.old
+
+    class Stream(Enter):
+        def __init__(self, stream):
+            super().__init__(1, None if stream is None else stream.cuda_stream)
+            self.stream = stream
+
+        def __enter__(self):
+            super().__enter__()
+            if self.stream is not None:
+                now[0] = self.stream.device.index  # as torch does: a stream brings its device along
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", lambda d: Enter(0, torch.device(d).index))
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: FakeStream(*now))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    return now
+
+
+def test_fp8_status_is_the_asked_devices(mm, monkeypatch, two_devices):
+    """After a product on another device than the current one its status is asked of that device."""
+    from newton_schulz_04_gb300 import binding
+    asked = []
+
+    class Lib:
+        @staticmethod
+        def muon_fp8_status(stream):
+            asked.append((two_devices[0], int(getattr(stream, "value", stream))))
+            return 6 if two_devices[0] == 1 else 0
+
+        @staticmethod
+        def muon_debug_bounded_wait_fp8(cycles, stream):
+            asked.append((two_devices[0], int(getattr(stream, "value", stream)), cycles))
+            return 0
+
+    monkeypatch.setattr(binding, "load", lambda: Lib)
+    assert mm.fp8_status(FakeStream(1, 7)) == 6 and asked.pop() == (1, 7)
+    assert mm.fp8_status(FakeStream(0, 8)) == 0 and asked.pop() == (0, 8)
+    assert mm.fp8_status() == 0 and asked.pop() == (0, 100)
+    assert mm.fp8_status(device=1) == 6 and asked.pop() == (1, 101)
+    assert mm.fp8_status(device="cuda:1") == 6 and asked.pop() == (1, 101)
+    assert mm.fp8_status(device="cuda") == 0 and asked.pop() == (0, 100)
+    mm.debug_bounded_wait_fp8(5, FakeStream(1, 7))
+    assert asked.pop() == (1, 7, 5)
+
+
+@gpu
+def test_fp8_status_loses_no_report(mm):
+    """Reports made on one stream while another one's status is asked for again and again are each given once."""
+    import threading
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    assert mm.fp8_status() == 0
+    given, calls, stop = [], [0], threading.Event()
+
+    def ask():
+        while not stop.is_set():
+            status = mm.fp8_status(other)
+            if status != 0:
+                given.append(status)
+            calls[0] += 1
+
+    thread = threading.Thread(target=ask)
+    thread.start()
+    try:
+        for i in range(400):
+            before = len(given)
+            mm.debug_bounded_wait_fp8(1 + 97 * i, side)
+            side.synchronize()
+            n = calls[0]
+            while calls[0] < n + 2 and thread.is_alive():  # a call begun after the report has returned
+                pass
+            assert given[before:] == [6], i
+    finally:
+        stop.set()
+        thread.join()
+    assert mm.fp8_status() == 0
