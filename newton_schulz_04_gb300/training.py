@@ -69,6 +69,8 @@ def _like(t, ref, name):
 def _on(stream, device, call, *args):
     """call(*args, stream pointer) with `device` and `stream` (None: its current one) current, so that the tensors made
     within belong to that stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
     if stream is None and device.index == torch.cuda.current_device():
         return call(*args, torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device), torch.cuda.stream(stream):

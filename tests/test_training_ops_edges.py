@@ -162,6 +162,21 @@ def test_fp8_status_is_the_asked_devices(mm, monkeypatch, two_devices):
     assert asked.pop() == (1, 7, 5)
 
 
+def test_stream_of_another_device_is_refused(mm, two_devices):
+    """A stream of another device would make that device current and launch there with this device's pointers."""
+    from newton_schulz_04_gb300 import training
+    ran = []
+    here = torch.device("cuda", 0)
+    training._on(FakeStream(0, 7), here, lambda *a: ran.append(a), 1)
+    training._on(None, torch.device("cuda", 1), lambda *a: ran.append(a), 2)
+    assert ran == [(1, 7), (2, 101)]
+    with pytest.raises(ValueError, match="stream"):
+        training._on(FakeStream(1, 7), here, lambda *a: ran.append(a))
+    with pytest.raises(ValueError, match="stream"):
+        mm.fp8_status(FakeStream(1, 7), device=0)
+    assert len(ran) == 2
+
+
 @gpu
 def test_fp8_status_loses_no_report(mm):
     """Reports made on one stream while another one's status is asked for again and again are each given once."""
