@@ -9,6 +9,9 @@ gradient clipping by the global norm, the RMS norm with an 8-bit copy and its gr
     dW = fp8_matmul(dqt, fp8_quantize(r.y, rows=False, cols=True)[1], torch.float32, add=dW)   # weight gradient
     dx, dw_norm = rms_norm_backward(dy, r.h, w_norm, r.rstd, dresidual=dstream)
     clip_grads(grads, max_norm=1.0)                            # then muon_step
+
+With `stream=` (a stream of the tensors' device) a call runs there and its results belong to that stream; the caller
+orders it after what its inputs wait for, and what reads the results after it.
 """
 from __future__ import annotations
 
@@ -66,13 +69,18 @@ def _like(t, ref, name):
         raise ValueError(f"{name} must have the shape, dtype and device of the input")
 
 
-def _on(stream, device, call, *args):
+def _on(stream, device, tensors, call, *args):
     """call(*args, stream pointer) with `device` and `stream` (None: its current one) current, so that the tensors made
-    within belong to that stream."""
+    within belong to that stream.  The memory of `tensors` (or None among them), which it reads or writes, is not given
+    away before a `stream` of the caller's has passed the call."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
     if stream is None and device.index == torch.cuda.current_device():
         return call(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
     with torch.cuda.device(device), torch.cuda.stream(stream):
         return call(*args, torch.cuda.current_stream().cuda_stream)
 
@@ -163,7 +171,7 @@ def fp8_quantize(x: torch.Tensor, fmt: str = "e4m3", square: bool = False, rows:
     if not (rows or cols):
         raise ValueError("neither rows nor cols is asked for")
     n, ld = _rows(x, "x")
-    return _on(stream, x.device, _quantize, x, n, ld, _dt(x, "x"), _fmt_code(fmt), fmt, 1 if square else 0, rows, cols)
+    return _on(stream, x.device, (x,), _quantize, x, n, ld, _dt(x, "x"), _fmt_code(fmt), fmt, 1 if square else 0, rows, cols)
 
 
 def _quantize(x, n, ld, dt, code, fmt, square, rows, cols, st):
@@ -195,7 +203,7 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, out_dtype=torch.bfloat16, add: Option
         raise ValueError("a must be on a CUDA device")
     if b.data.device != dev:
         raise ValueError(f"b is on {b.data.device}, not {dev}")
-    return _on(stream, dev, _matmul, a, b, out_dtype, add, out, dev)
+    return _on(stream, dev, (a.data, a.scale, b.data, b.scale, add, out), _matmul, a, b, out_dtype, add, out, dev)
 
 
 def _matmul(a, b, out_dtype, add, out, dev, st):
@@ -230,12 +238,12 @@ def fp8_status(stream=None, device=None) -> int:
 
     The status is that of `device` (default: the stream's, or the current one): one for all its streams, each report given
     once."""
-    return _on(stream, _status_device(stream, device), _b.load().muon_fp8_status)
+    return _on(stream, _status_device(stream, device), (), _b.load().muon_fp8_status)
 
 
 def debug_bounded_wait_fp8(max_cycles: int, stream=None, device=None) -> None:
     """Self-test of fp8_status: a wait on `device` that runs out after `max_cycles`."""
-    _b._check(_on(stream, _status_device(stream, device), _b.load().muon_debug_bounded_wait_fp8, int(max_cycles)))
+    _b._check(_on(stream, _status_device(stream, device), (), _b.load().muon_debug_bounded_wait_fp8, int(max_cycles)))
 
 
 # ---------------------------------------------------------------- RMS norm
@@ -273,7 +281,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Optional
         ldr, res = _rows(residual, "residual")[1], residual.data_ptr()
     dev = x.device
     wp, wdt = _weight(weight, shape[-1], dev)
-    return _on(stream, dev, _rms_norm, x, ldx, res, ldr, wp, wdt, rows, shape[-1], float(eps), fp8, y, _dt(x, "x"), dev)
+    return _on(stream, dev, (x, residual, weight), _rms_norm, x, ldx, res, ldr, wp, wdt, rows, shape[-1], float(eps), fp8, y,
+               _dt(x, "x"), dev)
 
 
 def _rms_norm(x, ldx, res, ldr, wp, wdt, rows, cols, eps, fp8, y, dt, dev, st):
@@ -318,8 +327,8 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.
     if rstd.dtype != torch.float32 or rstd.numel() != rows or not rstd.is_contiguous() or rstd.device != dev:
         raise ValueError(f"rstd must be {rows} contiguous float32 values on {dev}")
     wp, wdt = _weight(weight, cols, dev)
-    return _on(stream, dev, _rms_norm_backward, dy, lddy, h.data_ptr(), ldh, wp, wdt, rstd.data_ptr(), res, lddr, rows, cols,
-               dweight, _dt(dy, "dy"), dev)
+    return _on(stream, dev, (dy, h, weight, rstd, dresidual), _rms_norm_backward, dy, lddy, h.data_ptr(), ldh, wp, wdt,
+               rstd.data_ptr(), res, lddr, rows, cols, dweight, _dt(dy, "dy"), dev)
 
 
 def _rms_norm_backward(dy, lddy, hp, ldh, wp, wdt, rp, res, lddr, rows, cols, dweight, dt, dev, st):
@@ -364,7 +373,8 @@ def _clip(grads, max_norm, out, eps, stream):
     table = array("q", table)
     base = table.buffer_info()[0]
     outs = None if out is None else base if out is grads else base + 16 * count
-    return _on(stream, dev, _clip_call, base, outs, base + 8 * count, dts.buffer_info()[0], count, max_norm, eps, dev,
+    tensors = grads if out is None or out is grads else [*grads, *out]
+    return _on(stream, dev, tensors, _clip_call, base, outs, base + 8 * count, dts.buffer_info()[0], count, max_norm, eps, dev,
                (table, dts))
 
 

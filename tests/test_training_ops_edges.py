@@ -167,14 +167,64 @@ def test_stream_of_another_device_is_refused(mm, two_devices):
     from newton_schulz_04_gb300 import training
     ran = []
     here = torch.device("cuda", 0)
-    training._on(FakeStream(0, 7), here, lambda *a: ran.append(a), 1)
-    training._on(None, torch.device("cuda", 1), lambda *a: ran.append(a), 2)
+    training._on(FakeStream(0, 7), here, (), lambda *a: ran.append(a), 1)
+    training._on(None, torch.device("cuda", 1), (), lambda *a: ran.append(a), 2)
     assert ran == [(1, 7), (2, 101)]
     with pytest.raises(ValueError, match="stream"):
-        training._on(FakeStream(1, 7), here, lambda *a: ran.append(a))
+        training._on(FakeStream(1, 7), here, (), lambda *a: ran.append(a))
     with pytest.raises(ValueError, match="stream"):
         mm.fp8_status(FakeStream(1, 7), device=0)
     assert len(ran) == 2
+
+
+@gpu
+def test_inputs_outlive_the_stream_that_reads_them(mm):
+    """Inputs that the caller lets go while the call still waits on another stream keep their memory until it has run."""
+    side = torch.cuda.Stream()
+    size = 1 << 20
+
+    def filled(value, *shape, dtype=torch.float32):
+        return torch.full(shape, value, dtype=dtype, device="cuda")
+
+    def taken_again(call, *shapes):
+        """Addresses that `call`'s inputs had and a new tensor of the same size gets while the call waits."""
+        inputs = [filled(2.0, *s) for s in shapes]
+        at = {t.data_ptr() for t in inputs}
+        call(*inputs)  # loads the code, which may wait for the device
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)  # some 25 ms
+        result = call(*inputs)
+        del inputs
+        again = [torch.empty(*s, device="cuda") for s in shapes for _ in range(2)]
+        hit = at & {t.data_ptr() for t in again}
+        side.synchronize()
+        return hit, result
+
+    rows = (1024, size // 1024)
+    hit, r = taken_again(lambda x, res: mm.rms_norm(x, None, res, stream=side), rows, rows)
+    assert not hit and bool((r.h == 4).all())
+    hit, r = taken_again(lambda x: mm.fp8_quantize(x, stream=side), rows)
+    assert not hit and bool((r[0].dequantize() == 2).all())
+    hit, _ = taken_again(lambda dy, h: mm.rms_norm_backward(dy, h, None, filled(1.0, 1024), stream=side), rows, rows)
+    assert not hit
+    hit, norm = taken_again(lambda g: mm.grad_norm([g], stream=side), (size,))
+    assert not hit and float(norm) == 2.0 * 1024
+    # the product's operands and addend
+    x = filled(2.0, *rows)
+    a, b = mm.fp8_quantize(x)[0], mm.fp8_quantize(x)[0]
+    add = filled(1.0, 1024, 1024)
+    at = {t.data_ptr() for t in (a.data, b.data, add)}
+    mm.fp8_matmul(a, b, torch.float32, add=add)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    c = mm.fp8_matmul(a, b, torch.float32, add=add, stream=side)
+    del a, b, add
+    again = [torch.empty(*rows, dtype=d, device="cuda") for d in (torch.uint8, torch.uint8, torch.float32, torch.float32)]
+    assert not at & {t.data_ptr() for t in again}
+    side.synchronize()
+    assert bool((c == 4097).all())
 
 
 @gpu
