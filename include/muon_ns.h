@@ -476,7 +476,8 @@ MUON_API size_t muon_clip_workspace_bytes(int count);
  * Squares that leave fp32's range do not spoil the norm of finite gradients.  An
  * infinite norm gives c = 0 (infinite elements become NaN), a NaN one gives NaN.
  * max_norm may be infinite.  Sums run in a fixed order.  Two launches up to 1024
- * tensors.  A tensor is listed once, and outputs overlap no other tensor.
+ * tensors.  Refused (MUON_ERR_ARG) are an output that overlaps another tensor of the
+ * list, as when one is listed twice in place, and tensors that overlap ws.
  */
 MUON_API muon_status muon_clip_grads(const void* const* grads, void* const* out, const int64_t* numel,
                                      const int32_t* dtypes, int count, float max_norm, float eps, float* norm,

@@ -7,6 +7,8 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <memory>
+#include <new>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -61,6 +63,51 @@ using namespace muon;
 extern "C" {
 
 // ------------------------------------------------------------------ clipping
+// Clipped in two places at once a tensor would be scaled twice, or by one CTA while another reads it: no output may
+// share memory with another tensor's output or gradient.  (out[i] is grads[i] or disjoint from it.)
+struct ClipSpan {
+  uintptr_t begin, end;
+};
+struct ClipSpans {
+  ClipSpan* s;
+  int n = 0;
+  bool sorted = true;
+  void put(const void* p, long long bytes) {
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(p);
+    if (n > 0 && begin < s[n - 1].begin) sorted = false;
+    s[n++] = {begin, begin + static_cast<uintptr_t>(bytes)};
+  }
+  void sort() {
+    if (!sorted) std::sort(s, s + n, [](const ClipSpan& a, const ClipSpan& b) { return a.begin < b.begin; });
+  }
+};
+static muon_status clip_disjoint(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* dtypes,
+                                 int count) {
+  ClipSpan few[2 * kClipSmall];
+  std::unique_ptr<ClipSpan[]> many;
+  if (count > kClipSmall) {
+    many.reset(new (std::nothrow) ClipSpan[2 * static_cast<size_t>(count)]);
+    if (!many) return fail(MUON_ERR_ARG, "no memory to look over %d tensors", count);
+  }
+  ClipSpans written{many ? many.get() : few}, read{written.s + count};
+  for (int i = 0; i < count; ++i) {
+    const long long bytes = numel[i] * dtype_bytes(dtypes[i]);
+    if (bytes == 0) continue;
+    written.put(out[i], bytes);
+    if (out[i] != grads[i]) read.put(grads[i], bytes);
+  }
+  written.sort();
+  read.sort();
+  uintptr_t last = 0, seen = 0;  // ends of the outputs so far, and of the gradients that begin before this output's end
+  for (int i = 0, r = 0; i < written.n; ++i) {
+    for (; r < read.n && read.s[r].begin < written.s[i].end; ++r) seen = std::max(seen, read.s[r].end);
+    if (written.s[i].begin < last || written.s[i].begin < seen)
+      return fail(MUON_ERR_ARG, "an output overlaps another tensor's output or gradient");
+    last = written.s[i].end;
+  }
+  return MUON_OK;
+}
+
 size_t muon_clip_workspace_bytes(int count) {
   // one 64-bit partial sum for each CTA of each launch
   const size_t launches = count <= kClipSmall ? 1 : (static_cast<size_t>(count) + kClipLarge - 1) / kClipLarge;
@@ -90,10 +137,15 @@ muon_status muon_clip_grads(const void* const* grads, void* const* out, const in
       return fail(MUON_ERR_ALIGN, "tensor %d is not aligned to its element size", i);
     if (out && out[i] != grads[i] && overlap(out[i], numel[i] * size, grads[i], numel[i] * size))
       return fail(MUON_ERR_ARG, "tensor %d: out overlaps the gradient", i);
-    if (out && overlap(out[i], numel[i] * size, ws, static_cast<long long>(ws_bytes)))
-      return fail(MUON_ERR_ARG, "tensor %d: out overlaps the workspace", i);
+    if (overlap(grads[i], numel[i] * size, ws, static_cast<long long>(ws_bytes)) ||
+        (out && overlap(out[i], numel[i] * size, ws, static_cast<long long>(ws_bytes))))
+      return fail(MUON_ERR_ARG, "tensor %d overlaps the workspace", i);
     chunks += (numel[i] * size + kClipChunkBytes - 1) / kClipChunkBytes;
     if (chunks > 0x7fffffffLL) return fail(MUON_ERR_SHAPE, "too many elements");
+  }
+  if (out) {
+    const muon_status apart = clip_disjoint(grads, out, numel, dtypes, count);
+    if (apart != MUON_OK) return apart;
   }
   muon_status st;
   const int sms = gpu(&st);

@@ -391,7 +391,9 @@ def _clip_call(grads, outs, numel, dts, count, max_norm, eps, dev, keep, st):
 def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
                eps: float = 1e-6, stream=None) -> torch.Tensor:
     """Scales all gradients by min(1, max_norm / (N + eps)), N their global norm, in place or into `out` (C-ABI
-    muon_clip_grads), and returns N (a 0-d fp32 tensor on the device; nothing waits for it)."""
+    muon_clip_grads), and returns N (a 0-d fp32 tensor on the device; nothing waits for it).
+
+    A tensor is listed once: outputs that share memory with another tensor of the list are refused."""
     return _clip(grads, float(max_norm), grads if out is None else out, float(eps), stream)
 
 

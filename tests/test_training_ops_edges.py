@@ -257,3 +257,56 @@ def test_fp8_status_loses_no_report(mm):
         stop.set()
         thread.join()
     assert mm.fp8_status() == 0
+
+
+# ---------------------------------------------------------------- clipping
+
+def _clip(mm, grads, outs, numel, ws=1 << 40, dtype=1):
+    """muon_clip_grads on addresses that are never read: of what is not refused, only the refusal is asked for."""
+    count = len(grads)
+    P, N, D = ctypes.c_void_p * count, ctypes.c_int64 * count, ctypes.c_int32 * count
+    size = mm.load().muon_clip_workspace_bytes(count)
+    return mm.load().muon_clip_grads(P(*grads), None if outs is None else P(*outs), N(*numel), D(*[dtype] * count), count,
+                                     1.0, 1e-6, 1 << 41, ws, size, None)
+
+
+@pytest.mark.parametrize("count", [2, 3, 65, 200])
+def test_clip_refuses_outputs_that_share_memory(mm, count):
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: for hosts where nothing can be launched")
+    step = 4096
+    a = [(1 << 30) + step * ((7 * i) % count if count % 7 else i) for i in range(count)]  # in no order
+    b = [p + (1 << 32) for p in a]
+    n = [step // 4] * count
+    fine = _clip(mm, a, a, n)
+    assert fine not in (0, 1)                      # what the missing device says
+    assert _clip(mm, a, b, n) == fine and _clip(mm, a, b, [0, *n[1:]]) == fine
+    last = count - 1
+    twice = [*a[:last], a[0]]
+    assert _clip(mm, twice, twice, n) == 1         # one tensor listed twice, in place
+    assert "overlaps another" in mm.load().muon_last_error().decode()
+    assert _clip(mm, twice, None, n) == fine       # the norm alone may count it twice
+    assert _clip(mm, twice, b, n) == fine          # and so may outputs of their own
+    assert _clip(mm, a, [*b[:last], b[0]], n) == 1
+    assert _clip(mm, a, [*b[:last], b[0] + step - 4], n) == 1
+    assert _clip(mm, a, a[1:] + a[:1], n) == 1     # outputs in another order than the gradients
+    assert _clip(mm, a, [*b[:last], a[0] + step - 4], n) == 1
+    assert _clip(mm, twice, twice, [*n[:last], 0]) == fine
+    assert _clip(mm, a, None, n, ws=a[last] + 8) == 1 and _clip(mm, a, b, n, ws=b[0] + 8) == 1
+
+
+@gpu
+def test_clip_refuses_a_tensor_listed_twice(mm):
+    g, h = torch.ones(5000, device="cuda"), torch.ones(70, device="cuda")
+    with pytest.raises(mm.MuonError, match="overlaps"):
+        mm.clip_grads([g, h, g], 0.5)
+    with pytest.raises(mm.MuonError, match="overlaps"):
+        mm.clip_grads([g[:100], g[50:200]], 0.5)
+    with pytest.raises(mm.MuonError, match="overlaps"):
+        mm.clip_grads([g, h], 0.5, out=[g, g[:70]])
+    assert bool((g == 1).all()) and float(mm.grad_norm([g, g])) == 100.0
+    out = [torch.zeros_like(g), torch.zeros_like(g)]
+    mm.clip_grads([g, g], 50.0, out=out)
+    assert torch.equal(*out) and abs(float(out[0][0]) - 0.5) < 1e-6
+    mm.clip_grads([g[2500:], g[:2500]], 10.0)      # neighbours, in any order
+    assert abs(float(mm.grad_norm([g])) - 10.0) < 1e-5
