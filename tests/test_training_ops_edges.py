@@ -310,3 +310,54 @@ def test_clip_refuses_a_tensor_listed_twice(mm):
     assert torch.equal(*out) and abs(float(out[0][0]) - 0.5) < 1e-6
     mm.clip_grads([g[2500:], g[:2500]], 10.0)      # neighbours, in any order
     assert abs(float(mm.grad_norm([g])) - 10.0) < 1e-5
+
+
+def _kernels(text):
+    """(name, body) of each kernel in a source."""
+    for m in re.finditer(r"__global__[^;{]*?(\w+_kernel)\([^{;]*\) \{", text):
+        depth, at = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[at], 0)
+            at += 1
+        yield m.group(1), text[m.end():at - 1]
+
+
+def test_every_thread_waits_for_the_kernels_before():
+    """A kernel that may start before the one ahead of it has ended waits for it in every thread, not in a branch or on
+    some threads only: nothing else makes visible what earlier kernels wrote."""
+    seen = []
+    for name in ("clip.cu", "rms_norm.cu", "fp8_quant.cu", "fp8_gemm.cu", "fp8_few.cu"):
+        for kernel, body in _kernels(open(os.path.join(CSRC, name)).read()):
+            if kernel == "fp8_take_status_kernel":  # launched in stream order
+                continue
+            before = body[:body.index("pdl_wait();")]
+            assert before.count("{") == before.count("}"), kernel
+            seen.append(kernel)
+    assert len(seen) >= 9 and "clip_scale_kernel" in seen
+
+
+@gpu
+def test_clip_right_after_the_kernels_that_write_its_gradients(mm):
+    """Gradients rewritten by this package's kernels and clipped at once, again and again at the same addresses."""
+    a = [mm.fp8_quantize(gen(i, 48, 256).cuda(), "e5m2")[0] for i in range(4)]
+    b = [mm.fp8_quantize(gen(9 + i, 80, 256).cuda())[0] for i in range(4)]
+    dy, h = gen(20, 300, 512).cuda(), gen(21, 300, 512).cuda()
+    rstd = torch.ones(300, device="cuda")
+    g = torch.empty(48, 80, device="cuda")
+    want = []
+    for i in range(4):
+        dw = mm.rms_norm_backward(dy, h, None, rstd * (i + 1))[1]
+        torch.cuda.synchronize()
+        t = [mm.fp8_matmul(a[i], b[i], torch.float32), dw]
+        torch.cuda.synchronize()
+        n = mm.clip_grads(t, 1.0)
+        torch.cuda.synchronize()
+        want.append([n, *t])
+    scaled = [rstd * (i + 1) for i in range(4)]
+    for turn in range(200):
+        i = turn % 4
+        mm.fp8_matmul(a[i], b[i], out=g)
+        dw = mm.rms_norm_backward(dy, h, None, scaled[i])[1]
+        n = mm.clip_grads([g, dw], 1.0)
+        got = [n.clone(), g.clone(), dw]
+        assert all(torch.equal(x, y) for x, y in zip(got, want[i])), turn
