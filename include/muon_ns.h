@@ -495,7 +495,9 @@ MUON_API muon_status muon_clip_grads(const void* const* grads, void* const* out,
  *   rstd    [rows] fp32 rho (the gradient needs it), or NULL.
  *   q, q_scale  8-bit copy of the unrounded y (see above), or both NULL.
  * y or h may be x or residual themselves.  cols in [1, MUON_MAX_DIM], rows in
- * [0, MUON_MAX_ROWS].
+ * [0, MUON_MAX_ROWS].  The squares and their sum are fp32: a row whose sum of squares
+ * leaves its range (values from about 1.8e19 / sqrt(cols) on) gets rho = 0, and y = 0 where
+ * s is finite; squares below 1e-45 count as 0, which shows only with an eps as small.
  */
 MUON_API muon_status muon_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                    const void* weight, muon_dtype weight_dt, int64_t rows, int64_t cols, float eps,
@@ -509,8 +511,8 @@ MUON_API muon_status muon_rms_norm(const void* x, int64_t ldx, const void* resid
  *   dweight_j = sum over rows of dy_j h_j rho   (fp32, overwritten)
  *
  * dx is the gradient of x and of residual alike; dresidual (or NULL) is what reaches
- * h on its way past the norm.  dx may be dy, dresidual or h itself.  dx or
- * dweight may be NULL.  The workspace (16-byte aligned, size from
+ * h on its way past the norm.  dx may be dy, dresidual or h itself.  Products and sums
+ * are fp32, which dy_j weight_j h_j and their sum have to fit.  dx or dweight may be NULL.  The workspace (16-byte aligned, size from
  * muon_rms_norm_backward_workspace_bytes) is needed with dweight.
  */
 MUON_API size_t muon_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);

@@ -268,7 +268,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Optional
     """Root-mean-square norm over the last dimension (C-ABI muon_rms_norm): h = x + residual,
     y = h / sqrt(mean(h^2) + eps) * weight, and with `fp8` ("e4m3" or "e5m2") y in 8 bits as well; `y=False` leaves out
     the 16- or 32-bit y.  x is bf16, fp16 or fp32 with any leading dimensions; weight (or None) may have another of these
-    types."""
+    types.  The sum of squares is fp32: a row for which it overflows gets rstd = 0 and y = 0."""
     shape = x.shape
     if not shape or shape[-1] < 1:
         raise ValueError("x needs a last dimension of at least 1")

@@ -361,3 +361,23 @@ def test_clip_right_after_the_kernels_that_write_its_gradients(mm):
         n = mm.clip_grads([g, dw], 1.0)
         got = [n.clone(), g.clone(), dw]
         assert all(torch.equal(x, y) for x, y in zip(got, want[i])), turn
+
+
+# ---------------------------------------------------------------- RMS norm
+
+@gpu
+@pytest.mark.parametrize("cols", [256, 1000, 1001, 4096, 16384, 20001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rms_norm_range(mm, dtype, cols):
+    """As stated: right while a row's sum of squares is below fp32's largest value, rho = 0 and y = 0 beyond."""
+    large, small = 2.0 ** 63 / math.sqrt(cols), 1e-15
+    x = gen(1, 4, cols).clamp(-3, 3)
+    x = (x / 3 * torch.tensor([[large], [small], [1.0], [large]])).to(dtype)
+    x[3] = 2.0 ** 66
+    r = mm.rms_norm(x.cuda(), None, eps=0.0, fp8="e4m3")
+    want, _, rstd = ref.rms_norm(x[:3], None, eps=0.0)
+    rel = (137 / 2 + 4) * F24
+    close(r.rstd[:3], rstd.flatten(), rel * rstd.flatten())
+    close(r.y[:3], want, (U[dtype] + rel + 3 * F24) * want.abs() + TINY[dtype])
+    assert float(r.rstd[3]) == 0 and float(r.y[3].abs().sum()) == 0
+    assert float(r.q.dequantize()[3].abs().sum()) == 0 and bool(r.q.dequantize().isfinite().all())
