@@ -118,6 +118,8 @@ class Fp8Tensor:
     @classmethod
     def empty(cls, rows: int, cols: int, fmt: str = "e4m3", device=None) -> "Fp8Tensor":
         """Uninitialised, with the row padding that the product asks for."""
+        if fmt not in _FMT_TYPE:
+            raise _unknown(fmt)
         self = object.__new__(cls)
         pitch = (cols + 15) // 16 * 16
         data = torch.empty((rows, pitch), dtype=_FMT_TYPE[fmt], device=device or "cuda")
@@ -152,11 +154,15 @@ class Fp8Tensor:
         return f"Fp8Tensor({list(self.data.shape)}, {self.fmt}, device={self.data.device})"
 
 
+def _unknown(fmt) -> ValueError:
+    return ValueError(f"unknown 8-bit format {fmt!r}: 'e4m3' or 'e5m2'")
+
+
 def _fmt_code(fmt: str) -> int:
     try:
         return _FMT[fmt]
     except KeyError:
-        raise ValueError(f"unknown 8-bit format {fmt!r}: 'e4m3' or 'e5m2'") from None
+        raise _unknown(fmt) from None
 
 
 def fp8_quantize(x: torch.Tensor, fmt: str = "e4m3", square: bool = False, rows: bool = True, cols: bool = False,

@@ -381,3 +381,17 @@ def test_rms_norm_range(mm, dtype, cols):
     close(r.y[:3], want, (U[dtype] + rel + 3 * F24) * want.abs() + TINY[dtype])
     assert float(r.rstd[3]) == 0 and float(r.y[3].abs().sum()) == 0
     assert float(r.q.dequantize()[3].abs().sum()) == 0 and bool(r.q.dequantize().isfinite().all())
+
+
+def test_empty_refuses_an_unknown_format(mm):
+    with pytest.raises(ValueError, match="format"):
+        mm.Fp8Tensor.empty(2, 128, "e3m4", device="cpu")
+    assert mm.Fp8Tensor.empty(2, 100, "e5m2", device="cpu").data.stride(0) == 112
+
+
+@gpu
+def test_unknown_formats_are_refused(mm):
+    x = torch.ones(2, 128, device="cuda")
+    for call in (lambda: mm.fp8_quantize(x, fmt="e3m4"), lambda: mm.rms_norm(x, None, fp8="e3m4")):
+        with pytest.raises(ValueError, match="format"):
+            call()
