@@ -383,6 +383,184 @@ def test_rms_norm_range(mm, dtype, cols):
     assert float(r.q.dequantize()[3].abs().sum()) == 0 and bool(r.q.dequantize().isfinite().all())
 
 
+RING = {  # columns that a ring takes, in 16-bit types (half of them in fp32): (rows ahead, rows per CTA, CTAs per SM)
+    248: ((8, 4, 6), (4, 4, 6)), 504: ((4, 2, 8), (4, 4, 3)), 1000: ((4, 2, 4), (4, 2, 3)), 2040: ((4, 1, 3), (5, 1, 3)),
+    4088: ((5, 1, 2), (4, 1, 2)), 8184: ((4, 1, 1), (4, 1, 1)), 16376: ((3, 1, 1), (2, 1, 1))}
+
+
+def _many_rows(cols, dtype, which):
+    """(rows, cols): more than enough for every CTA to refill its whole ring, and an odd rest; rows of one turn."""
+    ahead, per, ctas = RING[cols][which]
+    turn = per * ctas * torch.cuda.get_device_properties(0).multi_processor_count
+    return (ahead + 2) * turn + 3, cols if dtype != torch.float32 else cols // 2, turn
+
+
+def _raw(t):
+    return t.contiguous().view(torch.uint8)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("cols", list(RING))
+def test_rms_norm_rings_many_turns(mm, cols, dtype):
+    """The persistent kernel over many turns: near the oracle, and the bits that the same rows have in one turn."""
+    rows, cols, turn = _many_rows(cols, dtype, 0)
+    g = torch.Generator("cuda").manual_seed(5)
+    x = (torch.randn(rows, cols, device="cuda", generator=g) * torch.exp(torch.randn(rows, 1, device="cuda", generator=g)))
+    x, res = x.to(dtype), torch.randn(rows, cols, device="cuda", generator=g).to(dtype)
+    w = 1 + 0.1 * torch.randn(cols, device="cuda", generator=g)
+    r = mm.rms_norm(x, w, res, fp8="e4m3")
+    y, h, rstd = ref.rms_norm(x, w, res)
+    rel = (137 / 2 + 4) * F24
+    close(r.rstd, rstd.flatten(), rel * rstd.flatten().cpu())
+    close(r.h, h, (U[dtype] * h.abs() + TINY[dtype]).cpu())
+    tol = (U[dtype] + rel + 3 * F24) * y.abs() + TINY[dtype] + F24 * h.abs() * rstd[..., None] * w.double().abs()
+    close(r.y, y, tol.cpu())
+    data, scale, scales = _raw(r.q.data), r.q.scale.view(torch.uint8), r.q.scales()
+    assert int((scale == 255).sum()) == 0
+    for i in range(0, rows, turn):
+        part = slice(i, min(rows, i + turn))
+        s = mm.rms_norm(x[part], w, res[part], fp8="e4m3")
+        assert torch.equal(s.y, r.y[part]) and torch.equal(s.h, r.h[part]) and torch.equal(s.rstd, r.rstd[part]), i
+        assert torch.equal(_raw(s.q.data), data[part]) and torch.equal(s.q.scales(), scales[part]), i
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("cols", list(RING))
+def test_rms_norm_gradient_rings_many_turns(mm, cols, dtype):
+    rows, cols, turn = _many_rows(cols, dtype, 1)
+    g = torch.Generator("cuda").manual_seed(6)
+    dy, h, res = (torch.randn(rows, cols, device="cuda", generator=g).to(dtype) for _ in range(3))
+    w = 1 + 0.2 * torch.randn(cols, device="cuda", generator=g)
+    rstd = ref.rms_norm(h)[2].float()
+    dx, dw = mm.rms_norm_backward(dy, h, w, rstd, res)
+    want, want_w = ref.rms_norm_backward(dy, h, w, rstd, res)
+    r, gw = rstd.double()[:, None], dy.double() * w.double()
+    mean = (gw * h.double()).abs().mean(dim=1, keepdim=True)
+    tol = (140 * F24) * h.double().abs() * r ** 3 * mean + 6 * F24 * ((r * gw).abs() + want.abs())
+    close(dx, want, (tol + U[dtype] * want.abs() + TINY[dtype]).cpu())
+    # a column's chain: 8 turns, 4 rows of a CTA, a 32nd of up to 912 CTAs, five joins; two products
+    close(dw, want_w, (8 + 4 + 29 + 5 + 2) * F24 * (dy.double() * h.double() * r).abs().sum(dim=0).cpu())
+    for i in range(0, rows, turn):
+        part = slice(i, min(rows, i + turn))
+        s = mm.rms_norm_backward(dy[part], h[part], w, rstd[part], res[part], dweight=False)[0]
+        assert torch.equal(s, dx[part]), i
+
+
+def _norm_in_place(mm, x, res, w, y, h, ld):
+    """muon_rms_norm on [rows, cols] views of row stride ld; y, h or res may be None."""
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    rows, cols = x.shape
+    dt = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}[x.dtype]
+    rstd = torch.empty(rows, device="cuda")
+    assert mm.load().muon_rms_norm(at(x), ld, at(res), ld, at(w), 1, rows, cols, 1e-6, at(y), ld, at(h), ld, at(rstd), None, 0,
+                                   None, 0, dt, torch.cuda.current_stream().cuda_stream) == 0
+    return rstd
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(3, 5), (40000, 64), (5000, 1000), (700, 1001), (2500, 4096), (700, 8192), (500, 16376),
+                                       (300, 9001), (40, 33000)])
+def test_norms_in_place(mm, dtype, rows, cols):
+    """y or h over x or the residual, dx over dy, the residual's gradient or h: the bits of separate outputs."""
+    ld = cols + 24
+    big = lambda seed: torch.randn(rows, ld, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)).to(dtype)  # noqa: E731
+    x, res, w = big(1), big(2), 1 + 0.1 * gen(3, cols).cuda()
+    v = lambda t: t[:, :cols]  # noqa: E731
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    rstd = _norm_in_place(mm, v(x), v(res), w, v(y), v(h), ld)
+    assert bool(v(y).isfinite().all())
+    for py, ph in (("x", None), ("res", None), (None, "x"), (None, "res"), ("x", "res"), ("res", "x")):
+        t = {"x": x.clone(), "res": res.clone(), None: torch.empty_like(x)}
+        out_y, out_h = t[py], (torch.empty_like(x) if ph is None else t[ph])
+        got = _norm_in_place(mm, v(t["x"]), v(t["res"]), w, v(out_y), v(out_h), ld)
+        assert torch.equal(got, rstd) and torch.equal(v(out_y), v(y)) and torch.equal(v(out_h), v(h)), (py, ph)
+        for name, old in (("x", x), ("res", res)):  # between the rows, and what is only read
+            assert torch.equal(t[name][:, cols:], old[:, cols:])
+            assert name in (py, ph) or torch.equal(t[name], old)
+    alone = x.clone()
+    _norm_in_place(mm, v(alone), None, w, v(alone), None, ld)
+    assert torch.equal(v(alone), mm.rms_norm(v(x), w).y)
+
+    dy, lib = big(7), mm.load()
+    dt = 0 if dtype == torch.bfloat16 else 1
+    want, want_w = mm.rms_norm_backward(v(dy), v(h), w, rstd, v(res))
+    ws = torch.empty(lib.muon_rms_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    for over in ("dy", "h", "res"):
+        t = {"dy": dy.clone(), "h": h.clone(), "res": res.clone()}
+        dw = torch.empty(cols, device="cuda")
+        assert lib.muon_rms_norm_backward(t["dy"].data_ptr(), ld, t["h"].data_ptr(), ld, w.data_ptr(), 1, rstd.data_ptr(),
+                                          t["res"].data_ptr(), ld, rows, cols, t[over].data_ptr(), ld, dw.data_ptr(),
+                                          ws.data_ptr(), ws.numel(), dt, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(v(t[over]), want) and torch.equal(dw, want_w), over
+
+
+# ---------------------------------------------------------------- what the looser tests let pass
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("size", [1, 9, 8193, 100_003, 2_000_001])
+def test_clip_misses_no_element(mm, dtype, size):
+    """One element alone makes the norm: at both ends, around every boundary of 32 KB, in the rest."""
+    per = 32768 // (4 if dtype == torch.float32 else 2)
+    at = sorted({p for c in range(0, size + per, per) for p in (c - 1, c, c + 1, c + 255, c + 256) if 0 <= p < size}
+                | {0, size // 2, size - 1})
+    for offset in (0, 1):  # aligned to 16 bytes, and not
+        g = torch.zeros(size + offset, dtype=dtype, device="cuda")[offset:]
+        other = torch.zeros(5, device="cuda")
+        norms = []
+        for p in at:
+            g[p] = 3.0
+            norms.append(mm.grad_norm([other, g, other]))
+            g[p] = 0.0
+        assert torch.stack(norms).tolist() == [3.0] * len(at)
+    for p in (0, size // 2, size - 1):  # and all of it is scaled
+        g = torch.full((size,), 2.0 ** -6, dtype=dtype, device="cuda")
+        g[p] = 2.0 ** 6
+        norm = mm.clip_grads([g], 0.25, eps=0.0)
+        want = torch.full((size,), 2.0 ** -6, dtype=dtype, device="cuda")
+        want[p] = 2.0 ** 6
+        assert torch.equal(g, (want.float() * (0.25 / norm)).to(dtype))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("parts", [1, 7])
+def test_clip_runs_of_many_chunks(mm, dtype, parts):
+    """Six or more whole chunks for each CTA: the norm to its own chain, and every element."""
+    width = 4 if dtype == torch.float32 else 2
+    ctas = 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    size = (7 * ctas * 32768 // width) // parts + 11
+    g = [torch.randn(size + 3 * i, device="cuda", generator=torch.Generator("cuda").manual_seed(i)).to(dtype) for i in range(parts)]
+    old = [t.clone() for t in g]
+    want = math.sqrt(math.fsum(float(t.double().square().sum()) for t in g))
+    norm = mm.clip_grads(g, 1.0)
+    # 16 elements of a chunk to each of a thread's four sums (8 in fp32, but 16 holds), 9 chunks, and the joins
+    assert abs(float(norm) - want) <= (16 * 9 + 2 + 5 + 4) * F24 * want
+    factor = 1.0 / (norm + 1e-6)
+    for a, b in zip(g, old):
+        assert torch.equal(a, (b.float() * factor).to(dtype))
+
+
+@gpu
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 129), (8, 33, 2500), (9, 33, 2500), (33, 100, 31), (64, 513, 1152), (225, 257, 513),
+                                   (500, 40, 2049), (1000, 1500, 700)])
+def test_products_without_nan(mm, out, fa, fb, m, n, k):
+    a, av = _operand(mm, 1, m, k, fa)
+    b, bv = _operand(mm, 3, n, k, fb)
+    want = ref.matmul(av, bv)
+    tol = _product_tol(av, bv, want, out, k)
+    buf = torch.full((m, n), math.nan, dtype=out, device="cuda")
+    close(mm.fp8_matmul(a, b, out=buf), want, tol)
+    add = (gen(9, m, n) * float(want.abs().mean())).to(out)
+    want = want + add.double()
+    close(mm.fp8_matmul(a, b, add=add.cuda(), out=buf.fill_(math.nan)), want, tol + (U[out] + F24) * (want.abs() + add.double().abs()))
+
+
 def test_empty_refuses_an_unknown_format(mm):
     with pytest.raises(ValueError, match="format"):
         mm.Fp8Tensor.empty(2, 128, "e3m4", device="cpu")
