@@ -25,6 +25,8 @@ static bool aligned16(const void* p, long long ld, int size) { return !misaligne
 static long long span(long long rows, long long cols, long long ld, int size) {
   return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * size : 0;
 }
+// And by an 8-bit one, whose rows are written up to the next multiple of 16 bytes.
+static long long span8(long long rows, long long cols, long long ld) { return span(rows, (cols + 15) / 16 * 16, ld, 1); }
 static bool overlap(const void* a, long long na, const void* b, long long nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
@@ -223,7 +225,7 @@ muon_status muon_rms_norm(const void* x, int64_t ldx, const void* residual, int6
       return fail(MUON_ERR_ARG, "an output partly overlaps an input");
   if (y && h && overlap(y, span(rows, cols, ldy, size), h, span(rows, cols, ldh, size)))
     return fail(MUON_ERR_ARG, "y and h overlap");
-  const long long nq = span(rows, cols, ldq, 1);
+  const long long nq = span8(rows, cols, ldq);
   if (overlap(q, nq, x, span(rows, cols, ldx, size)) || overlap(q, nq, residual, span(rows, cols, ldr, size)) ||
       overlap(q, nq, y, span(rows, cols, ldy, size)) || overlap(q, nq, h, span(rows, cols, ldh, size)))
     return fail(MUON_ERR_ARG, "q overlaps another matrix");
@@ -312,8 +314,8 @@ muon_status muon_fp8_quantize(const void* x, int64_t ldx, int64_t rows, int64_t 
   TRY(check_fp8_out("q", q, q_scale, rows, cols, ldq));
   TRY(check_fp8_out("qt", qt, qt_scale, cols, rows, ldqt));
   const long long nx = span(rows, cols, ldx, dtype_bytes(dt));
-  if (overlap(x, nx, q, span(rows, cols, ldq, 1)) || overlap(x, nx, qt, span(cols, rows, ldqt, 1)) ||
-      overlap(q, span(rows, cols, ldq, 1), qt, span(cols, rows, ldqt, 1)))
+  const long long nq = span8(rows, cols, ldq), nqt = span8(cols, rows, ldqt);
+  if (overlap(x, nx, q, nq) || overlap(x, nx, qt, nqt) || overlap(q, nq, qt, nqt))
     return fail(MUON_ERR_ARG, "an output overlaps x or the other output");
   muon_status st;
   gpu(&st);

@@ -497,6 +497,25 @@ def test_norms_in_place(mm, dtype, rows, cols):
         assert torch.equal(v(t[over]), want) and torch.equal(dw, want_w), over
 
 
+def test_padding_of_an_8_bit_output_overlaps_too(mm):
+    """Rows of 8-bit outputs are written up to the next multiple of 16 bytes: nothing else may lie there."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: for hosts where nothing can be launched")
+    lib = mm.load()
+    q, scale, far = 1 << 30, 1 << 31, 1 << 32
+
+    def norm(x, cols=100, rows=4, ldq=112):
+        return lib.muon_rms_norm(x, cols, None, 0, None, 0, rows, cols, 1e-6, None, 0, None, 0, None, q, ldq, scale, 0, 0, None)
+
+    def quantize(x, qt=None):
+        return lib.muon_fp8_quantize(x, 100, 4, 100, 0, 0, 0, q, 112, scale, qt, 16, None if qt is None else far, None)
+
+    end = q + 3 * 112 + 112
+    assert norm(end) == quantize(end) == quantize(far << 1, end) not in (0, 1)
+    assert norm(end - 2) == 1 and quantize(end - 2) == 1           # between the last column and the row's padded end
+    assert quantize(far << 1, end - 16) == 1 and quantize(far << 1, end - 112) == 1
+
+
 # ---------------------------------------------------------------- what the looser tests let pass
 
 @gpu
