@@ -544,8 +544,10 @@ MUON_API muon_status muon_fp8_quantize(const void* x, int64_t ldx, int64_t rows,
 /*
  * muon_fp8_matmul -- out = round(A B^T + add) for 8-bit A [m, k] and B [n, k] as
  * described above, of either format each; add (or NULL) and out are [m, n] of
- * out_dt.  add may be out itself.  Products are summed in fp32.  k = 0 gives
- * add, or zeros.  With few tiles k is split over the CTAs of a cluster, whose sums
+ * out_dt.  add may be out itself.  k = 0 gives add, or zeros.  Products are summed in
+ * fp32; with more than 8 rows of A or more than 32 of B per SM by the tensor core over all of k, which truncates:
+ * off by at most k 2^-28 of the sum of the products' magnitudes (measured where all have
+ * one sign: 5e-7 at k = 8192, 2.4e-5 at 131072, 4.2e-4 at 1048576).  With few tiles k is split over the CTAs of a cluster, whose sums
  * are added in a fixed order.  A kernel that gives up on a bounded wait leaves the output incomplete and is
  * reported by muon_fp8_status.
  */

@@ -592,3 +592,23 @@ def test_unknown_formats_are_refused(mm):
     for call in (lambda: mm.fp8_quantize(x, fmt="e3m4"), lambda: mm.rms_norm(x, None, fp8="e3m4")):
         with pytest.raises(ValueError, match="format"):
             call()
+
+
+@gpu
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("m,k", [(8, 131072), (40, 131072), (8, 1 << 20), (40, 1 << 20), (300, 1 << 20)])
+def test_products_over_a_long_axis(mm, m, k, positive):
+    """The stated bound of the sums over k, against 64 bits."""
+    n = 64
+    g = torch.Generator("cuda").manual_seed(1)
+    x, w = torch.randn(m, k, device="cuda", generator=g), torch.randn(n, k, device="cuda", generator=g)
+    if positive:
+        x, w = x.abs(), w.abs()
+    a, b = mm.fp8_quantize(x)[0], mm.fp8_quantize(w)[0]
+    av, bv = a.dequantize(), b.dequantize()
+    want, most = (torch.zeros(m, n, dtype=torch.float64, device="cuda") for _ in range(2))
+    for i in range(0, k, 65536):
+        p, q = av[:, i:i + 65536].double(), bv[:, i:i + 65536].double()
+        want += p @ q.t()
+        most += p.abs() @ q.abs().t()
+    close(mm.fp8_matmul(a, b, torch.float32), want, ((k * 2.0 ** -28 + 48 * 2.0 ** -23) * most + 2.0 ** -24 * want.abs()).cpu())
