@@ -236,7 +236,6 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ float sh[2][TH / 32];
   const Ring<T, TH, C, S, 2> ring{ring_smem};
-  constexpr bool KEEP = C <= 2;  // the weight stays in registers
   const int t = threadIdx.x % G, rr = threadIdx.x / G;
   int n[C], off[C];  // existing columns of each piece, and its first (0 where none exists)
 #pragma unroll
@@ -265,11 +264,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
   pdl_wait();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
-  float w[KEEP ? C : 1][E];
-  if (KEEP) {
+  float w[C][E];  // the weight stays in registers
 #pragma unroll
-    for (int c = 0; c < C; ++c) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[KEEP ? c : 0]);
-  }
+  for (int c = 0; c < C; ++c) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[c]);
   const float inv_cols = 1.f / static_cast<float>(a.cols);
   T* ph = static_cast<T*>(a.h) + (a.h ? row0 * a.ldh : 0);
   T* py = static_cast<T*>(a.y) + (a.y ? row0 * a.ldy : 0);
@@ -305,9 +302,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_ring_kernel(
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (live && a.h) store_piece(ph + off[c], n[c], s[c]);
-      if (!KEEP) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[0]);
 #pragma unroll
-      for (int i = 0; i < E; ++i) s[c][i] = s[c][i] * rstd * w[KEEP ? c : 0][i];
+      for (int i = 0; i < E; ++i) s[c][i] = s[c][i] * rstd * w[c][i];
       if (n[c] < E) {
 #pragma unroll
         for (int i = 0; i < E; ++i)
@@ -573,7 +569,6 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_grad_kernel(const 
 template <typename T, int G, int C, int S, int MINB>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_kernel(const RmsNormGradArgs a) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G, E = 16 / static_cast<int>(sizeof(T));
-  constexpr bool KEEP = C <= 2;  // the weight stays in registers
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ float sh[2][TH / 32];
   const Ring<T, TH, C, S, 3> ring{ring_smem};
@@ -609,11 +604,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
   pdl_wait();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
-  float w[KEEP ? C : 1][E], dw[C][E];
-  if (KEEP) {
+  float w[C][E], dw[C][E];  // the weight stays in registers
 #pragma unroll
-    for (int c = 0; c < C; ++c) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[KEEP ? c : 0]);
-  }
+  for (int c = 0; c < C; ++c) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[c]);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -639,10 +632,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
 #pragma unroll
         for (int i = 0; i < E; ++i) d[c][i] = x[c][i] = 0.f;
       }
-      if (!KEEP) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[0]);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        sum = fmaf(d[c][i] * w[KEEP ? c : 0][i], x[c][i], sum);
+        sum = fmaf(d[c][i] * w[c][i], x[c][i], sum);
         dw[c][i] = fmaf(d[c][i] * x[c][i], rstd, dw[c][i]);
       }
     }
@@ -652,7 +644,6 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         float v[E];
-        if (!KEEP) load_weight_piece<E>(a.weight, a.weight_dt, off[c], n[c], w[0]);
         if (add) {
           ring.read(slot, 2, c, v);
         } else {
@@ -660,7 +651,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) rms_norm_grad_ring_ke
           for (int i = 0; i < E; ++i) v[i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] += rstd * (d[c][i] * w[KEEP ? c : 0][i] - x[c][i] * k);
+        for (int i = 0; i < E; ++i) v[i] += rstd * (d[c][i] * w[c][i] - x[c][i] * k);
         store_piece(px + off[c], n[c], v);
       }
     }
