@@ -475,7 +475,7 @@ MUON_API size_t muon_clip_workspace_bytes(int count);
  *   ws    device workspace of muon_clip_workspace_bytes(count), 8-byte aligned.
  * Squares that leave fp32's range do not spoil the norm of finite gradients.  An
  * infinite norm gives c = 0 (infinite elements become NaN), a NaN one gives NaN.
- * max_norm may be infinite.  Sums run in a fixed order.  Two launches up to 1024
+ * max_norm may be infinite: c = 1, or NaN where the norm is infinite too.  Sums run in a fixed order.  Two launches up to 1024
  * tensors.  Refused (MUON_ERR_ARG) are an output that overlaps another tensor of the
  * list, as when one is listed twice in place, and tensors that overlap ws.
  */

@@ -18,7 +18,7 @@ from . import build as _build
 OK, ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED = range(8)
 STATUS_NAMES = ["OK", "ERR_ARG", "ERR_SHAPE", "ERR_ALIGN", "ERR_WORKSPACE", "ERR_CUDA", "ERR_TIMEOUT",
                 "ERR_UNSUPPORTED"]
-BF16, FP32, FP16 = 0, 1, 2  # FP16: muon_debug_gemm only
+BF16, FP32, FP16 = 0, 1, 2  # FP16: muon_debug_gemm and the operators of training.py
 F16_LO_SCALE = 2048.0  # an fp16 pair stores lo = fp16((v - hi) * 2^11)
 SCHED = {"auto": 0, "gram_x3": 1, "gram_x1": 2, "orig": 3, "orig_bf16": 4, "orig_f16x3": 5, "gram_r2": 6}
 SCHED_NAMES = {v: k for k, v in SCHED.items()}

@@ -32,7 +32,10 @@
 //   warp 14      fetches the words to shared memory, up to eight groups ahead: behind a
 //                queue of TMA loads a fetch takes 1500 to 2500 cycles, and one that
 //                was issued a group (1792 cycles) ahead held the MMAs up at every
-//                other stage (8192 x 14336 x 4096 in 326 us instead of 308)
+//                other stage (18 us more at 8192 x 14336 x 4096)
+//
+// 8192 x 14336 x 4096 takes 270 us in short bursts, 322 to 326 in long runs under the 1.4 kW limit.  Times that
+// comments here give for it are of bursts, and differences that a step made when it was taken.
 //
 // At most 8 rows of A with a B that small tiles cover at once have a kernel of their own (fp8_few.cu).
 // When there are too few tiles to fill the GPU, 2 or 4 pairs of one cluster share a tile of
@@ -61,7 +64,7 @@ __global__ void fp8_take_status_kernel() { g_fp8_taken = atomicExch(&g_fp8_statu
 
 // Three shapes of the kernel, by the tile's rows of A.
 //   BIG    224: single blocks of K in a ring of 7, taken two at a time by the MMAs (against
-//          3 stages of two blocks: 270 instead of 280 us at 8192 x 14336 x 4096)
+//          3 stages of two blocks 10 us less at 8192 x 14336 x 4096)
 //   MID    96 to 192: a pair of blocks' MMAs are shorter than two waits and two commits, so
 //          stages of two blocks (2048^3: 11 us, in single blocks 12.5)
 //   SMALL  32 and 64: smaller boxes, and room for the split of K
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(F8Cfg<KIND>::THREADS, 1) fp8_gemm_kernel(const
       // The whole warp runs the loop, so that addresses and descriptors stay in
       // uniform registers; one elected lane issues.  An MMA lasts T / 2 cycles: issued by
       // a divergent lane that rebuilt its descriptors, each took longer than that
-      // (8192 x 14336 x 4096 in 473 us instead of 326).
+      // (147 us more at 8192 x 14336 x 4096).
       int st = 0, grp = 0, tile = 0;
       bool ok = true;
       const uint32_t base = smem_u32(tiles);
@@ -698,7 +701,7 @@ static cudaError_t fp8_clusters(int sms, Fp8Clusters* out) {
 // and 1, 2 and 4 parts: a block of K takes the longest of its MMAs (2 T), its loads ((128 + T / 2)
 // rows of 128 bytes at 64 bytes a cycle: 256 + T) and the handling of a stage (313); a tile some 2000 cycles to
 // fill and drain the pipeline; joining parts 85 T.  K is split only where every tile has a cluster of
-// its own.  A tile of 32 rows of A by 4096 x 4096 takes 6.7 us on two parts (32 clusters; of four parts 15
+// its own.  A tile of 32 rows of A by 4096 x 4096 takes 7.0 us on two parts (32 clusters; of four parts 15
 // fit) and 7.9 unsplit, by 1024 x 4096 5.4 on four and 7.9; 512 x 4096 x 4096 10.3 with T = 128, 14.9 with 64, 12.7 with 224.
 static Fp8Plan fp8_plan(long long m, long long n, long long k, const Fp8Clusters& fit) {
   const long long groups = (k + 511) / 512, nI = (n + 255) / 256;

@@ -10,6 +10,9 @@ gradient clipping by the global norm, the RMS norm with an 8-bit copy and its gr
     dx, dw_norm = rms_norm_backward(dy, r.h, w_norm, r.rstd, dresidual=dstream)
     clip_grads(grads, max_norm=1.0)                            # then muon_step
 
+Autograd does not see these calls: their results have no gradient function, whatever the inputs require, and what is
+written in place or to `out` keeps its version.  The backward pass is written out, as above.
+
 With `stream=` (a stream of the tensors' device) a call runs there and its results belong to that stream; the caller
 orders it after what its inputs wait for, and what reads the results after it.
 """
