@@ -568,6 +568,141 @@ MUON_API muon_status muon_fp8_status(void* stream);
 /* muon_debug_bounded_wait on the 8-bit product's status word (failure-detection self-test of muon_fp8_status). */
 MUON_API muon_status muon_debug_bounded_wait_fp8(long long max_cycles, void* stream);
 
+/*
+ * ---- norms around a block, gated activation, 8-bit checkpoints
+ *
+ * What stands around and within a residual network's block, and keeps what its backward pass needs in 8 bits: an "8-bit
+ * copy" is a matrix in the format above with blocks of 128 columns, which the gradients read in the place of the
+ * bf16, fp16 or fp32 matrix.  Their arguments travel in structs, which are read during the call only; a row stride (ld) is
+ * ignored for a single row.  No output may overlap an input or another output.
+ */
+
+/* An 8-bit matrix that a call writes; data and scale NULL: not asked for. */
+typedef struct {
+    void* data;      /* 16-byte aligned, rows padded to 16 bytes */
+    void* scale;     /* muon_fp8_scale_bytes, 16-byte aligned */
+    int64_t ld;
+} muon_fp8_out;
+
+/*
+ * muon_block_norm -- a block's output joins the residual stream through a norm, a gate and a scale of its own, and the next
+ * block's norm follows:
+ *
+ *   rho_x = 1 / sqrt(mean_j x_j^2 + eps)      h = alpha residual + sigmoid(gate) scale post (x rho_x)
+ *   rho_h = 1 / sqrt(mean_j h_j^2 + eps)      y = h rho_h pre
+ *
+ *   x, residual   [rows, cols] of dt
+ *   gate          [rows, cols] of dt; with gate_per_row [rows] (ld: its stride); NULL: no gate (1)
+ *   post, scale, pre  [cols] of weight_dt; scale may be NULL (1)
+ *   y, h          [rows, cols] of dt, each may be NULL
+ *   rstd_x, rstd_h  [rows] fp32 rho_x, rho_h, each may be NULL
+ *   q             8-bit y of format fmt
+ *   x8, h8, gate8 8-bit copies of kept_fmt for the gradient; gate8 only of a gate [rows, cols]
+ * h goes on unrounded.  A gate of -infinity is 0 (as one below -87 may be).  Squares and sums are fp32, as in muon_rms_norm.
+ */
+typedef struct {
+    const void* x; int64_t ldx;
+    const void* residual; int64_t ldr;
+    const void* gate; int64_t ldg;
+    const void* post; const void* scale; const void* pre;
+    void* y; int64_t ldy;
+    void* h; int64_t ldh;
+    float* rstd_x; float* rstd_h;
+    muon_fp8_out q, x8, h8, gate8;
+    int64_t rows, cols;
+    int32_t dt, weight_dt, gate_per_row, fmt, kept_fmt;
+    float alpha, eps;
+} muon_block_norm_args;
+MUON_API muon_status muon_block_norm(const muon_block_norm_args* args, void* stream);
+
+/*
+ * muon_block_norm_backward -- its gradient for dy = dL/dy and dh, what reaches h on its way past the second norm (or NULL),
+ * with X = x rho_x and H = h rho_h:
+ *
+ *   a = dy pre      D = dh + rho_h (a - H mean_j(a_j H_j))      dresidual = alpha D
+ *   b = D sigmoid(gate) scale post      dx = rho_x (b - X mean_j(b_j X_j))
+ *   dgate = (1 - sigmoid(gate)) b X, summed over the row for a gate of its own
+ *   dpre = sum_rows dy H      S = sum_rows D sigmoid(gate) X      dpost = S scale      dscale = S post
+ *
+ *   x, h, gate    as the forward pass had them; or with x_scale, h_scale (and gate_scale where the gate is [rows, cols])
+ *                 8-bit copies of kept_fmt
+ *   rstd_x, rstd_h  [rows]
+ *   dx, dresidual, dgate  like x, residual and gate, of dt; each may be NULL
+ *   dpost, dpre, dscale   [cols] fp32, overwritten; each may be NULL
+ * The workspace (16-byte aligned, size from muon_block_norm_backward_workspace_bytes) is needed with any of the last three.
+ * Sums run in a fixed order.
+ */
+typedef struct {
+    const void* dy; int64_t lddy;
+    const void* dh; int64_t lddh;
+    const void* x; const void* x_scale; int64_t ldx;
+    const void* h; const void* h_scale; int64_t ldh;
+    const void* gate; const void* gate_scale; int64_t ldg;
+    const float* rstd_x; const float* rstd_h;
+    const void* post; const void* scale; const void* pre;
+    void* dx; int64_t lddx;
+    void* dresidual; int64_t lddr;
+    void* dgate; int64_t lddgate;
+    float* dpost; float* dpre; float* dscale;
+    void* ws; int64_t ws_bytes;
+    int64_t rows, cols;
+    int32_t dt, weight_dt, gate_per_row, kept_fmt;
+    float alpha;
+} muon_block_norm_grad_args;
+MUON_API size_t muon_block_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+MUON_API muon_status muon_block_norm_backward(const muon_block_norm_grad_args* args, void* stream);
+
+typedef enum {
+    MUON_SILU = 0,   /* g / (1 + exp(-g)) */
+    MUON_GELU = 1    /* g Phi(g), Phi the normal distribution's function */
+} muon_activation;
+
+/*
+ * muon_gated_activation -- y = f(gate) up for two matrices [rows, cols] of dt, of any row strides (two halves of one product's
+ * output, say).  y may be NULL; q is y in 8 bits of format fmt, gate8 and up8 are copies of kept_fmt for the gradient.  rows
+ * and cols in [0, MUON_MAX_ROWS].
+ */
+typedef struct {
+    const void* gate; int64_t ldg;
+    const void* up; int64_t ldu;
+    void* y; int64_t ldy;
+    muon_fp8_out q, gate8, up8;
+    int64_t rows, cols;
+    int32_t dt, act, fmt, kept_fmt;
+} muon_gated_args;
+MUON_API muon_status muon_gated_activation(const muon_gated_args* args, void* stream);
+
+/*
+ * muon_gated_activation_backward -- its gradient:  dgate = dy up f'(gate)      dup = dy f(gate)
+ *
+ *   gate, up      as the forward pass had them, or with gate_scale and up_scale 8-bit copies of kept_fmt
+ *   dgate, dup    [rows, cols] of dt, each may be NULL
+ *   dgate_rows, dup_rows   the unrounded gradients in 8 bits of format fmt, blocks along their columns
+ *   dgate_cols, dup_cols   and transposed ([cols, rows], blocks along the rows)
+ *   y_cols        f(gate) up again, transposed, in 8 bits of y_fmt
+ * Any of them may be left out, but not all.
+ */
+typedef struct {
+    const void* dy; int64_t lddy;
+    const void* gate; const void* gate_scale; int64_t ldg;
+    const void* up; const void* up_scale; int64_t ldu;
+    void* dgate; int64_t lddgate;
+    void* dup; int64_t lddup;
+    muon_fp8_out dgate_rows, dgate_cols, dup_rows, dup_cols, y_cols;
+    int64_t rows, cols;
+    int32_t dt, act, kept_fmt, fmt, y_fmt;
+} muon_gated_grad_args;
+MUON_API muon_status muon_gated_activation_backward(const muon_gated_grad_args* args, void* stream);
+
+/*
+ * muon_fp8_transpose -- an 8-bit matrix [rows, cols] transposed, with new scales for 128 of its rows, in the same format:
+ * muon_fp8_quantize's rule applied to what the matrix stands for, exactly.  A checkpoint becomes the operand of a
+ * product that sums over its rows.  Only values below the type's normal range at their new scale are rounded.  A block
+ * with an infinity or NaN becomes NaN.
+ */
+MUON_API muon_status muon_fp8_transpose(const void* q, int64_t ldq, const void* q_scale, int64_t rows, int64_t cols,
+                                        muon_fp8 fmt, void* qt, int64_t ldqt, void* qt_scale, void* stream);
+
 /* Thread-local message of the last failed call on this thread ("" if none). */
 MUON_API const char* muon_last_error(void);
 

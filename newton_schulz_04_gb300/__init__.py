@@ -14,3 +14,7 @@ from .training import (  # noqa: F401
     Fp8Tensor, RmsNormOutput, clip_grads, debug_bounded_wait_fp8, fp8_matmul, fp8_quantize, fp8_status, grad_norm,
     rms_norm, rms_norm_backward,
 )
+from .blocks import (  # noqa: F401
+    BlockNormGrads, BlockNormKept, BlockNormOutput, GatedGrads, GatedKept, GatedOutput, block_norm, block_norm_backward,
+    fp8_transpose, gated_activation, gated_activation_backward,
+)

@@ -121,6 +121,12 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.muon_fp8_status.restype = i32
     lib.muon_debug_bounded_wait_fp8.argtypes = [ctypes.c_longlong, vp]
     lib.muon_debug_bounded_wait_fp8.restype = i32
+    for f in (lib.muon_block_norm, lib.muon_block_norm_backward, lib.muon_gated_activation, lib.muon_gated_activation_backward):
+        f.argtypes, f.restype = [ctypes.c_char_p, vp], i32  # the packed argument struct, the stream
+    lib.muon_block_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.muon_block_norm_backward_workspace_bytes.restype = sz
+    lib.muon_fp8_transpose.argtypes = [vp, i64, vp, i64, i64, i32, vp, i64, vp, vp]
+    lib.muon_fp8_transpose.restype = i32
     lib.muon_last_error.argtypes = []
     lib.muon_last_error.restype = ctypes.c_char_p
     lib.muon_version.argtypes = []

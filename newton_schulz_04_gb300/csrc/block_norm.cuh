@@ -1,0 +1,100 @@
+// block_norm.cuh -- arithmetic shared by the norms around a block and the gated activation.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "fp8.cuh"
+#include "train_ops.h"
+
+namespace muon {
+
+// 1 / (1 + exp(-g)), 0 at -infinity and from about g = -87 on.  fp32 data takes the accurate exponential and quotient;
+// 16-bit data, which is rounded by 2^-11 at best, the hardware's: off by (4 + 1.2 |g|) 2^-23 of the value.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (sizeof(T) == 4) {
+    return 1.f / (1.f + expf(-g));
+  } else {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+    return r;
+  }
+}
+
+// 1 / sqrt(sum / cols + eps), the quotient and the root corrected by a step of Newton's:
+// y goes on to 8 bits, and an error common to a row moves all its values that lie near the middle of two.
+__device__ __forceinline__ float row_rstd(float sum, float cols, float inv_cols, float eps) {
+  const float q = sum * inv_cols;
+  const float m = (isfinite(q) ? fmaf(fmaf(-q, cols, sum), inv_cols, q) : q) + eps;
+  const float r = rsqrtf(m);
+  const float better = fmaf(0.5f * r, fmaf(-(m * r), r, 1.f), r);
+  return isfinite(better) ? better : r;  // of a sum of 0 (without eps), infinity or NaN
+}
+
+// ---- a block of 128 columns to a warp
+// Rows of any alignment: lane l holds columns l, l + 32, l + 64 and l + 96 of a block, so that a warp's accesses are
+// 32 neighbours whatever the row's first address, and a block's largest magnitude is one reduction of the warp.
+template <typename T>
+__device__ __forceinline__ float load_or(const void* p, long long i, bool in, float other) {
+  return in ? to_f32(static_cast<const T*>(p)[i]) : other;
+}
+__device__ __forceinline__ float load_weight(const void* w, int dt, int col, bool in) {
+  if (!w) return 1.f;
+  if (dt == MUON_FP32) return load_or<float>(w, col, in, 0.f);
+  return dt == MUON_BF16 ? load_or<__nv_bfloat16>(w, col, in, 0.f) : load_or<__half>(w, col, in, 0.f);
+}
+
+// Block kb of a row in 8 bits.  All lanes call; v is 0 past the last column.
+__device__ __forceinline__ void store_block8(const muon_fp8_out& o, int fmt, long long row, long long rows, int cols, int kb,
+                                             const float (&v)[4]) {
+  uint8_t* data = static_cast<uint8_t*>(o.data) + row * o.ld;
+  uint8_t* scale = static_cast<uint8_t*>(o.scale);
+  uint32_t m = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = max(m, abs_bits(v[j]));
+  const uint32_t byte = fp8_scale_byte(__reduce_max_sync(0xffffffffu, m), fmt ? 15 : 8);
+  const float inv = fp8_inverse_scale(byte);
+  const int lane = threadIdx.x % 32, end = (cols + 15) & ~15;
+  const uint32_t four = fmt ? fp8_pack4<true>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv)
+                            : fp8_pack4<false>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (kb * 128 + lane + 32 * j < end) data[kb * 128 + lane + 32 * j] = static_cast<uint8_t>(four >> (8 * j));
+  if (lane == 0) {
+    const long long rows4 = (rows + 3) & ~3LL;
+    scale[fp8_scale_offset(kb, row, rows4)] = static_cast<uint8_t>(byte);
+    if (row == rows - 1)
+      for (long long r = rows; r < rows4; ++r) scale[fp8_scale_offset(kb, r, rows4)] = 127;
+  }
+}
+// The scale words' blocks past the last column.
+__device__ __forceinline__ void pad_blocks8(const muon_fp8_out& o, long long row, long long rows, int cols) {
+  uint8_t* scale = static_cast<uint8_t*>(o.scale);
+  const long long rows4 = (rows + 3) & ~3LL;
+  for (int kb = (cols + 127) / 128 + threadIdx.x; kb < (cols + 511) / 512 * 4; kb += blockDim.x) {
+    scale[fp8_scale_offset(kb, row, rows4)] = 127;
+    if (row == rows - 1)
+      for (long long r = rows; r < rows4; ++r) scale[fp8_scale_offset(kb, r, rows4)] = 127;
+  }
+}
+
+
+// A kernel's limit of dynamic shared memory, raised once per device.
+template <typename F>
+inline cudaError_t smem_limit(F kernel, int bytes, bool (&done)[64]) {
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace muon

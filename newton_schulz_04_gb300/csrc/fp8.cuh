@@ -53,6 +53,21 @@ __device__ __forceinline__ uint2 fp8_pack8(const float (&v)[8], float inv) {
   return make_uint2(fp8_pack4<E5M2>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                     fp8_pack4<E5M2>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
+// What a scale byte stands for: 2^(b - 127), NaN for 255 (2^-127 is subnormal).
+__device__ __forceinline__ float fp8_scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fffffffu : byte == 0u ? 0x400000u : byte << 23);
+}
+// Two 8-bit values as fp32, exactly; the first is the low byte.  (e5m2 is fp16 without its last 8 bits.)
+template <bool E5M2>
+__device__ __forceinline__ float2 fp8_unpack2(uint32_t two) {
+  uint32_t h;
+  if (E5M2) h = __byte_perm(two, 0u, 0x1404);
+  else asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(two)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float2 fp8_unpack2(uint32_t two, int fmt) {
+  return fmt ? fp8_unpack2<true>(two) : fp8_unpack2<false>(two);
+}
 // Byte offset of the scale of block kb of row r; rows4 = rows rounded up to 4.
 __host__ __device__ __forceinline__ long long fp8_scale_offset(long long kb, long long r, long long rows4) {
   return ((kb >> 2) * rows4 + r) * 4 + (kb & 3);

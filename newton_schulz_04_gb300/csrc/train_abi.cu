@@ -4,61 +4,15 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <memory>
 #include <new>
 
+#include "abi.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "train_ops.h"
-
-namespace muon {
-
-static bool float_dt(int dt) { return dt == MUON_BF16 || dt == MUON_FP32 || dt == MUON_FP16; }
-static bool fp8_fmt(int f) { return f == MUON_E4M3 || f == MUON_E5M2; }
-static bool misaligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
-static bool aligned16(const void* p, long long ld, int size) { return !misaligned(p, 16) && ld * size % 16 == 0; }
-
-// Bytes spanned by a matrix of `rows` rows of `cols` elements, `ld` apart.
-static long long span(long long rows, long long cols, long long ld, int size) {
-  return rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * size : 0;
-}
-// And by an 8-bit one, whose rows are written up to the next multiple of 16 bytes.
-static long long span8(long long rows, long long cols, long long ld) { return span(rows, (cols + 15) / 16 * 16, ld, 1); }
-static bool overlap(const void* a, long long na, const void* b, long long nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
-}
-
-// The device is an sm_103 GPU: its SM count (asked for once per device), or 0 with *st set.
-static int gpu(muon_status* st) {
-  static std::atomic<int> known[64];
-  int dev = -1;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
-    const int sms = known[dev].load(std::memory_order_relaxed);
-    if (sms) {
-      *st = MUON_OK;
-      return sms;
-    }
-  }
-  int major = 0, minor = 0;
-  const int sms = device_sms(&major, &minor, st);
-  if (*st != MUON_OK) return 0;
-  if (major != 10 || minor != 3) {
-    *st = fail(MUON_ERR_UNSUPPORTED, "this library is built for sm_103a (GB300); device is sm_%d%d", major, minor);
-    return 0;
-  }
-  if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
-  return sms;
-}
-static muon_status launched(cudaError_t e, const char* what, const char* why = nullptr) {
-  if (e == cudaSuccess) return MUON_OK;
-  return fail(MUON_ERR_CUDA, "%s failed: %s%s%s", what, cudaGetErrorString(e), why ? ": " : "", why ? why : "");
-}
-
-}  // namespace muon
 
 using namespace muon;
 
@@ -159,25 +113,6 @@ muon_status muon_clip_grads(const void* const* grads, void* const* out, const in
 }
 
 // ------------------------------------------------------------------ RMS norm
-// One matrix argument: NULL is allowed when `optional`; sets *vec to 0 where 16-byte accesses are not possible.
-static muon_status check_rows(const char* name, const void* p, bool optional, long long rows, long long cols, long long ld,
-                              int size, int* vec) {
-  if (!p) return optional ? MUON_OK : fail(MUON_ERR_ARG, "%s is NULL", name);
-  if (misaligned(p, size)) return fail(MUON_ERR_ALIGN, "%s is not aligned to its element size", name);
-  if (rows > 1 && ld < cols) return fail(MUON_ERR_SHAPE, "%s: row stride %lld < %lld columns", name, ld, cols);
-  if (misaligned(p, 16) || (rows > 1 && ld * size % 16)) *vec = 0;
-  return MUON_OK;
-}
-static muon_status check_fp8_out(const char* name, const void* q, const void* scale, long long rows, long long cols,
-                                 long long ld) {
-  if (!q && !scale) return MUON_OK;
-  if (!q || !scale) return fail(MUON_ERR_ARG, "%s: data and scale go together", name);
-  if (misaligned(q, 16) || misaligned(scale, 16) || ld % 16)
-    return fail(MUON_ERR_ALIGN, "%s: data and scale must be 16-byte aligned, the row stride a multiple of 16", name);
-  if (ld < (cols + 15) / 16 * 16 && rows > 0)
-    return fail(MUON_ERR_SHAPE, "%s: row stride %lld does not hold %lld columns padded to 16", name, ld, cols);
-  return MUON_OK;
-}
 static muon_status check_norm_shape(long long rows, long long cols, int dt, const void* weight, int weight_dt) {
   if (rows < 0 || rows > MUON_MAX_ROWS) return fail(MUON_ERR_SHAPE, "rows=%lld out of [0, %lld]", rows, MUON_MAX_ROWS);
   if (cols < 1 || cols > MUON_MAX_DIM) return fail(MUON_ERR_SHAPE, "cols=%lld out of [1, %d]", cols, MUON_MAX_DIM);
@@ -192,12 +127,6 @@ static bool clash(const void* a, long long lda, const void* b, long long ldb, lo
   if (a == b && (lda == ldb || rows <= 1)) return false;
   return overlap(a, span(rows, cols, lda, size), b, span(rows, cols, ldb, size));
 }
-
-#define TRY(expr)                         \
-  do {                                    \
-    const muon_status st_ = (expr);       \
-    if (st_ != MUON_OK) return st_;       \
-  } while (0)
 
 muon_status muon_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
                           muon_dtype weight_dt, int64_t rows, int64_t cols, float eps, void* y, int64_t ldy, void* h,

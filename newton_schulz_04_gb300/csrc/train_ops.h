@@ -1,5 +1,6 @@
 // train_ops.h -- internal interface of the operators around the update: gradient
-// clipping, the RMS norm, 8-bit quantisation and the 8-bit product.
+// clipping, the RMS norm, 8-bit quantisation and the 8-bit product; the norms around a
+// block, the gated activation and the transposition of 8-bit matrices.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -73,6 +74,27 @@ struct Fp8QuantArgs {
   long long ldq, ldqt;
 };
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, int dt, cudaStream_t st);
+
+// ---- block_norm.cu
+constexpr int kBlockNormCtasPerSm = 2;  // of the gradient kernel at most
+// vec: every row of the matrices allows 16-byte accesses.
+cudaError_t launch_block_norm(const muon_block_norm_args& a, int vec, int sms, cudaStream_t st);
+// CTAs of the gradient kernel, each with two rows of `partial` (or nullptr: no gradients of the weights).
+int block_norm_grad_ctas(long long rows, int sms);
+cudaError_t launch_block_norm_grad(const muon_block_norm_grad_args& a, float* partial, int vec, int sms, cudaStream_t st);
+
+// ---- gated.cu
+cudaError_t launch_gated(const muon_gated_args& a, int vec, cudaStream_t st);
+cudaError_t launch_gated_grad(const muon_gated_grad_args& a, int vec, cudaStream_t st);
+
+// ---- fp8_transpose.cu
+struct Fp8TransposeArgs {
+  const uint8_t *q, *qs;
+  long long ldq, rows, cols;
+  uint8_t *qt, *qts;
+  long long ldqt;
+};
+cudaError_t launch_fp8_transpose(const Fp8TransposeArgs& a, int fmt, cudaStream_t st);
 
 // ---- fp8_gemm.cu
 struct Fp8GemmDesc {
