@@ -2,9 +2,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "fp8.cuh"
+#include "row_ring.cuh"
 #include "train_ops.h"
 
 namespace muon {
@@ -20,16 +19,6 @@ __device__ __forceinline__ float sigmoid(float g) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
     return r;
   }
-}
-
-// 1 / sqrt(sum / cols + eps), the quotient and the root corrected by a step of Newton's:
-// y goes on to 8 bits, and an error common to a row moves all its values that lie near the middle of two.
-__device__ __forceinline__ float row_rstd(float sum, float cols, float inv_cols, float eps) {
-  const float q = sum * inv_cols;
-  const float m = (isfinite(q) ? fmaf(fmaf(-q, cols, sum), inv_cols, q) : q) + eps;
-  const float r = rsqrtf(m);
-  const float better = fmaf(0.5f * r, fmaf(-(m * r), r, 1.f), r);
-  return isfinite(better) ? better : r;  // of a sum of 0 (without eps), infinity or NaN
 }
 
 // ---- a block of 128 columns to a warp
@@ -79,22 +68,5 @@ __device__ __forceinline__ void pad_blocks8(const muon_fp8_out& o, long long row
   }
 }
 
-
-// A kernel's limit of dynamic shared memory, raised once per device.
-template <typename F>
-inline cudaError_t smem_limit(F kernel, int bytes, bool (&done)[64]) {
-  static std::mutex mu;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lk(mu);
-  if (!done[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    done[dev] = true;
-  }
-  return cudaSuccess;
-}
 
 }  // namespace muon
