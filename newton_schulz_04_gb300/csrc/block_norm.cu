@@ -1,18 +1,10 @@
-// block_norm.cu -- the norms behind a block and before the next one, with the block's gate and scale between
-// them, and their gradient.
+// block_norm.cu -- the norms behind a block and before the next one, with the block's gate and scale between them.
 //
 //   rho_x = 1 / sqrt(mean_j x_j^2 + eps)       h = alpha residual + sigmoid(gate) scale post (x rho_x)
 //   rho_h = 1 / sqrt(mean_j h_j^2 + eps)       y = h rho_h pre
 //
 // Everything goes on in fp32 from unrounded values; y, h, the 8-bit y and the 8-bit copies of x, h and gate are each
-// rounded once.  The gradient, with X = x rho_x and H = h rho_h as kept and c = scale post:
-//
-//   a = dy pre       D = dh + rho_h (a - H mean(a H))       dresidual = alpha D
-//   b = D sigmoid(gate) c       dx = rho_x (b - X mean(b X))       dgate = (1 - sigmoid(gate)) b X
-//   dpre = sum_rows dy H       S = sum_rows D sigmoid(gate) X       dpost = S scale       dscale = S post
-//
-// mean(b X) needs mean(a H) first.  With u = dh + rho_h a and e = sigmoid(gate) c X it is mean(u e) - rho_h mean(a H)
-// mean(H e), so a row takes one pass and one exchange of three sums.
+// rounded once.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,27 +14,6 @@
 #include "ptx.cuh"
 
 namespace muon {
-
-// ------------------------------------------------------------------ a block of 128 columns to a warp
-// Sums over a CTA of W warps; every thread gets them.  `sh` alternates between two buffers: one barrier each.
-template <int W, int N>
-__device__ __forceinline__ void cta_sums(float (&v)[N], float (*sh)[N][W], int turn) {
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-  if (threadIdx.x % 32 == 0) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) sh[turn & 1][n][threadIdx.x / 32] = v[n];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    v[n] = sh[turn & 1][n][threadIdx.x % W];
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-  }
-}
 
 // W warps to a row, K blocks to a warp; K = 0: any number, computed from memory again in each phase.
 template <typename T, int W, int K>
@@ -129,6 +100,214 @@ __global__ void __launch_bounds__(W * 32) block_norm_kernel(const muon_block_nor
   if (a.gate8.data) pad_blocks8(a.gate8, row, a.rows, cols);
 }
 
+// ------------------------------------------------------------------ ring of rows
+// Largest magnitude of a piece as the upper 16 bits of its fp32 bits, rounded up.  A scale byte is the exponent field of
+// bits + 0x1fffff, whose only border within a binade (0x600000) is a multiple of 2^16: it comes out the same.
+template <int E>
+__device__ __forceinline__ uint32_t piece_max(const float (&v)[E]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < E; ++i) m = max(m, abs_bits(v[i]));
+  return (m + 0xffffu) >> 16;
+}
+// A row's 8-bit copies: a block of 128 columns lies in 128 / E neighbouring lanes, two matrices share one exchange.
+template <int E>
+struct Row8 {
+  long long row, rows, rows4;
+  int cols, blocks;
+  bool live;
+  __device__ __forceinline__ void store(const muon_fp8_out& o, int fmt, int col, uint32_t amax, const float (&v)[E]) const {
+    const uint32_t byte = fp8_scale_byte(amax, fmt ? 15 : 8);
+    const float inv = fp8_inverse_scale(byte);
+    if (!live) return;
+    if (col < ((cols + 15) & ~15)) {
+      uint8_t* p = static_cast<uint8_t*>(o.data) + row * o.ld + col;
+      if constexpr (E == 8) {
+        *reinterpret_cast<uint2*>(p) = fmt ? fp8_pack8<true>(v, inv) : fp8_pack8<false>(v, inv);
+      } else {
+        *reinterpret_cast<uint32_t*>(p) = fmt ? fp8_pack4<true>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv)
+                                              : fp8_pack4<false>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+      }
+    }
+    const int kb = col / 128;
+    if (col % 128 == 0 && kb < blocks) scale(o, kb, byte);
+  }
+  __device__ __forceinline__ void scale(const muon_fp8_out& o, int kb, uint32_t byte) const {
+    uint8_t* p = static_cast<uint8_t*>(o.scale) + fp8_scale_offset(kb, row, rows4);
+    *p = static_cast<uint8_t>(byte);
+    if (row == rows - 1)  // scales of no row are 1
+      for (long long r = rows; r < rows4; ++r) p[(r - rows + 1) * 4] = 127;
+  }
+  // Pieces of two matrices, each stored where it is asked for; all lanes call.
+  __device__ __forceinline__ void two(const muon_fp8_out& a, int fa, const float (&va)[E], const muon_fp8_out& b, int fb,
+                                      const float (&vb)[E], int col) const {
+    if (!a.data && !b.data) return;
+    uint32_t m = piece_max(va) | piece_max(vb) << 16;
+#pragma unroll
+    for (int o = 64 / E; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (a.data) store(a, fa, col, m << 16, va);
+    if (b.data) store(b, fb, col, m & 0xffff0000u, vb);
+  }
+};
+
+// CL CTAs of a cluster to a row, G threads of each, C pieces of 16 bytes to a thread, a ring of S rows.
+template <typename T, int G, int C, int S, int MINB, int CL>
+__global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kernel(const muon_block_norm_args a) {
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G, E = 16 / static_cast<int>(sizeof(T));
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ RowSums<G, TH, 1, CL> sums;
+  const Ring<T, TH, C, S, 3> ring{ring_smem};
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
+  int n[C], col[C], off[C];  // existing columns of each piece, its first, and the same where one exists
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    col[c] = ((rank * C + c) * G + t) * E;
+    n[c] = max(0, min(E, cols - col[c]));
+    off[c] = n[c] ? col[c] : 0;
+  }
+  const bool element = a.gate && !a.gate_per_row;
+  const long long step = static_cast<long long>(gridDim.x / CL) * R, row0 = static_cast<long long>(blockIdx.x / CL) * R + rr;
+  long long frow = row0;  // next row to fetch
+  auto fetch = [&](int slot) {
+    if (frow < a.rows) {
+      const T* fx = static_cast<const T*>(a.x) + frow * a.ldx;
+      const T* fr = static_cast<const T*>(a.residual) + frow * a.ldr;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int bytes = n[c] * static_cast<int>(sizeof(T));
+        ring.fetch(slot, 0, c, fx + off[c], bytes);
+        ring.fetch(slot, 1, c, fr + off[c], bytes);
+        if (element) ring.fetch(slot, 2, c, static_cast<const T*>(a.gate) + frow * a.ldg + off[c], bytes);
+      }
+    }
+    cp_async_commit();
+    frow += step;
+  };
+  if (CL > 1) cluster_sync();  // the others' shared memory is there
+  pdl_wait();
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(s);
+  float w1[C][E], w2[C][E];  // scale post, pre
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    load_weight_piece<E>(a.scale, a.weight_dt, off[c], n[c], w2[c]);
+    load_weight_piece<E>(a.post, a.weight_dt, off[c], n[c], w1[c]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) w1[c][i] *= w2[c][i];
+    load_weight_piece<E>(a.pre, a.weight_dt, off[c], n[c], w2[c]);
+  }
+  const auto row_gate = [&](long long row) {
+    return a.gate && !element && row < a.rows ? to_f32(static_cast<const T*>(a.gate)[row * a.ldg]) : 0.f;
+  };
+  float next_gate = row_gate(row0);  // a row ahead
+  const float fcols = static_cast<float>(cols), inv_cols = 1.f / fcols;
+  Row8<E> out{row0, a.rows, (a.rows + 3) & ~3LL, cols, (cols + 127) / 128, true};
+  int slot = 0, turn = 0;
+  // all threads of a CTA take the same number of turns (the barriers of the sums)
+  for (long long row = row0; row - rr < a.rows; row += step, turn += 2) {
+    const bool live = R == 1 || row < a.rows;
+    if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row: earlier, the next kernel's CTAs take SMs from these
+    const float row_sig = a.gate && !element ? sigmoid<T>(next_gate) : 1.f;
+    next_gate = row_gate(row + step);
+    fetch(slot == 0 ? S - 1 : slot - 1);
+    cp_async_wait<S - 1>();
+    float h[C][E], sum[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float x[E];
+      ring.read(slot, 0, c, x);
+#pragma unroll
+      for (int i = 0; i < E; ++i) sum[0] = fmaf(x[i], x[i], sum[0]);
+    }
+    sums(sum, turn);
+    const float rx = row_rstd(sum[0], fcols, inv_cols, a.eps);
+    sum[0] = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float x[E], g[E];
+      ring.read(slot, 0, c, x);
+      ring.read(slot, 1, c, h[c]);
+      if (element) ring.read(slot, 2, c, g);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float b = x[i] * rx * w1[c][i] * (element ? sigmoid<T>(g[i]) : row_sig);
+        h[c][i] = fmaf(a.alpha, h[c][i], b);
+        sum[0] = fmaf(h[c][i], h[c][i], sum[0]);
+      }
+    }
+    sums(sum, turn + 1);
+    const float rh = row_rstd(sum[0], fcols, inv_cols, a.eps);
+    if (live && t == 0 && rank == 0) {
+      if (a.rstd_x) a.rstd_x[row] = rx;
+      if (a.rstd_h) a.rstd_h[row] = rh;
+    }
+    out.row = row, out.live = live;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float y[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const bool in = n[c] == E || i < n[c];
+        y[i] = in ? h[c][i] * rh * w2[c][i] : 0.f;
+        h[c][i] = in ? h[c][i] : 0.f;
+      }
+      if (live && a.h) store_piece(static_cast<T*>(a.h) + row * a.ldh + off[c], n[c], h[c]);
+      if (live && a.y) store_piece(static_cast<T*>(a.y) + row * a.ldy + off[c], n[c], y);
+      out.two(a.q, a.fmt, y, a.h8, a.kept_fmt, h[c], col[c]);
+      if (a.x8.data || a.gate8.data) {
+        ring.read(slot, 0, c, y);
+        if (element) ring.read(slot, 2, c, h[c]);
+        out.two(a.x8, a.kept_fmt, y, a.gate8, a.kept_fmt, h[c], col[c]);
+      }
+    }
+    // blocks past the last column, up to a whole scale word
+    if (rank == 0 && live && t < (cols + 511) / 512 * 4 - out.blocks) {
+      const int kb = out.blocks + t;
+      if (a.q.data) out.scale(a.q, kb, 127u);
+      if (a.x8.data) out.scale(a.x8, kb, 127u);
+      if (a.h8.data) out.scale(a.h8, kb, 127u);
+      if (a.gate8.data) out.scale(a.gate8, kb, 127u);
+    }
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+}
+
+template <typename T, int G, int C, int S, int MINB, int CL>
+static cudaError_t launch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
+  constexpr int smem = Ring<T, TH, C, S, 3>::BYTES;
+  static_assert(smem * MINB <= 220 * 1024, "shared memory of an SM");
+  static bool done[64] = {false};
+  static int known[64] = {0};
+  const auto kernel = block_norm_ring_kernel<T, G, C, S, MINB, CL>;
+  cudaError_t e = smem_limit(kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  int most = MINB * sms;
+  if (CL > 1) {
+    e = resident_clusters(kernel, TH, smem, CL, known, &most);
+    if (e != cudaSuccess) return e;
+  }
+  const long long want = (a.rows + R - 1) / R;
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(std::min<long long>(want, most)) * CL), dim3(TH), smem, CL, st, a);
+}
+
+// Threads, pieces and CTAs of a row by its width.
+template <typename T>
+static cudaError_t dispatch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const int pieces = static_cast<int>((a.cols + E - 1) / E);
+  if (pieces <= 32) return launch_ring<T, 32, 1, 6, 5, 1>(a, sms, st);
+  if (pieces <= 64) return launch_ring<T, 64, 1, 4, 8, 1>(a, sms, st);
+  if (pieces <= 128) return launch_ring<T, 64, 2, 3, 5, 1>(a, sms, st);
+  if (pieces <= 256) return launch_ring<T, 256, 1, 4, 4, 1>(a, sms, st);
+  if (pieces <= 512) return launch_ring<T, 256, 2, 4, 2, 1>(a, sms, st);
+  if (pieces <= 1024) return launch_ring<T, 512, 2, 4, 1, 1>(a, sms, st);
+  if (pieces <= 2048) return launch_ring<T, 512, 2, 4, 1, 2>(a, sms, st);
+  if (pieces <= 4096) return launch_ring<T, 512, 2, 4, 1, 4>(a, sms, st);
+  return launch_ring<T, 512, 2, 4, 1, 8>(a, sms, st);
+}
+
 template <typename T>
 static cudaError_t dispatch_norm(const muon_block_norm_args& a, cudaStream_t st) {
   const auto go = [&](auto kernel, int warps) {
@@ -142,176 +321,13 @@ static cudaError_t dispatch_norm(const muon_block_norm_args& a, cudaStream_t st)
 }
 
 cudaError_t launch_block_norm(const muon_block_norm_args& a, int vec, int sms, cudaStream_t st) {
-  if (a.dt == MUON_BF16) return dispatch_norm<__nv_bfloat16>(a, st);
-  if (a.dt == MUON_FP16) return dispatch_norm<__half>(a, st);
-  return dispatch_norm<float>(a, st);
-}
-
-// ------------------------------------------------------------------ gradient
-// A kept matrix: T, or 8 bits.
-template <typename T, bool KEPT8>
-struct Kept {
-  const uint8_t* data;
-  const uint8_t* scale;  // this row's first scale
-  long long rows4;
-  int fmt;
-  __device__ __forceinline__ Kept(const void* p, const void* s, long long ld, long long row, long long rows, int fmt_)
-      : data(static_cast<const uint8_t*>(p) + (p ? row * ld * (KEPT8 ? 1 : static_cast<long long>(sizeof(T))) : 0)),
-        scale(static_cast<const uint8_t*>(s) + (KEPT8 && p ? row * 4 : 0)),
-        rows4((rows + 3) & ~3LL),
-        fmt(fmt_) {}
-  __device__ __forceinline__ float block_scale(int kb) const {
-    return KEPT8 ? fp8_scale_value(scale[(kb >> 2) * rows4 * 4 + (kb & 3)]) : 1.f;
-  }
-  __device__ __forceinline__ float at(int col, float block) const {
-    if constexpr (KEPT8) return fp8_unpack2(data[col], fmt).x * block;
-    else return to_f32(reinterpret_cast<const T*>(data)[col]);
-  }
-};
-
-template <typename T, int W, int K, bool KEPT8>
-__global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_block_norm_grad_args a, float* partial) {
-  constexpr int KK = K ? K : 1;
-  __shared__ float sh[2][3][W];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cols = static_cast<int>(a.cols);
-  const int blocks = (cols + 127) / 128, turns = K ? K : (blocks + W - 1) / W;
-  float* part = partial ? partial + static_cast<long long>(blockIdx.x) * 2 * cols : nullptr;
-  float dpre[KK][4], sx[KK][4];
-#pragma unroll
-  for (int k = 0; k < KK; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dpre[k][j] = sx[k][j] = 0.f;
-  const float inv_n = 1.f / static_cast<float>(cols);
-  int turn = 0;
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
-    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
-    const T* dh = static_cast<const T*>(a.dh) + (a.dh ? row * a.lddh : 0);
-    const Kept<T, KEPT8> kx(a.x, a.x_scale, a.ldx, row, a.rows, a.kept_fmt), kh(a.h, a.h_scale, a.ldh, row, a.rows, a.kept_fmt);
-    const bool element = a.gate && !a.gate_per_row;
-    const Kept<T, KEPT8> kg(element ? a.gate : nullptr, a.gate_scale, a.ldg, row, a.rows, a.kept_fmt);
-    const float rx = a.rstd_x[row], rh = a.rstd_h[row];
-    const float row_sig = a.gate && !element ? sigmoid<T>(to_f32(static_cast<const T*>(a.gate)[row * a.ldg])) : 1.f;
-    struct Element {
-      float d, u, hn, xn, sig, c;  // dy, dh + rho_h dy pre, H, X, sigmoid(gate), scale post
-    };
-    auto load = [&](int col, float xs, float hs, float gs) {
-      Element e;
-      e.d = to_f32(dy[col]);
-      e.hn = kh.at(col, hs) * rh;
-      e.xn = kx.at(col, xs) * rx;
-      e.sig = element ? sigmoid<T>(kg.at(col, gs)) : row_sig;
-      e.c = load_weight(a.post, a.weight_dt, col, true) * load_weight(a.scale, a.weight_dt, col, true);
-      e.u = fmaf(rh, e.d * load_weight(a.pre, a.weight_dt, col, true), a.dh ? to_f32(dh[col]) : 0.f);
-      return e;
-    };
-    float sum[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < turns; ++k) {
-      const int kb = warp + W * k;
-      if (kb >= blocks) break;
-      const float xs = kx.block_scale(kb), hs = kh.block_scale(kb), gs = element ? kg.block_scale(kb) : 1.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = kb * 128 + lane + 32 * j;
-        if (col >= cols) break;
-        const Element e = load(col, xs, hs, gs);
-        const float f = e.sig * e.c * e.xn;
-        sum[0] = fmaf(e.d * load_weight(a.pre, a.weight_dt, col, true), e.hn, sum[0]);
-        sum[1] = fmaf(e.u, f, sum[1]);
-        sum[2] = fmaf(e.hn, f, sum[2]);
-      }
-    }
-    cta_sums<W, 3>(sum, sh, turn);
-    const float k1 = sum[0] * inv_n * rh, along = sum[1] - k1 * sum[2], k2 = along * inv_n;
-    if (threadIdx.x == 0 && a.dgate && !element) static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>((1.f - row_sig) * along);
-#pragma unroll
-    for (int k = 0; k < turns; ++k) {
-      const int kb = warp + W * k, kk = K ? k : 0;
-      if (kb >= blocks) break;
-      const float xs = kx.block_scale(kb), hs = kh.block_scale(kb), gs = element ? kg.block_scale(kb) : 1.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = kb * 128 + lane + 32 * j;
-        if (col >= cols) break;
-        const Element e = load(col, xs, hs, gs);
-        const float d = e.u - k1 * e.hn, t = d * e.sig, b = t * e.c;
-        if (a.dresidual) static_cast<T*>(a.dresidual)[row * a.lddr + col] = from_f32<T>(a.alpha * d);
-        if (a.dx) static_cast<T*>(a.dx)[row * a.lddx + col] = from_f32<T>(rx * (b - e.xn * k2));
-        if (a.dgate && element) static_cast<T*>(a.dgate)[row * a.lddgate + col] = from_f32<T>((1.f - e.sig) * (b * e.xn));
-        if (K) {
-          dpre[kk][j] = fmaf(e.d, e.hn, dpre[kk][j]);
-          sx[kk][j] = fmaf(t, e.xn, sx[kk][j]);
-        } else if (part) {  // this thread alone holds these columns of the CTA's sums
-          part[col] = (turn ? part[col] : 0.f) + e.d * e.hn;
-          part[cols + col] = (turn ? part[cols + col] : 0.f) + t * e.xn;
-        }
-      }
-    }
-  }
-  if (!K || !part) return;
-#pragma unroll
-  for (int k = 0; k < KK; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = (warp + W * k) * 128 + lane + 32 * j;
-      if (col < cols) part[col] = dpre[k][j], part[cols + col] = sx[k][j];
-    }
-}
-
-// Sums over the CTAs' rows in a fixed order, 32 columns by 32 row groups per CTA; blockIdx.y 0: dpre, 1: dpost and dscale.
-__global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float* partial, int ctas,
-                                                                  const muon_block_norm_grad_args a) {
-  __shared__ float sh[32][33];
-  pdl_wait();
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, cols = static_cast<int>(a.cols);
-  int col = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (col < cols) {
-#pragma unroll 4
-    for (int r = g; r < ctas; r += 32) s += partial[(static_cast<long long>(r) * 2 + blockIdx.y) * cols + col];
-  }
-  sh[g][lane] = s;
-  __syncthreads();
-  pdl_launch_dependents();  // not before: a persistent grid that starts beside these CTAs finds no room for all of its own
-  s = sh[lane][g];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  col = blockIdx.x * 32 + g;
-  if (lane != 0 || col >= cols) return;
-  if (blockIdx.y == 0) {
-    if (a.dpre) a.dpre[col] = s;
-  } else {
-    if (a.dpost) a.dpost[col] = s * load_weight(a.scale, a.weight_dt, col, true);
-    if (a.dscale) a.dscale[col] = s * load_weight(a.post, a.weight_dt, col, true);
-  }
-}
-
-int block_norm_grad_ctas(long long rows, int sms) {
-  return static_cast<int>(std::max(1LL, std::min<long long>(rows, static_cast<long long>(kBlockNormCtasPerSm) * sms)));
-}
-
-template <typename T, bool KEPT8>
-static cudaError_t dispatch_grad(const muon_block_norm_grad_args& a, float* partial, int ctas, cudaStream_t st) {
-  const auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, dim3(ctas), dim3(warps * 32), 0, st, a, partial); };
-  if (a.cols <= 512) return go(block_norm_grad_kernel<T, 4, 1, KEPT8>, 4);
-  if (a.cols <= 2048) return go(block_norm_grad_kernel<T, 8, 2, KEPT8>, 8);
-  if (a.cols <= 4096) return go(block_norm_grad_kernel<T, 16, 2, KEPT8>, 16);
-  if (a.cols <= 16384) return go(block_norm_grad_kernel<T, 16, 8, KEPT8>, 16);
-  return go(block_norm_grad_kernel<T, 16, 0, KEPT8>, 16);
-}
-
-cudaError_t launch_block_norm_grad(const muon_block_norm_grad_args& a, float* partial, int vec, int sms, cudaStream_t st) {
-  const int ctas = block_norm_grad_ctas(a.rows, sms);
   const auto go = [&](auto t) {
     using T = decltype(t);
-    return a.x_scale ? dispatch_grad<T, true>(a, partial, ctas, st) : dispatch_grad<T, false>(a, partial, ctas, st);
+    // 8 CTAs of 1024 pieces hold MUON_MAX_DIM 16-bit columns and half as many of fp32
+    const bool ring = vec && a.cols <= 8 * 1024 * (16 / static_cast<int>(sizeof(T)));
+    return ring ? dispatch_ring<T>(a, sms, st) : dispatch_norm<T>(a, st);
   };
-  const cudaError_t e = a.dt == MUON_BF16 ? go(__nv_bfloat16()) : a.dt == MUON_FP16 ? go(__half()) : go(float());
-  if (e != cudaSuccess || !partial) return e;
-  return launch_pdl(block_norm_weights_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), dim3(1024), 0, st,
-                    static_cast<const float*>(partial), ctas, a);
+  return a.dt == MUON_BF16 ? go(__nv_bfloat16()) : a.dt == MUON_FP16 ? go(__half()) : go(float());
 }
 
 }  // namespace muon

@@ -69,4 +69,24 @@ __device__ __forceinline__ void pad_blocks8(const muon_fp8_out& o, long long row
 }
 
 
+// Sums over a CTA of W warps; every thread gets them.  `sh` alternates between two buffers: one barrier each.
+template <int W, int N>
+__device__ __forceinline__ void cta_sums(float (&v)[N], float (*sh)[N][W], int turn) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  if (threadIdx.x % 32 == 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) sh[turn & 1][n][threadIdx.x / 32] = v[n];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    v[n] = sh[turn & 1][n][threadIdx.x % W];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  }
+}
+
 }  // namespace muon

@@ -127,4 +127,79 @@ inline cudaError_t smem_limit(F kernel, int bytes, bool (&done)[64]) {
   return cudaSuccess;
 }
 
+// Sums over the threads of a row, N at once: G threads of each of the CL CTAs of a cluster (CL = 1: of a CTA that holds
+// TH / G rows).  One barrier; `sh` alternates between two buffers.
+template <int G, int TH, int N, int CL>
+struct RowSums {
+  static constexpr int WARPS = TH / 32, W = G / 32;
+  float v[2][N][CL * WARPS];
+  __device__ __forceinline__ void operator()(float (&s)[N], int turn) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
+    if (G == 32 && CL == 1) return;
+    float(&b)[N][CL * WARPS] = v[turn & 1];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if constexpr (CL == 1) {
+      if (lane == 0) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) b[n][warp] = s[n];
+      }
+      __syncthreads();
+      const int at = (threadIdx.x / G) * W + (threadIdx.x & (W - 1));
+#pragma unroll
+      for (int n = 0; n < N; ++n) {  // as a tree: each of the last additions rounds the whole
+        s[n] = b[n][at];
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
+      }
+    } else {
+      static_assert(CL == 1 || (G == TH && (CL * WARPS) % 32 == 0), "rows of whole CTAs");
+      if (lane < CL) {  // a lane to a CTA of the cluster
+        const uint32_t rank = cluster_ctarank();
+#pragma unroll
+        for (int n = 0; n < N; ++n) st_shared_cluster(mapa_cluster(&b[n][rank * WARPS + warp], lane), __float_as_int(s[n]));
+      }
+      __syncwarp();
+      cluster_sync();
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float f = b[n][lane];
+#pragma unroll
+        for (int k = 32; k < CL * WARPS; k += 32) f += b[n][k + lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+        s[n] = f;
+      }
+    }
+  }
+};
+
+// Clusters of a kernel that run at the same time, asked for once per device (0: not asked yet).
+template <typename F>
+inline cudaError_t resident_clusters(F kernel, int threads, int smem, int cluster, int (&known)[64], int* count) {
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!known[dev]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr, cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    known[dev] = n;
+  }
+  *count = known[dev];
+  return cudaSuccess;
+}
+
 }  // namespace muon
