@@ -129,6 +129,231 @@ __global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_bloc
     }
 }
 
+// ------------------------------------------------------------------ ring of rows
+// E values of a kept 8-bit matrix, E bytes of shared memory.
+template <int E>
+__device__ __forceinline__ void read8(const uint8_t* p, int fmt, float (&v)[E]) {
+  uint32_t w[E / 4];
+  if constexpr (E == 8) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+#pragma unroll
+  for (int q = 0; q < E / 2; ++q) {
+    const float2 f = fp8_unpack2(w[q / 2] >> (16 * (q & 1)), fmt);
+    v[2 * q] = f.x, v[2 * q + 1] = f.y;
+  }
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int bytes) {  // the rest is zero
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "n"(BYTES), "r"(bytes)
+               : "memory");
+}
+
+// A thread's slots: S rows of dy, dh, x, h and gate, C pieces each; kept 8-bit ones take E bytes a piece instead of 16.
+template <typename T, int TH, int C, int S, bool KEPT8>
+struct GradRing {
+  static constexpr int E = 16 / static_cast<int>(sizeof(T)), WIDE = KEPT8 ? 2 : 5;
+  static constexpr int STAGE = TH * C * (WIDE * 16 + (5 - WIDE) * E), BYTES = S * STAGE;
+  uint8_t* base;
+  __device__ __forceinline__ uint8_t* at(int slot, int arr, int c) const {
+    uint8_t* stage = base + slot * STAGE;
+    if (arr < WIDE) return stage + ((arr * C + c) * TH + static_cast<int>(threadIdx.x)) * 16;
+    return stage + WIDE * C * TH * 16 + (((arr - WIDE) * C + c) * TH + static_cast<int>(threadIdx.x)) * E;
+  }
+  // n of the piece's elements exist.
+  __device__ __forceinline__ void fetch(int slot, int arr, int c, const void* row, int off, int n) const {
+    if (arr < WIDE) copy16(smem_u32(at(slot, arr, c)), static_cast<const T*>(row) + off, n * static_cast<int>(sizeof(T)));
+    else copy_small<E>(smem_u32(at(slot, arr, c)), static_cast<const uint8_t*>(row) + off, n);
+  }
+  __device__ __forceinline__ void read(int slot, int arr, int c, int fmt, float (&v)[E]) const {
+    if (arr < WIDE) unpack_piece<T>(*reinterpret_cast<const uint4*>(at(slot, arr, c)), v);
+    else read8<E>(at(slot, arr, c), fmt, v);
+  }
+};
+
+template <typename T, int G, int C, int S, int MINB, int CL, bool KEPT8>
+__global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
+    block_norm_grad_ring_kernel(const muon_block_norm_grad_args a, float* partial) {
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G, E = 16 / static_cast<int>(sizeof(T));
+  constexpr int DY = 0, DH = 1, X = 2, H = 3, GATE = 4;
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ RowSums<G, TH, 3, CL> sums;
+  const GradRing<T, TH, C, S, KEPT8> ring{ring_smem};
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
+  int n[C], off[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = ((rank * C + c) * G + t) * E;
+    n[c] = max(0, min(E, cols - col));
+    off[c] = n[c] ? col : 0;
+  }
+  const bool element = a.gate && !a.gate_per_row;
+  const long long step = static_cast<long long>(gridDim.x / CL) * R, row0 = static_cast<long long>(blockIdx.x / CL) * R + rr;
+  const long long rows4 = (a.rows + 3) & ~3LL;
+  long long frow = row0;  // next row to fetch
+  auto fetch = [&](int slot) {
+    if (frow < a.rows) {
+      constexpr int kept = KEPT8 ? 1 : static_cast<int>(sizeof(T));
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        ring.fetch(slot, DY, c, static_cast<const T*>(a.dy) + frow * a.lddy, off[c], n[c]);
+        if (a.dh) ring.fetch(slot, DH, c, static_cast<const T*>(a.dh) + frow * a.lddh, off[c], n[c]);
+        ring.fetch(slot, X, c, static_cast<const uint8_t*>(a.x) + frow * a.ldx * kept, off[c], n[c]);
+        ring.fetch(slot, H, c, static_cast<const uint8_t*>(a.h) + frow * a.ldh * kept, off[c], n[c]);
+        if (element) ring.fetch(slot, GATE, c, static_cast<const uint8_t*>(a.gate) + frow * a.ldg * kept, off[c], n[c]);
+      }
+    }
+    cp_async_commit();
+    frow += step;
+  };
+  if (CL > 1) cluster_sync();  // the others' shared memory is there
+  pdl_wait();
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(s);
+  float w1[C][E], w2[C][E], dpre[C][E], sx[C][E];  // scale post, pre, and the columns' sums
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    load_weight_piece<E>(a.scale, a.weight_dt, off[c], n[c], w2[c]);
+    load_weight_piece<E>(a.post, a.weight_dt, off[c], n[c], w1[c]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) w1[c][i] *= w2[c][i], dpre[c][i] = sx[c][i] = 0.f;
+    load_weight_piece<E>(a.pre, a.weight_dt, off[c], n[c], w2[c]);
+  }
+  // of a row: the norms' factors, its gate, the scales of the kept pieces; fetched a row ahead
+  struct RowHead {
+    float rx, rh, gate;
+    uint32_t xs[C], hs[C], gs[C];
+  };
+  const auto head = [&](long long row) {
+    RowHead r = {};
+    if (row < a.rows) {
+      r.rx = __ldg(a.rstd_x + row);
+      r.rh = __ldg(a.rstd_h + row);
+      if (a.gate && !element) r.gate = to_f32(static_cast<const T*>(a.gate)[row * a.ldg]);
+      if (KEPT8) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const long long o = fp8_scale_offset(off[c] / 128, row, rows4);
+          r.xs[c] = __ldg(static_cast<const uint8_t*>(a.x_scale) + o);
+          r.hs[c] = __ldg(static_cast<const uint8_t*>(a.h_scale) + o);
+          if (element) r.gs[c] = __ldg(static_cast<const uint8_t*>(a.gate_scale) + o);
+        }
+      }
+    }
+    return r;
+  };
+  RowHead next = head(row0);
+  const float inv_cols = 1.f / static_cast<float>(cols);
+  int slot = 0, turn = 0;
+  for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
+    const bool live = R == 1 || row < a.rows;
+    if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row, as in the forward kernel
+    const RowHead now = next;
+    next = head(row + step);
+    const float row_sig = a.gate && !element ? sigmoid<T>(now.gate) : 1.f;
+    fetch(slot == 0 ? S - 1 : slot - 1);
+    cp_async_wait<S - 1>();
+    float u[C][E], sig[C][E], sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float d[E], x[E], h[E];
+      ring.read(slot, DY, c, a.kept_fmt, d);
+      ring.read(slot, X, c, a.kept_fmt, x);
+      ring.read(slot, H, c, a.kept_fmt, h);
+      if (a.dh) {
+        ring.read(slot, DH, c, a.kept_fmt, u[c]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[c][i] = 0.f;
+      }
+      if (element) ring.read(slot, GATE, c, a.kept_fmt, sig[c]);
+      const float xf = KEPT8 ? now.rx * fp8_scale_value(now.xs[c]) : now.rx, hf = KEPT8 ? now.rh * fp8_scale_value(now.hs[c]) : now.rh;
+      const float gf = KEPT8 ? fp8_scale_value(now.gs[c]) : 1.f;
+      if (R > 1 && !live) {  // the slot holds another row's remains
+#pragma unroll
+        for (int i = 0; i < E; ++i) d[i] = x[i] = h[i] = u[c][i] = sig[c][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float hn = h[i] * hf, ad = d[i] * w2[c][i];
+        u[c][i] = fmaf(now.rh, ad, u[c][i]);
+        sig[c][i] = element ? sigmoid<T>(sig[c][i] * gf) : row_sig;
+        const float e = sig[c][i] * w1[c][i] * (x[i] * xf);
+        sum[0] = fmaf(ad, hn, sum[0]);
+        sum[1] = fmaf(u[c][i], e, sum[1]);
+        sum[2] = fmaf(hn, e, sum[2]);
+        dpre[c][i] = fmaf(d[i], hn, dpre[c][i]);
+      }
+    }
+    sums(sum, turn);
+    const float k1 = sum[0] * inv_cols * now.rh, along = sum[1] - k1 * sum[2], k2 = along * inv_cols;
+    if (live && a.dgate && !element && t == 0 && rank == 0)
+      static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>((1.f - row_sig) * along);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float x[E], h[E];
+      ring.read(slot, X, c, a.kept_fmt, x);
+      ring.read(slot, H, c, a.kept_fmt, h);
+      const float xf = KEPT8 ? now.rx * fp8_scale_value(now.xs[c]) : now.rx, hf = KEPT8 ? now.rh * fp8_scale_value(now.hs[c]) : now.rh;
+      if (R > 1 && !live) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = h[i] = 0.f;
+      }
+      float dr[E], dg[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float xn = x[i] * xf, d = u[c][i] - k1 * (h[i] * hf), td = d * sig[c][i], b = td * w1[c][i];
+        sx[c][i] = fmaf(td, xn, sx[c][i]);
+        dr[i] = a.alpha * d;
+        dg[i] = (1.f - sig[c][i]) * (b * xn);
+        x[i] = now.rx * (b - xn * k2);
+      }
+      if (live) {
+        if (a.dresidual) store_piece(static_cast<T*>(a.dresidual) + row * a.lddr + off[c], n[c], dr);
+        if (a.dx) store_piece(static_cast<T*>(a.dx) + row * a.lddx + off[c], n[c], x);
+        if (element && a.dgate) store_piece(static_cast<T*>(a.dgate) + row * a.lddgate + off[c], n[c], dg);
+      }
+    }
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+  if (!partial) return;
+  float* part = partial + static_cast<long long>(blockIdx.x / CL) * 2 * cols;
+  if (R > 1) {  // join the CTA's row groups through the ring's memory
+    static_assert(R == 1 || (R - 1) * 2 * C * E * G * 4 <= GradRing<T, TH, C, S, KEPT8>::BYTES, "room to join");
+    cp_async_wait<0>();
+    __syncthreads();
+    float* all = reinterpret_cast<float*>(ring_smem);  // [R - 1][2][C * E][G]
+    if (rr > 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          all[(((rr - 1) * 2 + 0) * C * E + c * E + i) * G + t] = dpre[c][i];
+          all[(((rr - 1) * 2 + 1) * C * E + c * E + i) * G + t] = sx[c][i];
+        }
+    }
+    __syncthreads();
+    if (rr > 0) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        for (int r = 1; r < R; ++r) {
+          dpre[c][i] += all[(((r - 1) * 2 + 0) * C * E + c * E + i) * G + t];
+          sx[c][i] += all[(((r - 1) * 2 + 1) * C * E + c * E + i) * G + t];
+        }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i < n[c]) part[off[c] + i] = dpre[c][i], part[cols + off[c] + i] = sx[c][i];
+}
+
 // Sums over the CTAs' rows in a fixed order, 32 columns by 32 row groups per CTA; blockIdx.y 0: dpre, 1: dpost and dscale.
 __global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float* partial, int ctas,
                                                                   const muon_block_norm_grad_args a) {
@@ -157,13 +382,16 @@ __global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float* p
   }
 }
 
+// The kernels add up rows of `partial` for at most this many CTAs (or clusters).
+static int most_ctas(int sms) { return kBlockNormCtasPerSm * sms; }
 int block_norm_grad_ctas(long long rows, int sms) {
-  return static_cast<int>(std::max(1LL, std::min<long long>(rows, static_cast<long long>(kBlockNormCtasPerSm) * sms)));
+  return static_cast<int>(std::max(1LL, std::min<long long>(rows, most_ctas(sms))));
 }
 
 template <typename T, bool KEPT8>
-static cudaError_t dispatch_grad(const muon_block_norm_grad_args& a, float* partial, int ctas, cudaStream_t st) {
-  const auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, dim3(ctas), dim3(warps * 32), 0, st, a, partial); };
+static cudaError_t dispatch_grad(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
+  *ctas = static_cast<int>(std::min<long long>(a.rows, 2 * sms));
+  const auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, dim3(*ctas), dim3(warps * 32), 0, st, a, partial); };
   if (a.cols <= 512) return go(block_norm_grad_kernel<T, 4, 1, KEPT8>, 4);
   if (a.cols <= 2048) return go(block_norm_grad_kernel<T, 8, 2, KEPT8>, 8);
   if (a.cols <= 4096) return go(block_norm_grad_kernel<T, 16, 2, KEPT8>, 16);
@@ -171,11 +399,49 @@ static cudaError_t dispatch_grad(const muon_block_norm_grad_args& a, float* part
   return go(block_norm_grad_kernel<T, 16, 0, KEPT8>, 16);
 }
 
+template <typename T, int G, int C, int S, int MINB, int CL, bool KEPT8>
+static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
+  constexpr int smem = GradRing<T, TH, C, S, KEPT8>::BYTES;
+  static_assert(smem * MINB <= 224 * 1024, "shared memory of an SM");
+  static_assert(MINB <= kBlockNormCtasPerSm, "rows of partial");
+  static bool done[64] = {false};
+  static int known[64] = {0};
+  const auto kernel = block_norm_grad_ring_kernel<T, G, C, S, MINB, CL, KEPT8>;
+  cudaError_t e = smem_limit(kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  int most = MINB * sms;
+  if (CL > 1) {
+    e = resident_clusters(kernel, TH, smem, CL, known, &most);
+    if (e != cudaSuccess) return e;
+  }
+  *ctas = static_cast<int>(std::min<long long>((a.rows + R - 1) / R, std::min(most, most_ctas(sms))));
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(*ctas * CL)), dim3(TH), smem, CL, st, a, partial);
+}
+
+// Threads, pieces and CTAs of a row by its width.
+template <typename T, bool KEPT8>
+static cudaError_t dispatch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const int pieces = static_cast<int>((a.cols + E - 1) / E);
+  if (pieces <= 32) return launch_ring<T, 32, 1, 4, 4, 1, KEPT8>(a, partial, sms, ctas, st);
+  if (pieces <= 64) return launch_ring<T, 64, 1, 4, 4, 1, KEPT8>(a, partial, sms, ctas, st);
+  if (pieces <= 128) return launch_ring<T, 128, 1, 4, 4, 1, KEPT8>(a, partial, sms, ctas, st);
+  if (pieces <= 256) return launch_ring<T, 256, 1, 4, 2, 1, KEPT8>(a, partial, sms, ctas, st);
+  if (pieces <= 512) return launch_ring<T, 512, 1, 5, 1, 1, KEPT8>(a, partial, sms, ctas, st);
+  if (pieces <= 1024) return launch_ring<T, 512, 1, 5, 1, 2, KEPT8>(a, partial, sms, ctas, st);
+  if (pieces <= 2048) return launch_ring<T, 512, 1, 5, 1, 4, KEPT8>(a, partial, sms, ctas, st);
+  return launch_ring<T, 512, 1, 5, 1, 8, KEPT8>(a, partial, sms, ctas, st);
+}
+
 cudaError_t launch_block_norm_grad(const muon_block_norm_grad_args& a, float* partial, int vec, int sms, cudaStream_t st) {
-  const int ctas = block_norm_grad_ctas(a.rows, sms);
+  int ctas = 0;
   const auto go = [&](auto t) {
     using T = decltype(t);
-    return a.x_scale ? dispatch_grad<T, true>(a, partial, ctas, st) : dispatch_grad<T, false>(a, partial, ctas, st);
+    // 8 CTAs of 512 pieces: 32768 16-bit columns, half as many of fp32
+    if (vec && a.cols <= 8 * 512 * (16 / static_cast<int>(sizeof(T))))
+      return a.x_scale ? dispatch_ring<T, true>(a, partial, sms, &ctas, st) : dispatch_ring<T, false>(a, partial, sms, &ctas, st);
+    return a.x_scale ? dispatch_grad<T, true>(a, partial, sms, &ctas, st) : dispatch_grad<T, false>(a, partial, sms, &ctas, st);
   };
   const cudaError_t e = a.dt == MUON_BF16 ? go(__nv_bfloat16()) : a.dt == MUON_FP16 ? go(__half()) : go(float());
   if (e != cudaSuccess || !partial) return e;
