@@ -11,6 +11,7 @@
 
 #include "block_norm.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace muon {
@@ -101,176 +102,158 @@ __global__ void __launch_bounds__(W * 32) block_norm_kernel(const muon_block_nor
 }
 
 // ------------------------------------------------------------------ ring of rows
-// Largest magnitude of a piece as the upper 16 bits of its fp32 bits, rounded up.  A scale byte is the exponent field of
-// bits + 0x1fffff, whose only border within a binade (0x600000) is a multiple of 2^16: it comes out the same.
-template <int E>
-__device__ __forceinline__ uint32_t piece_max(const float (&v)[E]) {
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < E; ++i) m = max(m, abs_bits(v[i]));
-  return (m + 0xffffu) >> 16;
-}
-// A row's 8-bit copies: a block of 128 columns lies in 128 / E neighbouring lanes, two matrices share one exchange.
-template <int E>
-struct Row8 {
-  long long row, rows, rows4;
-  int cols, blocks;
-  bool live;
-  __device__ __forceinline__ void store(const muon_fp8_out& o, int fmt, int col, uint32_t amax, const float (&v)[E]) const {
-    const uint32_t byte = fp8_scale_byte(amax, fmt ? 15 : 8);
-    const float inv = fp8_inverse_scale(byte);
-    if (!live) return;
-    if (col < ((cols + 15) & ~15)) {
-      uint8_t* p = static_cast<uint8_t*>(o.data) + row * o.ld + col;
-      if constexpr (E == 8) {
-        *reinterpret_cast<uint2*>(p) = fmt ? fp8_pack8<true>(v, inv) : fp8_pack8<false>(v, inv);
-      } else {
-        *reinterpret_cast<uint32_t*>(p) = fmt ? fp8_pack4<true>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv)
-                                              : fp8_pack4<false>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-      }
-    }
-    const int kb = col / 128;
-    if (col % 128 == 0 && kb < blocks) scale(o, kb, byte);
-  }
-  __device__ __forceinline__ void scale(const muon_fp8_out& o, int kb, uint32_t byte) const {
-    uint8_t* p = static_cast<uint8_t*>(o.scale) + fp8_scale_offset(kb, row, rows4);
-    *p = static_cast<uint8_t>(byte);
-    if (row == rows - 1)  // scales of no row are 1
-      for (long long r = rows; r < rows4; ++r) p[(r - rows + 1) * 4] = 127;
-  }
-  // Pieces of two matrices, each stored where it is asked for; all lanes call.
-  __device__ __forceinline__ void two(const muon_fp8_out& a, int fa, const float (&va)[E], const muon_fp8_out& b, int fb,
-                                      const float (&vb)[E], int col) const {
-    if (!a.data && !b.data) return;
-    uint32_t m = piece_max(va) | piece_max(vb) << 16;
-#pragma unroll
-    for (int o = 64 / E; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (a.data) store(a, fa, col, m << 16, va);
-    if (b.data) store(b, fb, col, m & 0xffff0000u, vb);
-  }
-};
-
 // CL CTAs of a cluster to a row, G threads of each, C pieces of 16 bytes to a thread, a ring of S rows.
 template <typename T, int G, int C, int S, int MINB, int CL>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kernel(const muon_block_norm_args a) {
-  constexpr int TH = G < 128 ? 128 : G, R = TH / G, E = 16 / static_cast<int>(sizeof(T));
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
+  using P = Pairs<T>;
+  constexpr int E = P::E, N = P::N, PIECE = G * E;  // PIECE: from a thread's piece to its next
+  using Scales = Scales4<128 / E>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ RowSums<G, TH, 1, CL> sums;
   const Ring<T, TH, C, S, 3> ring{ring_smem};
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
-  int n[C], col[C], off[C];  // existing columns of each piece, its first, and the same where one exists
+  const int col = (rank * C * G + t) * E;  // of the first piece
+  int n[C];                                // existing columns of each
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    col[c] = ((rank * C + c) * G + t) * E;
-    n[c] = max(0, min(E, cols - col[c]));
-    off[c] = n[c] ? col[c] : 0;
-  }
+  for (int c = 0; c < C; ++c) n[c] = max(0, min(E, cols - col - c * PIECE));
   const bool element = a.gate && !a.gate_per_row;
   const long long step = static_cast<long long>(gridDim.x / CL) * R, row0 = static_cast<long long>(blockIdx.x / CL) * R + rr;
   long long frow = row0;  // next row to fetch
+  const T* fx = static_cast<const T*>(a.x) + row0 * a.ldx + col;
+  const T* fr = static_cast<const T*>(a.residual) + row0 * a.ldr + col;
+  const T* fg = static_cast<const T*>(a.gate) + (element ? row0 * a.ldg + col : 0);
   auto fetch = [&](int slot) {
     if (frow < a.rows) {
-      const T* fx = static_cast<const T*>(a.x) + frow * a.ldx;
-      const T* fr = static_cast<const T*>(a.residual) + frow * a.ldr;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int bytes = n[c] * static_cast<int>(sizeof(T));
-        ring.fetch(slot, 0, c, fx + off[c], bytes);
-        ring.fetch(slot, 1, c, fr + off[c], bytes);
-        if (element) ring.fetch(slot, 2, c, static_cast<const T*>(a.gate) + frow * a.ldg + off[c], bytes);
+        const int bytes = n[c] * static_cast<int>(sizeof(T)), at = n[c] ? c * PIECE : -col;
+        ring.fetch(slot, 0, c, fx + at, bytes);
+        ring.fetch(slot, 1, c, fr + at, bytes);
+        if (element) ring.fetch(slot, 2, c, fg + at, bytes);
       }
     }
     cp_async_commit();
-    frow += step;
+    frow += step, fx += step * a.ldx, fr += step * a.ldr;
+    if (element) fg += step * a.ldg;
   };
   if (CL > 1) cluster_sync();  // the others' shared memory is there
   pdl_wait();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
-  float w1[C][E], w2[C][E];  // scale post, pre
+  float2 w1[C][N], w2[C][N];  // scale post, pre
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    load_weight_piece<E>(a.scale, a.weight_dt, off[c], n[c], w2[c]);
-    load_weight_piece<E>(a.post, a.weight_dt, off[c], n[c], w1[c]);
+    const int at = n[c] ? col + c * PIECE : 0;
+    float v[E], s[E];
+    load_weight_piece<E>(a.scale, a.weight_dt, at, n[c], s);
+    load_weight_piece<E>(a.post, a.weight_dt, at, n[c], v);
 #pragma unroll
-    for (int i = 0; i < E; ++i) w1[c][i] *= w2[c][i];
-    load_weight_piece<E>(a.pre, a.weight_dt, off[c], n[c], w2[c]);
+    for (int i = 0; i < N; ++i) w1[c][i] = make_float2(v[2 * i] * s[2 * i], v[2 * i + 1] * s[2 * i + 1]);
+    load_weight_piece<E>(a.pre, a.weight_dt, at, n[c], v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w2[c][i] = make_float2(v[2 * i], v[2 * i + 1]);
   }
   const auto row_gate = [&](long long row) {
     return a.gate && !element && row < a.rows ? to_f32(static_cast<const T*>(a.gate)[row * a.ldg]) : 0.f;
   };
   float next_gate = row_gate(row0);  // a row ahead
   const float fcols = static_cast<float>(cols), inv_cols = 1.f / fcols;
-  Row8<E> out{row0, a.rows, (a.rows + 3) & ~3LL, cols, (cols + 127) / 128, true};
+  T* ph = static_cast<T*>(a.h) + row0 * a.ldh + col;
+  T* py = static_cast<T*>(a.y) + row0 * a.ldy + col;
+  // the 8-bit copies: y, h, x, gate; each lane keeps the scales of one of them
+  const bool eight = a.q.data || a.h8.data || a.x8.data || a.gate8.data;
+  uint8_t* p8[4] = {static_cast<uint8_t*>(a.q.data) + row0 * a.q.ld + col, static_cast<uint8_t*>(a.h8.data) + row0 * a.h8.ld + col,
+                    static_cast<uint8_t*>(a.x8.data) + row0 * a.x8.ld + col, static_cast<uint8_t*>(a.gate8.data) + row0 * a.gate8.ld + col};
+  const int mine = Scales::mine(), top = (mine ? a.kept_fmt : a.fmt) ? 15 : 8, cols16 = (cols + 15) & ~15;
+  const long long rows4 = (a.rows + 3) & ~3LL;
+  uint8_t* const scales = static_cast<uint8_t*>(mine == 0 ? a.q.scale : mine == 1 ? a.h8.scale : mine == 2 ? a.x8.scale : a.gate8.scale);
+  uint8_t* ps = scales + row0 * 4;
+  const bool keeper = scales && threadIdx.x % Scales::Q == 0;
   int slot = 0, turn = 0;
   // all threads of a CTA take the same number of turns (the barriers of the sums)
   for (long long row = row0; row - rr < a.rows; row += step, turn += 2) {
     const bool live = R == 1 || row < a.rows;
     if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row: earlier, the next kernel's CTAs take SMs from these
-    const float row_sig = a.gate && !element ? sigmoid<T>(next_gate) : 1.f;
-    next_gate = row_gate(row + step);
+    float2 sig = both(1.f);
+    if (a.gate && !element) sig = both(sigmoid2<T>(both(next_gate)).x), next_gate = row_gate(row + step);
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
-    float h[C][E], sum[1] = {0.f};
+    P h[C];
+    float2 two = both(0.f);
+    float sum[1];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float x[E];
-      ring.read(slot, 0, c, x);
+      P x;
+      x.unpack(ring.piece(slot, 0, c));
 #pragma unroll
-      for (int i = 0; i < E; ++i) sum[0] = fmaf(x[i], x[i], sum[0]);
+      for (int i = 0; i < N; ++i) two = fma2(x.v[i], x.v[i], two);
     }
+    sum[0] = total(two);
     sums(sum, turn);
     const float rx = row_rstd(sum[0], fcols, inv_cols, a.eps);
-    sum[0] = 0.f;
+    two = both(0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float x[E], g[E];
-      ring.read(slot, 0, c, x);
-      ring.read(slot, 1, c, h[c]);
-      if (element) ring.read(slot, 2, c, g);
+      P x, g;
+      x.unpack(ring.piece(slot, 0, c));
+      h[c].unpack(ring.piece(slot, 1, c));
+      if (element) g.unpack(ring.piece(slot, 2, c));
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float b = x[i] * rx * w1[c][i] * (element ? sigmoid<T>(g[i]) : row_sig);
-        h[c][i] = fmaf(a.alpha, h[c][i], b);
-        sum[0] = fmaf(h[c][i], h[c][i], sum[0]);
+      for (int i = 0; i < N; ++i) {
+        if (element) sig = sigmoid2<T>(g.v[i]);
+        const float2 b = mul2(mul2(mul2(x.v[i], both(rx)), w1[c][i]), sig);
+        h[c].v[i] = fma2(both(a.alpha), h[c].v[i], b);
+        two = fma2(h[c].v[i], h[c].v[i], two);
       }
     }
+    sum[0] = total(two);
     sums(sum, turn + 1);
     const float rh = row_rstd(sum[0], fcols, inv_cols, a.eps);
     if (live && t == 0 && rank == 0) {
       if (a.rstd_x) a.rstd_x[row] = rx;
       if (a.rstd_h) a.rstd_h[row] = rh;
     }
-    out.row = row, out.live = live;
+    // past the last column everything is 0 (or NaN, where a norm's factor is not finite and so the whole row)
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float y[E];
+      P y;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const bool in = n[c] == E || i < n[c];
-        y[i] = in ? h[c][i] * rh * w2[c][i] : 0.f;
-        h[c][i] = in ? h[c][i] : 0.f;
-      }
-      if (live && a.h) store_piece(static_cast<T*>(a.h) + row * a.ldh + off[c], n[c], h[c]);
-      if (live && a.y) store_piece(static_cast<T*>(a.y) + row * a.ldy + off[c], n[c], y);
-      out.two(a.q, a.fmt, y, a.h8, a.kept_fmt, h[c], col[c]);
-      if (a.x8.data || a.gate8.data) {
-        ring.read(slot, 0, c, y);
-        if (element) ring.read(slot, 2, c, h[c]);
-        out.two(a.x8, a.kept_fmt, y, a.gate8, a.kept_fmt, h[c], col[c]);
+      for (int i = 0; i < N; ++i) y.v[i] = mul2(mul2(h[c].v[i], both(rh)), w2[c][i]);
+      if (live && a.h) h[c].store(ph + c * PIECE, n[c]);
+      if (live && a.y) y.store(py + c * PIECE, n[c]);
+      if (eight) {
+        P x, g;
+        uint32_t m[4] = {y.largest(), h[c].largest(), 0u, 0u};
+        if (a.x8.data) x.unpack(ring.piece(slot, 0, c)), m[2] = x.largest();
+        if (a.gate8.data) g.unpack(ring.piece(slot, 2, c)), m[3] = g.largest();
+        const Scales s(m, top);
+        if (live && col + c * PIECE < cols16) {
+          if (a.q.data) y.store8(p8[0] + c * PIECE, s.inv[0], a.fmt);
+          if (a.h8.data) h[c].store8(p8[1] + c * PIECE, s.inv[1], a.kept_fmt);
+          if (a.x8.data) x.store8(p8[2] + c * PIECE, s.inv[2], a.kept_fmt);
+          if (a.gate8.data) g.store8(p8[3] + c * PIECE, s.inv[3], a.kept_fmt);
+        }
+        const int kb = (col + c * PIECE) / 128;
+        if (keeper && live && kb * 128 < cols) ps[(kb >> 2) * rows4 * 4 + (kb & 3)] = static_cast<uint8_t>(s.byte);
       }
     }
-    // blocks past the last column, up to a whole scale word
-    if (rank == 0 && live && t < (cols + 511) / 512 * 4 - out.blocks) {
-      const int kb = out.blocks + t;
-      if (a.q.data) out.scale(a.q, kb, 127u);
-      if (a.x8.data) out.scale(a.x8, kb, 127u);
-      if (a.h8.data) out.scale(a.h8, kb, 127u);
-      if (a.gate8.data) out.scale(a.gate8, kb, 127u);
-    }
+    ph += step * a.ldh, py += step * a.ldy, ps += step * 4;
+    p8[0] += step * a.q.ld, p8[1] += step * a.h8.ld, p8[2] += step * a.x8.ld, p8[3] += step * a.gate8.ld;
     slot = slot + 1 == S ? 0 : slot + 1;
   }
+  // scales of no block or row, up to whole words and to four rows, are 1
+  if (!eight || rank != 0) return;
+  const int blocks = (cols + 127) / 128, end = (cols + 511) / 512 * 4;
+  const auto fill = [&](const muon_fp8_out& o, int kb, long long row) {
+    if (o.data) static_cast<uint8_t*>(o.scale)[fp8_scale_offset(kb, row, rows4)] = 127;
+  };
+  for (long long row = row0; row < a.rows; row += step)
+    for (int kb = blocks + t; kb < end; kb += G) fill(a.q, kb, row), fill(a.h8, kb, row), fill(a.x8, kb, row), fill(a.gate8, kb, row);
+  if (blockIdx.x == 0)
+    for (long long row = a.rows + rr; row < rows4; row += R)
+      for (int kb = t; kb < end; kb += G) fill(a.q, kb, row), fill(a.h8, kb, row), fill(a.x8, kb, row), fill(a.gate8, kb, row);
 }
 
 template <typename T, int G, int C, int S, int MINB, int CL>
@@ -297,10 +280,10 @@ template <typename T>
 static cudaError_t dispatch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const int pieces = static_cast<int>((a.cols + E - 1) / E);
-  if (pieces <= 32) return launch_ring<T, 32, 1, 6, 5, 1>(a, sms, st);
-  if (pieces <= 64) return launch_ring<T, 64, 1, 4, 8, 1>(a, sms, st);
-  if (pieces <= 128) return launch_ring<T, 64, 2, 3, 5, 1>(a, sms, st);
-  if (pieces <= 256) return launch_ring<T, 256, 1, 4, 4, 1>(a, sms, st);
+  if (pieces <= 32) return launch_ring<T, 32, 1, 8, 4, 1>(a, sms, st);
+  if (pieces <= 64) return launch_ring<T, 64, 1, 6, 5, 1>(a, sms, st);
+  if (pieces <= 128) return launch_ring<T, 128, 1, 6, 5, 1>(a, sms, st);
+  if (pieces <= 256) return launch_ring<T, 256, 1, 6, 3, 1>(a, sms, st);
   if (pieces <= 512) return launch_ring<T, 256, 2, 4, 2, 1>(a, sms, st);
   if (pieces <= 1024) return launch_ring<T, 512, 2, 4, 1, 1>(a, sms, st);
   if (pieces <= 2048) return launch_ring<T, 512, 2, 4, 1, 2>(a, sms, st);

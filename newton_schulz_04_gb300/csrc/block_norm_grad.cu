@@ -10,9 +10,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "block_norm.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace muon {
@@ -130,22 +132,6 @@ __global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_bloc
 }
 
 // ------------------------------------------------------------------ ring of rows
-// E values of a kept 8-bit matrix, E bytes of shared memory.
-template <int E>
-__device__ __forceinline__ void read8(const uint8_t* p, int fmt, float (&v)[E]) {
-  uint32_t w[E / 4];
-  if constexpr (E == 8) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    w[0] = x.x, w[1] = x.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
-#pragma unroll
-  for (int q = 0; q < E / 2; ++q) {
-    const float2 f = fp8_unpack2(w[q / 2] >> (16 * (q & 1)), fmt);
-    v[2 * q] = f.x, v[2 * q + 1] = f.y;
-  }
-}
 template <int BYTES>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int bytes) {  // the rest is zero
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "n"(BYTES), "r"(bytes)
@@ -164,64 +150,76 @@ struct GradRing {
     return stage + WIDE * C * TH * 16 + (((arr - WIDE) * C + c) * TH + static_cast<int>(threadIdx.x)) * E;
   }
   // n of the piece's elements exist.
-  __device__ __forceinline__ void fetch(int slot, int arr, int c, const void* row, int off, int n) const {
-    if (arr < WIDE) copy16(smem_u32(at(slot, arr, c)), static_cast<const T*>(row) + off, n * static_cast<int>(sizeof(T)));
-    else copy_small<E>(smem_u32(at(slot, arr, c)), static_cast<const uint8_t*>(row) + off, n);
+  __device__ __forceinline__ void fetch(int slot, int arr, int c, const void* src, int n) const {
+    if (arr < WIDE) copy16(smem_u32(at(slot, arr, c)), src, n * static_cast<int>(sizeof(T)));
+    else copy_small<E>(smem_u32(at(slot, arr, c)), src, n);
   }
-  __device__ __forceinline__ void read(int slot, int arr, int c, int fmt, float (&v)[E]) const {
-    if (arr < WIDE) unpack_piece<T>(*reinterpret_cast<const uint4*>(at(slot, arr, c)), v);
-    else read8<E>(at(slot, arr, c), fmt, v);
+  __device__ __forceinline__ void read(int slot, int arr, int c, int fmt, Pairs<T>& p) const {
+    if (arr < WIDE) p.unpack(*reinterpret_cast<const uint4*>(at(slot, arr, c)));
+    else if (fmt) p.template unpack8<true>(at(slot, arr, c));
+    else p.template unpack8<false>(at(slot, arr, c));
   }
 };
 
 template <typename T, int G, int C, int S, int MINB, int CL, bool KEPT8>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
     block_norm_grad_ring_kernel(const muon_block_norm_grad_args a, float* partial) {
-  constexpr int TH = G < 128 ? 128 : G, R = TH / G, E = 16 / static_cast<int>(sizeof(T));
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
   constexpr int DY = 0, DH = 1, X = 2, H = 3, GATE = 4;
+  using P = Pairs<T>;
+  using K = std::conditional_t<KEPT8, uint8_t, T>;
+  constexpr int E = P::E, N = P::N, PIECE = G * E;  // PIECE: from a thread's piece to its next
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ RowSums<G, TH, 3, CL> sums;
   const GradRing<T, TH, C, S, KEPT8> ring{ring_smem};
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
-  int n[C], off[C];
+  const int col = (rank * C * G + t) * E;  // of the first piece
+  int n[C];                                // existing columns of each
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = ((rank * C + c) * G + t) * E;
-    n[c] = max(0, min(E, cols - col));
-    off[c] = n[c] ? col : 0;
-  }
+  for (int c = 0; c < C; ++c) n[c] = max(0, min(E, cols - col - c * PIECE));
   const bool element = a.gate && !a.gate_per_row;
   const long long step = static_cast<long long>(gridDim.x / CL) * R, row0 = static_cast<long long>(blockIdx.x / CL) * R + rr;
   const long long rows4 = (a.rows + 3) & ~3LL;
   long long frow = row0;  // next row to fetch
+  const T* fdy = static_cast<const T*>(a.dy) + row0 * a.lddy + col;
+  const T* fdh = static_cast<const T*>(a.dh) + (a.dh ? row0 * a.lddh + col : 0);
+  const K* fx = static_cast<const K*>(a.x) + row0 * a.ldx + col;
+  const K* fh = static_cast<const K*>(a.h) + row0 * a.ldh + col;
+  const K* fg = static_cast<const K*>(a.gate) + (element ? row0 * a.ldg + col : 0);
   auto fetch = [&](int slot) {
     if (frow < a.rows) {
-      constexpr int kept = KEPT8 ? 1 : static_cast<int>(sizeof(T));
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        ring.fetch(slot, DY, c, static_cast<const T*>(a.dy) + frow * a.lddy, off[c], n[c]);
-        if (a.dh) ring.fetch(slot, DH, c, static_cast<const T*>(a.dh) + frow * a.lddh, off[c], n[c]);
-        ring.fetch(slot, X, c, static_cast<const uint8_t*>(a.x) + frow * a.ldx * kept, off[c], n[c]);
-        ring.fetch(slot, H, c, static_cast<const uint8_t*>(a.h) + frow * a.ldh * kept, off[c], n[c]);
-        if (element) ring.fetch(slot, GATE, c, static_cast<const uint8_t*>(a.gate) + frow * a.ldg * kept, off[c], n[c]);
+        const int at = n[c] ? c * PIECE : -col;
+        ring.fetch(slot, DY, c, fdy + at, n[c]);
+        if (a.dh) ring.fetch(slot, DH, c, fdh + at, n[c]);
+        ring.fetch(slot, X, c, fx + at, n[c]);
+        ring.fetch(slot, H, c, fh + at, n[c]);
+        if (element) ring.fetch(slot, GATE, c, fg + at, n[c]);
       }
     }
     cp_async_commit();
-    frow += step;
+    frow += step, fdy += step * a.lddy, fx += step * a.ldx, fh += step * a.ldh;
+    if (a.dh) fdh += step * a.lddh;
+    if (element) fg += step * a.ldg;
   };
   if (CL > 1) cluster_sync();  // the others' shared memory is there
   pdl_wait();
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fetch(s);
-  float w1[C][E], w2[C][E], dpre[C][E], sx[C][E];  // scale post, pre, and the columns' sums
+  float2 w1[C][N], w2[C][N], dpre[C][N], sx[C][N];  // scale post, pre, and the columns' sums
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    load_weight_piece<E>(a.scale, a.weight_dt, off[c], n[c], w2[c]);
-    load_weight_piece<E>(a.post, a.weight_dt, off[c], n[c], w1[c]);
+    const int at = n[c] ? col + c * PIECE : 0;
+    float v[E], s[E];
+    load_weight_piece<E>(a.scale, a.weight_dt, at, n[c], s);
+    load_weight_piece<E>(a.post, a.weight_dt, at, n[c], v);
 #pragma unroll
-    for (int i = 0; i < E; ++i) w1[c][i] *= w2[c][i], dpre[c][i] = sx[c][i] = 0.f;
-    load_weight_piece<E>(a.pre, a.weight_dt, off[c], n[c], w2[c]);
+    for (int i = 0; i < N; ++i) w1[c][i] = make_float2(v[2 * i] * s[2 * i], v[2 * i + 1] * s[2 * i + 1]);
+    load_weight_piece<E>(a.pre, a.weight_dt, at, n[c], v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w2[c][i] = make_float2(v[2 * i], v[2 * i + 1]), dpre[c][i] = sx[c][i] = both(0.f);
   }
   // of a row: the norms' factors, its gate, the scales of the kept pieces; fetched a row ahead
   struct RowHead {
@@ -237,7 +235,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
       if (KEPT8) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const long long o = fp8_scale_offset(off[c] / 128, row, rows4);
+          const long long o = fp8_scale_offset(n[c] ? (col + c * PIECE) / 128 : 0, row, rows4);
           r.xs[c] = __ldg(static_cast<const uint8_t*>(a.x_scale) + o);
           r.hs[c] = __ldg(static_cast<const uint8_t*>(a.h_scale) + o);
           if (element) r.gs[c] = __ldg(static_cast<const uint8_t*>(a.gate_scale) + o);
@@ -248,92 +246,94 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   };
   RowHead next = head(row0);
   const float inv_cols = 1.f / static_cast<float>(cols);
+  T* pdr = static_cast<T*>(a.dresidual) + row0 * a.lddr + col;
+  T* pdx = static_cast<T*>(a.dx) + row0 * a.lddx + col;
+  T* pdg = static_cast<T*>(a.dgate) + (element ? row0 * a.lddgate + col : 0);
   int slot = 0, turn = 0;
   for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
     const bool live = R == 1 || row < a.rows;
     if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row, as in the forward kernel
     const RowHead now = next;
     next = head(row + step);
-    const float row_sig = a.gate && !element ? sigmoid<T>(now.gate) : 1.f;
+    const float row_sig = a.gate && !element ? sigmoid2<T>(both(now.gate)).x : 1.f;
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
-    float u[C][E], sig[C][E], sum[3] = {0.f, 0.f, 0.f};
+    P u[C], sig[C], xn[C], hn[C];
+    float2 s0 = both(0.f), s1 = s0, s2 = s0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float d[E], x[E], h[E];
+      P d;
       ring.read(slot, DY, c, a.kept_fmt, d);
-      ring.read(slot, X, c, a.kept_fmt, x);
-      ring.read(slot, H, c, a.kept_fmt, h);
+      ring.read(slot, X, c, a.kept_fmt, xn[c]);
+      ring.read(slot, H, c, a.kept_fmt, hn[c]);
       if (a.dh) {
         ring.read(slot, DH, c, a.kept_fmt, u[c]);
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) u[c][i] = 0.f;
+        for (int i = 0; i < N; ++i) u[c].v[i] = both(0.f);
       }
       if (element) ring.read(slot, GATE, c, a.kept_fmt, sig[c]);
-      const float xf = KEPT8 ? now.rx * fp8_scale_value(now.xs[c]) : now.rx, hf = KEPT8 ? now.rh * fp8_scale_value(now.hs[c]) : now.rh;
-      const float gf = KEPT8 ? fp8_scale_value(now.gs[c]) : 1.f;
       if (R > 1 && !live) {  // the slot holds another row's remains
 #pragma unroll
-        for (int i = 0; i < E; ++i) d[i] = x[i] = h[i] = u[c][i] = sig[c][i] = 0.f;
+        for (int i = 0; i < N; ++i) d.v[i] = xn[c].v[i] = hn[c].v[i] = u[c].v[i] = sig[c].v[i] = both(0.f);
       }
+      const float2 xf = both(KEPT8 ? now.rx * fp8_scale_value(now.xs[c]) : now.rx);
+      const float2 hf = both(KEPT8 ? now.rh * fp8_scale_value(now.hs[c]) : now.rh);
+      const float2 gf = both(KEPT8 ? fp8_scale_value(now.gs[c]) : 1.f);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float hn = h[i] * hf, ad = d[i] * w2[c][i];
-        u[c][i] = fmaf(now.rh, ad, u[c][i]);
-        sig[c][i] = element ? sigmoid<T>(sig[c][i] * gf) : row_sig;
-        const float e = sig[c][i] * w1[c][i] * (x[i] * xf);
-        sum[0] = fmaf(ad, hn, sum[0]);
-        sum[1] = fmaf(u[c][i], e, sum[1]);
-        sum[2] = fmaf(hn, e, sum[2]);
-        dpre[c][i] = fmaf(d[i], hn, dpre[c][i]);
+      for (int i = 0; i < N; ++i) {
+        hn[c].v[i] = mul2(hn[c].v[i], hf);
+        xn[c].v[i] = mul2(xn[c].v[i], xf);
+        const float2 ad = mul2(d.v[i], w2[c][i]);
+        u[c].v[i] = fma2(both(now.rh), ad, u[c].v[i]);
+        sig[c].v[i] = element ? sigmoid2<T>(KEPT8 ? mul2(sig[c].v[i], gf) : sig[c].v[i]) : both(row_sig);
+        const float2 e = mul2(mul2(sig[c].v[i], w1[c][i]), xn[c].v[i]);
+        s0 = fma2(ad, hn[c].v[i], s0);
+        s1 = fma2(u[c].v[i], e, s1);
+        s2 = fma2(hn[c].v[i], e, s2);
+        dpre[c][i] = fma2(d.v[i], hn[c].v[i], dpre[c][i]);
       }
     }
+    float sum[3] = {total(s0), total(s1), total(s2)};
     sums(sum, turn);
     const float k1 = sum[0] * inv_cols * now.rh, along = sum[1] - k1 * sum[2], k2 = along * inv_cols;
     if (live && a.dgate && !element && t == 0 && rank == 0)
       static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>((1.f - row_sig) * along);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float x[E], h[E];
-      ring.read(slot, X, c, a.kept_fmt, x);
-      ring.read(slot, H, c, a.kept_fmt, h);
-      const float xf = KEPT8 ? now.rx * fp8_scale_value(now.xs[c]) : now.rx, hf = KEPT8 ? now.rh * fp8_scale_value(now.hs[c]) : now.rh;
-      if (R > 1 && !live) {
+      P dr, dx, dg;
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = h[i] = 0.f;
-      }
-      float dr[E], dg[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float xn = x[i] * xf, d = u[c][i] - k1 * (h[i] * hf), td = d * sig[c][i], b = td * w1[c][i];
-        sx[c][i] = fmaf(td, xn, sx[c][i]);
-        dr[i] = a.alpha * d;
-        dg[i] = (1.f - sig[c][i]) * (b * xn);
-        x[i] = now.rx * (b - xn * k2);
+      for (int i = 0; i < N; ++i) {
+        const float2 d = fma2(both(-k1), hn[c].v[i], u[c].v[i]), td = mul2(d, sig[c].v[i]), b = mul2(td, w1[c][i]);
+        sx[c][i] = fma2(td, xn[c].v[i], sx[c][i]);
+        dr.v[i] = mul2(both(a.alpha), d);
+        dx.v[i] = mul2(both(now.rx), fma2(both(-k2), xn[c].v[i], b));
+        dg.v[i] = mul2(fma2(both(-1.f), sig[c].v[i], both(1.f)), mul2(b, xn[c].v[i]));
       }
       if (live) {
-        if (a.dresidual) store_piece(static_cast<T*>(a.dresidual) + row * a.lddr + off[c], n[c], dr);
-        if (a.dx) store_piece(static_cast<T*>(a.dx) + row * a.lddx + off[c], n[c], x);
-        if (element && a.dgate) store_piece(static_cast<T*>(a.dgate) + row * a.lddgate + off[c], n[c], dg);
+        if (a.dresidual) dr.store(pdr + c * PIECE, n[c]);
+        if (a.dx) dx.store(pdx + c * PIECE, n[c]);
+        if (element && a.dgate) dg.store(pdg + c * PIECE, n[c]);
       }
     }
+    pdr += step * a.lddr, pdx += step * a.lddx;
+    if (element) pdg += step * a.lddgate;
     slot = slot + 1 == S ? 0 : slot + 1;
   }
   if (!partial) return;
   float* part = partial + static_cast<long long>(blockIdx.x / CL) * 2 * cols;
   if (R > 1) {  // join the CTA's row groups through the ring's memory
-    static_assert(R == 1 || (R - 1) * 2 * C * E * G * 4 <= GradRing<T, TH, C, S, KEPT8>::BYTES, "room to join");
+    static_assert(R == 1 || (R - 1) * 2 * C * N * G * 8 <= GradRing<T, TH, C, S, KEPT8>::BYTES, "room to join");
     cp_async_wait<0>();
     __syncthreads();
-    float* all = reinterpret_cast<float*>(ring_smem);  // [R - 1][2][C * E][G]
+    float2* all = reinterpret_cast<float2*>(ring_smem);  // [R - 1][2][C * N][G]
     if (rr > 0) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          all[(((rr - 1) * 2 + 0) * C * E + c * E + i) * G + t] = dpre[c][i];
-          all[(((rr - 1) * 2 + 1) * C * E + c * E + i) * G + t] = sx[c][i];
+        for (int i = 0; i < N; ++i) {
+          all[(((rr - 1) * 2 + 0) * C * N + c * N + i) * G + t] = dpre[c][i];
+          all[(((rr - 1) * 2 + 1) * C * N + c * N + i) * G + t] = sx[c][i];
         }
     }
     __syncthreads();
@@ -341,17 +341,20 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < E; ++i)
+      for (int i = 0; i < N; ++i)
         for (int r = 1; r < R; ++r) {
-          dpre[c][i] += all[(((r - 1) * 2 + 0) * C * E + c * E + i) * G + t];
-          sx[c][i] += all[(((r - 1) * 2 + 1) * C * E + c * E + i) * G + t];
+          dpre[c][i] = add2(dpre[c][i], all[(((r - 1) * 2 + 0) * C * N + c * N + i) * G + t]);
+          sx[c][i] = add2(sx[c][i], all[(((r - 1) * 2 + 1) * C * N + c * N + i) * G + t]);
         }
   }
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i < n[c]) part[off[c] + i] = dpre[c][i], part[cols + off[c] + i] = sx[c][i];
+    for (int i = 0; i < N; ++i) {
+      float* p = part + col + c * PIECE + 2 * i;
+      if (2 * i < n[c]) p[0] = dpre[c][i].x, p[cols] = sx[c][i].x;
+      if (2 * i + 1 < n[c]) p[1] = dpre[c][i].y, p[cols + 1] = sx[c][i].y;
+    }
 }
 
 // Sums over the CTAs' rows in a fixed order, 32 columns by 32 row groups per CTA; blockIdx.y 0: dpre, 1: dpost and dscale.

@@ -1,0 +1,148 @@
+// pairs.cuh -- a thread's piece of a row as pairs of fp32 values (sm_100's two-wide FMA, multiplication and addition halve the
+// instructions of what is bound by issuing them), and the exchange by which a row's 8-bit copies get their scales.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "fp8.cuh"
+#include "ptx.cuh"
+
+namespace muon {
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ uint32_t pack2(float2 v, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float2 v, __half) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 16 bytes of T.
+template <typename T>
+struct Pairs {
+  static constexpr int E = 16 / static_cast<int>(sizeof(T)), N = E / 2;
+  float2 v[N];
+  __device__ __forceinline__ void unpack(const uint4& w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = unpack2(u[i], T());
+    } else {
+      v[0] = make_float2(__uint_as_float(u[0]), __uint_as_float(u[1]));
+      v[1] = make_float2(__uint_as_float(u[2]), __uint_as_float(u[3]));
+    }
+  }
+  // E bytes of 8-bit values
+  template <bool E5M2>
+  __device__ __forceinline__ void unpack8(const uint8_t* p) {
+    uint32_t w[E / 4];
+    if constexpr (E == 8) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x, w[1] = x.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = fp8_unpack2<E5M2>(w[i / 2] >> (16 * (i & 1)));
+  }
+  // n of the elements exist.
+  __device__ __forceinline__ void store(T* p, int n) const {
+    if (n == E) {
+      uint4 w;
+      if constexpr (sizeof(T) == 2) {
+        w = make_uint4(pack2(v[0], T()), pack2(v[1], T()), pack2(v[2], T()), pack2(v[3], T()));
+      } else {
+        w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+      }
+      *reinterpret_cast<uint4*>(p) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (2 * i < n) p[2 * i] = from_f32<T>(v[i].x);
+        if (2 * i + 1 < n) p[2 * i + 1] = from_f32<T>(v[i].y);
+      }
+    }
+  }
+  // fp32 bits of the largest magnitude; a NaN's are above all others
+  __device__ __forceinline__ uint32_t largest() const {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(v[i].x)), "f"(fabsf(v[i].y)));
+    return __float_as_uint(m);
+  }
+  template <bool E5M2>
+  __device__ __forceinline__ void store8(uint8_t* p, float inv) const {
+    float2 s[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = mul2(v[i], both(inv));
+    if constexpr (E == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(fp8_pack4<E5M2>(s[0].x, s[0].y, s[1].x, s[1].y),
+                                                fp8_pack4<E5M2>(s[2].x, s[2].y, s[3].x, s[3].y));
+    } else {
+      *reinterpret_cast<uint32_t*>(p) = fp8_pack4<E5M2>(s[0].x, s[0].y, s[1].x, s[1].y);
+    }
+  }
+  __device__ __forceinline__ void store8(uint8_t* p, float inv, int fmt) const {
+    if (fmt) store8<true>(p, inv);
+    else store8<false>(p, inv);
+  }
+};
+
+// Pieces that hold every column are summed as pairs, too.
+__device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
+
+// 1 / (1 + exp(-g)) of a pair, 0 at -infinity and from about g = -87 on.  fp32 data takes the accurate exponential and
+// quotient; 16-bit data, which is rounded by 2^-11 at best, the hardware's: off by (4 + 1.2 |g|) 2^-23 of the value.
+template <typename T>
+__device__ __forceinline__ float2 sigmoid2(float2 g) {
+  if constexpr (sizeof(T) == 4) {
+    return make_float2(1.f / (1.f + expf(-g.x)), 1.f / (1.f + expf(-g.y)));
+  } else {
+    float2 e = mul2(g, both(-1.4426950408889634f)), r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+    e = add2(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return r;
+  }
+}
+
+// Scales of up to four matrices' blocks, whose 128 columns lie in LANES = 16 or 32 neighbouring lanes.  The largest
+// magnitudes travel as the upper 16 bits of their fp32 bits, rounded up, two to a word: a scale byte is the exponent field of
+// bits + 0x1fffff, and the only border within a binade, 0x600000, is a multiple of 2^16, so that it comes out the same.  A
+// quarter of the lanes ends up with one matrix each, computes its byte, keeps it and hands the others its inverse: a third of
+// the instructions of four exchanges in all lanes.
+template <int LANES>
+struct Scales4 {
+  static constexpr int Q = LANES / 4;
+  uint32_t byte;   // of matrix (lane / Q) % 4
+  float inv[4];
+  static __device__ __forceinline__ int mine() { return (threadIdx.x / Q) % 4; }
+  // m: fp32 bits of the lane's largest magnitudes; top: 8 or 15 for the matrix mine() says
+  __device__ __forceinline__ Scales4(const uint32_t (&m)[4], int top) {
+    const int lane = threadIdx.x % 32;
+    const uint32_t ab = __byte_perm(m[0] + 0xffffu, m[1] + 0xffffu, 0x7632);
+    const uint32_t cd = __byte_perm(m[2] + 0xffffu, m[3] + 0xffffu, 0x7632);
+    const bool up = lane & (2 * Q);
+    uint32_t w = __vmaxu2(up ? cd : ab, __shfl_xor_sync(0xffffffffu, up ? ab : cd, 2 * Q));
+#pragma unroll
+    for (int o = Q; o > 0; o >>= 1) w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, o));
+    byte = fp8_scale_byte(lane & Q ? w & 0xffff0000u : w << 16, top);
+    const float mine_inv = fp8_inverse_scale(byte);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) inv[k] = __shfl_sync(0xffffffffu, mine_inv, (lane & ~(LANES - 1)) + k * Q);
+  }
+};
+
+}  // namespace muon
