@@ -19,7 +19,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmuon_ns.so")
 SOURCES = ["engine.cu", "tc_gemm.cu", "simt_gemm.cu", "elementwise.cu", "adamw.cu", "planner.cpp",
            "train_abi.cu", "clip.cu", "rms_norm.cu", "fp8_quant.cu", "fp8_gemm.cu",
-           "fp8_few.cu", "block_abi.cu", "block_norm.cu", "block_norm_grad.cu", "gated.cu", "fp8_transpose.cu"]
+           "fp8_few.cu", "block_abi.cu", "block_norm.cu", "block_norm_fp16.cu", "block_norm_fp32.cu", "block_norm_grad.cu",
+           "block_norm_grad_fp16.cu", "block_norm_grad_fp32.cu", "gated.cu", "fp8_transpose.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,316 +1,15 @@
-// block_norm.cu -- the norms behind a block and before the next one, with the block's gate and scale between them.
-//
-//   rho_x = 1 / sqrt(mean_j x_j^2 + eps)       h = alpha residual + sigmoid(gate) scale post (x rho_x)
-//   rho_h = 1 / sqrt(mean_j h_j^2 + eps)       y = h rho_h pre
-//
-// Everything goes on in fp32 from unrounded values; y, h, the 8-bit y and the 8-bit copies of x, h and gate are each
-// rounded once.
-#include <cuda_runtime.h>
-
-#include <algorithm>
-
-#include "block_norm.cuh"
-#include "kernels.h"
-#include "pairs.cuh"
-#include "ptx.cuh"
+// block_norm.cu -- the norms around a block: bf16 rows, and the choice by type.
+#include "block_norm_rows.cuh"
 
 namespace muon {
 
-// W warps to a row, K blocks to a warp; K = 0: any number, computed from memory again in each phase.
-template <typename T, int W, int K>
-__global__ void __launch_bounds__(W * 32) block_norm_kernel(const muon_block_norm_args a) {
-  constexpr int KK = K ? K : 1;
-  __shared__ float sh[2][1][W];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cols = static_cast<int>(a.cols);
-  const int turns = K ? K : ((cols + 127) / 128 + W - 1) / W;
-  const long long row = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  const T* res = static_cast<const T*>(a.residual) + row * a.ldr;
-  const T* gate = static_cast<const T*>(a.gate) + (a.gate ? row * a.ldg : 0);
-  float v[KK][4];
-  float sum[1] = {0.f};
-  float sig = 1.f;
-  if (a.gate && a.gate_per_row) sig = sigmoid<T>(to_f32(*gate));
-  auto column = [&](int k, int j) { return (warp + W * k) * 128 + lane + 32 * j; };
-#pragma unroll
-  for (int k = 0; k < turns; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = column(k, j);
-      const float f = load_or<T>(x, col, col < cols, 0.f);
-      if (K) v[k < KK ? k : 0][j] = f;
-      sum[0] = fmaf(f, f, sum[0]);
-    }
-  cta_sums<W, 1>(sum, sh, 0);
-  const float n = static_cast<float>(cols), inv_n = 1.f / n;
-  const float rx = row_rstd(sum[0], n, inv_n, a.eps);
-  auto stream = [&](int col, float f) {
-    if (col >= cols) return 0.f;
-    float b = f * rx * (load_weight(a.post, a.weight_dt, col, true) * load_weight(a.scale, a.weight_dt, col, true));
-    b *= a.gate && !a.gate_per_row ? sigmoid<T>(to_f32(gate[col])) : sig;
-    return fmaf(a.alpha, to_f32(res[col]), b);
-  };
-  sum[0] = 0.f;
-#pragma unroll
-  for (int k = 0; k < turns; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = column(k, j);
-      const float h = stream(col, K ? v[k < KK ? k : 0][j] : load_or<T>(x, col, col < cols, 0.f));
-      if (K) v[k < KK ? k : 0][j] = h;
-      sum[0] = fmaf(h, h, sum[0]);
-    }
-  cta_sums<W, 1>(sum, sh, 1);
-  const float rh = row_rstd(sum[0], n, inv_n, a.eps);
-  if (threadIdx.x == 0) {
-    if (a.rstd_x) a.rstd_x[row] = rx;
-    if (a.rstd_h) a.rstd_h[row] = rh;
-  }
-#pragma unroll
-  for (int k = 0; k < turns; ++k) {
-    const int kb = warp + W * k;
-    if (kb * 128 >= cols) break;
-    float h[4], f[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = column(k, j);
-      h[j] = K ? v[k < KK ? k : 0][j] : stream(col, load_or<T>(x, col, col < cols, 0.f));
-      if (a.h && col < cols) static_cast<T*>(a.h)[row * a.ldh + col] = from_f32<T>(h[j]);
-      f[j] = h[j] * rh * load_weight(a.pre, a.weight_dt, col, col < cols);
-      if (col >= cols) f[j] = 0.f;
-      if (a.y && col < cols) static_cast<T*>(a.y)[row * a.ldy + col] = from_f32<T>(f[j]);
-    }
-    if (a.q.data) store_block8(a.q, a.fmt, row, a.rows, cols, kb, f);
-    if (a.h8.data) store_block8(a.h8, a.kept_fmt, row, a.rows, cols, kb, h);
-    if (a.x8.data) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = load_or<T>(x, column(k, j), column(k, j) < cols, 0.f);
-      store_block8(a.x8, a.kept_fmt, row, a.rows, cols, kb, f);
-    }
-    if (a.gate8.data) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = load_or<T>(gate, column(k, j), column(k, j) < cols, 0.f);
-      store_block8(a.gate8, a.kept_fmt, row, a.rows, cols, kb, f);
-    }
-  }
-  if (a.q.data) pad_blocks8(a.q, row, a.rows, cols);
-  if (a.h8.data) pad_blocks8(a.h8, row, a.rows, cols);
-  if (a.x8.data) pad_blocks8(a.x8, row, a.rows, cols);
-  if (a.gate8.data) pad_blocks8(a.gate8, row, a.rows, cols);
-}
-
-// ------------------------------------------------------------------ ring of rows
-// CL CTAs of a cluster to a row, G threads of each, C pieces of 16 bytes to a thread, a ring of S rows.
-template <typename T, int G, int C, int S, int MINB, int CL>
-__global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kernel(const muon_block_norm_args a) {
-  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
-  using P = Pairs<T>;
-  constexpr int E = P::E, N = P::N, PIECE = G * E;  // PIECE: from a thread's piece to its next
-  using Scales = Scales4<128 / E>;
-  extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ RowSums<G, TH, 1, CL> sums;
-  const Ring<T, TH, C, S, 3> ring{ring_smem};
-  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
-  const int col = (rank * C * G + t) * E;  // of the first piece
-  int n[C];                                // existing columns of each
-#pragma unroll
-  for (int c = 0; c < C; ++c) n[c] = max(0, min(E, cols - col - c * PIECE));
-  const bool element = a.gate && !a.gate_per_row;
-  const long long step = static_cast<long long>(gridDim.x / CL) * R, row0 = static_cast<long long>(blockIdx.x / CL) * R + rr;
-  long long frow = row0;  // next row to fetch
-  const T* fx = static_cast<const T*>(a.x) + row0 * a.ldx + col;
-  const T* fr = static_cast<const T*>(a.residual) + row0 * a.ldr + col;
-  const T* fg = static_cast<const T*>(a.gate) + (element ? row0 * a.ldg + col : 0);
-  auto fetch = [&](int slot) {
-    if (frow < a.rows) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int bytes = n[c] * static_cast<int>(sizeof(T)), at = n[c] ? c * PIECE : -col;
-        ring.fetch(slot, 0, c, fx + at, bytes);
-        ring.fetch(slot, 1, c, fr + at, bytes);
-        if (element) ring.fetch(slot, 2, c, fg + at, bytes);
-      }
-    }
-    cp_async_commit();
-    frow += step, fx += step * a.ldx, fr += step * a.ldr;
-    if (element) fg += step * a.ldg;
-  };
-  if (CL > 1) cluster_sync();  // the others' shared memory is there
-  pdl_wait();
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s) fetch(s);
-  float2 w1[C][N], w2[C][N];  // scale post, pre
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int at = n[c] ? col + c * PIECE : 0;
-    float v[E], s[E];
-    load_weight_piece<E>(a.scale, a.weight_dt, at, n[c], s);
-    load_weight_piece<E>(a.post, a.weight_dt, at, n[c], v);
-#pragma unroll
-    for (int i = 0; i < N; ++i) w1[c][i] = make_float2(v[2 * i] * s[2 * i], v[2 * i + 1] * s[2 * i + 1]);
-    load_weight_piece<E>(a.pre, a.weight_dt, at, n[c], v);
-#pragma unroll
-    for (int i = 0; i < N; ++i) w2[c][i] = make_float2(v[2 * i], v[2 * i + 1]);
-  }
-  const auto row_gate = [&](long long row) {
-    return a.gate && !element && row < a.rows ? to_f32(static_cast<const T*>(a.gate)[row * a.ldg]) : 0.f;
-  };
-  float next_gate = row_gate(row0);  // a row ahead
-  const float fcols = static_cast<float>(cols), inv_cols = 1.f / fcols;
-  T* ph = static_cast<T*>(a.h) + row0 * a.ldh + col;
-  T* py = static_cast<T*>(a.y) + row0 * a.ldy + col;
-  // the 8-bit copies: y, h, x, gate; each lane keeps the scales of one of them
-  const bool eight = a.q.data || a.h8.data || a.x8.data || a.gate8.data;
-  uint8_t* p8[4] = {static_cast<uint8_t*>(a.q.data) + row0 * a.q.ld + col, static_cast<uint8_t*>(a.h8.data) + row0 * a.h8.ld + col,
-                    static_cast<uint8_t*>(a.x8.data) + row0 * a.x8.ld + col, static_cast<uint8_t*>(a.gate8.data) + row0 * a.gate8.ld + col};
-  const int mine = Scales::mine(), top = (mine ? a.kept_fmt : a.fmt) ? 15 : 8, cols16 = (cols + 15) & ~15;
-  const long long rows4 = (a.rows + 3) & ~3LL;
-  uint8_t* const scales = static_cast<uint8_t*>(mine == 0 ? a.q.scale : mine == 1 ? a.h8.scale : mine == 2 ? a.x8.scale : a.gate8.scale);
-  uint8_t* ps = scales + row0 * 4;
-  const bool keeper = scales && threadIdx.x % Scales::Q == 0;
-  int slot = 0, turn = 0;
-  // all threads of a CTA take the same number of turns (the barriers of the sums)
-  for (long long row = row0; row - rr < a.rows; row += step, turn += 2) {
-    const bool live = R == 1 || row < a.rows;
-    if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row: earlier, the next kernel's CTAs take SMs from these
-    float2 sig = both(1.f);
-    if (a.gate && !element) sig = both(sigmoid2<T>(both(next_gate)).x), next_gate = row_gate(row + step);
-    fetch(slot == 0 ? S - 1 : slot - 1);
-    cp_async_wait<S - 1>();
-    P h[C];
-    float2 two = both(0.f);
-    float sum[1];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      P x;
-      x.unpack(ring.piece(slot, 0, c));
-#pragma unroll
-      for (int i = 0; i < N; ++i) two = fma2(x.v[i], x.v[i], two);
-    }
-    sum[0] = total(two);
-    sums(sum, turn);
-    const float rx = row_rstd(sum[0], fcols, inv_cols, a.eps);
-    two = both(0.f);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      P x, g;
-      x.unpack(ring.piece(slot, 0, c));
-      h[c].unpack(ring.piece(slot, 1, c));
-      if (element) g.unpack(ring.piece(slot, 2, c));
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (element) sig = sigmoid2<T>(g.v[i]);
-        const float2 b = mul2(mul2(mul2(x.v[i], both(rx)), w1[c][i]), sig);
-        h[c].v[i] = fma2(both(a.alpha), h[c].v[i], b);
-        two = fma2(h[c].v[i], h[c].v[i], two);
-      }
-    }
-    sum[0] = total(two);
-    sums(sum, turn + 1);
-    const float rh = row_rstd(sum[0], fcols, inv_cols, a.eps);
-    if (live && t == 0 && rank == 0) {
-      if (a.rstd_x) a.rstd_x[row] = rx;
-      if (a.rstd_h) a.rstd_h[row] = rh;
-    }
-    // past the last column everything is 0 (or NaN, where a norm's factor is not finite and so the whole row)
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      P y;
-#pragma unroll
-      for (int i = 0; i < N; ++i) y.v[i] = mul2(mul2(h[c].v[i], both(rh)), w2[c][i]);
-      if (live && a.h) h[c].store(ph + c * PIECE, n[c]);
-      if (live && a.y) y.store(py + c * PIECE, n[c]);
-      if (eight) {
-        P x, g;
-        uint32_t m[4] = {y.largest(), h[c].largest(), 0u, 0u};
-        if (a.x8.data) x.unpack(ring.piece(slot, 0, c)), m[2] = x.largest();
-        if (a.gate8.data) g.unpack(ring.piece(slot, 2, c)), m[3] = g.largest();
-        const Scales s(m, top);
-        if (live && col + c * PIECE < cols16) {
-          if (a.q.data) y.store8(p8[0] + c * PIECE, s.inv[0], a.fmt);
-          if (a.h8.data) h[c].store8(p8[1] + c * PIECE, s.inv[1], a.kept_fmt);
-          if (a.x8.data) x.store8(p8[2] + c * PIECE, s.inv[2], a.kept_fmt);
-          if (a.gate8.data) g.store8(p8[3] + c * PIECE, s.inv[3], a.kept_fmt);
-        }
-        const int kb = (col + c * PIECE) / 128;
-        if (keeper && live && kb * 128 < cols) ps[(kb >> 2) * rows4 * 4 + (kb & 3)] = static_cast<uint8_t>(s.byte);
-      }
-    }
-    ph += step * a.ldh, py += step * a.ldy, ps += step * 4;
-    p8[0] += step * a.q.ld, p8[1] += step * a.h8.ld, p8[2] += step * a.x8.ld, p8[3] += step * a.gate8.ld;
-    slot = slot + 1 == S ? 0 : slot + 1;
-  }
-  // scales of no block or row, up to whole words and to four rows, are 1
-  if (!eight || rank != 0) return;
-  const int blocks = (cols + 127) / 128, end = (cols + 511) / 512 * 4;
-  const auto fill = [&](const muon_fp8_out& o, int kb, long long row) {
-    if (o.data) static_cast<uint8_t*>(o.scale)[fp8_scale_offset(kb, row, rows4)] = 127;
-  };
-  for (long long row = row0; row < a.rows; row += step)
-    for (int kb = blocks + t; kb < end; kb += G) fill(a.q, kb, row), fill(a.h8, kb, row), fill(a.x8, kb, row), fill(a.gate8, kb, row);
-  if (blockIdx.x == 0)
-    for (long long row = a.rows + rr; row < rows4; row += R)
-      for (int kb = t; kb < end; kb += G) fill(a.q, kb, row), fill(a.h8, kb, row), fill(a.x8, kb, row), fill(a.gate8, kb, row);
-}
-
-template <typename T, int G, int C, int S, int MINB, int CL>
-static cudaError_t launch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
-  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
-  constexpr int smem = Ring<T, TH, C, S, 3>::BYTES;
-  static_assert(smem * MINB <= 220 * 1024, "shared memory of an SM");
-  static bool done[64] = {false};
-  static int known[64] = {0};
-  const auto kernel = block_norm_ring_kernel<T, G, C, S, MINB, CL>;
-  cudaError_t e = smem_limit(kernel, smem, done);
-  if (e != cudaSuccess) return e;
-  int most = MINB * sms;
-  if (CL > 1) {
-    e = resident_clusters(kernel, TH, smem, CL, known, &most);
-    if (e != cudaSuccess) return e;
-  }
-  const long long want = (a.rows + R - 1) / R;
-  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(std::min<long long>(want, most)) * CL), dim3(TH), smem, CL, st, a);
-}
-
-// Threads, pieces and CTAs of a row by its width.
-template <typename T>
-static cudaError_t dispatch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
-  constexpr int E = 16 / static_cast<int>(sizeof(T));
-  const int pieces = static_cast<int>((a.cols + E - 1) / E);
-  if (pieces <= 32) return launch_ring<T, 32, 1, 8, 4, 1>(a, sms, st);
-  if (pieces <= 64) return launch_ring<T, 64, 1, 6, 5, 1>(a, sms, st);
-  if (pieces <= 128) return launch_ring<T, 128, 1, 6, 5, 1>(a, sms, st);
-  if (pieces <= 256) return launch_ring<T, 256, 1, 6, 3, 1>(a, sms, st);
-  if (pieces <= 512) return launch_ring<T, 256, 2, 4, 2, 1>(a, sms, st);
-  if (pieces <= 1024) return launch_ring<T, 512, 2, 4, 1, 1>(a, sms, st);
-  if (pieces <= 2048) return launch_ring<T, 512, 2, 4, 1, 2>(a, sms, st);
-  if (pieces <= 4096) return launch_ring<T, 512, 2, 4, 1, 4>(a, sms, st);
-  return launch_ring<T, 512, 2, 4, 1, 8>(a, sms, st);
-}
-
-template <typename T>
-static cudaError_t dispatch_norm(const muon_block_norm_args& a, cudaStream_t st) {
-  const auto go = [&](auto kernel, int warps) {
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(a.rows)), dim3(warps * 32), 0, st, a);
-  };
-  if (a.cols <= 512) return go(block_norm_kernel<T, 4, 1>, 4);
-  if (a.cols <= 2048) return go(block_norm_kernel<T, 8, 2>, 8);
-  if (a.cols <= 4096) return go(block_norm_kernel<T, 16, 2>, 16);
-  if (a.cols <= 16384) return go(block_norm_kernel<T, 16, 8>, 16);
-  return go(block_norm_kernel<T, 16, 0>, 16);
-}
+// the other types are compiled in files of their own
+extern template cudaError_t launch_block_norm_rows<__half>(const muon_block_norm_args&, int, int, cudaStream_t);
+extern template cudaError_t launch_block_norm_rows<float>(const muon_block_norm_args&, int, int, cudaStream_t);
 
 cudaError_t launch_block_norm(const muon_block_norm_args& a, int vec, int sms, cudaStream_t st) {
-  const auto go = [&](auto t) {
-    using T = decltype(t);
-    // 8 CTAs of 1024 pieces hold MUON_MAX_DIM 16-bit columns and half as many of fp32
-    const bool ring = vec && a.cols <= 8 * 1024 * (16 / static_cast<int>(sizeof(T)));
-    return ring ? dispatch_ring<T>(a, sms, st) : dispatch_norm<T>(a, st);
-  };
-  return a.dt == MUON_BF16 ? go(__nv_bfloat16()) : a.dt == MUON_FP16 ? go(__half()) : go(float());
+  if (a.dt == MUON_BF16) return launch_block_norm_rows<__nv_bfloat16>(a, vec, sms, st);
+  return a.dt == MUON_FP16 ? launch_block_norm_rows<__half>(a, vec, sms, st) : launch_block_norm_rows<float>(a, vec, sms, st);
 }
 
 }  // namespace muon

@@ -1,0 +1,402 @@
+// block_norm_grad.cuh -- gradient of the norms around a block, from what the forward pass kept (of the data's type, or in 8
+// bits).  With X = x rho_x and H = h rho_h as kept and c = scale post:
+//
+//   a = dy pre       D = dh + rho_h (a - H mean(a H))       dresidual = alpha D
+//   b = D sigmoid(gate) c       dx = rho_x (b - X mean(b X))       dgate = (1 - sigmoid(gate)) b X
+//   dpre = sum_rows dy H       S = sum_rows D sigmoid(gate) X       dpost = S scale       dscale = S post
+//
+// mean(b X) needs mean(a H) first.  With u = dh + rho_h a and e = sigmoid(gate) c X it is mean(u e) - rho_h mean(a H)
+// mean(H e), so a row takes one pass and one exchange of three sums.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "block_norm.cuh"
+#include "kernels.h"
+#include "pairs.cuh"
+#include "ptx.cuh"
+
+namespace muon {
+
+// A kept matrix: T, or 8 bits.
+template <typename T, bool KEPT8>
+struct Kept {
+  const uint8_t* data;
+  const uint8_t* scale;  // this row's first scale
+  long long rows4;
+  int fmt;
+  __device__ __forceinline__ Kept(const void* p, const void* s, long long ld, long long row, long long rows, int fmt_)
+      : data(static_cast<const uint8_t*>(p) + (p ? row * ld * (KEPT8 ? 1 : static_cast<long long>(sizeof(T))) : 0)),
+        scale(static_cast<const uint8_t*>(s) + (KEPT8 && p ? row * 4 : 0)),
+        rows4((rows + 3) & ~3LL),
+        fmt(fmt_) {}
+  __device__ __forceinline__ float block_scale(int kb) const {
+    return KEPT8 ? fp8_scale_value(scale[(kb >> 2) * rows4 * 4 + (kb & 3)]) : 1.f;
+  }
+  __device__ __forceinline__ float at(int col, float block) const {
+    if constexpr (KEPT8) return fp8_unpack2(data[col], fmt).x * block;
+    else return to_f32(reinterpret_cast<const T*>(data)[col]);
+  }
+};
+
+template <typename T, int W, int K, bool KEPT8>
+__global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_block_norm_grad_args a, float* partial) {
+  constexpr int KK = K ? K : 1;
+  __shared__ float sh[2][3][W];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cols = static_cast<int>(a.cols);
+  const int blocks = (cols + 127) / 128, turns = K ? K : (blocks + W - 1) / W;
+  float* part = partial ? partial + static_cast<long long>(blockIdx.x) * 2 * cols : nullptr;
+  float dpre[KK][4], sx[KK][4];
+#pragma unroll
+  for (int k = 0; k < KK; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dpre[k][j] = sx[k][j] = 0.f;
+  const float inv_n = 1.f / static_cast<float>(cols);
+  int turn = 0;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
+    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+    const T* dh = static_cast<const T*>(a.dh) + (a.dh ? row * a.lddh : 0);
+    const Kept<T, KEPT8> kx(a.x, a.x_scale, a.ldx, row, a.rows, a.kept_fmt), kh(a.h, a.h_scale, a.ldh, row, a.rows, a.kept_fmt);
+    const bool element = a.gate && !a.gate_per_row;
+    const Kept<T, KEPT8> kg(element ? a.gate : nullptr, a.gate_scale, a.ldg, row, a.rows, a.kept_fmt);
+    const float rx = a.rstd_x[row], rh = a.rstd_h[row];
+    const float row_sig = a.gate && !element ? sigmoid<T>(to_f32(static_cast<const T*>(a.gate)[row * a.ldg])) : 1.f;
+    struct Element {
+      float d, u, hn, xn, sig, c;  // dy, dh + rho_h dy pre, H, X, sigmoid(gate), scale post
+    };
+    auto load = [&](int col, float xs, float hs, float gs) {
+      Element e;
+      e.d = to_f32(dy[col]);
+      e.hn = kh.at(col, hs) * rh;
+      e.xn = kx.at(col, xs) * rx;
+      e.sig = element ? sigmoid<T>(kg.at(col, gs)) : row_sig;
+      e.c = load_weight(a.post, a.weight_dt, col, true) * load_weight(a.scale, a.weight_dt, col, true);
+      e.u = fmaf(rh, e.d * load_weight(a.pre, a.weight_dt, col, true), a.dh ? to_f32(dh[col]) : 0.f);
+      return e;
+    };
+    float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < turns; ++k) {
+      const int kb = warp + W * k;
+      if (kb >= blocks) break;
+      const float xs = kx.block_scale(kb), hs = kh.block_scale(kb), gs = element ? kg.block_scale(kb) : 1.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = kb * 128 + lane + 32 * j;
+        if (col >= cols) break;
+        const Element e = load(col, xs, hs, gs);
+        const float f = e.sig * e.c * e.xn;
+        sum[0] = fmaf(e.d * load_weight(a.pre, a.weight_dt, col, true), e.hn, sum[0]);
+        sum[1] = fmaf(e.u, f, sum[1]);
+        sum[2] = fmaf(e.hn, f, sum[2]);
+      }
+    }
+    cta_sums<W, 3>(sum, sh, turn);
+    const float k1 = sum[0] * inv_n * rh, along = sum[1] - k1 * sum[2], k2 = along * inv_n;
+    if (threadIdx.x == 0 && a.dgate && !element) static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>((1.f - row_sig) * along);
+#pragma unroll
+    for (int k = 0; k < turns; ++k) {
+      const int kb = warp + W * k, kk = K ? k : 0;
+      if (kb >= blocks) break;
+      const float xs = kx.block_scale(kb), hs = kh.block_scale(kb), gs = element ? kg.block_scale(kb) : 1.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = kb * 128 + lane + 32 * j;
+        if (col >= cols) break;
+        const Element e = load(col, xs, hs, gs);
+        const float d = e.u - k1 * e.hn, t = d * e.sig, b = t * e.c;
+        if (a.dresidual) static_cast<T*>(a.dresidual)[row * a.lddr + col] = from_f32<T>(a.alpha * d);
+        if (a.dx) static_cast<T*>(a.dx)[row * a.lddx + col] = from_f32<T>(rx * (b - e.xn * k2));
+        if (a.dgate && element) static_cast<T*>(a.dgate)[row * a.lddgate + col] = from_f32<T>((1.f - e.sig) * (b * e.xn));
+        if (K) {
+          dpre[kk][j] = fmaf(e.d, e.hn, dpre[kk][j]);
+          sx[kk][j] = fmaf(t, e.xn, sx[kk][j]);
+        } else if (part) {  // this thread alone holds these columns of the CTA's sums
+          part[col] = (turn ? part[col] : 0.f) + e.d * e.hn;
+          part[cols + col] = (turn ? part[cols + col] : 0.f) + t * e.xn;
+        }
+      }
+    }
+  }
+  if (!K || !part) return;
+#pragma unroll
+  for (int k = 0; k < KK; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = (warp + W * k) * 128 + lane + 32 * j;
+      if (col < cols) part[col] = dpre[k][j], part[cols + col] = sx[k][j];
+    }
+}
+
+// ------------------------------------------------------------------ ring of rows
+template <int BYTES>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int bytes) {  // the rest is zero
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "n"(BYTES), "r"(bytes)
+               : "memory");
+}
+
+// A thread's slots: S rows of dy, dh, x, h and gate, a piece each; kept 8-bit ones take E bytes instead of 16.
+template <typename T, int TH, int S, bool KEPT8>
+struct GradRing {
+  static constexpr int E = 16 / static_cast<int>(sizeof(T)), WIDE = KEPT8 ? 2 : 5;
+  static constexpr int STAGE = TH * (WIDE * 16 + (5 - WIDE) * E), BYTES = S * STAGE;
+  uint8_t* base;
+  __device__ __forceinline__ uint8_t* at(int slot, int arr) const {
+    uint8_t* stage = base + slot * STAGE;
+    if (arr < WIDE) return stage + (arr * TH + static_cast<int>(threadIdx.x)) * 16;
+    return stage + WIDE * TH * 16 + ((arr - WIDE) * TH + static_cast<int>(threadIdx.x)) * E;
+  }
+  // n of the piece's elements exist.
+  __device__ __forceinline__ void fetch(int slot, int arr, const void* src, int n) const {
+    if (arr < WIDE) copy16(smem_u32(at(slot, arr)), src, n * static_cast<int>(sizeof(T)));
+    else copy_small<E>(smem_u32(at(slot, arr)), src, n);
+  }
+};
+
+// CL CTAs of a cluster to a row, G threads of each with a piece of 16 bytes, a ring of S rows.  KEPT: of x, h and an
+// element's gate; 0: T, 1: e4m3, 2: e5m2.  GATE: a gate of every element.  Both compiled apart: chosen at run time they
+// cost 8192 x 4096 a third more instructions, in pieces too small to be overlapped.
+template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE>
+__global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
+    block_norm_grad_ring_kernel(const muon_block_norm_grad_args a, float* partial) {
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
+  constexpr int DY = 0, DH = 1, X = 2, H = 3, GA = 4;
+  using P = Pairs<T>;
+  using K = std::conditional_t<KEPT != 0, uint8_t, T>;
+  using Slots = GradRing<T, TH, S, KEPT != 0>;
+  constexpr int E = P::E, N = P::N;
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ RowSums<G, TH, 3, CL> sums;
+  const Slots ring{ring_smem};
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
+  const int n = max(0, min(E, cols - (rank * G + t) * E));  // existing columns of the piece
+  const int col = n ? (rank * G + t) * E : 0;
+  const long long step = static_cast<long long>(gridDim.x / CL) * R, row0 = static_cast<long long>(blockIdx.x / CL) * R + rr;
+  const long long rows4 = (a.rows + 3) & ~3LL;
+  long long frow = row0;  // next row to fetch
+  const int ndh = a.dh ? n : 0;
+  const T* fdy = static_cast<const T*>(a.dy) + row0 * a.lddy + col;
+  const T* fdh = a.dh ? static_cast<const T*>(a.dh) + row0 * a.lddh + col : fdy;
+  const long long lddh = a.dh ? a.lddh : a.lddy;  // without dh nothing is read, and zeros arrive
+  const K* fx = static_cast<const K*>(a.x) + row0 * a.ldx + col;
+  const K* fh = static_cast<const K*>(a.h) + row0 * a.ldh + col;
+  const K* fg = static_cast<const K*>(a.gate) + (GATE ? row0 * a.ldg + col : 0);
+  auto fetch = [&](int slot) {
+    if (frow < a.rows) {
+      ring.fetch(slot, DY, fdy, n);
+      ring.fetch(slot, DH, fdh, ndh);
+      ring.fetch(slot, X, fx, n);
+      ring.fetch(slot, H, fh, n);
+      if (GATE) ring.fetch(slot, GA, fg, n);
+    }
+    cp_async_commit();
+    frow += step, fdy += step * a.lddy, fdh += step * lddh, fx += step * a.ldx, fh += step * a.ldh;
+    if (GATE) fg += step * a.ldg;
+  };
+  const auto read_kept = [&](int slot, int arr, P& p) {
+    if constexpr (KEPT == 0) p.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, arr)));
+    else p.template unpack8<KEPT == 2>(ring.at(slot, arr));
+  };
+  if (CL > 1) cluster_sync();  // the others' shared memory is there
+  pdl_wait();
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(s);
+  float2 w1[N], w2[N], dpre[N], sx[N];  // scale post, pre, and the columns' sums
+  {
+    float v[E], s[E];
+    load_weight_piece<E>(a.scale, a.weight_dt, col, n, s);
+    load_weight_piece<E>(a.post, a.weight_dt, col, n, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w1[i] = make_float2(v[2 * i] * s[2 * i], v[2 * i + 1] * s[2 * i + 1]);
+    load_weight_piece<E>(a.pre, a.weight_dt, col, n, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w2[i] = make_float2(v[2 * i], v[2 * i + 1]), dpre[i] = sx[i] = both(0.f);
+  }
+  // of a row: the norms' factors, its gate, the scales of the kept pieces; fetched a row ahead
+  struct RowHead {
+    float rx, rh, gate;
+    uint32_t xs, hs, gs;
+  };
+  const bool row_gated = !GATE && a.gate;
+  const float* prx = a.rstd_x + row0;
+  const float* prh = a.rstd_h + row0;
+  long long so = fp8_scale_offset(col / 128, row0, rows4);
+  const auto head = [&](long long row) {
+    RowHead r = {};
+    if (row < a.rows) {
+      r.rx = __ldg(prx);
+      r.rh = __ldg(prh);
+      if (row_gated) r.gate = to_f32(static_cast<const T*>(a.gate)[row * a.ldg]);
+      if (KEPT) {
+        r.xs = __ldg(static_cast<const uint8_t*>(a.x_scale) + so);
+        r.hs = __ldg(static_cast<const uint8_t*>(a.h_scale) + so);
+        if (GATE) r.gs = __ldg(static_cast<const uint8_t*>(a.gate_scale) + so);
+      }
+    }
+    prx += step, prh += step, so += 4 * step;
+    return r;
+  };
+  RowHead next = head(row0);
+  const float inv_cols = 1.f / static_cast<float>(cols);
+  T* pdr = static_cast<T*>(a.dresidual) + row0 * a.lddr + col;
+  T* pdx = static_cast<T*>(a.dx) + row0 * a.lddx + col;
+  T* pdg = static_cast<T*>(a.dgate) + (GATE ? row0 * a.lddgate + col : 0);
+  const int ndr = a.dresidual ? n : 0, ndx = a.dx ? n : 0, ndg = GATE && a.dgate ? n : 0;
+  const bool gate_out = row_gated && a.dgate && t == 0 && rank == 0;
+  int slot = 0, turn = 0;
+  for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
+    const bool live = R == 1 || row < a.rows;
+    if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row, as in the forward kernel
+    const RowHead now = next;
+    next = head(row + step);
+    fetch(slot == 0 ? S - 1 : slot - 1);
+    cp_async_wait<S - 1>();
+    P d, u, sig, xn, hn;
+    d.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, DY)));
+    u.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, DH)));
+    read_kept(slot, X, xn);
+    read_kept(slot, H, hn);
+    if (GATE) read_kept(slot, GA, sig);
+    if (R > 1 && !live) {  // the slot holds another row's remains
+#pragma unroll
+      for (int i = 0; i < N; ++i) d.v[i] = xn.v[i] = hn.v[i] = u.v[i] = sig.v[i] = both(0.f);
+    }
+    const float2 xf = both(KEPT ? now.rx * fp8_scale_value(now.xs) : now.rx), hf = both(KEPT ? now.rh * fp8_scale_value(now.hs) : now.rh);
+    const float2 gf = both(KEPT ? fp8_scale_value(now.gs) : 1.f);
+    const float row_sig = row_gated ? sigmoid2<T>(both(now.gate)).x : 1.f;
+    float2 s0 = both(0.f), s1 = s0, s2 = s0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      hn.v[i] = mul2(hn.v[i], hf);
+      xn.v[i] = mul2(xn.v[i], xf);
+      const float2 ad = mul2(d.v[i], w2[i]);
+      u.v[i] = fma2(both(now.rh), ad, u.v[i]);
+      sig.v[i] = GATE ? sigmoid2<T>(KEPT ? mul2(sig.v[i], gf) : sig.v[i]) : both(row_sig);
+      const float2 e = mul2(mul2(sig.v[i], w1[i]), xn.v[i]);
+      s0 = fma2(ad, hn.v[i], s0);
+      s1 = fma2(u.v[i], e, s1);
+      s2 = fma2(hn.v[i], e, s2);
+      dpre[i] = fma2(d.v[i], hn.v[i], dpre[i]);
+    }
+    float sum[3] = {total(s0), total(s1), total(s2)};
+    sums(sum, turn);
+    const float k1 = sum[0] * inv_cols * now.rh, along = sum[1] - k1 * sum[2], k2 = along * inv_cols;
+    if (gate_out && live) static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>((1.f - row_sig) * along);
+    P dr, dx, dg;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 v = fma2(both(-k1), hn.v[i], u.v[i]), td = mul2(v, sig.v[i]), b = mul2(td, w1[i]);
+      sx[i] = fma2(td, xn.v[i], sx[i]);
+      dr.v[i] = mul2(both(a.alpha), v);
+      dx.v[i] = mul2(both(now.rx), fma2(both(-k2), xn.v[i], b));
+      if (GATE) dg.v[i] = mul2(fma2(both(-1.f), sig.v[i], both(1.f)), mul2(b, xn.v[i]));
+    }
+    if (live) {
+      dr.store(pdr, ndr);
+      dx.store(pdx, ndx);
+      if (GATE) dg.store(pdg, ndg);
+    }
+    pdr += step * a.lddr, pdx += step * a.lddx;
+    if (GATE) pdg += step * a.lddgate;
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+  if (!partial) return;
+  float* part = partial + static_cast<long long>(blockIdx.x / CL) * 2 * cols;
+  if (R > 1) {  // join the CTA's row groups through the ring's memory
+    static_assert(R == 1 || (R - 1) * 2 * N * G * 8 <= Slots::BYTES, "room to join");
+    cp_async_wait<0>();
+    __syncthreads();
+    float2* all = reinterpret_cast<float2*>(ring_smem);  // [R - 1][2][N][G]
+    if (rr > 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        all[(((rr - 1) * 2 + 0) * N + i) * G + t] = dpre[i];
+        all[(((rr - 1) * 2 + 1) * N + i) * G + t] = sx[i];
+      }
+    }
+    __syncthreads();
+    if (rr > 0) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      for (int r = 1; r < R; ++r) {
+        dpre[i] = add2(dpre[i], all[(((r - 1) * 2 + 0) * N + i) * G + t]);
+        sx[i] = add2(sx[i], all[(((r - 1) * 2 + 1) * N + i) * G + t]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float* p = part + col + 2 * i;
+    if (2 * i < n) p[0] = dpre[i].x, p[cols] = sx[i].x;
+    if (2 * i + 1 < n) p[1] = dpre[i].y, p[cols + 1] = sx[i].y;
+  }
+}
+
+// The kernels add up rows of `partial` for at most this many CTAs (or clusters).
+inline int most_ctas(int sms) { return kBlockNormCtasPerSm * sms; }
+
+template <typename T, bool KEPT8>
+static cudaError_t dispatch_grad(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
+  *ctas = static_cast<int>(std::min<long long>(a.rows, 2 * sms));
+  const auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, dim3(*ctas), dim3(warps * 32), 0, st, a, partial); };
+  if (a.cols <= 512) return go(block_norm_grad_kernel<T, 4, 1, KEPT8>, 4);
+  if (a.cols <= 2048) return go(block_norm_grad_kernel<T, 8, 2, KEPT8>, 8);
+  if (a.cols <= 4096) return go(block_norm_grad_kernel<T, 16, 2, KEPT8>, 16);
+  if (a.cols <= 16384) return go(block_norm_grad_kernel<T, 16, 8, KEPT8>, 16);
+  return go(block_norm_grad_kernel<T, 16, 0, KEPT8>, 16);
+}
+
+template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE>
+static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
+  constexpr int TH = G < 128 ? 128 : G, R = TH / G;
+  constexpr int smem = GradRing<T, TH, S, KEPT != 0>::BYTES;
+  static_assert(smem * MINB <= 224 * 1024, "shared memory of an SM");
+  static_assert(MINB <= kBlockNormCtasPerSm, "rows of partial");
+  static bool done[64] = {false};
+  static int known[64] = {0};
+  const auto kernel = block_norm_grad_ring_kernel<T, G, S, MINB, CL, KEPT, GATE>;
+  cudaError_t e = smem_limit(kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  int most = MINB * sms;
+  if (CL > 1) {
+    e = resident_clusters(kernel, TH, smem, CL, known, &most);
+    if (e != cudaSuccess) return e;
+  }
+  *ctas = static_cast<int>(std::min<long long>((a.rows + R - 1) / R, std::min(most, most_ctas(sms))));
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(*ctas * CL)), dim3(TH), smem, CL, st, a, partial);
+}
+
+// Threads and CTAs of a row by its width.
+template <typename T, int KEPT, bool GATE>
+static cudaError_t dispatch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const int pieces = static_cast<int>((a.cols + E - 1) / E);
+  if (pieces <= 32) return launch_ring<T, 32, 4, 4, 1, KEPT, GATE>(a, partial, sms, ctas, st);
+  if (pieces <= 64) return launch_ring<T, 64, 4, 4, 1, KEPT, GATE>(a, partial, sms, ctas, st);
+  if (pieces <= 128) return launch_ring<T, 128, 4, 4, 1, KEPT, GATE>(a, partial, sms, ctas, st);
+  if (pieces <= 256) return launch_ring<T, 256, 4, 2, 1, KEPT, GATE>(a, partial, sms, ctas, st);
+  if (pieces <= 512) return launch_ring<T, 512, 5, 1, 1, KEPT, GATE>(a, partial, sms, ctas, st);
+  if (pieces <= 1024) return launch_ring<T, 512, 5, 1, 2, KEPT, GATE>(a, partial, sms, ctas, st);
+  if (pieces <= 2048) return launch_ring<T, 512, 5, 1, 4, KEPT, GATE>(a, partial, sms, ctas, st);
+  return launch_ring<T, 512, 5, 1, 8, KEPT, GATE>(a, partial, sms, ctas, st);
+}
+
+template <typename T>
+cudaError_t launch_block_norm_grad_rows(const muon_block_norm_grad_args& a, float* partial, int vec, int sms, int* ctas, cudaStream_t st) {
+  // 8 CTAs of 512 pieces: 32768 16-bit columns, half as many of fp32
+  if (!vec || a.cols > 8 * 512 * (16 / static_cast<int>(sizeof(T))))
+    return a.x_scale ? dispatch_grad<T, true>(a, partial, sms, ctas, st) : dispatch_grad<T, false>(a, partial, sms, ctas, st);
+  const int kept = !a.x_scale ? 0 : a.kept_fmt ? 2 : 1;
+  const auto go = [&](auto gate) {
+    constexpr bool GATE = decltype(gate)::value;
+    if (kept == 0) return dispatch_ring<T, 0, GATE>(a, partial, sms, ctas, st);
+    return kept == 1 ? dispatch_ring<T, 1, GATE>(a, partial, sms, ctas, st) : dispatch_ring<T, 2, GATE>(a, partial, sms, ctas, st);
+  };
+  return a.gate && !a.gate_per_row ? go(std::true_type()) : go(std::false_type());
+}
+
+}  // namespace muon
