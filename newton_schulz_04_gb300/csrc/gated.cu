@@ -13,10 +13,12 @@
 // from f and f' in registers and leave through shared memory.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "block_norm.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace muon {
@@ -24,6 +26,24 @@ namespace muon {
 struct Activation {
   float value, slope;
 };
+template <typename T, bool GELU>
+__device__ __forceinline__ float2 activation2(float2 g) {
+  if (GELU) return make_float2(g.x * normcdff(g.x), g.y * normcdff(g.y));
+  return mul2(g, sigmoid2<T>(g));
+}
+// The first n elements at p, the rest 0.
+template <typename T>
+__device__ __forceinline__ uint4 load_part(const T* p, int n) {
+  union {
+    uint4 w;
+    T e[16 / sizeof(T)];
+  } u;
+  u.w = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i)
+    if (i < n) u.e[i] = p[i];
+  return u.w;
+}
 template <typename T, bool GELU>
 __device__ __forceinline__ Activation activate(float g) {
   if (GELU) {
@@ -34,48 +54,109 @@ __device__ __forceinline__ Activation activate(float g) {
   return {v, fmaf(v, 1.f - s, s)};
 }
 
-// ------------------------------------------------------------------ forward: a block of 128 columns to a warp
-template <typename T, bool GELU>
+// ------------------------------------------------------------------ forward
+// A block of 128 columns to 16 lanes (32 in fp32), U rows to a lane, fetched together.  EIGHT: 8-bit outputs; 0: none, 1: any, 2:
+// both checkpoints, and all of e4m3.  ANYWHERE: rows that do not start on 16 bytes.
+constexpr int kGatedRows = 2;
+template <typename T, bool GELU, int EIGHT, bool ANYWHERE>
 __global__ void __launch_bounds__(256) gated_kernel(const muon_gated_args a) {
+  using P = Pairs<T>;
+  constexpr int E = P::E, N = P::N, LANES = 128 / E, GROUPS = 256 / LANES, U = kGatedRows;
+  using Scales = Scales4<LANES>;
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x % 32, kb = blockIdx.y * 8 + threadIdx.x / 32;
-  const long long row = blockIdx.x;
-  const int cols = static_cast<int>(a.cols), padded = (cols + 511) / 512 * 4;
-  if (kb >= padded) return;
-  const T* gate = static_cast<const T*>(a.gate) + row * a.ldg;
-  const T* up = static_cast<const T*>(a.up) + row * a.ldu;
-  float g[4], u[4], y[4];
+  const int t = threadIdx.x % LANES, kb = blockIdx.x, cols = static_cast<int>(a.cols), col = kb * 128 + t * E, left = cols - col;
+  const long long group = blockIdx.y + static_cast<long long>(blockIdx.z) * gridDim.y, row0 = group * GROUPS * U + threadIdx.x / LANES;
+  const T* gate = static_cast<const T*>(a.gate);
+  const T* up = static_cast<const T*>(a.up);
+  uint4 rg[U], ru[U];
+  if constexpr (ANYWHERE) {
+    const Span sg = Span::of<T>(gate, a.rows, cols, a.ldg), su = Span::of<T>(up, a.rows, cols, a.ldu);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const long long col = kb * 128LL + lane + 32 * j;
-    const bool in = col < cols;
-    g[j] = in ? to_f32(gate[col]) : 0.f;
-    u[j] = in ? to_f32(up[col]) : 0.f;
-  }
+    for (int u = 0; u < U; ++u) {
+      const long long row = row0 + u * GROUPS;
+      const bool in = row < a.rows;
+      rg[u] = load_anywhere<T, LANES>(gate + (in ? row * a.ldg : 0), col / E, in ? left : 0, sg);
+      ru[u] = load_anywhere<T, LANES>(up + (in ? row * a.ldu : 0), col / E, in ? left : 0, su);
+    }
+  } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const long long col = kb * 128LL + lane + 32 * j;
-    y[j] = activate<T, GELU>(g[j]).value * u[j];
-    if (a.y && col < cols) static_cast<T*>(a.y)[row * a.ldy + col] = from_f32<T>(y[j]);
+    for (int u = 0; u < U; ++u) {
+      const long long row = row0 + u * GROUPS;
+      rg[u] = ru[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < a.rows && left >= E) {
+        rg[u] = *reinterpret_cast<const uint4*>(gate + row * a.ldg + col);
+        ru[u] = *reinterpret_cast<const uint4*>(up + row * a.ldu + col);
+      } else if (row < a.rows && left > 0) {
+        rg[u] = load_part(gate + row * a.ldg + col, left);
+        ru[u] = load_part(up + row * a.ldu + col, left);
+      }
+    }
   }
-  // blocks past the last column, up to a whole scale word, hold zeros
-  if (a.q.data) store_block8(a.q, a.fmt, row, a.rows, cols, kb, y);
-  if (a.gate8.data) store_block8(a.gate8, a.kept_fmt, row, a.rows, cols, kb, g);
-  if (a.up8.data) store_block8(a.up8, a.kept_fmt, row, a.rows, cols, kb, u);
+  const long long rows4 = (a.rows + 3) & ~3LL;
+  const int mine = Scales::mine(), cols16 = (cols + 15) & ~15;
+  const int top = (mine ? a.kept_fmt : a.fmt) ? 15 : 8;
+  uint8_t* const scales = static_cast<uint8_t*>(mine == 0 ? a.q.scale : mine == 1 ? a.gate8.scale : mine == 2 ? a.up8.scale : nullptr);
+  const bool keeper = scales && threadIdx.x % Scales::Q == 0;
+  const int more = kb * 128 + 128 >= cols ? (cols + 511) / 512 * 4 - kb : 1;  // up to a whole scale word, in the last block
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = row0 + u * GROUPS;
+    const bool live = row < a.rows;
+    P g, v, y;
+    g.unpack(rg[u]);
+    v.unpack(ru[u]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) y.v[i] = mul2(activation2<T, GELU>(g.v[i]), v.v[i]);
+    if (a.y) {
+      if constexpr (ANYWHERE) store_anywhere<T, LANES>(static_cast<T*>(a.y) + (live ? row * a.ldy : 0), col / E, live ? left : 0, y);
+      else if (live) y.store(static_cast<T*>(a.y) + row * a.ldy + col, min(E, left));
+    }
+    if (EIGHT) {
+      const uint32_t m[4] = {y.largest(), g.largest(), v.largest(), 0u};
+      const Scales s(m, top);
+      if (live && col < cols16) {
+        if constexpr (EIGHT == 2) {
+          if (a.q.data) y.template store8<false>(static_cast<uint8_t*>(a.q.data) + row * a.q.ld + col, s.inv[0]);
+          g.template store8<false>(static_cast<uint8_t*>(a.gate8.data) + row * a.gate8.ld + col, s.inv[1]);
+          v.template store8<false>(static_cast<uint8_t*>(a.up8.data) + row * a.up8.ld + col, s.inv[2]);
+        } else {
+          if (a.q.data) y.store8(static_cast<uint8_t*>(a.q.data) + row * a.q.ld + col, s.inv[0], a.fmt);
+          if (a.gate8.data) g.store8(static_cast<uint8_t*>(a.gate8.data) + row * a.gate8.ld + col, s.inv[1], a.kept_fmt);
+          if (a.up8.data) v.store8(static_cast<uint8_t*>(a.up8.data) + row * a.up8.ld + col, s.inv[2], a.kept_fmt);
+        }
+      }
+      if (keeper) {  // scales of no block or row, up to whole words and to four rows, are 1
+        if (row < rows4) scales[fp8_scale_offset(kb, row, rows4)] = static_cast<uint8_t>(live ? s.byte : 127u);
+        if (more > 1 && row < rows4)
+          for (int k = 1; k < more; ++k) scales[fp8_scale_offset(kb + k, row, rows4)] = 127;
+      }
+    }
+  }
 }
 
 template <typename T>
-static cudaError_t dispatch_gated(const muon_gated_args& a, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.rows), static_cast<unsigned>(((a.cols + 511) / 512 * 4 + 7) / 8));
-  return a.act ? launch_pdl(gated_kernel<T, true>, grid, dim3(256), 0, st, a)
-               : launch_pdl(gated_kernel<T, false>, grid, dim3(256), 0, st, a);
+static cudaError_t dispatch_gated(const muon_gated_args& a, int vec, cudaStream_t st) {
+  constexpr int ROWS = 256 * 16 / static_cast<int>(sizeof(T)) / 128 * kGatedRows;  // of a CTA
+  const long long groups = (a.rows + ROWS - 1) / ROWS;
+  const long long y = std::min(groups, 32768LL);
+  const dim3 grid(static_cast<unsigned>((a.cols + 127) / 128), static_cast<unsigned>(y), static_cast<unsigned>((groups + y - 1) / y));
+  const bool any = a.q.data || a.gate8.data || a.up8.data;
+  const bool e4m3 = a.gate8.data && a.up8.data && a.kept_fmt == MUON_E4M3 && (!a.q.data || a.fmt == MUON_E4M3);
+  const auto go = [&](auto gelu, auto anywhere) {
+    constexpr bool G = decltype(gelu)::value, A = decltype(anywhere)::value;
+    if (!any) return launch_pdl(gated_kernel<T, G, 0, A>, grid, dim3(256), 0, st, a);
+    return e4m3 ? launch_pdl(gated_kernel<T, G, 2, A>, grid, dim3(256), 0, st, a)
+                : launch_pdl(gated_kernel<T, G, 1, A>, grid, dim3(256), 0, st, a);
+  };
+  const auto by_act = [&](auto anywhere) { return a.act ? go(std::true_type(), anywhere) : go(std::false_type(), anywhere); };
+  return vec ? by_act(std::false_type()) : by_act(std::true_type());
 }
 
 cudaError_t launch_gated(const muon_gated_args& a, int vec, cudaStream_t st) {
-  if (a.dt == MUON_BF16) return dispatch_gated<__nv_bfloat16>(a, st);
-  if (a.dt == MUON_FP16) return dispatch_gated<__half>(a, st);
-  return dispatch_gated<float>(a, st);
+  if (a.dt == MUON_BF16) return dispatch_gated<__nv_bfloat16>(a, vec, st);
+  if (a.dt == MUON_FP16) return dispatch_gated<__half>(a, vec, st);
+  return dispatch_gated<float>(a, vec, st);
 }
 
 // ------------------------------------------------------------------ gradient

@@ -54,16 +54,14 @@ struct Pairs {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = fp8_unpack2<E5M2>(w[i / 2] >> (16 * (i & 1)));
   }
+  __device__ __forceinline__ uint4 packed() const {
+    if constexpr (sizeof(T) == 2) return make_uint4(pack2(v[0], T()), pack2(v[1], T()), pack2(v[2], T()), pack2(v[3], T()));
+    else return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+  }
   // n of the elements exist.
   __device__ __forceinline__ void store(T* p, int n) const {
     if (n == E) {
-      uint4 w;
-      if constexpr (sizeof(T) == 2) {
-        w = make_uint4(pack2(v[0], T()), pack2(v[1], T()), pack2(v[2], T()), pack2(v[3], T()));
-      } else {
-        w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
-      }
-      *reinterpret_cast<uint4*>(p) = w;
+      *reinterpret_cast<uint4*>(p) = packed();
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -116,6 +114,92 @@ __device__ __forceinline__ float2 sigmoid2(float2 g) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
     return r;
   }
+}
+
+// ---- rows that do not start on 16 bytes
+// 16 bytes from byte o (0 .. 15, the same in all lanes) of the 32 bytes lo, hi.
+__device__ __forceinline__ uint4 window(const uint4& lo, const uint4& hi, int o) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const bool eight = o & 8, four = o & 4;
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = eight ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = four ? w[i + 1] : w[i];
+  const int bits = 8 * (o & 3);
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+// The aligned 16 bytes at p as far as they lie in [from, to), the rest as 0.  T: what the memory holds.
+template <typename T>
+__device__ __forceinline__ uint4 load_granule(const uint8_t* p, const uint8_t* from, const uint8_t* to) {
+  if (p >= from && p + 16 <= to) return *reinterpret_cast<const uint4*>(p);
+  union {
+    uint4 w;
+    T e[16 / sizeof(T)];
+  } u;
+  u.w = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i) {
+    const uint8_t* q = p + i * sizeof(T);
+    if (q >= from && q < to) u.e[i] = *reinterpret_cast<const T*>(q);
+  }
+  return u.w;
+}
+// A matrix whose rows start anywhere: its memory's ends, so that whole 16 bytes are read only where they lie within.
+struct Span {
+  const uint8_t *from, *to;
+  template <typename T>
+  static __device__ __forceinline__ Span of(const void* p, long long rows, long long cols, long long ld) {
+    const uint8_t* b = static_cast<const uint8_t*>(p);
+    return {b, b + ((rows - 1) * ld + cols) * static_cast<long long>(sizeof(T))};
+  }
+};
+// Pieces of one row in LANES neighbouring lanes: piece t of a row of `cols` columns, of which `left` = cols - t E (0 or less:
+// none) are there from its first on.  What a neighbour has of a lane's 16 bytes comes from it; the lanes at the ends fetch
+// or write the rest themselves.  All lanes of a warp call.
+template <typename T, int LANES>
+__device__ __forceinline__ uint4 load_anywhere(const T* row, int t, int left, const Span& s) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x % LANES;
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(row) - off + 16LL * t;
+  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+  if (left > 0) lo = load_granule<T>(p, s.from, s.to);
+  const bool end = lane == LANES - 1 || left <= E;
+  if (end && left * static_cast<int>(sizeof(T)) > 16 - off) hi = load_granule<T>(p + 16, s.from, s.to);
+  const uint4 next = make_uint4(__shfl_down_sync(0xffffffffu, lo.x, 1, LANES), __shfl_down_sync(0xffffffffu, lo.y, 1, LANES),
+                                __shfl_down_sync(0xffffffffu, lo.z, 1, LANES), __shfl_down_sync(0xffffffffu, lo.w, 1, LANES));
+  union {
+    uint4 w;
+    T e[E];
+  } u;
+  u.w = window(lo, end ? hi : next, off);
+  if (left < E) {  // the next row's
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i >= left) u.e[i] = from_f32<T>(0.f);
+  }
+  return u.w;
+}
+template <typename T, int LANES>
+__device__ __forceinline__ void store_anywhere(T* row, int t, int left, const Pairs<T>& v) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x % LANES;
+  union {
+    uint4 w;
+    T e[E];
+  } u;
+  u.w = v.packed();
+  const uint4 before = make_uint4(__shfl_up_sync(0xffffffffu, u.w.x, 1, LANES), __shfl_up_sync(0xffffffffu, u.w.y, 1, LANES),
+                                  __shfl_up_sync(0xffffffffu, u.w.z, 1, LANES), __shfl_up_sync(0xffffffffu, u.w.w, 1, LANES));
+  const int head = E - off / static_cast<int>(sizeof(T));  // elements of the piece in its first 16 aligned bytes
+  uint8_t* p = reinterpret_cast<uint8_t*>(row) - off + 16LL * t;
+  const bool whole = left >= head && (lane > 0 || off == 0);
+  if (whole) *reinterpret_cast<uint4*>(p) = off ? window(before, u.w, 16 - off) : u.w;
+  // the rest: before the first lane's next 16 bytes, behind the last one's, and a row's end
+  const bool tail = lane == LANES - 1 || left - E < head;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (i < left && (i < head ? !whole : tail)) row[t * E + i] = u.e[i];
 }
 
 // Scales of up to four matrices' blocks, whose 128 columns lie in LANES = 16 or 32 neighbouring lanes.  The largest
