@@ -7,10 +7,7 @@
 // Computed in fp32; every output is rounded once.
 //
 // The gradient's 8-bit operands are needed by rows (the products with the weights) and transposed (the weights'
-// gradients, summed over the rows), and the weight behind y needs y transposed, computed again from what was kept.  A CTA
-// takes a tile of 128 x 128, a warp 8 rows of it, a lane 4 columns: a row's largest magnitude is one reduction of a warp,
-// and its bytes are written at once; the columns' are collected in shared memory, after which the transposed bytes are made
-// from f and f' in registers and leave through shared memory.
+// gradients, summed over the rows), and the weight behind y needs y transposed, computed again from what was kept.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -23,13 +20,51 @@
 
 namespace muon {
 
-struct Activation {
-  float value, slope;
+// Phi of a pair and exp(-g^2 / 2), for 16-bit data: erfc(z) = t R(t) exp(-z^2) with t = 1 / (1 + z / 2), the form of Press et
+// al. (Numerical Recipes, erfcc), with R a polynomial fitted to 1.6e-7 of the value over all z >= 0.  Both tails keep their
+// relative precision; the exponential's, (2 + 0.6 g^2) 2^-23, is the larger part.
+struct Normal {
+  float2 phi, bell;
 };
+__device__ __forceinline__ Normal normal2(float2 g) {
+  const float2 a = make_float2(fabsf(g.x), fabsf(g.y));
+  float2 bell = mul2(mul2(g, g), both(-0.5f * 1.4426950408889634f)), t;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(bell.x) : "f"(bell.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(bell.y) : "f"(bell.y));
+  const float2 d = fma2(a, both(0.3535533905932738f), both(1.f));  // z = |g| / sqrt(2)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(d.y));
+  constexpr float c[10] = {0.28209474704897347f, 0.2821042190368617f,  0.2465122105572134f,    0.1804148380537399f,
+                           0.0582618433141641f,  0.07946854893160596f, -0.19854795364580055f,  0.030752471632890434f,
+                           0.06446185801186056f, -0.02552294149528864f};
+  float2 r = both(c[9]);
+#pragma unroll
+  for (int k = 8; k >= 0; --k) r = fma2(r, t, both(c[k]));
+  const float2 tail = mul2(mul2(mul2(t, both(0.5f)), bell), r), rest = fma2(tail, both(-1.f), both(1.f));
+  return {make_float2(g.x < 0.f ? tail.x : rest.x, g.y < 0.f ? tail.y : rest.y), bell};
+}
+
 template <typename T, bool GELU>
 __device__ __forceinline__ float2 activation2(float2 g) {
-  if (GELU) return make_float2(g.x * normcdff(g.x), g.y * normcdff(g.y));
-  return mul2(g, sigmoid2<T>(g));
+  if constexpr (!GELU) return mul2(g, sigmoid2<T>(g));
+  else if constexpr (sizeof(T) == 4) return make_float2(g.x * normcdff(g.x), g.y * normcdff(g.y));
+  else return mul2(g, normal2(g).phi);
+}
+struct Activation {
+  float2 value, slope;
+};
+template <typename T, bool GELU>
+__device__ __forceinline__ Activation activate2(float2 g) {
+  if constexpr (!GELU) {
+    const float2 s = sigmoid2<T>(g), v = mul2(g, s);
+    return {v, fma2(v, fma2(s, both(-1.f), both(1.f)), s)};
+  } else {
+    Normal n;
+    if constexpr (sizeof(T) == 4)
+      n = {make_float2(normcdff(g.x), normcdff(g.y)), make_float2(expf(-0.5f * g.x * g.x), expf(-0.5f * g.y * g.y))};
+    else n = normal2(g);
+    return {mul2(g, n.phi), fma2(mul2(g, both(0.3989422804014327f)), n.bell, n.phi)};
+  }
 }
 // The first n elements at p, the rest 0.
 template <typename T>
@@ -160,255 +195,360 @@ cudaError_t launch_gated(const muon_gated_args& a, int vec, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ gradient
-// Four neighbouring elements of a row as they are in memory.
-template <typename T>
-struct Four {
-  static constexpr int W = sizeof(T);  // 32-bit words
-  uint32_t w[W];
-  // n exist; `whole`: all four do, and the address allows one access
-  __device__ __forceinline__ void load(const T* p, int n, bool whole) {
-    if (whole) {
-      if constexpr (W == 1) w[0] = *reinterpret_cast<const uint32_t*>(p);
-      if constexpr (W == 2) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        w[0] = x.x, w[1] = x.y;
-      }
-      if constexpr (W == 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-      }
-    } else {
-      union {
-        T e[4];
-        uint32_t u[W];
-      } x;
-#pragma unroll
-      for (int i = 0; i < W; ++i) x.u[i] = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) x.e[i] = p[i];
-#pragma unroll
-      for (int i = 0; i < W; ++i) w[i] = x.u[i];
-    }
-  }
-};
-__device__ __forceinline__ void values(const Four<float>& q, float, int, float (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(q.w[i]);
-}
-__device__ __forceinline__ void values(const Four<__nv_bfloat16>& q, float, int, float (&v)[4]) {
-  v[0] = __uint_as_float(q.w[0] << 16), v[1] = __uint_as_float(q.w[0] & 0xffff0000u);
-  v[2] = __uint_as_float(q.w[1] << 16), v[3] = __uint_as_float(q.w[1] & 0xffff0000u);
-}
-__device__ __forceinline__ void values(const Four<__half>& q, float, int, float (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q.w[i]));
-    v[2 * i] = f.x, v[2 * i + 1] = f.y;
-  }
-}
-__device__ __forceinline__ void values(const Four<uint8_t>& q, float scale, int fmt, float (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 f = fp8_unpack2(q.w[0] >> (16 * i), fmt);
-    v[2 * i] = f.x * scale, v[2 * i + 1] = f.y * scale;
-  }
-}
+// A 128 x 128 tile to a CTA, 16 rows to each of its 8 warps, 4 neighbouring columns to a lane.  A warp copies its rows to shared
+// memory in chunks of 4 and goes through them twice: for the gradients as they are, by rows, and the columns' largest
+// magnitudes, which the CTA then joins; and, with the columns' scales, for the transposed bytes, which take the place of
+// the chunk that they come from (a word of 4 rows for each column and output) and leave from there, 16 rows at a time.
+// Computing everything twice costs a fifth of the instructions and saves the registers that three outputs of a tile
+// would fill, so that three CTAs on an SM overlap one another's copies.
+constexpr int kTile = 128, kTileWarps = 8, kChunkRows = 4, kChunks = kTile / kTileWarps / kChunkRows;
 
+// Four neighbouring elements in shared memory.
+__device__ __forceinline__ void four(const float* p, float2 (&v)[2]) {
+  const float4 f = *reinterpret_cast<const float4*>(p);
+  v[0] = make_float2(f.x, f.y), v[1] = make_float2(f.z, f.w);
+}
 template <typename T>
-__device__ __forceinline__ void store_four(T* p, int n, bool whole, const float (&v)[4]) {
-  if (whole) {
+__device__ __forceinline__ void four(const T* p, float2 (&v)[2]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  v[0] = unpack2(w.x, T()), v[1] = unpack2(w.y, T());
+}
+template <bool E5M2>
+__device__ __forceinline__ void four8(const uint8_t* p, float scale, float2 (&v)[2]) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  v[0] = mul2(fp8_unpack2<E5M2>(w), both(scale));
+  v[1] = mul2(fp8_unpack2<E5M2>(w >> 16), both(scale));
+}
+__device__ __forceinline__ float largest3(float m, float a, float b) {
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return m;
+}
+template <bool E5M2>
+__device__ __forceinline__ uint32_t pack_scaled(float2 a, float2 b, float inv) {
+  a = mul2(a, both(inv)), b = mul2(b, both(inv));
+  return fp8_pack4<E5M2>(a.x, a.y, b.x, b.y);
+}
+// Four elements of a lane's row, its neighbours' before and behind; rows that start anywhere.
+template <typename T>
+__device__ __forceinline__ void store_four_anywhere(T* row, int lane, long long left, const float2 (&v)[2]) {
+  if constexpr (sizeof(T) == 4) {
+    Pairs<T> p;
+    p.v[0] = v[0], p.v[1] = v[1];
+    store_anywhere<T, 32>(row, lane, static_cast<int>(max(-1LL << 30, min(1LL << 30, left))), p);
+  } else {  // as store_anywhere, in pieces of 8 bytes
     union {
+      uint32_t w[2];
       T e[4];
-      uint2 two;
-      uint4 four;
-    } x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.e[i] = from_f32<T>(v[i]);
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = x.two;
-    else *reinterpret_cast<uint4*>(p) = x.four;
-  } else {
+    } u;
+    u.w[0] = pack2(v[0], T()), u.w[1] = pack2(v[1], T());
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 7), head = 4 - off / 2, bits = 64 - 8 * off;
+    const uint32_t b0 = __shfl_up_sync(0xffffffffu, u.w[0], 1), b1 = __shfl_up_sync(0xffffffffu, u.w[1], 1);
+    const bool whole = left >= head && (lane > 0 || off == 0), tail = lane == 31 || left - 4 < head;
+    if (whole) {
+      const unsigned long long before = b0 | static_cast<unsigned long long>(b1) << 32;
+      const unsigned long long own = u.w[0] | static_cast<unsigned long long>(u.w[1]) << 32;
+      *reinterpret_cast<unsigned long long*>(reinterpret_cast<uint8_t*>(row) - off + 8LL * lane) =
+          off ? before >> bits | own << (64 - bits) : own;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = from_f32<T>(v[i]);
+      if (i < left && (i < head ? !whole : tail)) row[lane * 4 + i] = u.e[i];
   }
 }
 
-constexpr int kTile = 128, kTileWarps = 16, kTileRows = kTile / kTileWarps;
-
-// A transposed 8-bit tile on its way out: 8 bytes (8 rows) to a slot, 16 slots to a column, swizzled so that both the
-// writes (a lane has 4 neighbouring columns) and the reads are free of bank conflicts.
-struct TransposedTile {
-  uint2 slot[kTile][16];
-  __device__ __forceinline__ uint2& at(int col, int s) { return slot[col][s ^ ((col >> 2) & 15)]; }
+// KEPT: of gate and up; 0: T, 1: e4m3, 2: e5m2.  ANYWHERE: rows of T that do not start on 16 bytes.
+template <typename T, int KEPT, bool GELU, bool ANYWHERE>
+struct GatedTile {
+  using K = std::conditional_t<KEPT != 0, uint8_t, T>;
+  static constexpr int DY = kTile * static_cast<int>(sizeof(T)), KEEP = kTile * static_cast<int>(sizeof(K));  // bytes of a row
+  static constexpr int CHUNK = kChunkRows * (DY + 2 * KEEP), WARP = kChunks * CHUNK, BYTES = kTileWarps * WARP;
+  static constexpr int CTAS = BYTES <= 72 * 1024 ? 3 : BYTES <= 108 * 1024 ? 2 : 1;  // on an SM
+  static_assert(CHUNK >= 3 * 4 * 128, "a chunk's transposed words");
 };
 
-// Row-wise 8 bits of one row of the tile; a warp's lanes hold its 128 columns.  Returns nothing past the last row.
-__device__ __forceinline__ void store_row8(const muon_fp8_out& o, int fmt, long long row, bool in, long long c0, long long cols,
-                                           long long offset, const float (&v)[4]) {
-  uint32_t m = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
-  m = __reduce_max_sync(0xffffffffu, m);
-  const uint32_t byte = in ? fp8_scale_byte(m, fmt ? 15 : 8) : 127u;
-  const float inv = fp8_inverse_scale(byte);
-  if (in && c0 < ((cols + 15) & ~15LL))
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(o.data) + row * o.ld + c0) =
-        fmt ? fp8_pack4<true>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv)
-            : fp8_pack4<false>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-  if (threadIdx.x % 32 == 0 && offset >= 0) static_cast<uint8_t*>(o.scale)[offset] = static_cast<uint8_t>(byte);
-}
-
-template <typename T, bool KEPT8, bool GELU>
-__global__ void __launch_bounds__(kTileWarps * 32, 1) gated_grad_kernel(const muon_gated_grad_args a, const int vec) {
-  using K = std::conditional_t<KEPT8, uint8_t, T>;
+template <typename T, int KEPT, bool GELU, bool ANYWHERE>
+__global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYWHERE>::CTAS)
+    gated_grad_kernel(const muon_gated_grad_args a) {
+  using G = GatedTile<T, KEPT, GELU, ANYWHERE>;
+  using K = typename G::K;
   extern __shared__ __align__(16) uint8_t gated_smem[];
-  TransposedTile* tiles = reinterpret_cast<TransposedTile*>(gated_smem);  // dgate, dup, y
-  __shared__ uint32_t cmax[3][kTile];  // [4 i + j] of the tile's columns at j * 32 + i
-  pdl_launch_dependents();
+  __shared__ uint32_t cmax[3][kTile];  // of column 4 l + j at j * 32 + l; later the inverse scale
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x < kTile) cmax[0][threadIdx.x] = cmax[1][threadIdx.x] = cmax[2][threadIdx.x] = 0u;
-  __syncthreads();
-  pdl_wait();
+  uint8_t* const mine = gated_smem + warp * G::WARP;
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < 3 * kTile; i += kTileWarps * 32) cmax[0][i] = 0u;
   const long long kbc = blockIdx.x, kbr = blockIdx.y, rows = a.rows, cols = a.cols;
-  const long long c0 = kbc * kTile + lane * 4, r0 = kbr * kTile + warp * kTileRows, rows4 = (rows + 3) & ~3LL;
-  const int nc = static_cast<int>(max(0LL, min(4LL, cols - c0)));
-  const bool last = (kbc + 1) * kTile >= cols;
-  const int more = static_cast<int>((cols + 511) / 512 * 4 - kbc - 1);  // blocks up to a whole scale word, in the last tile
-  Four<T> dy[kTileRows];
-  Four<K> up[kTileRows], gate[kTileRows];
-  float gs[kTileRows], us[kTileRows];
+  const long long c00 = kbc * kTile, r0 = kbr * kTile + warp * (kTile / kTileWarps);
+  const long long left = cols - c00;  // columns from the tile's first on
+  pdl_wait();
+  // ---- the warp's rows, a group of copies for each chunk
+  const auto copy = [&](uint8_t* to, const auto* matrix, long long ld, auto anywhere) {  // one row after another
+    using M = std::remove_const_t<std::remove_pointer_t<decltype(matrix)>>;
+    constexpr int E = 16 / static_cast<int>(sizeof(M)), PER_ROW = kTile / E;
+    return [=](int chunk) {
 #pragma unroll
-  for (int i = 0; i < kTileRows; ++i) {
-    const long long row = r0 + i;
-    const bool in = row < rows;
-    const int n = in ? nc : 0;
-    dy[i].load(static_cast<const T*>(a.dy) + (n ? row * a.lddy + c0 : 0), n, n == 4 && vec);
-    gate[i].load(static_cast<const K*>(a.gate) + (n ? row * a.ldg + c0 : 0), n, n == 4 && (KEPT8 || vec));
-    up[i].load(static_cast<const K*>(a.up) + (n ? row * a.ldu + c0 : 0), n, n == 4 && (KEPT8 || vec));
-    gs[i] = us[i] = 1.f;
-    if (KEPT8 && in) {
-      const long long o = fp8_scale_offset(kbc, row, rows4);
-      gs[i] = fp8_scale_value(static_cast<const uint8_t*>(a.gate_scale)[o]);
-      us[i] = fp8_scale_value(static_cast<const uint8_t*>(a.up_scale)[o]);
-    }
-  }
-  float value[kTileRows][4], slope[kTileRows][4];
-  uint32_t cm[3][4];
-#pragma unroll
-  for (int o = 0; o < 3; ++o)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cm[o][j] = 0u;
-#pragma unroll
-  for (int i = 0; i < kTileRows; ++i) {
-    const long long row = r0 + i;
-    const bool in = row < rows;
-    float d[4], g[4], u[4], dg[4], du[4];
-    values(dy[i], 1.f, 0, d);
-    values(gate[i], gs[i], a.kept_fmt, g);
-    values(up[i], us[i], a.kept_fmt, u);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= nc) g[j] = u[j] = 0.f;  // a NaN scale
-      const Activation f = activate<T, GELU>(g[j]);
-      value[i][j] = f.value, slope[i][j] = f.slope;
-      dg[j] = d[j] * u[j] * f.slope;
-      du[j] = d[j] * f.value;
-      cm[0][j] = max(cm[0][j], abs_bits(dg[j]));
-      cm[1][j] = max(cm[1][j], abs_bits(du[j]));
-      cm[2][j] = max(cm[2][j], abs_bits(f.value * u[j]));
-    }
-    if (a.dgate && in) store_four(static_cast<T*>(a.dgate) + row * a.lddgate + c0, nc, nc == 4 && vec, dg);
-    if (a.dup && in) store_four(static_cast<T*>(a.dup) + row * a.lddup + c0, nc, nc == 4 && vec, du);
-    const long long offset = row < rows4 ? fp8_scale_offset(kbc, row, rows4) : -1;
-    if (a.dgate_rows.data) store_row8(a.dgate_rows, a.fmt, row, in, c0, cols, offset, dg);
-    if (a.dup_rows.data) store_row8(a.dup_rows, a.fmt, row, in, c0, cols, offset, du);
-    if (last && offset >= 0 && lane < more) {
-      if (a.dgate_rows.data) static_cast<uint8_t*>(a.dgate_rows.scale)[fp8_scale_offset(kbc + 1 + lane, row, rows4)] = 127;
-      if (a.dup_rows.data) static_cast<uint8_t*>(a.dup_rows.scale)[fp8_scale_offset(kbc + 1 + lane, row, rows4)] = 127;
-    }
-  }
-  if (!a.dgate_cols.data && !a.dup_cols.data && !a.y_cols.data) return;
-#pragma unroll
-  for (int o = 0; o < 3; ++o)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) atomicMax(&cmax[o][j * 32 + lane], cm[o][j]);
-  __syncthreads();
-  const long long cols4 = (cols + 3) & ~3LL, kend = (rows + 511) / 512 * 4;
-  const bool bottom = (kbr + 1) * kTile >= rows;
-#pragma unroll
-  for (int o = 0; o < 3; ++o) {
-    const muon_fp8_out& out = o == 0 ? a.dgate_cols : o == 1 ? a.dup_cols : a.y_cols;
-    if (!out.data) continue;
-    const int fmt = o < 2 ? a.fmt : a.y_fmt;
-    float inv[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t byte = j < nc ? fp8_scale_byte(cmax[o][j * 32 + lane], fmt ? 15 : 8) : 127u;
-      inv[j] = fp8_inverse_scale(byte);
-      if (warp == 0 && c0 + j < cols4) {
-        static_cast<uint8_t*>(out.scale)[fp8_scale_offset(kbr, c0 + j, cols4)] = static_cast<uint8_t>(byte);
-        if (bottom)
-          for (long long kb = kbr + 1; kb < kend; ++kb) static_cast<uint8_t*>(out.scale)[fp8_scale_offset(kb, c0 + j, cols4)] = 127;
-      }
-    }
-    uint32_t bytes[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = 4 * h + k;
-        float d[4], u[4];
-        if (o < 2) values(dy[i], 1.f, 0, d);
-        if (o != 1) values(up[i], us[i], a.kept_fmt, u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (o != 1 && j >= nc) u[j] = 0.f;
-          v[k][j] = (o == 0 ? d[j] * u[j] * slope[i][j] : o == 1 ? d[j] * value[i][j] : value[i][j] * u[j]) * inv[j];
+      for (int k = 0; k < kChunkRows * PER_ROW / 32; ++k) {
+        const int item = k * 32 + lane, r = item / PER_ROW, t = item % PER_ROW;
+        const long long row = r0 + chunk * kChunkRows + r;
+        const int n = row < rows ? static_cast<int>(max(0LL, min(static_cast<long long>(E), left - t * E))) : 0;
+        uint8_t* dst = to + chunk * G::CHUNK + r * kTile * static_cast<int>(sizeof(M)) + t * 16;
+        const M* src = matrix + (n ? row * ld + c00 + t * E : 0);
+        if constexpr (decltype(anywhere)::value) {
+          const Span all = Span::of<M>(matrix, rows, cols, ld);
+          const int l = static_cast<int>(row < rows ? min(left - t * E, 1LL << 20) : 0LL);
+          *reinterpret_cast<uint4*>(dst) =
+              load_anywhere<M, (PER_ROW < 32 ? PER_ROW : 32)>(matrix + (row < rows ? row * ld + c00 : 0), t, l, all);
+        } else {
+          copy16(smem_u32(dst), src, n * static_cast<int>(sizeof(M)));
         }
       }
+    };
+  };
+  using Any = std::bool_constant<ANYWHERE>;
+  const auto copy_dy = copy(mine, static_cast<const T*>(a.dy), a.lddy, Any());
+  const auto copy_gate = copy(mine + kChunkRows * G::DY, static_cast<const K*>(a.gate), a.ldg, std::bool_constant<ANYWHERE && KEPT == 0>());
+  const auto copy_up =
+      copy(mine + kChunkRows * (G::DY + G::KEEP), static_cast<const K*>(a.up), a.ldu, std::bool_constant<ANYWHERE && KEPT == 0>());
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        bytes[h][j] = fmt ? fp8_pack4<true>(v[0][j], v[1][j], v[2][j], v[3][j]) : fp8_pack4<false>(v[0][j], v[1][j], v[2][j], v[3][j]);
+  for (int chunk = 0; chunk < kChunks; ++chunk) {
+    copy_dy(chunk), copy_gate(chunk), copy_up(chunk);
+    cp_async_commit();
+  }
+  // the kept rows' scales: lane l has those of row l (gate) and row l - 16 (up)
+  const long long rows4 = (rows + 3) & ~3LL;
+  uint32_t kept_scale = 127u;
+  if (KEPT && r0 + lane % 16 < rows)
+    kept_scale = static_cast<const uint8_t*>(lane < 16 ? a.gate_scale : a.up_scale)[fp8_scale_offset(kbc, r0 + lane % 16, rows4)];
+  const float kept_value = fp8_scale_value(kept_scale);
+  const int n = static_cast<int>(max(0LL, min(4LL, left - lane * 4)));  // the lane's columns
+  const long long col = c00 + lane * 4;
+  const bool store8 = col < ((cols + 15) & ~15LL);
+  const bool by_cols = a.dgate_cols.data || a.dup_cols.data || a.y_cols.data;
+  // values of a row of the tile
+  const auto load = [&](int r, float2 (&d)[2], float2 (&g)[2], float2 (&u)[2]) {
+    const uint8_t* chunk = mine + r / kChunkRows * G::CHUNK;
+    const int i = r % kChunkRows;
+    four(reinterpret_cast<const T*>(chunk + i * G::DY) + lane * 4, d);
+    const K* pg = reinterpret_cast<const K*>(chunk + kChunkRows * G::DY + i * G::KEEP) + lane * 4;
+    const K* pu = reinterpret_cast<const K*>(chunk + kChunkRows * (G::DY + G::KEEP) + i * G::KEEP) + lane * 4;
+    if constexpr (KEPT != 0) {
+      four8<KEPT == 2>(pg, __shfl_sync(0xffffffffu, kept_value, r), g);
+      four8<KEPT == 2>(pu, __shfl_sync(0xffffffffu, kept_value, r + 16), u);
+    } else {
+      four(pg, g), four(pu, u);
     }
+  };
+  float cm[3][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) tiles[o].at(lane * 4 + j, warp) = make_uint2(bytes[0][j], bytes[1][j]);
+  for (int o = 0; o < 3; ++o)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cm[o][j] = 0.f;
+  // the 8 scales of a chunk's rows (4 of dgate, 4 of dup): lane l keeps that of row l / 8 and output l / 4 % 2
+  const int my_row = lane / 8, my_out = lane / 4 % 2, top = a.fmt ? 15 : 8;
+  const muon_fp8_out& my_rows = my_out ? a.dup_rows : a.dgate_rows;
+  uint8_t* const my_scales = lane % 4 == 0 ? static_cast<uint8_t*>(my_rows.scale) : nullptr;
+  const bool by_rows = a.dgate_rows.data || a.dup_rows.data;
+#pragma unroll 1
+  for (int chunk = 0; chunk < kChunks; ++chunk) {
+    if (chunk == 0) cp_async_wait<kChunks - 1>();
+    else if (chunk == 1) cp_async_wait<kChunks - 2>();
+    else if (chunk == 2) cp_async_wait<kChunks - 3>();
+    else cp_async_wait<0>();
+    __syncwarp();
+    float2 dg[kChunkRows][2], du[kChunkRows][2];
+    uint32_t m[kChunkRows];
+#pragma unroll
+    for (int r = 0; r < kChunkRows; ++r) {
+      float2 d[2], g[2], u[2];
+      load(chunk * kChunkRows + r, d, g, u);
+      float mg = 0.f, mu = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Activation f = activate2<T, GELU>(g[i]);
+        const float2 y = mul2(f.value, u[i]);
+        dg[r][i] = mul2(mul2(d[i], u[i]), f.slope);
+        du[r][i] = mul2(d[i], f.value);
+        mg = largest3(mg, dg[r][i].x, dg[r][i].y);
+        mu = largest3(mu, du[r][i].x, du[r][i].y);
+        cm[2][2 * i] = largest3(cm[2][2 * i], y.x, 0.f);
+        cm[2][2 * i + 1] = largest3(cm[2][2 * i + 1], y.y, 0.f);
+      }
+      m[r] = __byte_perm(__float_as_uint(mg) + 0xffffu, __float_as_uint(mu) + 0xffffu, 0x7632);
+      if (r % 2 == 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          cm[0][2 * i] = largest3(cm[0][2 * i], dg[r - 1][i].x, dg[r][i].x);
+          cm[0][2 * i + 1] = largest3(cm[0][2 * i + 1], dg[r - 1][i].y, dg[r][i].y);
+          cm[1][2 * i] = largest3(cm[1][2 * i], du[r - 1][i].x, du[r][i].x);
+          cm[1][2 * i + 1] = largest3(cm[1][2 * i + 1], du[r - 1][i].y, du[r][i].y);
+        }
+      }
+    }
+    const long long row0 = r0 + chunk * kChunkRows;
+    if (a.dgate || a.dup) {
+#pragma unroll
+      for (int r = 0; r < kChunkRows; ++r) {
+        const bool in = row0 + r < rows;
+        const auto put = [&](void* p, long long ld, const float2(&v)[2]) {
+          T* to = static_cast<T*>(p) + (in ? (row0 + r) * ld + c00 : 0);
+          if constexpr (ANYWHERE) {
+            store_four_anywhere(to, lane, in ? left - lane * 4 : 0LL, v);
+          } else if (in && n == 4) {
+            if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(to + lane * 4) = make_uint2(pack2(v[0], T()), pack2(v[1], T()));
+            else *reinterpret_cast<float4*>(to + lane * 4) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+          } else if (in) {
+            if (n > 0) to[lane * 4] = from_f32<T>(v[0].x);
+            if (n > 1) to[lane * 4 + 1] = from_f32<T>(v[0].y);
+            if (n > 2) to[lane * 4 + 2] = from_f32<T>(v[1].x);
+          }
+        };
+        if (a.dgate) put(a.dgate, a.lddgate, dg[r]);
+        if (a.dup) put(a.dup, a.lddup, du[r]);
+      }
+    }
+    if (by_rows) {
+      // largest magnitudes over the row's lanes, four words of two shared out as they shrink: lane l ends with row l / 8
+      const bool hi = lane & 16, odd = lane & 8;
+      const uint32_t w0 = __vmaxu2(hi ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 16));
+      const uint32_t w1 = __vmaxu2(hi ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], 16));
+      uint32_t w = __vmaxu2(odd ? w1 : w0, __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, 8));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, o));
+      const uint32_t byte = row0 + my_row < rows ? fp8_scale_byte(my_out ? w & 0xffff0000u : w << 16, top) : 127u;
+      if (my_scales && row0 + my_row < rows4) {
+        my_scales[fp8_scale_offset(kbc, row0 + my_row, rows4)] = static_cast<uint8_t>(byte);
+        if (left <= kTile)  // blocks past the last column, up to a whole scale word
+          for (long long kb = kbc + 1; kb < (cols + 511) / 512 * 4; ++kb) my_scales[fp8_scale_offset(kb, row0 + my_row, rows4)] = 127;
+      }
+      const float my_inv = fp8_inverse_scale(byte);
+      float ig[kChunkRows], iu[kChunkRows];
+#pragma unroll
+      for (int r = 0; r < kChunkRows; ++r) {
+        ig[r] = __shfl_sync(0xffffffffu, my_inv, 8 * r);
+        iu[r] = __shfl_sync(0xffffffffu, my_inv, 8 * r + 4);
+      }
+      uint8_t* pg = static_cast<uint8_t*>(a.dgate_rows.data) + row0 * a.dgate_rows.ld + col;
+      uint8_t* pu = static_cast<uint8_t*>(a.dup_rows.data) + row0 * a.dup_rows.ld + col;
+      const auto put = [&](auto e5m2) {
+        constexpr bool E5M2 = decltype(e5m2)::value;
+#pragma unroll
+        for (int r = 0; r < kChunkRows; ++r) {
+          const uint32_t wg = pack_scaled<E5M2>(dg[r][0], dg[r][1], ig[r]), wu = pack_scaled<E5M2>(du[r][0], du[r][1], iu[r]);
+          if (store8 && row0 + r < rows) {
+            if (a.dgate_rows.data) *reinterpret_cast<uint32_t*>(pg + r * a.dgate_rows.ld) = wg;
+            if (a.dup_rows.data) *reinterpret_cast<uint32_t*>(pu + r * a.dup_rows.ld) = wu;
+          }
+        }
+      };
+      if (a.fmt) put(std::true_type());
+      else put(std::false_type());
+    }
+  }
+  if (!by_cols) return;
+  __syncthreads();  // cmax is 0
+#pragma unroll
+  for (int o = 0; o < 3; ++o)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) atomicMax(&cmax[o][j * 32 + lane], __float_as_uint(cm[o][j]));
+  __syncthreads();
+  // ---- a scale for each column and output
+  for (int i = threadIdx.x; i < 3 * kTile; i += kTileWarps * 32) {
+    const int o = i / kTile, c = i % 32 * 4 + i % kTile / 32;  // the column
+    const muon_fp8_out& out = o == 0 ? a.dgate_cols : o == 1 ? a.dup_cols : a.y_cols;
+    const uint32_t byte = c < left ? fp8_scale_byte(cmax[0][i], (o < 2 ? a.fmt : a.y_fmt) ? 15 : 8) : 127u;
+    cmax[0][i] = __float_as_uint(fp8_inverse_scale(byte));
+    const long long cols4 = (cols + 3) & ~3LL;
+    if (out.data && c00 + c < cols4) {
+      uint8_t* s = static_cast<uint8_t*>(out.scale);
+      s[fp8_scale_offset(kbr, c00 + c, cols4)] = static_cast<uint8_t>(byte);
+      if ((kbr + 1) * kTile >= rows)
+        for (long long kb = kbr + 1; kb < (rows + 511) / 512 * 4; ++kb) s[fp8_scale_offset(kb, c00 + c, cols4)] = 127;
+    }
+  }
+  __syncthreads();
+  float2 inv[3][2];
+#pragma unroll
+  for (int o = 0; o < 3; ++o)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      inv[o][i] = make_float2(__uint_as_float(cmax[o][2 * i * 32 + lane]), __uint_as_float(cmax[o][(2 * i + 1) * 32 + lane]));
+  // ---- transposed words; lanes are turned by 4 for each warp, so that reading a column from 8 warps meets 8 banks
+  const int turned = (lane + 4 * warp) % 32;
+#pragma unroll 1
+  for (int chunk = 0; chunk < kChunks; ++chunk) {
+    float2 v[3][kChunkRows][2];
+#pragma unroll
+    for (int r = 0; r < kChunkRows; ++r) {
+      float2 d[2], g[2], u[2];
+      load(chunk * kChunkRows + r, d, g, u);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Activation f = activate2<T, GELU>(g[i]);
+        v[0][r][i] = mul2(mul2(mul2(d[i], u[i]), f.slope), inv[0][i]);
+        v[1][r][i] = mul2(mul2(d[i], f.value), inv[1][i]);
+        v[2][r][i] = mul2(mul2(f.value, u[i]), inv[2][i]);
+      }
+    }
+    __syncwarp();  // the chunk has been read
+    uint32_t* words = reinterpret_cast<uint32_t*>(mine + chunk * G::CHUNK);
+    const auto put = [&](int o, auto e5m2) {
+      constexpr bool E5M2 = decltype(e5m2)::value;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const auto at = [&](int r) { return j & 1 ? v[o][r][j / 2].y : v[o][r][j / 2].x; };
+        words[(o * 4 + j) * 32 + turned] = fp8_pack4<E5M2>(at(0), at(1), at(2), at(3));
+      }
+    };
+    if (a.fmt) put(0, std::true_type()), put(1, std::true_type());
+    else put(0, std::false_type()), put(1, std::false_type());
+    if (a.y_fmt) put(2, std::true_type());
+    else put(2, std::false_type());
   }
   __syncthreads();
 #pragma unroll
   for (int o = 0; o < 3; ++o) {
     const muon_fp8_out& out = o == 0 ? a.dgate_cols : o == 1 ? a.dup_cols : a.y_cols;
     if (!out.data) continue;
+    // 16 bytes (the 16 rows of warp w) to a thread, 8 threads to a column; a warp has 4 columns
+    const int w = threadIdx.x / 4 % 8, l4 = threadIdx.x % 4 + threadIdx.x / 32 * 4;
+    const long long r = kbr * kTile + w * 16;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(gated_smem + w * G::WARP) + (l4 + 4 * w) % 32;
 #pragma unroll
-    for (int it = 0; it < 2; ++it) {  // 16 bytes per thread, 8 threads to a column; a warp's 4 columns are 4 apart
-      const int q = it * 64 + (threadIdx.x >> 3), cl = (q % 32) * 4 + q / 32, s = (threadIdx.x & 7) * 2;
-      const long long c = kbc * kTile + cl, r = kbr * kTile + s * 8;
+    for (int j = 0; j < 4; ++j) {
+      const long long c = c00 + l4 * 4 + j;
       if (c < cols && r < rows) {
-        const uint2 lo = tiles[o].at(cl, s), hi = tiles[o].at(cl, s + 1);
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out.data) + c * out.ld + r) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        constexpr int STEP = G::CHUNK / 4;
+        const int at = (o * 4 + j) * 32;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out.data) + c * out.ld + r) =
+            make_uint4(words[at], words[STEP + at], words[2 * STEP + at], words[3 * STEP + at]);
       }
     }
   }
 }
 
-template <typename T, bool KEPT8>
+template <typename T>
 static cudaError_t dispatch_gated_grad(const muon_gated_grad_args& a, int vec, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>((a.cols + kTile - 1) / kTile), static_cast<unsigned>((a.rows + kTile - 1) / kTile));
-  constexpr int smem = 3 * static_cast<int>(sizeof(TransposedTile));
-  const auto go = [&](auto kernel, bool (&done)[64]) {
+  const auto go = [&](auto kept, auto gelu, auto anywhere) {
+    constexpr int KEPT = decltype(kept)::value;
+    constexpr bool GELU = decltype(gelu)::value, ANYWHERE = decltype(anywhere)::value;
+    static bool done[64] = {false};
+    constexpr int smem = GatedTile<T, KEPT, GELU, ANYWHERE>::BYTES;
+    const auto kernel = gated_grad_kernel<T, KEPT, GELU, ANYWHERE>;
     const cudaError_t e = smem_limit(kernel, smem, done);
-    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kTileWarps * 32), smem, st, a, vec);
+    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kTileWarps * 32), smem, st, a);
   };
-  static bool silu[64] = {false}, gelu[64] = {false};
-  return a.act ? go(gated_grad_kernel<T, KEPT8, true>, gelu) : go(gated_grad_kernel<T, KEPT8, false>, silu);
+  const auto by_kept = [&](auto gelu, auto anywhere) {
+    if (!a.gate_scale) return go(std::integral_constant<int, 0>(), gelu, anywhere);
+    return a.kept_fmt ? go(std::integral_constant<int, 2>(), gelu, anywhere) : go(std::integral_constant<int, 1>(), gelu, anywhere);
+  };
+  const auto by_act = [&](auto anywhere) { return a.act ? by_kept(std::true_type(), anywhere) : by_kept(std::false_type(), anywhere); };
+  return vec ? by_act(std::false_type()) : by_act(std::true_type());
 }
 
 cudaError_t launch_gated_grad(const muon_gated_grad_args& a, int vec, cudaStream_t st) {
-  const auto go = [&](auto t) {
-    using T = decltype(t);
-    return a.gate_scale ? dispatch_gated_grad<T, true>(a, vec, st) : dispatch_gated_grad<T, false>(a, vec, st);
-  };
-  if (a.dt == MUON_BF16) return go(__nv_bfloat16());
-  return a.dt == MUON_FP16 ? go(__half()) : go(float());
+  if (a.dt == MUON_BF16) return dispatch_gated_grad<__nv_bfloat16>(a, vec, st);
+  return a.dt == MUON_FP16 ? dispatch_gated_grad<__half>(a, vec, st) : dispatch_gated_grad<float>(a, vec, st);
 }
 
 }  // namespace muon

@@ -551,8 +551,8 @@ def test_block_norm_backward_matches_differences(mm):
 GATED_SHAPES = [(1, 1), (3, 8), (129, 127), (2, 513), (130, 256), (7, 1000), (257, 640), (1, 14336), (3, 20001)]
 
 
-def act_err(g, kind):
-    """(error of f, error of f') for gate values g."""
+def act_err(g, kind, dtype):
+    """(error of f, error of f') for gate values g of data of `dtype`."""
     g = g.double()
     f, slope = ref.activation(g, kind)
     if kind == "silu":
@@ -561,6 +561,14 @@ def act_err(g, kind):
         s, low = torch.sigmoid(g), 2.0 ** -126
         return (f.abs() * (sig_err(g) + 2 * F24) + g.abs() * low,
                 s * sig_err(g) * (1 + g.abs()) + 4 * F24 * (f.abs() + s) + (1 + g.abs()) * low)
+    if dtype != torch.float32:
+        # Phi = t R(t) exp(-g^2 / 2) / 2 in its lower tail: R fitted to 2.7 2^-24 and evaluated with 10 roundings (6), t off by
+        # 3 (a reciprocal and a sum), which counts twice in t R(t), three products (3); the exponential by 2 units (4) and
+        # the three roundings of its argument, 1.5 g^2 in all.  Below 2^-126 it may count as 0
+        phi, low = 0.5 * torch.special.erfc(-g * math.sqrt(0.5)), 2.0 ** -126
+        bell = g.abs() * torch.exp(-0.5 * g * g) * 0.4
+        return (f.abs() * (24 + 1.6 * g * g) * F24 + g.abs() * low,
+                phi * (22 + 1.5 * g * g) * F24 + bell * (8 + 1.5 * g * g) * F24 + F24 * slope.abs() + (1 + g.abs()) * low)
     # Phi: 5 units in the last place, below fp32's normal range 2^-149 of its own and f |g| times that;
     # exp(-g^2 / 2): 2 + 1.17 g^2 / 2 units, and two roundings of its argument, g^2 / 2 2^-24 each
     phi = 0.5 * torch.special.erfc(-g * math.sqrt(0.5))
@@ -578,7 +586,7 @@ def check_gated(mm, g, u, kind, fp8=None, checkpoint=None, y=True, run=None):
     got = mm.gated_activation(dg, du, activation=kind, fp8=fp8, y=y, checkpoint=checkpoint)
     torch.cuda.synchronize()
     want = ref.gated(g, u, kind)
-    err = act_err(g, kind)[0] * u.double().abs() + 2 * F24 * want.abs()
+    err = act_err(g, kind, g.dtype)[0] * u.double().abs() + 2 * F24 * want.abs()
     assert (got.y is not None) == y and (got.q is not None) == (fp8 is not None)
     if y:
         close(got.y, want, U[g.dtype] * want.abs() + err + TINY[g.dtype], "y")
@@ -616,7 +624,7 @@ def check_gated_grad(mm, seed, rows, cols, dtype, kind, kept=None, fp8="e5m2", y
     got = mm.gated_activation_backward(put(dy), mm.GatedKept(kg, ku), activation=kind, dense=dense, fp8=fp8, y_fp8=y_fp8)
     torch.cuda.synchronize()
     wg, wu, wy = ref.gated_backward(dy, g, u, kind)
-    ef, es = act_err(g, kind)
+    ef, es = act_err(g, kind, dtype)
     d, ua = dy.double().abs(), u.double().abs()
     eg, eu, ey = d * ua * es + 3 * F24 * wg.abs(), d * ef + 2 * F24 * wu.abs(), ef * ua + 2 * F24 * wy.abs()
     lost = TINY[torch.float32]
