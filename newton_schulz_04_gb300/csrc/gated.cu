@@ -171,11 +171,15 @@ __global__ void __launch_bounds__(256) gated_kernel(const muon_gated_args a) {
 }
 
 template <typename T>
-static cudaError_t dispatch_gated(const muon_gated_args& a, int vec, cudaStream_t st) {
+static dim3 gated_grid(long long rows, long long cols) {
   constexpr int ROWS = 256 * 16 / static_cast<int>(sizeof(T)) / 128 * kGatedRows;  // of a CTA
-  const long long groups = (a.rows + ROWS - 1) / ROWS;
-  const long long y = std::min(groups, 32768LL);
-  const dim3 grid(static_cast<unsigned>((a.cols + 127) / 128), static_cast<unsigned>(y), static_cast<unsigned>((groups + y - 1) / y));
+  const long long groups = (rows + ROWS - 1) / ROWS, y = std::min(groups, 32768LL);
+  return dim3(static_cast<unsigned>((cols + 127) / 128), static_cast<unsigned>(y), static_cast<unsigned>((groups + y - 1) / y));
+}
+
+template <typename T>
+static cudaError_t dispatch_gated(const muon_gated_args& a, int vec, cudaStream_t st) {
+  const dim3 grid = gated_grid<T>(a.rows, a.cols);
   const bool any = a.q.data || a.gate8.data || a.up8.data;
   const bool e4m3 = a.gate8.data && a.up8.data && a.kept_fmt == MUON_E4M3 && (!a.q.data || a.fmt == MUON_E4M3);
   const auto go = [&](auto gelu, auto anywhere) {
@@ -526,12 +530,90 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
   }
 }
 
+// ------------------------------------------------------------------ gradient of the data's type alone
+// Without 8-bit outputs no block has to be gathered, and the forward kernel's layout gives small matrices more CTAs.
+template <typename T, int KEPT, bool GELU, bool ANYWHERE>
+__global__ void __launch_bounds__(256) gated_grad_dense_kernel(const muon_gated_grad_args a) {
+  using P = Pairs<T>;
+  using K = std::conditional_t<KEPT != 0, uint8_t, T>;
+  constexpr int E = P::E, N = P::N, LANES = 128 / E, GROUPS = 256 / LANES, U = kGatedRows;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t = threadIdx.x % LANES, kb = blockIdx.x, cols = static_cast<int>(a.cols), col = kb * 128 + t * E, left = cols - col;
+  const long long group = blockIdx.y + static_cast<long long>(blockIdx.z) * gridDim.y, row0 = group * GROUPS * U + threadIdx.x / LANES;
+  const long long rows4 = (a.rows + 3) & ~3LL;
+  P d[U], g[U], v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = row0 + u * GROUPS;
+    const bool in = row < a.rows;
+    const auto plain = [&](P& p, const void* matrix, long long ld) {
+      const T* m = static_cast<const T*>(matrix);
+      if constexpr (ANYWHERE) {
+        p.unpack(load_anywhere<T, LANES>(m + (in ? row * ld : 0), col / E, in ? left : 0, Span::of<T>(m, a.rows, cols, ld)));
+      } else {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (in && left >= E) w = *reinterpret_cast<const uint4*>(m + row * ld + col);
+        else if (in && left > 0) w = load_part(m + row * ld + col, left);
+        p.unpack(w);
+      }
+    };
+    const auto kept = [&](P& p, const void* matrix, const void* scale, long long ld) {
+      if constexpr (KEPT == 0) {
+        plain(p, matrix, ld);
+      } else {
+        __align__(8) uint8_t b[E] = {};
+        const uint8_t* q = static_cast<const uint8_t*>(matrix) + row * ld + col;
+        float s = 1.f;
+        if (in && left > 0) {
+          s = fp8_scale_value(static_cast<const uint8_t*>(scale)[fp8_scale_offset(kb, row, rows4)]);
+          if (left >= E) {
+            if constexpr (E == 8) *reinterpret_cast<uint2*>(b) = *reinterpret_cast<const uint2*>(q);
+            else *reinterpret_cast<uint32_t*>(b) = *reinterpret_cast<const uint32_t*>(q);
+          } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+              if (i < left) b[i] = q[i];
+          }
+        }
+        p.template unpack8<KEPT == 2>(b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) p.v[i] = mul2(p.v[i], both(s));
+      }
+    };
+    plain(d[u], a.dy, a.lddy);
+    kept(g[u], a.gate, a.gate_scale, a.ldg);
+    kept(v[u], a.up, a.up_scale, a.ldu);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = row0 + u * GROUPS;
+    const bool in = row < a.rows;
+    P dg, du;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const Activation f = activate2<T, GELU>(g[u].v[i]);
+      dg.v[i] = mul2(mul2(d[u].v[i], v[u].v[i]), f.slope);
+      du.v[i] = mul2(d[u].v[i], f.value);
+    }
+    const auto put = [&](void* matrix, long long ld, const P& p) {
+      T* m = static_cast<T*>(matrix);
+      if constexpr (ANYWHERE) store_anywhere<T, LANES>(m + (in ? row * ld : 0), col / E, in ? left : 0, p);
+      else if (in) p.store(m + row * ld + col, min(E, left));
+    };
+    if (a.dgate) put(a.dgate, a.lddgate, dg);
+    if (a.dup) put(a.dup, a.lddup, du);
+  }
+}
+
 template <typename T>
 static cudaError_t dispatch_gated_grad(const muon_gated_grad_args& a, int vec, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>((a.cols + kTile - 1) / kTile), static_cast<unsigned>((a.rows + kTile - 1) / kTile));
+  const bool eight = a.dgate_rows.data || a.dgate_cols.data || a.dup_rows.data || a.dup_cols.data || a.y_cols.data;
   const auto go = [&](auto kept, auto gelu, auto anywhere) {
     constexpr int KEPT = decltype(kept)::value;
     constexpr bool GELU = decltype(gelu)::value, ANYWHERE = decltype(anywhere)::value;
+    if (!eight) return launch_pdl(gated_grad_dense_kernel<T, KEPT, GELU, ANYWHERE>, gated_grid<T>(a.rows, a.cols), dim3(256), 0, st, a);
     static bool done[64] = {false};
     constexpr int smem = GatedTile<T, KEPT, GELU, ANYWHERE>::BYTES;
     const auto kernel = gated_grad_kernel<T, KEPT, GELU, ANYWHERE>;
