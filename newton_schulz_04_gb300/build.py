@@ -19,8 +19,13 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmuon_ns.so")
 SOURCES = ["engine.cu", "tc_gemm.cu", "simt_gemm.cu", "elementwise.cu", "adamw.cu", "planner.cpp",
            "train_abi.cu", "clip.cu", "rms_norm.cu", "fp8_quant.cu", "fp8_gemm.cu",
-           "fp8_few.cu", "block_abi.cu", "block_norm.cu", "block_norm_fp16.cu", "block_norm_fp32.cu", "block_norm_grad.cu",
-           "block_norm_grad_fp16.cu", "block_norm_grad_fp32.cu", "gated.cu", "fp8_transpose.cu"]
+           "fp8_few.cu", "block_abi.cu", "block_norm.cu", "block_norm_grad.cu", "gated.cu", "fp8_transpose.cu"]
+# (source, object, defines): compiled once for each type and alignment, in parallel
+ROWS = [(src, f"{src[:-3]}_{name}{'_any' if anywhere else ''}",
+         [f"-DMUON_ROWS_T={t}", f"-DMUON_ROWS_ANYWHERE={'true' if anywhere else 'false'}"])
+        for src in ("block_norm_rows.cu", "block_norm_grad_rows.cu")
+        for name, t in (("bf16", "__nv_bfloat16"), ("fp16", "__half"), ("fp32", "float"))
+        for anywhere in (False, True)]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -51,9 +56,10 @@ def build(verbose=False, force=False, extra=()) -> str:
     cc = nvcc()
     objs = []
 
-    def comp(src):
-        obj = os.path.join(OUT_DIR, os.path.splitext(src)[0] + ".o")
-        cmd = [cc, *_flags(extra), "-c", os.path.join(CSRC, src), "-o", obj]
+    def comp(unit):
+        src, name, defines = unit
+        obj = os.path.join(OUT_DIR, name + ".o")
+        cmd = [cc, *_flags(extra), *defines, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
@@ -61,8 +67,9 @@ def build(verbose=False, force=False, extra=()) -> str:
             sys.stdout.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(comp, SOURCES))
+    units = ROWS + [(src, os.path.splitext(src)[0], []) for src in SOURCES]  # the longest first
+    with cf.ThreadPoolExecutor(max_workers=len(units)) as ex:
+        objs = list(ex.map(comp, units))
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

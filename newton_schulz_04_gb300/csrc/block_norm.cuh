@@ -8,19 +8,6 @@
 
 namespace muon {
 
-// 1 / (1 + exp(-g)), 0 at -infinity and from about g = -87 on.  fp32 data takes the accurate exponential and quotient;
-// 16-bit data, which is rounded by 2^-11 at best, the hardware's: off by (4 + 1.2 |g|) 2^-23 of the value.
-template <typename T>
-__device__ __forceinline__ float sigmoid(float g) {
-  if constexpr (sizeof(T) == 4) {
-    return 1.f / (1.f + expf(-g));
-  } else {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
-    return r;
-  }
-}
-
 // ---- a block of 128 columns to a warp
 // Rows of any alignment: lane l holds columns l, l + 32, l + 64 and l + 96 of a block, so that a warp's accesses are
 // 32 neighbours whatever the row's first address, and a block's largest magnitude is one reduction of the warp.
@@ -32,6 +19,18 @@ __device__ __forceinline__ float load_weight(const void* w, int dt, int col, boo
   if (!w) return 1.f;
   if (dt == MUON_FP32) return load_or<float>(w, col, in, 0.f);
   return dt == MUON_BF16 ? load_or<__nv_bfloat16>(w, col, in, 0.f) : load_or<__half>(w, col, in, 0.f);
+}
+
+// n weights from `col` on, the rest 0; ANYWHERE: their address allows no vector accesses.
+template <typename T, bool ANYWHERE>
+__device__ __forceinline__ void load_weights(const void* w, int dt, int col, int n, float (&v)[16 / sizeof(T)]) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  if constexpr (ANYWHERE) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = i < n ? load_weight(w, dt, col + i, true) : 0.f;
+  } else {
+    load_weight_piece<E>(w, dt, col, n, v);
+  }
 }
 
 // Block kb of a row in 8 bits.  All lanes call; v is 0 past the last column.
@@ -88,5 +87,12 @@ __device__ __forceinline__ void cta_sums(float (&v)[N], float (*sh)[N][W], int t
     for (int o = W / 2; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
   }
 }
+
+// Kernels compiled in block_norm_rows.cu and block_norm_grad_rows.cu, for T and rows that start on 16 bytes or ANYWHERE.
+template <typename T, bool ANYWHERE>
+cudaError_t launch_block_norm_rows(const muon_block_norm_args& a, int sms, cudaStream_t st);
+// *ctas: the rows of `partial` that the kernel writes.
+template <typename T, bool ANYWHERE>
+cudaError_t launch_block_norm_grad_rows(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st);
 
 }  // namespace muon

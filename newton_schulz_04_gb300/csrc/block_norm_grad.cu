@@ -1,11 +1,14 @@
-// block_norm_grad.cu -- gradient of the norms around a block: bf16 rows, and the sums of the weights' gradients.
-#include "block_norm_grad.cuh"
+// block_norm_grad.cu -- gradient of the norms around a block: the choice by type and alignment, and the sums of the weights'
+// gradients.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "block_norm.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
 
 namespace muon {
-
-// the other types are compiled in files of their own
-extern template cudaError_t launch_block_norm_grad_rows<__half>(const muon_block_norm_grad_args&, float*, int, int, int*, cudaStream_t);
-extern template cudaError_t launch_block_norm_grad_rows<float>(const muon_block_norm_grad_args&, float*, int, int, int*, cudaStream_t);
 
 // Sums over the CTAs' rows in a fixed order, 32 columns by 32 row groups per CTA; blockIdx.y 0: dpre, 1: dpost and dscale.
 __global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float* partial, int ctas,
@@ -36,14 +39,17 @@ __global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float* p
 }
 
 int block_norm_grad_ctas(long long rows, int sms) {
-  return static_cast<int>(std::max(1LL, std::min<long long>(rows, most_ctas(sms))));
+  return static_cast<int>(std::max(1LL, std::min<long long>(rows, kBlockNormCtasPerSm * sms)));
 }
 
 cudaError_t launch_block_norm_grad(const muon_block_norm_grad_args& a, float* partial, int vec, int sms, cudaStream_t st) {
   int ctas = 0;
-  const cudaError_t e = a.dt == MUON_BF16   ? launch_block_norm_grad_rows<__nv_bfloat16>(a, partial, vec, sms, &ctas, st)
-                        : a.dt == MUON_FP16 ? launch_block_norm_grad_rows<__half>(a, partial, vec, sms, &ctas, st)
-                                            : launch_block_norm_grad_rows<float>(a, partial, vec, sms, &ctas, st);
+  const auto go = [&](auto t) {
+    using T = decltype(t);
+    return vec ? launch_block_norm_grad_rows<T, false>(a, partial, sms, &ctas, st)
+               : launch_block_norm_grad_rows<T, true>(a, partial, sms, &ctas, st);
+  };
+  const cudaError_t e = a.dt == MUON_BF16 ? go(__nv_bfloat16()) : a.dt == MUON_FP16 ? go(__half()) : go(float());
   if (e != cudaSuccess || !partial) return e;
   return launch_pdl(block_norm_weights_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), dim3(1024), 0, st,
                     static_cast<const float*>(partial), ctas, a);

@@ -1,4 +1,4 @@
-// block_norm_grad.cuh -- gradient of the norms around a block, from what the forward pass kept (of the data's type, or in 8
+// block_norm_grad_rows.cu -- gradient of the norms around a block, from what the forward pass kept (of the data's type, or in 8
 // bits).  With X = x rho_x and H = h rho_h as kept and c = scale post:
 //
 //   a = dy pre       D = dh + rho_h (a - H mean(a H))       dresidual = alpha D
@@ -7,7 +7,8 @@
 //
 // mean(b X) needs mean(a H) first.  With u = dh + rho_h a and e = sigmoid(gate) c X it is mean(u e) - rho_h mean(a H)
 // mean(H e), so a row takes one pass and one exchange of three sums.
-#pragma once
+//
+// Compiled once for each type and alignment of rows (MUON_ROWS_T, MUON_ROWS_ANYWHERE).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -41,20 +42,17 @@ struct Kept {
   }
 };
 
-template <typename T, int W, int K, bool KEPT8>
-__global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_block_norm_grad_args a, float* partial) {
-  constexpr int KK = K ? K : 1;
+// The widest rows, which a cluster's rings do not hold: 16 warps to a row, read again for the second phase, the columns' sums
+// in the CTA's part of the workspace.
+template <typename T, bool KEPT8>
+__global__ void __launch_bounds__(512) block_norm_grad_wide_kernel(const muon_block_norm_grad_args a, float* partial) {
+  constexpr int W = 16;
   __shared__ float sh[2][3][W];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cols = static_cast<int>(a.cols);
-  const int blocks = (cols + 127) / 128, turns = K ? K : (blocks + W - 1) / W;
+  const int blocks = (cols + 127) / 128, turns = (blocks + W - 1) / W;
   float* part = partial ? partial + static_cast<long long>(blockIdx.x) * 2 * cols : nullptr;
-  float dpre[KK][4], sx[KK][4];
-#pragma unroll
-  for (int k = 0; k < KK; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dpre[k][j] = sx[k][j] = 0.f;
   const float inv_n = 1.f / static_cast<float>(cols);
   int turn = 0;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
@@ -64,7 +62,7 @@ __global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_bloc
     const bool element = a.gate && !a.gate_per_row;
     const Kept<T, KEPT8> kg(element ? a.gate : nullptr, a.gate_scale, a.ldg, row, a.rows, a.kept_fmt);
     const float rx = a.rstd_x[row], rh = a.rstd_h[row];
-    const float row_sig = a.gate && !element ? sigmoid<T>(to_f32(static_cast<const T*>(a.gate)[row * a.ldg])) : 1.f;
+    const float row_sig = a.gate && !element ? sigmoid2<T>(both(to_f32(static_cast<const T*>(a.gate)[row * a.ldg]))).x : 1.f;
     struct Element {
       float d, u, hn, xn, sig, c;  // dy, dh + rho_h dy pre, H, X, sigmoid(gate), scale post
     };
@@ -73,13 +71,12 @@ __global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_bloc
       e.d = to_f32(dy[col]);
       e.hn = kh.at(col, hs) * rh;
       e.xn = kx.at(col, xs) * rx;
-      e.sig = element ? sigmoid<T>(kg.at(col, gs)) : row_sig;
+      e.sig = element ? sigmoid2<T>(both(kg.at(col, gs))).x : row_sig;
       e.c = load_weight(a.post, a.weight_dt, col, true) * load_weight(a.scale, a.weight_dt, col, true);
       e.u = fmaf(rh, e.d * load_weight(a.pre, a.weight_dt, col, true), a.dh ? to_f32(dh[col]) : 0.f);
       return e;
     };
     float sum[3] = {0.f, 0.f, 0.f};
-#pragma unroll
     for (int k = 0; k < turns; ++k) {
       const int kb = warp + W * k;
       if (kb >= blocks) break;
@@ -98,9 +95,8 @@ __global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_bloc
     cta_sums<W, 3>(sum, sh, turn);
     const float k1 = sum[0] * inv_n * rh, along = sum[1] - k1 * sum[2], k2 = along * inv_n;
     if (threadIdx.x == 0 && a.dgate && !element) static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>((1.f - row_sig) * along);
-#pragma unroll
     for (int k = 0; k < turns; ++k) {
-      const int kb = warp + W * k, kk = K ? k : 0;
+      const int kb = warp + W * k;
       if (kb >= blocks) break;
       const float xs = kx.block_scale(kb), hs = kh.block_scale(kb), gs = element ? kg.block_scale(kb) : 1.f;
 #pragma unroll
@@ -112,24 +108,13 @@ __global__ void __launch_bounds__(W * 32) block_norm_grad_kernel(const muon_bloc
         if (a.dresidual) static_cast<T*>(a.dresidual)[row * a.lddr + col] = from_f32<T>(a.alpha * d);
         if (a.dx) static_cast<T*>(a.dx)[row * a.lddx + col] = from_f32<T>(rx * (b - e.xn * k2));
         if (a.dgate && element) static_cast<T*>(a.dgate)[row * a.lddgate + col] = from_f32<T>((1.f - e.sig) * (b * e.xn));
-        if (K) {
-          dpre[kk][j] = fmaf(e.d, e.hn, dpre[kk][j]);
-          sx[kk][j] = fmaf(t, e.xn, sx[kk][j]);
-        } else if (part) {  // this thread alone holds these columns of the CTA's sums
+        if (part) {  // this thread alone holds these columns of the CTA's sums
           part[col] = (turn ? part[col] : 0.f) + e.d * e.hn;
           part[cols + col] = (turn ? part[cols + col] : 0.f) + t * e.xn;
         }
       }
     }
   }
-  if (!K || !part) return;
-#pragma unroll
-  for (int k = 0; k < KK; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = (warp + W * k) * 128 + lane + 32 * j;
-      if (col < cols) part[col] = dpre[k][j], part[cols + col] = sx[k][j];
-    }
 }
 
 // ------------------------------------------------------------------ ring of rows
@@ -140,34 +125,30 @@ __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int by
 }
 
 // A thread's slots: S rows of dy, dh, x, h and gate, a piece each; kept 8-bit ones take E bytes instead of 16.
-template <typename T, int TH, int S, bool KEPT8>
+// ANYWHERE: of T, a warp's 33 times 16 bytes.
+template <typename T, int TH, int S, bool KEPT8, bool ANYWHERE>
 struct GradRing {
-  static constexpr int E = 16 / static_cast<int>(sizeof(T)), WIDE = KEPT8 ? 2 : 5;
-  static constexpr int STAGE = TH * (WIDE * 16 + (5 - WIDE) * E), BYTES = S * STAGE;
+  static constexpr int E = 16 / static_cast<int>(sizeof(T)), WIDE = KEPT8 ? 2 : 5, ARRAY = ANYWHERE ? TH / 32 * kWarpSlot : TH * 16;
+  static constexpr int STAGE = WIDE * ARRAY + (5 - WIDE) * TH * E, BYTES = S * STAGE;
   uint8_t* base;
   __device__ __forceinline__ uint8_t* at(int slot, int arr) const {
     uint8_t* stage = base + slot * STAGE;
-    if (arr < WIDE) return stage + (arr * TH + static_cast<int>(threadIdx.x)) * 16;
-    return stage + WIDE * TH * 16 + ((arr - WIDE) * TH + static_cast<int>(threadIdx.x)) * E;
-  }
-  // n of the piece's elements exist.
-  __device__ __forceinline__ void fetch(int slot, int arr, const void* src, int n) const {
-    if (arr < WIDE) copy16(smem_u32(at(slot, arr)), src, n * static_cast<int>(sizeof(T)));
-    else copy_small<E>(smem_u32(at(slot, arr)), src, n);
+    if (arr < WIDE) return stage + arr * ARRAY + (ANYWHERE ? threadIdx.x / 32 * kWarpSlot : threadIdx.x * 16);
+    return stage + WIDE * ARRAY + ((arr - WIDE) * TH + static_cast<int>(threadIdx.x)) * E;
   }
 };
 
 // CL CTAs of a cluster to a row, G threads of each with a piece of 16 bytes, a ring of S rows.  KEPT: of x, h and an
 // element's gate; 0: T, 1: e4m3, 2: e5m2.  GATE: a gate of every element.  Both compiled apart: chosen at run time they
 // cost 8192 x 4096 a third more instructions, in pieces too small to be overlapped.
-template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE>
+template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE, bool ANYWHERE>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
     block_norm_grad_ring_kernel(const muon_block_norm_grad_args a, float* partial) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
   constexpr int DY = 0, DH = 1, X = 2, H = 3, GA = 4;
   using P = Pairs<T>;
   using K = std::conditional_t<KEPT != 0, uint8_t, T>;
-  using Slots = GradRing<T, TH, S, KEPT != 0>;
+  using Slots = GradRing<T, TH, S, KEPT != 0, ANYWHERE>;
   constexpr int E = P::E, N = P::N;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ RowSums<G, TH, 3, CL> sums;
@@ -179,27 +160,47 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   const long long step = static_cast<long long>(gridDim.x / CL) * R, row0 = static_cast<long long>(blockIdx.x / CL) * R + rr;
   const long long rows4 = (a.rows + 3) & ~3LL;
   long long frow = row0;  // next row to fetch
-  const int ndh = a.dh ? n : 0;
-  const T* fdy = static_cast<const T*>(a.dy) + row0 * a.lddy + col;
-  const T* fdh = a.dh ? static_cast<const T*>(a.dh) + row0 * a.lddh + col : fdy;
-  const long long lddh = a.dh ? a.lddh : a.lddy;  // without dh nothing is read, and zeros arrive
-  const K* fx = static_cast<const K*>(a.x) + row0 * a.ldx + col;
-  const K* fh = static_cast<const K*>(a.h) + row0 * a.ldh + col;
-  const K* fg = static_cast<const K*>(a.gate) + (GATE ? row0 * a.ldg + col : 0);
+  // pointers to rows, or to the thread's pieces of them
+  constexpr int BEGIN = ANYWHERE ? 0 : 1, KBEGIN = ANYWHERE && KEPT == 0 ? 0 : 1;
+  const void* const dh = a.dh ? a.dh : a.dy;  // without dh nothing is read, and zeros arrive
+  const long long lddh = a.dh ? a.lddh : a.lddy;
+  const T* fdy = static_cast<const T*>(a.dy) + row0 * a.lddy + BEGIN * col;
+  const T* fdh = static_cast<const T*>(dh) + row0 * lddh + BEGIN * col;
+  const K* fx = static_cast<const K*>(a.x) + row0 * a.ldx + KBEGIN * col;
+  const K* fh = static_cast<const K*>(a.h) + row0 * a.ldh + KBEGIN * col;
+  const K* fg = static_cast<const K*>(a.gate) + (GATE ? row0 * a.ldg + KBEGIN * col : 0);
   auto fetch = [&](int slot) {
     if (frow < a.rows) {
-      ring.fetch(slot, DY, fdy, n);
-      ring.fetch(slot, DH, fdh, ndh);
-      ring.fetch(slot, X, fx, n);
-      ring.fetch(slot, H, fh, n);
-      if (GATE) ring.fetch(slot, GA, fg, n);
+      const auto plain = [&](int arr, const T* row, const void* matrix, bool there) {
+        if constexpr (ANYWHERE)
+          fetch_anywhere<T>(ring.at(slot, arr), row, rank * G + t, there ? cols : 0, static_cast<const uint8_t*>(matrix));
+        else copy16(smem_u32(ring.at(slot, arr)), row, there ? n * static_cast<int>(sizeof(T)) : 0);
+      };
+      const auto kept = [&](int arr, const K* row, const void* matrix) {
+        if constexpr (KEPT == 0) plain(arr, row, matrix, true);
+        else copy_small<E>(smem_u32(ring.at(slot, arr)), row, n);
+      };
+      plain(DY, fdy, a.dy, true);
+      plain(DH, fdh, dh, a.dh != nullptr);
+      kept(X, fx, a.x);
+      kept(H, fh, a.h);
+      if (GATE) kept(GA, fg, a.gate);
     }
     cp_async_commit();
     frow += step, fdy += step * a.lddy, fdh += step * lddh, fx += step * a.ldx, fh += step * a.ldh;
     if (GATE) fg += step * a.ldg;
   };
-  const auto read_kept = [&](int slot, int arr, P& p) {
-    if constexpr (KEPT == 0) p.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, arr)));
+  // row: for its address modulo 16
+  const auto read = [&](int slot, int arr, const void* matrix, long long ld, long long row, P& p) {
+    if constexpr (ANYWHERE) {
+      const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(matrix)) + static_cast<uint32_t>(row * ld) * sizeof(T);
+      p.unpack(read_anywhere(ring.at(slot, arr), static_cast<int>(at & 15u)));
+    } else {
+      p.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, arr)));
+    }
+  };
+  const auto read_kept = [&](int slot, int arr, const void* matrix, long long ld, long long row, P& p) {
+    if constexpr (KEPT == 0) read(slot, arr, matrix, ld, row, p);
     else p.template unpack8<KEPT == 2>(ring.at(slot, arr));
   };
   if (CL > 1) cluster_sync();  // the others' shared memory is there
@@ -209,11 +210,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   float2 w1[N], w2[N], dpre[N], sx[N];  // scale post, pre, and the columns' sums
   {
     float v[E], s[E];
-    load_weight_piece<E>(a.scale, a.weight_dt, col, n, s);
-    load_weight_piece<E>(a.post, a.weight_dt, col, n, v);
+    load_weights<T, ANYWHERE>(a.scale, a.weight_dt, col, n, s);
+    load_weights<T, ANYWHERE>(a.post, a.weight_dt, col, n, v);
 #pragma unroll
     for (int i = 0; i < N; ++i) w1[i] = make_float2(v[2 * i] * s[2 * i], v[2 * i + 1] * s[2 * i + 1]);
-    load_weight_piece<E>(a.pre, a.weight_dt, col, n, v);
+    load_weights<T, ANYWHERE>(a.pre, a.weight_dt, col, n, v);
 #pragma unroll
     for (int i = 0; i < N; ++i) w2[i] = make_float2(v[2 * i], v[2 * i + 1]), dpre[i] = sx[i] = both(0.f);
   }
@@ -243,10 +244,13 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   };
   RowHead next = head(row0);
   const float inv_cols = 1.f / static_cast<float>(cols);
-  T* pdr = static_cast<T*>(a.dresidual) + row0 * a.lddr + col;
-  T* pdx = static_cast<T*>(a.dx) + row0 * a.lddx + col;
-  T* pdg = static_cast<T*>(a.dgate) + (GATE ? row0 * a.lddgate + col : 0);
-  const int ndr = a.dresidual ? n : 0, ndx = a.dx ? n : 0, ndg = GATE && a.dgate ? n : 0;
+  T* pdr = static_cast<T*>(a.dresidual) + row0 * a.lddr + BEGIN * col;
+  T* pdx = static_cast<T*>(a.dx) + row0 * a.lddx + BEGIN * col;
+  T* pdg = static_cast<T*>(a.dgate) + (GATE ? row0 * a.lddgate + BEGIN * col : 0);
+  const auto put = [&](T* p, bool there, const P& v) {
+    if constexpr (ANYWHERE) store_anywhere<T, 32>(p, rank * G + t, there ? cols - (rank * G + t) * E : 0, v);
+    else if (there) v.store(p, n);
+  };
   const bool gate_out = row_gated && a.dgate && t == 0 && rank == 0;
   int slot = 0, turn = 0;
   for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
@@ -254,14 +258,16 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
     if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row, as in the forward kernel
     const RowHead now = next;
     next = head(row + step);
+    if (ANYWHERE) __syncwarp();
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
+    if (ANYWHERE) __syncwarp();
     P d, u, sig, xn, hn;
-    d.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, DY)));
-    u.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, DH)));
-    read_kept(slot, X, xn);
-    read_kept(slot, H, hn);
-    if (GATE) read_kept(slot, GA, sig);
+    read(slot, DY, a.dy, a.lddy, row, d);
+    read(slot, DH, dh, lddh, row, u);
+    read_kept(slot, X, a.x, a.ldx, row, xn);
+    read_kept(slot, H, a.h, a.ldh, row, hn);
+    if (GATE) read_kept(slot, GA, a.gate, a.ldg, row, sig);
     if (R > 1 && !live) {  // the slot holds another row's remains
 #pragma unroll
       for (int i = 0; i < N; ++i) d.v[i] = xn.v[i] = hn.v[i] = u.v[i] = sig.v[i] = both(0.f);
@@ -296,11 +302,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
       dx.v[i] = mul2(both(now.rx), fma2(both(-k2), xn.v[i], b));
       if (GATE) dg.v[i] = mul2(fma2(both(-1.f), sig.v[i], both(1.f)), mul2(b, xn.v[i]));
     }
-    if (live) {
-      dr.store(pdr, ndr);
-      dx.store(pdx, ndx);
-      if (GATE) dg.store(pdg, ndg);
-    }
+    put(pdr, live && a.dresidual, dr);
+    put(pdx, live && a.dx, dx);
+    if (GATE) put(pdg, live && a.dgate, dg);
     pdr += step * a.lddr, pdx += step * a.lddx;
     if (GATE) pdg += step * a.lddgate;
     slot = slot + 1 == S ? 0 : slot + 1;
@@ -337,28 +341,17 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
 }
 
 // The kernels add up rows of `partial` for at most this many CTAs (or clusters).
-inline int most_ctas(int sms) { return kBlockNormCtasPerSm * sms; }
+static int most_ctas(int sms) { return kBlockNormCtasPerSm * sms; }
 
-template <typename T, bool KEPT8>
-static cudaError_t dispatch_grad(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
-  *ctas = static_cast<int>(std::min<long long>(a.rows, 2 * sms));
-  const auto go = [&](auto kernel, int warps) { return launch_pdl(kernel, dim3(*ctas), dim3(warps * 32), 0, st, a, partial); };
-  if (a.cols <= 512) return go(block_norm_grad_kernel<T, 4, 1, KEPT8>, 4);
-  if (a.cols <= 2048) return go(block_norm_grad_kernel<T, 8, 2, KEPT8>, 8);
-  if (a.cols <= 4096) return go(block_norm_grad_kernel<T, 16, 2, KEPT8>, 16);
-  if (a.cols <= 16384) return go(block_norm_grad_kernel<T, 16, 8, KEPT8>, 16);
-  return go(block_norm_grad_kernel<T, 16, 0, KEPT8>, 16);
-}
-
-template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE>
+template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE, bool ANYWHERE>
 static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
-  constexpr int smem = GradRing<T, TH, S, KEPT != 0>::BYTES;
+  constexpr int smem = GradRing<T, TH, S, KEPT != 0, ANYWHERE>::BYTES;
   static_assert(smem * MINB <= 224 * 1024, "shared memory of an SM");
   static_assert(MINB <= kBlockNormCtasPerSm, "rows of partial");
   static bool done[64] = {false};
   static int known[64] = {0};
-  const auto kernel = block_norm_grad_ring_kernel<T, G, S, MINB, CL, KEPT, GATE>;
+  const auto kernel = block_norm_grad_ring_kernel<T, G, S, MINB, CL, KEPT, GATE, ANYWHERE>;
   cudaError_t e = smem_limit(kernel, smem, done);
   if (e != cudaSuccess) return e;
   int most = MINB * sms;
@@ -371,32 +364,37 @@ static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partia
 }
 
 // Threads and CTAs of a row by its width.
-template <typename T, int KEPT, bool GATE>
+template <typename T, int KEPT, bool GATE, bool ANYWHERE>
 static cudaError_t dispatch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const int pieces = static_cast<int>((a.cols + E - 1) / E);
-  if (pieces <= 32) return launch_ring<T, 32, 4, 4, 1, KEPT, GATE>(a, partial, sms, ctas, st);
-  if (pieces <= 64) return launch_ring<T, 64, 4, 4, 1, KEPT, GATE>(a, partial, sms, ctas, st);
-  if (pieces <= 128) return launch_ring<T, 128, 4, 4, 1, KEPT, GATE>(a, partial, sms, ctas, st);
-  if (pieces <= 256) return launch_ring<T, 256, 4, 2, 1, KEPT, GATE>(a, partial, sms, ctas, st);
-  if (pieces <= 512) return launch_ring<T, 512, 5, 1, 1, KEPT, GATE>(a, partial, sms, ctas, st);
-  if (pieces <= 1024) return launch_ring<T, 512, 5, 1, 2, KEPT, GATE>(a, partial, sms, ctas, st);
-  if (pieces <= 2048) return launch_ring<T, 512, 5, 1, 4, KEPT, GATE>(a, partial, sms, ctas, st);
-  return launch_ring<T, 512, 5, 1, 8, KEPT, GATE>(a, partial, sms, ctas, st);
+  if (pieces <= 32) return launch_ring<T, 32, 4, 4, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  if (pieces <= 64) return launch_ring<T, 64, 4, 4, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  if (pieces <= 128) return launch_ring<T, 128, 4, 4, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  if (pieces <= 256) return launch_ring<T, 256, 4, 2, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  if (pieces <= 512) return launch_ring<T, 512, 5, 1, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  if (pieces <= 1024) return launch_ring<T, 512, 5, 1, 2, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  if (pieces <= 2048) return launch_ring<T, 512, 5, 1, 4, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  return launch_ring<T, 512, 5, 1, 8, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
 }
 
-template <typename T>
-cudaError_t launch_block_norm_grad_rows(const muon_block_norm_grad_args& a, float* partial, int vec, int sms, int* ctas, cudaStream_t st) {
+template <typename T, bool ANYWHERE>
+cudaError_t launch_block_norm_grad_rows(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   // 8 CTAs of 512 pieces: 32768 16-bit columns, half as many of fp32
-  if (!vec || a.cols > 8 * 512 * (16 / static_cast<int>(sizeof(T))))
-    return a.x_scale ? dispatch_grad<T, true>(a, partial, sms, ctas, st) : dispatch_grad<T, false>(a, partial, sms, ctas, st);
+  if (a.cols > 8 * 512 * (16 / static_cast<int>(sizeof(T)))) {
+    *ctas = static_cast<int>(std::min<long long>(a.rows, 2 * sms));
+    return a.x_scale ? launch_pdl(block_norm_grad_wide_kernel<T, true>, dim3(*ctas), dim3(512), 0, st, a, partial)
+                     : launch_pdl(block_norm_grad_wide_kernel<T, false>, dim3(*ctas), dim3(512), 0, st, a, partial);
+  }
   const int kept = !a.x_scale ? 0 : a.kept_fmt ? 2 : 1;
   const auto go = [&](auto gate) {
     constexpr bool GATE = decltype(gate)::value;
-    if (kept == 0) return dispatch_ring<T, 0, GATE>(a, partial, sms, ctas, st);
-    return kept == 1 ? dispatch_ring<T, 1, GATE>(a, partial, sms, ctas, st) : dispatch_ring<T, 2, GATE>(a, partial, sms, ctas, st);
+    if (kept == 0) return dispatch_ring<T, 0, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+    return kept == 1 ? dispatch_ring<T, 1, GATE, ANYWHERE>(a, partial, sms, ctas, st) : dispatch_ring<T, 2, GATE, ANYWHERE>(a, partial, sms, ctas, st);
   };
   return a.gate && !a.gate_per_row ? go(std::true_type()) : go(std::false_type());
 }
+template cudaError_t launch_block_norm_grad_rows<MUON_ROWS_T, MUON_ROWS_ANYWHERE>(const muon_block_norm_grad_args&, float*, int, int*,
+                                                                                   cudaStream_t);
 
 }  // namespace muon

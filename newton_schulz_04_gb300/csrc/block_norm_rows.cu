@@ -1,11 +1,12 @@
-// block_norm_rows.cuh -- the norms behind a block and before the next one, with the block's gate and scale between them.
+// block_norm_rows.cu -- the norms behind a block and before the next one, with the block's gate and scale between them.
 //
 //   rho_x = 1 / sqrt(mean_j x_j^2 + eps)       h = alpha residual + sigmoid(gate) scale post (x rho_x)
 //   rho_h = 1 / sqrt(mean_j h_j^2 + eps)       y = h rho_h pre
 //
+// Compiled once for each type and alignment of rows (MUON_ROWS_T, MUON_ROWS_ANYWHERE).
+//
 // Everything goes on in fp32 from unrounded values; y, h, the 8-bit y and the 8-bit copies of x, h and gate are each
 // rounded once.
-#pragma once
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -18,82 +19,63 @@
 
 namespace muon {
 
-// W warps to a row, K blocks to a warp; K = 0: any number, computed from memory again in each phase.
-template <typename T, int W, int K>
-__global__ void __launch_bounds__(W * 32) block_norm_kernel(const muon_block_norm_args a) {
-  constexpr int KK = K ? K : 1;
+// ------------------------------------------------------------------ the widest rows
+// fp32 rows that a cluster's rings do not hold: 16 warps to a row, computed from memory again in each phase.
+template <typename T>
+__global__ void __launch_bounds__(512) block_norm_wide_kernel(const muon_block_norm_args a) {
+  constexpr int W = 16;
   __shared__ float sh[2][1][W];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cols = static_cast<int>(a.cols);
-  const int turns = K ? K : ((cols + 127) / 128 + W - 1) / W;
   const long long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* res = static_cast<const T*>(a.residual) + row * a.ldr;
   const T* gate = static_cast<const T*>(a.gate) + (a.gate ? row * a.ldg : 0);
-  float v[KK][4];
   float sum[1] = {0.f};
   float sig = 1.f;
-  if (a.gate && a.gate_per_row) sig = sigmoid<T>(to_f32(*gate));
-  auto column = [&](int k, int j) { return (warp + W * k) * 128 + lane + 32 * j; };
-#pragma unroll
-  for (int k = 0; k < turns; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = column(k, j);
-      const float f = load_or<T>(x, col, col < cols, 0.f);
-      if (K) v[k < KK ? k : 0][j] = f;
-      sum[0] = fmaf(f, f, sum[0]);
-    }
+  if (a.gate && a.gate_per_row) sig = sigmoid2<T>(both(to_f32(*gate))).x;
+  for (int col = threadIdx.x; col < cols; col += 512) sum[0] = fmaf(to_f32(x[col]), to_f32(x[col]), sum[0]);
   cta_sums<W, 1>(sum, sh, 0);
   const float n = static_cast<float>(cols), inv_n = 1.f / n;
   const float rx = row_rstd(sum[0], n, inv_n, a.eps);
-  auto stream = [&](int col, float f) {
+  auto stream = [&](int col) {
     if (col >= cols) return 0.f;
-    float b = f * rx * (load_weight(a.post, a.weight_dt, col, true) * load_weight(a.scale, a.weight_dt, col, true));
-    b *= a.gate && !a.gate_per_row ? sigmoid<T>(to_f32(gate[col])) : sig;
+    float b = to_f32(x[col]) * rx * (load_weight(a.post, a.weight_dt, col, true) * load_weight(a.scale, a.weight_dt, col, true));
+    b *= a.gate && !a.gate_per_row ? sigmoid2<T>(both(to_f32(gate[col]))).x : sig;
     return fmaf(a.alpha, to_f32(res[col]), b);
   };
   sum[0] = 0.f;
-#pragma unroll
-  for (int k = 0; k < turns; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = column(k, j);
-      const float h = stream(col, K ? v[k < KK ? k : 0][j] : load_or<T>(x, col, col < cols, 0.f));
-      if (K) v[k < KK ? k : 0][j] = h;
-      sum[0] = fmaf(h, h, sum[0]);
-    }
+  for (int col = threadIdx.x; col < cols; col += 512) {
+    const float h = stream(col);
+    sum[0] = fmaf(h, h, sum[0]);
+  }
   cta_sums<W, 1>(sum, sh, 1);
   const float rh = row_rstd(sum[0], n, inv_n, a.eps);
   if (threadIdx.x == 0) {
     if (a.rstd_x) a.rstd_x[row] = rx;
     if (a.rstd_h) a.rstd_h[row] = rh;
   }
-#pragma unroll
-  for (int k = 0; k < turns; ++k) {
-    const int kb = warp + W * k;
-    if (kb * 128 >= cols) break;
+  for (int kb = warp; kb * 128 < cols; kb += W) {
     float h[4], f[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int col = column(k, j);
-      h[j] = K ? v[k < KK ? k : 0][j] : stream(col, load_or<T>(x, col, col < cols, 0.f));
+      const int col = kb * 128 + lane + 32 * j;
+      h[j] = stream(col);
+      f[j] = col < cols ? h[j] * rh * load_weight(a.pre, a.weight_dt, col, true) : 0.f;
       if (a.h && col < cols) static_cast<T*>(a.h)[row * a.ldh + col] = from_f32<T>(h[j]);
-      f[j] = h[j] * rh * load_weight(a.pre, a.weight_dt, col, col < cols);
-      if (col >= cols) f[j] = 0.f;
       if (a.y && col < cols) static_cast<T*>(a.y)[row * a.ldy + col] = from_f32<T>(f[j]);
     }
     if (a.q.data) store_block8(a.q, a.fmt, row, a.rows, cols, kb, f);
     if (a.h8.data) store_block8(a.h8, a.kept_fmt, row, a.rows, cols, kb, h);
     if (a.x8.data) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = load_or<T>(x, column(k, j), column(k, j) < cols, 0.f);
+      for (int j = 0; j < 4; ++j) f[j] = load_or<T>(x, kb * 128 + lane + 32 * j, kb * 128 + lane + 32 * j < cols, 0.f);
       store_block8(a.x8, a.kept_fmt, row, a.rows, cols, kb, f);
     }
     if (a.gate8.data) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = load_or<T>(gate, column(k, j), column(k, j) < cols, 0.f);
+      for (int j = 0; j < 4; ++j) f[j] = load_or<T>(gate, kb * 128 + lane + 32 * j, kb * 128 + lane + 32 * j < cols, 0.f);
       store_block8(a.gate8, a.kept_fmt, row, a.rows, cols, kb, f);
     }
   }
@@ -104,10 +86,25 @@ __global__ void __launch_bounds__(W * 32) block_norm_kernel(const muon_block_nor
 }
 
 // ------------------------------------------------------------------ ring of rows
+// S rows of x, residual and gate, C pieces each: a thread's own 16 bytes, or (ANYWHERE) a warp's 33 times 16.
+template <typename T, int TH, int C, int S, bool ANYWHERE>
+struct RowRing {
+  static constexpr int ARRAY = ANYWHERE ? TH / 32 * kWarpSlot : TH * 16, BYTES = S * 3 * C * ARRAY;
+  uint8_t* base;
+  __device__ __forceinline__ uint8_t* at(int slot, int arr, int c) const {
+    uint8_t* p = base + ((slot * 3 + arr) * C + c) * ARRAY;
+    return ANYWHERE ? p + threadIdx.x / 32 * kWarpSlot : p + threadIdx.x * 16;
+  }
+  __device__ __forceinline__ uint4 piece(int slot, int arr, int c, int off) const {
+    if constexpr (ANYWHERE) return read_anywhere(at(slot, arr, c), off);
+    else return *reinterpret_cast<const uint4*>(at(slot, arr, c));
+  }
+};
+
 // CL CTAs of a cluster to a row, G threads of each, C pieces of 16 bytes to a thread, a ring of S rows.  GATE: a gate of every
 // element.  EIGHT: 8-bit outputs; 0: none, 1: any, 2: all of e4m3 and the copies for the gradient among them.  Compiled apart:
 // choices at run time leave pieces of code too small to be overlapped.
-template <typename T, int G, int C, int S, int MINB, int CL, bool GATE, int EIGHT>
+template <typename T, int G, int C, int S, int MINB, int CL, bool GATE, int EIGHT, bool ANYWHERE>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kernel(const muon_block_norm_args a) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
   using P = Pairs<T>;
@@ -115,7 +112,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
   using Scales = Scales4<128 / E>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ RowSums<G, TH, 1, CL> sums;
-  const Ring<T, TH, C, S, 3> ring{ring_smem};
+  const RowRing<T, TH, C, S, ANYWHERE> ring{ring_smem};
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
   const int col = (rank * C * G + t) * E;  // of the first piece
@@ -125,17 +122,24 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
   const bool row_gated = !GATE && a.gate;
   const long long step = static_cast<long long>(gridDim.x / CL) * R, row0 = static_cast<long long>(blockIdx.x / CL) * R + rr;
   long long frow = row0;  // next row to fetch
-  const T* fx = static_cast<const T*>(a.x) + row0 * a.ldx + col;
-  const T* fr = static_cast<const T*>(a.residual) + row0 * a.ldr + col;
-  const T* fg = static_cast<const T*>(a.gate) + (GATE ? row0 * a.ldg + col : 0);
+  constexpr int BEGIN = ANYWHERE ? 0 : 1;  // pointers to rows, or to the thread's pieces of them
+  const T* fx = static_cast<const T*>(a.x) + row0 * a.ldx + BEGIN * col;
+  const T* fr = static_cast<const T*>(a.residual) + row0 * a.ldr + BEGIN * col;
+  const T* fg = static_cast<const T*>(a.gate) + (GATE ? row0 * a.ldg + BEGIN * col : 0);
   auto fetch = [&](int slot) {
     if (frow < a.rows) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int bytes = n[c] * static_cast<int>(sizeof(T)), at = n[c] ? c * PIECE : -col;
-        ring.fetch(slot, 0, c, fx + at, bytes);
-        ring.fetch(slot, 1, c, fr + at, bytes);
-        if (GATE) ring.fetch(slot, 2, c, fg + at, bytes);
+        const auto get = [&](int arr, const T* row, const void* matrix) {
+          if constexpr (ANYWHERE) {
+            fetch_anywhere<T>(ring.at(slot, arr, c), row, (col + c * PIECE) / E, cols, static_cast<const uint8_t*>(matrix));
+          } else {
+            copy16(smem_u32(ring.at(slot, arr, c)), row + (n[c] ? c * PIECE : -col), n[c] * static_cast<int>(sizeof(T)));
+          }
+        };
+        get(0, fx, a.x);
+        get(1, fr, a.residual);
+        if (GATE) get(2, fg, a.gate);
       }
     }
     cp_async_commit();
@@ -151,11 +155,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
   for (int c = 0; c < C; ++c) {
     const int at = n[c] ? col + c * PIECE : 0;
     float v[E], s[E];
-    load_weight_piece<E>(a.scale, a.weight_dt, at, n[c], s);
-    load_weight_piece<E>(a.post, a.weight_dt, at, n[c], v);
+    load_weights<T, ANYWHERE>(a.scale, a.weight_dt, at, n[c], s);
+    load_weights<T, ANYWHERE>(a.post, a.weight_dt, at, n[c], v);
 #pragma unroll
     for (int i = 0; i < N; ++i) w1[c][i] = make_float2(v[2 * i] * s[2 * i], v[2 * i + 1] * s[2 * i + 1]);
-    load_weight_piece<E>(a.pre, a.weight_dt, at, n[c], v);
+    load_weights<T, ANYWHERE>(a.pre, a.weight_dt, at, n[c], v);
 #pragma unroll
     for (int i = 0; i < N; ++i) w2[c][i] = make_float2(v[2 * i], v[2 * i + 1]);
   }
@@ -164,8 +168,16 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
   };
   float next_gate = row_gate(row0);  // a row ahead
   const float fcols = static_cast<float>(cols), inv_cols = 1.f / fcols;
-  T* ph = static_cast<T*>(a.h) + row0 * a.ldh + col;
-  T* py = static_cast<T*>(a.y) + row0 * a.ldy + col;
+  T* ph = static_cast<T*>(a.h) + row0 * a.ldh + BEGIN * col;
+  T* py = static_cast<T*>(a.y) + row0 * a.ldy + BEGIN * col;
+  const auto put = [&](T* p, int c, bool live, const P& v) {
+    if constexpr (ANYWHERE) store_anywhere<T, 32>(p, (col + c * PIECE) / E, live ? cols - col - c * PIECE : 0, v);
+    else if (live) v.store(p + c * PIECE, n[c]);
+  };
+  // rows' addresses modulo 16
+  const auto off = [&](const void* p, long long ld, long long row) {
+    return static_cast<int>((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) + static_cast<uint32_t>(row * ld) * sizeof(T)) & 15u);
+  };
   // the 8-bit copies: y, h, x, gate; each lane keeps the scales of one of them
   uint8_t* p8[4] = {static_cast<uint8_t*>(a.q.data) + row0 * a.q.ld + col, static_cast<uint8_t*>(a.h8.data) + row0 * a.h8.ld + col,
                     static_cast<uint8_t*>(a.x8.data) + row0 * a.x8.ld + col, static_cast<uint8_t*>(a.gate8.data) + row0 * a.gate8.ld + col};
@@ -181,15 +193,19 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
     if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row: earlier, the next kernel's CTAs take SMs from these
     float2 sig = both(1.f);
     if (row_gated) sig = both(sigmoid2<T>(both(next_gate)).x), next_gate = row_gate(row + step);
+    if (ANYWHERE) __syncwarp();
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
+    if (ANYWHERE) __syncwarp();
+    const int ox = ANYWHERE ? off(a.x, a.ldx, row) : 0, orr = ANYWHERE ? off(a.residual, a.ldr, row) : 0;
+    const int og = ANYWHERE && GATE ? off(a.gate, a.ldg, row) : 0;
     P h[C];
     float2 two = both(0.f);
     float sum[1];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       P x;
-      x.unpack(ring.piece(slot, 0, c));
+      x.unpack(ring.piece(slot, 0, c, ox));
 #pragma unroll
       for (int i = 0; i < N; ++i) two = fma2(x.v[i], x.v[i], two);
     }
@@ -200,9 +216,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       P x, g;
-      x.unpack(ring.piece(slot, 0, c));
-      h[c].unpack(ring.piece(slot, 1, c));
-      if (GATE) g.unpack(ring.piece(slot, 2, c));
+      x.unpack(ring.piece(slot, 0, c, ox));
+      h[c].unpack(ring.piece(slot, 1, c, orr));
+      if (GATE) g.unpack(ring.piece(slot, 2, c, og));
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (GATE) sig = sigmoid2<T>(g.v[i]);
@@ -224,13 +240,13 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
       P y;
 #pragma unroll
       for (int i = 0; i < N; ++i) y.v[i] = mul2(mul2(h[c].v[i], both(rh)), w2[c][i]);
-      if (live && a.h) h[c].store(ph + c * PIECE, n[c]);
-      if (live && a.y) y.store(py + c * PIECE, n[c]);
+      if (a.h) put(ph, c, live, h[c]);
+      if (a.y) put(py, c, live, y);
       if (EIGHT) {
         P x, g;
         uint32_t m[4] = {y.largest(), h[c].largest(), 0u, 0u};
-        if (EIGHT == 2 || a.x8.data) x.unpack(ring.piece(slot, 0, c)), m[2] = x.largest();
-        if (GATE && (EIGHT == 2 || a.gate8.data)) g.unpack(ring.piece(slot, 2, c)), m[3] = g.largest();
+        if (EIGHT == 2 || a.x8.data) x.unpack(ring.piece(slot, 0, c, ox)), m[2] = x.largest();
+        if (GATE && (EIGHT == 2 || a.gate8.data)) g.unpack(ring.piece(slot, 2, c, og)), m[3] = g.largest();
         const Scales s(m, top);
         if (live && col + c * PIECE < cols16) {
           if constexpr (EIGHT == 2) {
@@ -266,14 +282,14 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
       for (int kb = t; kb < end; kb += G) fill(a.q, kb, row), fill(a.h8, kb, row), fill(a.x8, kb, row), fill(a.gate8, kb, row);
 }
 
-template <typename T, int G, int C, int S, int MINB, int CL, bool GATE, int EIGHT>
+template <typename T, int G, int C, int S, int MINB, int CL, bool GATE, int EIGHT, bool ANYWHERE>
 static cudaError_t launch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
-  constexpr int smem = Ring<T, TH, C, S, 3>::BYTES;
+  constexpr int smem = RowRing<T, TH, C, S, ANYWHERE>::BYTES;
   static_assert(smem * MINB <= 220 * 1024, "shared memory of an SM");
   static bool done[64] = {false};
   static int known[64] = {0};
-  const auto kernel = block_norm_ring_kernel<T, G, C, S, MINB, CL, GATE, EIGHT>;
+  const auto kernel = block_norm_ring_kernel<T, G, C, S, MINB, CL, GATE, EIGHT, ANYWHERE>;
   cudaError_t e = smem_limit(kernel, smem, done);
   if (e != cudaSuccess) return e;
   int most = MINB * sms;
@@ -286,46 +302,36 @@ static cudaError_t launch_ring(const muon_block_norm_args& a, int sms, cudaStrea
 }
 
 // Threads, pieces and CTAs of a row by its width.
-template <typename T, bool GATE, int EIGHT>
+template <typename T, bool GATE, int EIGHT, bool ANYWHERE>
 static cudaError_t dispatch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const int pieces = static_cast<int>((a.cols + E - 1) / E);
-  if (pieces <= 32) return launch_ring<T, 32, 1, 8, 4, 1, GATE, EIGHT>(a, sms, st);
-  if (pieces <= 64) return launch_ring<T, 64, 1, 6, 5, 1, GATE, EIGHT>(a, sms, st);
-  if (pieces <= 128) return launch_ring<T, 128, 1, 6, 5, 1, GATE, EIGHT>(a, sms, st);
-  if (pieces <= 256) return launch_ring<T, 256, 1, 6, 3, 1, GATE, EIGHT>(a, sms, st);
-  if (pieces <= 512) return launch_ring<T, 256, 2, 4, 2, 1, GATE, EIGHT>(a, sms, st);
-  if (pieces <= 1024) return launch_ring<T, 512, 2, 4, 1, 1, GATE, EIGHT>(a, sms, st);
-  if (pieces <= 2048) return launch_ring<T, 512, 2, 4, 1, 2, GATE, EIGHT>(a, sms, st);
-  if (pieces <= 4096) return launch_ring<T, 512, 2, 4, 1, 4, GATE, EIGHT>(a, sms, st);
-  return launch_ring<T, 512, 2, 4, 1, 8, GATE, EIGHT>(a, sms, st);
+  if (pieces <= 32) return launch_ring<T, 32, 1, 8, 4, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  if (pieces <= 64) return launch_ring<T, 64, 1, 6, 5, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  if (pieces <= 128) return launch_ring<T, 128, 1, 6, 5, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  if (pieces <= 256) return launch_ring<T, 256, 1, 5, 3, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  if (pieces <= 512) return launch_ring<T, 256, 2, 4, 2, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  if (pieces <= 1024) return launch_ring<T, 512, 2, 4, 1, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  if (pieces <= 2048) return launch_ring<T, 512, 2, 4, 1, 2, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  if (pieces <= 4096) return launch_ring<T, 512, 2, 4, 1, 4, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  return launch_ring<T, 512, 2, 4, 1, 8, GATE, EIGHT, ANYWHERE>(a, sms, st);
 }
 
-template <typename T>
-static cudaError_t dispatch_norm(const muon_block_norm_args& a, cudaStream_t st) {
-  const auto go = [&](auto kernel, int warps) {
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(a.rows)), dim3(warps * 32), 0, st, a);
-  };
-  if (a.cols <= 512) return go(block_norm_kernel<T, 4, 1>, 4);
-  if (a.cols <= 2048) return go(block_norm_kernel<T, 8, 2>, 8);
-  if (a.cols <= 4096) return go(block_norm_kernel<T, 16, 2>, 16);
-  if (a.cols <= 16384) return go(block_norm_kernel<T, 16, 8>, 16);
-  return go(block_norm_kernel<T, 16, 0>, 16);
-}
-
-template <typename T>
-cudaError_t launch_block_norm_rows(const muon_block_norm_args& a, int vec, int sms, cudaStream_t st) {
+template <typename T, bool ANYWHERE>
+cudaError_t launch_block_norm_rows(const muon_block_norm_args& a, int sms, cudaStream_t st) {
   // 8 CTAs of 1024 pieces hold MUON_MAX_DIM 16-bit columns and half as many of fp32
-  if (!vec || a.cols > 8 * 1024 * (16 / static_cast<int>(sizeof(T)))) return dispatch_norm<T>(a, st);
+  if (a.cols > 8 * 1024 * (16 / static_cast<int>(sizeof(T))))
+    return launch_pdl(block_norm_wide_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(512), 0, st, a);
   const bool element = a.gate && !a.gate_per_row, kept = a.x8.data && a.h8.data && (a.gate8.data || !element);
   const bool e4m3 = kept && a.kept_fmt == MUON_E4M3 && (!a.q.data || a.fmt == MUON_E4M3);
   const bool any = a.q.data || a.x8.data || a.h8.data || a.gate8.data;
   const auto go = [&](auto gate) {
     constexpr bool GATE = decltype(gate)::value;
-    if (!any) return dispatch_ring<T, GATE, 0>(a, sms, st);
-    return e4m3 ? dispatch_ring<T, GATE, 2>(a, sms, st) : dispatch_ring<T, GATE, 1>(a, sms, st);
+    if (!any) return dispatch_ring<T, GATE, 0, ANYWHERE>(a, sms, st);
+    return e4m3 ? dispatch_ring<T, GATE, 2, ANYWHERE>(a, sms, st) : dispatch_ring<T, GATE, 1, ANYWHERE>(a, sms, st);
   };
   return element ? go(std::true_type()) : go(std::false_type());
 }
+template cudaError_t launch_block_norm_rows<MUON_ROWS_T, MUON_ROWS_ANYWHERE>(const muon_block_norm_args&, int, cudaStream_t);
 
 }  // namespace muon

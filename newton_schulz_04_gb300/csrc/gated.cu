@@ -79,16 +79,6 @@ __device__ __forceinline__ uint4 load_part(const T* p, int n) {
     if (i < n) u.e[i] = p[i];
   return u.w;
 }
-template <typename T, bool GELU>
-__device__ __forceinline__ Activation activate(float g) {
-  if (GELU) {
-    const float phi = normcdff(g);
-    return {g * phi, fmaf(g * 0.3989422804f, __expf(-0.5f * g * g), phi)};
-  }
-  const float s = sigmoid<T>(g), v = g * s;
-  return {v, fmaf(v, 1.f - s, s)};
-}
-
 // ------------------------------------------------------------------ forward
 // A block of 128 columns to 16 lanes (32 in fp32), U rows to a lane, fetched together.  EIGHT: 8-bit outputs; 0: none, 1: any, 2:
 // both checkpoints, and all of e4m3.  ANYWHERE: rows that do not start on 16 bytes.
@@ -320,26 +310,29 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
   }
   // the kept rows' scales: lane l has those of row l (gate) and row l - 16 (up)
   const long long rows4 = (rows + 3) & ~3LL;
+  const int rows_here = static_cast<int>(max(0LL, min(16LL, rows - r0))), rows4_here = static_cast<int>(max(0LL, min(16LL, rows4 - r0)));
   uint32_t kept_scale = 127u;
-  if (KEPT && r0 + lane % 16 < rows)
+  if (KEPT && lane % 16 < rows_here)
     kept_scale = static_cast<const uint8_t*>(lane < 16 ? a.gate_scale : a.up_scale)[fp8_scale_offset(kbc, r0 + lane % 16, rows4)];
-  const float kept_value = fp8_scale_value(kept_scale);
+  __shared__ float kept_values[kTileWarps][32];
+  kept_values[warp][lane] = fp8_scale_value(kept_scale);
   const int n = static_cast<int>(max(0LL, min(4LL, left - lane * 4)));  // the lane's columns
   const long long col = c00 + lane * 4;
   const bool store8 = col < ((cols + 15) & ~15LL);
   const bool by_cols = a.dgate_cols.data || a.dup_cols.data || a.y_cols.data;
-  // values of a row of the tile
-  const auto load = [&](int r, float2 (&d)[2], float2 (&g)[2], float2 (&u)[2]) {
-    const uint8_t* chunk = mine + r / kChunkRows * G::CHUNK;
-    const int i = r % kChunkRows;
-    four(reinterpret_cast<const T*>(chunk + i * G::DY) + lane * 4, d);
-    const K* pg = reinterpret_cast<const K*>(chunk + kChunkRows * G::DY + i * G::KEEP) + lane * 4;
-    const K* pu = reinterpret_cast<const K*>(chunk + kChunkRows * (G::DY + G::KEEP) + i * G::KEEP) + lane * 4;
-    if constexpr (KEPT != 0) {
-      four8<KEPT == 2>(pg, __shfl_sync(0xffffffffu, kept_value, r), g);
-      four8<KEPT == 2>(pu, __shfl_sync(0xffffffffu, kept_value, r + 16), u);
-    } else {
-      four(pg, g), four(pu, u);
+  // values of a row of a chunk, with the chunk's kept scales
+  const auto load = [&](int chunk, int i, const float (&gs)[4], const float (&us)[4], float2 (&d)[2], float2 (&g)[2], float2 (&u)[2]) {
+    const uint8_t* p = mine + chunk * G::CHUNK;
+    four(reinterpret_cast<const T*>(p + i * G::DY) + lane * 4, d);
+    const K* pg = reinterpret_cast<const K*>(p + kChunkRows * G::DY + i * G::KEEP) + lane * 4;
+    const K* pu = reinterpret_cast<const K*>(p + kChunkRows * (G::DY + G::KEEP) + i * G::KEEP) + lane * 4;
+    if constexpr (KEPT != 0) four8<KEPT == 2>(pg, gs[i], g), four8<KEPT == 2>(pu, us[i], u);
+    else four(pg, g), four(pu, u);
+  };
+  const auto kept_of = [&](int at, float (&s)[4]) {
+    if (KEPT) {
+      const float4 f = *reinterpret_cast<const float4*>(&kept_values[warp][at]);
+      s[0] = f.x, s[1] = f.y, s[2] = f.z, s[3] = f.w;
     }
   };
   float cm[3][4];
@@ -352,6 +345,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
   const muon_fp8_out& my_rows = my_out ? a.dup_rows : a.dgate_rows;
   uint8_t* const my_scales = lane % 4 == 0 ? static_cast<uint8_t*>(my_rows.scale) : nullptr;
   const bool by_rows = a.dgate_rows.data || a.dup_rows.data;
+  uint8_t* rows_g = static_cast<uint8_t*>(a.dgate_rows.data) + r0 * a.dgate_rows.ld + col;
+  uint8_t* rows_u = static_cast<uint8_t*>(a.dup_rows.data) + r0 * a.dup_rows.ld + col;
 #pragma unroll 1
   for (int chunk = 0; chunk < kChunks; ++chunk) {
     if (chunk == 0) cp_async_wait<kChunks - 1>();
@@ -359,12 +354,14 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
     else if (chunk == 2) cp_async_wait<kChunks - 3>();
     else cp_async_wait<0>();
     __syncwarp();
-    float2 dg[kChunkRows][2], du[kChunkRows][2];
+    float2 dg[kChunkRows][2], du[kChunkRows][2], y_before[2];
     uint32_t m[kChunkRows];
+    float gs[4], us[4];
+    kept_of(chunk * kChunkRows, gs), kept_of(16 + chunk * kChunkRows, us);
 #pragma unroll
     for (int r = 0; r < kChunkRows; ++r) {
       float2 d[2], g[2], u[2];
-      load(chunk * kChunkRows + r, d, g, u);
+      load(chunk, r, gs, us, d, g, u);
       float mg = 0.f, mu = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -374,8 +371,12 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
         du[r][i] = mul2(d[i], f.value);
         mg = largest3(mg, dg[r][i].x, dg[r][i].y);
         mu = largest3(mu, du[r][i].x, du[r][i].y);
-        cm[2][2 * i] = largest3(cm[2][2 * i], y.x, 0.f);
-        cm[2][2 * i + 1] = largest3(cm[2][2 * i + 1], y.y, 0.f);
+        if (r % 2 == 0) {
+          y_before[i] = y;
+        } else {
+          cm[2][2 * i] = largest3(cm[2][2 * i], y_before[i].x, y.x);
+          cm[2][2 * i + 1] = largest3(cm[2][2 * i + 1], y_before[i].y, y.y);
+        }
       }
       m[r] = __byte_perm(__float_as_uint(mg) + 0xffffu, __float_as_uint(mu) + 0xffffu, 0x7632);
       if (r % 2 == 1) {
@@ -418,8 +419,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
       uint32_t w = __vmaxu2(odd ? w1 : w0, __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, 8));
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, o));
-      const uint32_t byte = row0 + my_row < rows ? fp8_scale_byte(my_out ? w & 0xffff0000u : w << 16, top) : 127u;
-      if (my_scales && row0 + my_row < rows4) {
+      const uint32_t byte = chunk * kChunkRows + my_row < rows_here ? fp8_scale_byte(my_out ? w & 0xffff0000u : w << 16, top) : 127u;
+      if (my_scales && chunk * kChunkRows + my_row < rows4_here) {
         my_scales[fp8_scale_offset(kbc, row0 + my_row, rows4)] = static_cast<uint8_t>(byte);
         if (left <= kTile)  // blocks past the last column, up to a whole scale word
           for (long long kb = kbc + 1; kb < (cols + 511) / 512 * 4; ++kb) my_scales[fp8_scale_offset(kb, row0 + my_row, rows4)] = 127;
@@ -431,17 +432,17 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
         ig[r] = __shfl_sync(0xffffffffu, my_inv, 8 * r);
         iu[r] = __shfl_sync(0xffffffffu, my_inv, 8 * r + 4);
       }
-      uint8_t* pg = static_cast<uint8_t*>(a.dgate_rows.data) + row0 * a.dgate_rows.ld + col;
-      uint8_t* pu = static_cast<uint8_t*>(a.dup_rows.data) + row0 * a.dup_rows.ld + col;
+      uint8_t *pg = rows_g, *pu = rows_u;
+      rows_g += kChunkRows * a.dgate_rows.ld, rows_u += kChunkRows * a.dup_rows.ld;
       const auto put = [&](auto e5m2) {
         constexpr bool E5M2 = decltype(e5m2)::value;
 #pragma unroll
         for (int r = 0; r < kChunkRows; ++r) {
           const uint32_t wg = pack_scaled<E5M2>(dg[r][0], dg[r][1], ig[r]), wu = pack_scaled<E5M2>(du[r][0], du[r][1], iu[r]);
-          if (store8 && row0 + r < rows) {
-            if (a.dgate_rows.data) *reinterpret_cast<uint32_t*>(pg + r * a.dgate_rows.ld) = wg;
-            if (a.dup_rows.data) *reinterpret_cast<uint32_t*>(pu + r * a.dup_rows.ld) = wu;
-          }
+          const bool in = store8 && chunk * kChunkRows + r < rows_here;
+          if (in && a.dgate_rows.data) *reinterpret_cast<uint32_t*>(pg) = wg;
+          if (in && a.dup_rows.data) *reinterpret_cast<uint32_t*>(pu) = wu;
+          pg += a.dgate_rows.ld, pu += a.dup_rows.ld;
         }
       };
       if (a.fmt) put(std::true_type());
@@ -481,10 +482,12 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
 #pragma unroll 1
   for (int chunk = 0; chunk < kChunks; ++chunk) {
     float2 v[3][kChunkRows][2];
+    float gs[4], us[4];
+    kept_of(chunk * kChunkRows, gs), kept_of(16 + chunk * kChunkRows, us);
 #pragma unroll
     for (int r = 0; r < kChunkRows; ++r) {
       float2 d[2], g[2], u[2];
-      load(chunk * kChunkRows + r, d, g, u);
+      load(chunk, r, gs, us, d, g, u);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const Activation f = activate2<T, GELU>(g[i]);

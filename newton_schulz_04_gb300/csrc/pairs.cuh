@@ -5,6 +5,7 @@
 
 #include "fp8.cuh"
 #include "ptx.cuh"
+#include "row_ring.cuh"
 
 namespace muon {
 
@@ -200,6 +201,39 @@ __device__ __forceinline__ void store_anywhere(T* row, int t, int left, const Pa
 #pragma unroll
   for (int i = 0; i < E; ++i)
     if (i < left && (i < head ? !whole : tail)) row[t * E + i] = u.e[i];
+}
+
+// A ring's slot of one array and piece for rows that start anywhere: the 16 aligned bytes of each lane and the next lane's, 33
+// for a warp, from which a lane takes its own by `window`.  The warp is synchronised before it reads and before it fetches
+// into the same slot again.
+constexpr int kWarpSlot = 33 * 16;
+template <typename T>
+__device__ __forceinline__ void fetch_anywhere(uint8_t* slot, const T* row, int t, int cols, const uint8_t* from) {
+  constexpr int E = 16 / static_cast<int>(sizeof(T));
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x % 32;
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(row) - off + 16LL * t;
+  const long long there = static_cast<long long>(cols) * static_cast<int>(sizeof(T)) + off - 16LL * t;  // bytes to the row's end
+  const auto get = [&](int at, const uint8_t* src, long long bytes) {
+    const int n = static_cast<int>(max(0LL, min(16LL, bytes)));
+    if (src < from) {  // the matrix begins within these 16 bytes
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const uint8_t* q = src + i * sizeof(T);
+        reinterpret_cast<T*>(slot + at * 16)[i] = q >= from && i * static_cast<int>(sizeof(T)) < n ? *reinterpret_cast<const T*>(q) : from_f32<T>(0.f);
+      }
+    } else if (n == 0) {
+      *reinterpret_cast<uint4*>(slot + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      copy16(smem_u32(slot + at * 16), src, n);
+    }
+  };
+  get(lane, p, there);
+  if (lane == 31) get(32, p + 16, there - 16);
+}
+// off: the row's address modulo 16.
+__device__ __forceinline__ uint4 read_anywhere(const uint8_t* slot, int off) {
+  const uint4* q = reinterpret_cast<const uint4*>(slot) + threadIdx.x % 32;
+  return window(q[0], q[1], off);
 }
 
 // Scales of up to four matrices' blocks, whose 128 columns lie in LANES = 16 or 32 neighbouring lanes.  The largest
