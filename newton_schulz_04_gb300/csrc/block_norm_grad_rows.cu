@@ -125,15 +125,16 @@ __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int by
 }
 
 // A thread's slots: S rows of dy, dh, x, h and gate, a piece each; kept 8-bit ones take E bytes instead of 16.
-// ANYWHERE: of T, a warp's 33 times 16 bytes.
-template <typename T, int TH, int S, bool KEPT8, bool ANYWHERE>
+// ANYWHERE: of T, a warp's and a little more.
+template <typename T, int G, int S, bool KEPT8, bool ANYWHERE>
 struct GradRing {
-  static constexpr int E = 16 / static_cast<int>(sizeof(T)), WIDE = KEPT8 ? 2 : 5, ARRAY = ANYWHERE ? TH / 32 * kWarpSlot : TH * 16;
+  static constexpr int TH = G < 128 ? 128 : G, LANES = G < 32 ? G : 32;
+  static constexpr int E = 16 / static_cast<int>(sizeof(T)), WIDE = KEPT8 ? 2 : 5, ARRAY = ANYWHERE ? TH / 32 * kWarpSlot<LANES> : TH * 16;
   static constexpr int STAGE = WIDE * ARRAY + (5 - WIDE) * TH * E, BYTES = S * STAGE;
   uint8_t* base;
   __device__ __forceinline__ uint8_t* at(int slot, int arr) const {
     uint8_t* stage = base + slot * STAGE;
-    if (arr < WIDE) return stage + arr * ARRAY + (ANYWHERE ? threadIdx.x / 32 * kWarpSlot : threadIdx.x * 16);
+    if (arr < WIDE) return stage + arr * ARRAY + (ANYWHERE ? threadIdx.x / 32 * kWarpSlot<LANES> : threadIdx.x * 16);
     return stage + WIDE * ARRAY + ((arr - WIDE) * TH + static_cast<int>(threadIdx.x)) * E;
   }
 };
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   constexpr int DY = 0, DH = 1, X = 2, H = 3, GA = 4;
   using P = Pairs<T>;
   using K = std::conditional_t<KEPT != 0, uint8_t, T>;
-  using Slots = GradRing<T, TH, S, KEPT != 0, ANYWHERE>;
+  using Slots = GradRing<T, G, S, KEPT != 0, ANYWHERE>;
   constexpr int E = P::E, N = P::N;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ RowSums<G, TH, 3, CL> sums;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
     if (frow < a.rows) {
       const auto plain = [&](int arr, const T* row, const void* matrix, bool there) {
         if constexpr (ANYWHERE)
-          fetch_anywhere<T>(ring.at(slot, arr), row, rank * G + t, there ? cols : 0, static_cast<const uint8_t*>(matrix));
+          fetch_anywhere<T, Slots::LANES>(ring.at(slot, arr), row, rank * G + t, there ? cols : 0, static_cast<const uint8_t*>(matrix));
         else copy16(smem_u32(ring.at(slot, arr)), row, there ? n * static_cast<int>(sizeof(T)) : 0);
       };
       const auto kept = [&](int arr, const K* row, const void* matrix) {
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   const auto read = [&](int slot, int arr, const void* matrix, long long ld, long long row, P& p) {
     if constexpr (ANYWHERE) {
       const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(matrix)) + static_cast<uint32_t>(row * ld) * sizeof(T);
-      p.unpack(read_anywhere(ring.at(slot, arr), static_cast<int>(at & 15u)));
+      p.unpack(read_anywhere<Slots::LANES>(ring.at(slot, arr), static_cast<int>(at & 15u)));
     } else {
       p.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, arr)));
     }
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   T* pdx = static_cast<T*>(a.dx) + row0 * a.lddx + BEGIN * col;
   T* pdg = static_cast<T*>(a.dgate) + (GATE ? row0 * a.lddgate + BEGIN * col : 0);
   const auto put = [&](T* p, bool there, const P& v) {
-    if constexpr (ANYWHERE) store_anywhere<T, 32>(p, rank * G + t, there ? cols - (rank * G + t) * E : 0, v);
+    if constexpr (ANYWHERE) store_anywhere<T, Slots::LANES>(p, rank * G + t, there ? cols - (rank * G + t) * E : 0, v);
     else if (there) v.store(p, n);
   };
   const bool gate_out = row_gated && a.dgate && t == 0 && rank == 0;
@@ -346,7 +347,7 @@ static int most_ctas(int sms) { return kBlockNormCtasPerSm * sms; }
 template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE, bool ANYWHERE>
 static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
-  constexpr int smem = GradRing<T, TH, S, KEPT != 0, ANYWHERE>::BYTES;
+  constexpr int smem = GradRing<T, G, S, KEPT != 0, ANYWHERE>::BYTES;
   static_assert(smem * MINB <= 224 * 1024, "shared memory of an SM");
   static_assert(MINB <= kBlockNormCtasPerSm, "rows of partial");
   static bool done[64] = {false};
@@ -363,19 +364,32 @@ static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partia
   return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(*ctas * CL)), dim3(TH), smem, CL, st, a, partial);
 }
 
-// Threads and CTAs of a row by its width.
+template <int N>
+using Int = std::integral_constant<int, N>;
+// Threads of a CTA, rows of the ring, CTAs of an SM and of a cluster by a row's width, as measured at 33.5M elements.
 template <typename T, int KEPT, bool GATE, bool ANYWHERE>
 static cudaError_t dispatch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const int pieces = static_cast<int>((a.cols + E - 1) / E);
-  if (pieces <= 32) return launch_ring<T, 32, 4, 4, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
-  if (pieces <= 64) return launch_ring<T, 64, 4, 4, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
-  if (pieces <= 128) return launch_ring<T, 128, 4, 4, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
-  if (pieces <= 256) return launch_ring<T, 256, 4, 2, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
-  if (pieces <= 512) return launch_ring<T, 512, 5, 1, 1, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
-  if (pieces <= 1024) return launch_ring<T, 512, 5, 1, 2, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
-  if (pieces <= 2048) return launch_ring<T, 512, 5, 1, 4, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
-  return launch_ring<T, 512, 5, 1, 8, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  const auto go = [&](auto threads, auto depth, auto ctas_per_sm, auto cluster) {
+    return launch_ring<T, decltype(threads)::value, decltype(depth)::value, decltype(ctas_per_sm)::value, decltype(cluster)::value, KEPT,
+                       GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  };
+  if (pieces <= 16) return go(Int<16>(), Int<4>(), Int<4>(), Int<1>());
+  if (pieces <= 32) return go(Int<32>(), Int<4>(), Int<4>(), Int<1>());
+  if (pieces <= 64) return go(Int<64>(), Int<4>(), Int<4>(), Int<1>());
+  if (pieces <= 128) return go(Int<128>(), Int<4>(), Int<4>(), Int<1>());
+  if (pieces <= 256) return go(Int<256>(), Int<4>(), Int<2>(), Int<1>());
+  if (pieces <= 512) return go(Int<512>(), Int<4>(), Int<1>(), Int<1>());
+  // 33.5M elements at 8192 columns: from 8 bits 126 us in clusters of four small CTAs, two of which share an SM and overlap
+  // their exchanges, 139 in clusters of two large ones; from 16 bits 165 and 144
+  if constexpr (KEPT != 0) {
+    if (pieces <= 1024) return go(Int<256>(), Int<5>(), Int<2>(), Int<4>());
+  } else {
+    if (pieces <= 1024) return go(Int<512>(), Int<5>(), Int<1>(), Int<2>());
+  }
+  if (pieces <= 2048) return go(Int<512>(), Int<5>(), Int<1>(), Int<4>());
+  return go(Int<512>(), Int<5>(), Int<1>(), Int<8>());
 }
 
 template <typename T, bool ANYWHERE>

@@ -86,33 +86,35 @@ __global__ void __launch_bounds__(512) block_norm_wide_kernel(const muon_block_n
 }
 
 // ------------------------------------------------------------------ ring of rows
-// S rows of x, residual and gate, C pieces each: a thread's own 16 bytes, or (ANYWHERE) a warp's 33 times 16.
-template <typename T, int TH, int C, int S, bool ANYWHERE>
+// S rows of x, residual and gate, C pieces each: a thread's own 16 bytes, or (ANYWHERE) a warp's and a little more.
+template <typename T, int G, int C, int S, bool ANYWHERE>
 struct RowRing {
-  static constexpr int ARRAY = ANYWHERE ? TH / 32 * kWarpSlot : TH * 16, BYTES = S * 3 * C * ARRAY;
+  static constexpr int TH = G < 128 ? 128 : G, LANES = G < 32 ? G : 32;
+  static constexpr int ARRAY = ANYWHERE ? TH / 32 * kWarpSlot<LANES> : TH * 16, BYTES = S * 3 * C * ARRAY;
   uint8_t* base;
   __device__ __forceinline__ uint8_t* at(int slot, int arr, int c) const {
     uint8_t* p = base + ((slot * 3 + arr) * C + c) * ARRAY;
-    return ANYWHERE ? p + threadIdx.x / 32 * kWarpSlot : p + threadIdx.x * 16;
+    return ANYWHERE ? p + threadIdx.x / 32 * kWarpSlot<LANES> : p + threadIdx.x * 16;
   }
   __device__ __forceinline__ uint4 piece(int slot, int arr, int c, int off) const {
-    if constexpr (ANYWHERE) return read_anywhere(at(slot, arr, c), off);
+    if constexpr (ANYWHERE) return read_anywhere<LANES>(at(slot, arr, c), off);
     else return *reinterpret_cast<const uint4*>(at(slot, arr, c));
   }
 };
 
 // CL CTAs of a cluster to a row, G threads of each, C pieces of 16 bytes to a thread, a ring of S rows.  GATE: a gate of every
-// element.  EIGHT: 8-bit outputs; 0: none, 1: any, 2: all of e4m3 and the copies for the gradient among them.  Compiled apart:
-// choices at run time leave pieces of code too small to be overlapped.
-template <typename T, int G, int C, int S, int MINB, int CL, bool GATE, int EIGHT, bool ANYWHERE>
+// element.  E4M3: all 8-bit outputs are of e4m3, and the copies for the gradient among them.  Compiled apart: choices at run
+// time leave pieces of code too small to be overlapped.
+template <typename T, int G, int C, int S, int MINB, int CL, bool GATE, bool E4M3, bool ANYWHERE>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kernel(const muon_block_norm_args a) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
   using P = Pairs<T>;
   constexpr int E = P::E, N = P::N, PIECE = G * E;  // PIECE: from a thread's piece to its next
-  using Scales = Scales4<128 / E>;
+  constexpr int LANES = G < 32 ? G : 32;  // of a row in a warp
+  using Scales = Scales4<(128 / E < G ? 128 / E : G)>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ RowSums<G, TH, 1, CL> sums;
-  const RowRing<T, TH, C, S, ANYWHERE> ring{ring_smem};
+  const RowRing<T, G, C, S, ANYWHERE> ring{ring_smem};
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
   const int col = (rank * C * G + t) * E;  // of the first piece
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
       for (int c = 0; c < C; ++c) {
         const auto get = [&](int arr, const T* row, const void* matrix) {
           if constexpr (ANYWHERE) {
-            fetch_anywhere<T>(ring.at(slot, arr, c), row, (col + c * PIECE) / E, cols, static_cast<const uint8_t*>(matrix));
+            fetch_anywhere<T, LANES>(ring.at(slot, arr, c), row, (col + c * PIECE) / E, cols, static_cast<const uint8_t*>(matrix));
           } else {
             copy16(smem_u32(ring.at(slot, arr, c)), row + (n[c] ? c * PIECE : -col), n[c] * static_cast<int>(sizeof(T)));
           }
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
   T* ph = static_cast<T*>(a.h) + row0 * a.ldh + BEGIN * col;
   T* py = static_cast<T*>(a.y) + row0 * a.ldy + BEGIN * col;
   const auto put = [&](T* p, int c, bool live, const P& v) {
-    if constexpr (ANYWHERE) store_anywhere<T, 32>(p, (col + c * PIECE) / E, live ? cols - col - c * PIECE : 0, v);
+    if constexpr (ANYWHERE) store_anywhere<T, LANES>(p, (col + c * PIECE) / E, live ? cols - col - c * PIECE : 0, v);
     else if (live) v.store(p + c * PIECE, n[c]);
   };
   // rows' addresses modulo 16
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
   // the 8-bit copies: y, h, x, gate; each lane keeps the scales of one of them
   uint8_t* p8[4] = {static_cast<uint8_t*>(a.q.data) + row0 * a.q.ld + col, static_cast<uint8_t*>(a.h8.data) + row0 * a.h8.ld + col,
                     static_cast<uint8_t*>(a.x8.data) + row0 * a.x8.ld + col, static_cast<uint8_t*>(a.gate8.data) + row0 * a.gate8.ld + col};
+  const bool eight = E4M3 || a.q.data || a.h8.data || a.x8.data || a.gate8.data;
   const int mine = Scales::mine(), top = (mine ? a.kept_fmt : a.fmt) ? 15 : 8, cols16 = (cols + 15) & ~15;
   const long long rows4 = (a.rows + 3) & ~3LL;
   uint8_t* const scales = static_cast<uint8_t*>(mine == 0 ? a.q.scale : mine == 1 ? a.h8.scale : mine == 2 ? a.x8.scale : a.gate8.scale);
@@ -242,14 +245,14 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
       for (int i = 0; i < N; ++i) y.v[i] = mul2(mul2(h[c].v[i], both(rh)), w2[c][i]);
       if (a.h) put(ph, c, live, h[c]);
       if (a.y) put(py, c, live, y);
-      if (EIGHT) {
+      if (eight) {
         P x, g;
         uint32_t m[4] = {y.largest(), h[c].largest(), 0u, 0u};
-        if (EIGHT == 2 || a.x8.data) x.unpack(ring.piece(slot, 0, c, ox)), m[2] = x.largest();
-        if (GATE && (EIGHT == 2 || a.gate8.data)) g.unpack(ring.piece(slot, 2, c, og)), m[3] = g.largest();
+        if (E4M3 || a.x8.data) x.unpack(ring.piece(slot, 0, c, ox)), m[2] = x.largest();
+        if (GATE && (E4M3 || a.gate8.data)) g.unpack(ring.piece(slot, 2, c, og)), m[3] = g.largest();
         const Scales s(m, top);
         if (live && col + c * PIECE < cols16) {
-          if constexpr (EIGHT == 2) {
+          if constexpr (E4M3) {
             if (a.q.data) y.template store8<false>(p8[0] + c * PIECE, s.inv[0]);
             h[c].template store8<false>(p8[1] + c * PIECE, s.inv[1]);
             x.template store8<false>(p8[2] + c * PIECE, s.inv[2]);
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
     slot = slot + 1 == S ? 0 : slot + 1;
   }
   // scales of no block or row, up to whole words and to four rows, are 1
-  if (!EIGHT || rank != 0) return;
+  if (!eight || rank != 0) return;
   const int blocks = (cols + 127) / 128, end = (cols + 511) / 512 * 4;
   const auto fill = [&](const muon_fp8_out& o, int kb, long long row) {
     if (o.data) static_cast<uint8_t*>(o.scale)[fp8_scale_offset(kb, row, rows4)] = 127;
@@ -282,14 +285,14 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
       for (int kb = t; kb < end; kb += G) fill(a.q, kb, row), fill(a.h8, kb, row), fill(a.x8, kb, row), fill(a.gate8, kb, row);
 }
 
-template <typename T, int G, int C, int S, int MINB, int CL, bool GATE, int EIGHT, bool ANYWHERE>
+template <typename T, int G, int C, int S, int MINB, int CL, bool GATE, bool E4M3, bool ANYWHERE>
 static cudaError_t launch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
-  constexpr int smem = RowRing<T, TH, C, S, ANYWHERE>::BYTES;
+  constexpr int smem = RowRing<T, G, C, S, ANYWHERE>::BYTES;
   static_assert(smem * MINB <= 220 * 1024, "shared memory of an SM");
   static bool done[64] = {false};
   static int known[64] = {0};
-  const auto kernel = block_norm_ring_kernel<T, G, C, S, MINB, CL, GATE, EIGHT, ANYWHERE>;
+  const auto kernel = block_norm_ring_kernel<T, G, C, S, MINB, CL, GATE, E4M3, ANYWHERE>;
   cudaError_t e = smem_limit(kernel, smem, done);
   if (e != cudaSuccess) return e;
   int most = MINB * sms;
@@ -302,33 +305,32 @@ static cudaError_t launch_ring(const muon_block_norm_args& a, int sms, cudaStrea
 }
 
 // Threads, pieces and CTAs of a row by its width.
-template <typename T, bool GATE, int EIGHT, bool ANYWHERE>
+template <typename T, bool GATE, bool E4M3, bool ANYWHERE>
 static cudaError_t dispatch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const int pieces = static_cast<int>((a.cols + E - 1) / E);
-  if (pieces <= 32) return launch_ring<T, 32, 1, 8, 4, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
-  if (pieces <= 64) return launch_ring<T, 64, 1, 6, 5, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
-  if (pieces <= 128) return launch_ring<T, 128, 1, 6, 5, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
-  if (pieces <= 256) return launch_ring<T, 256, 1, 5, 3, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
-  if (pieces <= 512) return launch_ring<T, 256, 2, 4, 2, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
-  if (pieces <= 1024) return launch_ring<T, 512, 2, 4, 1, 1, GATE, EIGHT, ANYWHERE>(a, sms, st);
-  if (pieces <= 2048) return launch_ring<T, 512, 2, 4, 1, 2, GATE, EIGHT, ANYWHERE>(a, sms, st);
-  if (pieces <= 4096) return launch_ring<T, 512, 2, 4, 1, 4, GATE, EIGHT, ANYWHERE>(a, sms, st);
-  return launch_ring<T, 512, 2, 4, 1, 8, GATE, EIGHT, ANYWHERE>(a, sms, st);
+  if (pieces <= 16) return launch_ring<T, 16, 1, 8, 4, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
+  if (pieces <= 32) return launch_ring<T, 32, 1, 8, 4, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
+  if (pieces <= 64) return launch_ring<T, 32, 2, 5, 3, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
+  if (pieces <= 128) return launch_ring<T, 64, 2, 5, 3, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
+  if (pieces <= 256) return launch_ring<T, 128, 2, 5, 3, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
+  if (pieces <= 512) return launch_ring<T, 256, 2, 3, 2, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
+  if (pieces <= 1024) return launch_ring<T, 512, 2, 3, 1, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
+  if (pieces <= 2048) return launch_ring<T, 512, 4, 2, 1, 1, GATE, false, ANYWHERE>(a, sms, st);
+  if (pieces <= 4096) return launch_ring<T, 512, 4, 2, 1, 2, GATE, false, ANYWHERE>(a, sms, st);
+  return launch_ring<T, 512, 4, 2, 1, 4, GATE, false, ANYWHERE>(a, sms, st);
 }
 
 template <typename T, bool ANYWHERE>
 cudaError_t launch_block_norm_rows(const muon_block_norm_args& a, int sms, cudaStream_t st) {
-  // 8 CTAs of 1024 pieces hold MUON_MAX_DIM 16-bit columns and half as many of fp32
-  if (a.cols > 8 * 1024 * (16 / static_cast<int>(sizeof(T))))
+  // 4 CTAs of 2048 pieces hold MUON_MAX_DIM 16-bit columns and half as many of fp32
+  if (a.cols > 4 * 2048 * (16 / static_cast<int>(sizeof(T))))
     return launch_pdl(block_norm_wide_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(512), 0, st, a);
   const bool element = a.gate && !a.gate_per_row, kept = a.x8.data && a.h8.data && (a.gate8.data || !element);
   const bool e4m3 = kept && a.kept_fmt == MUON_E4M3 && (!a.q.data || a.fmt == MUON_E4M3);
-  const bool any = a.q.data || a.x8.data || a.h8.data || a.gate8.data;
   const auto go = [&](auto gate) {
     constexpr bool GATE = decltype(gate)::value;
-    if (!any) return dispatch_ring<T, GATE, 0, ANYWHERE>(a, sms, st);
-    return e4m3 ? dispatch_ring<T, GATE, 2, ANYWHERE>(a, sms, st) : dispatch_ring<T, GATE, 1, ANYWHERE>(a, sms, st);
+    return e4m3 ? dispatch_ring<T, GATE, true, ANYWHERE>(a, sms, st) : dispatch_ring<T, GATE, false, ANYWHERE>(a, sms, st);
   };
   return element ? go(std::true_type()) : go(std::false_type());
 }

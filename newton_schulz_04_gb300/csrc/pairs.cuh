@@ -203,14 +203,16 @@ __device__ __forceinline__ void store_anywhere(T* row, int t, int left, const Pa
     if (i < left && (i < head ? !whole : tail)) row[t * E + i] = u.e[i];
 }
 
-// A ring's slot of one array and piece for rows that start anywhere: the 16 aligned bytes of each lane and the next lane's, 33
-// for a warp, from which a lane takes its own by `window`.  The warp is synchronised before it reads and before it fetches
-// into the same slot again.
-constexpr int kWarpSlot = 33 * 16;
-template <typename T>
+// A warp's slot of one array and piece in a ring, for rows that start anywhere: the 16 aligned bytes of each of a row's LANES
+// lanes and one more, from which a lane takes its own by `window`.  The warp is synchronised before it reads and before
+// it fetches into the same slot again.
+template <int LANES>
+constexpr int kWarpSlot = 32 / LANES * (LANES + 1) * 16;
+template <typename T, int LANES>
 __device__ __forceinline__ void fetch_anywhere(uint8_t* slot, const T* row, int t, int cols, const uint8_t* from) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x % 32;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x % LANES;
+  slot += threadIdx.x % 32 / LANES * (LANES + 1) * 16;
   const uint8_t* p = reinterpret_cast<const uint8_t*>(row) - off + 16LL * t;
   const long long there = static_cast<long long>(cols) * static_cast<int>(sizeof(T)) + off - 16LL * t;  // bytes to the row's end
   const auto get = [&](int at, const uint8_t* src, long long bytes) {
@@ -228,11 +230,12 @@ __device__ __forceinline__ void fetch_anywhere(uint8_t* slot, const T* row, int 
     }
   };
   get(lane, p, there);
-  if (lane == 31) get(32, p + 16, there - 16);
+  if (lane == LANES - 1) get(LANES, p + 16, there - 16);
 }
 // off: the row's address modulo 16.
+template <int LANES>
 __device__ __forceinline__ uint4 read_anywhere(const uint8_t* slot, int off) {
-  const uint4* q = reinterpret_cast<const uint4*>(slot) + threadIdx.x % 32;
+  const uint4* q = reinterpret_cast<const uint4*>(slot) + threadIdx.x % 32 / LANES * (LANES + 1) + threadIdx.x % LANES;
   return window(q[0], q[1], off);
 }
 

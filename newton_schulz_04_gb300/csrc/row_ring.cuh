@@ -134,14 +134,14 @@ inline cudaError_t smem_limit(F kernel, int bytes, bool (&done)[64]) {
 // TH / G rows).  One barrier; `sh` alternates between two buffers.
 template <int G, int TH, int N, int CL>
 struct RowSums {
-  static constexpr int WARPS = TH / 32, W = G / 32;
+  static constexpr int WARPS = TH / 32, W = G < 32 ? 1 : G / 32;
   float v[2][N][CL * WARPS];
   __device__ __forceinline__ void operator()(float (&s)[N], int turn) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
-    if (G == 32 && CL == 1) return;
+      for (int o = G < 32 ? G / 2 : 16; o > 0; o >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
+    if (G <= 32 && CL == 1) return;
     float(&b)[N][CL * WARPS] = v[turn & 1];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if constexpr (CL == 1) {
@@ -158,7 +158,7 @@ struct RowSums {
         for (int o = W / 2; o > 0; o >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
       }
     } else {
-      static_assert(CL == 1 || (G == TH && (CL * WARPS) % 32 == 0), "rows of whole CTAs");
+      static_assert(CL == 1 || (G == TH && (CL * WARPS <= 32 || CL * WARPS % 32 == 0)), "rows of whole CTAs");
       if (lane < CL) {  // a lane to a CTA of the cluster
         const uint32_t rank = cluster_ctarank();
 #pragma unroll
@@ -168,7 +168,7 @@ struct RowSums {
       cluster_sync();
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        float f = b[n][lane];
+        float f = lane < CL * WARPS ? b[n][lane] : 0.f;
 #pragma unroll
         for (int k = 32; k < CL * WARPS; k += 32) f += b[n][k + lane];
 #pragma unroll
