@@ -166,8 +166,8 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tenso
 def _block_norm(x, ldx, residual, ldr, gate, ldg, post, scale, pre, rows, codes, alpha, eps, fp8, y, checkpoint, dev, st):
     cols = x.shape[-1]
     h, out = _new(x, dev), _new(x, dev) if y else None
-    rstd = torch.empty((2, rows), dtype=torch.float32, device=dev)
-    rstd_x, rstd_h = rstd.unbind()
+    rstd = torch.empty(2 * rows, dtype=torch.float32, device=dev)
+    rstd_x, rstd_h = rstd.as_strided((rows,), (1,)), rstd.as_strided((rows,), (1,), rows)
     q = None if fp8 is None else Fp8Tensor.empty(rows, cols, fp8, dev)
     x8 = h8 = gate8 = None
     kept = BlockNormKept(x, h, gate, rstd_x, rstd_h)
@@ -239,12 +239,12 @@ def _block_norm_backward(dy, lddy, dh, lddh, kx, kh, kg, gate, rstd_x, rstd_h, p
     dpost = dpre = dscale = ws = None
     at, size = (0, 0, 0), 0
     if dweights:
-        dw = torch.empty((2 if scale is None else 3, cols), dtype=torch.float32, device=dev)
-        dpost, dpre, *rest = dw.unbind()
-        dscale = rest[0] if rest else None
+        dw = torch.empty((2 if scale is None else 3) * cols, dtype=torch.float32, device=dev)
+        dpost, dpre = dw.as_strided((cols,), (1,)), dw.as_strided((cols,), (1,), cols)
+        dscale = None if scale is None else dw.as_strided((cols,), (1,), 2 * cols)
         size = lib.muon_block_norm_backward_workspace_bytes(rows, cols)
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        at = dw.data_ptr(), dw.data_ptr() + 4 * cols, dw.data_ptr() + 8 * cols if rest else 0
+        at = dw.data_ptr(), dw.data_ptr() + 4 * cols, 0 if scale is None else dw.data_ptr() + 8 * cols
     _b._check(lib.muon_block_norm_backward(_BLOCK_NORM_GRAD(
         dy.data_ptr(), lddy, _ptr(dh), lddh, *kx[:3], *kh[:3], *kg[:3], rstd_x.data_ptr(), rstd_h.data_ptr(), post.data_ptr(),
         _ptr(scale), pre.data_ptr(), dx.data_ptr(), cols, dresidual.data_ptr(), cols, _ptr(dgate), ldgate, *at, _ptr(ws), size,

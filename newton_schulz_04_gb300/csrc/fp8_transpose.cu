@@ -15,49 +15,116 @@
 
 namespace muon {
 
-// A 128 x 128 tile to a CTA of 256 threads: 8 rows x 8 columns to a thread, 16 lanes to a row.
+// That takes some 20 instructions a value.  Where the scales of a tile's rows lie near enough to one another, 16-bit types hold
+// every value times 2^(s - largest s) exactly, and two at a time take half of them.  The other way, a function of its own that
+// costs this one no registers, is for the rest, and for tiles in which some column's largest magnitude is so small that
+// its factor leaves the 16-bit type's range.
+//
+// e4m3 goes through fp16, to and from which the hardware converts: scales within 2^14 (values are multiples of 2^-9, fp16's of
+// 2^-24).  e5m2 has fp16's exponents, which leaves no room for scales; its bits are those of a bf16 number times 2^-112, and
+// within 2^100 the products stay normal.
 template <bool E5M2>
-__global__ void __launch_bounds__(256, 3) fp8_transpose_kernel(const Fp8TransposeArgs a) {
-  __shared__ uint2 tile[128][16];  // transposed bytes: [column][8-row slot, swizzled]
-  __shared__ uint32_t cmax[128];   // of column 8 g + j at j * 16 + g
-  constexpr uint32_t bad_from = E5M2 ? 0x04040404u : 0x01010101u;  // added to magnitudes, sets bit 7 of infinities and NaN
-  pdl_launch_dependents();
-  if (threadIdx.x < 128) cmax[threadIdx.x] = 0u;
-  __syncthreads();
-  pdl_wait();
+struct Pairwise {  // e4m3
+  using V = __half2;
+  static constexpr uint32_t SPREAD = 14, LEAST = (127u - 6u) << 23;  // of scales; fp32 bits of a column's maximum
+  static __device__ __forceinline__ V bits(uint32_t w) { return *reinterpret_cast<const V*>(&w); }
+  static __device__ __forceinline__ V row_factor(uint32_t d) { return bits(((15u - d) << 10) * 0x10001u); }  // 2^-d
+  static __device__ __forceinline__ uint32_t column_factor(int k) { return (15 + max(0, min(14, k))) << 10; }  // 2^k
+  static __device__ __forceinline__ V decode(uint32_t two, V f) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(two)));
+    return __hmul2(bits(h), f);
+  }
+  static __device__ __forceinline__ uint32_t encode(V v, V f) {
+    const V p = __hmul2(v, f);
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&p)));
+    return r;
+  }
+  static __device__ __forceinline__ float2 wide(V v) { return __half22float2(v); }
+  static __device__ __forceinline__ bool bad(const uint2&) { return false; }  // a NaN's product is one
+};
+template <>
+struct Pairwise<true> {  // e5m2
+  using V = __nv_bfloat162;
+  static constexpr uint32_t SPREAD = 100, LEAST = (127u - 60u) << 23;
+  static __device__ __forceinline__ V bits(uint32_t w) { return *reinterpret_cast<const V*>(&w); }
+  static __device__ __forceinline__ V row_factor(uint32_t d) { return bits(((127u + 112u - d) << 7) * 0x10001u); }  // 2^(112 - d)
+  static __device__ __forceinline__ uint32_t column_factor(int k) { return (127 + max(0, min(100, k))) << 7; }
+  static __device__ __forceinline__ V decode(uint32_t two, V f) {
+    const uint32_t t = __byte_perm(two, 0u, 0x1404);
+    return __hmul2(bits((t & 0x80008000u) | ((t >> 3) & 0x0fe00fe0u)), f);
+  }
+  static __device__ __forceinline__ uint32_t encode(V v, V f) {
+    const V p = __hmul2(v, f);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&p);
+    unsigned short r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(__uint_as_float(w & 0xffff0000u)), "f"(__uint_as_float(w << 16)));
+    return r;
+  }
+  static __device__ __forceinline__ float2 wide(V v) { return __bfloat1622float2(v); }
+  static __device__ __forceinline__ bool bad(const uint2& q) {  // infinities and NaN have no such bits
+    return (((q.x & 0x7f7f7f7fu) + 0x04040404u) | ((q.y & 0x7f7f7f7fu) + 0x04040404u)) & 0x80808080u;
+  }
+};
+
+// A 128 x 128 tile to a CTA of 256 threads: 8 rows x 8 columns to a thread, 16 lanes to a row.
+struct TransposeTile {
+  uint2 slot[128][16];     // transposed bytes: [column][8-row slot, swizzled]
+  uint32_t column[128];    // of column 8 g + j at j * 16 + g: its maximum, then its scale byte
+  uint32_t most, least;    // of the rows' scale bytes
+};
+struct TransposePart {
+  long long c0, r0, rows4;
+  int nc, nr;              // columns and rows of the thread's that exist
+  __device__ __forceinline__ TransposePart(const Fp8TransposeArgs& a)
+      : c0(blockIdx.x * 128LL + (threadIdx.x & 15) * 8),
+        r0(blockIdx.y * 128LL + (threadIdx.x >> 4) * 8),
+        rows4((a.rows + 3) & ~3LL),
+        nc(static_cast<int>(max(0LL, min(8LL, a.cols - c0)))),
+        nr(static_cast<int>(max(0LL, min(8LL, a.rows - r0)))) {}
+  __device__ __forceinline__ void load(const Fp8TransposeArgs& a, uint2 (&q)[8], uint32_t (&s)[8]) const {
+    const uint8_t* p = a.q + (nc && nr ? r0 * a.ldq + c0 : 0);
+    const uint8_t* ps = a.qs + (nr ? fp8_scale_offset(blockIdx.x, r0, rows4) : 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      q[i] = make_uint2(0u, 0u);
+      s[i] = i < nr ? ps[4 * i] : 0u;
+      if (i < nr && nc == 8) {
+        q[i] = *reinterpret_cast<const uint2*>(p);
+      } else if (i < nr) {
+        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < nc) w[j >> 2] |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
+        q[i] = make_uint2(w[0], w[1]);
+      }
+      p += a.ldq;
+    }
+  }
+};
+
+// Any scales: fills the tile and the columns' scale bytes (the columns are 0 on entry).
+template <bool E5M2>
+__device__ __noinline__ void transpose_any(const Fp8TransposeArgs& a, TransposeTile& tile) {
+  constexpr int TOP = E5M2 ? 15 : 8;
+  constexpr uint32_t BAD = E5M2 ? 0x04040404u : 0x01010101u;  // added to magnitudes, sets bit 7 of infinities and NaN
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-  const long long kbc = blockIdx.x, kbr = blockIdx.y, c0 = kbc * 128 + cg * 8, r0 = kbr * 128 + rg * 8;
-  const long long rows4 = (a.rows + 3) & ~3LL, cols4 = (a.cols + 3) & ~3LL, kend = (a.rows + 511) / 512 * 4;
-  const int nc = static_cast<int>(max(0LL, min(8LL, a.cols - c0)));
+  const TransposePart part(a);
   uint2 q[8];
   uint32_t s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const long long row = r0 + i;
-    const int n = row < a.rows ? nc : 0;
-    const uint8_t* p = a.q + (n ? row * a.ldq + c0 : 0);
-    if (n == 8) {
-      q[i] = *reinterpret_cast<const uint2*>(p);
-    } else {
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) w[j >> 2] |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
-      q[i] = make_uint2(w[0], w[1]);
-    }
-    s[i] = n ? a.qs[fp8_scale_offset(kbc, row, rows4)] : 0u;
-  }
+  part.load(a, q, s);
   uint32_t bad = 0u;  // bit j: column j holds an infinity or NaN
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t x = ((q[i].x & 0x7f7f7f7fu) + bad_from) & 0x80808080u, y = ((q[i].y & 0x7f7f7f7fu) + bad_from) & 0x80808080u;
+    const uint32_t x = ((q[i].x & 0x7f7f7f7fu) + BAD) & 0x80808080u, y = ((q[i].y & 0x7f7f7f7fu) + BAD) & 0x80808080u;
     if ((x | y) || s[i] == 255u) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < nc && (s[i] == 255u || ((j < 4 ? x : y) >> (8 * (j & 3)) & 0x80u))) bad |= 1u << j;
+        if (j < part.nc && (s[i] == 255u || ((j < 4 ? x : y) >> (8 * (j & 3)) & 0x80u))) bad |= 1u << j;
     }
   }
-  // Two columns at a time: the signed keys of their 8 rows, 0 for 0.
+  // the signed keys of two columns of a row, 0 for 0
   const auto keys = [&](int j, int i, int (&k)[2]) {
     const uint32_t two = (j < 4 ? q[i].x : q[i].y) >> (8 * (j & 2));
     const float2 f = fp8_unpack2<E5M2>(two);
@@ -77,24 +144,17 @@ __global__ void __launch_bounds__(256, 3) fp8_transpose_kernel(const Fp8Transpos
     }
     if (bad >> j & 1) m0 = 0xffffffffu;
     if (bad >> j & 2) m1 = 0xffffffffu;
-    // the two half-warps hold other rows of the same columns: each takes one of the two on
-    const bool up = threadIdx.x & 16;
+    const bool up = threadIdx.x & 16;  // the half-warps hold other rows of the same columns: each takes one of two on
     const uint32_t m = max(up ? m1 : m0, __shfl_xor_sync(0xffffffffu, up ? m0 : m1, 16));
-    atomicMax(&cmax[(j + up) * 16 + cg], m);
+    atomicMax(&tile.column[(j + up) * 16 + cg], m);
   }
   __syncthreads();
-  if (threadIdx.x < 128) {  // a scale byte for each column
-    const uint32_t m = cmax[threadIdx.x];
+  if (threadIdx.x < 128) {
+    const uint32_t m = tile.column[threadIdx.x];
     uint32_t byte = 127u;
     if (m == 0xffffffffu) byte = 255u;
-    else if (m) byte = static_cast<uint32_t>(max(static_cast<int>((m + 0x1fffffu) >> 23) - 127 - (E5M2 ? 15 : 8), 0));
-    cmax[threadIdx.x] = byte;
-    const long long c = kbc * 128 + threadIdx.x % 16 * 8 + threadIdx.x / 16;
-    if (c < cols4) {
-      a.qts[fp8_scale_offset(kbr, c, cols4)] = static_cast<uint8_t>(byte);
-      if ((kbr + 1) * 128 >= a.rows)
-        for (long long kb = kbr + 1; kb < kend; ++kb) a.qts[fp8_scale_offset(kb, c, cols4)] = 127;
-    }
+    else if (m) byte = static_cast<uint32_t>(max(static_cast<int>((m + 0x1fffffu) >> 23) - 127 - TOP, 0));
+    tile.column[threadIdx.x] = byte;
   }
   __syncthreads();
   // computed again: 128 keys do not fit into registers, and the compiler would keep them
@@ -102,34 +162,141 @@ __global__ void __launch_bounds__(256, 3) fp8_transpose_kernel(const Fp8Transpos
   for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(q[i].x), "+r"(q[i].y), "+r"(s[i]));
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    const uint32_t b0 = cmax[j * 16 + cg], b1 = cmax[(j + 1) * 16 + cg];
+    const uint32_t b0 = tile.column[j * 16 + cg], b1 = tile.column[(j + 1) * 16 + cg];
     uint32_t out[2][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int k = 0; k < 2; ++k) {
       float v[2][4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 4 * h + r;
-        int k[2];
-        keys(j, i, k);
+        const int i = 4 * k + r;
+        int key[2];
+        keys(j, i, key);
         // exponents below fp32's end as 0 or subnormal, far below the 8-bit type's smallest value
         const uint32_t raw = j < 4 ? q[i].x : q[i].y;
-        v[0][r] = __uint_as_float(static_cast<uint32_t>(max(k[0] - static_cast<int>(b0 << 23), 0)) | (raw << (24 - 8 * (j & 3)) & 0x80000000u));
-        v[1][r] = __uint_as_float(static_cast<uint32_t>(max(k[1] - static_cast<int>(b1 << 23), 0)) | (raw << (16 - 8 * (j & 3)) & 0x80000000u));
+        v[0][r] = __uint_as_float(static_cast<uint32_t>(max(key[0] - static_cast<int>(b0 << 23), 0)) | (raw << (24 - 8 * (j & 3)) & 0x80000000u));
+        v[1][r] = __uint_as_float(static_cast<uint32_t>(max(key[1] - static_cast<int>(b1 << 23), 0)) | (raw << (16 - 8 * (j & 3)) & 0x80000000u));
       }
-      out[0][h] = b0 == 255u ? 0x7f7f7f7fu : fp8_pack4<E5M2>(v[0][0], v[0][1], v[0][2], v[0][3]);
-      out[1][h] = b1 == 255u ? 0x7f7f7f7fu : fp8_pack4<E5M2>(v[1][0], v[1][1], v[1][2], v[1][3]);
+      out[0][k] = b0 == 255u ? 0x7f7f7f7fu : fp8_pack4<E5M2>(v[0][0], v[0][1], v[0][2], v[0][3]);
+      out[1][k] = b1 == 255u ? 0x7f7f7f7fu : fp8_pack4<E5M2>(v[1][0], v[1][1], v[1][2], v[1][3]);
     }
-    tile[cg * 8 + j][rg ^ cg] = make_uint2(out[0][0], out[0][1]);
-    tile[cg * 8 + j + 1][rg ^ cg] = make_uint2(out[1][0], out[1][1]);
+    tile.slot[cg * 8 + j][rg ^ cg] = make_uint2(out[0][0], out[0][1]);
+    tile.slot[cg * 8 + j + 1][rg ^ cg] = make_uint2(out[1][0], out[1][1]);
+  }
+}
+
+template <bool E5M2>
+__global__ void __launch_bounds__(256, 4) fp8_transpose_kernel(const __grid_constant__ Fp8TransposeArgs a) {
+  using Way = Pairwise<E5M2>;
+  using V = typename Way::V;
+  constexpr int TOP = E5M2 ? 15 : 8;
+  __shared__ TransposeTile tile;
+  __shared__ uint32_t factor[64];  // of column pair 4 g + k at k * 16 + g: 2^(largest s - s')
+  pdl_launch_dependents();
+  if (threadIdx.x < 128) tile.column[threadIdx.x] = 0u;
+  if (threadIdx.x == 128) tile.most = 0u, tile.least = 255u;
+  __syncthreads();
+  pdl_wait();
+  const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  V h[8][4];
+  bool fast;
+  uint32_t base;
+  {
+    const TransposePart part(a);
+    uint2 q[8];
+    uint32_t s[8];
+    part.load(a, q, s);
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bad |= Way::bad(q[i]);
+    if (bad) atomicMax(&tile.most, 255u);
+    if (cg == 0) {  // the same in the row's 16 lanes
+      uint32_t hi = 0u, lo = 255u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < part.nr) hi = max(hi, s[i]), lo = min(lo, s[i]);
+      atomicMax(&tile.most, hi);
+      atomicMin(&tile.least, lo);
+    }
+    __syncthreads();
+    base = tile.most;
+    fast = base - tile.least <= Way::SPREAD && base != 255u;
+    if (fast) {
+      V m[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = Way::bits(0u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const V f = Way::row_factor(i < part.nr ? base - s[i] : 0u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          h[i][k] = Way::decode((k < 2 ? q[i].x : q[i].y) >> (16 * (k & 1)), f);
+          m[k] = __hmax2_nan(m[k], __habs2(h[i][k]));
+        }
+      }
+      const bool up = threadIdx.x & 16;  // the half-warps hold other rows of the same columns: each takes two words of four on
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const V keep = up ? m[k + 2] : m[k], give = up ? m[k] : m[k + 2];
+        const float2 v = Way::wide(__hmax2_nan(keep, __shfl_xor_sync(0xffffffffu, give, 16)));
+        const int j = 2 * k + (up ? 4 : 0);
+        atomicMax(&tile.column[j * 16 + cg], abs_bits(v.x));
+        atomicMax(&tile.column[(j + 1) * 16 + cg], abs_bits(v.y));
+      }
+    }
+  }
+  if (fast) {
+    __syncthreads();
+    const uint32_t mine = threadIdx.x < 128 ? tile.column[threadIdx.x] : 0u;
+    fast = !__syncthreads_or(mine != 0u && mine < Way::LEAST);
+    if (threadIdx.x < 128) {
+      uint32_t byte = 127u;
+      if (mine >= 0x7f800000u) byte = 255u;
+      else if (mine) byte = static_cast<uint32_t>(max(static_cast<int>((mine + 0x1fffffu) >> 23) - TOP + static_cast<int>(base) - 127, 0));
+      tile.column[threadIdx.x] = fast ? byte : 0u;
+      const int j = threadIdx.x / 16, g = threadIdx.x % 16;  // the factor of a column of zeros or NaN: any
+      reinterpret_cast<unsigned short*>(factor)[((j / 2) * 16 + g) * 2 + (j & 1)] =
+          static_cast<unsigned short>(Way::column_factor(static_cast<int>(base) - static_cast<int>(byte)));
+    }
+    __syncthreads();
+  }
+  if (fast) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const uint32_t b0 = tile.column[j * 16 + cg], b1 = tile.column[(j + 1) * 16 + cg];
+      const V f = Way::bits(factor[j / 2 * 16 + cg]);
+      uint32_t out[2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r] = Way::encode(h[4 * k + r][j / 2], f);
+        const uint32_t lo = __byte_perm(w[0], w[1], 0x5140), hi = __byte_perm(w[2], w[3], 0x5140);
+        out[0][k] = b0 == 255u ? 0x7f7f7f7fu : __byte_perm(lo, hi, 0x5410);
+        out[1][k] = b1 == 255u ? 0x7f7f7f7fu : __byte_perm(lo, hi, 0x7632);
+      }
+      tile.slot[cg * 8 + j][rg ^ cg] = make_uint2(out[0][0], out[0][1]);
+      tile.slot[cg * 8 + j + 1][rg ^ cg] = make_uint2(out[1][0], out[1][1]);
+    }
+  } else {
+    transpose_any<E5M2>(a, tile);
+  }
+  const long long cols4 = (a.cols + 3) & ~3LL, kend = (a.rows + 511) / 512 * 4, kbr = blockIdx.y;
+  if (threadIdx.x < 128) {
+    const long long c = blockIdx.x * 128LL + threadIdx.x % 16 * 8 + threadIdx.x / 16;
+    if (c < cols4) {
+      a.qts[fp8_scale_offset(kbr, c, cols4)] = static_cast<uint8_t>(tile.column[threadIdx.x]);
+      if ((kbr + 1) * 128 >= a.rows)
+        for (long long kb = kbr + 1; kb < kend; ++kb) a.qts[fp8_scale_offset(kb, c, cols4)] = 127;
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int it = 0; it < 4; ++it) {  // 16 bytes per thread, 8 threads to a column
     const int cl = it * 32 + (threadIdx.x >> 3), slot = (threadIdx.x & 7) * 2;
-    const long long c = kbc * 128 + cl, r = kbr * 128 + slot * 8;
+    const long long c = blockIdx.x * 128LL + cl, r = kbr * 128 + slot * 8;
     if (c < a.cols && r < a.rows) {
-      const uint2 lo = tile[cl][slot ^ (cl >> 3)], hi = tile[cl][(slot + 1) ^ (cl >> 3)];
+      const uint2 lo = tile.slot[cl][slot ^ (cl >> 3)], hi = tile.slot[cl][(slot + 1) ^ (cl >> 3)];
       *reinterpret_cast<uint4*>(a.qt + c * a.ldqt + r) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
   }

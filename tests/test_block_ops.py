@@ -729,6 +729,23 @@ def test_transpose_is_exact(mm, fmt, shape):
 
 @gpu
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("spread", [0, 8, 13, 14, 15, 99, 100, 101])
+@pytest.mark.parametrize("low", [1.0, 2.0 ** -14, 2.0 ** -16, 2.0 ** -73, 2.0 ** -78])
+def test_transpose_at_the_limits_of_16_bits(mm, fmt, spread, low):
+    """Rows whose scales are as far apart as the two-at-a-time way takes, and a little more; columns that are small
+    everywhere; the type's smallest values."""
+    rows = torch.linspace(0, spread, 200).round()
+    x = gen(98, 200, 256) * 2.0 ** -rows[:, None]
+    x[:, 1::3] *= low
+    x[7, 9], x[:, 200] = 0.0, -0.0
+    q, _ = mm.fp8_quantize(x.cuda(), fmt)
+    t = mm.fp8_transpose(q)
+    data, scale = transposed_exactly(q)
+    assert torch.equal(t.data.float().cpu().double(), data) and torch.equal(t.scale.view(torch.uint8).cpu(), scale)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_transpose_over_the_whole_range(mm, fmt):
     """Every byte under every scale, far apart within a column."""
     dt = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
