@@ -822,3 +822,98 @@ def test_calls_on_another_stream_and_in_a_graph(mm):
     torch.cuda.synchronize()
     for a, b in zip(out, step()):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- together, as a training step runs them
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "fp8_checkpoint_step.py")
+    spec = importlib.util.spec_from_file_location("fp8_checkpoint_step", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@gpu
+def test_example_gradients_match_autograd(mm):
+    """The example's forward and backward pass from 8-bit checkpoints against fp32 autograd of the same model."""
+    ex = _example()
+    model = ex.Network(2, 256, 384, seed=3)
+    for i, v in enumerate(model.vectors):
+        v += 0.2 * gen(200 + i, 256).cuda()
+    x, dy = gen(1, 300, 256).bfloat16().cuda(), gen(2, 300, 256).bfloat16().cuda()
+    y, saved = model.forward(x)
+    matrices, vectors = model.backward(dy, saved)
+    ws = [w.master.float().requires_grad_() for w in model.weights]
+    vs = [v.clone().requires_grad_() for v in model.vectors]
+    norm = lambda t, w: t * torch.rsqrt(t.square().mean(1, keepdim=True) + 1e-6) * w  # noqa: E731
+    s, n = x.float(), norm(x.float(), vs[0])
+    for i in range(2):
+        branch, up, down, gate = ws[4 * i:4 * i + 4]
+        post, pre, scale = vs[1 + 3 * i:4 + 3 * i]
+        o = (torch.nn.functional.silu(n @ branch.t()) * (n @ up.t())) @ down.t()
+        s = s + torch.sigmoid(n @ gate.t()) * scale * norm(o, post)
+        n = norm(s, pre)
+    (n * dy.float()).sum().backward()
+    # an 8-bit matrix is off by 2^-4 (e4m3) or 2^-3 (e5m2) of its values at most, a third of that in the mean square; a
+    # gradient of the first block has passed at most 17 of them (in each block three checkpoints of the norms, two of
+    # the branches, two operands of gradients and two weights, less one weight)
+    far = lambda a, b: float((a.float() - b.detach()).norm() / b.detach().norm())  # noqa: E731
+    limit = 17 ** 0.5 * 2.0 ** -3 / 3 ** 0.5
+    assert far(y, n) < limit
+    for got, want in zip(matrices + vectors, ws + vs):
+        assert got.shape == want.shape and far(got, want.grad) < limit
+    # 5 matrices of `width` columns' size in 8 bits and 2 of `hidden`: at most 8 / 7 of their bytes with scales and factors
+    assert ex.kept_bytes(saved) < 2 * 300 * (4 * 256 + 2 * 384) * 8 / 7
+
+
+@gpu
+def test_example_runs(mm):
+    losses, norms = _example().train(steps=4, tokens=1024, log=lambda *_: None)
+    assert all(math.isfinite(v) for v in losses + norms) and min(norms) > 0
+
+
+@gpu
+def test_backward_captured_while_an_eager_graph_of_the_same_leaves_lives(mm):
+    """The calls take no part in autograd: they are captured into a graph beside one that autograd holds."""
+    x = gen(1, 64, 256).cuda().requires_grad_()
+    loss = (x * x).sum()
+    w = torch.ones(256, device="cuda")
+    o = mm.block_norm(x.detach(), x.detach(), w, w)
+    d = mm.block_norm_backward(x.detach(), o.kept, w, w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2 = mm.block_norm(x, x, w, w)
+        d2 = mm.block_norm_backward(x, o2.kept, w, w)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not o2.y.requires_grad and torch.equal(d.dx, d2.dx)
+    loss.backward()
+    assert torch.equal(x.grad, 2 * x.detach())
+
+
+@gpu
+def test_offsets_past_32_bits(mm):
+    """Matrices of more than 2^31 elements and bytes: their last rows equal those of the same rows alone."""
+    rows, cols = 66_003, 33_000
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    raw = lambda t: t.contiguous().view(torch.uint8)  # noqa: E731
+    end = x[-7:].contiguous()
+    a, b = mm.gated_activation(x, x, fp8="e4m3", checkpoint="e4m3"), mm.gated_activation(end, end, fp8="e4m3", checkpoint="e4m3")
+    assert torch.equal(a.y[-7:], b.y) and torch.equal(raw(a.q.data[-7:]), raw(b.q.data)) and torch.equal(a.q.scales()[-7:], b.q.scales())
+    assert torch.equal(raw(a.kept.up.data[-7:]), raw(b.kept.up.data))
+    d = mm.gated_activation_backward(x, a.kept, fp8="e5m2", dense=False)
+    e = mm.gated_activation_backward(end, b.kept, fp8="e5m2", dense=False)
+    assert torch.equal(raw(d.dup_rows.data[-7:]), raw(e.dup_rows.data)) and torch.equal(d.dgate_rows.scales()[-7:], e.dgate_rows.scales())
+    del d, e
+    t = mm.fp8_transpose(a.q)
+    last = a.q.dequantize()[-83:, -3:]          # the last block of rows: 66003 = 515 * 128 + 83
+    assert torch.allclose(t.dequantize()[-3:, -83:].t(), last, rtol=2.0 ** -4, atol=float(last.abs().max()) * 2.0 ** -18)
+    del t, a, b
+    w = torch.ones(cols, device="cuda")
+    m, n = mm.block_norm(x, x, w, w, gate=x, checkpoint="e4m3"), mm.block_norm(end, end, w, w, gate=end, checkpoint="e4m3")
+    assert torch.equal(m.y[-7:], n.y) and torch.equal(m.h[-7:], n.h) and torch.equal(raw(m.kept.gate.data[-7:]), raw(n.kept.gate.data))
+    g, h = mm.block_norm_backward(x, m.kept, w, w, dh=x, dweights=False), mm.block_norm_backward(end, n.kept, w, w, dh=end, dweights=False)
+    assert torch.equal(g.dx[-7:], h.dx) and torch.equal(g.dgate[-7:], h.dgate) and torch.equal(g.dresidual[-7:], h.dresidual)
