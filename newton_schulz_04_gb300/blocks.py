@@ -95,6 +95,10 @@ def _tensors(*kept):
     return out
 
 
+def _vector(n, device):  # one allocation each: views of a new one cost the host twice as much
+    return torch.empty(n, dtype=torch.float32, device=device)
+
+
 def _new(like, device):
     return torch.empty(like.shape, dtype=like.dtype, device=device)
 
@@ -166,8 +170,7 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tenso
 def _block_norm(x, ldx, residual, ldr, gate, ldg, post, scale, pre, rows, codes, alpha, eps, fp8, y, checkpoint, dev, st):
     cols = x.shape[-1]
     h, out = _new(x, dev), _new(x, dev) if y else None
-    rstd = torch.empty(2 * rows, dtype=torch.float32, device=dev)
-    rstd_x, rstd_h = rstd.as_strided((rows,), (1,)), rstd.as_strided((rows,), (1,), rows)
+    rstd_x, rstd_h = _vector(rows, dev), _vector(rows, dev)
     q = None if fp8 is None else Fp8Tensor.empty(rows, cols, fp8, dev)
     x8 = h8 = gate8 = None
     kept = BlockNormKept(x, h, gate, rstd_x, rstd_h)
@@ -176,10 +179,9 @@ def _block_norm(x, ldx, residual, ldr, gate, ldg, post, scale, pre, rows, codes,
         if gate is not None and not codes[2]:
             gate8 = Fp8Tensor.empty(rows, cols, checkpoint, dev)
         kept = BlockNormKept(x8, h8, gate if gate8 is None else gate8, rstd_x, rstd_h)
-    at = rstd.data_ptr()
     _b._check(_b.load().muon_block_norm(_BLOCK_NORM(
         x.data_ptr(), ldx, residual.data_ptr(), ldr, _ptr(gate), ldg, post.data_ptr(), _ptr(scale), pre.data_ptr(),
-        _ptr(out), cols, h.data_ptr(), cols, at, at + 4 * rows, *_out8(q), *_out8(x8), *_out8(h8), *_out8(gate8), rows, cols,
+        _ptr(out), cols, h.data_ptr(), cols, rstd_x.data_ptr(), rstd_h.data_ptr(), *_out8(q), *_out8(x8), *_out8(h8), *_out8(gate8), rows, cols,
         *codes, alpha, eps), st))
     return BlockNormOutput(out, h, q, kept)
 
@@ -237,17 +239,14 @@ def _block_norm_backward(dy, lddy, dh, lddh, kx, kh, kg, gate, rstd_x, rstd_h, p
         dgate = torch.empty((*dy.shape[:-1], 1) if codes[2] else dy.shape, dtype=dy.dtype, device=dev)
         ldgate = 1 if codes[2] else cols
     dpost = dpre = dscale = ws = None
-    at, size = (0, 0, 0), 0
+    size = 0
     if dweights:
-        dw = torch.empty((2 if scale is None else 3) * cols, dtype=torch.float32, device=dev)
-        dpost, dpre = dw.as_strided((cols,), (1,)), dw.as_strided((cols,), (1,), cols)
-        dscale = None if scale is None else dw.as_strided((cols,), (1,), 2 * cols)
+        dpost, dpre, dscale = _vector(cols, dev), _vector(cols, dev), None if scale is None else _vector(cols, dev)
         size = lib.muon_block_norm_backward_workspace_bytes(rows, cols)
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        at = dw.data_ptr(), dw.data_ptr() + 4 * cols, 0 if scale is None else dw.data_ptr() + 8 * cols
     _b._check(lib.muon_block_norm_backward(_BLOCK_NORM_GRAD(
         dy.data_ptr(), lddy, _ptr(dh), lddh, *kx[:3], *kh[:3], *kg[:3], rstd_x.data_ptr(), rstd_h.data_ptr(), post.data_ptr(),
-        _ptr(scale), pre.data_ptr(), dx.data_ptr(), cols, dresidual.data_ptr(), cols, _ptr(dgate), ldgate, *at, _ptr(ws), size,
+        _ptr(scale), pre.data_ptr(), dx.data_ptr(), cols, dresidual.data_ptr(), cols, _ptr(dgate), ldgate, _ptr(dpost), _ptr(dpre), _ptr(dscale), _ptr(ws), size,
         rows, cols, *codes, alpha), st))
     return BlockNormGrads(dx, dresidual, dgate, dpost, dpre, dscale)
 
