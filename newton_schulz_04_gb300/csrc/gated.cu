@@ -237,16 +237,20 @@ __device__ __forceinline__ void store_four_anywhere(T* row, int lane, long long 
     u.w[0] = pack2(v[0], T()), u.w[1] = pack2(v[1], T());
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 7), head = 4 - off / 2, bits = 64 - 8 * off;
     const uint32_t b0 = __shfl_up_sync(0xffffffffu, u.w[0], 1), b1 = __shfl_up_sync(0xffffffffu, u.w[1], 1);
-    const bool whole = left >= head && (lane > 0 || off == 0), tail = lane == 31 || left - 4 < head;
+    const bool whole = left >= head && (lane > 0 || off == 0);
     if (whole) {
       const unsigned long long before = b0 | static_cast<unsigned long long>(b1) << 32;
       const unsigned long long own = u.w[0] | static_cast<unsigned long long>(u.w[1]) << 32;
       *reinterpret_cast<unsigned long long*>(reinterpret_cast<uint8_t*>(row) - off + 8LL * lane) =
           off ? before >> bits | own << (64 - bits) : own;
     }
+    const uint32_t first = (1u << head) - 1u, there = (1u << max(0LL, min(4LL, left))) - 1u;
+    const uint32_t rest = there & ((whole ? 0u : first) | (lane == 31 || left - 4 < head ? ~first : 0u));
+    if (rest) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left && (i < head ? !whole : tail)) row[lane * 4 + i] = u.e[i];
+      for (int i = 0; i < 4; ++i)
+        if (rest >> i & 1u) row[lane * 4 + i] = u.e[i];
+    }
   }
 }
 

@@ -196,11 +196,15 @@ __device__ __forceinline__ void store_anywhere(T* row, int t, int left, const Pa
   uint8_t* p = reinterpret_cast<uint8_t*>(row) - off + 16LL * t;
   const bool whole = left >= head && (lane > 0 || off == 0);
   if (whole) *reinterpret_cast<uint4*>(p) = off ? window(before, u.w, 16 - off) : u.w;
-  // the rest: before the first lane's next 16 bytes, behind the last one's, and a row's end
-  const bool tail = lane == LANES - 1 || left - E < head;
+  // the rest, a bit for each element: before the first lane's next 16 bytes, behind the last one's, and a row's end
+  const uint32_t first = (1u << head) - 1u, there = (1u << max(0, min(E, left))) - 1u;
+  const uint32_t rest = there & ((whole ? 0u : first) | (lane == LANES - 1 || left - E < head ? ~first : 0u));
+  if (rest) {
+    row += t * E;
 #pragma unroll
-  for (int i = 0; i < E; ++i)
-    if (i < left && (i < head ? !whole : tail)) row[t * E + i] = u.e[i];
+    for (int i = 0; i < E; ++i)
+      if (rest >> i & 1u) row[i] = u.e[i];
+  }
 }
 
 // A warp's slot of one array and piece in a ring, for rows that start anywhere: the 16 aligned bytes of each of a row's LANES
@@ -212,25 +216,24 @@ template <typename T, int LANES>
 __device__ __forceinline__ void fetch_anywhere(uint8_t* slot, const T* row, int t, int cols, const uint8_t* from) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x % LANES;
-  slot += threadIdx.x % 32 / LANES * (LANES + 1) * 16;
+  slot += (threadIdx.x % 32 / LANES * (LANES + 1) + lane) * 16;
   const uint8_t* p = reinterpret_cast<const uint8_t*>(row) - off + 16LL * t;
-  const long long there = static_cast<long long>(cols) * static_cast<int>(sizeof(T)) + off - 16LL * t;  // bytes to the row's end
-  const auto get = [&](int at, const uint8_t* src, long long bytes) {
-    const int n = static_cast<int>(max(0LL, min(16LL, bytes)));
-    if (src < from) {  // the matrix begins within these 16 bytes
+  const int there = cols * static_cast<int>(sizeof(T)) + off - 16 * t;  // bytes to the row's end
+  if (p < from && there > 0) {  // the matrix begins within these 16 bytes
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const uint8_t* q = src + i * sizeof(T);
-        reinterpret_cast<T*>(slot + at * 16)[i] = q >= from && i * static_cast<int>(sizeof(T)) < n ? *reinterpret_cast<const T*>(q) : from_f32<T>(0.f);
-      }
-    } else if (n == 0) {
-      *reinterpret_cast<uint4*>(slot + at * 16) = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-      copy16(smem_u32(slot + at * 16), src, n);
+    for (int i = 0; i < E; ++i) {
+      const int at = i * static_cast<int>(sizeof(T));
+      reinterpret_cast<T*>(slot)[i] = at >= off && at < there ? *reinterpret_cast<const T*>(p + at) : from_f32<T>(0.f);
     }
-  };
-  get(lane, p, there);
-  if (lane == LANES - 1) get(LANES, p + 16, there - 16);
+  } else if (there > 0) {
+    copy16(smem_u32(slot), p, min(16, there));
+  } else {
+    *reinterpret_cast<uint4*>(slot) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (lane == LANES - 1) {
+    if (there > 16) copy16(smem_u32(slot + 16), p + 16, min(16, there - 16));
+    else *reinterpret_cast<uint4*>(slot + 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
 }
 // off: the row's address modulo 16.
 template <int LANES>
