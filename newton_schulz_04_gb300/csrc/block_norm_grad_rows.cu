@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   const auto read = [&](int slot, int arr, const void* matrix, long long ld, long long row, P& p) {
     if constexpr (ANYWHERE) {
       const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(matrix)) + static_cast<uint32_t>(row * ld) * sizeof(T);
-      p.unpack(read_anywhere<Slots::LANES>(ring.at(slot, arr), static_cast<int>(at & 15u)));
+      p.unpack(read_anywhere<Slots::LANES, false>(ring.at(slot, arr), static_cast<int>(at & 15u)));
     } else {
       p.unpack(*reinterpret_cast<const uint4*>(ring.at(slot, arr)));
     }

@@ -97,7 +97,7 @@ struct RowRing {
     return ANYWHERE ? p + threadIdx.x / 32 * kWarpSlot<LANES> : p + threadIdx.x * 16;
   }
   __device__ __forceinline__ uint4 piece(int slot, int arr, int c, int off) const {
-    if constexpr (ANYWHERE) return read_anywhere<LANES>(at(slot, arr, c), off);
+    if constexpr (ANYWHERE) return read_anywhere<LANES, C <= 2>(at(slot, arr, c), off);
     else return *reinterpret_cast<const uint4*>(at(slot, arr, c));
   }
 };
@@ -203,12 +203,15 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
     const int ox = ANYWHERE ? off(a.x, a.ldx, row) : 0, orr = ANYWHERE ? off(a.residual, a.ldr, row) : 0;
     const int og = ANYWHERE && GATE ? off(a.gate, a.ldg, row) : 0;
     P h[C];
+    constexpr bool KEEP = ANYWHERE && C <= 2;  // what takes shifts to read, where there are registers for it
+    uint4 kx[C], kg[C];
     float2 two = both(0.f);
     float sum[1];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       P x;
-      x.unpack(ring.piece(slot, 0, c, ox));
+      kx[c] = ring.piece(slot, 0, c, ox);
+      x.unpack(kx[c]);
 #pragma unroll
       for (int i = 0; i < N; ++i) two = fma2(x.v[i], x.v[i], two);
     }
@@ -219,9 +222,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       P x, g;
-      x.unpack(ring.piece(slot, 0, c, ox));
+      x.unpack(KEEP ? kx[c] : ring.piece(slot, 0, c, ox));
       h[c].unpack(ring.piece(slot, 1, c, orr));
-      if (GATE) g.unpack(ring.piece(slot, 2, c, og));
+      if (GATE) kg[c] = ring.piece(slot, 2, c, og), g.unpack(kg[c]);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (GATE) sig = sigmoid2<T>(g.v[i]);
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
       if (eight) {
         P x, g;
         uint32_t m[4] = {y.largest(), h[c].largest(), 0u, 0u};
-        if (E4M3 || a.x8.data) x.unpack(ring.piece(slot, 0, c, ox)), m[2] = x.largest();
-        if (GATE && (E4M3 || a.gate8.data)) g.unpack(ring.piece(slot, 2, c, og)), m[3] = g.largest();
+        if (E4M3 || a.x8.data) x.unpack(KEEP ? kx[c] : ring.piece(slot, 0, c, ox)), m[2] = x.largest();
+        if (GATE && (E4M3 || a.gate8.data)) g.unpack(KEEP ? kg[c] : ring.piece(slot, 2, c, og)), m[3] = g.largest();
         const Scales s(m, top);
         if (live && col + c * PIECE < cols16) {
           if constexpr (E4M3) {

@@ -95,14 +95,15 @@ __global__ void __launch_bounds__(256) gated_kernel(const muon_gated_args a) {
   const T* gate = static_cast<const T*>(a.gate);
   const T* up = static_cast<const T*>(a.up);
   uint4 rg[U], ru[U];
+  LoadAnywhere<T> lg[U], lu[U];
   if constexpr (ANYWHERE) {
     const Span sg = Span::of<T>(gate, a.rows, cols, a.ldg), su = Span::of<T>(up, a.rows, cols, a.ldu);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const long long row = row0 + u * GROUPS;
       const bool in = row < a.rows;
-      rg[u] = load_anywhere<T, LANES>(gate + (in ? row * a.ldg : 0), col / E, in ? left : 0, sg);
-      ru[u] = load_anywhere<T, LANES>(up + (in ? row * a.ldu : 0), col / E, in ? left : 0, su);
+      lg[u].load(gate + (in ? row * a.ldg : 0), col / E, in ? left : 0, sg);
+      lu[u].load(up + (in ? row * a.ldu : 0), col / E, in ? left : 0, su);
     }
   } else {
 #pragma unroll
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(256) gated_kernel(const muon_gated_args a) {
     const long long row = row0 + u * GROUPS;
     const bool live = row < a.rows;
     P g, v, y;
+    if constexpr (ANYWHERE) rg[u] = lg[u].get(), ru[u] = lu[u].get();
     g.unpack(rg[u]);
     v.unpack(ru[u]);
 #pragma unroll
@@ -284,6 +286,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
     using M = std::remove_const_t<std::remove_pointer_t<decltype(matrix)>>;
     constexpr int E = 16 / static_cast<int>(sizeof(M)), PER_ROW = kTile / E;
     return [=](int chunk) {
+      LoadAnywhere<std::conditional_t<sizeof(M) == 1, __half, M>> loads[kChunkRows * PER_ROW / 32];  // of rows that start anywhere
 #pragma unroll
       for (int k = 0; k < kChunkRows * PER_ROW / 32; ++k) {
         const int item = k * 32 + lane, r = item / PER_ROW, t = item % PER_ROW;
@@ -294,10 +297,16 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
         if constexpr (decltype(anywhere)::value) {
           const Span all = Span::of<M>(matrix, rows, cols, ld);
           const int l = static_cast<int>(row < rows ? min(left - t * E, 1LL << 20) : 0LL);
-          *reinterpret_cast<uint4*>(dst) =
-              load_anywhere<M, (PER_ROW < 32 ? PER_ROW : 32)>(matrix + (row < rows ? row * ld + c00 : 0), t, l, all);
+          loads[k].load(matrix + (row < rows ? row * ld + c00 : 0), t, l, all);
         } else {
           copy16(smem_u32(dst), src, n * static_cast<int>(sizeof(M)));
+        }
+      }
+      if constexpr (decltype(anywhere)::value) {
+#pragma unroll
+        for (int k = 0; k < kChunkRows * PER_ROW / 32; ++k) {
+          const int item = k * 32 + lane;
+          *reinterpret_cast<uint4*>(to + chunk * G::CHUNK + item / PER_ROW * kTile * static_cast<int>(sizeof(M)) + item % PER_ROW * 16) = loads[k].get();
         }
       }
     };
@@ -550,14 +559,15 @@ __global__ void __launch_bounds__(256) gated_grad_dense_kernel(const muon_gated_
   const long long group = blockIdx.y + static_cast<long long>(blockIdx.z) * gridDim.y, row0 = group * GROUPS * U + threadIdx.x / LANES;
   const long long rows4 = (a.rows + 3) & ~3LL;
   P d[U], g[U], v[U];
+  LoadAnywhere<T> ld[U], lg[U], lv[U];  // of rows that start anywhere
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const long long row = row0 + u * GROUPS;
     const bool in = row < a.rows;
-    const auto plain = [&](P& p, const void* matrix, long long ld) {
+    const auto plain = [&](P& p, LoadAnywhere<T>& l, const void* matrix, long long ld) {
       const T* m = static_cast<const T*>(matrix);
       if constexpr (ANYWHERE) {
-        p.unpack(load_anywhere<T, LANES>(m + (in ? row * ld : 0), col / E, in ? left : 0, Span::of<T>(m, a.rows, cols, ld)));
+        l.load(m + (in ? row * ld : 0), col / E, in ? left : 0, Span::of<T>(m, a.rows, cols, ld));
       } else {
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
         if (in && left >= E) w = *reinterpret_cast<const uint4*>(m + row * ld + col);
@@ -565,9 +575,9 @@ __global__ void __launch_bounds__(256) gated_grad_dense_kernel(const muon_gated_
         p.unpack(w);
       }
     };
-    const auto kept = [&](P& p, const void* matrix, const void* scale, long long ld) {
+    const auto kept = [&](P& p, LoadAnywhere<T>& l, const void* matrix, const void* scale, long long ld) {
       if constexpr (KEPT == 0) {
-        plain(p, matrix, ld);
+        plain(p, l, matrix, ld);
       } else {
         __align__(8) uint8_t b[E] = {};
         const uint8_t* q = static_cast<const uint8_t*>(matrix) + row * ld + col;
@@ -588,15 +598,19 @@ __global__ void __launch_bounds__(256) gated_grad_dense_kernel(const muon_gated_
         for (int i = 0; i < N; ++i) p.v[i] = mul2(p.v[i], both(s));
       }
     };
-    plain(d[u], a.dy, a.lddy);
-    kept(g[u], a.gate, a.gate_scale, a.ldg);
-    kept(v[u], a.up, a.up_scale, a.ldu);
+    plain(d[u], ld[u], a.dy, a.lddy);
+    kept(g[u], lg[u], a.gate, a.gate_scale, a.ldg);
+    kept(v[u], lv[u], a.up, a.up_scale, a.ldu);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const long long row = row0 + u * GROUPS;
     const bool in = row < a.rows;
     P dg, du;
+    if constexpr (ANYWHERE) {
+      d[u].unpack(ld[u].get());
+      if constexpr (KEPT == 0) g[u].unpack(lg[u].get()), v[u].unpack(lv[u].get());
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const Activation f = activate2<T, GELU>(g[u].v[i]);

@@ -130,22 +130,6 @@ __device__ __forceinline__ uint4 window(const uint4& lo, const uint4& hi, int o)
   return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
                     __funnelshift_r(w[3], w[4], bits));
 }
-// The aligned 16 bytes at p as far as they lie in [from, to), the rest as 0.  T: what the memory holds.
-template <typename T>
-__device__ __forceinline__ uint4 load_granule(const uint8_t* p, const uint8_t* from, const uint8_t* to) {
-  if (p >= from && p + 16 <= to) return *reinterpret_cast<const uint4*>(p);
-  union {
-    uint4 w;
-    T e[16 / sizeof(T)];
-  } u;
-  u.w = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i) {
-    const uint8_t* q = p + i * sizeof(T);
-    if (q >= from && q < to) u.e[i] = *reinterpret_cast<const T*>(q);
-  }
-  return u.w;
-}
 // A matrix whose rows start anywhere: its memory's ends, so that whole 16 bytes are read only where they lie within.
 struct Span {
   const uint8_t *from, *to;
@@ -155,32 +139,44 @@ struct Span {
     return {b, b + ((rows - 1) * ld + cols) * static_cast<long long>(sizeof(T))};
   }
 };
-// Pieces of one row in LANES neighbouring lanes: piece t of a row of `cols` columns, of which `left` = cols - t E (0 or less:
-// none) are there from its first on.  What a neighbour has of a lane's 16 bytes comes from it; the lanes at the ends fetch
-// or write the rest themselves.  All lanes of a warp call.
-template <typename T, int LANES>
-__device__ __forceinline__ uint4 load_anywhere(const T* row, int t, int left, const Span& s) {
-  constexpr int E = 16 / static_cast<int>(sizeof(T));
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x % LANES;
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(row) - off + 16LL * t;
-  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-  if (left > 0) lo = load_granule<T>(p, s.from, s.to);
-  const bool end = lane == LANES - 1 || left <= E;
-  if (end && left * static_cast<int>(sizeof(T)) > 16 - off) hi = load_granule<T>(p + 16, s.from, s.to);
-  const uint4 next = make_uint4(__shfl_down_sync(0xffffffffu, lo.x, 1, LANES), __shfl_down_sync(0xffffffffu, lo.y, 1, LANES),
-                                __shfl_down_sync(0xffffffffu, lo.z, 1, LANES), __shfl_down_sync(0xffffffffu, lo.w, 1, LANES));
-  union {
-    uint4 w;
-    T e[E];
-  } u;
-  u.w = window(lo, end ? hi : next, off);
-  if (left < E) {  // the next row's
+// Piece t of a row of `cols` columns, of which `left` = cols - t E (0 or less: none) are there from its first on: from the four
+// or five aligned words that it lies in, which neighbouring lanes' loads share in L1.  Loading and using are apart, so that a
+// thread's loads are under way together.
+template <typename T>
+struct LoadAnywhere {
+  uint32_t w[5];
+  int bits;
+  __device__ __forceinline__ void load(const T* row, int t, int left, const Span& s) {
+    constexpr int E = 16 / static_cast<int>(sizeof(T));
+    const uint8_t* piece = reinterpret_cast<const uint8_t*>(row) + 16LL * t;
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(piece) & 3);
+    const uint8_t* p = piece - odd;
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i >= left) u.e[i] = from_f32<T>(0.f);
+    for (int i = 0; i < 5; ++i) w[i] = 0u;
+    bits = 0;
+    if (left >= E && p >= s.from && p + 20 <= s.to) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = q[i];
+      bits = 8 * odd;
+    } else if (left > 0) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (i < left) {
+          const T v = reinterpret_cast<const T*>(piece)[i];
+          if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v);
+          else w[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(&v)) << (16 * (i & 1));
+        }
+      }
+    }
   }
-  return u.w;
-}
+  __device__ __forceinline__ uint4 get() const {
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+  }
+};
+// And written, by LANES neighbouring lanes with neighbouring pieces: what a neighbour has of a lane's aligned 16 bytes comes from
+// it; the lanes at the ends write the rest themselves.  All lanes of a warp call.
 template <typename T, int LANES>
 __device__ __forceinline__ void store_anywhere(T* row, int t, int left, const Pairs<T>& v) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
@@ -235,11 +231,22 @@ __device__ __forceinline__ void fetch_anywhere(uint8_t* slot, const T* row, int 
     else *reinterpret_cast<uint4*>(slot + 16) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
-// off: the row's address modulo 16.
-template <int LANES>
+// off: the row's address modulo 16.  By WORDS, four lanes of which share a bank, or as two accesses of 16 bytes and the choice
+// among their words, which takes twice the instructions and less than half of shared memory's time: the norms, which read
+// three arrays and are bound by issuing, are 10 us of 33.5M elements faster with the first, their gradient, which reads
+// five, 14 with the second.
+template <int LANES, bool WORDS>
 __device__ __forceinline__ uint4 read_anywhere(const uint8_t* slot, int off) {
-  const uint4* q = reinterpret_cast<const uint4*>(slot) + threadIdx.x % 32 / LANES * (LANES + 1) + threadIdx.x % LANES;
-  return window(q[0], q[1], off);
+  slot += (threadIdx.x % 32 / LANES * (LANES + 1) + threadIdx.x % LANES) * 16;
+  if constexpr (WORDS) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(slot + (off & 12));
+    const int bits = 8 * (off & 3);
+    const uint32_t w[5] = {q[0], q[1], q[2], q[3], off & 3 ? q[4] : 0u};
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+  } else {
+    return window(reinterpret_cast<const uint4*>(slot)[0], reinterpret_cast<const uint4*>(slot)[1], off);
+  }
 }
 
 // Scales of up to four matrices' blocks, whose 128 columns lie in LANES = 16 or 32 neighbouring lanes.  The largest
