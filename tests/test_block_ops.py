@@ -363,6 +363,30 @@ def test_block_norm_many_rows(mm, cols):
     check_norm(mm, norm_inputs(4, rows, cols, torch.bfloat16, "element", True), fp8="e4m3", checkpoint="e4m3")
 
 
+# rows of one CTA's widest ring, of clusters, and those that no cluster's rings hold
+WIDE = [(torch.bfloat16, 12_000), (torch.bfloat16, 16_392), (torch.bfloat16, 32_768), (torch.bfloat16, 32_769), (torch.bfloat16, 40_960),
+        (torch.bfloat16, 65_536), (torch.float16, 65_535), (torch.float32, 8_192), (torch.float32, 16_384), (torch.float32, 16_385),
+        (torch.float32, 32_768), (torch.float32, 40_000), (torch.float32, 65_536)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype,cols", WIDE)
+def test_block_norm_wide_rows(mm, dtype, cols):
+    check_norm(mm, norm_inputs(16, 3, cols, dtype, "element", True), fp8="e4m3", checkpoint="e4m3")
+    check_norm(mm, norm_inputs(17, 2, cols, dtype, "row", False), fp8="e5m2", checkpoint="e4m3", y=False)
+    for kept in ("e4m3", None, "e5m2"):
+        check_norm_grad(mm, 18, 3, cols, dtype, "element", True, kept=kept)
+        check_norm_grad(mm, 19, 2, cols, dtype, "row", False, kept=kept, dh=False)
+
+
+@gpu
+@pytest.mark.parametrize("cols", [8_200, 16_392, 33_000])
+@pytest.mark.parametrize("kept", [None, "e4m3"])
+def test_block_norm_wide_rows_more_than_clusters(mm, cols, kept):
+    check_norm(mm, norm_inputs(20, 170, cols, torch.bfloat16, "element", True), fp8="e4m3", checkpoint=kept)
+    check_norm_grad(mm, 21, 170, cols, torch.bfloat16, "element", True, kept=kept)
+
+
 def strided(t, pad, offset=0):
     """t's values on the GPU in rows with `pad` more elements, `offset` elements into the allocation."""
     rows, cols = t.shape
@@ -383,6 +407,17 @@ def test_block_norm_strides_alignment_and_weight_types(mm, wdt, pad, offset):
         again = mm.block_norm(*run[:2], *run[3:5], gate=run[2], scale=run[5], fp8="e4m3", checkpoint="e5m2")
         assert torch.equal(got.y, again.y) and torch.equal(got.h, again.h)
         check_norm_grad(mm, 6, 11, 520, torch.bfloat16, gate, True, wdt=wdt, pad=pad, offset=offset)
+
+
+@gpu
+@pytest.mark.parametrize("cols,pad", [(4, 4), (12, 4), (100, 4), (123, 5), (130, 6), (1_020, 4), (4_093, 3)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_block_norm_ragged_rows_on_16_bytes(mm, dtype, cols, pad):
+    """Rows that start on 16 bytes and end off them."""
+    ins = norm_inputs(22, 37, cols, dtype, "element", True)
+    check_norm(mm, ins, fp8="e4m3", checkpoint="e4m3", run=[strided(t, pad) for t in ins[:3]] + dev(*ins[3:]))
+    check_norm_grad(mm, 23, 37, cols, dtype, "element", True, pad=pad)
+    check_norm_grad(mm, 24, 37, cols, dtype, "row", True, pad=pad, kept="e4m3")
 
 
 @gpu
@@ -917,3 +952,69 @@ def test_offsets_past_32_bits(mm):
     assert torch.equal(m.y[-7:], n.y) and torch.equal(m.h[-7:], n.h) and torch.equal(raw(m.kept.gate.data[-7:]), raw(n.kept.gate.data))
     g, h = mm.block_norm_backward(x, m.kept, w, w, dh=x, dweights=False), mm.block_norm_backward(end, n.kept, w, w, dh=end, dweights=False)
     assert torch.equal(g.dx[-7:], h.dx) and torch.equal(g.dgate[-7:], h.dgate) and torch.equal(g.dresidual[-7:], h.dresidual)
+
+
+@gpu
+@pytest.mark.parametrize("cols", [9, 120, 515, 1300])
+@pytest.mark.parametrize("pad,offset", [(8, 0), (3, 0), (1, 1), (5, 3)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_outputs_with_strides_leave_what_lies_between_their_rows(mm, dtype, cols, pad, offset):
+    """The C entry points with outputs of any stride and alignment: values as for contiguous ones, and nothing else written."""
+    from newton_schulz_04_gb300 import blocks
+    rows, lib, st = 21, mm.load(), torch.cuda.current_stream().cuda_stream
+    code = {torch.bfloat16: 0, torch.float32: 1}[dtype]
+    x, r, g, post, pre, scale = dev(*norm_inputs(110, rows, cols, dtype, "element", True))
+    dy = gen(111, rows, cols).to(dtype).cuda()
+    buffers = []
+
+    def out():
+        buf = torch.full((rows * (cols + pad) + offset + 16,), 5.0, dtype=dtype, device="cuda")
+        v = buf[offset:].as_strided((rows, cols), (cols + pad, 1))
+        buffers.append((buf, v))
+        return v
+
+    def same(v, want):
+        assert torch.equal(v, want)
+        v.fill_(5.0)
+
+    ld = cols + pad
+    want = mm.block_norm(x, r, post, pre, gate=g, scale=scale)
+    y, h = out(), out()
+    stats = torch.empty(2, rows, device="cuda")
+    assert lib.muon_block_norm(blocks._BLOCK_NORM(
+        x.data_ptr(), cols, r.data_ptr(), cols, g.data_ptr(), cols, post.data_ptr(), scale.data_ptr(), pre.data_ptr(), y.data_ptr(), ld,
+        h.data_ptr(), ld, stats[0].data_ptr(), stats[1].data_ptr(), *([0] * 12), rows, cols, code, 1, 0, 0, 0, 1.0, 1e-6), st) == 0
+    same(y, want.y), same(h, want.h)
+    grads = mm.block_norm_backward(dy, want.kept, post, pre, scale=scale, dh=r)
+    dx, dr, dg = out(), out(), out()
+    assert lib.muon_block_norm_backward(blocks._BLOCK_NORM_GRAD(
+        dy.data_ptr(), cols, r.data_ptr(), cols, x.data_ptr(), 0, cols, want.h.data_ptr(), 0, cols, g.data_ptr(), 0, cols,
+        want.kept.rstd_x.data_ptr(), want.kept.rstd_h.data_ptr(), post.data_ptr(), scale.data_ptr(), pre.data_ptr(), dx.data_ptr(), ld,
+        dr.data_ptr(), ld, dg.data_ptr(), ld, 0, 0, 0, 0, 0, rows, cols, code, 1, 0, 0, 1.0), st) == 0
+    same(dx, grads.dx), same(dr, grads.dresidual), same(dg, grads.dgate)
+    a = mm.gated_activation(g, x)
+    y = out()
+    assert lib.muon_gated_activation(blocks._GATED(g.data_ptr(), cols, x.data_ptr(), cols, y.data_ptr(), ld, *([0] * 9), rows, cols, code, 0, 0,
+                                                   0), st) == 0
+    same(y, a.y)
+    for eight in (False, True):   # the two kernels
+        b = mm.gated_activation_backward(dy, a.kept, y_fp8="e4m3" if eight else None)
+        dg, du = out(), out()
+        q = [b.y_cols.data.data_ptr(), b.y_cols.scale.data_ptr(), b.y_cols._ld()] if eight else [0, 0, 0]
+        assert lib.muon_gated_activation_backward(blocks._GATED_GRAD(
+            dy.data_ptr(), cols, g.data_ptr(), 0, cols, x.data_ptr(), 0, cols, dg.data_ptr(), ld, du.data_ptr(), ld, *([0] * 12), *q, rows, cols,
+            code, 0, 0, 0, 0), st) == 0
+        same(dg, b.dgate), same(du, b.dup)
+    torch.cuda.synchronize()
+    for buf, _ in buffers:
+        assert bool((buf == 5.0).all())
+
+
+@gpu
+def test_calls_give_the_same_bits_again(mm):
+    x, r, g, post, pre, scale = dev(*norm_inputs(120, 1000, 1100, torch.bfloat16, "element", True))
+    a = mm.block_norm(x, r, post, pre, gate=g, scale=scale, checkpoint="e4m3")
+    first = mm.block_norm_backward(x, a.kept, post, pre, scale=scale, dh=r)
+    for _ in range(5):
+        for one, two in zip(first, mm.block_norm_backward(x, a.kept, post, pre, scale=scale, dh=r)):
+            assert torch.equal(one, two)
