@@ -47,24 +47,32 @@ def _out8(q: Optional[Fp8Tensor]):
     return _NONE8 if q is None else (q.data.data_ptr(), q.scale.data_ptr(), q._ld())
 
 
-def _vectors(names, tensors, cols, device):
-    """The one type of contiguous [cols] vectors (or None among them)."""
-    kind = None
-    for name, t in zip(names, tensors):
+def _vectors(post, pre, scale, cols, device):
+    """post_weight, pre_weight and the scale (or None): contiguous [cols] of one type."""
+    shape, kind = (cols,), post.dtype
+    if post.shape == shape == pre.shape and pre.dtype == kind and post.device == device == pre.device \
+            and post.is_contiguous() and pre.is_contiguous() \
+            and (scale is None or scale.shape == shape and scale.dtype == kind and scale.device == device and scale.is_contiguous()):
+        return
+    for name, t in (("post_weight", post), ("pre_weight", pre), ("scale", scale)):
         if t is None:
             continue
-        if t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous() or t.device != device:
+        if t.shape != shape or not t.is_contiguous() or t.device != device:
             raise ValueError(f"{name} must be a contiguous [{cols}] tensor on {device}")
-        if kind is None:
-            kind = t.dtype
-        elif t.dtype != kind:
+        if t.dtype != kind:
             raise TypeError(f"{name} is {t.dtype}: the weights and the scale have one dtype, {kind}")
-    return kind
 
 
-def _required(name, t):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
+def _required(**tensors):
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+
+
+def _stride(t, like, cols, name) -> int:
+    """Row stride of a tensor of `like`'s shape, dtype and device."""
+    _like(t, like, name)
+    return cols if t.is_contiguous() else _rows(t, name)[1]
 
 
 def _per_row(gate, like) -> bool:
@@ -82,9 +90,9 @@ def _kept(name, t, dy, rows, cols):
         if t.data.shape != (rows, cols) or t.data.device != dy.device:
             raise ValueError(f"{name} must be an 8-bit [{rows}, {cols}] matrix on {dy.device}")
         return t.data.data_ptr(), t.scale.data_ptr(), t._ld(), _TYPE_FMT[t.data.dtype]
-    _required(name, t)
-    _like(t, dy, name)
-    return t.data_ptr(), 0, _rows(t, name)[1], None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor or an Fp8Tensor")
+    return t.data_ptr(), 0, _stride(t, dy, cols, name), None
 
 
 def _tensors(*kept):
@@ -100,7 +108,7 @@ def _vector(n, device):  # one allocation each: views of a new one cost the host
 
 
 def _new(like, device):
-    return torch.empty(like.shape, dtype=like.dtype, device=device)
+    return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=device)
 
 
 # ---------------------------------------------------------------- norms around a block
@@ -144,23 +152,22 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tenso
     weights and scale (or None) are [cols] of one type.  `fp8` ("e4m3" or "e5m2") asks for y in 8 bits as well, `y=False`
     leaves out the other y.  What the gradient needs is in `kept`: x, h and gate themselves, or with `checkpoint` 8-bit
     copies of them (a gate of each row stays as it is)."""
-    for name, t in (("x", x), ("residual", residual), ("post_weight", post_weight), ("pre_weight", pre_weight)):
-        _required(name, t)
+    _required(x=x, residual=residual, post_weight=post_weight, pre_weight=pre_weight)
     shape = x.shape
     if not shape or shape[-1] < 1:
         raise ValueError("x needs a last dimension of at least 1")
     if not (y or fp8):
         raise ValueError("neither y nor an 8-bit copy is asked for")
     rows, ldx = _rows(x, "x")
-    _like(residual, x, "residual")
-    ldr = _rows(residual, "residual")[1]
+    cols = shape[-1]
+    ldr = _stride(residual, x, cols, "residual")
     dev, per_row, ldg = x.device, 0, 0
     if gate is not None:
         if gate.dtype != x.dtype or gate.device != dev:
             raise ValueError("gate must have the dtype and device of x")
         per_row = 1 if _per_row(gate, x) else 0
-        ldg = _rows(gate, "gate")[1]
-    kind = _vectors(("post_weight", "pre_weight", "scale"), (post_weight, pre_weight, scale), shape[-1], dev)
+        ldg = cols if not per_row and gate.is_contiguous() else _rows(gate, "gate")[1]
+    _vectors(post_weight, pre_weight, scale, cols, dev)
     codes = (_dt(x, "x"), _dt(post_weight, "post_weight"), per_row, 0 if fp8 is None else _fmt_code(fp8),
              0 if checkpoint is None else _fmt_code(checkpoint))
     return _on(stream, dev, (x, residual, gate, post_weight, scale, pre_weight), _block_norm, x, ldx, residual, ldr, gate, ldg,
@@ -193,17 +200,13 @@ def block_norm_backward(dy: torch.Tensor, kept: BlockNormKept, post_weight: torc
 
     `dh` is what reaches h on its way past the second norm.  dx, dresidual and dgate have the types of the forward pass;
     the gradients of the weights and of the scale are fp32 [cols], or None with `dweights=False`."""
-    for name, t in (("dy", dy), ("post_weight", post_weight), ("pre_weight", pre_weight)):
-        _required(name, t)
+    _required(dy=dy, post_weight=post_weight, pre_weight=pre_weight)
     shape = dy.shape
     if not shape or shape[-1] < 1:
         raise ValueError("dy needs a last dimension of at least 1")
     cols, dev = shape[-1], dy.device
     rows, lddy = _rows(dy, "dy")
-    lddh = 0
-    if dh is not None:
-        _like(dh, dy, "dh")
-        lddh = _rows(dh, "dh")[1]
+    lddh = 0 if dh is None else _stride(dh, dy, cols, "dh")
     x, h, gate, rstd_x, rstd_h = kept
     kx, kh = _kept("kept.x", x, dy, rows, cols), _kept("kept.h", h, dy, rows, cols)
     kg, per_row, fmts = (0, 0, 0, kx[3]), 0, {kx[3], kh[3]}
@@ -222,7 +225,7 @@ def block_norm_backward(dy: torch.Tensor, kept: BlockNormKept, post_weight: torc
     for name, t in (("kept.rstd_x", rstd_x), ("kept.rstd_h", rstd_h)):
         if t.dtype != torch.float32 or t.numel() != rows or not t.is_contiguous() or t.device != dev:
             raise ValueError(f"{name} must be {rows} contiguous float32 values on {dev}")
-    _vectors(("post_weight", "pre_weight", "scale"), (post_weight, pre_weight, scale), cols, dev)
+    _vectors(post_weight, pre_weight, scale, cols, dev)
     codes = (_dt(dy, "dy"), _dt(post_weight, "post_weight"), per_row, kx[3] or 0)
     return _on(stream, dev, (dy, dh, rstd_x, rstd_h, post_weight, scale, pre_weight, *_tensors(x, h, gate)), _block_norm_backward,
                dy, lddy, dh, lddh, kx, kh, kg, gate, rstd_x, rstd_h, post_weight, scale, pre_weight, rows, codes, float(alpha),
@@ -290,16 +293,14 @@ def gated_activation(gate: torch.Tensor, up: torch.Tensor, activation: str = "si
     gate and up are bf16, fp16 or fp32 of one shape, each with its own row stride (the halves of one product, say).  `fp8`
     ("e4m3" or "e5m2") asks for y in 8 bits as well, `y=False` leaves out the other y.  `kept` is for the gradient: gate
     and up themselves, or with `checkpoint` 8-bit copies of them."""
-    for name, t in (("gate", gate), ("up", up)):
-        _required(name, t)
+    _required(gate=gate, up=up)
     if not gate.shape:
         raise ValueError("gate must have at least one dimension")
     act = _activation(activation)
     if not (y or fp8):
         raise ValueError("neither y nor an 8-bit copy is asked for")
     rows, ldg = _rows(gate, "gate")
-    _like(up, gate, "up")
-    ldu = _rows(up, "up")[1]
+    ldu = _stride(up, gate, gate.shape[-1], "up")
     codes = (_dt(gate, "gate"), act, 0 if fp8 is None else _fmt_code(fp8), 0 if checkpoint is None else _fmt_code(checkpoint))
     return _on(stream, gate.device, (gate, up), _gated, gate, ldg, up, ldu, rows, codes, fp8, y, checkpoint, gate.device)
 
@@ -325,7 +326,7 @@ def gated_activation_backward(dy: torch.Tensor, kept: GatedKept, activation: str
     `dense` asks for dgate and dup in dy's type; `fp8` for both in 8 bits, along their columns and transposed, as the
     products that follow read them; `y_fp8` for the activation again, transposed in 8 bits, for the gradient of the
     weight behind it."""
-    _required("dy", dy)
+    _required(dy=dy)
     if not dy.shape:
         raise ValueError("dy must have at least one dimension")
     act = _activation(activation)
