@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   using Slots = GradRing<T, G, S, KEPT != 0, ANYWHERE>;
   constexpr int E = P::E, N = P::N;
   extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ RowSums<G, TH, 3, CL> sums;
+  __shared__ RowSums3<G, TH, CL> sums;
   const Slots ring{ring_smem};
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
   constexpr int LANES = G < 32 ? G : 32;  // of a row in a warp
   using Scales = Scales4<(128 / E < G ? 128 / E : G)>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ RowSums<G, TH, 1, CL> sums;
+  __shared__ RowSum<G, TH, CL> row_total;
   const RowRing<T, G, C, S, ANYWHERE> ring{ring_smem};
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
@@ -206,7 +206,6 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
     constexpr bool KEEP = ANYWHERE && C <= 2;  // what takes shifts to read, where there are registers for it
     uint4 kx[C], kg[C];
     float2 two = both(0.f);
-    float sum[1];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       P x;
@@ -215,9 +214,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
 #pragma unroll
       for (int i = 0; i < N; ++i) two = fma2(x.v[i], x.v[i], two);
     }
-    sum[0] = total(two);
-    sums(sum, turn);
-    const float rx = row_rstd(sum[0], fcols, inv_cols, a.eps);
+    const float rx = row_rstd(row_total(total(two), turn), fcols, inv_cols, a.eps);
     two = both(0.f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -233,9 +230,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
         two = fma2(h[c].v[i], h[c].v[i], two);
       }
     }
-    sum[0] = total(two);
-    sums(sum, turn + 1);
-    const float rh = row_rstd(sum[0], fcols, inv_cols, a.eps);
+    const float rh = row_rstd(row_total(total(two), turn + 1), fcols, inv_cols, a.eps);
     if (live && t == 0 && rank == 0) {
       if (a.rstd_x) a.rstd_x[row] = rx;
       if (a.rstd_h) a.rstd_h[row] = rh;
@@ -327,8 +322,9 @@ static cudaError_t dispatch_ring(const muon_block_norm_args& a, int sms, cudaStr
 template <typename T, bool ANYWHERE>
 cudaError_t launch_block_norm_rows(const muon_block_norm_args& a, int sms, cudaStream_t st) {
   // 4 CTAs of 2048 pieces hold MUON_MAX_DIM 16-bit columns and half as many of fp32
-  if (a.cols > 4 * 2048 * (16 / static_cast<int>(sizeof(T))))
-    return launch_pdl(block_norm_wide_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(512), 0, st, a);
+  if constexpr (sizeof(T) == 4) {
+    if (a.cols > 4 * 2048 * 4) return launch_pdl(block_norm_wide_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(512), 0, st, a);
+  }
   const bool element = a.gate && !a.gate_per_row, kept = a.x8.data && a.h8.data && (a.gate8.data || !element);
   const bool e4m3 = kept && a.kept_fmt == MUON_E4M3 && (!a.q.data || a.fmt == MUON_E4M3);
   const auto go = [&](auto gate) {

@@ -130,52 +130,83 @@ inline cudaError_t smem_limit(F kernel, int bytes, bool (&done)[64]) {
   return cudaSuccess;
 }
 
-// Sums over the threads of a row, N at once: G threads of each of the CL CTAs of a cluster (CL = 1: of a CTA that holds
-// TH / G rows).  One barrier; `sh` alternates between two buffers.
-template <int G, int TH, int N, int CL>
-struct RowSums {
+// Sums over the threads of a row: G threads of each of the CL CTAs of a cluster (CL = 1: of a CTA that holds TH / G rows).  One
+// barrier; the shared memory alternates between two buffers.
+template <int G, int TH, int CL>
+struct RowSum {
   static constexpr int WARPS = TH / 32, W = G < 32 ? 1 : G / 32;
-  float v[2][N][CL * WARPS];
-  __device__ __forceinline__ void operator()(float (&s)[N], int turn) {
+  static_assert(CL == 1 || (G == TH && (CL * WARPS <= 32 || CL * WARPS % 32 == 0)), "rows of whole CTAs");
+  float v[2][CL * WARPS];
+  __device__ __forceinline__ float operator()(float s, int turn) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int o = G < 32 ? G / 2 : 16; o > 0; o >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
-    if (G <= 32 && CL == 1) return;
-    float(&b)[N][CL * WARPS] = v[turn & 1];
+    for (int o = G < 32 ? G / 2 : 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (G <= 32 && CL == 1) return s;
+    float(&b)[CL * WARPS] = v[turn & 1];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if constexpr (CL == 1) {
-      if (lane == 0) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) b[n][warp] = s[n];
-      }
+      if (lane == 0) b[warp] = s;
       __syncthreads();
-      const int at = (threadIdx.x / G) * W + (threadIdx.x & (W - 1));
+      s = b[(threadIdx.x / G) * W + (threadIdx.x & (W - 1))];
 #pragma unroll
-      for (int n = 0; n < N; ++n) {  // as a tree: each of the last additions rounds the whole
-        s[n] = b[n][at];
-#pragma unroll
-        for (int o = W / 2; o > 0; o >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
-      }
+      for (int o = W / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);  // a tree: each of the last additions rounds the whole
     } else {
-      static_assert(CL == 1 || (G == TH && (CL * WARPS <= 32 || CL * WARPS % 32 == 0)), "rows of whole CTAs");
-      if (lane < CL) {  // a lane to a CTA of the cluster
-        const uint32_t rank = cluster_ctarank();
-#pragma unroll
-        for (int n = 0; n < N; ++n) st_shared_cluster(mapa_cluster(&b[n][rank * WARPS + warp], lane), __float_as_int(s[n]));
-      }
+      if (lane < CL) st_shared_cluster(mapa_cluster(&b[cluster_ctarank() * WARPS + warp], lane), __float_as_int(s));  // a lane to a CTA
       __syncwarp();
       cluster_sync();
+      s = lane < CL * WARPS ? b[lane] : 0.f;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        float f = lane < CL * WARPS ? b[n][lane] : 0.f;
+      for (int k = 32; k < CL * WARPS; k += 32) s += b[k + lane];
 #pragma unroll
-        for (int k = 32; k < CL * WARPS; k += 32) f += b[n][k + lane];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
-        s[n] = f;
-      }
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     }
+    return s;
+  }
+};
+
+// Three sums at once: they part company as the lanes that hold them halve, so that a quarter of a warp (or half warp) ends
+// with one of them; half of the instructions of three sums in all lanes.
+template <int G, int TH, int CL>
+struct RowSums3 {
+  static constexpr int WARPS = TH / 32, W = G < 32 ? 1 : G / 32, LANES = G < 32 ? G : 32, Q = LANES / 4;
+  static_assert(CL == 1 || (G == TH && CL <= Q), "rows of whole CTAs");
+  alignas(16) float v[2][3][CL * WARPS];
+  __device__ __forceinline__ void operator()(float (&s)[3], int turn) {
+    const int lane = threadIdx.x % LANES, mine = lane / Q;  // lanes of quarter 0: the first sum, 1 and 3: the second, 2: the third
+    const bool up = lane & (2 * Q), odd = lane & Q;
+    const float k = (up ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, up ? s[0] : s[2], 2 * Q);
+    const float m = s[1] + __shfl_xor_sync(0xffffffffu, s[1], 2 * Q);
+    float f = (odd ? m : k) + __shfl_xor_sync(0xffffffffu, odd ? k : m, Q);
+    auto quarter = [&] {
+#pragma unroll
+      for (int o = Q / 2; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+    };
+    quarter();
+    if constexpr (G > 32 || CL > 1) {
+      float(&b)[3][CL * WARPS] = v[turn & 1];
+      const int warp = threadIdx.x / 32, sum = odd ? 1 : up ? 2 : 0, at = lane % Q;
+      if constexpr (CL == 1) {
+        if (at == 0 && mine < 3) b[sum][warp] = f;
+        __syncthreads();
+        const int first = (threadIdx.x / G) * W;
+        f = at < W ? b[sum][first + at] : 0.f;
+#pragma unroll
+        for (int k2 = Q; k2 < W; k2 += Q) f += b[sum][first + k2 + at];
+      } else {
+        if (at < CL && mine < 3)  // a lane to a CTA of the cluster
+          st_shared_cluster(mapa_cluster(&b[sum][cluster_ctarank() * WARPS + warp], at), __float_as_int(f));
+        __syncwarp();
+        cluster_sync();
+        f = 0.f;
+#pragma unroll
+        for (int k2 = 0; k2 < CL * WARPS; k2 += 4 * Q) {
+          const float4 p = k2 + 4 * at < CL * WARPS ? *reinterpret_cast<const float4*>(&b[sum][k2 + 4 * at]) : make_float4(0.f, 0.f, 0.f, 0.f);
+          f += (p.x + p.y) + (p.z + p.w);
+        }
+      }
+      quarter();
+    }
+#pragma unroll
+    for (int n = 0; n < 3; ++n) s[n] = __shfl_sync(0xffffffffu, f, n * Q, LANES);
   }
 };
 
