@@ -1,4 +1,4 @@
-// block_norm.cuh -- arithmetic shared by the norms around a block and the gated activation.
+// block_norm.cuh -- what the kernels of the norms around a block share: sums and blocks of the widest rows, entry points.
 #pragma once
 #include <cuda_runtime.h>
 

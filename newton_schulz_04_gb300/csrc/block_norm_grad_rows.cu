@@ -6,7 +6,13 @@
 //   dpre = sum_rows dy H       S = sum_rows D sigmoid(gate) X       dpost = S scale       dscale = S post
 //
 // mean(b X) needs mean(a H) first.  With u = dh + rho_h a and e = sigmoid(gate) c X it is mean(u e) - rho_h mean(a H)
-// mean(H e), so a row takes one pass and one exchange of three sums.
+// mean(H e), so a row takes one pass and one exchange of three sums.  The columns' sums stay in registers, are written per CTA
+// and added in a fixed order by a second kernel.
+//
+// A ring of rows as in the forward kernel, one piece to a thread.  8191 x 4096 bf16 takes 92 us from e4m3 (4.7 TB/s, 70 % of the
+// copy rate) and 94 from bf16 (84 %): 16 warps of 128 registers on an SM issue 56 % of its slots, 56 instructions an element.
+// With scalars of fp32 it took 125, with choices at run time 120; two rows a turn, or the rows' factors and scales copied with
+// the rows, gained nothing.  Rows that start anywhere: 139 and 167 at 4095 columns.
 //
 // Compiled once for each type and alignment of rows (MUON_ROWS_T, MUON_ROWS_ANYWHERE).
 #include <cuda_runtime.h>
