@@ -78,7 +78,7 @@ def _on(stream, device, tensors, call, *args):
     away before a `stream` of the caller's has passed the call."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
-    if stream is None and device.index == torch._C._cuda_getDevice():
+    if stream is None and device.index == torch.cuda.current_device():
         return call(*args, torch._C._cuda_getCurrentRawStream(device.index))
     if stream is not None:
         for t in tensors:
