@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_wide_kernel(const muon_bl
     const bool element = a.gate && !a.gate_per_row;
     const Kept<T, KEPT8> kg(element ? a.gate : nullptr, a.gate_scale, a.ldg, row, a.rows, a.kept_fmt);
     const float rx = a.rstd_x[row], rh = a.rstd_h[row];
-    const float row_sig = a.gate && !element ? sigmoid2<T>(both(to_f32(static_cast<const T*>(a.gate)[row * a.ldg]))).x : 1.f;
+    const float row_sig = a.gate && !element ? sigmoid2<float>(both(to_f32(static_cast<const T*>(a.gate)[row * a.ldg]))).x : 1.f;
     struct Element {
       float d, u, hn, xn, sig, c;  // dy, dh + rho_h dy pre, H, X, sigmoid(gate), scale post
     };
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
     }
     const float2 xf = both(KEPT ? now.rx * fp8_scale_value(now.xs) : now.rx), hf = both(KEPT ? now.rh * fp8_scale_value(now.hs) : now.rh);
     const float2 gf = both(KEPT ? fp8_scale_value(now.gs) : 1.f);
-    const float row_sig = row_gated ? sigmoid2<T>(both(now.gate)).x : 1.f;
+    const float row_sig = row_gated ? sigmoid2<float>(both(now.gate)).x : 1.f;
     float2 s0 = both(0.f), s1 = s0, s2 = s0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(512) block_norm_wide_kernel(const muon_block_n
   const T* gate = static_cast<const T*>(a.gate) + (a.gate ? row * a.ldg : 0);
   float sum[1] = {0.f};
   float sig = 1.f;
-  if (a.gate && a.gate_per_row) sig = sigmoid2<T>(both(to_f32(*gate))).x;
+  if (a.gate && a.gate_per_row) sig = sigmoid2<float>(both(to_f32(*gate))).x;
   for (int col = threadIdx.x; col < cols; col += 512) sum[0] = fmaf(to_f32(x[col]), to_f32(x[col]), sum[0]);
   cta_sums<W, 1>(sum, sh, 0);
   const float n = static_cast<float>(cols), inv_n = 1.f / n;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
     const bool live = R == 1 || row < a.rows;
     if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row: earlier, the next kernel's CTAs take SMs from these
     float2 sig = both(1.f);
-    if (row_gated) sig = both(sigmoid2<T>(both(next_gate)).x), next_gate = row_gate(row + step);
+    if (row_gated) sig = both(sigmoid2<float>(both(next_gate)).x), next_gate = row_gate(row + step);
     if (ANYWHERE) __syncwarp();
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();

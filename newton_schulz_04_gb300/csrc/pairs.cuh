@@ -101,7 +101,8 @@ struct Pairs {
 __device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
 
 // 1 / (1 + exp(-g)) of a pair, 0 at -infinity and from about g = -87 on.  fp32 data takes the accurate exponential and
-// quotient; 16-bit data, which is rounded by 2^-11 at best, the hardware's: off by (4 + 1.2 |g|) 2^-23 of the value.
+// quotient, and so does a gate of a whole row, whose error all its elements share; 16-bit data, which is rounded by 2^-11 at
+// best, the hardware's: off by (4 + 1.2 |g|) 2^-23 of the value.
 template <typename T>
 __device__ __forceinline__ float2 sigmoid2(float2 g) {
   if constexpr (sizeof(T) == 4) {
