@@ -15,21 +15,26 @@
 
 namespace muon {
 
-// That takes some 20 instructions a value.  Where the scales of a tile's rows lie near enough to one another, 16-bit types hold
-// every value times 2^(s - largest s) exactly, and two at a time take half of them.  The other way, a function of its own that
+// That takes some 20 instructions a value.  Where the scales of a tile's rows lie near enough to its first row's, 16-bit types hold
+// every value times 2^(s - first s) exactly, and two at a time take half of them.  The other way, a function of its own that
 // costs this one no registers, is for the rest, and for tiles in which some column's largest magnitude is so small that
 // its factor leaves the 16-bit type's range.
 //
-// e4m3 goes through fp16, to and from which the hardware converts: scales within 2^14 (values are multiples of 2^-9, fp16's of
-// 2^-24).  e5m2 has fp16's exponents, which leaves no room for scales; its bits are those of a bf16 number times 2^-112, and
-// within 2^100 the products stay normal.
+// e4m3 goes through fp16, to and from which the hardware converts: scales 2^14 below the first (values are multiples of 2^-9, fp16's
+// of 2^-24) to 2^7 above it (values are at most 448).  e5m2 has fp16's exponents, which leaves no room for scales; its
+// bits are those of a bf16 number times 2^-112, and within 2^100 the products stay normal.  What a column's factor below 1
+// takes out of the normal range lies far below the 8-bit types' smallest values.
+//
+// 8192 x 4096 takes 18.6 us from e4m3 (54 % of the copy rate) and 23 from e5m2, by whole numbers 30: a tile's barriers and its
+// loads are hidden by three others on the SM only, at 61 % of the issue slots.
 template <bool E5M2>
 struct Pairwise {  // e4m3
   using V = __half2;
-  static constexpr uint32_t SPREAD = 14, LEAST = (127u - 6u) << 23;  // of scales; fp32 bits of a column's maximum
+  static constexpr int BELOW = 14, ABOVE = 7;                // the first row's scale
+  static constexpr uint32_t LEAST = (127u - 6u) << 23;       // fp32 bits of a column's maximum
   static __device__ __forceinline__ V bits(uint32_t w) { return *reinterpret_cast<const V*>(&w); }
-  static __device__ __forceinline__ V row_factor(uint32_t d) { return bits(((15u - d) << 10) * 0x10001u); }  // 2^-d
-  static __device__ __forceinline__ uint32_t column_factor(int k) { return (15 + max(0, min(14, k))) << 10; }  // 2^k
+  static __device__ __forceinline__ V row_factor(int k) { return bits(((15u + k) << 10) * 0x10001u); }  // 2^k
+  static __device__ __forceinline__ uint32_t column_factor(int k) { return (15 + max(-ABOVE, min(14, k))) << 10; }
   static __device__ __forceinline__ V decode(uint32_t two, V f) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(two)));
@@ -47,10 +52,11 @@ struct Pairwise {  // e4m3
 template <>
 struct Pairwise<true> {  // e5m2
   using V = __nv_bfloat162;
-  static constexpr uint32_t SPREAD = 100, LEAST = (127u - 60u) << 23;
+  static constexpr int BELOW = 100, ABOVE = 14;
+  static constexpr uint32_t LEAST = (127u - 60u) << 23;
   static __device__ __forceinline__ V bits(uint32_t w) { return *reinterpret_cast<const V*>(&w); }
-  static __device__ __forceinline__ V row_factor(uint32_t d) { return bits(((127u + 112u - d) << 7) * 0x10001u); }  // 2^(112 - d)
-  static __device__ __forceinline__ uint32_t column_factor(int k) { return (127 + max(0, min(100, k))) << 7; }
+  static __device__ __forceinline__ V row_factor(int k) { return bits(((127u + 112u + k) << 7) * 0x10001u); }  // 2^(112 + k)
+  static __device__ __forceinline__ uint32_t column_factor(int k) { return (127 + max(-ABOVE, min(100, k))) << 7; }
   static __device__ __forceinline__ V decode(uint32_t two, V f) {
     const uint32_t t = __byte_perm(two, 0u, 0x1404);
     return __hmul2(bits((t & 0x80008000u) | ((t >> 3) & 0x0fe00fe0u)), f);
@@ -71,8 +77,8 @@ struct Pairwise<true> {  // e5m2
 // A 128 x 128 tile to a CTA of 256 threads: 8 rows x 8 columns to a thread, 16 lanes to a row.
 struct TransposeTile {
   uint2 slot[128][16];     // transposed bytes: [column][8-row slot, swizzled]
-  uint32_t column[128];    // of column 8 g + j at j * 16 + g: its maximum, then its scale byte
-  uint32_t most, least;    // of the rows' scale bytes
+  uint32_t column[128];    // of column 8 g + j at j * 16 + g: its maximum
+  uint32_t byte[128];      // and its scale byte
 };
 struct TransposePart {
   long long c0, r0, rows4;
@@ -104,7 +110,7 @@ struct TransposePart {
   }
 };
 
-// Any scales: fills the tile and the columns' scale bytes (the columns are 0 on entry).
+// Any scales: fills the tile and the columns' scale bytes.
 template <bool E5M2>
 __device__ __noinline__ void transpose_any(const Fp8TransposeArgs& a, TransposeTile& tile) {
   constexpr int TOP = E5M2 ? 15 : 8;
@@ -113,6 +119,8 @@ __device__ __noinline__ void transpose_any(const Fp8TransposeArgs& a, TransposeT
   const TransposePart part(a);
   uint2 q[8];
   uint32_t s[8];
+  if (threadIdx.x < 128) tile.column[threadIdx.x] = 0u;
+  __syncthreads();
   part.load(a, q, s);
   uint32_t bad = 0u;  // bit j: column j holds an infinity or NaN
 #pragma unroll
@@ -154,7 +162,7 @@ __device__ __noinline__ void transpose_any(const Fp8TransposeArgs& a, TransposeT
     uint32_t byte = 127u;
     if (m == 0xffffffffu) byte = 255u;
     else if (m) byte = static_cast<uint32_t>(max(static_cast<int>((m + 0x1fffffu) >> 23) - 127 - TOP, 0));
-    tile.column[threadIdx.x] = byte;
+    tile.byte[threadIdx.x] = byte;
   }
   __syncthreads();
   // computed again: 128 keys do not fit into registers, and the compiler would keep them
@@ -162,7 +170,7 @@ __device__ __noinline__ void transpose_any(const Fp8TransposeArgs& a, TransposeT
   for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(q[i].x), "+r"(q[i].y), "+r"(s[i]));
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    const uint32_t b0 = tile.column[j * 16 + cg], b1 = tile.column[(j + 1) * 16 + cg];
+    const uint32_t b0 = tile.byte[j * 16 + cg], b1 = tile.byte[(j + 1) * 16 + cg];
     uint32_t out[2][2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -191,79 +199,62 @@ __global__ void __launch_bounds__(256, 4) fp8_transpose_kernel(const __grid_cons
   using V = typename Way::V;
   constexpr int TOP = E5M2 ? 15 : 8;
   __shared__ TransposeTile tile;
-  __shared__ uint32_t factor[64];  // of column pair 4 g + k at k * 16 + g: 2^(largest s - s')
+  __shared__ uint32_t factor[64];  // of column pair 4 g + k at k * 16 + g: 2^(first s - s')
   pdl_launch_dependents();
   if (threadIdx.x < 128) tile.column[threadIdx.x] = 0u;
-  if (threadIdx.x == 128) tile.most = 0u, tile.least = 255u;
   __syncthreads();
   pdl_wait();
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
   V h[8][4];
-  bool fast;
-  uint32_t base;
+  bool other = false;  // the other way
+  const uint32_t base = a.qs[fp8_scale_offset(blockIdx.x, blockIdx.y * 128LL, (a.rows + 3) & ~3LL)];
   {
     const TransposePart part(a);
     uint2 q[8];
     uint32_t s[8];
     part.load(a, q, s);
-    bool bad = false;
+    V m[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) bad |= Way::bad(q[i]);
-    if (bad) atomicMax(&tile.most, 255u);
-    if (cg == 0) {  // the same in the row's 16 lanes
-      uint32_t hi = 0u, lo = 255u;
+    for (int k = 0; k < 4; ++k) m[k] = Way::bits(0u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < part.nr) hi = max(hi, s[i]), lo = min(lo, s[i]);
-      atomicMax(&tile.most, hi);
-      atomicMin(&tile.least, lo);
-    }
-    __syncthreads();
-    base = tile.most;
-    fast = base - tile.least <= Way::SPREAD && base != 255u;
-    if (fast) {
-      V m[4];
+    for (int i = 0; i < 8; ++i) {
+      const int d = i < part.nr ? static_cast<int>(s[i]) - static_cast<int>(base) : 0;
+      const bool zero = ((q[i].x | q[i].y) & 0x7f7f7f7fu) == 0u;  // zeros' scales, which are 1, are as good as any
+      other |= (!zero && (d < -Way::BELOW || d > Way::ABOVE)) || s[i] == 255u || Way::bad(q[i]);
+      const V f = Way::row_factor(max(-Way::BELOW, min(Way::ABOVE, d)));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m[k] = Way::bits(0u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const V f = Way::row_factor(i < part.nr ? base - s[i] : 0u);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          h[i][k] = Way::decode((k < 2 ? q[i].x : q[i].y) >> (16 * (k & 1)), f);
-          m[k] = __hmax2_nan(m[k], __habs2(h[i][k]));
-        }
-      }
-      const bool up = threadIdx.x & 16;  // the half-warps hold other rows of the same columns: each takes two words of four on
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const V keep = up ? m[k + 2] : m[k], give = up ? m[k] : m[k + 2];
-        const float2 v = Way::wide(__hmax2_nan(keep, __shfl_xor_sync(0xffffffffu, give, 16)));
-        const int j = 2 * k + (up ? 4 : 0);
-        atomicMax(&tile.column[j * 16 + cg], abs_bits(v.x));
-        atomicMax(&tile.column[(j + 1) * 16 + cg], abs_bits(v.y));
+      for (int k = 0; k < 4; ++k) {
+        h[i][k] = Way::decode((k < 2 ? q[i].x : q[i].y) >> (16 * (k & 1)), f);
+        m[k] = __hmax2_nan(m[k], __habs2(h[i][k]));
       }
     }
-  }
-  if (fast) {
-    __syncthreads();
-    const uint32_t mine = threadIdx.x < 128 ? tile.column[threadIdx.x] : 0u;
-    fast = !__syncthreads_or(mine != 0u && mine < Way::LEAST);
-    if (threadIdx.x < 128) {
-      uint32_t byte = 127u;
-      if (mine >= 0x7f800000u) byte = 255u;
-      else if (mine) byte = static_cast<uint32_t>(max(static_cast<int>((mine + 0x1fffffu) >> 23) - TOP + static_cast<int>(base) - 127, 0));
-      tile.column[threadIdx.x] = fast ? byte : 0u;
-      const int j = threadIdx.x / 16, g = threadIdx.x % 16;  // the factor of a column of zeros or NaN: any
-      reinterpret_cast<unsigned short*>(factor)[((j / 2) * 16 + g) * 2 + (j & 1)] =
-          static_cast<unsigned short>(Way::column_factor(static_cast<int>(base) - static_cast<int>(byte)));
+    const bool up = threadIdx.x & 16;  // the half-warps hold other rows of the same columns: each takes two words of four on
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const V keep = up ? m[k + 2] : m[k], give = up ? m[k] : m[k + 2];
+      const float2 v = Way::wide(__hmax2_nan(keep, __shfl_xor_sync(0xffffffffu, give, 16)));
+      const int j = 2 * k + (up ? 4 : 0);
+      atomicMax(&tile.column[j * 16 + cg], abs_bits(v.x));
+      atomicMax(&tile.column[(j + 1) * 16 + cg], abs_bits(v.y));
     }
-    __syncthreads();
   }
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const uint32_t mine = tile.column[threadIdx.x];
+    other |= mine != 0u && mine < Way::LEAST;
+    uint32_t byte = 127u;
+    if (mine >= 0x7f800000u) byte = 255u;
+    else if (mine) byte = static_cast<uint32_t>(max(static_cast<int>((mine + 0x1fffffu) >> 23) - TOP + static_cast<int>(base) - 127, 0));
+    tile.byte[threadIdx.x] = byte;
+    const int j = threadIdx.x / 16, g = threadIdx.x % 16;  // the factor of a column of zeros or NaN: any
+    reinterpret_cast<unsigned short*>(factor)[((j / 2) * 16 + g) * 2 + (j & 1)] =
+        static_cast<unsigned short>(Way::column_factor(static_cast<int>(base) - static_cast<int>(byte)));
+  }
+  const bool fast = !__syncthreads_or(other);
   if (fast) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      const uint32_t b0 = tile.column[j * 16 + cg], b1 = tile.column[(j + 1) * 16 + cg];
+      const uint32_t b0 = tile.byte[j * 16 + cg], b1 = tile.byte[(j + 1) * 16 + cg];
       const V f = Way::bits(factor[j / 2 * 16 + cg]);
       uint32_t out[2][2];
 #pragma unroll
@@ -285,7 +276,7 @@ __global__ void __launch_bounds__(256, 4) fp8_transpose_kernel(const __grid_cons
   if (threadIdx.x < 128) {
     const long long c = blockIdx.x * 128LL + threadIdx.x % 16 * 8 + threadIdx.x / 16;
     if (c < cols4) {
-      a.qts[fp8_scale_offset(kbr, c, cols4)] = static_cast<uint8_t>(tile.column[threadIdx.x]);
+      a.qts[fp8_scale_offset(kbr, c, cols4)] = static_cast<uint8_t>(tile.byte[threadIdx.x]);
       if ((kbr + 1) * 128 >= a.rows)
         for (long long kb = kbr + 1; kb < kend; ++kb) a.qts[fp8_scale_offset(kb, c, cols4)] = 127;
     }
