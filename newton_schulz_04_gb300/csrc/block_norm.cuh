@@ -8,7 +8,7 @@
 
 namespace muon {
 
-// ---- a block of 128 columns to a warp
+// ---- a block of 128 columns to a warp: the widest rows
 // Rows of any alignment: lane l holds columns l, l + 32, l + 64 and l + 96 of a block, so that a warp's accesses are
 // 32 neighbours whatever the row's first address, and a block's largest magnitude is one reduction of the warp.
 template <typename T>
@@ -66,7 +66,6 @@ __device__ __forceinline__ void pad_blocks8(const muon_fp8_out& o, long long row
       for (long long r = rows; r < rows4; ++r) scale[fp8_scale_offset(kb, r, rows4)] = 127;
   }
 }
-
 
 // Sums over a CTA of W warps; every thread gets them.  `sh` alternates between two buffers: one barrier each.
 template <int W, int N>

@@ -11,8 +11,8 @@
 //
 // A ring of rows as in the forward kernel, one piece to a thread.  8191 x 4096 bf16 takes 92 us from e4m3 (4.7 TB/s, 70 % of the
 // copy rate) and 94 from bf16 (84 %): 16 warps of 128 registers on an SM issue 56 % of its slots, 56 instructions an element.
-// With scalars of fp32 it took 125, with choices at run time 120; two rows a turn, or the rows' factors and scales copied with
-// the rows, gained nothing.  Rows that start anywhere: 139 and 167 at 4095 columns.
+// With scalars of fp32 it took 125, with choices at run time 120; there two rows a turn, or the rows' factors and scales copied
+// with the rows, gained nothing.  Rows that start anywhere: 139 and 167 at 4095 columns.
 //
 // Compiled once for each type and alignment of rows (MUON_ROWS_T, MUON_ROWS_ANYWHERE).
 #include <cuda_runtime.h>
@@ -130,13 +130,13 @@ __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int by
                : "memory");
 }
 
-// A thread's slots: S rows of dy, dh, x, h and gate, a piece each; kept 8-bit ones take E bytes instead of 16.
+// A thread's slots: S times ROWS rows of dy, dh, x, h and gate, a piece each; kept 8-bit ones take E bytes instead of 16.
 // ANYWHERE: of T, a warp's and a little more.
-template <typename T, int G, int S, bool KEPT8, bool ANYWHERE>
+template <typename T, int G, int S, int ROWS, bool KEPT8, bool ANYWHERE>
 struct GradRing {
   static constexpr int TH = G < 128 ? 128 : G, LANES = G < 32 ? G : 32;
   static constexpr int E = 16 / static_cast<int>(sizeof(T)), WIDE = KEPT8 ? 2 : 5, ARRAY = ANYWHERE ? TH / 32 * kWarpSlot<LANES> : TH * 16;
-  static constexpr int STAGE = WIDE * ARRAY + (5 - WIDE) * TH * E, BYTES = S * STAGE;
+  static constexpr int STAGE = WIDE * ARRAY + (5 - WIDE) * TH * E, BYTES = S * ROWS * STAGE;
   uint8_t* base;
   __device__ __forceinline__ uint8_t* at(int slot, int arr) const {
     uint8_t* stage = base + slot * STAGE;
@@ -145,20 +145,20 @@ struct GradRing {
   }
 };
 
-// CL CTAs of a cluster to a row, G threads of each with a piece of 16 bytes, a ring of S rows.  KEPT: of x, h and an
-// element's gate; 0: T, 1: e4m3, 2: e5m2.  GATE: a gate of every element.  Both compiled apart: chosen at run time they
-// cost 8192 x 4096 a third more instructions, in pieces too small to be overlapped.
-template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE, bool ANYWHERE>
+// CL CTAs of a cluster to a row, G threads of each with a piece of 16 bytes, ROWS rows at a time, a ring S times as deep.
+// KEPT: of x, h and an element's gate; 0: T, 1: e4m3, 2: e5m2.  GATE: a gate of every element.  Both compiled apart: chosen
+// at run time they cost 8192 x 4096 a third more instructions, in pieces too small to be overlapped.
+template <typename T, int G, int S, int ROWS, int MINB, int CL, int KEPT, bool GATE, bool ANYWHERE>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
     block_norm_grad_ring_kernel(const muon_block_norm_grad_args a, float* partial) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
   constexpr int DY = 0, DH = 1, X = 2, H = 3, GA = 4;
   using P = Pairs<T>;
   using K = std::conditional_t<KEPT != 0, uint8_t, T>;
-  using Slots = GradRing<T, G, S, KEPT != 0, ANYWHERE>;
+  using Slots = GradRing<T, G, S, ROWS, KEPT != 0, ANYWHERE>;
   constexpr int E = P::E, N = P::N;
   extern __shared__ __align__(16) uint8_t ring_smem[];
-  __shared__ RowSums3<G, TH, CL> sums;
+  __shared__ RowSums3<G, TH, CL, ROWS> sums;
   const Slots ring{ring_smem};
   const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int t = threadIdx.x % G, rr = threadIdx.x / G, cols = static_cast<int>(a.cols);
@@ -177,25 +177,29 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   const K* fh = static_cast<const K*>(a.h) + row0 * a.ldh + KBEGIN * col;
   const K* fg = static_cast<const K*>(a.gate) + (GATE ? row0 * a.ldg + KBEGIN * col : 0);
   auto fetch = [&](int slot) {
-    if (frow < a.rows) {
-      const auto plain = [&](int arr, const T* row, const void* matrix, bool there) {
-        if constexpr (ANYWHERE)
-          fetch_anywhere<T, Slots::LANES>(ring.at(slot, arr), row, rank * G + t, there ? cols : 0, static_cast<const uint8_t*>(matrix));
-        else copy16(smem_u32(ring.at(slot, arr)), row, there ? n * static_cast<int>(sizeof(T)) : 0);
-      };
-      const auto kept = [&](int arr, const K* row, const void* matrix) {
-        if constexpr (KEPT == 0) plain(arr, row, matrix, true);
-        else copy_small<E>(smem_u32(ring.at(slot, arr)), row, n);
-      };
-      plain(DY, fdy, a.dy, true);
-      plain(DH, fdh, dh, a.dh != nullptr);
-      kept(X, fx, a.x);
-      kept(H, fh, a.h);
-      if (GATE) kept(GA, fg, a.gate);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int at = slot * ROWS + r;
+      if (frow < a.rows) {
+        const auto plain = [&](int arr, const T* row, const void* matrix, bool there) {
+          if constexpr (ANYWHERE)
+            fetch_anywhere<T, Slots::LANES>(ring.at(at, arr), row, rank * G + t, there ? cols : 0, static_cast<const uint8_t*>(matrix));
+          else copy16(smem_u32(ring.at(at, arr)), row, there ? n * static_cast<int>(sizeof(T)) : 0);
+        };
+        const auto kept = [&](int arr, const K* row, const void* matrix) {
+          if constexpr (KEPT == 0) plain(arr, row, matrix, true);
+          else copy_small<E>(smem_u32(ring.at(at, arr)), row, n);
+        };
+        plain(DY, fdy, a.dy, true);
+        plain(DH, fdh, dh, a.dh != nullptr);
+        kept(X, fx, a.x);
+        kept(H, fh, a.h);
+        if (GATE) kept(GA, fg, a.gate);
+      }
+      frow += step, fdy += step * a.lddy, fdh += step * lddh, fx += step * a.ldx, fh += step * a.ldh;
+      if (GATE) fg += step * a.ldg;
     }
     cp_async_commit();
-    frow += step, fdy += step * a.lddy, fdh += step * lddh, fx += step * a.ldx, fh += step * a.ldh;
-    if (GATE) fg += step * a.ldg;
   };
   // row: for its address modulo 16
   const auto read = [&](int slot, int arr, const void* matrix, long long ld, long long row, P& p) {
@@ -249,7 +253,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
     prx += step, prh += step, so += 4 * step;
     return r;
   };
-  RowHead next = head(row0);
+  RowHead next[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) next[r] = head(row0 + r * step);
   const float inv_cols = 1.f / static_cast<float>(cols);
   T* pdr = static_cast<T*>(a.dresidual) + row0 * a.lddr + BEGIN * col;
   T* pdx = static_cast<T*>(a.dx) + row0 * a.lddx + BEGIN * col;
@@ -260,60 +266,73 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   };
   const bool gate_out = row_gated && a.dgate && t == 0 && rank == 0;
   int slot = 0, turn = 0;
-  for (long long row = row0; row - rr < a.rows; row += step, ++turn) {
-    const bool live = R == 1 || row < a.rows;
-    if (row - rr + step >= a.rows) pdl_launch_dependents();  // the last row, as in the forward kernel
-    const RowHead now = next;
-    next = head(row + step);
+  for (long long row = row0; row - rr < a.rows; row += ROWS * step, ++turn) {
+    if (row - rr + ROWS * step >= a.rows) pdl_launch_dependents();  // the last turn, as in the forward kernel
+    RowHead now[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) now[r] = next[r], next[r] = head(row + (ROWS + r) * step);
     if (ANYWHERE) __syncwarp();
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
     if (ANYWHERE) __syncwarp();
-    P d, u, sig, xn, hn;
-    read(slot, DY, a.dy, a.lddy, row, d);
-    read(slot, DH, dh, lddh, row, u);
-    read_kept(slot, X, a.x, a.ldx, row, xn);
-    read_kept(slot, H, a.h, a.ldh, row, hn);
-    if (GATE) read_kept(slot, GA, a.gate, a.ldg, row, sig);
-    if (R > 1 && !live) {  // the slot holds another row's remains
+    P u[ROWS], sig[ROWS], xn[ROWS], hn[ROWS];
+    float sum[ROWS][3], row_sig[ROWS];
 #pragma unroll
-      for (int i = 0; i < N; ++i) d.v[i] = xn.v[i] = hn.v[i] = u.v[i] = sig.v[i] = both(0.f);
-    }
-    const float2 xf = both(KEPT ? now.rx * fp8_scale_value(now.xs) : now.rx), hf = both(KEPT ? now.rh * fp8_scale_value(now.hs) : now.rh);
-    const float2 gf = both(KEPT ? fp8_scale_value(now.gs) : 1.f);
-    const float row_sig = row_gated ? sigmoid2<float>(both(now.gate)).x : 1.f;
-    float2 s0 = both(0.f), s1 = s0, s2 = s0;
+    for (int r = 0; r < ROWS; ++r) {
+      const int at = slot * ROWS + r;
+      const long long here = row + r * step;
+      P d;
+      read(at, DY, a.dy, a.lddy, here, d);
+      read(at, DH, dh, lddh, here, u[r]);
+      read_kept(at, X, a.x, a.ldx, here, xn[r]);
+      read_kept(at, H, a.h, a.ldh, here, hn[r]);
+      if (GATE) read_kept(at, GA, a.gate, a.ldg, here, sig[r]);
+      if ((R > 1 || ROWS > 1) && here >= a.rows) {  // the slot holds another row's remains
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      hn.v[i] = mul2(hn.v[i], hf);
-      xn.v[i] = mul2(xn.v[i], xf);
-      const float2 ad = mul2(d.v[i], w2[i]);
-      u.v[i] = fma2(both(now.rh), ad, u.v[i]);
-      sig.v[i] = GATE ? sigmoid2<T>(KEPT ? mul2(sig.v[i], gf) : sig.v[i]) : both(row_sig);
-      const float2 e = mul2(mul2(sig.v[i], w1[i]), xn.v[i]);
-      s0 = fma2(ad, hn.v[i], s0);
-      s1 = fma2(u.v[i], e, s1);
-      s2 = fma2(hn.v[i], e, s2);
-      dpre[i] = fma2(d.v[i], hn.v[i], dpre[i]);
+        for (int i = 0; i < N; ++i) d.v[i] = xn[r].v[i] = hn[r].v[i] = u[r].v[i] = sig[r].v[i] = both(0.f);
+      }
+      const float2 xf = both(KEPT ? now[r].rx * fp8_scale_value(now[r].xs) : now[r].rx);
+      const float2 hf = both(KEPT ? now[r].rh * fp8_scale_value(now[r].hs) : now[r].rh);
+      const float2 gf = both(KEPT ? fp8_scale_value(now[r].gs) : 1.f);
+      row_sig[r] = row_gated ? sigmoid2<float>(both(now[r].gate)).x : 1.f;
+      float2 s0 = both(0.f), s1 = s0, s2 = s0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        hn[r].v[i] = mul2(hn[r].v[i], hf);
+        xn[r].v[i] = mul2(xn[r].v[i], xf);
+        const float2 ad = mul2(d.v[i], w2[i]);
+        u[r].v[i] = fma2(both(now[r].rh), ad, u[r].v[i]);
+        sig[r].v[i] = GATE ? sigmoid2<T>(KEPT ? mul2(sig[r].v[i], gf) : sig[r].v[i]) : both(row_sig[r]);
+        const float2 e = mul2(mul2(sig[r].v[i], w1[i]), xn[r].v[i]);
+        s0 = fma2(ad, hn[r].v[i], s0);
+        s1 = fma2(u[r].v[i], e, s1);
+        s2 = fma2(hn[r].v[i], e, s2);
+        dpre[i] = fma2(d.v[i], hn[r].v[i], dpre[i]);
+      }
+      sum[r][0] = total(s0), sum[r][1] = total(s1), sum[r][2] = total(s2);
     }
-    float sum[3] = {total(s0), total(s1), total(s2)};
     sums(sum, turn);
-    const float k1 = sum[0] * inv_cols * now.rh, along = sum[1] - k1 * sum[2], k2 = along * inv_cols;
-    if (gate_out && live) static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>((1.f - row_sig) * along);
-    P dr, dx, dg;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 v = fma2(both(-k1), hn.v[i], u.v[i]), td = mul2(v, sig.v[i]), b = mul2(td, w1[i]);
-      sx[i] = fma2(td, xn.v[i], sx[i]);
-      dr.v[i] = mul2(both(a.alpha), v);
-      dx.v[i] = mul2(both(now.rx), fma2(both(-k2), xn.v[i], b));
-      if (GATE) dg.v[i] = mul2(fma2(both(-1.f), sig.v[i], both(1.f)), mul2(b, xn.v[i]));
+    for (int r = 0; r < ROWS; ++r) {
+      const long long here = row + r * step;
+      const bool live = (R == 1 && ROWS == 1) || here < a.rows;
+      const float k1 = sum[r][0] * inv_cols * now[r].rh, along = sum[r][1] - k1 * sum[r][2], k2 = along * inv_cols;
+      if (gate_out && live) static_cast<T*>(a.dgate)[here * a.lddgate] = from_f32<T>((1.f - row_sig[r]) * along);
+      P dr, dx, dg;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float2 v = fma2(both(-k1), hn[r].v[i], u[r].v[i]), td = mul2(v, sig[r].v[i]), b = mul2(td, w1[i]);
+        sx[i] = fma2(td, xn[r].v[i], sx[i]);
+        dr.v[i] = mul2(both(a.alpha), v);
+        dx.v[i] = mul2(both(now[r].rx), fma2(both(-k2), xn[r].v[i], b));
+        if (GATE) dg.v[i] = mul2(fma2(both(-1.f), sig[r].v[i], both(1.f)), mul2(b, xn[r].v[i]));
+      }
+      put(pdr, live && a.dresidual, dr);
+      put(pdx, live && a.dx, dx);
+      if (GATE) put(pdg, live && a.dgate, dg);
+      pdr += step * a.lddr, pdx += step * a.lddx;
+      if (GATE) pdg += step * a.lddgate;
     }
-    put(pdr, live && a.dresidual, dr);
-    put(pdx, live && a.dx, dx);
-    if (GATE) put(pdg, live && a.dgate, dg);
-    pdr += step * a.lddr, pdx += step * a.lddx;
-    if (GATE) pdg += step * a.lddgate;
     slot = slot + 1 == S ? 0 : slot + 1;
   }
   if (!partial) return;
@@ -350,15 +369,15 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
 // The kernels add up rows of `partial` for at most this many CTAs (or clusters).
 static int most_ctas(int sms) { return kBlockNormCtasPerSm * sms; }
 
-template <typename T, int G, int S, int MINB, int CL, int KEPT, bool GATE, bool ANYWHERE>
+template <typename T, int G, int S, int ROWS, int MINB, int CL, int KEPT, bool GATE, bool ANYWHERE>
 static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
-  constexpr int smem = GradRing<T, G, S, KEPT != 0, ANYWHERE>::BYTES;
+  constexpr int smem = GradRing<T, G, S, ROWS, KEPT != 0, ANYWHERE>::BYTES;
   static_assert(smem * MINB <= 224 * 1024, "shared memory of an SM");
   static_assert(MINB <= kBlockNormCtasPerSm, "rows of partial");
   static bool done[64] = {false};
   static int known[64] = {0};
-  const auto kernel = block_norm_grad_ring_kernel<T, G, S, MINB, CL, KEPT, GATE, ANYWHERE>;
+  const auto kernel = block_norm_grad_ring_kernel<T, G, S, ROWS, MINB, CL, KEPT, GATE, ANYWHERE>;
   cudaError_t e = smem_limit(kernel, smem, done);
   if (e != cudaSuccess) return e;
   int most = MINB * sms;
@@ -377,25 +396,29 @@ template <typename T, int KEPT, bool GATE, bool ANYWHERE>
 static cudaError_t dispatch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));
   const int pieces = static_cast<int>((a.cols + E - 1) / E);
-  const auto go = [&](auto threads, auto depth, auto ctas_per_sm, auto cluster) {
-    return launch_ring<T, decltype(threads)::value, decltype(depth)::value, decltype(ctas_per_sm)::value, decltype(cluster)::value, KEPT,
-                       GATE, ANYWHERE>(a, partial, sms, ctas, st);
+  const auto go = [&](auto threads, auto depth, auto rows, auto ctas_per_sm, auto cluster) {
+    return launch_ring<T, decltype(threads)::value, decltype(depth)::value, decltype(rows)::value, decltype(ctas_per_sm)::value,
+                       decltype(cluster)::value, KEPT, GATE, ANYWHERE>(a, partial, sms, ctas, st);
   };
-  if (pieces <= 16) return go(Int<16>(), Int<4>(), Int<4>(), Int<1>());
-  if (pieces <= 32) return go(Int<32>(), Int<4>(), Int<4>(), Int<1>());
-  if (pieces <= 64) return go(Int<64>(), Int<4>(), Int<4>(), Int<1>());
-  if (pieces <= 128) return go(Int<128>(), Int<4>(), Int<4>(), Int<1>());
-  if (pieces <= 256) return go(Int<256>(), Int<4>(), Int<2>(), Int<1>());
-  if (pieces <= 512) return go(Int<512>(), Int<4>(), Int<1>(), Int<1>());
-  // 33.5M elements at 8192 columns: from 8 bits 126 us in clusters of four small CTAs, two of which share an SM and overlap
-  // their exchanges, 139 in clusters of two large ones; from 16 bits 165 and 144
-  if constexpr (KEPT != 0) {
-    if (pieces <= 1024) return go(Int<256>(), Int<5>(), Int<2>(), Int<4>());
+  if (pieces <= 16) return go(Int<16>(), Int<4>(), Int<1>(), Int<4>(), Int<1>());
+  if (pieces <= 32) return go(Int<32>(), Int<4>(), Int<1>(), Int<4>(), Int<1>());
+  if (pieces <= 64) return go(Int<64>(), Int<4>(), Int<1>(), Int<4>(), Int<1>());
+  if (pieces <= 128) return go(Int<128>(), Int<4>(), Int<1>(), Int<4>(), Int<1>());
+  if (pieces <= 256) return go(Int<256>(), Int<4>(), Int<1>(), Int<2>(), Int<1>());
+  if (pieces <= 512) return go(Int<512>(), Int<4>(), Int<1>(), Int<1>(), Int<1>());
+  // Rows over a cluster, which waits for its exchange: two rows at a time share it where their values fit the registers.
+  // 33.5M elements at 8192 and 16384 columns: 16-bit rows 115 and 124 us (one row at a time 141 and 157), fp32 241 and 288
+  // (270 and 329), fp32 from 8 bits 216 and 282 (243 and 292).  16-bit rows from 8 bits spill: 126 and 150, two at a time
+  // 140 and 159; at 8192 columns they take clusters of four small CTAs, two of which share an SM, against two large ones' 139
+  if constexpr (KEPT == 0 || sizeof(T) == 4) {
+    if (pieces <= 1024) return go(Int<512>(), Int<2>(), Int<2>(), Int<1>(), Int<2>());
+    if (pieces <= 2048) return go(Int<512>(), Int<2>(), Int<2>(), Int<1>(), Int<4>());
+    return go(Int<512>(), Int<2>(), Int<2>(), Int<1>(), Int<8>());
   } else {
-    if (pieces <= 1024) return go(Int<512>(), Int<5>(), Int<1>(), Int<2>());
+    if (pieces <= 1024) return go(Int<256>(), Int<5>(), Int<1>(), Int<2>(), Int<4>());
+    if (pieces <= 2048) return go(Int<512>(), Int<5>(), Int<1>(), Int<1>(), Int<4>());
+    return go(Int<512>(), Int<5>(), Int<1>(), Int<1>(), Int<8>());
   }
-  if (pieces <= 2048) return go(Int<512>(), Int<5>(), Int<1>(), Int<4>());
-  return go(Int<512>(), Int<5>(), Int<1>(), Int<8>());
 }
 
 template <typename T, bool ANYWHERE>

@@ -322,6 +322,7 @@ static cudaError_t dispatch_ring(const muon_block_norm_args& a, int sms, cudaStr
   if (pieces <= 256) return launch_ring<T, 128, 2, 5, 3, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
   if (pieces <= 512) return launch_ring<T, 256, 2, 3, 2, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
   if (pieces <= 1024) return launch_ring<T, 512, 2, 3, 1, 1, GATE, E4M3, ANYWHERE>(a, sms, st);
+  // four pieces to a thread take the longest to compile: the general kernel serves e4m3 too
   if (pieces <= 2048) return launch_ring<T, 512, 4, 2, 1, 1, GATE, false, ANYWHERE>(a, sms, st);
   if (pieces <= 4096) return launch_ring<T, 512, 4, 2, 1, 2, GATE, false, ANYWHERE>(a, sms, st);
   return launch_ring<T, 512, 4, 2, 1, 4, GATE, false, ANYWHERE>(a, sms, st);

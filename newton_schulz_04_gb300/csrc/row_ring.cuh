@@ -163,50 +163,67 @@ struct RowSum {
   }
 };
 
-// Three sums at once: they part company as the lanes that hold them halve, so that a quarter of a warp (or half warp) ends
-// with one of them; half of the instructions of three sums in all lanes.
-template <int G, int TH, int CL>
+// Three sums of each of ROWS rows at once: they part company as the lanes that hold them halve, so that a quarter of a warp
+// (or half warp) ends with one of them; half of the instructions of three sums in all lanes.
+template <int G, int TH, int CL, int ROWS>
 struct RowSums3 {
   static constexpr int WARPS = TH / 32, W = G < 32 ? 1 : G / 32, LANES = G < 32 ? G : 32, Q = LANES / 4;
   static_assert(CL == 1 || (G == TH && CL <= Q), "rows of whole CTAs");
-  alignas(16) float v[2][3][CL * WARPS];
-  __device__ __forceinline__ void operator()(float (&s)[3], int turn) {
-    const int lane = threadIdx.x % LANES, mine = lane / Q;  // lanes of quarter 0: the first sum, 1 and 3: the second, 2: the third
-    const bool up = lane & (2 * Q), odd = lane & Q;
-    const float k = (up ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, up ? s[0] : s[2], 2 * Q);
-    const float m = s[1] + __shfl_xor_sync(0xffffffffu, s[1], 2 * Q);
-    float f = (odd ? m : k) + __shfl_xor_sync(0xffffffffu, odd ? k : m, Q);
-    auto quarter = [&] {
+  alignas(16) float v[2][ROWS][3][CL * WARPS];
+  static __device__ __forceinline__ float quarter(float f) {
 #pragma unroll
-      for (int o = Q / 2; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
-    };
-    quarter();
+    for (int o = Q / 2; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+    return f;
+  }
+  __device__ __forceinline__ void operator()(float (&s)[ROWS][3], int turn) {
+    const int lane = threadIdx.x % LANES, at = lane % Q;  // lanes of quarter 0: the first sum, 1 and 3: the second, 2: the third
+    const bool up = lane & (2 * Q), odd = lane & Q, one = lane / Q < 3;
+    const int warp = threadIdx.x / 32, sum = odd ? 1 : up ? 2 : 0;
+    float f[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const float k = (up ? s[r][2] : s[r][0]) + __shfl_xor_sync(0xffffffffu, up ? s[r][0] : s[r][2], 2 * Q);
+      const float m = s[r][1] + __shfl_xor_sync(0xffffffffu, s[r][1], 2 * Q);
+      f[r] = quarter((odd ? m : k) + __shfl_xor_sync(0xffffffffu, odd ? k : m, Q));
+    }
     if constexpr (G > 32 || CL > 1) {
-      float(&b)[3][CL * WARPS] = v[turn & 1];
-      const int warp = threadIdx.x / 32, sum = odd ? 1 : up ? 2 : 0, at = lane % Q;
+      float(&b)[ROWS][3][CL * WARPS] = v[turn & 1];
       if constexpr (CL == 1) {
-        if (at == 0 && mine < 3) b[sum][warp] = f;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+          if (at == 0 && one) b[r][sum][warp] = f[r];
         __syncthreads();
         const int first = (threadIdx.x / G) * W;
-        f = at < W ? b[sum][first + at] : 0.f;
 #pragma unroll
-        for (int k2 = Q; k2 < W; k2 += Q) f += b[sum][first + k2 + at];
+        for (int r = 0; r < ROWS; ++r) {
+          f[r] = at < W ? b[r][sum][first + at] : 0.f;
+#pragma unroll
+          for (int k = Q; k < W; k += Q) f[r] += b[r][sum][first + k + at];
+        }
       } else {
-        if (at < CL && mine < 3)  // a lane to a CTA of the cluster
-          st_shared_cluster(mapa_cluster(&b[sum][cluster_ctarank() * WARPS + warp], at), __float_as_int(f));
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+          if (at < CL && one)  // a lane to a CTA of the cluster
+            st_shared_cluster(mapa_cluster(&b[r][sum][cluster_ctarank() * WARPS + warp], at), __float_as_int(f[r]));
         __syncwarp();
         cluster_sync();
-        f = 0.f;
 #pragma unroll
-        for (int k2 = 0; k2 < CL * WARPS; k2 += 4 * Q) {
-          const float4 p = k2 + 4 * at < CL * WARPS ? *reinterpret_cast<const float4*>(&b[sum][k2 + 4 * at]) : make_float4(0.f, 0.f, 0.f, 0.f);
-          f += (p.x + p.y) + (p.z + p.w);
+        for (int r = 0; r < ROWS; ++r) {
+          f[r] = 0.f;
+#pragma unroll
+          for (int k = 0; k < CL * WARPS; k += 4 * Q) {
+            const float4 p = k + 4 * at < CL * WARPS ? *reinterpret_cast<const float4*>(&b[r][sum][k + 4 * at]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            f[r] += (p.x + p.y) + (p.z + p.w);
+          }
         }
       }
-      quarter();
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) f[r] = quarter(f[r]);
     }
 #pragma unroll
-    for (int n = 0; n < 3; ++n) s[n] = __shfl_sync(0xffffffffu, f, n * Q, LANES);
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int n = 0; n < 3; ++n) s[r][n] = __shfl_sync(0xffffffffu, f[r], n * Q, LANES);
   }
 };
 

@@ -387,6 +387,16 @@ def test_block_norm_wide_rows_more_than_clusters(mm, cols, kept):
     check_norm_grad(mm, 21, 170, cols, torch.bfloat16, "element", True, kept=kept)
 
 
+# two rows at a time in a cluster: several turns, of which some end in one row or none, from aligned rows and others
+@gpu
+@pytest.mark.parametrize("dtype,cols,kept", [(torch.bfloat16, 8_192, None), (torch.float16, 16_390, None), (torch.float32, 4_096, None),
+                                             (torch.float32, 4_104, "e4m3"), (torch.float32, 8_192, "e5m2"), (torch.float32, 16_384, None)])
+@pytest.mark.parametrize("rows", [1, 39, 331])
+def test_block_norm_backward_of_pairs_of_rows(mm, dtype, cols, kept, rows):
+    check_norm_grad(mm, 22, rows, cols, dtype, "element", True, kept=kept)
+    check_norm_grad(mm, 23, rows, cols, dtype, "row", False, kept=kept, pad=3, offset=1)
+
+
 def strided(t, pad, offset=0):
     """t's values on the GPU in rows with `pad` more elements, `offset` elements into the allocation."""
     rows, cols = t.shape
