@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
           cm[2][2 * i + 1] = largest3(cm[2][2 * i + 1], y_before[i].y, y.y);
         }
       }
-      m[r] = __byte_perm(__float_as_uint(mg) + 0xffffu, __float_as_uint(mu) + 0xffffu, 0x7632);
+      m[r] = upper_halves(__float_as_uint(mg), __float_as_uint(mu));
       if (r % 2 == 1) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -250,11 +250,17 @@ __device__ __forceinline__ uint4 read_anywhere(const uint8_t* slot, int off) {
   }
 }
 
+// The fp32 bits of two magnitudes, a in the lower half, as words of 16 bits that order them and give the same scale bytes: the
+// upper bits, rounded up.  A scale byte is the exponent field of bits + 0x1fffff, and the only border within a binade,
+// 0x600000, is a multiple of 2^16.  Finite magnitudes stay below infinity: those above 0x7f7f0000 have the byte of 0x7f7f0000.
+__device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
+  constexpr uint32_t LAST = 0x7f7fffffu;  // FLT_MAX; infinity and NaN are above it and stay as they are
+  return __byte_perm(max(__viaddmin_u32(a, 0xffffu, LAST), a), max(__viaddmin_u32(b, 0xffffu, LAST), b), 0x7632);
+}
+
 // Scales of up to four matrices' blocks, whose 128 columns lie in LANES = 16 or 32 neighbouring lanes.  The largest
-// magnitudes travel as the upper 16 bits of their fp32 bits, rounded up, two to a word: a scale byte is the exponent field of
-// bits + 0x1fffff, and the only border within a binade, 0x600000, is a multiple of 2^16, so that it comes out the same.  A
-// quarter of the lanes ends up with one matrix each, computes its byte, keeps it and hands the others its inverse: a third of
-// the instructions of four exchanges in all lanes.
+// magnitudes travel two to a word.  A quarter of the lanes ends up with one matrix each, computes its byte, keeps it and hands
+// the others its inverse: a third of the instructions of four exchanges in all lanes.
 template <int LANES>
 struct Scales4 {
   static constexpr int Q = LANES / 4;
@@ -264,8 +270,7 @@ struct Scales4 {
   // m: fp32 bits of the lane's largest magnitudes; top: 8 or 15 for the matrix mine() says
   __device__ __forceinline__ Scales4(const uint32_t (&m)[4], int top) {
     const int lane = threadIdx.x % 32;
-    const uint32_t ab = __byte_perm(m[0] + 0xffffu, m[1] + 0xffffu, 0x7632);
-    const uint32_t cd = __byte_perm(m[2] + 0xffffu, m[3] + 0xffffu, 0x7632);
+    const uint32_t ab = upper_halves(m[0], m[1]), cd = upper_halves(m[2], m[3]);
     const bool up = lane & (2 * Q);
     uint32_t w = __vmaxu2(up ? cd : ab, __shfl_xor_sync(0xffffffffu, up ? ab : cd, 2 * Q));
 #pragma unroll
