@@ -57,6 +57,12 @@ __device__ __forceinline__ uint2 fp8_pack8(const float (&v)[8], float inv) {
 __device__ __forceinline__ float fp8_scale_value(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7fffffffu : byte == 0u ? 0x400000u : byte << 23);
 }
+// The same for reading values back that are used as they are: FLT_MAX and its neighbours are kept as 2^128, which under this
+// factor, 2^-24 less for the scales that reach it, is FLT_MAX again.
+template <bool E5M2>
+__device__ __forceinline__ float fp8_finite_scale_value(uint32_t byte) {
+  return byte > 254u - (E5M2 ? 15u : 8u) && byte != 255u ? __uint_as_float((byte << 23) - 1u) : fp8_scale_value(byte);
+}
 // Two 8-bit values as fp32, exactly; the first is the low byte.  (e5m2 is fp16 without its last 8 bits.)
 template <bool E5M2>
 __device__ __forceinline__ float2 fp8_unpack2(uint32_t two) {

@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
   if (KEPT && lane % 16 < rows_here)
     kept_scale = static_cast<const uint8_t*>(lane < 16 ? a.gate_scale : a.up_scale)[fp8_scale_offset(kbc, r0 + lane % 16, rows4)];
   __shared__ float kept_values[kTileWarps][32];
-  kept_values[warp][lane] = fp8_scale_value(kept_scale);
+  kept_values[warp][lane] = fp8_finite_scale_value<KEPT == 2>(kept_scale);
   const int n = static_cast<int>(max(0LL, min(4LL, left - lane * 4)));  // the lane's columns
   const long long col = c00 + lane * 4;
   const bool store8 = col < ((cols + 15) & ~15LL);
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(256) gated_grad_dense_kernel(const muon_gated_
         const uint8_t* q = static_cast<const uint8_t*>(matrix) + row * ld + col;
         float s = 1.f;
         if (in && left > 0) {
-          s = fp8_scale_value(static_cast<const uint8_t*>(scale)[fp8_scale_offset(kb, row, rows4)]);
+          s = fp8_finite_scale_value<KEPT == 2>(static_cast<const uint8_t*>(scale)[fp8_scale_offset(kb, row, rows4)]);
           if (left >= E) {
             if constexpr (E == 8) *reinterpret_cast<uint2*>(b) = *reinterpret_cast<const uint2*>(q);
             else *reinterpret_cast<uint32_t*>(b) = *reinterpret_cast<const uint32_t*>(q);

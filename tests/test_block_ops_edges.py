@@ -75,3 +75,37 @@ def test_outputs_of_the_largest_finite_values(mm, fmt):
     n = mm.block_norm(*dev(torch.zeros(3, 1), torch.ones(3, 1), pre, pre), fp8=fmt)
     assert bool(torch.isfinite(n.y).all()) and float(n.y.min()) > TOP32[1]
     check8_exact(n.q, n.y.cpu(), fmt)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("cols", [256, 300])
+def test_gradient_from_checkpoints_of_the_largest_finite_values(mm, dtype, fmt, kind, cols):
+    """Gates at both ends of the type's range, and linear branches: their 8-bit copies stand for +-2^128, of which the
+    gradient's values are those of the largest finite number, within a rounding."""
+    lim = torch.finfo(dtype)
+    g, u, dy = (t.clone() for t in (torch.zeros(9, cols), torch.full((9, cols), 0.5), torch.full((9, cols), 0.5)))
+    g[1, :] = lim.min                          # shut, open, and beside them gates that 8 bits round to 0 under such a scale
+    g[2, ::3], g[3, 5], g[4, 130] = lim.min, lim.max, lim.max
+    g[7], g[8] = 1.0, gen(2, cols)
+    u[5], u[6, 1::2] = lim.max, lim.min
+    a = mm.gated_activation(*dev(g.to(dtype), u.to(dtype)), activation=kind, checkpoint=fmt)
+    kg, ku = (torch.where(t.abs() >= lim.max / 2, t.sign() * 2.0 ** 128, t.double()) for t in (g.double(), u.double()))
+    for t in (kg, ku):                         # what the copies stand for, of the values as they are here
+        block = torch.arange(cols) // 128
+        for r in range(9):
+            for b in range(int(block[-1]) + 1):
+                if float(t[r, block == b].abs().max()) > 1e38:
+                    t[r, (block == b) & (t[r].abs() < 1e38)] = 0.0
+    kg[8] = mm.fp8_quantize(g[8:].to(dtype).cuda(), fmt)[0].dequantize().cpu().double()[0]
+    wg, wu, _ = ref.gated_backward(dy, kg, ku, kind)
+    for fp8 in (None, "e5m2"):                 # the two kernels
+        d = mm.gated_activation_backward(dy.to(dtype).cuda(), a.kept, activation=kind, fp8=fp8)
+        u_, tol = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}[dtype], 64 * F24
+        close(d.dgate, wg, (u_ + tol) * wg.abs() + tol * 0.25 * ku.abs().clamp(max=1.0), "dgate")
+        close(d.dup, wu, (u_ + tol) * wu.abs(), "dup")
+        if fp8:
+            for q, w in ((d.dgate_rows, wg), (d.dup_rows, wu), (d.dgate_cols, wg.t()), (d.dup_cols, wu.t())):
+                assert not bool(torch.isnan(q.data.float()).any())
