@@ -68,16 +68,19 @@ __global__ void __launch_bounds__(512) block_norm_grad_wide_kernel(const muon_bl
     const bool element = a.gate && !a.gate_per_row;
     const Kept<T, KEPT8> kg(element ? a.gate : nullptr, a.gate_scale, a.ldg, row, a.rows, a.kept_fmt);
     const float rx = a.rstd_x[row], rh = a.rstd_h[row];
-    const float row_sig = a.gate && !element ? sigmoid2<float>(both(to_f32(static_cast<const T*>(a.gate)[row * a.ldg]))).x : 1.f;
+    const float2 row_exp = exp_minus2<float>(both(a.gate && !element ? to_f32(static_cast<const T*>(a.gate)[row * a.ldg]) : 0.f));
+    const float row_sig = a.gate && !element ? sigmoid_of2<float>(row_exp).x : 1.f;
     struct Element {
-      float d, u, hn, xn, sig, c;  // dy, dh + rho_h dy pre, H, X, sigmoid(gate), scale post
+      float d, u, hn, xn, sig, shut, c;  // dy, dh + rho_h dy pre, H, X, sigmoid(gate) and 1 less, scale post
     };
     auto load = [&](int col, float xs, float hs, float gs) {
       Element e;
       e.d = to_f32(dy[col]);
       e.hn = kh.at(col, hs) * rh;
       e.xn = kx.at(col, xs) * rx;
-      e.sig = element ? sigmoid2<T>(both(kg.at(col, gs))).x : row_sig;
+      const float2 ex = exp_minus2<T>(both(element ? kg.at(col, gs) : 0.f)), s = sigmoid_of2<T>(ex);
+      e.sig = element ? s.x : row_sig;
+      e.shut = shut2(ex, s).x;
       e.c = load_weight(a.post, a.weight_dt, col, true) * load_weight(a.scale, a.weight_dt, col, true);
       e.u = fmaf(rh, e.d * load_weight(a.pre, a.weight_dt, col, true), a.dh ? to_f32(dh[col]) : 0.f);
       return e;
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_wide_kernel(const muon_bl
     }
     cta_sums<W, 3>(sum, sh, turn);
     const float k1 = sum[0] * inv_n * rh, along = sum[1] - k1 * sum[2], k2 = along * inv_n;
-    if (threadIdx.x == 0 && a.dgate && !element) static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>((1.f - row_sig) * along);
+    if (threadIdx.x == 0 && a.dgate && !element) static_cast<T*>(a.dgate)[row * a.lddgate] = from_f32<T>(shut2(row_exp, both(row_sig)).x * along);
     for (int k = 0; k < turns; ++k) {
       const int kb = warp + W * k;
       if (kb >= blocks) break;
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_wide_kernel(const muon_bl
         const float d = e.u - k1 * e.hn, t = d * e.sig, b = t * e.c;
         if (a.dresidual) static_cast<T*>(a.dresidual)[row * a.lddr + col] = from_f32<T>(a.alpha * d);
         if (a.dx) static_cast<T*>(a.dx)[row * a.lddx + col] = from_f32<T>(rx * (b - e.xn * k2));
-        if (a.dgate && element) static_cast<T*>(a.dgate)[row * a.lddgate + col] = from_f32<T>((1.f - e.sig) * (b * e.xn));
+        if (a.dgate && element) static_cast<T*>(a.dgate)[row * a.lddgate + col] = from_f32<T>(e.shut * (b * e.xn));
         if (part) {  // this thread alone holds these columns of the CTA's sums
           part[col] = (turn ? part[col] : 0.f) + e.d * e.hn;
           part[cols + col] = (turn ? part[cols + col] : 0.f) + t * e.xn;
@@ -157,6 +160,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   using K = std::conditional_t<KEPT != 0, uint8_t, T>;
   using Slots = GradRing<T, G, S, ROWS, KEPT != 0, ANYWHERE>;
   constexpr int E = P::E, N = P::N;
+  // For the second phase a gate's exponential is kept and its sigmoid formed again (TWICE), or, where not even the exponentials of two
+  // rows fit, read from the ring once more (AGAIN: 8192 bf16 columns 114 us, kept 134).  fp32 rows, whose quotients are dear, keep
+  // both where one row at a time leaves the registers (2048 columns from e4m3 145 us, twice 162; two rows from e4m3 237 and 193).
+  constexpr bool AGAIN = GATE && KEPT == 0 && sizeof(T) == 2 && ROWS > 1;
+  constexpr bool TWICE = GATE && !AGAIN && (sizeof(T) == 2 || (KEPT != 0 && ROWS > 1));
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ RowSums3<G, TH, CL, ROWS> sums;
   const Slots ring{ring_smem};
@@ -275,8 +283,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
     fetch(slot == 0 ? S - 1 : slot - 1);
     cp_async_wait<S - 1>();
     if (ANYWHERE) __syncwarp();
-    P u[ROWS], sig[ROWS], xn[ROWS], hn[ROWS];
-    float sum[ROWS][3], row_sig[ROWS];
+    P u[ROWS], ex[ROWS], xn[ROWS], hn[ROWS];  // ex: the gate, then exp(-gate), from which its sigmoid is formed twice
+    float sum[ROWS][3];
+    float2 row_exp[ROWS], row_sig[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const int at = slot * ROWS + r;
@@ -286,15 +295,16 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
       read(at, DH, dh, lddh, here, u[r]);
       read_kept(at, X, a.x, a.ldx, here, xn[r]);
       read_kept(at, H, a.h, a.ldh, here, hn[r]);
-      if (GATE) read_kept(at, GA, a.gate, a.ldg, here, sig[r]);
+      if (GATE) read_kept(at, GA, a.gate, a.ldg, here, ex[r]);
       if ((R > 1 || ROWS > 1) && here >= a.rows) {  // the slot holds another row's remains
 #pragma unroll
-        for (int i = 0; i < N; ++i) d.v[i] = xn[r].v[i] = hn[r].v[i] = u[r].v[i] = sig[r].v[i] = both(0.f);
+        for (int i = 0; i < N; ++i) d.v[i] = xn[r].v[i] = hn[r].v[i] = u[r].v[i] = ex[r].v[i] = both(0.f);
       }
       const float2 xf = both(KEPT ? now[r].rx * fp8_scale_value(now[r].xs) : now[r].rx);
       const float2 hf = both(KEPT ? now[r].rh * fp8_scale_value(now[r].hs) : now[r].rh);
       const float2 gf = both(KEPT ? fp8_scale_value(now[r].gs) : 1.f);
-      row_sig[r] = row_gated ? sigmoid2<float>(both(now[r].gate)).x : 1.f;
+      row_exp[r] = both(row_gated ? exp_minus2<float>(both(now[r].gate)).x : 0.f);
+      row_sig[r] = both(row_gated ? sigmoid_of2<float>(row_exp[r]).x : 1.f);
       float2 s0 = both(0.f), s1 = s0, s2 = s0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -302,8 +312,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
         xn[r].v[i] = mul2(xn[r].v[i], xf);
         const float2 ad = mul2(d.v[i], w2[i]);
         u[r].v[i] = fma2(both(now[r].rh), ad, u[r].v[i]);
-        sig[r].v[i] = GATE ? sigmoid2<T>(KEPT ? mul2(sig[r].v[i], gf) : sig[r].v[i]) : both(row_sig[r]);
-        const float2 e = mul2(mul2(sig[r].v[i], w1[i]), xn[r].v[i]);
+        if (GATE) ex[r].v[i] = exp_minus2<T>(KEPT ? mul2(ex[r].v[i], gf) : ex[r].v[i]);
+        const float2 e = mul2(mul2(GATE ? sigmoid_of2<T>(ex[r].v[i]) : row_sig[r], w1[i]), xn[r].v[i]);
         s0 = fma2(ad, hn[r].v[i], s0);
         s1 = fma2(u[r].v[i], e, s1);
         s2 = fma2(hn[r].v[i], e, s2);
@@ -312,20 +322,32 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
       sum[r][0] = total(s0), sum[r][1] = total(s1), sum[r][2] = total(s2);
     }
     sums(sum, turn);
+    if (TWICE) {  // the compiler would keep both
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("" : "+f"(ex[r].v[i].x), "+f"(ex[r].v[i].y));
+    }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const long long here = row + r * step;
       const bool live = (R == 1 && ROWS == 1) || here < a.rows;
       const float k1 = sum[r][0] * inv_cols * now[r].rh, along = sum[r][1] - k1 * sum[r][2], k2 = along * inv_cols;
-      if (gate_out && live) static_cast<T*>(a.dgate)[here * a.lddgate] = from_f32<T>((1.f - row_sig[r]) * along);
+      if (gate_out && live) static_cast<T*>(a.dgate)[here * a.lddgate] = from_f32<T>(shut2(row_exp[r], row_sig[r]).x * along);
       P dr, dx, dg;
+      if (AGAIN) {
+        read(slot * ROWS + r, GA, a.gate, a.ldg, here, ex[r]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) ex[r].v[i] = live ? exp_minus2<T>(ex[r].v[i]) : both(0.f);
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float2 v = fma2(both(-k1), hn[r].v[i], u[r].v[i]), td = mul2(v, sig[r].v[i]), b = mul2(td, w1[i]);
+        const float2 sig = GATE ? sigmoid_of2<T>(ex[r].v[i]) : row_sig[r];
+        const float2 v = fma2(both(-k1), hn[r].v[i], u[r].v[i]), td = mul2(v, sig), b = mul2(td, w1[i]);
         sx[i] = fma2(td, xn[r].v[i], sx[i]);
         dr.v[i] = mul2(both(a.alpha), v);
         dx.v[i] = mul2(both(now[r].rx), fma2(both(-k2), xn[r].v[i], b));
-        if (GATE) dg.v[i] = mul2(fma2(both(-1.f), sig[r].v[i], both(1.f)), mul2(b, xn[r].v[i]));
+        if (GATE) dg.v[i] = mul2(shut2(ex[r].v[i], sig), mul2(b, xn[r].v[i]));
       }
       put(pdr, live && a.dresidual, dr);
       put(pdx, live && a.dx, dx);

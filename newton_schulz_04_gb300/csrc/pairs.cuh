@@ -100,22 +100,40 @@ struct Pairs {
 // Pieces that hold every column are summed as pairs, too.
 __device__ __forceinline__ float total(float2 v) { return v.x + v.y; }
 
-// 1 / (1 + exp(-g)) of a pair, 0 at -infinity and from about g = -87 on.  fp32 data takes the accurate exponential and
-// quotient, and so does a gate of a whole row, whose error all its elements share; 16-bit data, which is rounded by 2^-11 at
-// best, the hardware's: off by (4 + 1.2 |g|) 2^-23 of the value.
+// exp(-g) of a pair and, of it, the sigmoid 1 / (1 + exp(-g)), 0 at -infinity and from about g = -87 on.  fp32 data takes the
+// accurate exponential and quotient, and so does a gate of a whole row, whose error all its elements share; 16-bit data, which
+// is rounded by 2^-11 at best, the hardware's: the sigmoid is off by (4 + 1.2 |g|) 2^-23 of the value.
 template <typename T>
-__device__ __forceinline__ float2 sigmoid2(float2 g) {
+__device__ __forceinline__ float2 exp_minus2(float2 g) {
   if constexpr (sizeof(T) == 4) {
-    return make_float2(1.f / (1.f + expf(-g.x)), 1.f / (1.f + expf(-g.y)));
+    return make_float2(expf(-g.x), expf(-g.y));
   } else {
-    float2 e = mul2(g, both(-1.4426950408889634f)), r;
+    float2 e = mul2(g, both(-1.4426950408889634f));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
-    e = add2(e, both(1.f));
+    return e;
+  }
+}
+template <typename T>
+__device__ __forceinline__ float2 sigmoid_of2(float2 e) {
+  e = add2(e, both(1.f));
+  if constexpr (sizeof(T) == 4) {
+    return make_float2(1.f / e.x, 1.f / e.y);
+  } else {
+    float2 r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
     return r;
   }
+}
+template <typename T>
+__device__ __forceinline__ float2 sigmoid2(float2 g) {
+  return sigmoid_of2<T>(exp_minus2<T>(g));
+}
+// 1 - s for a derivative, which is multiplied by s: as the product, since the difference of an open gate keeps nothing of it.
+// Where exp(-g) is infinite s is 0, and this any finite number.
+__device__ __forceinline__ float2 shut2(float2 e, float2 s) {
+  return mul2(make_float2(fminf(e.x, 3.402823466e38f), fminf(e.y, 3.402823466e38f)), s);
 }
 
 // ---- rows that do not start on 16 bytes

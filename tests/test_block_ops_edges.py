@@ -109,3 +109,42 @@ def test_gradient_from_checkpoints_of_the_largest_finite_values(mm, dtype, fmt, 
         if fp8:
             for q, w in ((d.dgate_rows, wg), (d.dup_rows, wu), (d.dgate_cols, wg.t()), (d.dup_cols, wu.t())):
                 assert not bool(torch.isnan(q.data.float()).any())
+
+
+# ---------------------------------------------------------------- gates that are wide open
+
+@gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kept", [None, "e4m3"])
+@pytest.mark.parametrize("cols", [5, 264, 1000, 8200, 40_000])
+def test_gradient_of_open_gates(mm, dtype, kept, cols):
+    """dgate = sigmoid(g) sigmoid(-g) ... of gates from 8 to 80, whose sigmoids are 1 but for 2^-12 to 2^-115 of it: relative to
+    the value.  Without dy the stream's gradient is dh, so that nothing else of it cancels."""
+    rows = 6
+    x, h, _, post, pre, scale = norm_inputs(30, rows, cols, dtype, "none", True)
+    dh = gen(31, rows, cols).to(dtype)
+    rx, rh = ((t.double() ** 2).mean(dim=1).rsqrt().float() for t in (x, h))
+    steps = torch.tensor([-80.0, -20.0, -8.0, 8.0, 10.0, 12.0, 16.0, 20.0, 40.0, 80.0])
+    gate = steps[torch.arange(rows * cols) % 10].view(rows, cols).to(dtype)
+    per_row = steps[3:3 + rows, None].to(dtype)
+    X, c = x.double() * rx.double()[:, None], post.double() * scale.double()
+    # an exponential (2 + 1.17 |g| units) counts twice, in exp(-g) and the sigmoid; two roundings each of theirs, six products'
+    rel = lambda g: (2 * (4 + 1.2 * g.double().abs()) * 2 + 10) * F24  # noqa: E731
+    u = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: F24}[dtype]
+    tiny = torch.finfo(dtype).smallest_normal * u * 2
+    for g in (gate, per_row):
+        if kept:
+            qx, qh = (mm.fp8_quantize(t.cuda(), kept)[0] for t in (x, h))
+            kg = mm.fp8_quantize(g.cuda(), kept)[0] if g is gate else g.cuda()
+            state = mm.BlockNormKept(qx, qh, kg, rx.cuda(), rh.cuda())
+            xs, gs = qx.dequantize().cpu().double() * rx.double()[:, None], kg.dequantize().cpu() if g is gate else g
+        else:
+            state, xs, gs = mm.BlockNormKept(*dev(x, h, g, rx, rh)), X, g
+        d = mm.block_norm_backward(torch.zeros_like(dh).cuda(), state, *dev(post, pre), scale=scale.cuda(), dh=dh.cuda())
+        s, shut = torch.sigmoid(gs.double()), torch.sigmoid(-gs.double())
+        along = dh.double() * s * c * xs
+        if g is gate:
+            close(d.dgate, along * shut, ((u + rel(gs)) * along.abs() * shut + tiny), "dgate")
+        else:                                  # a sum of at most 140 terms one after another, and those of its roundings
+            total = along.abs().sum(dim=1, keepdim=True) * shut
+            close(d.dgate, along.sum(dim=1, keepdim=True) * shut, (u + 150 * F24 + rel(gs)) * total + tiny, "dgate of rows")
