@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB) block_norm_ring_kerne
   using P = Pairs<T>;
   constexpr int E = P::E, N = P::N, PIECE = G * E;  // PIECE: from a thread's piece to its next
   constexpr int LANES = G < 32 ? G : 32;  // of a row in a warp
-  using Scales = Scales4<(128 / E < G ? 128 / E : G)>;
+  using Scales = Scales4<(128 / E < G ? 128 / E : G), sizeof(T) == 2>;
   extern __shared__ __align__(16) uint8_t ring_smem[];
   __shared__ RowSum<G, TH, CL> row_total;
   const RowRing<T, G, C, S, ANYWHERE> ring{ring_smem};

@@ -91,7 +91,7 @@ template <typename T, bool GELU, int EIGHT, bool ANYWHERE>
 __global__ void __launch_bounds__(256) gated_kernel(const muon_gated_args a) {
   using P = Pairs<T>;
   constexpr int E = P::E, N = P::N, LANES = 128 / E, GROUPS = 256 / LANES, U = kGatedRows;
-  using Scales = Scales4<LANES>;
+  using Scales = Scales4<LANES, sizeof(T) == 2>;
   pdl_launch_dependents();
   pdl_wait();
   const int t = threadIdx.x % LANES, kb = blockIdx.x, cols = static_cast<int>(a.cols), col = kb * 128 + t * E, left = cols - col;

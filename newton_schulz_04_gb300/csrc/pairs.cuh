@@ -275,11 +275,14 @@ __device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
   constexpr uint32_t LAST = 0x7f7fffffu;  // FLT_MAX; infinity and NaN are above it and stay as they are
   return __byte_perm(max(__viaddmin_u32(a, 0xffffu, LAST), a), max(__viaddmin_u32(b, 0xffffu, LAST), b), 0x7632);
 }
+// The same of 16-bit types' values, none of which lies between 0x7f7f0000 and infinity.
+__device__ __forceinline__ uint32_t upper_halves16(uint32_t a, uint32_t b) { return __byte_perm(a + 0xffffu, b + 0xffffu, 0x7632); }
 
 // Scales of up to four matrices' blocks, whose 128 columns lie in LANES = 16 or 32 neighbouring lanes.  The largest
 // magnitudes travel two to a word.  A quarter of the lanes ends up with one matrix each, computes its byte, keeps it and hands
-// the others its inverse: a third of the instructions of four exchanges in all lanes.
-template <int LANES>
+// the others its inverse: a third of the instructions of four exchanges in all lanes.  INPUTS16: the last two hold a 16-bit type's
+// values.
+template <int LANES, bool INPUTS16>
 struct Scales4 {
   static constexpr int Q = LANES / 4;
   uint32_t byte;   // of matrix (lane / Q) % 4
@@ -288,7 +291,7 @@ struct Scales4 {
   // m: fp32 bits of the lane's largest magnitudes; top: 8 or 15 for the matrix mine() says
   __device__ __forceinline__ Scales4(const uint32_t (&m)[4], int top) {
     const int lane = threadIdx.x % 32;
-    const uint32_t ab = upper_halves(m[0], m[1]), cd = upper_halves(m[2], m[3]);
+    const uint32_t ab = upper_halves(m[0], m[1]), cd = INPUTS16 ? upper_halves16(m[2], m[3]) : upper_halves(m[2], m[3]);
     const bool up = lane & (2 * Q);
     uint32_t w = __vmaxu2(up ? cd : ab, __shfl_xor_sync(0xffffffffu, up ? ab : cd, 2 * Q));
 #pragma unroll
