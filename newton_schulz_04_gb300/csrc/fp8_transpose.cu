@@ -132,23 +132,23 @@ __device__ __noinline__ void transpose_any(const Fp8TransposeArgs& a, TransposeT
         if (j < part.nc && (s[i] == 255u || ((j < 4 ? x : y) >> (8 * (j & 3)) & 0x80u))) bad |= 1u << j;
     }
   }
-  // the signed keys of two columns of a row, 0 for 0
-  const auto keys = [&](int j, int i, int (&k)[2]) {
+  // the keys of two columns of a row, 0 for 0; they pass 2^31
+  const auto keys = [&](int j, int i, uint32_t (&k)[2]) {
     const uint32_t two = (j < 4 ? q[i].x : q[i].y) >> (8 * (j & 2));
     const float2 f = fp8_unpack2<E5M2>(two);
     const uint32_t x = abs_bits(f.x), y = abs_bits(f.y);
-    k[0] = x ? static_cast<int>(x + (s[i] << 23)) : 0;
-    k[1] = y ? static_cast<int>(y + (s[i] << 23)) : 0;
+    k[0] = x ? x + (s[i] << 23) : 0u;
+    k[1] = y ? y + (s[i] << 23) : 0u;
   };
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     uint32_t m0 = 0u, m1 = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      int k[2];
+      uint32_t k[2];
       keys(j, i, k);
-      m0 = max(m0, static_cast<uint32_t>(k[0]));
-      m1 = max(m1, static_cast<uint32_t>(k[1]));
+      m0 = max(m0, k[0]);
+      m1 = max(m1, k[1]);
     }
     if (bad >> j & 1) m0 = 0xffffffffu;
     if (bad >> j & 2) m1 = 0xffffffffu;
@@ -178,12 +178,12 @@ __device__ __noinline__ void transpose_any(const Fp8TransposeArgs& a, TransposeT
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = 4 * k + r;
-        int key[2];
+        uint32_t key[2];
         keys(j, i, key);
-        // exponents below fp32's end as 0 or subnormal, far below the 8-bit type's smallest value
+        // exponents below fp32's end as 0 or subnormal, far below the 8-bit type's smallest value: where a column's scale is above a key
         const uint32_t raw = j < 4 ? q[i].x : q[i].y;
-        v[0][r] = __uint_as_float(static_cast<uint32_t>(max(key[0] - static_cast<int>(b0 << 23), 0)) | (raw << (24 - 8 * (j & 3)) & 0x80000000u));
-        v[1][r] = __uint_as_float(static_cast<uint32_t>(max(key[1] - static_cast<int>(b1 << 23), 0)) | (raw << (16 - 8 * (j & 3)) & 0x80000000u));
+        v[0][r] = __uint_as_float((max(key[0], b0 << 23) - (b0 << 23)) | (raw << (24 - 8 * (j & 3)) & 0x80000000u));
+        v[1][r] = __uint_as_float((max(key[1], b1 << 23) - (b1 << 23)) | (raw << (16 - 8 * (j & 3)) & 0x80000000u));
       }
       out[0][k] = b0 == 255u ? 0x7f7f7f7fu : fp8_pack4<E5M2>(v[0][0], v[0][1], v[0][2], v[0][3]);
       out[1][k] = b1 == 255u ? 0x7f7f7f7fu : fp8_pack4<E5M2>(v[1][0], v[1][1], v[1][2], v[1][3]);

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import oracle.blocks as ref
-from test_block_ops import DTYPES, F24, check8_exact, close, dev, gen, gpu, mm, norm_inputs  # noqa: F401
+from test_block_ops import (  # noqa: F401
+    DTYPES, F24, check8_exact, close, dev, gen, gpu, mm, norm_inputs, transposed_exactly,
+)
 
 FLT_MAX = torch.finfo(torch.float32).max
 
@@ -148,3 +150,21 @@ def test_gradient_of_open_gates(mm, dtype, kept, cols):
         else:                                  # a sum of at most 140 terms one after another, and those of its roundings
             total = along.abs().sum(dim=1, keepdim=True) * shut
             close(d.dgate, along.sum(dim=1, keepdim=True) * shut, (u + 150 * F24 + rel(gs)) * total + tiny, "dgate of rows")
+
+
+# ---------------------------------------------------------------- transposition
+
+@gpu
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("scales", [(0, 1), (120, 136), (130, 131), (200, 239), (0, 239)])
+def test_transpose_of_any_scales(mm, fmt, scales):
+    """Rows whose scale bytes lie in a range, small and large, near one another and not; values of every size."""
+    dt = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+    g = torch.Generator().manual_seed(7)
+    b = torch.randint(0, 256, (300, 208), generator=g).to(torch.uint8)
+    b[~torch.isfinite(b.view(dt).float())] = 0x38
+    scale = torch.randint(*scales, (1, 300, 4), generator=g).to(torch.uint8)
+    q = mm.Fp8Tensor(b.cuda().view(dt), scale.cuda())
+    t = mm.fp8_transpose(q)
+    data, want = transposed_exactly(q)
+    assert torch.equal(t.scale.view(torch.uint8).cpu(), want) and torch.equal(t.data.float().cpu().double(), data)
