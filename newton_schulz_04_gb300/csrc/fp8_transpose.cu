@@ -18,7 +18,7 @@ namespace muon {
 // That takes some 20 instructions a value.  Where the scales of a tile's rows lie near enough to its first row's, 16-bit types hold
 // every value times 2^(s - first s) exactly, and two at a time take half of them.  The other way, a function of its own that
 // costs this one no registers, is for the rest, and for tiles in which some column's largest magnitude is so small that
-// its factor leaves the 16-bit type's range.
+// its factor leaves the 16-bit type's range.  Where the first row's scale is 1, as that of zeros is, the next other one takes its place.
 //
 // e4m3 goes through fp16, to and from which the hardware converts: scales 2^14 below the first (values are multiples of 2^-9, fp16's
 // of 2^-24) to 2^7 above it (values are at most 448).  e5m2 has fp16's exponents, which leaves no room for scales; its
@@ -109,6 +109,19 @@ struct TransposePart {
     }
   }
 };
+
+// The first scale byte of the tile's rows that is not `base`, or base: a row of zeros has scale 1, which says nothing of the others.
+__device__ __forceinline__ uint32_t other_scale(const Fp8TransposeArgs& a, uint32_t base) {
+  const long long rows4 = (a.rows + 3) & ~3LL, row0 = blockIdx.y * 128LL;
+#pragma unroll 1
+  for (int k = 0; k < 128; k += 32) {
+    const long long row = row0 + k + threadIdx.x % 32;
+    const uint32_t s = row < a.rows ? a.qs[fp8_scale_offset(blockIdx.x, row, rows4)] : base;
+    const uint32_t found = __ballot_sync(0xffffffffu, s != base);
+    if (found) return __shfl_sync(0xffffffffu, s, __ffs(found) - 1);
+  }
+  return base;
+}
 
 // Any scales: fills the tile and the columns' scale bytes.
 template <bool E5M2>
@@ -207,12 +220,13 @@ __global__ void __launch_bounds__(256, 4) fp8_transpose_kernel(const __grid_cons
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
   V h[8][4];
   bool other = false;  // the other way
-  const uint32_t base = a.qs[fp8_scale_offset(blockIdx.x, blockIdx.y * 128LL, (a.rows + 3) & ~3LL)];
+  uint32_t base = a.qs[fp8_scale_offset(blockIdx.x, blockIdx.y * 128LL, (a.rows + 3) & ~3LL)];
   {
     const TransposePart part(a);
     uint2 q[8];
     uint32_t s[8];
     part.load(a, q, s);
+    if (base == 127u) base = other_scale(a, base);  // a row of zeros, perhaps
     V m[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) m[k] = Way::bits(0u);

@@ -168,3 +168,18 @@ def test_transpose_of_any_scales(mm, fmt, scales):
     t = mm.fp8_transpose(q)
     data, want = transposed_exactly(q)
     assert torch.equal(t.scale.view(torch.uint8).cpu(), want) and torch.equal(t.data.float().cpu().double(), data)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("size", [2.0 ** -120, 1e-6, 1.0, 300.0, 1e9, 2.0 ** 100])
+@pytest.mark.parametrize("zeros", [1, 31, 33, 128, 200])
+def test_transpose_of_rows_behind_zeros(mm, fmt, size, zeros):
+    """Tiles that begin with rows of zeros, whose scales are 1 whatever the others' are."""
+    x = gen(40, 270, 160) * size
+    x[:zeros], x[256:256 + zeros % 14] = 0.0, 0.0
+    x[250, :128] = 0.0
+    q, _ = mm.fp8_quantize(x.cuda(), fmt)
+    t = mm.fp8_transpose(q)
+    data, want = transposed_exactly(q)
+    assert torch.equal(t.scale.view(torch.uint8).cpu(), want) and torch.equal(t.data.float().cpu().double(), data)
