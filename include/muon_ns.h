@@ -649,7 +649,8 @@ typedef struct {
     int32_t dt, weight_dt, gate_per_row, kept_fmt;
     float alpha;
 } muon_block_norm_grad_args;
-MUON_API size_t muon_block_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+MUON_API size_t muon_block_norm_backward_workspace_bytes(int64_t rows, int64_t cols);                     /* for any dt */
+MUON_API size_t muon_block_norm_backward_workspace_bytes_for(int64_t rows, int64_t cols, muon_dtype dt);  /* for this one */
 MUON_API muon_status muon_block_norm_backward(const muon_block_norm_grad_args* args, void* stream);
 
 typedef enum {

@@ -125,6 +125,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         f.argtypes, f.restype = [ctypes.c_char_p, vp], i32  # the packed argument struct, the stream
     lib.muon_block_norm_backward_workspace_bytes.argtypes = [i64, i64]
     lib.muon_block_norm_backward_workspace_bytes.restype = sz
+    lib.muon_block_norm_backward_workspace_bytes_for.argtypes = [i64, i64, i32]
+    lib.muon_block_norm_backward_workspace_bytes_for.restype = sz
     lib.muon_fp8_transpose.argtypes = [vp, i64, vp, i64, i64, i32, vp, i64, vp, vp]
     lib.muon_fp8_transpose.restype = i32
     lib.muon_last_error.argtypes = []

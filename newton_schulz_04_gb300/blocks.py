@@ -245,7 +245,7 @@ def _block_norm_backward(dy, lddy, dh, lddh, kx, kh, kg, gate, rstd_x, rstd_h, p
     size = 0
     if dweights:
         dpost, dpre, dscale = _vector(cols, dev), _vector(cols, dev), None if scale is None else _vector(cols, dev)
-        size = lib.muon_block_norm_backward_workspace_bytes(rows, cols)
+        size = lib.muon_block_norm_backward_workspace_bytes_for(rows, cols, codes[0])
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
     _b._check(lib.muon_block_norm_backward(_BLOCK_NORM_GRAD(
         dy.data_ptr(), lddy, _ptr(dh), lddh, *kx[:3], *kh[:3], *kg[:3], rstd_x.data_ptr(), rstd_h.data_ptr(), post.data_ptr(),

@@ -97,9 +97,13 @@ muon_status muon_block_norm(const muon_block_norm_args* args, void* stream) {
   return launched(launch_block_norm(a, vec, sms, static_cast<cudaStream_t>(stream)), "launch_block_norm");
 }
 
+size_t muon_block_norm_backward_workspace_bytes_for(int64_t rows, int64_t cols, muon_dtype dt) {
+  if (rows < 0 || cols < 1 || cols > MUON_MAX_DIM || !float_dt(dt)) return 0;
+  return static_cast<size_t>(block_norm_grad_parts(rows, cols, dtype_bytes(dt), MUON_MAX_SMS)) * 2 * cols * sizeof(float);
+}
 size_t muon_block_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols < 1 || cols > MUON_MAX_DIM) return 0;
-  return static_cast<size_t>(block_norm_grad_ctas(rows, MUON_MAX_SMS)) * 2 * cols * sizeof(float);
+  return std::max(muon_block_norm_backward_workspace_bytes_for(rows, cols, MUON_BF16),
+                  muon_block_norm_backward_workspace_bytes_for(rows, cols, MUON_FP32));
 }
 
 muon_status muon_block_norm_backward(const muon_block_norm_grad_args* args, void* stream) {
@@ -140,7 +144,7 @@ muon_status muon_block_norm_backward(const muon_block_norm_grad_args* args, void
       all.add(p, rows * 4, false);
     }
     if (weights) {
-      const size_t need = muon_block_norm_backward_workspace_bytes(rows, cols);
+      const size_t need = muon_block_norm_backward_workspace_bytes_for(rows, cols, static_cast<muon_dtype>(a.dt));
       if (!a.ws) return fail(MUON_ERR_ARG, "workspace is NULL");
       if (misaligned(a.ws, 16)) return fail(MUON_ERR_ALIGN, "workspace is not 16-byte aligned");
       if (a.ws_bytes < 0 || static_cast<size_t>(a.ws_bytes) < need)

@@ -38,8 +38,17 @@ __global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float* p
   }
 }
 
-int block_norm_grad_ctas(long long rows, int sms) {
-  return static_cast<int>(std::max(1LL, std::min<long long>(rows, kBlockNormCtasPerSm * sms)));
+// As many as the shapes in block_norm_grad_rows.cu let run at the same time.
+int block_norm_grad_parts(long long rows, long long cols, int elem_size, int sms) {
+  const long long pieces = (cols * elem_size + 15) / 16;
+  const int most = pieces > 4096   ? 2 * sms  // the widest rows
+                   : pieces <= 128 ? 4 * sms
+                   : pieces <= 256 ? 2 * sms
+                   : pieces <= 512 ? sms
+                   : pieces <= 1024 ? sms / 2
+                   : pieces <= 2048 ? sms / 4
+                                    : sms / 8;
+  return static_cast<int>(std::max(1LL, std::min<long long>(rows, most)));
 }
 
 cudaError_t launch_block_norm_grad(const muon_block_norm_grad_args& a, float* partial, int vec, int sms, cudaStream_t st) {

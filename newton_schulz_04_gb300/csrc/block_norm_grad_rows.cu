@@ -388,15 +388,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   }
 }
 
-// The kernels add up rows of `partial` for at most this many CTAs (or clusters).
-static int most_ctas(int sms) { return kBlockNormCtasPerSm * sms; }
-
 template <typename T, int G, int S, int ROWS, int MINB, int CL, int KEPT, bool GATE, bool ANYWHERE>
 static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   constexpr int TH = G < 128 ? 128 : G, R = TH / G;
   constexpr int smem = GradRing<T, G, S, ROWS, KEPT != 0, ANYWHERE>::BYTES;
   static_assert(smem * MINB <= 224 * 1024, "shared memory of an SM");
-  static_assert(MINB <= kBlockNormCtasPerSm, "rows of partial");
   static bool done[64] = {false};
   static int known[64] = {0};
   const auto kernel = block_norm_grad_ring_kernel<T, G, S, ROWS, MINB, CL, KEPT, GATE, ANYWHERE>;
@@ -407,7 +403,8 @@ static cudaError_t launch_ring(const muon_block_norm_grad_args& a, float* partia
     e = resident_clusters(kernel, TH, smem, CL, known, &most);
     if (e != cudaSuccess) return e;
   }
-  *ctas = static_cast<int>(std::min<long long>((a.rows + R - 1) / R, std::min(most, most_ctas(sms))));
+  most = std::min(most, block_norm_grad_parts(a.rows, a.cols, sizeof(T), sms));
+  *ctas = static_cast<int>(std::min<long long>((a.rows + R - 1) / R, most));
   return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(*ctas * CL)), dim3(TH), smem, CL, st, a, partial);
 }
 
@@ -447,7 +444,7 @@ template <typename T, bool ANYWHERE>
 cudaError_t launch_block_norm_grad_rows(const muon_block_norm_grad_args& a, float* partial, int sms, int* ctas, cudaStream_t st) {
   // 8 CTAs of 512 pieces: 32768 16-bit columns, half as many of fp32
   if (a.cols > 8 * 512 * (16 / static_cast<int>(sizeof(T)))) {
-    *ctas = static_cast<int>(std::min<long long>(a.rows, 2 * sms));
+    *ctas = block_norm_grad_parts(a.rows, a.cols, sizeof(T), sms);
     return a.x_scale ? launch_pdl(block_norm_grad_wide_kernel<T, true>, dim3(*ctas), dim3(512), 0, st, a, partial)
                      : launch_pdl(block_norm_grad_wide_kernel<T, false>, dim3(*ctas), dim3(512), 0, st, a, partial);
   }

@@ -76,11 +76,10 @@ struct Fp8QuantArgs {
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, int dt, cudaStream_t st);
 
 // ---- block_norm.cu
-constexpr int kBlockNormCtasPerSm = 4;  // of the gradient kernel at most
 // vec: every row of the matrices allows 16-byte accesses.
 cudaError_t launch_block_norm(const muon_block_norm_args& a, int vec, int sms, cudaStream_t st);
-// CTAs of the gradient kernel, each with two rows of `partial` (or nullptr: no gradients of the weights).
-int block_norm_grad_ctas(long long rows, int sms);
+// CTAs or clusters of the gradient kernel at most, each with two rows of `partial` (or nullptr: no gradients of the weights).
+int block_norm_grad_parts(long long rows, long long cols, int elem_size, int sms);
 cudaError_t launch_block_norm_grad(const muon_block_norm_grad_args& a, float* partial, int vec, int sms, cudaStream_t st);
 
 // ---- gated.cu

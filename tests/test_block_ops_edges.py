@@ -183,3 +183,53 @@ def test_transpose_of_rows_behind_zeros(mm, fmt, size, zeros):
     t = mm.fp8_transpose(q)
     data, want = transposed_exactly(q)
     assert torch.equal(t.scale.view(torch.uint8).cpu(), want) and torch.equal(t.data.float().cpu().double(), data)
+
+
+# ---------------------------------------------------------------- the gradient's workspace
+
+PARTS = [(256, 0, 608), (1024, 0, 608), (2048, 0, 304), (4096, 0, 152), (8192, 0, 76), (16384, 0, 38), (32768, 0, 19), (32769, 0, 304),
+         (512, 1, 608), (1024, 1, 304), (2048, 1, 152), (4096, 1, 76), (16384, 1, 19), (16385, 1, 304)]
+
+
+@pytest.mark.parametrize("cols,dt,parts", PARTS)
+def test_workspace_of_the_norm_gradient(mm, cols, dt, parts):
+    """Two fp32 rows for each CTA or cluster that can run, no more; a call asks for as much and no more."""
+    from test_block_ops import P, norm_grad_call
+    lib = mm.load()
+    size = lib.muon_block_norm_backward_workspace_bytes_for(4_194_304, cols, dt)
+    assert size == parts * 2 * cols * 4
+    assert lib.muon_block_norm_backward_workspace_bytes_for(3, cols, dt) == min(3, parts) * 2 * cols * 4
+    most = lib.muon_block_norm_backward_workspace_bytes(4_194_304, cols)
+    assert most == max(lib.muon_block_norm_backward_workspace_bytes_for(4_194_304, cols, d) for d in (0, 1, 2))
+    far = dict(rows=200_000, cols=cols, dt=dt, dpre=P[10], ws=P[11])
+    far |= {k: cols for k in ("lddy", "lddh", "ldx", "ldh", "ldg", "lddx", "lddr", "lddg")}
+    far |= {k: (1 << 40) * (i + 1) for i, k in enumerate(("dy", "x", "h", "rx", "rh", "dx", "dr"))}
+    assert norm_grad_call(mm, **far, bytes=size - 1) == 4
+    if not torch.cuda.is_available():          # enough: the next thing that is missing is the device
+        assert norm_grad_call(mm, **far, bytes=size) not in (0, 1, 2, 3, 4)
+    for bad in ((-1, 64, 0), (4, 0, 0), (4, 65537, 0), (4, 64, 7)):
+        assert lib.muon_block_norm_backward_workspace_bytes_for(*bad) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kept", [None, "e4m3"])
+@pytest.mark.parametrize("cols,dtype", [(c, torch.float32 if d else torch.bfloat16) for c, d, _ in PARTS] + [(65_536, torch.float16)])
+def test_norm_gradient_stays_within_its_workspace(mm, cols, dtype, kept):
+    from newton_schulz_04_gb300 import blocks
+    rows, lib, st = 900 if cols < 8192 else 340, mm.load(), torch.cuda.current_stream().cuda_stream
+    x, r, g, post, pre, scale = dev(*norm_inputs(50, rows, cols, dtype, "element", True))
+    o = mm.block_norm(x, r, post, pre, gate=g, scale=scale, checkpoint=kept)
+    want = mm.block_norm_backward(r, o.kept, post, pre, scale=scale, dh=x)
+    code = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}[dtype]
+    size = lib.muon_block_norm_backward_workspace_bytes_for(rows, cols, code)
+    ws = torch.full((size + 65_536,), 77, dtype=torch.uint8, device="cuda")
+    sums = torch.empty(3, cols, device="cuda")
+    k = [blocks._kept("k", t, r, rows, cols)[:3] for t in (o.kept.x, o.kept.h, o.kept.gate)]
+    assert lib.muon_block_norm_backward(blocks._BLOCK_NORM_GRAD(
+        r.data_ptr(), cols, x.data_ptr(), cols, *k[0], *k[1], *k[2], o.kept.rstd_x.data_ptr(), o.kept.rstd_h.data_ptr(), post.data_ptr(),
+        scale.data_ptr(), pre.data_ptr(), 0, 0, 0, 0, 0, 0, sums[0].data_ptr(), sums[1].data_ptr(), sums[2].data_ptr(), ws.data_ptr(), size,
+        rows, cols, code, 1, 0, 0, 1.0), st) == 0
+    torch.cuda.synchronize()
+    assert bool((ws[size:] == 77).all())
+    for got, w in zip(sums, (want.dpost_weight, want.dpre_weight, want.dscale)):
+        assert torch.equal(got, w)
