@@ -574,7 +574,8 @@ MUON_API muon_status muon_debug_bounded_wait_fp8(long long max_cycles, void* str
  * What stands around and within a residual network's block, and keeps what its backward pass needs in 8 bits: an "8-bit
  * copy" is a matrix in the format above with blocks of 128 columns, which the gradients read in the place of the
  * bf16, fp16 or fp32 matrix.  Their arguments travel in structs, which are read during the call only; a row stride (ld) is
- * ignored for a single row.  No output may overlap an input or another output.
+ * ignored for a single row.  No output may overlap an input or another output.  Rows of bf16, fp16 and fp32 matrices may lie
+ * between one another's where the strides are the same (the halves of one matrix); 8-bit ones take all from first to last.
  */
 
 /* An 8-bit matrix that a call writes; data and scale NULL: not asked for. */

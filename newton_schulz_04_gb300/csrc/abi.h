@@ -76,20 +76,31 @@ inline muon_status check_fp8_out(const char* name, const void* q, const void* sc
     if (st_ != MUON_OK) return st_;       \
   } while (0)
 
-// The memory that a call touches: what it writes may share no byte with anything else.
+// The memory that a call touches: what it writes may share no byte with anything else.  Matrices whose rows lie between one
+// another's (the halves of a wider one, say) share none.
 struct Spans {
   struct One {
-    uintptr_t begin, end;
+    uintptr_t begin, end, pitch, width;  // pitch and width: of rows, in bytes
     bool out;
   } s[32];
   int n = 0;
-  void add(const void* p, long long bytes, bool out) {
-    if (p && bytes > 0) s[n++] = {reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(bytes), out};
+  void add(const void* p, long long bytes, bool out) { add_rows(p, 1, bytes, bytes, out); }
+  void add_rows(const void* p, long long rows, long long pitch, long long width, bool out) {
+    if (!p || rows < 1 || width < 1) return;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p), w = static_cast<uintptr_t>(width);
+    s[n++] = {b, b + static_cast<uintptr_t>((rows - 1) * pitch) + w, rows > 1 ? static_cast<uintptr_t>(pitch) : 0, w, out};
+  }
+  static bool between(const One& a, const One& b) {  // a begins first
+    if (a.pitch == 0 || a.pitch != b.pitch) return false;
+    const uintptr_t d = (b.begin - a.begin) % a.pitch;
+    return d >= a.width && d + b.width <= a.pitch;
   }
   bool clash() const {
     for (int i = 0; i < n; ++i)
       for (int j = 0; j < i; ++j)
-        if ((s[i].out || s[j].out) && s[i].begin < s[j].end && s[j].begin < s[i].end) return true;
+        if ((s[i].out || s[j].out) && s[i].begin < s[j].end && s[j].begin < s[i].end &&
+            !(s[i].begin <= s[j].begin ? between(s[i], s[j]) : between(s[j], s[i])))
+          return true;
     return false;
   }
 };

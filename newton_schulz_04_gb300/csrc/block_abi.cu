@@ -15,7 +15,7 @@ static long long scale_bytes(long long rows, long long cols) { return static_cas
 static muon_status take(Spans* all, const char* name, const void* p, bool optional, long long rows, long long cols, long long ld,
                         int size, bool out, int* vec) {
   TRY(check_rows(name, p, optional, rows, cols, ld, size, vec));
-  all->add(p, span(rows, cols, ld, size), out);
+  all->add_rows(p, rows, ld * size, cols * size, out);
   return MUON_OK;
 }
 static muon_status take8(Spans* all, const char* name, const muon_fp8_out& o, int fmt, long long rows, long long cols) {

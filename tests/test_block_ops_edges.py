@@ -233,3 +233,75 @@ def test_norm_gradient_stays_within_its_workspace(mm, cols, dtype, kept):
     assert bool((ws[size:] == 77).all())
     for got, w in zip(sums, (want.dpost_weight, want.dpre_weight, want.dscale)):
         assert torch.equal(got, w)
+
+
+# ---------------------------------------------------------------- where memory lies
+
+def accepted(status):
+    """Without a GPU a call whose arguments are right ends where it asks for the device."""
+    return status not in (0, 1, 2, 3, 4)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory")
+def test_outputs_between_the_rows_of_others(mm):
+    from test_block_ops import P, gated_call, gated_grad_call, norm_call, norm_grad_call
+    half = 128                                  # bytes of a row of 64 bf16 columns; all strides are 128 columns
+    assert accepted(gated_grad_call(mm, lddg=128, lddu=128, du=P[3] + half))
+    assert accepted(gated_grad_call(mm, ldg=128, ldu=128, up=P[1] + half, lddg=128, lddu=128, du=P[3] + half))
+    assert accepted(norm_call(mm, ldy=128, ldh=128, y=P[5] + half))
+    assert accepted(norm_call(mm, ldx=128, ldy=128, y=P[0] + half))
+    assert accepted(norm_grad_call(mm, lddx=128, lddr=128, dr=P[7] + half))
+    assert accepted(norm_call(mm, ldy=128, ldh=128, h=P[4] + 5 * 256 + half))    # further down, and the rows above
+    assert accepted(norm_call(mm, ldy=128, ldh=128, y=P[5] + 256 + half))
+    for clash in (gated_grad_call(mm, lddg=128, lddu=128, du=P[3] + half - 2), gated_grad_call(mm, lddg=128, lddu=128, du=P[3] + 256 - 16),
+                  gated_grad_call(mm, lddg=128, lddu=136, du=P[3] + half), gated_grad_call(mm, lddg=64, lddu=64, du=P[3] + half),
+                  norm_call(mm, ldy=128, ldh=128, y=P[5] + 256), norm_call(mm, ldx=128, ldy=128, y=P[0] + half - 16),
+                  gated_call(mm, g8=P[3], g8s=P[4], u8=P[3] + 64, u8s=P[5], ldg8=128, ldu8=128)):     # 8-bit ones are not looked into
+        assert clash == 1
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols,gap", [(64, 0), (264, 0), (264, 8), (123, 0), (123, 2), (1_000, 3)])
+def test_outputs_in_the_halves_of_a_matrix(mm, dtype, cols, gap):
+    """The C entry points with outputs, and inputs, side by side in one matrix: as apart, and nothing between them is written."""
+    from newton_schulz_04_gb300 import blocks
+    rows, lib, st = 150, mm.load(), torch.cuda.current_stream().cuda_stream
+    code, size, ld = {torch.bfloat16: 0, torch.float32: 1}[dtype], dtype.itemsize, 2 * (cols + gap)
+    x, r, g, post, pre, scale = dev(*norm_inputs(60, rows, cols, dtype, "element", True))
+    dy = gen(61, rows, cols).to(dtype).cuda()
+
+    def wide():
+        t = torch.full((rows, ld), 5.0, dtype=dtype, device="cuda")
+        return t, t[:, :cols], t[:, cols + gap:2 * cols + gap]
+
+    def between(t):
+        return torch.cat([t[:, cols:cols + gap], t[:, 2 * cols + gap:]], dim=1)
+
+    inputs, gate, up = wide()
+    gate.copy_(g), up.copy_(x)
+    grads, dgate, dup = wide()
+    want = mm.gated_activation_backward(dy, mm.GatedKept(g, x))
+    for q in (None, "e4m3"):                    # the two kernels
+        y8 = mm.Fp8Tensor.empty(cols, rows, "e4m3")
+        args = [0, 0, 0] if q is None else [y8.data.data_ptr(), y8.scale.data_ptr(), y8._ld()]
+        assert lib.muon_gated_activation_backward(blocks._GATED_GRAD(
+            dy.data_ptr(), cols, gate.data_ptr(), 0, ld, up.data_ptr(), 0, ld, dgate.data_ptr(), ld, dup.data_ptr(), ld, *([0] * 12), *args,
+            rows, cols, code, 0, 0, 0, 0), st) == 0
+        assert torch.equal(dgate, want.dgate) and torch.equal(dup, want.dup) and bool((between(grads) == 5.0).all())
+        grads.fill_(5.0)
+    out, h, y = wide()
+    n = mm.block_norm(x, r, post, pre, gate=g, scale=scale)
+    stats = torch.empty(2, rows, device="cuda")
+    assert lib.muon_block_norm(blocks._BLOCK_NORM(
+        up.data_ptr(), ld, r.data_ptr(), cols, gate.data_ptr(), ld, post.data_ptr(), scale.data_ptr(), pre.data_ptr(), y.data_ptr(), ld,
+        h.data_ptr(), ld, stats[0].data_ptr(), stats[1].data_ptr(), *([0] * 12), rows, cols, code, 1, 0, 0, 0, 1.0, 1e-6), st) == 0
+    assert torch.equal(y, n.y) and torch.equal(h, n.h) and bool((between(out) == 5.0).all())
+    back, dx, dr = wide()
+    dg = torch.empty_like(g)
+    d = mm.block_norm_backward(dy, n.kept, post, pre, scale=scale, dh=r)
+    assert lib.muon_block_norm_backward(blocks._BLOCK_NORM_GRAD(
+        dy.data_ptr(), cols, r.data_ptr(), cols, up.data_ptr(), 0, ld, h.data_ptr(), 0, ld, gate.data_ptr(), 0, ld,
+        n.kept.rstd_x.data_ptr(), n.kept.rstd_h.data_ptr(), post.data_ptr(), scale.data_ptr(), pre.data_ptr(), dx.data_ptr(), ld,
+        dr.data_ptr(), ld, dg.data_ptr(), cols, 0, 0, 0, 0, 0, rows, cols, code, 1, 0, 0, 1.0), st) == 0
+    assert torch.equal(dx, d.dx) and torch.equal(dr, d.dresidual) and torch.equal(dg, d.dgate) and bool((between(back) == 5.0).all())
