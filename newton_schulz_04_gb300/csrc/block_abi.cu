@@ -21,7 +21,7 @@ static muon_status take(Spans* all, const char* name, const void* p, bool option
 static muon_status take8(Spans* all, const char* name, const muon_fp8_out& o, int fmt, long long rows, long long cols) {
   if (!o.data && !o.scale) return MUON_OK;
   if (!fp8_fmt(fmt)) return fail(MUON_ERR_ARG, "%s: bad 8-bit format %d", name, fmt);
-  TRY(check_fp8_out(name, o.data, o.scale, rows, cols, o.ld));
+  TRY(check_fp8_out(name, o.data, o.scale, rows, cols, rows == 1 ? (cols + 15) / 16 * 16 : o.ld));
   all->add(o.data, span8(rows, cols, o.ld), true);
   all->add(o.scale, scale_bytes(rows, cols), true);
   return MUON_OK;

@@ -260,6 +260,48 @@ def test_outputs_between_the_rows_of_others(mm):
         assert clash == 1
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory")
+def test_strides_of_single_rows_are_not_looked_at(mm):
+    from test_block_ops import P, gated_call, gated_grad_call, norm_call, norm_grad_call, transpose_call
+    for ld in (0, 1, 7, -16):
+        assert accepted(norm_call(mm, rows=1, ldx=ld, ldr=ld, gate=P[20], ldg=ld, ldy=ld, ldh=ld, q=P[8], qs=P[9], ldq=ld, x8=P[10], x8s=P[11],
+                                  ldx8=ld, h8=P[12], h8s=P[13], ldh8=ld, g8=P[14], g8s=P[15], ldg8=ld))
+        assert accepted(norm_grad_call(mm, rows=1, lddy=ld, dh=P[20], lddh=ld, ldx=ld, ldh=ld, lddx=ld, lddr=ld, xs=P[10], hs=P[11]))
+        assert accepted(gated_call(mm, rows=1, ldg=ld, ldu=ld, ldy=ld, q=P[3], qs=P[4], ldq=ld, g8=P[5], g8s=P[6], ldg8=ld, u8=P[7], u8s=P[8],
+                                   ldu8=ld))
+        assert accepted(gated_grad_call(mm, rows=1, lddy=ld, ldg=ld, ldu=ld, lddg=ld, lddu=ld, gr=P[5], grs=P[6], ldgr=ld, ur=P[7], urs=P[8],
+                                        ldur=ld))
+        assert accepted(gated_grad_call(mm, cols=1, gc=P[5], gcs=P[6], ldgc=ld, uc=P[7], ucs=P[8], lduc=ld, yc=P[9], ycs=P[10], ldyc=ld))
+        assert accepted(transpose_call(mm, rows=1, ldq=ld, cols=100)) and accepted(transpose_call(mm, cols=1, ldqt=ld))
+    assert gated_call(mm, rows=1, q=P[3] + 8, qs=P[4], ldq=0) == 3
+
+
+@gpu
+@pytest.mark.parametrize("ld", [0, 7, 1 << 40])
+def test_single_rows_of_any_stride(mm, ld):
+    from newton_schulz_04_gb300 import blocks
+    lib, st, cols = mm.load(), torch.cuda.current_stream().cuda_stream, 300
+    g, u = (gen(i, 1, cols).bfloat16().cuda() for i in (70, 71))
+    want = mm.gated_activation(g, u, fp8="e4m3", checkpoint="e4m3")
+    q = [mm.Fp8Tensor.empty(1, cols) for _ in range(3)]
+    outs = [v for t in q for v in (t.data.data_ptr(), t.scale.data_ptr(), ld)]
+    assert lib.muon_gated_activation(blocks._GATED(g.data_ptr(), ld, u.data_ptr(), ld, 0, ld, *outs, 1, cols, 0, 0, 0, 0), st) == 0
+    for t, w in zip(q, (want.q, want.kept.gate, want.kept.up)):
+        assert torch.equal(t.data.view(torch.uint8), w.data.view(torch.uint8))
+        assert torch.equal(t.scale.view(torch.uint8), w.scale.view(torch.uint8))
+    back = mm.gated_activation_backward(u, want.kept, fp8="e5m2", y_fp8="e4m3", dense=False)
+    rows8 = [mm.Fp8Tensor.empty(1, cols, "e5m2") for _ in range(2)]
+    cols8 = [mm.Fp8Tensor.empty(cols, 1, f) for f in ("e5m2", "e5m2", "e4m3")]
+    a = lambda t, ld: (t.data.data_ptr(), t.scale.data_ptr(), ld)  # noqa: E731
+    k = [(t.data.data_ptr(), t.scale.data_ptr(), ld) for t in (want.kept.gate, want.kept.up)]
+    assert lib.muon_gated_activation_backward(blocks._GATED_GRAD(
+        u.data_ptr(), ld, *k[0], *k[1], 0, 0, 0, 0, *a(rows8[0], ld), *a(cols8[0], 16), *a(rows8[1], ld), *a(cols8[1], 16), *a(cols8[2], 16),
+        1, cols, 0, 0, 0, 1, 0), st) == 0
+    for t, w in zip(rows8 + cols8, (back.dgate_rows, back.dup_rows, back.dgate_cols, back.dup_cols, back.y_cols)):
+        assert torch.equal(t.data.view(torch.uint8), w.data.view(torch.uint8))
+        assert torch.equal(t.scale.view(torch.uint8), w.scale.view(torch.uint8))
+
+
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("cols,gap", [(64, 0), (264, 0), (264, 8), (123, 0), (123, 2), (1_000, 3)])
