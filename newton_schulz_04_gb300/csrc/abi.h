@@ -12,7 +12,6 @@ namespace muon {
 inline bool float_dt(int dt) { return dt == MUON_BF16 || dt == MUON_FP32 || dt == MUON_FP16; }
 inline bool fp8_fmt(int f) { return f == MUON_E4M3 || f == MUON_E5M2; }
 inline bool misaligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
-inline bool aligned16(const void* p, long long ld, int size) { return !misaligned(p, 16) && ld * size % 16 == 0; }
 
 // Bytes spanned by a matrix of `rows` rows of `cols` elements, `ld` apart.
 inline long long span(long long rows, long long cols, long long ld, int size) {

@@ -80,9 +80,6 @@ struct Ring {
   __device__ __forceinline__ void fetch(int slot, int arr, int c, const T* src, int bytes) const {
     copy16(smem_u32(at(slot, arr, c)), src, bytes);
   }
-  __device__ __forceinline__ const uint4& piece(int slot, int arr, int c) const {
-    return *reinterpret_cast<const uint4*>(at(slot, arr, c));
-  }
   __device__ __forceinline__ void read(int slot, int arr, int c, float (&v)[16 / sizeof(T)]) const {
     unpack_piece<T>(*reinterpret_cast<const uint4*>(at(slot, arr, c)), v);
   }
