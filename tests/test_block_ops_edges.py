@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import oracle.blocks as ref
+import test_block_ops as block_ops
 from test_block_ops import (  # noqa: F401
     DTYPES, F24, check8_exact, close, dev, gen, gpu, mm, norm_inputs, transposed_exactly,
 )
@@ -347,3 +348,103 @@ def test_outputs_in_the_halves_of_a_matrix(mm, dtype, cols, gap):
         n.kept.rstd_x.data_ptr(), n.kept.rstd_h.data_ptr(), post.data_ptr(), scale.data_ptr(), pre.data_ptr(), dx.data_ptr(), ld,
         dr.data_ptr(), ld, dg.data_ptr(), cols, 0, 0, 0, 0, 0, rows, cols, code, 1, 0, 0, 1.0), st) == 0
     assert torch.equal(dx, d.dx) and torch.equal(dr, d.dresidual) and torch.equal(dg, d.dgate) and bool((between(back) == 5.0).all())
+
+
+# ---------------------------------------------------------------- 8-bit outputs, scale by scale
+
+def check8_by_blocks(q, x, err, fmt, what=""):
+    """q stands for x within half a step and `err`.  Each block's scale is the smallest power of two under which a largest magnitude
+    within the block's own error fits, 1 only of a block that may be zero; scales of no row or block are 1."""
+    cols = x.shape[1]
+    x, err = x.double(), err.double().expand(x.shape)
+    s = q.scales().cpu().double()
+    half, sub = block_ops.HALF8[fmt]
+    close(q.dequantize(), x, half * x.abs() + (1 + half) * err + sub * s.repeat_interleave(128, dim=1)[:, :cols], what)
+    pool = lambda t: torch.nn.functional.max_pool2d(t[None], (1, 128), ceil_mode=True)[0]  # noqa: E731
+    low, high, top = pool((x.abs() - err).clamp(min=0)), pool(x.abs() + err), block_ops.ref8.TOP[fmt]
+    right = (low <= top * s) & ((high > top * s / 2) | ((low == 0) & (s == 1)) | (s == 2.0 ** -127))
+    assert bool(right.all()), f"{what}: scales of {int((~right).sum())} blocks"
+    rows, blocks = s.shape
+    kept = q.scale.view(torch.uint8).cpu().permute(1, 0, 2).reshape(q.scale.shape[1], -1)
+    assert bool((kept[rows:] == 127).all()) and bool((kept[:, blocks:] == 127).all()), what
+
+
+@pytest.fixture
+def by_blocks(monkeypatch):
+    monkeypatch.setattr(block_ops, "check8", check8_by_blocks)
+
+
+def test_a_wrong_scale_is_seen():
+    """The check itself, on the CPU: scales of 1 throughout, and one that is a power too large or too small."""
+    class Q:
+        def __init__(self, data, exps, fmt):
+            self.data, self.scale, self.fmt, self.shape = data, block_ops.kept_scales(exps), fmt, data.shape
+
+        def scales(self):
+            s = 2.0 ** (self.scale.double() - 127)
+            return s.permute(1, 0, 2).reshape(s.shape[1], -1)[:self.shape[0], :-(-self.shape[1] // 128)]
+
+        def dequantize(self):
+            return self.data * self.scales().repeat_interleave(128, dim=1)[:, :self.shape[1]]
+
+    x = gen(80, 5, 300).double()
+    x[3] = 0
+    for fmt in ("e4m3", "e5m2"):
+        data, exps = block_ops.ref8.quantize(x, fmt)
+        check8_by_blocks(Q(data, exps, fmt), x, x.abs() * 1e-6, fmt)
+        some = (x[:, :1] != 0).int()
+        for bad in (torch.zeros_like(exps), exps + (torch.arange(3) == 1) * some, exps - (torch.arange(3) == 2) * some):
+            wide = 2.0 ** bad.repeat_interleave(128, dim=1)[:, :300].double()
+            with pytest.raises(AssertionError):
+                check8_by_blocks(Q(block_ops.ref8.round8(x / wide, fmt).clamp(-block_ops.ref8.TOP[fmt], block_ops.ref8.TOP[fmt]), bad, fmt), x,
+                                 x.abs() * 1e-6, fmt)
+        q = Q(data, exps, fmt)
+        q.scale[0, 5, 0] = 0
+        with pytest.raises(AssertionError):
+            check8_by_blocks(q, x, x.abs() * 1e-6, fmt)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(1, 1), (5, 127), (130, 256), (7, 1_000), (37, 4_100), (3, 16_385), (2, 40_000)])
+def test_norm_outputs_scale_by_scale(mm, by_blocks, dtype, shape):
+    for fp8, kept in (("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e5m2", "e5m2")):
+        block_ops.check_norm(mm, norm_inputs(81, *shape, dtype, "element", True), fp8=fp8, checkpoint=kept)
+        block_ops.check_norm(mm, norm_inputs(82, *shape, dtype, "row", False), alpha=0.5, fp8=fp8, checkpoint=kept, y=False)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("shape", [(1, 1), (5, 127), (129, 130), (130, 256), (7, 1_000), (257, 640), (3, 16_385)])
+def test_gated_outputs_scale_by_scale(mm, by_blocks, dtype, kind, shape):
+    g, u = block_ops.gated_inputs(83, *shape, dtype)
+    for fp8, kept in (("e4m3", "e4m3"), ("e5m2", "e5m2"), ("e5m2", None)):
+        block_ops.check_gated(mm, g, u, kind, fp8=fp8, checkpoint=kept)
+        block_ops.check_gated_grad(mm, 84, *shape, dtype, kind, kept=kept, fp8=fp8, y_fp8="e4m3")
+    if dtype == torch.float32:                  # every 8-bit output to the bit, from the dense ones
+        y = mm.gated_activation(*dev(g, u), activation=kind).y.cpu()
+        dy = gen(85, *shape)
+        d = mm.gated_activation_backward(dy.cuda(), mm.GatedKept(*dev(g, u)), activation=kind, fp8="e5m2", y_fp8="e4m3")
+        for q, t in ((d.dgate_rows, d.dgate), (d.dup_rows, d.dup), (d.dgate_cols, d.dgate.t()), (d.dup_cols, d.dup.t())):
+            check8_exact(q, t.cpu(), "e5m2")
+        check8_exact(d.y_cols, y.t(), "e4m3")
+
+
+# ---------------------------------------------------------------- offsets past 32 bits, in the rings too
+
+@gpu
+@pytest.mark.parametrize("cols", [4_096, 8_192])
+@pytest.mark.parametrize("kept", [None, "e4m3"])
+def test_ring_offsets_past_32_bits(mm, cols, kept):
+    """More than 2^31 elements in rows that CTAs (4096 columns) and clusters (8192) hold: the last rows equal those alone."""
+    rows = 2 ** 31 // cols + 5
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(2))
+    w, end = torch.ones(cols, device="cuda"), x[-7:].contiguous()
+    m = mm.block_norm(x, x, w, w, gate=x, fp8="e4m3", y=False, checkpoint=kept)
+    n = mm.block_norm(end, end, w, w, gate=end, fp8="e4m3", y=False, checkpoint=kept)
+    assert torch.equal(m.h[-7:], n.h) and torch.equal(m.q.scales()[-7:], n.q.scales()) and torch.equal(m.kept.rstd_h[-7:], n.kept.rstd_h)
+    assert torch.equal(m.q.data[-7:].contiguous().view(torch.uint8), n.q.data.view(torch.uint8))
+    g = mm.block_norm_backward(x, m.kept, w, w, dh=x, dweights=False)
+    h = mm.block_norm_backward(end, n.kept, w, w, dh=end, dweights=False)
+    assert torch.equal(g.dx[-7:], h.dx) and torch.equal(g.dgate[-7:], h.dgate) and torch.equal(g.dresidual[-7:], h.dresidual)
