@@ -151,7 +151,10 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, post_weight: torch.Tenso
     gate (or None) holds logits of x's type, one for each element or, with a last dimension of 1, for each row; the
     weights and scale (or None) are [cols] of one type.  `fp8` ("e4m3" or "e5m2") asks for y in 8 bits as well, `y=False`
     leaves out the other y.  What the gradient needs is in `kept`: x, h and gate themselves, or with `checkpoint` 8-bit
-    copies of them (a gate of each row stays as it is)."""
+    copies of them (a gate of each row stays as it is).
+
+    With `checkpoint` a gate of every element is shut by a finite value: an infinity makes its block of 128 NaN in 8 bits, and
+    the type's lowest value leaves the block's other gates 0 there; -100 does neither."""
     _required(x=x, residual=residual, post_weight=post_weight, pre_weight=pre_weight)
     shape = x.shape
     if not shape or shape[-1] < 1:

@@ -10,9 +10,9 @@
 // and added in a fixed order by a second kernel.
 //
 // A ring of rows as in the forward kernel, one piece to a thread.  8191 x 4096 bf16 takes 92 us from e4m3 (4.7 TB/s, 70 % of the
-// copy rate) and 94 from bf16 (84 %): 16 warps of 128 registers on an SM issue 56 % of its slots, 56 instructions an element.
+// copy rate) and 94 from bf16 (84 %): 16 warps of 128 registers on an SM issue 60 % of its slots, 60 instructions an element.
 // With scalars of fp32 it took 125, with choices at run time 120; there two rows a turn, or the rows' factors and scales copied
-// with the rows, gained nothing.  Rows that start anywhere: 139 and 167 at 4095 columns.
+// with the rows, gained nothing.  Rows that start anywhere: 142 and 164 at 4095 columns.
 //
 // Compiled once for each type and alignment of rows (MUON_ROWS_T, MUON_ROWS_ANYWHERE).
 #include <cuda_runtime.h>
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   using Slots = GradRing<T, G, S, ROWS, KEPT != 0, ANYWHERE>;
   constexpr int E = P::E, N = P::N;
   // For the second phase a gate's exponential is kept and its sigmoid formed again (TWICE), or, where not even the exponentials of two
-  // rows fit, read from the ring once more (AGAIN: 8192 bf16 columns 114 us, kept 134).  fp32 rows, whose quotients are dear, keep
+  // rows fit, read from the ring once more (AGAIN: 8192 bf16 columns 112 us, kept 134, with 188 bytes of spills).  fp32 rows, whose quotients are dear, keep
   // both where one row at a time leaves the registers (2048 columns from e4m3 145 us, twice 162; two rows from e4m3 237 and 193).
   constexpr bool AGAIN = GATE && KEPT == 0 && sizeof(T) == 2 && ROWS > 1;
   constexpr bool TWICE = GATE && !AGAIN && (sizeof(T) == 2 || (KEPT != 0 && ROWS > 1));
@@ -425,10 +425,11 @@ static cudaError_t dispatch_ring(const muon_block_norm_grad_args& a, float* part
   if (pieces <= 128) return go(Int<128>(), Int<4>(), Int<1>(), Int<4>(), Int<1>());
   if (pieces <= 256) return go(Int<256>(), Int<4>(), Int<1>(), Int<2>(), Int<1>());
   if (pieces <= 512) return go(Int<512>(), Int<4>(), Int<1>(), Int<1>(), Int<1>());
-  // Rows over a cluster, which waits for its exchange: two rows at a time share it where their values fit the registers.
-  // 33.5M elements at 8192 and 16384 columns: 16-bit rows 115 and 124 us (one row at a time 141 and 157), fp32 241 and 288
-  // (270 and 329), fp32 from 8 bits 216 and 282 (243 and 292).  16-bit rows from 8 bits spill: 126 and 150, two at a time
-  // 140 and 159; at 8192 columns they take clusters of four small CTAs, two of which share an SM, against two large ones' 139
+  // Rows over a cluster, which waits for its exchange: two rows at a time share it where that was measured faster, which is where
+  // their values fit the registers but for a few bytes (none to 24 of spills).  33.5M elements at 8192 and 16384 columns: 16-bit
+  // rows 112 and 123 us (one row at a time 141 and 157), fp32 237 and 282 (270 and 329), fp32 from 8 bits 211 and 294 (243 and 292).
+  // 16-bit rows from 8 bits, one at a time: 126 and 150, two at a time 140 and 159 with spills; at 8192 columns they take clusters
+  // of four small CTAs, two of which share an SM, against two large ones' 139
   if constexpr (KEPT == 0 || sizeof(T) == 4) {
     if (pieces <= 1024) return go(Int<512>(), Int<2>(), Int<2>(), Int<1>(), Int<2>());
     if (pieces <= 2048) return go(Int<512>(), Int<2>(), Int<2>(), Int<1>(), Int<4>());

@@ -13,7 +13,7 @@
 // gate, an 8-bit output and three 8-bit copies takes 71 us (5.7 TB/s, 45 instructions an element, 57 % of the issue
 // slots); with scalars of fp32 and an exchange for the scales of each copy it took 126, with choices at run time 81.  A
 // cluster's exchange takes half of a row's time, so a row belongs to one CTA up to 16384 16-bit columns (8192 columns 75 us,
-// 16384 104, in clusters of two 123).  Rows that start anywhere: 112 at 4095 columns, 120 at 1023.
+// 16384 104, in clusters of two 123).  Rows that start anywhere: 113 at 4095 columns, 121 at 1023.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -310,7 +310,9 @@ static cudaError_t launch_ring(const muon_block_norm_args& a, int sms, cudaStrea
 }
 
 // Threads and pieces of a row, rows of the ring, CTAs of an SM and of a cluster by the row's width, as measured at 33.5M elements:
-// 256, 512, 1024, 2048 columns take 77, 76, 70, 71 us; one piece to a thread 77, 76 to 80, 79 to 81, 84 to 94.
+// 256, 512, 1024, 2048 columns take 77, 74, 71, 71 us; one piece to a thread 77, 76 to 80, 79 to 81, 84 to 94.  Four pieces of
+// 16-bit rows, whose weights alone are 64 registers, spill 76 to 168 bytes a thread, and so do 40 two pieces with a gate of rows
+// that start anywhere.
 template <typename T, bool GATE, bool E4M3, bool ANYWHERE>
 static cudaError_t dispatch_ring(const muon_block_norm_args& a, int sms, cudaStream_t st) {
   constexpr int E = 16 / static_cast<int>(sizeof(T));

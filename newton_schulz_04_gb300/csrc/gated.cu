@@ -81,7 +81,7 @@ __device__ __forceinline__ uint4 load_part(const T* p, int n) {
 }
 // ------------------------------------------------------------------ forward
 // Bound by memory and issuing: 8192 x 14336 bf16 with an 8-bit output and both checkpoints takes 142 us (5.8 TB/s, 32
-// instructions an element); with a block to a warp, a column of it to a lane, 326.  gelu 52 us at 33.5M elements, silu 44, rows
+// instructions an element); with a block to a warp, a column of it to a lane, 326.  gelu 53 us at 33.5M elements, silu 44, rows
 // that start anywhere 59.
 //
 // A block of 128 columns to 16 lanes (32 in fp32), U rows to a lane, fetched together.  EIGHT: 8-bit outputs; 0: none, 1: any, 2:
@@ -201,7 +201,7 @@ cudaError_t launch_gated(const muon_gated_args& a, int vec, cudaStream_t st) {
 // the chunk that they come from (a word of 4 rows for each column and output) and leave from there, 16 rows at a time.
 // Computing everything twice costs a quarter of the instructions and saves the registers that three outputs of a tile
 // would fill, so that three CTAs on an SM overlap one another's copies.  Bound by issuing: 8192 x 14336 bf16 from e4m3, e5m2
-// both ways and the activation again, takes 268 us (58 % of the copy rate, 70 % of the issue slots, 64 instructions an
+// both ways and the activation again, takes 272 us (58 % of the copy rate, 70 % of the issue slots, 65 instructions an
 // element); one CTA of 512 threads with f and f' in registers took 715.
 constexpr int kTile = 128, kTileWarps = 8, kChunkRows = 4, kChunks = kTile / kTileWarps / kChunkRows;
 
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, GatedTile<T, KEPT, GELU, ANYW
 
 // ------------------------------------------------------------------ gradient of the data's type alone
 // Without 8-bit outputs no block has to be gathered, and the forward kernel's layout gives small matrices more CTAs: 777 x 1101
-// fp16 takes 5.7 us (22 in tiles), 8192 x 4096 bf16 51 (96 % of the copy rate).
+// fp16 takes 7.3 us (22 in tiles), 8192 x 4096 bf16 51 (96 % of the copy rate).
 template <typename T, int KEPT, bool GELU, bool ANYWHERE>
 __global__ void __launch_bounds__(256) gated_grad_dense_kernel(const muon_gated_grad_args a) {
   using P = Pairs<T>;
