@@ -666,7 +666,8 @@ typedef enum {
  * muon_gated_activation -- y = f(gate) up for two matrices [rows, cols] of dt, of any row strides (two halves of one product's
  * output, say).  y may be NULL; q is y in 8 bits of format fmt, gate8 and up8 are copies of kept_fmt for the gradient.  rows
  * and cols in [0, MUON_MAX_ROWS].  For 16-bit dt, here and in the gradient, silu is off by at most (5 + 1.2 |g|) 2^-23 and gelu by
- * (24 + 1.6 g^2) 2^-24 of itself before it is rounded, for MUON_FP32 by a few units in the last place.
+ * (24 + 1.6 g^2) 2^-24 of itself before it is rounded, for MUON_FP32 by a few units in the last place; their derivatives, sums of
+ * two terms, by 1 + |g| times as much of the larger one.
  */
 typedef struct {
     const void* gate; int64_t ldg;

@@ -160,9 +160,10 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, MINB)
   using K = std::conditional_t<KEPT != 0, uint8_t, T>;
   using Slots = GradRing<T, G, S, ROWS, KEPT != 0, ANYWHERE>;
   constexpr int E = P::E, N = P::N;
-  // For the second phase a gate's exponential is kept and its sigmoid formed again (TWICE), or, where not even the exponentials of two
-  // rows fit, read from the ring once more (AGAIN: 8192 bf16 columns 112 us, kept 134, with 188 bytes of spills).  fp32 rows, whose quotients are dear, keep
-  // both where one row at a time leaves the registers (2048 columns from e4m3 145 us, twice 162; two rows from e4m3 237 and 193).
+  // For the second phase a gate's exponential is kept and its sigmoid formed again (TWICE), or, where not even the exponentials of
+  // two rows fit, the gate is read from the ring once more (AGAIN: 8192 bf16 columns 112 us, exponentials kept 134, with 188 bytes
+  // of spills).  fp32 rows, whose quotients are dear, keep exponential and sigmoid where one row at a time leaves the registers:
+  // 2048 columns from e4m3 145 us, formed twice 162; two rows of 4096 at a time from e4m3 237, formed twice 193.
   constexpr bool AGAIN = GATE && KEPT == 0 && sizeof(T) == 2 && ROWS > 1;
   constexpr bool TWICE = GATE && !AGAIN && (sizeof(T) == 2 || (KEPT != 0 && ROWS > 1));
   extern __shared__ __align__(16) uint8_t ring_smem[];
